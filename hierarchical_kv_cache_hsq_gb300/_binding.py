@@ -27,6 +27,7 @@ HSQ_DTYPE_F32, HSQ_DTYPE_BF16 = 0, 1
 HSQ_ATTN_FROM_STAGING = 1
 HSQ_FAULT_ALLOC, HSQ_FAULT_FETCH = 1, 2
 HSQ_DEVERR_SEL, HSQ_DEVERR_POS, HSQ_DEVERR_L1_OVER, HSQ_DEVERR_WAIT, HSQ_DEVERR_GROW = 1, 2, 4, 8, 16
+HSQ_DEVERR_PAGE, HSQ_DEVERR_LEN = 32, 64
 
 BUFFERS = ["l1_kc", "l1_vc", "l1_kn", "l1_vn", "l1_pos", "l1_count", "l2_kc", "l2_vc", "l2_kn",
            "l2_vn", "l2_cnt", "l3", "l1_bitmap", "staging", "win_kv", "gsum", "l1_qs", "l1_qn", "l3_qs", "l3_qn",
@@ -69,8 +70,13 @@ class hsq_cache(ctypes.Structure):
     ]
 
 
+class hsq_pages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_n", ctypes.c_int)]
+
+
 _lib = None
 _vp = ctypes.c_void_p
+_int, _i64 = ctypes.c_int, ctypes.c_int64
 _SIGS = {
     "hsq_codebook": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _vp, _vp]),
     "hsq_cache_sizes": (ctypes.c_int, [ctypes.POINTER(hsq_config), ctypes.c_int, ctypes.c_int, _vp]),
@@ -88,6 +94,11 @@ _SIGS = {
     "hsq_prefill_workspace_size": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "hsq_prefill": (ctypes.c_int, [_vp, ctypes.POINTER(hsq_cache), _vp, _vp, _vp, ctypes.c_int, ctypes.c_int, _vp,
                                    _vp, ctypes.c_size_t, _vp]),
+    "hsq_page_tables": (_int, [_vp, ctypes.POINTER(hsq_pages)] + [_int] * 5 + [_vp] * 11),
+    "hsq_page_write": (_int, [_vp, ctypes.POINTER(hsq_pages), _int, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _vp,
+                              _vp]),
+    "hsq_shared_attn_workspace_size": (_int, [_vp] + [_int] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "hsq_shared_attn": (_int, [_vp, ctypes.POINTER(hsq_pages)] + [_int] * 5 + [_vp] * 8 + [ctypes.c_size_t, _vp]),
     "hsq_last_error": (ctypes.c_char_p, [_vp]),
     "hsq_debug_set_fault": (ctypes.c_int, [ctypes.c_uint]),
     "hsq_version": (ctypes.c_char_p, []),
@@ -440,6 +451,168 @@ def hsq_route_noalloc(cfg: hsq_config, cache: CacheBuffers, q, pos, sel, stream=
     c = cache.struct()
     _check(lib.hsq_route_noalloc(ctypes.byref(cfg), ctypes.byref(c), q.data_ptr(), pos.data_ptr(),
                                  sel.data_ptr(), _stream_handle(stream)))
+
+
+# -- paged serving ---------------------------------------------------------------------
+
+@dataclass
+class PagePool:
+    """The pages of one layer: k, v [n_pages, Hkv, page_n, 128] bfloat16 on one
+    device, keys RoPE'd.  page_n is 16, 32, 64 or 128."""
+    k: "object"
+    v: "object"
+
+    def __post_init__(self):
+        import torch
+        for x in (self.k, self.v):
+            if x.dtype != torch.bfloat16 or x.dim() != 4 or x.shape[3] != 128 or not (x.is_cuda and x.is_contiguous()):
+                raise ValueError("k and v must be contiguous bfloat16 [n_pages, Hkv, page_n, 128] on the GPU")
+        if self.k.shape != self.v.shape or self.k.device != self.v.device:
+            raise ValueError("k and v must have one shape and one device")
+        self.index = self.k.get_device()
+        self._c = hsq_pages(k=self.k.data_ptr(), v=self.v.data_ptr(), n_pages=self.k.shape[0], page_n=self.k.shape[2])
+        self.ref = ctypes.byref(self._c)
+
+    @property
+    def n_pages(self) -> int:
+        return self._c.n_pages
+
+    @property
+    def page_n(self) -> int:
+        return self._c.page_n
+
+
+def allocate_pages(ctx: Context, n_pages: int, page_n: int, device=None) -> PagePool:
+    """A pool of n_pages pages of page_n tokens for every KV head of ctx (one layer)."""
+    import torch
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    shape = (n_pages, ctx.cfg.n_kv_heads, page_n, 128)
+    return PagePool(torch.zeros(shape, dtype=torch.bfloat16, device=dev),
+                    torch.zeros(shape, dtype=torch.bfloat16, device=dev))
+
+
+def _need(pool: PagePool, dtype, **tensors):
+    """Every tensor given is contiguous, of this type and on the pool's device."""
+    for name, x in tensors.items():
+        if x.dtype != dtype or x.get_device() != pool.index or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dtype} on the pool's device")
+
+
+def _need_heads(ctx: Context, pool: PagePool):
+    if pool.k.shape[1] != ctx.cfg.n_kv_heads:
+        raise ValueError("the pool's KV heads are not the context's")
+
+
+def hsq_page_tables(ctx: Context, pool: PagePool, cached, fresh, free_ids, used, table, slots, pos, q_start, lens,
+                    used_out, base: int = 0, stream=None):
+    """Block table and slot map of a step: request b has cached[b] tokens and brings
+    fresh[b] new ones (int32 [B]); free_ids int32 [n_free] and used int32 [1] are the
+    pool's free list and how much of it is taken.  Writes the new entries of table
+    int32 [B, width], slots int64 and pos int32 [rows] (-1 behind the last row),
+    q_start int32 [B + 1], lens int32 [B] and used_out int32 [1].  base: the
+    position of a request's first own token (the shared prefix's length)."""
+    import torch
+    _need(pool, torch.int32, cached=cached, fresh=fresh, free_ids=free_ids, used=used, table=table, pos=pos,
+          q_start=q_start, lens=lens, used_out=used_out)
+    _need(pool, torch.int64, slots=slots)
+    B = cached.numel()
+    if fresh.numel() != B or lens.numel() != B or q_start.numel() != B + 1 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("fresh, lens [B], q_start [B + 1] and table [B, width] must agree with cached [B]")
+    rows = slots.numel()
+    if pos.numel() != rows or used.numel() != 1 or used_out.numel() != 1:
+        raise ValueError("pos and slots must be [rows], used and used_out [1]")
+    st = ctx.lib.hsq_page_tables(ctx.handle, pool.ref, B, table.shape[1], rows, free_ids.numel(), base,
+                                 cached.data_ptr(), fresh.data_ptr(), free_ids.data_ptr(), used.data_ptr(),
+                                 table.data_ptr(), slots.data_ptr(), pos.data_ptr(), q_start.data_ptr(),
+                                 lens.data_ptr(), used_out.data_ptr(), _stream_handle(stream))
+    if st:
+        _check(st, ctx.handle)
+
+
+def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, stream=None):
+    """Rotate q [rows, Hq, 128] and k [rows, Hkv, 128] (bfloat16 or float32; rows may be
+    strided, as views of one fused projection) at pos and store k and v [rows, Hkv, 128]
+    in the pool at slots; q_out bfloat16 [rows, Hq, 128] gets the rotated queries
+    (q and q_out may both be None).  Rows with pos < 0 are skipped; a slot < 0 stores nothing."""
+    import torch
+    _need_heads(ctx, pool)
+    _need(pool, torch.int32, pos=pos)
+    _need(pool, torch.int64, slots=slots)
+    if k.dtype == torch.bfloat16:
+        dt = HSQ_DTYPE_BF16
+    elif k.dtype == torch.float32:
+        dt = HSQ_DTYPE_F32
+    else:
+        raise ValueError("q, k and v must be bfloat16 or float32")
+    rows, Hkv = pos.numel(), ctx.cfg.n_kv_heads
+    parts = (("k", k, Hkv), ("v", v, Hkv)) if q is None else (("k", k, Hkv), ("v", v, Hkv), ("q", q, ctx.cfg.n_q_heads))
+    for name, x, heads in parts:
+        if x.dtype != k.dtype or x.get_device() != pool.index or x.shape != (rows, heads, 128):
+            raise ValueError(f"{name} must be [rows, heads, 128], of one dtype, on the pool's device")
+        s = x.stride()
+        if s[2] != 1 or (s[1] != 128 and heads > 1):
+            raise ValueError(f"{name}: the heads of a row must lie side by side")
+    if slots.numel() != rows:
+        raise ValueError("pos and slots must be [rows]")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        _need(pool, torch.bfloat16, q_out=q_out)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    one = rows == 1  # (the row stride of a single row says nothing)
+    st = ctx.lib.hsq_page_write(ctx.handle, pool.ref, rows, _ptr(q), k.data_ptr(), v.data_ptr(),
+                                0 if q is None else ctx.cfg.n_q_heads * 128 if one else q.stride(0),
+                                Hkv * 128 if one else k.stride(0), Hkv * 128 if one else v.stride(0), dt,
+                                pos.data_ptr(), slots.data_ptr(), _ptr(q_out), _stream_handle(stream))
+    if st:
+        _check(st, ctx.handle)
+
+
+def hsq_shared_attn_workspace_size(ctx: Context, rows: int, B: int, prefix_len: int, max_new: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(ctx.lib.hsq_shared_attn_workspace_size(ctx.handle, rows, B, prefix_len, max_new, ctypes.byref(n)),
+           ctx.handle)
+    return int(n.value)
+
+
+def hsq_shared_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, out, workspace, prefix=None,
+                    prefix_len: int = 0, max_new: int = 1, lse=None, stream=None):
+    """Attention of a batch whose requests share a prefix: the rows
+    q_start[b] .. q_start[b + 1] of q [rows, Hq, 128] (bfloat16, rotated) see the first
+    prefix_len tokens of the pages in prefix (int32) and request b's own lens[b] tokens
+    in the pages of table[b] (int32 [B, width]), causally: the request's last row sees
+    its last token.  out bfloat16 like q; lse float32 [rows, Hq] or None (natural log).
+    max_new: the largest number of rows of one request.  workspace: uint8, of
+    hsq_shared_attn_workspace_size bytes, one for each call that may run at the same time."""
+    import torch
+    _need_heads(ctx, pool)
+    _need(pool, torch.bfloat16, q=q, out=out)
+    _need(pool, torch.int32, q_start=q_start, lens=lens, table=table)
+    B, rows = lens.numel(), q.shape[0]
+    if q.shape[1:] != (ctx.cfg.n_q_heads, 128) or out.shape != q.shape:
+        raise ValueError("q and out must be [rows, Hq, 128]")
+    if q_start.numel() != B + 1 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("q_start [B + 1] and table [B, width] must agree with lens [B]")
+    if prefix_len > 0:
+        if prefix is None:
+            raise ValueError("prefix is None with prefix_len > 0")
+        _need(pool, torch.int32, prefix=prefix)
+        if prefix.numel() * pool.page_n < prefix_len:
+            raise ValueError("prefix has too few pages for prefix_len")
+    if lse is not None:
+        _need(pool, torch.float32, lse=lse)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [rows, Hq]")
+    if workspace.get_device() != pool.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the pool's device")
+    st = ctx.lib.hsq_shared_attn(ctx.handle, pool.ref, rows, B, table.shape[1], prefix_len, max_new, q.data_ptr(),
+                                 q_start.data_ptr(), lens.data_ptr(), table.data_ptr(),
+                                 prefix.data_ptr() if prefix_len > 0 else None, out.data_ptr(), _ptr(lse),
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                 _stream_handle(stream))
+    if st:
+        _check(st, ctx.handle)
 
 
 def hsq_sync_status(ctx: Context, stream=None) -> int:

@@ -71,4 +71,9 @@ hsq_status prefill_prep_kv(hsq_ctx* ctx, const PrefillImages& im, const void* K,
                            cudaStream_t st);
 hsq_status prefill_attention(hsq_ctx* ctx, const PrefillImages& im, float* out, int B, int T, cudaStream_t st);
 
+// Paged serving (hsq_pages.cu): the pool's shape (and, with buffers, its memory) is
+// valid; the current device is the context's.
+hsq_status check_pages(hsq_ctx* ctx, const hsq_pages* pages, bool buffers);
+hsq_status check_device(hsq_ctx* ctx);
+
 }  // namespace hsq

@@ -129,9 +129,17 @@ bool lloyd_max(int bits, int dim, double* centroids, double* boundaries) {
 }
 
 void device_codebook(float out[kCodebookFloats]) {
-    double c4[16], t4[15], c3[8], t3[7];
-    lloyd_max(4, kDim, c4, t4);
-    lloyd_max(3, kDim, c3, t3);
+    // (the same numbers for every context: iterated once a process, 60 ms of host time)
+    struct Levels {
+        double c4[16], t4[15], c3[8], t3[7];
+        Levels() {
+            lloyd_max(4, kDim, c4, t4);
+            lloyd_max(3, kDim, c3, t3);
+        }
+    };
+    static const Levels levels;
+    const auto &c4 = levels.c4, &t4 = levels.t4;
+    const auto &c3 = levels.c3, &t3 = levels.t3;
     std::memset(out, 0, sizeof(float) * kCodebookFloats);
     for (int i = 0; i < 16; ++i) out[i] = (float)c4[i];
     for (int i = 0; i < 15; ++i) out[16 + i] = (float)t4[i];

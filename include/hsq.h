@@ -80,8 +80,12 @@ enum {
     HSQ_DEVERR_WAIT = 8,      /* a bounded wait of the prefill attention kernel (on its bulk
                                  copies or its tensor-core work) ran out: its output is not
                                  written */
-    HSQ_DEVERR_GROW = 16      /* hsq_append: the token leaving the recent window was not in L1
+    HSQ_DEVERR_GROW = 16,     /* hsq_append: the token leaving the recent window was not in L1
                                  (the cache was not encoded with that window): L1 left as is */
+    HSQ_DEVERR_PAGE = 32,     /* paged calls: the free list ran out, or a page id or slot lies outside
+                                 the pool: the tokens concerned are not stored / not attended to */
+    HSQ_DEVERR_LEN = 64       /* paged calls: a length is negative, exceeds its table or buffer, or
+                                 offsets do not ascend: clamped (see each call) */
 };
 
 /* Flags of hsq_decode_attn. */
@@ -496,6 +500,114 @@ hsq_status hsq_prefill(hsq_ctx* ctx, const hsq_cache* cache, const void* Q, cons
 enum { HSQ_NOALLOC_SCRATCH_BYTES = 4 << 20 };
 hsq_status hsq_route_noalloc(const hsq_config* cfg, const hsq_cache* cache, const float* q,
                              const int32_t* pos, int32_t* sel, hsq_stream_t stream);
+
+/*
+ * Paged serving of uncompressed tokens: the tokens that a batch's requests
+ * share (a long common prompt) and those they have just made, as bf16 keys and
+ * values in pages of one pool, before (or without) an encode into the tiers.
+ * The pages have no counterpart in the summaries; the attention is the model's
+ * ordinary one, as in hsq_prefill.  One serving step is hsq_page_tables, then per
+ * layer hsq_page_write and hsq_shared_attn; none of them allocates, synchronises or
+ * keeps state, so a step may be captured into a graph and replayed while
+ * the device-side lengths and tables change.
+ *
+ * hsq_pages -- the pool of one layer: page i holds page_n tokens of every KV head,
+ *   k, v: device [n_pages][Hkv][page_n][128] bf16, 16-byte aligned; keys RoPE'd.
+ *   page_n: 16, 32, 64 or 128.  n_pages >= 1, n_pages * Hkv * page_n < 2^31.
+ */
+typedef struct hsq_pages {
+    void* k;
+    void* v;
+    int n_pages;
+    int page_n;
+} hsq_pages;
+
+enum { HSQ_MAX_REQUESTS = 4096 };  /* largest B of the paged calls */
+
+/*
+ * hsq_page_tables -- block table and slot map of a step from request lengths.
+ *   Request b has cached[b] tokens stored and brings fresh[b] new ones (0 allowed).
+ *   With P = page_n, lens = cached + fresh, have = min(ceil(cached / P), width)
+ *   and need = min(ceil(lens / P), width):
+ *     q_start[b] [B + 1]: rows of the requests before b (q_start[B] = rows in use);
+ *     lens[b]    [B]: cached[b] + fresh[b];
+ *     table[b][have .. need) = the next free_ids from index *used on, request by
+ *       request; the other entries are left as they are;
+ *     row i = q_start[b] + j: pos[i] = base + cached[b] + j and slots[i] =
+ *       table[b][p / P] * P + p mod P with p = cached[b] + j; rows from
+ *       q_start[B] on: pos = slots = -1;
+ *     *used_out = *used + the pages taken (at most n_free).
+ *   Inputs are not written, so the call can be repeated; an output must
+ *   not be an input.  free_ids [n_free], table [B][width], slots, pos [rows]:
+ *   int32, slots int64; all device memory.
+ *   Out of pages: the entries past the list are -1, and the slots of their
+ *   tokens -1 (HSQ_DEVERR_PAGE); a page id outside the pool counts the same way.
+ *   HSQ_DEVERR_LEN: a negative length (taken as 0), a length above 2^30
+ *   (taken as that), tokens past the table's width (slot -1) or past `rows`
+ *   (not listed: q_start stops at `rows`), *used outside [0, n_free].
+ *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
+ *   HSQ_MAX_REQUESTS)], width, rows or n_free < 1, base < 0, an
+ *   output that is an input, another current device than the context's),
+ *   HSQ_ERR_CUDA.
+ */
+hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int width, int rows, int n_free, int base,
+                           const int32_t* cached, const int32_t* fresh, const int32_t* free_ids,
+                           const int32_t* used, int32_t* table, int64_t* slots, int32_t* pos, int32_t* q_start,
+                           int32_t* lens, int32_t* used_out, hsq_stream_t stream);
+
+/*
+ * hsq_page_write -- rotate the step's queries and keys and store its keys and
+ *   values: for row i with pos[i] >= 0, q_out[i] = RoPE(q[i], pos[i]) and, with
+ *   s = slots[i] >= 0, page s / P, token s mod P of the pool gets RoPE(k[i], pos[i])
+ *   and v[i].  Computed in fp32 and rounded once to bf16.  Rows with pos[i] < 0 are
+ *   skipped whole.  A slot must not occur twice: it then holds parts of both rows.
+ *   q: [rows][Hq][128] or NULL with q_out NULL; k, v: [rows][Hkv][128], of dtype,
+ *   device memory, rows q_stride, k_stride, v_stride elements apart (views of one fused
+ *   projection), 16-byte aligned rows.  q_out: [rows][Hq][128] bf16, 16-byte aligned.
+ *   HSQ_DEVERR_POS: a position >= max_pos (clamped); HSQ_DEVERR_PAGE: a slot
+ *   outside the pool (not stored).
+ *   Errors: HSQ_ERR_INVALID (NULL, rows < 1, a stride below a row's length or
+ *   alignment, another current device than the context's), HSQ_ERR_CUDA.
+ */
+hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const void* q, const void* k, const void* v,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride, hsq_dtype dtype,
+                          const int32_t* pos, const int64_t* slots, void* q_out, hsq_stream_t stream);
+
+/*
+ * hsq_shared_attn -- attention of a batch whose requests share a prefix.  The prefix's
+ *   keys and values are read once for all requests.  Row i = q_start[b] + j of
+ *   request b, query head jq of KV head h = jq / (Hq / Hkv): one softmax, scale
+ *   1/sqrt(128), over the prefix's tokens [0, prefix_len) and the request's own
+ *   tokens s <= lens[b] - n_b + j (n_b = q_start[b + 1] - q_start[b]; s >= 0).
+ *   out[i][jq] the weighted values, lse[i][jq] (optional) the natural log of the sum of
+ *   the exponentials (to merge with attention over other tokens).  A row without
+ *   any token to see gets out = 0 and lse = -inf.  Rows from q_start[B] on are
+ *   left as they were.
+ *   q: [rows][Hq][128] bf16, rotated (q_out of hsq_page_write); out: the
+ *   same shape and type; lse: [rows][Hq] f32 or NULL; q_start [B + 1], lens [B],
+ *   table [B][width], prefix [ceil(prefix_len / P)] (NULL with prefix_len 0):
+ *   int32; all device memory.  max_new: the largest n_b of the step.
+ *   workspace: device memory of hsq_shared_attn_workspace_size bytes, 256-byte
+ *   aligned, caller-owned; its contents are not needed before or after, but calls that may run at the
+ *   same time need one each.  Products are bf16 with fp32 accumulation; softmax
+ *   weights are rounded to bf16 for the product with the values, sums and statistics are fp32.
+ *   Keys and values of the tokens seen are expected finite: a value that is not may
+ *   reach every row of its request (of the batch, when in the prefix).  What
+ *   the pages hold past a request's length does not matter.
+ *   HSQ_DEVERR_PAGE: a page id outside the pool (its tokens are not attended to);
+ *   HSQ_DEVERR_LEN: lens[b] above width * P, negative or below n_b (clamped), q_start not
+ *   ascending in [0, rows] or n_b above max_new (that request's rows are not
+ *   written); HSQ_DEVERR_WAIT as for hsq_prefill.
+ *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
+ *   HSQ_MAX_REQUESTS)], rows, width or max_new < 1, prefix_len < 0, alignment, a
+ *   small workspace, another current device than the context's), HSQ_ERR_CUDA.
+ */
+hsq_status hsq_shared_attn_workspace_size(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new,
+                                          size_t* bytes);
+hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, int width, int prefix_len,
+                           int max_new, const void* q, const int32_t* q_start, const int32_t* lens,
+                           const int32_t* table, const int32_t* prefix, void* out, float* lse_opt, void* workspace,
+                           size_t workspace_bytes, hsq_stream_t stream);
 
 /* hsq_last_error -- text of the last error of ctx (or of the process when ctx is NULL). */
 const char* hsq_last_error(const hsq_ctx* ctx);
