@@ -138,8 +138,7 @@ void device_codebook(float out[kCodebookFloats]) {
         }
     };
     static const Levels levels;
-    const auto &c4 = levels.c4, &t4 = levels.t4;
-    const auto &c3 = levels.c3, &t3 = levels.t3;
+    const double *c4 = levels.c4, *t4 = levels.t4, *c3 = levels.c3, *t3 = levels.t3;
     std::memset(out, 0, sizeof(float) * kCodebookFloats);
     for (int i = 0; i < 16; ++i) out[i] = (float)c4[i];
     for (int i = 0; i < 15; ++i) out[16 + i] = (float)t4[i];
