@@ -1,4 +1,39 @@
 // Attention of a batch whose requests share a prefix (hsq_shared_attn).
+//
+// For row i of request b (token j of its n new ones) and query head jq of KV head
+// h: one softmax, scale 1/sqrt(128), over the prefix's tokens and the request's own
+// tokens s <= len - n + j.  A softmax over the union of two key sets is the
+// weighted sum of the softmaxes over each: with m, l, o the maximum, the sum of
+// exp(x - m) and the sum of exp(x - m) v of a part,
+//     out = sum_p exp(m_p - M) o_p / sum_p exp(m_p - M) l_p,   M = max_p m_p,
+// so the prefix is read once for all rows of the batch, each request's own pages
+// once for its rows, and the parts are joined at the end.
+//
+// Rows.  The r = Hq / Hkv query heads of a KV head and the rows of the batch
+// make one row index (token * r + head), so a tile of 128 rows holds
+// floor(128 / r) tokens of ANY requests for the prefix: the tensor cores see full
+// tiles in a decode step too.
+//
+// Three kernels, at most two of them in a call besides the prefix's:
+//   prefix  shared_tc_kernel<false>: pairs of 128-row tiles x the prefix's
+//           128-key tiles on the tensor cores, the whole (KV head, pair, key tile)
+//           space cut into equal runs, one per CTA (one CTA per SM); every run
+//           leaves its parts (m, l, o in fp32) in the workspace;
+//   own     shared_few_kernel for requests of few rows (n r <= 16, the decode step): one
+//           cluster per (request, KV head), warps stream keys and values from
+//           the pages straight into mma.sync fragments (bound by HBM: 16 rows are too
+//           few for a 128-row tile to matter);
+//           shared_tc_kernel<true> for requests with more rows: one CTA per
+//           (request, KV head, pair of row tiles), causal.
+//   Both own kernels read the prefix's parts of their rows, join them with their own and
+//   write the result.  They are launched with programmatic serialization: their own keys are
+//   read while the prefix kernel finishes, its parts only after griddepcontrol.wait.
+//
+// Rounding: q, k and v are bf16, products exact, sums fp32; the softmax weights are rounded to
+// bf16 for the product with the values (an error of 2^-9 of each weight at most, random over
+// the keys, where the output's own rounding is 2^-9 of the result), l sums
+// them before that rounding.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -9,15 +44,25 @@
 
 namespace {
 
+using namespace hsq_tc;
+
+constexpr int kFewRows = 16;                    // rows (tokens x r) of a request up to which the few-rows kernel takes it
+constexpr int kTileRows = 128, kTileKeys = 128;
+constexpr float kRaise = 8.f;                   // log2 units a logit may exceed the running maximum by before o is rescaled
+
 struct SharedArgs {
     const uint16_t *q, *pk, *pv;
     const int32_t *q_start, *lens, *table, *prefix;
     uint16_t* out; float* lse;
-    int rows, B, width, prefix_len, max_new, n_pages, page_n, Hq, Hkv;
+    int rows, B, width, prefix_len, max_new, n_pages, page_n, page_shift, Hq, Hkv, r;
+    int tpt;       // tokens of a row tile: 128 / r
+    int runs;      // CTAs of the prefix kernel
+    float* part_o;   // [slot][2 streams][128 rows][128]
+    float2* part_ml; // [slot][2 streams][128 rows]: maximum (of q.k, unscaled), sum
     int* err;
 };
 
-// Request b's rows and own tokens, checked: rows [first, first + n), own tokens len.
+// Request b's rows and own tokens, checked: rows [first, first + n), own tokens [0, len).
 struct Request { int first, n, len; };
 
 __device__ __forceinline__ Request request_of(const SharedArgs& a, int b, int& bad) {
@@ -27,69 +72,879 @@ __device__ __forceinline__ Request request_of(const SharedArgs& a, int b, int& b
     r.n = e - s;
     if (s < 0 || e < s || e > a.rows || r.n > a.max_new) {
         bad |= HSQ_DEVERR_LEN;
-        r.n = 0;
+        r.first = r.n = 0;
     }
     const int len = a.lens[b];
-    const long long cap = (long long)a.width * a.page_n;
+    const long long cap = (long long)a.width << a.page_shift;
     r.len = (int)min((long long)max(len, 0), cap);
     if (len != r.len || r.len < r.n) bad |= HSQ_DEVERR_LEN;
     return r;
 }
 
-// One warp per (row, query head): lane l holds dims 4 l .. 4 l + 3, keys one after another.
-__global__ void __launch_bounds__(kThreads) shared_attn_simple_kernel(SharedArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long w = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int row = (int)(w / a.Hq), jq = (int)(w % a.Hq), h = jq / (a.Hq / a.Hkv);
-    if (row >= a.rows) return;
-    int lo = 0, hi = a.B;  // the last b with q_start[b] <= row
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_start[mid] <= row) lo = mid; else hi = mid;
-    }
+// ---- the prefix's work: key tiles of (KV head, pair of row tiles), cut into equal runs ----
+
+struct PrefixPlan {
+    int tiles, pairs, steps;  // row tiles in use, pairs of them, key tiles
+    long long work;           // Hkv * pairs * steps
+};
+
+__device__ __forceinline__ PrefixPlan prefix_plan(const SharedArgs& a) {
+    PrefixPlan p;
+    const int live = min(max(a.q_start[a.B], 0), a.rows);
+    p.tiles = (live + a.tpt - 1) / a.tpt;
+    p.pairs = (p.tiles + 1) >> 1;
+    p.steps = (a.prefix_len + kTileKeys - 1) / kTileKeys;
+    p.work = (long long)a.Hkv * p.pairs * p.steps;
+    return p;
+}
+
+// run c covers the steps [c work / runs, (c + 1) work / runs); an item's segment in run c keeps its
+// parts in slot item + c (segments in order raise one of the two by one, so slots are unique)
+__device__ __forceinline__ long long run_begin(const PrefixPlan& p, int runs, int c) { return p.work * c / runs; }
+__device__ __forceinline__ int run_of(const PrefixPlan& p, int runs, long long w) {
+    return (int)(((w + 1) * runs - 1) / p.work);
+}
+
+// The parts of one row (token, head jj of KV head h): indices [at + k * step], k < n, of part_ml rows
+struct RowParts { size_t at; size_t step; int n; };
+
+__device__ __forceinline__ RowParts row_parts(const SharedArgs& a, const PrefixPlan& p, int h, int token, int jj) {
+    const int tile = token / a.tpt, pair = tile >> 1, stream = tile & 1;
+    const int row = (token - tile * a.tpt) * a.r + jj;
+    const long long item = (long long)h * p.pairs + pair, w0 = item * p.steps;
+    const int c0 = run_of(p, a.runs, w0), c1 = run_of(p, a.runs, w0 + p.steps - 1);
+    // a pair of one tile has its key tiles dealt to both streams
+    const bool split = tile == p.tiles - 1 && !(tile & 1);
+    RowParts x;
+    x.at = ((size_t)(item + c0) * 2 + stream) * kTileRows + row;
+    x.step = split ? kTileRows : 2 * kTileRows;
+    x.n = (c1 - c0 + 1) * (split ? 2 : 1);
+    return x;
+}
+
+// a bounded wait of a whole warp: true when it ended in time for every lane
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(kFull, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// ---------------------------------------------------------------------------------------
+// Tensor-core kernel.  One CTA per SM, 10 warps: softmax warps 0-3 (stream 0) and 4-7
+// (stream 1), warp 8 loads, warp 9 issues the MMAs.  A stream is a 128-row query tile with
+// its S / P and O in tensor memory.  The two streams either hold two row tiles and share every
+// key tile (so keys and values are loaded once for 256 rows), or, when only one row tile is
+// left, hold the same rows and take the key tiles in turn.  While one stream's softmax
+// runs, the tensor cores work for the other.
+//   shared memory: ring of five 32 KB tiles K0 V0 K1 V1 ... (TMA, 128-byte swizzle), two Q tiles;
+//   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kTcThreads = 320, kStages = 5;
+constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
+constexpr uint32_t kOffQ = kStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
+// barriers: full[5] | empty[5] | q_full[2] | s_full[2] | p_full[2] | o_full[2] | x_full
+constexpr int kTcBars = 2 * kStages + 9;
+constexpr uint32_t kOffMask = kOffBars + 8 * (kTcBars + 1);        // [8] pages of a key tile that lie in the pool
+constexpr uint32_t kTcSmem = kOffMask + 32 + 16 + 1024;      // + TMEM address, alignment
+
+// One run of key tiles [n0, n1) of an item.
+struct Segment {
+    int h, item;
+    int tok[2];        // first token of each stream's tile
+    int toks[2];       // its tokens
+    int n0, n1, end[2];
+    bool split;
+    int klen;          // keys in all
+    const int32_t* ids;  // page ids
+};
+
+// keys that token `t` of the request sees (own), or all (prefix)
+template <bool kOwn>
+__device__ __forceinline__ int key_limit(const Request& rq, int klen, int t) {
+    return kOwn ? min(klen, rq.len - rq.n + (t - rq.first) + 1) : klen;
+}
+
+template <bool kOwn>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    shared_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ SharedArgs a) {
+    extern __shared__ uint8_t tc_raw[];
+    const uint32_t raw = smem_addr(tc_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = tc_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full = base + kOffBars, empty = full + 8 * kStages, q_full = empty + 8 * kStages;
+    const uint32_t s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, x_full = o_full + 16;
+    volatile uint32_t* s_mask = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask);
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask + 32);
     int bad = 0;
-    const Request rq = request_of(a, lo, bad);
-    if (bad && lane == 0) atomicOr(a.err, bad);
-    if (row < rq.first || row >= rq.first + rq.n) return;
-    const int own = min(rq.len, max(0, rq.len - rq.n + (row - rq.first) + 1));
-    const size_t at = ((size_t)row * a.Hq + jq) * kDim + 4 * lane;
-    const uint2 qw = *reinterpret_cast<const uint2*>(a.q + at);
-    float q[4] = {__uint_as_float(qw.x << 16), __uint_as_float(qw.x & 0xFFFF0000u), __uint_as_float(qw.y << 16),
-                  __uint_as_float(qw.y & 0xFFFF0000u)};
+
+    // ---- what this CTA works on ----
+    Request rq{0, 0, 0};
+    PrefixPlan plan = prefix_plan(a);
+    long long w = 0, w_end = 0;
+    int unit = 0;
+    const int32_t* own_ids = nullptr;
+    bool have = true;
+    if (kOwn) {
+        // pair ids: request b's start at q_start[b] / (2 tpt) + b, which leaves room for all of them; the last ids first
+        // (later tokens see more keys)
+        const int two = 2 * a.tpt, id = (int)(gridDim.y - 1 - blockIdx.y);
+        int below = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kTcThreads) {
+            const int b = b0 + tid;
+            below += __syncthreads_count(b < a.B && max(a.q_start[b], 0) / two + b <= id);
+        }
+        const int b = max(below - 1, 0);
+        rq = request_of(a, b, bad);
+        unit = id - (max(a.q_start[b], 0) / two + b);
+        have = below > 0 && rq.n * a.r > kFewRows && unit * two < rq.n;
+        own_ids = a.table + (size_t)b * a.width;
+    } else {
+        w = run_begin(plan, a.runs, blockIdx.x);
+        w_end = run_begin(plan, a.runs, blockIdx.x + 1);
+        have = w < w_end;
+    }
+    if (!kOwn) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!have) {
+        if (kOwn) {
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // (a grid that ends has seen its predecessor end)
+        }
+        return;
+    }
+
+    // the next segment; false when there is none
+    auto next = [&](long long& w, Segment& s) {
+        if (w >= w_end) return false;
+        if (kOwn) {
+            s.h = blockIdx.x;
+            s.item = 0;
+            const int left = rq.n - unit * 2 * a.tpt;  // tokens from this pair's first on
+            s.split = left <= a.tpt;
+            s.toks[0] = min(left, a.tpt);
+            s.toks[1] = s.split ? s.toks[0] : min(left - a.tpt, a.tpt);
+            s.tok[0] = rq.first + unit * 2 * a.tpt;
+            s.tok[1] = s.split ? s.tok[0] : s.tok[0] + a.tpt;
+            s.klen = max(0, key_limit<true>(rq, rq.len, s.tok[1] + s.toks[1] - 1));
+            s.ids = own_ids;
+            s.n0 = 0;
+            s.n1 = (s.klen + kTileKeys - 1) / kTileKeys;
+            const int l0 = max(0, key_limit<true>(rq, s.klen, s.tok[0] + s.toks[0] - 1));
+            s.end[0] = (l0 + kTileKeys - 1) / kTileKeys;
+            s.end[1] = s.n1;
+            w = w_end;
+        } else {
+            s.item = (int)(w / plan.steps);
+            s.h = s.item / plan.pairs;
+            const int pair = s.item - s.h * plan.pairs;
+            s.split = 2 * pair + 1 == plan.tiles;
+            const int live = min(max(a.q_start[a.B], 0), a.rows);
+            s.tok[0] = 2 * pair * a.tpt;
+            s.tok[1] = s.split ? s.tok[0] : s.tok[0] + a.tpt;
+            s.toks[0] = min(a.tpt, live - s.tok[0]);
+            s.toks[1] = min(a.tpt, live - s.tok[1]);
+            s.klen = a.prefix_len;
+            s.ids = a.prefix;
+            s.n0 = (int)(w - (long long)s.item * plan.steps);
+            s.n1 = (int)min((long long)plan.steps, s.n0 + (w_end - w));
+            s.end[0] = s.end[1] = s.n1;
+            w += s.n1 - s.n0;
+        }
+        return true;
+    };
+    if (kOwn) w_end = 1;
+    // key tiles that stream s takes in a segment
+    auto tiles_of = [](const Segment& s, int st) {
+        if (!s.split) return s.end[st] - s.n0;
+        return (s.n1 - s.n0 + 1 - st) >> 1;
+    };
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 128);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        mbar_init(x_full, 128);
+        mbar_init_fence();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_addr((const void*)s_tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    bool ok = true;
+    Segment s;
+
+    if (warp == 8) {
+        // ---- loads: per key tile the K pages, then the V pages (lane i: page i of the tile) ----
+        int load = 0, step = 0;
+        const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
+        while (ok && next(w, s)) {
+#pragma unroll 1
+            for (int n = s.n0; n < s.n1 && ok; ++n, ++step) {
+                const int nk = min(kTileKeys, s.klen - n * kTileKeys), np = (nk + a.page_n - 1) >> a.page_shift;
+                int id = -1;
+                if (lane < np) id = s.ids[((n * kTileKeys) >> a.page_shift) + lane];
+                const bool in = lane < np && id >= 0 && id < a.n_pages;
+                const uint32_t mask = __ballot_sync(kFull, in);
+                if (mask != (1u << np) - 1u) bad |= HSQ_DEVERR_PAGE;
+                // (a page outside the pool is read past the map's extent: zeros, masked in the softmax)
+                const int y = in ? (id * a.Hkv + s.h) << a.page_shift : (a.n_pages * a.Hkv) << a.page_shift;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] *= kLogitScaleLog2;
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    auto run = [&](const int32_t* ids, int count) {
-        for (int s = 0; s < count; ++s) {
-            const int id = ids[s / a.page_n];
-            if (id < 0 || id >= a.n_pages) {
-                if (lane == 0) atomicOr(a.err, HSQ_DEVERR_PAGE);
-                continue;
+                for (int kv = 0; kv < 2; ++kv, ++load) {
+                    const int st = load % kStages, turn = load / kStages;
+                    if (turn > 0) ok = warp_wait(empty + 8 * st, (turn - 1) & 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (!kv) s_mask[step & 7] = mask;
+                        mbar_expect_tx(full + 8 * st, np * page_bytes);
+                    }
+                    __syncwarp();
+                    if (lane < np) {
+                        const uint32_t dst = base + st * kTileBytes + lane * half_page;
+                        const void* map = kv ? &mv : &mk;
+                        tma_2d(dst, map, 0, y, full + 8 * st);
+                        tma_2d(dst + kHalfBytes, map, 64, y, full + 8 * st);
+                    }
+                }
             }
-            const size_t k0 = (((size_t)id * a.Hkv + h) * a.page_n + s % a.page_n) * kDim + 4 * lane;
-            const uint2 kw = *reinterpret_cast<const uint2*>(a.pk + k0), vw = *reinterpret_cast<const uint2*>(a.pv + k0);
-            float x = q[0] * __uint_as_float(kw.x << 16);
-            x = fmaf(q[1], __uint_as_float(kw.x & 0xFFFF0000u), x);
-            x = fmaf(q[2], __uint_as_float(kw.y << 16), x);
-            x = fmaf(q[3], __uint_as_float(kw.y & 0xFFFF0000u), x);
+        }
+        if (!ok)  // a wait ran out: see the copies in flight land before the CTA ends
+            for (int l = max(0, load - kStages); l < load; ++l) mbar_wait(full + 8 * (l % kStages), (l / kStages) & 1);
+    } else if (warp == 9) {
+        // ---- MMAs ----
+        int load = 0, q_at[2] = {0, 0}, p_at[2] = {0, 0};
+        const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
+        auto load_q = [&](const Segment& s) {
+            if (lane) return;
+            for (int st = 0; st < 2; ++st) {
+                if (tiles_of(s, st) <= 0) continue;
+                const uint32_t dst = base + kOffQ + st * kTileBytes, bar = q_full + 8 * st;
+                mbar_expect_tx(bar, q_bytes);
+                tma_3d(dst, &mq, 0, s.h * a.r, s.tok[st], bar);
+                tma_3d(dst + kHalfBytes, &mq, 64, s.h * a.r, s.tok[st], bar);
+            }
+        };
+        bool more = next(w, s);
+        bool pending = more;  // a query tile on its way
+        if (more) load_q(s);
+        while (more && ok) {
+            const int lag = s.split ? 2 : 1, first = load;
+            pending = false;
+            int v_seen = s.n0 - 1;  // the last value tile waited for
+            for (int st = 0; st < 2 && ok; ++st)
+                if (tiles_of(s, st) > 0) ok = warp_wait(q_full + 8 * st, q_at[st]++ & 1);
+#pragma unroll 1
+            for (int n = s.n0; n < s.n1 + lag && ok; ++n) {
+                const int np = n - lag;  // the tile whose P V is due
+                const int kl = first + 2 * (n - s.n0), vl = first + 2 * (np - s.n0) + 1;
+                const uint32_t ks = base + (kl % kStages) * kTileBytes, vs = base + (vl % kStages) * kTileBytes;
+                if (n < s.n1) ok = warp_wait(full + 8 * (kl % kStages), (kl / kStages) & 1);
+#pragma unroll 1
+                for (int st = 0; st < 2 && ok; ++st) {
+                    if (s.split && ((n - s.n0) & 1) != st) continue;
+                    if (np >= s.n0 && np < s.end[st]) {
+                        ok = warp_wait(p_full + 8 * st, p_at[st]++ & 1);
+                        const int nk = min(kTileKeys, s.klen - np * kTileKeys);
+                        if (ok && v_seen < np) {
+                            v_seen = np;
+                            ok = warp_wait(full + 8 * (vl % kStages), (vl / kStages) & 1);
+                            if (nk & 15) {  // the rows between the last key and the next multiple of 16: stale, weight 0, must be finite
+                                const int z = (16 - (nk & 15)) * 16;  // 16-byte chunks in both halves
+                                for (int i = lane; i < z; i += 32) {
+                                    const int rowi = nk + (i >> 4), c = i & 15;
+                                    *reinterpret_cast<uint4*>(gbase + (vs - base) + (c >> 3) * kHalfBytes + rowi * 128 +
+                                                              (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                }
+                                fence_async_smem();
+                                __syncwarp();
+                            }
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128);
+                            const uint32_t dO = tmem + 256 + 128 * st, pa = tmem + 128 * st;
+                            const uint64_t dv = sw128_mn_desc(vs, kHalfBytes);
+                            const bool begun = np > s.n0 + (s.split ? st : 0);
+                            if (nk == kTileKeys) {
 #pragma unroll
-            for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
-            const float mn = fmaxf(m, x), c = exp2f(m - mn), p = exp2f(x - mn);
-            m = mn;
-            l = fmaf(l, c, p);
-            o[0] = fmaf(o[0], c, p * __uint_as_float(vw.x << 16));
-            o[1] = fmaf(o[1], c, p * __uint_as_float(vw.x & 0xFFFF0000u));
-            o[2] = fmaf(o[2], c, p * __uint_as_float(vw.y << 16));
-            o[3] = fmaf(o[3], c, p * __uint_as_float(vw.y & 0xFFFF0000u));
+                                for (int k = 0; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
+                            } else {
+                                for (int k = 0; k < (nk + 15) >> 4; ++k)
+                                    mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
+                            }
+                        }
+                    }
+                    if (lane == 0 && np >= s.n0 && (s.split || st == 1)) mma_commit(empty + 8 * (vl % kStages));
+                    if (n < s.end[st]) {
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const int nk = min(kTileKeys, s.klen - n * kTileKeys);
+                            const uint32_t idS = idesc_bf16_f32(128, (nk + 15) & ~15), dS = tmem + 128 * st;
+                            const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(ks);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                                mma_bf16(dS, dq + o, dk + o, idS, k > 0);
+                            }
+                            mma_commit(s_full + 8 * st);
+                        }
+                    }
+                    if (lane == 0 && n < s.n1 && (s.split || st == 1)) mma_commit(empty + 8 * (kl % kStages));
+                }
+            }
+            load += 2 * (s.n1 - s.n0);
+            if (ok && lane == 0 && s.n1 > s.n0) {  // (a stream without a tile waits too: it may write to the ring)
+                mma_commit(o_full);
+                mma_commit(o_full + 8);
+            }
+            more = next(w, s);
+            pending = more && ok;
+            if (pending) load_q(s);  // (every S of the segment is done: its P has been seen)
+        }
+        if (!ok && pending)
+            for (int st = 0; st < 2; ++st)
+                if (tiles_of(s, st) > 0) mbar_wait(q_full + 8 * st, q_at[st] & 1);
+    } else {
+        // ---- softmax: thread = row of its stream's tile ----
+        const int st = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + 128 * st, tO = tmem + lanes + 256 + 128 * st;
+        int s_at = 0, o_at = 0, step0 = 0;
+        while (ok && next(w, s)) {
+            const int own_token = row / a.r;
+            const bool live = own_token < s.toks[st];
+            const bool idle = 32 * (warp & 3) >= s.toks[st] * a.r;  // (warp-uniform) no row of this warp in use
+            const int lim = live ? key_limit<kOwn>(rq, s.klen, s.tok[st] + own_token) : 0;
+            const int lim_min = key_limit<kOwn>(rq, s.klen, s.tok[st]);
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int n = s.n0 + (s.split ? st : 0); n < s.end[st]; n += s.split ? 2 : 1) {
+                ok = warp_wait(s_full + 8 * st, s_at++ & 1);
+                if (!ok) break;
+                if (!idle) {
+                    tc_fence_after();
+                    float x[2][64];
+                    tmem_ld64(tS, x[0]);
+                    tmem_ld64(tS + 64, x[1]);
+                    const int nk = min(kTileKeys, s.klen - n * kTileKeys), np = (nk + a.page_n - 1) >> a.page_shift;
+                    const uint32_t mask = s_mask[(step0 + n - s.n0) & 7];
+                    if ((n + 1) * kTileKeys > lim_min || mask != (1u << np) - 1u) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (n * kTileKeys + c >= lim || !((mask >> (c >> a.page_shift)) & 1u)) x[c >> 6][c & 63] = -INFINITY;
+                    }
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c >> 6][c & 63]);
+                    const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    const bool raise = mn * kLogitScaleLog2 > m * kLogitScaleLog2 + kRaise;  // (the first key raises from -inf)
+                    if (__any_sync(kFull, raise)) {
+                        const float to = raise ? mn : m;
+                        const float alpha = raise ? (m == -INFINITY ? 0.f : ex2_approx((m - to) * kLogitScaleLog2)) : 1.f;
+                        m = to;
+                        l *= alpha;
+                        if (n >= s.n0 + (s.split ? 2 : 1)) {  // O holds the tiles before (S of this tile follows their P V)
+#pragma unroll 1
+                            for (int c0 = 0; c0 < 128; c0 += 32) {
+                                float o[32];
+                                tmem_ld32(tO + c0, o);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) o[c] *= alpha;
+                                tmem_st32(tO + c0, o);
+                            }
+                        }
+                    }
+                    const float off = m == -INFINITY ? 0.f : m * kLogitScaleLog2;
+                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const float e0 = ex2_approx(fmaf(x[hf][c], kLogitScaleLog2, -off));
+                            const float e1 = ex2_approx(fmaf(x[hf][c + 1], kLogitScaleLog2, -off));
+                            l4[c & 2] += e0;
+                            l4[(c & 2) + 1] += e1;
+                            p[c >> 1] = pack_bf16(e0, e1);
+                        }
+                        tmem_st32_nowait(tS + 32 * hf, p);
+                    }
+                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                mbar_arrive(p_full + 8 * st);
+            }
+            if (!ok) break;
+            const bool any = tiles_of(s, st) > 0;
+            if (s.n1 > s.n0) ok = warp_wait(o_full + 8 * st, o_at++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (!kOwn) {
+                const size_t at = ((size_t)(s.item + blockIdx.x) * 2 + st) * kTileRows + row;
+                if (live) a.part_ml[at] = make_float2(m, l);
+                if (any && !idle) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        float o[32];
+                        tmem_ld32(tO + c0, o);
+                        if (live) {
+                            float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128 + c0);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) dst[c >> 2] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                        }
+                    }
+                }
+            } else {
+                // join: the two streams of a split pair, then the prefix's parts
+                float* xo = reinterpret_cast<float*>(gbase);  // [128 dims][128 rows] of stream 1 (the ring is at rest)
+                float2* xml = reinterpret_cast<float2*>(gbase + 2 * kTileBytes);
+                float w_me = 1.f, w_ot = 0.f, M = m, L = l;
+                if (s.split) {
+                    if (st == 1) {
+                        xml[row] = make_float2(m, l);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            float o[32];
+                            if (any) tmem_ld32(tO + c0, o);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) xo[(c0 + c) * 128 + row] = any ? o[c] : 0.f;
+                        }
+                    }
+                    if (st == 1) {
+                        mbar_arrive(x_full);
+                        break;
+                    }
+                    ok = warp_wait(x_full, 0);
+                    if (!ok) break;
+                    const float2 ot = xml[row];
+                    M = fmaxf(m, ot.x);
+                    w_me = m == -INFINITY ? 0.f : ex2_approx((m - M) * kLogitScaleLog2);
+                    w_ot = ot.x == -INFINITY ? 0.f : ex2_approx((ot.x - M) * kLogitScaleLog2);
+                    L = l * w_me + ot.y * w_ot;
+                }
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                const int token = s.tok[st] + own_token, jj = row - own_token * a.r;
+                RowParts rp{0, 0, 0};
+                if (live && plan.work > 0) rp = row_parts(a, plan, s.h, token, jj);
+                float Mall = M;
+                for (int k = 0; k < rp.n; ++k) Mall = fmaxf(Mall, __ldcg(&a.part_ml[rp.at + k * rp.step]).x);
+                const float wm = M == -INFINITY ? 0.f : ex2_approx((M - Mall) * kLogitScaleLog2);
+                w_me *= wm;
+                w_ot *= wm;
+                L *= wm;
+                for (int k = 0; k < rp.n; ++k) {
+                    const float2 ml = __ldcg(&a.part_ml[rp.at + k * rp.step]);
+                    if (ml.y > 0.f) L += ml.y * ex2_approx((ml.x - Mall) * kLogitScaleLog2);
+                }
+                const float inv = L > 0.f ? 1.0f / L : 0.f;
+                if (live && a.lse)
+                    a.lse[(size_t)token * a.Hq + s.h * a.r + jj] = L > 0.f ? Mall * kRsqrtD + logf(L) : -INFINITY;
+#pragma unroll 1
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    float o[32];
+                    if (any) tmem_ld32(tO + c0, o);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        o[c] = w_me > 0.f ? o[c] * w_me : 0.f;
+                        if (w_ot > 0.f) o[c] = fmaf(xo[(c0 + c) * 128 + row], w_ot, o[c]);
+                    }
+                    if (live) {
+                        for (int k = 0; k < rp.n; ++k) {
+                            const size_t at = rp.at + k * rp.step;
+                            const float2 ml = __ldcg(&a.part_ml[at]);
+                            if (!(ml.y > 0.f)) continue;
+                            const float wp = ex2_approx((ml.x - Mall) * kLogitScaleLog2);
+                            const float4* src = reinterpret_cast<const float4*>(a.part_o + at * 128 + c0);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 v = __ldcg(src + (c >> 2));
+                                o[c] = fmaf(v.x, wp, o[c]);
+                                o[c + 1] = fmaf(v.y, wp, o[c + 1]);
+                                o[c + 2] = fmaf(v.z, wp, o[c + 2]);
+                                o[c + 3] = fmaf(v.w, wp, o[c + 3]);
+                            }
+                        }
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)token * a.Hq + s.h * a.r + jj) * 128 + c0);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8)
+                            dst[c >> 3] = make_uint4(
+                                pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
+                                pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv));
+                    }
+                }
+            }
+            tc_fence_before();  // (O has been read: the next segment's first P releases it)
+            step0 += s.n1 - s.n0;
+        }
+    }
+    if (!ok) bad |= HSQ_DEVERR_WAIT;
+    if (bad) atomicOr(a.err, bad);
+    tc_fence_before();
+    __syncthreads();
+    if (kOwn) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // (every thread: a grid that ends has seen its predecessor end)
+    }
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------------
+// Few rows: one cluster per (request, KV head), NT tiles of 8 rows (tokens x heads).  The
+// cluster's warps take groups of 16 keys in turn; a warp's fragments come straight from the
+// pages in 16-byte loads, without shared memory or barriers:
+//   S^T (16 keys x 8 rows) = K (A operand, 16 x 16) Q^T: the product over the 128 dims
+//     may take them in any order, so lane (g, t) reads dims [32 j + 8 t, + 8) of keys g and
+//     g + 8 (j = 0..3) and feeds two k-steps from each load; Q is read the same way;
+//   O^T (dims x 8 rows) += V^T (A) P^T (B): lane (g, t) reads dims [64 c + 8 g, + 8) of keys
+//     2t, 2t + 1, 2t + 8, 2t + 9 and interleaves pairs of keys with byte permutes; row g
+//     of MMA i is dim 8 g + i, row g + 8 dim 64 + 8 g + i.  P^T comes from S^T by two 8 x 8
+//     transposes (movmatrix).
+// So 16 rows cost two MMAs where 8 cost one, and a warp's bytes in flight are its
+// registers: the next group's keys are on their way while this one's values arrive.
+// Bound by HBM.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kFewWarps = 4, kFewThreads = 32 * kFewWarps;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};\n"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads) shared_few_kernel(const __grid_constant__ SharedArgs a) {
+    constexpr int kRows = 8 * NT;
+    __shared__ float s_o[kFewWarps][kRows][128];
+    __shared__ float2 s_ml[kFewWarps][kRows];
+    __shared__ float2 s_cta[kRows];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = blockIdx.x, splits = gridDim.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    int bad = 0;
+    const Request rq = request_of(a, b, bad);
+    const int rows = rq.n * a.r;
+    if (rows == 0 || rows > kFewRows) {  // (the same for the whole cluster)
+        if (bad && tid == 0) atomicOr(a.err, bad);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    const int32_t* ids = a.table + (size_t)b * a.width;
+    const int groups = (rq.len + 15) >> 4, stride = splits * kFewWarps;
+
+    uint32_t qf[NT][8][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int row = 8 * nt + g;
+        const bool in = row < rows;
+        const uint16_t* src = a.q + ((size_t)(rq.first + (in ? row / a.r : 0)) * a.Hq + h * a.r + (in ? row % a.r : 0)) * 128 + 8 * t;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 x = in ? *reinterpret_cast<const uint4*>(src + 32 * j) : make_uint4(0, 0, 0, 0);
+            qf[nt][2 * j][0] = x.x;
+            qf[nt][2 * j][1] = x.y;
+            qf[nt][2 * j + 1][0] = x.z;
+            qf[nt][2 * j + 1][1] = x.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int rr = 8 * nt + 2 * t + e;
+            lim[nt][e] = rr < rows ? min(rq.len, rq.len - rq.n + rr / a.r + 1) : 0;
+        }
+    }
+    float o[NT][8][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+    }
+    // offset of key 16 s in the pool, or -1 (no page there)
+    auto place = [&](int s) -> long long {
+        if (s >= groups) return -1;
+        const int id = ids[(16 * s) >> a.page_shift];
+        if (id < 0 || id >= a.n_pages) {
+            bad |= HSQ_DEVERR_PAGE;
+            return -1;
+        }
+        return ((((long long)id * a.Hkv + h) << a.page_shift) + ((16 * s) & (a.page_n - 1))) * 128;
+    };
+    uint4 kf[2][4];
+    // keys past the length (and of no page) read as zero, so that nothing stale enters a product
+    auto load_k = [&](int s, long long at) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bool in = at >= 0 && 16 * s + g + 8 * e < rq.len;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                kf[e][j] = in ? __ldcs(reinterpret_cast<const uint4*>(a.pk + at + (g + 8 * e) * 128 + 32 * j + 8 * t))
+                              : make_uint4(0, 0, 0, 0);
         }
     };
-    run(a.prefix, a.prefix_len);
-    run(a.table + (size_t)lo * a.width, own);
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), y = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-    *reinterpret_cast<uint2*>(a.out + at) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    if (a.lse && lane == 0) a.lse[(size_t)row * a.Hq + jq] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    int s = rank * kFewWarps + warp;
+    long long at = place(s);
+    if (s < groups) load_k(s, at);
+#pragma unroll 1
+    for (; s < groups; s += stride) {
+        const long long ahead = place(s + stride);
+        uint4 vf[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int key = 2 * t + (e & 1) + 8 * (e >> 1);
+            const bool in = at >= 0 && 16 * s + key < rq.len;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                vf[e][c] = in ? __ldcs(reinterpret_cast<const uint4*>(a.pv + at + key * 128 + 64 * c + 8 * g))
+                              : make_uint4(0, 0, 0, 0);
+        }
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mma_16816(x[nt], kf[0][j].x, kf[1][j].x, kf[0][j].y, kf[1][j].y, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+                mma_16816(x[nt], kf[0][j].z, kf[1][j].z, kf[0][j].w, kf[1][j].w, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+            }
+        if (s + stride < groups) load_k(s + stride, ahead);
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // key g + 8 (e >> 1), row 2 t + (e & 1)
+                if (at < 0 || 16 * s + g + 8 * (e >> 1) >= lim[nt][e & 1]) x[nt][e] = -INFINITY;
+                raise |= x[nt][e] * kLogitScaleLog2 > m[nt][e & 1] * kLogitScaleLog2 + kRaise;
+            }
+        if (__any_sync(kFull, raise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(m[nt][e], fmaxf(x[nt][e], x[nt][e + 2]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+                    const float alpha = mx == -INFINITY ? 1.f : ex2_approx((m[nt][e] - mx) * kLogitScaleLog2);
+                    m[nt][e] = mx;
+                    l[nt][e] *= alpha;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[nt][i][e] *= alpha;
+                        o[nt][i][e + 2] *= alpha;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float off = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1] * kLogitScaleLog2;
+                p[e] = ex2_approx(fmaf(x[nt][e], kLogitScaleLog2, -off));
+                l[nt][e & 1] += p[e];
+            }
+            pf[nt][0] = transpose_8x8(pack_bf16(p[0], p[1]));
+            pf[nt][1] = transpose_8x8(pack_bf16(p[2], p[3]));
+        }
+        const uint32_t* v[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) v[e][c] = reinterpret_cast<const uint32_t*>(&vf[e][c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
+            const uint32_t a0 = __byte_perm(v[0][0][i >> 1], v[1][0][i >> 1], sel);
+            const uint32_t a1 = __byte_perm(v[0][1][i >> 1], v[1][1][i >> 1], sel);
+            const uint32_t a2 = __byte_perm(v[2][0][i >> 1], v[3][0][i >> 1], sel);
+            const uint32_t a3 = __byte_perm(v[2][1][i >> 1], v[3][1][i >> 1], sel);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+        }
+        at = ahead;
+    }
+
+    // ---- join: the CTA's warps, the cluster's CTAs, the prefix's parts ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], d);
+            const int row = 8 * nt + 2 * t + e;
+            if (g == 0) s_ml[warp][row] = make_float2(m[nt][e], l[nt][e]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float4* dst = reinterpret_cast<float4*>(&s_o[warp][row][64 * c + 8 * g]);
+                dst[0] = make_float4(o[nt][0][e + 2 * c], o[nt][1][e + 2 * c], o[nt][2][e + 2 * c], o[nt][3][e + 2 * c]);
+                dst[1] = make_float4(o[nt][4][e + 2 * c], o[nt][5][e + 2 * c], o[nt][6][e + 2 * c], o[nt][7][e + 2 * c]);
+            }
+        }
+    }
+    if (bad) atomicOr(a.err, bad);
+    __syncthreads();
+    for (int row = 0; row < rows; ++row) {  // thread = dim
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, s_ml[w][row].x);
+        float L = 0.f, x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) {
+            const float2 ml = s_ml[w][row];
+            if (ml.y > 0.f) {
+                const float c = ex2_approx((ml.x - M) * kLogitScaleLog2);
+                L = fmaf(ml.y, c, L);
+                x = fmaf(s_o[w][row][tid], c, x);
+            }
+        }
+        s_o[0][row][tid] = x;  // (this thread alone reads and writes the column)
+        if (tid == 0) s_cta[row] = make_float2(M, L);
+    }
+    if (splits > 1) cl.sync(); else __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PrefixPlan plan = prefix_plan(a);
+    for (int row = rank; row < rows; row += splits) {
+        const int token = rq.first + row / a.r, jj = row % a.r;
+        RowParts rp{0, 0, 0};
+        if (plan.work > 0) rp = row_parts(a, plan, h, token, jj);
+        float M = -INFINITY;
+        for (int k = 0; k < splits; ++k) M = fmaxf(M, cl.map_shared_rank(s_cta, k)[row].x);
+        for (int k = 0; k < rp.n; ++k) M = fmaxf(M, __ldcg(&a.part_ml[rp.at + k * rp.step]).x);
+        float L = 0.f, x = 0.f;
+        for (int k = 0; k < splits; ++k) {
+            const float2 ml = cl.map_shared_rank(s_cta, k)[row];
+            if (ml.y > 0.f) {
+                const float c = ex2_approx((ml.x - M) * kLogitScaleLog2);
+                L = fmaf(ml.y, c, L);
+                x = fmaf(cl.map_shared_rank(&s_o[0][row][tid], k)[0], c, x);
+            }
+        }
+#pragma unroll 4
+        for (int k = 0; k < rp.n; ++k) {
+            const size_t from = rp.at + k * rp.step;
+            const float2 ml = __ldcg(&a.part_ml[from]);
+            const float v = __ldcg(&a.part_o[from * 128 + tid]);
+            if (ml.y > 0.f) {
+                const float c = ex2_approx((ml.x - M) * kLogitScaleLog2);
+                L = fmaf(ml.y, c, L);
+                x = fmaf(v, c, x);
+            }
+        }
+        const size_t to = (size_t)token * a.Hq + h * a.r + jj;
+        a.out[to * 128 + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(L > 0.f ? x / L : 0.f));
+        if (a.lse && tid == 0) a.lse[to] = L > 0.f ? M * kRsqrtD + logf(L) : -INFINITY;
+    }
+    if (splits > 1) cl.sync();  // (the others may still read this CTA's part)
+}
+
+// ---- host side --------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// bf16 rows of 128, seen as boxes of 64 columns (128-byte swizzle)
+bool encode_rows(CUtensorMap* map, void* p, uint64_t rows, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {128, rows}, strides[1] = {256};
+    const cuuint32_t box[2] = {64, box_rows}, es[2] = {1, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// queries [rows][Hq][128]: a box is `tokens` tokens x the r heads of a KV head x 64 columns
+bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint32_t r, uint32_t tokens) {
+    const cuuint64_t dims[3] = {128, Hq, rows}, strides[2] = {256, 256 * Hq};
+    const cuuint32_t box[3] = {64, r, tokens}, es[3] = {1, 1, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// workspace: part_o, then part_ml, of Hkv * pairs + runs slots
+struct Parts { long long slots; size_t o_bytes, bytes; int runs; };
+
+Parts parts_of(const hsq_ctx* ctx, int rows, int prefix_len) {
+    Parts p{0, 0, 256, 0};
+    if (prefix_len == 0) return p;
+    const int tpt = kTileRows / ctx->r, tiles = (rows + tpt - 1) / tpt, pairs = (tiles + 1) / 2;
+    const long long items = (long long)ctx->cfg.n_kv_heads * pairs;
+    const long long work = items * ((prefix_len + kTileKeys - 1) / kTileKeys);
+    p.runs = (int)std::min<long long>(ctx->num_sms, work);
+    p.slots = items + p.runs;
+    p.o_bytes = (size_t)p.slots * 2 * kTileRows * 128 * 4;
+    p.bytes = p.o_bytes + (size_t)p.slots * 2 * kTileRows * 8;
+    return p;
+}
+
+cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster, bool after,
+                   void** args) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute at[2];
+    int n = 0;
+    if (cluster > 1) {
+        at[n].id = cudaLaunchAttributeClusterDimension;
+        at[n].val.clusterDim.x = cluster;
+        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (after) {
+        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    lc.attrs = at;
+    lc.numAttrs = n;
+    return cudaLaunchKernelExC(&lc, fn, args);
 }
 
 }  // namespace
@@ -101,7 +956,7 @@ hsq_status hsq_shared_attn_workspace_size(const hsq_ctx* ctx, int rows, int B, i
     if (!ctx || !bytes) return hsq::fail(nullptr, HSQ_ERR_INVALID, "ctx or bytes is NULL");
     if (rows < 1 || B < 1 || prefix_len < 0 || max_new < 1)
         return hsq::fail(nullptr, HSQ_ERR_INVALID, "rows, B and max_new must be positive, prefix_len not negative");
-    *bytes = 256;
+    *bytes = parts_of(ctx, rows, prefix_len).bytes;
     return HSQ_OK;
 }
 
@@ -121,20 +976,65 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     if (((uintptr_t)q | (uintptr_t)out) & 15u)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "q and out must be 16-byte aligned");
     if ((uintptr_t)workspace & 255u) return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace must be 256-byte aligned");
-    size_t need = 0;
-    if ((st = hsq_shared_attn_workspace_size(ctx, rows, B, prefix_len, max_new, &need)) != HSQ_OK) return st;
-    if (workspace_bytes < need)
+    const Parts parts = parts_of(ctx, rows, prefix_len);
+    if (workspace_bytes < parts.bytes)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace smaller than hsq_shared_attn_workspace_size");
     if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
-    SharedArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(pages->k),
-                 static_cast<const uint16_t*>(pages->v), q_start, lens, table, prefix, static_cast<uint16_t*>(out),
-                 lse_opt, rows, B, width, prefix_len, max_new, pages->n_pages, pages->page_n, ctx->cfg.n_q_heads,
-                 ctx->cfg.n_kv_heads, ctx->d_err};
-    const long long warps = (long long)rows * ctx->cfg.n_q_heads;
-    const int grid = (int)((warps * 32 + kThreads - 1) / kThreads);
-    shared_attn_simple_kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? HSQ_OK : hsq::cuda_fail(ctx, e, "shared_attn");
+    const int r = ctx->r, Hkv = ctx->cfg.n_kv_heads, tpt = kTileRows / r;
+    SharedArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.pk = static_cast<const uint16_t*>(pages->k);
+    a.pv = static_cast<const uint16_t*>(pages->v);
+    a.q_start = q_start; a.lens = lens; a.table = table; a.prefix = prefix;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse_opt;
+    a.rows = rows; a.B = B; a.width = width; a.prefix_len = prefix_len; a.max_new = max_new;
+    a.n_pages = pages->n_pages; a.page_n = pages->page_n;
+    a.page_shift = pages->page_n == 16 ? 4 : pages->page_n == 32 ? 5 : pages->page_n == 64 ? 6 : 7;
+    a.Hq = ctx->cfg.n_q_heads; a.Hkv = Hkv; a.r = r; a.tpt = tpt; a.runs = parts.runs;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + parts.o_bytes);
+    a.err = ctx->d_err;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool many = (long long)max_new * r > kFewRows;
+    CUtensorMap mq, mk, mv;
+    if (prefix_len > 0 || many) {
+        if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+        const uint64_t n = (uint64_t)pages->n_pages * Hkv * pages->page_n;
+        if (!encode_q(&mq, q, rows, a.Hq, r, tpt) || !encode_rows(&mk, pages->k, n, pages->page_n) ||
+            !encode_rows(&mv, pages->v, n, pages->page_n))
+            return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
+    }
+    cudaError_t e = cudaSuccess;
+    bool after = false;
+    void* tc_args[] = {&mq, &mk, &mv, &a};
+    void* few_args[] = {&a};
+    if (prefix_len > 0) {
+        const void* fn = (const void*)shared_tc_kernel<false>;
+        if ((e = hsq::raise_smem_limit(fn, ctx->device, kTcSmem)) != cudaSuccess)
+            return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(shared_attn)");
+        e = launch(fn, dim3(parts.runs), kTcThreads, kTcSmem, s, 1, false, tc_args);
+        if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn prefix");
+        after = true;
+    }
+    if (many) {
+        const void* fn = (const void*)shared_tc_kernel<true>;
+        if ((e = hsq::raise_smem_limit(fn, ctx->device, kTcSmem)) != cudaSuccess)
+            return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(shared_attn)");
+        const int ids = rows / (2 * tpt) + B;
+        if (ids > 65535) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
+        e = launch(fn, dim3(Hkv, ids), kTcThreads, kTcSmem, s, 1, after, tc_args);
+        if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn rows");
+        after = true;
+    }
+    int splits = 1;
+    while (splits < 8 && (long long)B * Hkv * splits < 3 * ctx->num_sms &&
+           (long long)width * pages->page_n > 16LL * kFewWarps * 4 * splits)
+        splits *= 2;
+    const void* fn = many || max_new * r > 8 ? (const void*)shared_few_kernel<2> : (const void*)shared_few_kernel<1>;
+    e = launch(fn, dim3(splits, Hkv, B), kFewThreads, 0, s, splits, after, few_args);
+    if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn few");
+    return HSQ_OK;
 }
 
 }  // extern "C"
