@@ -122,9 +122,19 @@ __device__ __forceinline__ RowParts row_parts(const SharedArgs& a, const PrefixP
     return x;
 }
 
-// a bounded wait of a whole warp: true when it ended in time for every lane
+// A bounded wait of a whole warp, by one lane: 32 lanes that poll one barrier are served one after
+// another (175 cycles against 40 when the phase is already complete); the warp barrier orders the others behind it.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(kFull, mbar_wait(bar, parity));
+    uint32_t ok = 0;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity);
+    __syncwarp();
+    return __shfl_sync(kFull, ok, 0) != 0;
+}
+
+// One arrival for the whole warp, after every lane's writes.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -132,9 +142,31 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// two fp32 lanes in one instruction
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // ---------------------------------------------------------------------------------------
-// Tensor-core kernel.  One CTA per SM, 10 warps: softmax warps 0-3 (stream 0) and 4-7
-// (stream 1), warp 8 loads, warp 9 issues the MMAs.  A stream is a 128-row query tile with
+// Tensor-core kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7
+// (stream 1), warp 8 loads, warp 9 issues the MMAs (10 and 11 only give their registers away:
+// 168 a thread at launch, then 208 for the softmax warps, whose row of 128 logits
+// lives in registers, and 88 for the others).  A stream is a 128-row query tile with
 // its S / P and O in tensor memory.  The two streams either hold two row tiles and share every
 // key tile (so keys and values are loaded once for 256 rows), or, when only one row tile is
 // left, hold the same rows and take the key tiles in turn.  While one stream's softmax
@@ -143,11 +175,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 //   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kTcThreads = 320, kStages = 5;
+constexpr int kTcThreads = 384, kStages = 5;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = kStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
-// barriers: full[5] | empty[5] | q_full[2] | s_full[2] | p_full[2] | o_full[2] | x_full
-constexpr int kTcBars = 2 * kStages + 9;
+// barriers: full[5] | empty[5] | q_full[2] | s_full[2] | p_full[2] | o_full[2] | p_half[2] | x_full
+constexpr int kTcBars = 2 * kStages + 11;
 constexpr uint32_t kOffMask = kOffBars + 8 * (kTcBars + 1);        // [8] pages of a key tile that lie in the pool
 constexpr uint32_t kTcSmem = kOffMask + 32 + 16 + 1024;      // + TMEM address, alignment
 
@@ -177,7 +209,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t* gbase = tc_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = base + kOffBars, empty = full + 8 * kStages, q_full = empty + 8 * kStages;
-    const uint32_t s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, x_full = o_full + 16;
+    const uint32_t s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, p_half = o_full + 16, x_full = p_half + 16;
     volatile uint32_t* s_mask = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask);
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask + 32);
     int bad = 0;
@@ -271,10 +303,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
-            mbar_init(p_full + 8 * i, 128);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(p_half + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
         }
-        mbar_init(x_full, 128);
+        mbar_init(x_full, 4);
         mbar_init_fence();
     }
     if (warp == 9) {
@@ -288,6 +321,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool ok = true;
     Segment s;
 
+    // (128 x 168 x 3 registers at launch: 2 x 128 x 208 + 128 x 88)
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
     if (warp == 8) {
         // ---- loads: per key tile the K pages, then the V pages (lane i: page i of the tile) ----
         int load = 0, step = 0;
@@ -357,8 +393,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int st = 0; st < 2 && ok; ++st) {
                     if (s.split && ((n - s.n0) & 1) != st) continue;
                     if (np >= s.n0 && np < s.end[st]) {
-                        ok = warp_wait(p_full + 8 * st, p_at[st]++ & 1);
-                        const int nk = min(kTileKeys, s.klen - np * kTileKeys);
+                        ok = warp_wait(p_half + 8 * st, p_at[st] & 1);
+                        const int nk = min(kTileKeys, s.klen - np * kTileKeys), ks16 = (nk + 15) >> 4;
                         if (ok && v_seen < np) {
                             v_seen = np;
                             ok = warp_wait(full + 8 * (vl % kStages), (vl / kStages) & 1);
@@ -374,43 +410,54 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                         if (!ok) break;
+                        // O += P V, the first 64 keys while the softmax still works on the others
+                        constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128);
+                        const uint32_t dO = tmem + 256 + 128 * st, pa = tmem + 128 * st;
+                        const uint64_t dv = sw128_mn_desc(vs, kHalfBytes);
+                        const bool begun = np > s.n0 + (s.split ? st : 0);
                         tc_fence_after();
-                        if (lane == 0) {
-                            constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128);
-                            const uint32_t dO = tmem + 256 + 128 * st, pa = tmem + 128 * st;
-                            const uint64_t dv = sw128_mn_desc(vs, kHalfBytes);
-                            const bool begun = np > s.n0 + (s.split ? st : 0);
-                            if (nk == kTileKeys) {
+                        if (elect_one()) {
 #pragma unroll
-                                for (int k = 0; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
-                            } else {
-                                for (int k = 0; k < (nk + 15) >> 4; ++k)
-                                    mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                if (k < ks16) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
                         }
+                        __syncwarp();
+                        ok = warp_wait(p_full + 8 * st, p_at[st]++ & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 4; k < 8; ++k)
+                                if (k < ks16) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+                            if (s.split || st == 1) mma_commit(empty + 8 * (vl % kStages));
+                        }
+                        __syncwarp();
                     }
-                    if (lane == 0 && np >= s.n0 && (s.split || st == 1)) mma_commit(empty + 8 * (vl % kStages));
                     if (n < s.end[st]) {
                         tc_fence_after();
-                        if (lane == 0) {
-                            const int nk = min(kTileKeys, s.klen - n * kTileKeys);
-                            const uint32_t idS = idesc_bf16_f32(128, (nk + 15) & ~15), dS = tmem + 128 * st;
-                            const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(ks);
+                        const int nk = min(kTileKeys, s.klen - n * kTileKeys);
+                        const uint32_t idS = idesc_bf16_f32(128, (nk + 15) & ~15), dS = tmem + 128 * st;
+                        const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(ks);
+                        if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
                                 mma_bf16(dS, dq + o, dk + o, idS, k > 0);
                             }
                             mma_commit(s_full + 8 * st);
+                            if (s.split || st == 1) mma_commit(empty + 8 * (kl % kStages));
                         }
+                        __syncwarp();
                     }
-                    if (lane == 0 && n < s.n1 && (s.split || st == 1)) mma_commit(empty + 8 * (kl % kStages));
                 }
             }
             load += 2 * (s.n1 - s.n0);
-            if (ok && lane == 0 && s.n1 > s.n0) {  // (a stream without a tile waits too: it may write to the ring)
-                mma_commit(o_full);
-                mma_commit(o_full + 8);
+            if (ok && s.n1 > s.n0) {  // (a stream without a tile waits too: it may write to the ring)
+                if (elect_one()) {
+                    mma_commit(o_full);
+                    mma_commit(o_full + 8);
+                }
+                __syncwarp();
             }
             more = next(w, s);
             pending = more && ok;
@@ -419,7 +466,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok && pending)
             for (int st = 0; st < 2; ++st)
                 if (tiles_of(s, st) > 0) mbar_wait(q_full + 8 * st, q_at[st] & 1);
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         // ---- softmax: thread = row of its stream's tile ----
         const int st = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -450,7 +499,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c >> 6][c & 63]);
+                    for (int c = 0; c < 128; c += 2)
+                        m4[(c >> 1) & 3] = fmaxf(fmaxf(m4[(c >> 1) & 3], x[c >> 6][c & 63]), x[c >> 6][(c & 63) + 1]);
                     const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     const bool raise = mn * kLogitScaleLog2 > m * kLogitScaleLog2 + kRaise;  // (the first key raises from -inf)
                     if (__any_sync(kFull, raise)) {
@@ -469,26 +519,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                         }
                     }
-                    const float off = m == -INFINITY ? 0.f : m * kLogitScaleLog2;
-                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float off = m == -INFINITY ? 0.f : -m * kLogitScaleLog2;
+                    const uint64_t off2 = pack2(off, off), scale2 = pack2(kLogitScaleLog2, kLogitScaleLog2);
+                    uint64_t l2[2] = {0, 0};
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         uint32_t p[32];
 #pragma unroll
                         for (int c = 0; c < 64; c += 2) {
-                            const float e0 = ex2_approx(fmaf(x[hf][c], kLogitScaleLog2, -off));
-                            const float e1 = ex2_approx(fmaf(x[hf][c + 1], kLogitScaleLog2, -off));
-                            l4[c & 2] += e0;
-                            l4[(c & 2) + 1] += e1;
+                            float e0, e1;
+                            unpack2(fma2(pack2(x[hf][c], x[hf][c + 1]), scale2, off2), e0, e1);
+                            e0 = ex2_approx(e0);
+                            e1 = ex2_approx(e1);
+                            l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pack2(e0, e1));
                             p[c >> 1] = pack_bf16(e0, e1);
                         }
                         tmem_st32_nowait(tS + 32 * hf, p);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        warp_arrive((hf ? p_full : p_half) + 8 * st);
                     }
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                    tmem_st_wait();
-                    tc_fence_before();
+                    float l_lo, l_hi;
+                    unpack2(add2(l2[0], l2[1]), l_lo, l_hi);
+                    l += l_lo + l_hi;
+                } else {
+                    warp_arrive(p_half + 8 * st);
+                    warp_arrive(p_full + 8 * st);
                 }
-                mbar_arrive(p_full + 8 * st);
             }
             if (!ok) break;
             const bool any = tiles_of(s, st) > 0;
@@ -527,7 +584,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     if (st == 1) {
-                        mbar_arrive(x_full);
+                        warp_arrive(x_full);
                         break;
                     }
                     ok = warp_wait(x_full, 0);
@@ -645,6 +702,7 @@ __global__ void __launch_bounds__(kFewThreads) shared_few_kernel(const __grid_co
     __shared__ float s_o[kFewWarps][kRows][128];
     __shared__ float2 s_ml[kFewWarps][kRows];
     __shared__ float2 s_cta[kRows];
+    __shared__ float4 s_x[kFewWarps][32];
     namespace cg = cooperative_groups;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = blockIdx.x, splits = gridDim.x, h = blockIdx.y, b = blockIdx.z;
@@ -835,37 +893,72 @@ __global__ void __launch_bounds__(kFewThreads) shared_few_kernel(const __grid_co
     }
     if (splits > 1) cl.sync(); else __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // This CTA's rows (every splits-th), one warp a row, or two or four warps where there are
+    // that few rows: lane k holds the weights of parts k, k + 32, ..., then the warp adds
+    // the parts up, a lane four dims.  Loads do not wait for one another but for that one step.
     const PrefixPlan plan = prefix_plan(a);
-    for (int row = rank; row < rows; row += splits) {
-        const int token = rq.first + row / a.r, jj = row % a.r;
+    const int mine = (rows - rank + splits - 1) / splits;                  // (rows > rank, or none)
+    const int per = mine == 1 ? kFewWarps : mine == 2 ? kFewWarps / 2 : 1;  // warps a row
+    for (int i0 = 0; i0 < mine; i0 += kFewWarps / per) {
+        const int i = i0 + warp / per, sub = warp % per;
+        const bool live = i < mine;
+        const int row = rank + (live ? i : 0) * splits, token = rq.first + row / a.r, jj = row % a.r;
         RowParts rp{0, 0, 0};
-        if (plan.work > 0) rp = row_parts(a, plan, h, token, jj);
+        if (live && plan.work > 0) rp = row_parts(a, plan, h, token, jj);
+        // parts: the cluster's CTAs 0 .. splits - 1, then the prefix's
+        const int n = live ? splits + rp.n : 0;
         float M = -INFINITY;
-        for (int k = 0; k < splits; ++k) M = fmaxf(M, cl.map_shared_rank(s_cta, k)[row].x);
-        for (int k = 0; k < rp.n; ++k) M = fmaxf(M, __ldcg(&a.part_ml[rp.at + k * rp.step]).x);
-        float L = 0.f, x = 0.f;
-        for (int k = 0; k < splits; ++k) {
-            const float2 ml = cl.map_shared_rank(s_cta, k)[row];
-            if (ml.y > 0.f) {
-                const float c = ex2_approx((ml.x - M) * kLogitScaleLog2);
-                L = fmaf(ml.y, c, L);
-                x = fmaf(cl.map_shared_rank(&s_o[0][row][tid], k)[0], c, x);
+        for (int k = lane; k < n; k += 32)
+            M = fmaxf(M, k < splits ? cl.map_shared_rank(s_cta, k)[row].x : __ldcg(&a.part_ml[rp.at + (k - splits) * rp.step]).x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, d));
+        float L = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            float wt = 0.f;  // weight of part k0 + lane
+            if (k0 + lane < n) {
+                const int k = k0 + lane;
+                const float2 ml = k < splits ? cl.map_shared_rank(s_cta, k)[row] : __ldcg(&a.part_ml[rp.at + (k - splits) * rp.step]);
+                if (ml.y > 0.f) {
+                    wt = ex2_approx((ml.x - M) * kLogitScaleLog2);
+                    L = fmaf(ml.y, wt, L);
+                }
+            }
+            const int stop = min(32, n - k0);
+#pragma unroll 8
+            for (int e = sub; e < stop; e += per) {
+                const float wk = __shfl_sync(kFull, wt, e);
+                const int k = k0 + e;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wk > 0.f)
+                    v = k < splits ? *reinterpret_cast<const float4*>(cl.map_shared_rank(&s_o[0][row][4 * lane], k))
+                                   : __ldcg(reinterpret_cast<const float4*>(a.part_o + (rp.at + (k - splits) * rp.step) * 128) + lane);
+                x.x = fmaf(v.x, wk, x.x);
+                x.y = fmaf(v.y, wk, x.y);
+                x.z = fmaf(v.z, wk, x.z);
+                x.w = fmaf(v.w, wk, x.w);
             }
         }
-#pragma unroll 4
-        for (int k = 0; k < rp.n; ++k) {
-            const size_t from = rp.at + k * rp.step;
-            const float2 ml = __ldcg(&a.part_ml[from]);
-            const float v = __ldcg(&a.part_o[from * 128 + tid]);
-            if (ml.y > 0.f) {
-                const float c = ex2_approx((ml.x - M) * kLogitScaleLog2);
-                L = fmaf(ml.y, c, L);
-                x = fmaf(v, c, x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(kFull, L, d);
+        if (per > 1) {
+            s_x[warp][lane] = x;
+            __syncthreads();
+            for (int w = 1; w < per; ++w) {
+                const float4 v = s_x[warp - sub + (sub + w) % per][lane];
+                x.x += v.x;
+                x.y += v.y;
+                x.z += v.z;
+                x.w += v.w;
             }
         }
-        const size_t to = (size_t)token * a.Hq + h * a.r + jj;
-        a.out[to * 128 + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(L > 0.f ? x / L : 0.f));
-        if (a.lse && tid == 0) a.lse[to] = L > 0.f ? M * kRsqrtD + logf(L) : -INFINITY;
+        if (live && sub == 0) {
+            const size_t to = (size_t)token * a.Hq + h * a.r + jj;
+            const float inv = L > 0.f ? 1.0f / L : 0.f;
+            *reinterpret_cast<uint2*>(a.out + to * 128 + 4 * lane) =
+                make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+            if (a.lse && lane == 0) a.lse[to] = L > 0.f ? M * kRsqrtD + logf(L) : -INFINITY;
+        }
     }
     if (splits > 1) cl.sync();  // (the others may still read this CTA's part)
 }
