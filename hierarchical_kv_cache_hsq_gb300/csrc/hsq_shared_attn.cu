@@ -122,15 +122,6 @@ __device__ __forceinline__ RowParts row_parts(const SharedArgs& a, const PrefixP
     return x;
 }
 
-// A bounded wait of a whole warp, by one lane: 32 lanes that poll one barrier are served one after
-// another (175 cycles against 40 when the phase is already complete); the warp barrier orders the others behind it.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok = 0;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity);
-    __syncwarp();
-    return __shfl_sync(kFull, ok, 0) != 0;
-}
-
 // One arrival for the whole warp, after every lane's writes.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     __syncwarp();
@@ -178,10 +169,22 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 constexpr int kTcThreads = 384, kStages = 5;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = kStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
-// barriers: full[5] | empty[5] | q_full[2] | s_full[2] | p_full[2] | o_full[2] | p_half[2] | x_full
-constexpr int kTcBars = 2 * kStages + 11;
+// barriers: full[5] | empty[5] | q_full[2] | s_full[2] | p_full[2] | o_full[2] | tail | x_full
+constexpr int kTcBars = 2 * kStages + 10;
 constexpr uint32_t kOffMask = kOffBars + 8 * (kTcBars + 1);        // [8] pages of a key tile that lie in the pool
 constexpr uint32_t kTcSmem = kOffMask + 32 + 16 + 1024;      // + TMEM address, alignment
+
+// A place in the ring of stages, and the parity of its barriers' phase.
+struct Ring {
+    uint32_t stage, phase;
+    __device__ __forceinline__ void advance(uint32_t by) {
+        stage += by;
+        if (stage >= kStages) {
+            stage -= kStages;
+            phase ^= 1;
+        }
+    }
+};
 
 // One run of key tiles [n0, n1) of an item.
 struct Segment {
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint8_t* gbase = tc_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = base + kOffBars, empty = full + 8 * kStages, q_full = empty + 8 * kStages;
-    const uint32_t s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, p_half = o_full + 16, x_full = p_half + 16;
+    const uint32_t s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, tail = o_full + 16, x_full = tail + 8;
     volatile uint32_t* s_mask = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask);
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask + 32);
     int bad = 0;
@@ -304,9 +307,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(q_full + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, 4);
-            mbar_init(p_half + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
         }
+        mbar_init(tail, 1);
         mbar_init(x_full, 4);
         mbar_init_fence();
     }
@@ -318,163 +321,180 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    bool ok = true;
+    bool failed = false;
     Segment s;
 
     // (128 x 168 x 3 registers at launch: 2 x 128 x 208 + 128 x 88)
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    if (warp == 8) {
-        // ---- loads: per key tile the K pages, then the V pages (lane i: page i of the tile) ----
-        int load = 0, step = 0;
-        const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
-        while (ok && next(w, s)) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        if (warp == 8) {
+            // ---- loads: per key tile the K pages, then the V pages (lane i: page i of the tile) ----
+            Ring ring{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
+            uint32_t step = 0, tail_par = 0;
+            const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
+            while (next(w, s)) {
 #pragma unroll 1
-            for (int n = s.n0; n < s.n1 && ok; ++n, ++step) {
-                const int nk = min(kTileKeys, s.klen - n * kTileKeys), np = (nk + a.page_n - 1) >> a.page_shift;
-                int id = -1;
-                if (lane < np) id = s.ids[((n * kTileKeys) >> a.page_shift) + lane];
-                const bool in = lane < np && id >= 0 && id < a.n_pages;
-                const uint32_t mask = __ballot_sync(kFull, in);
-                if (mask != (1u << np) - 1u) bad |= HSQ_DEVERR_PAGE;
-                // (a page outside the pool is read past the map's extent: zeros, masked in the softmax)
-                const int y = in ? (id * a.Hkv + s.h) << a.page_shift : (a.n_pages * a.Hkv) << a.page_shift;
+                for (int n = s.n0; n < s.n1; ++n, ++step) {
+                    const int nk = min(kTileKeys, s.klen - n * kTileKeys), np = (nk + a.page_n - 1) >> a.page_shift;
+                    int id = -1;
+                    if (lane < np) id = s.ids[((n * kTileKeys) >> a.page_shift) + lane];
+                    const bool in = lane < np && id >= 0 && id < a.n_pages;
+                    const uint32_t mask = __ballot_sync(kFull, in);
+                    if (mask != (1u << np) - 1u) bad |= HSQ_DEVERR_PAGE;
+                    // (a page outside the pool is read past the map's extent: zeros, masked in the softmax)
+                    const int y = in ? (id * a.Hkv + s.h) << a.page_shift : (a.n_pages * a.Hkv) << a.page_shift;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++load) {
-                    const int st = load % kStages, turn = load / kStages;
-                    if (turn > 0) ok = warp_wait(empty + 8 * st, (turn - 1) & 1);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (!kv) s_mask[step & 7] = mask;
-                        mbar_expect_tx(full + 8 * st, np * page_bytes);
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t stage = base + ring.stage * kTileBytes, bar = full + 8 * ring.stage;
+                        mbar_wait_fast(empty + 8 * ring.stage, ring.phase, failed);
+                        failed = __any_sync(kFull, failed);
+                        // The values of a tile that does not end on a multiple of 16 keys: the rows up to there
+                        // hold what the page holds; their weights are 0, so they have to be finite.  Cleared
+                        // here before the tile is handed over.
+                        const bool ragged = kv && (nk & 15);
+                        const uint32_t lands = ragged ? tail : bar;
+                        if (lane == 0) {
+                            if (!kv) s_mask[step & 7] = mask;
+                            mbar_expect_tx(lands, np * page_bytes);
+                        }
+                        __syncwarp();
+                        if (lane < np) {
+                            const void* map = kv ? &mv : &mk;
+                            tma_2d(stage + lane * half_page, map, 0, y, lands);
+                            tma_2d(stage + lane * half_page + kHalfBytes, map, 64, y, lands);
+                        }
+                        if (ragged) {
+                            mbar_wait_fast(tail, tail_par, failed);
+                            failed = __any_sync(kFull, failed);
+                            tail_par ^= 1;
+                            const int z = (16 - (nk & 15)) * 16;  // 16-byte chunks in both halves
+                            for (int i = lane; i < z; i += 32)
+                                *reinterpret_cast<uint4*>(gbase + (stage - base) + ((i >> 3) & 1) * kHalfBytes +
+                                                          (nk + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar);
+                        }
+                        ring.advance(1);
                     }
-                    __syncwarp();
-                    if (lane < np) {
-                        const uint32_t dst = base + st * kTileBytes + lane * half_page;
-                        const void* map = kv ? &mv : &mk;
-                        tma_2d(dst, map, 0, y, full + 8 * st);
-                        tma_2d(dst + kHalfBytes, map, 64, y, full + 8 * st);
-                    }
+                    if (failed) break;
                 }
+                if (failed) break;
             }
-        }
-        if (!ok)  // a wait ran out: see the copies in flight land before the CTA ends
-            for (int l = max(0, load - kStages); l < load; ++l) mbar_wait(full + 8 * (l % kStages), (l / kStages) & 1);
-    } else if (warp == 9) {
-        // ---- MMAs ----
-        int load = 0, q_at[2] = {0, 0}, p_at[2] = {0, 0};
-        const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
-        auto load_q = [&](const Segment& s) {
-            if (lane) return;
-            for (int st = 0; st < 2; ++st) {
-                if (tiles_of(s, st) <= 0) continue;
+            if (failed) {  // see the copies in flight land before the CTA ends
+                for (int i = 0; i < kStages; ++i) mbar_wait(full + 8 * i, i < (int)ring.stage ? ring.phase ^ 1 : ring.phase);
+            }
+        } else if (warp == 9 && lane == 0) {
+            // ---- MMAs, one thread ----
+            // Straight code: per pair of key tiles three waits, each one poll; the tensor pipe takes an MMA every 64
+            // cycles and holds only one or two more, so what the thread does in between shows.
+            const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
+            constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128), idFull = idesc_bf16_f32(128, 128);
+            Ring kr{0, 0}, vr{1, 0};
+            uint32_t q_par = 0, p_par = 0;  // a bit for each stream
+            auto load_q = [&](int st, int tok) {
                 const uint32_t dst = base + kOffQ + st * kTileBytes, bar = q_full + 8 * st;
                 mbar_expect_tx(bar, q_bytes);
-                tma_3d(dst, &mq, 0, s.h * a.r, s.tok[st], bar);
-                tma_3d(dst + kHalfBytes, &mq, 64, s.h * a.r, s.tok[st], bar);
-            }
-        };
-        bool more = next(w, s);
-        bool pending = more;  // a query tile on its way
-        if (more) load_q(s);
-        while (more && ok) {
-            const int lag = s.split ? 2 : 1, first = load;
-            pending = false;
-            int v_seen = s.n0 - 1;  // the last value tile waited for
-            for (int st = 0; st < 2 && ok; ++st)
-                if (tiles_of(s, st) > 0) ok = warp_wait(q_full + 8 * st, q_at[st]++ & 1);
-#pragma unroll 1
-            for (int n = s.n0; n < s.n1 + lag && ok; ++n) {
-                const int np = n - lag;  // the tile whose P V is due
-                const int kl = first + 2 * (n - s.n0), vl = first + 2 * (np - s.n0) + 1;
-                const uint32_t ks = base + (kl % kStages) * kTileBytes, vs = base + (vl % kStages) * kTileBytes;
-                if (n < s.n1) ok = warp_wait(full + 8 * (kl % kStages), (kl / kStages) & 1);
-#pragma unroll 1
-                for (int st = 0; st < 2 && ok; ++st) {
-                    if (s.split && ((n - s.n0) & 1) != st) continue;
-                    if (np >= s.n0 && np < s.end[st]) {
-                        ok = warp_wait(p_half + 8 * st, p_at[st] & 1);
-                        const int nk = min(kTileKeys, s.klen - np * kTileKeys), ks16 = (nk + 15) >> 4;
-                        if (ok && v_seen < np) {
-                            v_seen = np;
-                            ok = warp_wait(full + 8 * (vl % kStages), (vl / kStages) & 1);
-                            if (nk & 15) {  // the rows between the last key and the next multiple of 16: stale, weight 0, must be finite
-                                const int z = (16 - (nk & 15)) * 16;  // 16-byte chunks in both halves
-                                for (int i = lane; i < z; i += 32) {
-                                    const int rowi = nk + (i >> 4), c = i & 15;
-                                    *reinterpret_cast<uint4*>(gbase + (vs - base) + (c >> 3) * kHalfBytes + rowi * 128 +
-                                                              (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                                }
-                                fence_async_smem();
-                                __syncwarp();
-                            }
-                        }
-                        if (!ok) break;
-                        // O += P V, the first 64 keys while the softmax still works on the others
-                        constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128);
-                        const uint32_t dO = tmem + 256 + 128 * st, pa = tmem + 128 * st;
-                        const uint64_t dv = sw128_mn_desc(vs, kHalfBytes);
-                        const bool begun = np > s.n0 + (s.split ? st : 0);
-                        tc_fence_after();
-                        if (elect_one()) {
+                tma_3d(dst, &mq, 0, s.h * a.r, tok, bar);
+                tma_3d(dst + kHalfBytes, &mq, 64, s.h * a.r, tok, bar);
+            };
+            auto load_both = [&] {
+                if (tiles_of(s, 0) > 0) load_q(0, s.tok[0]);
+                if (tiles_of(s, 1) > 0) load_q(1, s.tok[1]);
+            };
+            auto scores = [&](int st, uint32_t idS) {  // S = Q K^T of the tile at kr
+                const uint32_t dS = tmem + 128 * st;
+                const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + kr.stage * kTileBytes);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (k < ks16) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
-                        }
-                        __syncwarp();
-                        ok = warp_wait(p_full + 8 * st, p_at[st]++ & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                    mma_bf16(dS, dq + o, dk + o, idS, k > 0);
+                }
+                mma_commit(s_full + 8 * st);
+            };
+            auto product = [&](int st, int ks16, uint32_t begun) {  // O += P V of the tile at vr
+                const uint32_t pa = tmem + 128 * st, dO = pa + 256;
+                const uint64_t dv = sw128_mn_desc(base + vr.stage * kTileBytes, kHalfBytes);
+                mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
+                p_par ^= 1u << st;
+                tc_fence_after();
+                mma_bf16_ts(dO, pa, dv, idO, begun);
 #pragma unroll
-                            for (int k = 4; k < 8; ++k)
-                                if (k < ks16) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
-                            if (s.split || st == 1) mma_commit(empty + 8 * (vl % kStages));
+                for (int k = 1; k < 8; ++k)
+                    if (k < ks16) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+            };
+            bool more = next(w, s);
+            if (more) load_both();
+            while (more) {
+                const int n_last = s.n1 - 1, nk_last = s.klen - n_last * kTileKeys;
+                const uint32_t id_last = nk_last < kTileKeys ? idesc_bf16_f32(128, (nk_last + 15) & ~15) : idFull;
+                const int ks_last = min(8, (nk_last + 15) >> 4);
+                if (tiles_of(s, 0) > 0) { mbar_wait_fast(q_full, q_par & 1, failed); q_par ^= 1; }
+                if (tiles_of(s, 1) > 0) { mbar_wait_fast(q_full + 8, (q_par >> 1) & 1, failed); q_par ^= 2; }
+                if (!s.split) {
+                    const int end0 = s.end[0];
+#pragma unroll 1
+                    for (int n = s.n0; n < s.n1; ++n) {
+                        const uint32_t idS = n == n_last ? id_last : idFull;
+                        mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
+                        if (n > s.n0) mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
+                        if (n > s.n0 && n <= end0) product(0, 8, n - 1 > s.n0);
+                        if (n < end0) scores(0, idS);
+                        if (n > s.n0) {
+                            product(1, 8, n - 1 > s.n0);
+                            mma_commit(empty + 8 * vr.stage);
+                            vr.advance(2);
                         }
-                        __syncwarp();
+                        scores(1, idS);
+                        mma_commit(empty + 8 * kr.stage);
+                        kr.advance(2);
                     }
-                    if (n < s.end[st]) {
-                        tc_fence_after();
-                        const int nk = min(kTileKeys, s.klen - n * kTileKeys);
-                        const uint32_t idS = idesc_bf16_f32(128, (nk + 15) & ~15), dS = tmem + 128 * st;
-                        const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(ks);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-                                mma_bf16(dS, dq + o, dk + o, idS, k > 0);
-                            }
-                            mma_commit(s_full + 8 * st);
-                            if (s.split || st == 1) mma_commit(empty + 8 * (kl % kStages));
+                    if (s.n1 > s.n0) {
+                        mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
+                        if (end0 == s.n1) product(0, ks_last, n_last > s.n0);
+                        if (end0 > s.n0) mma_commit(o_full);
+                        product(1, ks_last, n_last > s.n0);
+                        mma_commit(o_full + 8);
+                        mma_commit(empty + 8 * vr.stage);
+                        vr.advance(2);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int n = s.n0; n < s.n1 + 2; ++n) {
+                        const int st = (n - s.n0) & 1, np = n - 2;
+                        if (np >= s.n0) {
+                            mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
+                            product(st, np == n_last ? ks_last : 8, np > s.n0 + 1);
+                            mma_commit(empty + 8 * vr.stage);
+                            vr.advance(2);
+                            if (n >= s.n1) mma_commit(o_full + 8 * st);
                         }
-                        __syncwarp();
+                        if (n < s.n1) {
+                            mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
+                            scores(st, n == n_last ? id_last : idFull);
+                            mma_commit(empty + 8 * kr.stage);
+                            kr.advance(2);
+                        }
                     }
                 }
+                if (failed) break;
+                more = next(w, s);
+                if (more) load_both();  // (every S of the segment is done: its P has been seen)
             }
-            load += 2 * (s.n1 - s.n0);
-            if (ok && s.n1 > s.n0) {  // (a stream without a tile waits too: it may write to the ring)
-                if (elect_one()) {
-                    mma_commit(o_full);
-                    mma_commit(o_full + 8);
-                }
-                __syncwarp();
+            if (failed) {  // query tiles in flight land before the CTA ends
+                mbar_wait(q_full, q_par & 1, 1 << 12);
+                mbar_wait(q_full + 8, (q_par >> 1) & 1, 1 << 12);
             }
-            more = next(w, s);
-            pending = more && ok;
-            if (pending) load_q(s);  // (every S of the segment is done: its P has been seen)
         }
-        if (!ok && pending)
-            for (int st = 0; st < 2; ++st)
-                if (tiles_of(s, st) > 0) mbar_wait(q_full + 8 * st, q_at[st] & 1);
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         // ---- softmax: thread = row of its stream's tile ----
         const int st = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + 128 * st, tO = tmem + lanes + 256 + 128 * st;
-        int s_at = 0, o_at = 0, step0 = 0;
-        while (ok && next(w, s)) {
+        uint32_t s_par = 0, o_par = 0;
+        int step0 = 0;
+        while (next(w, s)) {
             const int own_token = row / a.r;
             const bool live = own_token < s.toks[st];
             const bool idle = 32 * (warp & 3) >= s.toks[st] * a.r;  // (warp-uniform) no row of this warp in use
@@ -483,8 +503,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int n = s.n0 + (s.split ? st : 0); n < s.end[st]; n += s.split ? 2 : 1) {
-                ok = warp_wait(s_full + 8 * st, s_at++ & 1);
-                if (!ok) break;
+                mbar_wait_fast(s_full + 8 * st, s_par, failed);
+                s_par ^= 1;
                 if (!idle) {
                     tc_fence_after();
                     float x[2][64];
@@ -535,22 +555,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             p[c >> 1] = pack_bf16(e0, e1);
                         }
                         tmem_st32_nowait(tS + 32 * hf, p);
-                        tmem_st_wait();
-                        tc_fence_before();
-                        warp_arrive((hf ? p_full : p_half) + 8 * st);
                     }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    warp_arrive(p_full + 8 * st);
                     float l_lo, l_hi;
                     unpack2(add2(l2[0], l2[1]), l_lo, l_hi);
                     l += l_lo + l_hi;
                 } else {
-                    warp_arrive(p_half + 8 * st);
                     warp_arrive(p_full + 8 * st);
                 }
             }
-            if (!ok) break;
             const bool any = tiles_of(s, st) > 0;
-            if (s.n1 > s.n0) ok = warp_wait(o_full + 8 * st, o_at++ & 1);
-            if (!ok) break;
+            if (any) {
+                mbar_wait_fast(o_full + 8 * st, o_par, failed);
+                o_par ^= 1;
+            }
+            // (stream 1 of a split pair is about to write to the ring: the other stream's products first)
+            if (kOwn && s.split && st == 1 && s.n1 > s.n0) mbar_wait_fast(o_full, 0, failed);
+            failed = __any_sync(kFull, failed);
+            if (failed) break;
             tc_fence_after();
             if (!kOwn) {
                 const size_t at = ((size_t)(s.item + blockIdx.x) * 2 + st) * kTileRows + row;
@@ -587,8 +611,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         warp_arrive(x_full);
                         break;
                     }
-                    ok = warp_wait(x_full, 0);
-                    if (!ok) break;
+                    mbar_wait_fast(x_full, 0, failed);
+                    failed = __any_sync(kFull, failed);
+                    if (failed) break;
                     const float2 ot = xml[row];
                     M = fmaxf(m, ot.x);
                     w_me = m == -INFINITY ? 0.f : ex2_approx((m - M) * kLogitScaleLog2);
@@ -650,7 +675,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             step0 += s.n1 - s.n0;
         }
     }
-    if (!ok) bad |= HSQ_DEVERR_WAIT;
+    if (failed) bad |= HSQ_DEVERR_WAIT;
     if (bad) atomicOr(a.err, bad);
     tc_fence_before();
     __syncthreads();

@@ -52,6 +52,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int max
     return false;
 }
 
+// The same with the common case first: one poll and a branch that is not taken, where every taken
+// branch of a single running thread costs some 20 cycles of its issue.  A wait that runs out sets `failed`;
+// with `failed` set, waits return at once (the caller goes on without the data and ends soon).
+__device__ __forceinline__ void mbar_wait_fast(uint32_t bar, uint32_t parity, bool& failed) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__builtin_expect(!done, 0)) {
+        if (!failed) failed = !mbar_wait(bar, parity);
+    }
+}
+
 // one arrival on the barrier's current phase
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
@@ -154,13 +169,6 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-// true in one lane of a converged warp
-__device__ __forceinline__ bool elect_one() {
-    uint32_t on;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(on));
-    return on != 0;
 }
 
 // the mbarrier gets one arrival when every MMA issued before by this thread has completed
