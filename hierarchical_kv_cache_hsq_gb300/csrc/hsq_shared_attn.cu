@@ -49,6 +49,7 @@ using namespace hsq_tc;
 constexpr int kFewRows = 16;                    // rows (tokens x r) of a request up to which the few-rows kernel takes it
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr float kRaise = 8.f;                   // log2 units a logit may exceed the running maximum by before o is rescaled
+constexpr float kTileSum = 65536.f;             // sum of a tile's 128 weights from which the maximum is taken anew
 
 struct SharedArgs {
     const uint16_t *q, *pk, *pv;
@@ -156,8 +157,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // ---------------------------------------------------------------------------------------
 // Tensor-core kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7
 // (stream 1), warp 8 loads, warp 9 issues the MMAs (10 and 11 only give their registers away:
-// 168 a thread at launch, then 208 for the softmax warps, whose row of 128 logits
-// lives in registers, and 88 for the others).  A stream is a 128-row query tile with
+// 168 a thread at launch, then 184 for the softmax warps, whose row of 128 logits
+// lives in registers, and 136 for the others).  A stream is a 128-row query tile with
 // its S / P and O in tensor memory.  The two streams either hold two row tiles and share every
 // key tile (so keys and values are loaded once for 256 rows), or, when only one row tile is
 // left, hold the same rows and take the key tiles in turn.  While one stream's softmax
@@ -189,9 +190,9 @@ struct Ring {
 // One run of key tiles [n0, n1) of an item.
 struct Segment {
     int h, item;
-    int tok[2];        // first token of each stream's tile
-    int toks[2];       // its tokens
-    int n0, n1, end[2];
+    int tok0, tok1;    // first token of each stream's tile
+    int toks0, toks1;  // its tokens
+    int n0, n1, end0, end1;
     bool split;
     int klen;          // keys in all
     const int32_t* ids;  // page ids
@@ -260,17 +261,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             s.item = 0;
             const int left = rq.n - unit * 2 * a.tpt;  // tokens from this pair's first on
             s.split = left <= a.tpt;
-            s.toks[0] = min(left, a.tpt);
-            s.toks[1] = s.split ? s.toks[0] : min(left - a.tpt, a.tpt);
-            s.tok[0] = rq.first + unit * 2 * a.tpt;
-            s.tok[1] = s.split ? s.tok[0] : s.tok[0] + a.tpt;
-            s.klen = max(0, key_limit<true>(rq, rq.len, s.tok[1] + s.toks[1] - 1));
+            s.toks0 = min(left, a.tpt);
+            s.toks1 = s.split ? s.toks0 : min(left - a.tpt, a.tpt);
+            s.tok0 = rq.first + unit * 2 * a.tpt;
+            s.tok1 = s.split ? s.tok0 : s.tok0 + a.tpt;
+            s.klen = max(0, key_limit<true>(rq, rq.len, s.tok1 + s.toks1 - 1));
             s.ids = own_ids;
             s.n0 = 0;
             s.n1 = (s.klen + kTileKeys - 1) / kTileKeys;
-            const int l0 = max(0, key_limit<true>(rq, s.klen, s.tok[0] + s.toks[0] - 1));
-            s.end[0] = (l0 + kTileKeys - 1) / kTileKeys;
-            s.end[1] = s.n1;
+            const int l0 = max(0, key_limit<true>(rq, s.klen, s.tok0 + s.toks0 - 1));
+            s.end0 = (l0 + kTileKeys - 1) / kTileKeys;
+            s.end1 = s.n1;
             w = w_end;
         } else {
             s.item = (int)(w / plan.steps);
@@ -278,15 +279,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int pair = s.item - s.h * plan.pairs;
             s.split = 2 * pair + 1 == plan.tiles;
             const int live = min(max(a.q_start[a.B], 0), a.rows);
-            s.tok[0] = 2 * pair * a.tpt;
-            s.tok[1] = s.split ? s.tok[0] : s.tok[0] + a.tpt;
-            s.toks[0] = min(a.tpt, live - s.tok[0]);
-            s.toks[1] = min(a.tpt, live - s.tok[1]);
+            s.tok0 = 2 * pair * a.tpt;
+            s.tok1 = s.split ? s.tok0 : s.tok0 + a.tpt;
+            s.toks0 = min(a.tpt, live - s.tok0);
+            s.toks1 = min(a.tpt, live - s.tok1);
             s.klen = a.prefix_len;
             s.ids = a.prefix;
             s.n0 = (int)(w - (long long)s.item * plan.steps);
             s.n1 = (int)min((long long)plan.steps, s.n0 + (w_end - w));
-            s.end[0] = s.end[1] = s.n1;
+            s.end0 = s.end1 = s.n1;
             w += s.n1 - s.n0;
         }
         return true;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (kOwn) w_end = 1;
     // key tiles that stream s takes in a segment
     auto tiles_of = [](const Segment& s, int st) {
-        if (!s.split) return s.end[st] - s.n0;
+        if (!s.split) return (st ? s.end1 : s.end0) - s.n0;
         return (s.n1 - s.n0 + 1 - st) >> 1;
     };
 
@@ -324,9 +325,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool failed = false;
     Segment s;
 
-    // (128 x 168 x 3 registers at launch: 2 x 128 x 208 + 128 x 88)
+    // (128 x 168 x 3 registers at launch: 2 x 128 x 184 + 128 x 136)
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 136;\n");
         if (warp == 8) {
             // ---- loads: per key tile the K pages, then the V pages (lane i: page i of the tile) ----
             Ring ring{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (failed) {  // see the copies in flight land before the CTA ends
                 for (int i = 0; i < kStages; ++i) mbar_wait(full + 8 * i, i < (int)ring.stage ? ring.phase ^ 1 : ring.phase);
             }
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == 9 && elect_one()) {
             // ---- MMAs, one thread ----
             // Straight code: per pair of key tiles three waits, each one poll; the tensor pipe takes an MMA every 64
             // cycles and holds only one or two more, so what the thread does in between shows.
@@ -399,8 +400,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tma_3d(dst + kHalfBytes, &mq, 64, s.h * a.r, tok, bar);
             };
             auto load_both = [&] {
-                if (tiles_of(s, 0) > 0) load_q(0, s.tok[0]);
-                if (tiles_of(s, 1) > 0) load_q(1, s.tok[1]);
+                if (tiles_of(s, 0) > 0) load_q(0, s.tok0);
+                if (tiles_of(s, 1) > 0) load_q(1, s.tok1);
             };
             auto scores = [&](int st, uint32_t idS) {  // S = Q K^T of the tile at kr
                 const uint32_t dS = tmem + 128 * st;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 mma_commit(s_full + 8 * st);
             };
-            auto product = [&](int st, int ks16, uint32_t begun) {  // O += P V of the tile at vr
+            auto product = [&](int st, uint32_t begun) {  // O += P V of the whole tile at vr
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
                 const uint64_t dv = sw128_mn_desc(base + vr.stage * kTileBytes, kHalfBytes);
                 mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
@@ -420,8 +421,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
                 mma_bf16_ts(dO, pa, dv, idO, begun);
 #pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    if (k < ks16) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+                for (int k = 1; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+            };
+            auto product_last = [&](int st, int ks16, uint32_t begun) {  // the same of an item's last tile: ks16 groups of 16 keys
+                const uint32_t pa = tmem + 128 * st, dO = pa + 256;
+                const uint64_t dv = sw128_mn_desc(base + vr.stage * kTileBytes, kHalfBytes);
+                mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
+                p_par ^= 1u << st;
+                tc_fence_after();
+#pragma unroll 1
+                for (int k = 0; k < ks16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
             };
             bool more = next(w, s);
             if (more) load_both();
@@ -432,28 +441,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (tiles_of(s, 0) > 0) { mbar_wait_fast(q_full, q_par & 1, failed); q_par ^= 1; }
                 if (tiles_of(s, 1) > 0) { mbar_wait_fast(q_full + 8, (q_par >> 1) & 1, failed); q_par ^= 2; }
                 if (!s.split) {
-                    const int end0 = s.end[0];
-#pragma unroll 1
-                    for (int n = s.n0; n < s.n1; ++n) {
-                        const uint32_t idS = n == n_last ? id_last : idFull;
+                    const int n0 = s.n0, n1 = s.n1, end0 = s.end0;
+                    if (n1 > n0) {
                         mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
-                        if (n > s.n0) mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
-                        if (n > s.n0 && n <= end0) product(0, 8, n - 1 > s.n0);
-                        if (n < end0) scores(0, idS);
-                        if (n > s.n0) {
-                            product(1, 8, n - 1 > s.n0);
-                            mma_commit(empty + 8 * vr.stage);
-                            vr.advance(2);
-                        }
-                        scores(1, idS);
+                        if (n0 < end0) scores(0, n0 == n_last ? id_last : idFull);
+                        scores(1, n0 == n_last ? id_last : idFull);
                         mma_commit(empty + 8 * kr.stage);
                         kr.advance(2);
-                    }
-                    if (s.n1 > s.n0) {
+                        int n = n0 + 1;
+                        const int both = min(end0, n_last);
+#pragma unroll 1
+                        for (; n < both; ++n) {  // P V of tile n - 1 and S of tile n, all tiles whole
+                            mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
+                            mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
+                            product(0, n > n0 + 1);
+                            scores(0, idFull);
+                            product(1, n > n0 + 1);
+                            mma_commit(empty + 8 * vr.stage);
+                            vr.advance(2);
+                            scores(1, idFull);
+                            mma_commit(empty + 8 * kr.stage);
+                            kr.advance(2);
+                        }
+#pragma unroll 1
+                        for (; n < n1; ++n) {  // stream 0 ends before stream 1, or the last tile
+                            const uint32_t idS = n == n_last ? id_last : idFull;
+                            mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
+                            mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
+                            if (n <= end0) product_last(0, 8, n > n0 + 1);
+                            if (n < end0) scores(0, idS);
+                            product_last(1, 8, n > n0 + 1);
+                            mma_commit(empty + 8 * vr.stage);
+                            vr.advance(2);
+                            scores(1, idS);
+                            mma_commit(empty + 8 * kr.stage);
+                            kr.advance(2);
+                        }
                         mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
-                        if (end0 == s.n1) product(0, ks_last, n_last > s.n0);
-                        if (end0 > s.n0) mma_commit(o_full);
-                        product(1, ks_last, n_last > s.n0);
+                        if (end0 == n1) product_last(0, ks_last, n_last > n0);
+                        if (end0 > n0) mma_commit(o_full);
+                        product_last(1, ks_last, n_last > n0);
                         mma_commit(o_full + 8);
                         mma_commit(empty + 8 * vr.stage);
                         vr.advance(2);
@@ -464,7 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const int st = (n - s.n0) & 1, np = n - 2;
                         if (np >= s.n0) {
                             mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
-                            product(st, np == n_last ? ks_last : 8, np > s.n0 + 1);
+                            product_last(st, np == n_last ? ks_last : 8, np > s.n0 + 1);
                             mma_commit(empty + 8 * vr.stage);
                             vr.advance(2);
                             if (n >= s.n1) mma_commit(o_full + 8 * st);
@@ -487,7 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
         // ---- softmax: thread = row of its stream's tile ----
         const int st = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -496,72 +523,96 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int step0 = 0;
         while (next(w, s)) {
             const int own_token = row / a.r;
-            const bool live = own_token < s.toks[st];
-            const bool idle = 32 * (warp & 3) >= s.toks[st] * a.r;  // (warp-uniform) no row of this warp in use
-            const int lim = live ? key_limit<kOwn>(rq, s.klen, s.tok[st] + own_token) : 0;
-            const int lim_min = key_limit<kOwn>(rq, s.klen, s.tok[st]);
+            const bool live = own_token < (st ? s.toks1 : s.toks0);
+            const bool idle = 32 * (warp & 3) >= (st ? s.toks1 : s.toks0) * a.r;  // (warp-uniform) no row of this warp in use
+            const int lim = live ? key_limit<kOwn>(rq, s.klen, (st ? s.tok1 : s.tok0) + own_token) : 0;
+            const int lim_min = key_limit<kOwn>(rq, s.klen, (st ? s.tok1 : s.tok0));
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int n = s.n0 + (s.split ? st : 0); n < s.end[st]; n += s.split ? 2 : 1) {
+            for (int n = s.n0 + (s.split ? st : 0); n < (st ? s.end1 : s.end0); n += s.split ? 2 : 1) {
                 mbar_wait_fast(s_full + 8 * st, s_par, failed);
                 s_par ^= 1;
                 if (!idle) {
+                    // The running maximum need not be one: any m that keeps the sums in range gives the same
+                    // result, p and l being floating point.  So the row's maximum is looked for in its first tile and
+                    // where the tile's sum shows that the logits have outgrown m by far; every other tile goes without
+                    // (a third of the softmax's time).
                     tc_fence_after();
-                    float x[2][64];
-                    tmem_ld64(tS, x[0]);
-                    tmem_ld64(tS + 64, x[1]);
                     const int nk = min(kTileKeys, s.klen - n * kTileKeys), np = (nk + a.page_n - 1) >> a.page_shift;
                     const uint32_t mask = s_mask[(step0 + n - s.n0) & 7];
                     if ((n + 1) * kTileKeys > lim_min || mask != (1u << np) - 1u) {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            if (n * kTileKeys + c >= lim || !((mask >> (c >> a.page_shift)) & 1u)) x[c >> 6][c & 63] = -INFINITY;
-                    }
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < 128; c += 2)
-                        m4[(c >> 1) & 3] = fmaxf(fmaxf(m4[(c >> 1) & 3], x[c >> 6][c & 63]), x[c >> 6][(c & 63) + 1]);
-                    const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    const bool raise = mn * kLogitScaleLog2 > m * kLogitScaleLog2 + kRaise;  // (the first key raises from -inf)
-                    if (__any_sync(kFull, raise)) {
-                        const float to = raise ? mn : m;
-                        const float alpha = raise ? (m == -INFINITY ? 0.f : ex2_approx((m - to) * kLogitScaleLog2)) : 1.f;
-                        m = to;
-                        l *= alpha;
-                        if (n >= s.n0 + (s.split ? 2 : 1)) {  // O holds the tiles before (S of this tile follows their P V)
+                        // keys past the row's limit or of no page: hidden in S itself, so that the code below (and the
+                        // instruction cache) knows whole tiles only
 #pragma unroll 1
-                            for (int c0 = 0; c0 < 128; c0 += 32) {
-                                float o[32];
-                                tmem_ld32(tO + c0, o);
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            float x[32];
+                            tmem_ld32(tS + c0, x);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) o[c] *= alpha;
-                                tmem_st32(tO + c0, o);
+                            for (int c = 0; c < 32; ++c)
+                                if (n * kTileKeys + c0 + c >= lim || !((mask >> ((c0 + c) >> a.page_shift)) & 1u)) x[c] = -INFINITY;
+                            tmem_st32(tS + c0, x);
+                        }
+                    }
+                    float t;
+                    uint32_t p[2][32];
+                    bool look = __any_sync(kFull, live && m == -INFINITY);
+#pragma unroll 1
+                    while (true) {
+                        float x[2][64];
+                        if (look) {
+                            float m4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                            for (int c0 = 0; c0 < 128; c0 += 64) {
+                                tmem_ld64(tS + c0, x[0]);
+#pragma unroll
+                                for (int c = 0; c < 64; c += 2)
+                                    m4[(c >> 1) & 3] = fmaxf(fmaxf(m4[(c >> 1) & 3], x[0][c]), x[0][c + 1]);
+                            }
+                            const float mn = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            const float alpha = m == -INFINITY ? 0.f : ex2_approx((m - mn) * kLogitScaleLog2);
+                            m = mn;
+                            l *= alpha;
+                            if (n >= s.n0 + (s.split ? 2 : 1)) {  // O holds the tiles before (S of this tile follows their P V)
+#pragma unroll 1
+                                for (int c0 = 0; c0 < 128; c0 += 32) {
+                                    float o[32];
+                                    tmem_ld32(tO + c0, o);
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) o[c] *= alpha;
+                                    tmem_st32(tO + c0, o);
+                                }
                             }
                         }
-                    }
-                    const float off = m == -INFINITY ? 0.f : -m * kLogitScaleLog2;
-                    const uint64_t off2 = pack2(off, off), scale2 = pack2(kLogitScaleLog2, kLogitScaleLog2);
-                    uint64_t l2[2] = {0, 0};
+                        const float off = m == -INFINITY ? 0.f : -m * kLogitScaleLog2;
+                        const uint64_t off2 = pack2(off, off), scale2 = pack2(kLogitScaleLog2, kLogitScaleLog2);
+                        uint64_t l2[2] = {0, 0};
+                        tmem_ld64(tS, x[0]);
+                        tmem_ld64_nowait(tS + 64, x[1]);
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t p[32];
+                        for (int hf = 0; hf < 2; ++hf) {
+                            if (hf) tmem_ld64_wait(x[1]);
 #pragma unroll
-                        for (int c = 0; c < 64; c += 2) {
-                            float e0, e1;
-                            unpack2(fma2(pack2(x[hf][c], x[hf][c + 1]), scale2, off2), e0, e1);
-                            e0 = ex2_approx(e0);
-                            e1 = ex2_approx(e1);
-                            l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pack2(e0, e1));
-                            p[c >> 1] = pack_bf16(e0, e1);
+                            for (int c = 0; c < 64; c += 2) {
+                                float e0, e1;
+                                unpack2(fma2(pack2(x[hf][c], x[hf][c + 1]), scale2, off2), e0, e1);
+                                e0 = ex2_approx(e0);
+                                e1 = ex2_approx(e1);
+                                l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pack2(e0, e1));
+                                p[hf][c >> 1] = pack_bf16(e0, e1);
+                            }
                         }
-                        tmem_st32_nowait(tS + 32 * hf, p);
+                        float lo, hi;
+                        unpack2(add2(l2[0], l2[1]), lo, hi);
+                        t = lo + hi;
+                        if (look || !__any_sync(kFull, live && !(t < kTileSum))) break;
+                        look = true;
                     }
+                    tmem_st32_nowait(tS, p[0]);
+                    tmem_st32_nowait(tS + 32, p[1]);
+                    l += t;
                     tmem_st_wait();
                     tc_fence_before();
                     warp_arrive(p_full + 8 * st);
-                    float l_lo, l_hi;
-                    unpack2(add2(l2[0], l2[1]), l_lo, l_hi);
-                    l += l_lo + l_hi;
                 } else {
                     warp_arrive(p_full + 8 * st);
                 }
@@ -621,7 +672,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     L = l * w_me + ot.y * w_ot;
                 }
                 asm volatile("griddepcontrol.wait;" ::: "memory");
-                const int token = s.tok[st] + own_token, jj = row - own_token * a.r;
+                const int token = (st ? s.tok1 : s.tok0) + own_token, jj = row - own_token * a.r;
                 RowParts rp{0, 0, 0};
                 if (live && plan.work > 0) rp = row_parts(a, plan, s.h, token, jj);
                 float Mall = M;
