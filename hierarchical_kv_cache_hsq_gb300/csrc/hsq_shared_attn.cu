@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_wait_fast(o_full + 8 * st, o_par, failed);
                 o_par ^= 1;
             }
-            // (stream 1 of a split pair is about to write to the ring: the other stream's products first)
-            if (kOwn && s.split && st == 1 && s.n1 > s.n0) mbar_wait_fast(o_full, 0, failed);
+            // (the join writes to the ring: the other stream's products first)
+            if (kOwn && tiles_of(s, 1 - st) > 0) mbar_wait_fast(o_full + 8 * (1 - st), 0, failed);
             failed = __any_sync(kFull, failed);
             if (failed) break;
             tc_fence_after();
@@ -643,22 +643,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
             } else {
-                // join: the two streams of a split pair, then the prefix's parts
-                float* xo = reinterpret_cast<float*>(gbase);  // [128 dims][128 rows] of stream 1 (the ring is at rest)
-                float2* xml = reinterpret_cast<float2*>(gbase + 2 * kTileBytes);
-                float w_me = 1.f, w_ot = 0.f, M = m, L = l;
+                // Join: the two streams of a split pair, then the prefix's parts.  A thread has its row's statistics; the
+                // sums go through shared memory (the ring is at rest), where the warp takes its 32 rows one after
+                // another, a lane four dims, so that parts are read and results written in whole lines (thread by
+                // thread, row by row, this took 25 us of a CTA's 35).
+                constexpr int kPitch = 132;  // floats: 16-byte columns of 8 rows fall into different banks
+                float* mine = reinterpret_cast<float*>(gbase) + warp * 32 * kPitch;
+                const float* other = mine + 4 * 32 * kPitch;
+                float2* xml = reinterpret_cast<float2*>(gbase + 8 * 32 * kPitch * 4);
+                float M = m, L = l, w_me = 1.f, w_ot = 0.f;
+                auto put = [&](float scale) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        float o[32];
+                        if (any) tmem_ld32(tO + c0, o);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<float4*>(mine + lane * kPitch + c0 + c) =
+                                any && scale > 0.f ? make_float4(o[c] * scale, o[c + 1] * scale, o[c + 2] * scale, o[c + 3] * scale)
+                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                };
                 if (s.split) {
                     if (st == 1) {
                         xml[row] = make_float2(m, l);
-#pragma unroll 1
-                        for (int c0 = 0; c0 < 128; c0 += 32) {
-                            float o[32];
-                            if (any) tmem_ld32(tO + c0, o);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) xo[(c0 + c) * 128 + row] = any ? o[c] : 0.f;
-                        }
-                    }
-                    if (st == 1) {
+                        put(1.f);
                         warp_arrive(x_full);
                         break;
                     }
@@ -686,39 +695,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (ml.y > 0.f) L += ml.y * ex2_approx((ml.x - Mall) * kLogitScaleLog2);
                 }
                 const float inv = L > 0.f ? 1.0f / L : 0.f;
-                if (live && a.lse)
-                    a.lse[(size_t)token * a.Hq + s.h * a.r + jj] = L > 0.f ? Mall * kRsqrtD + logf(L) : -INFINITY;
+                const size_t to = (size_t)token * a.Hq + s.h * a.r + jj;
+                if (live && a.lse) a.lse[to] = L > 0.f ? Mall * kRsqrtD + logf(L) : -INFINITY;
+                put(w_me);
+                __syncwarp();
+                const int count = min(32, (st ? s.toks1 : s.toks0) * a.r - 32 * (warp & 3));  // rows of this warp in use
 #pragma unroll 1
-                for (int c0 = 0; c0 < 128; c0 += 32) {
-                    float o[32];
-                    if (any) tmem_ld32(tO + c0, o);
+                for (int i0 = 0; i0 < count; i0 += 4) {
+                    float4 x[4];
+                    int n[4], most = 0;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        o[c] = w_me > 0.f ? o[c] * w_me : 0.f;
-                        if (w_ot > 0.f) o[c] = fmaf(xo[(c0 + c) * 128 + row], w_ot, o[c]);
+                    for (int u = 0; u < 4; ++u) {
+                        const int i = i0 + u;  // (rows past count: computed from what lies there, not written)
+                        x[u] = *reinterpret_cast<const float4*>(mine + i * kPitch + 4 * lane);
+                        const float wo = __shfl_sync(kFull, w_ot, i);
+                        if (wo > 0.f) {
+                            const float4 y = *reinterpret_cast<const float4*>(other + i * kPitch + 4 * lane);
+                            x[u] = make_float4(fmaf(y.x, wo, x[u].x), fmaf(y.y, wo, x[u].y), fmaf(y.z, wo, x[u].z), fmaf(y.w, wo, x[u].w));
+                        }
+                        n[u] = __shfl_sync(kFull, rp.n, i);
+                        most = max(most, n[u]);
                     }
-                    if (live) {
-                        for (int k = 0; k < rp.n; ++k) {
-                            const size_t at = rp.at + k * rp.step;
-                            const float2 ml = __ldcg(&a.part_ml[at]);
-                            if (!(ml.y > 0.f)) continue;
-                            const float wp = ex2_approx((ml.x - Mall) * kLogitScaleLog2);
-                            const float4* src = reinterpret_cast<const float4*>(a.part_o + at * 128 + c0);
+#pragma unroll 1
+                    for (int k = 0; k < most; ++k) {
+                        float2 ml[4];
+                        float4 v[4];
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const float4 v = __ldcg(src + (c >> 2));
-                                o[c] = fmaf(v.x, wp, o[c]);
-                                o[c + 1] = fmaf(v.y, wp, o[c + 1]);
-                                o[c + 2] = fmaf(v.z, wp, o[c + 2]);
-                                o[c + 3] = fmaf(v.w, wp, o[c + 3]);
+                        for (int u = 0; u < 4; ++u) {
+                            const size_t at = __shfl_sync(kFull, (unsigned long long)(rp.at + k * rp.step), i0 + u);
+                            ml[u] = make_float2(0.f, 0.f);
+                            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (k < n[u]) {
+                                ml[u] = __ldcg(&a.part_ml[at]);
+                                v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * 128) + lane);
                             }
                         }
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)token * a.Hq + s.h * a.r + jj) * 128 + c0);
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8)
-                            dst[c >> 3] = make_uint4(
-                                pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
-                                pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv));
+                        for (int u = 0; u < 4; ++u) {
+                            const float Mu = __shfl_sync(kFull, Mall, i0 + u);
+                            if (ml[u].y > 0.f) {
+                                const float wp = ex2_approx((ml[u].x - Mu) * kLogitScaleLog2);
+                                x[u] = make_float4(fmaf(v[u].x, wp, x[u].x), fmaf(v[u].y, wp, x[u].y), fmaf(v[u].z, wp, x[u].z),
+                                                   fmaf(v[u].w, wp, x[u].w));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float iu = __shfl_sync(kFull, inv, i0 + u);
+                        const size_t tu = __shfl_sync(kFull, (unsigned long long)to, i0 + u);
+                        if (i0 + u < count)
+                            *reinterpret_cast<uint2*>(a.out + tu * 128 + 4 * lane) =
+                                make_uint2(pack_bf16(x[u].x * iu, x[u].y * iu), pack_bf16(x[u].z * iu, x[u].w * iu));
                     }
                 }
             }
