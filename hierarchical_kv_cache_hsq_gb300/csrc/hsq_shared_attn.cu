@@ -2,37 +2,42 @@
 //
 // For row i of request b (token j of its n new ones) and query head jq of KV head
 // h: one softmax, scale 1/sqrt(128), over the prefix's tokens and the request's own
-// tokens s <= len - n + j.  A softmax over the union of two key sets is the
-// weighted sum of the softmaxes over each: with m, l, o the maximum, the sum of
+// tokens s <= len - n + j.  A softmax over the union of key sets is the weighted
+// sum of the softmaxes over each: with m, l, o a reference exponent, the sum of
 // exp(x - m) and the sum of exp(x - m) v of a part,
 //     out = sum_p exp(m_p - M) o_p / sum_p exp(m_p - M) l_p,   M = max_p m_p,
 // so the prefix is read once for all rows of the batch, each request's own pages
 // once for its rows, and the parts are joined at the end.
 //
-// Rows.  The r = Hq / Hkv query heads of a KV head and the rows of the batch
-// make one row index (token * r + head), so a tile of 128 rows holds
-// floor(128 / r) tokens of ANY requests for the prefix: the tensor cores see full
-// tiles in a decode step too.
+// Rows.  The r = Hq / Hkv query heads of a KV head and the rows of the batch make
+// one row index (token * r + head): a tile of 128 rows holds floor(128 / r) tokens
+// of ANY requests for the prefix, so the tensor cores see full tiles in a decode
+// step too.
 //
-// Three kernels, at most two of them in a call besides the prefix's:
-//   prefix  shared_tc_kernel<false>: pairs of 128-row tiles x the prefix's
-//           128-key tiles on the tensor cores, the whole (KV head, pair, key tile)
-//           space cut into equal runs, one per CTA (one CTA per SM); every run
-//           leaves its parts (m, l, o in fp32) in the workspace;
-//   own     shared_few_kernel for requests of few rows (n r <= 16, the decode step): one
-//           cluster per (request, KV head), warps stream keys and values from
-//           the pages straight into mma.sync fragments (bound by HBM: 16 rows are too
-//           few for a 128-row tile to matter);
-//           shared_tc_kernel<true> for requests with more rows: one CTA per
-//           (request, KV head, pair of row tiles), causal.
-//   Both own kernels read the prefix's parts of their rows, join them with their own and
-//   write the result.  They are launched with programmatic serialization: their own keys are
-//   read while the prefix kernel finishes, its parts only after griddepcontrol.wait.
+// Work.  A request is short when its new tokens fit one tile (n <= 128 / r: decode,
+// proposals), else long (a prompt's chunk).  Three kinds of items:
+//   A  (KV head, pair of row tiles of the short requests' tokens, packed): the prefix;
+//   B  (short request, KV head): its own tokens;
+//   C  (long request, KV head, pair of its row tiles): the prefix, then its own
+//      tokens up to the pair's last.
+// An item is a run of 128-key tiles with a cost per tile; the items one after
+// another make one line of cost, cut into as many equal runs as the GPU has SMs:
+// a persistent CTA each.  Decode's A is bound by the tensor cores and its B by HBM, and since
+// they lie at different places of the line, different SMs work on either at
+// any time and both are in use throughout.
 //
-// Rounding: q, k and v are bf16, products exact, sums fp32; the softmax weights are rounded to
-// bf16 for the product with the values (an error of 2^-9 of each weight at most, random over
-// the keys, where the output's own rounding is 2^-9 of the result), l sums
-// them before that rounding.
+// Three kernels, the later two launched with programmatic serialization (their set-up
+// runs while the one before ends):
+//   shared_plan_kernel   checks the lengths, adds up the line (one CTA);
+//   shared_tc_kernel     the items' tiles on the tensor cores; a C item that no cut
+//                        divides is written at once, everything else leaves its parts (m, l, o in
+//                        fp32) in the workspace;
+//   shared_join_kernel   joins the parts.
+//
+// Rounding: q, k and v are bf16, products exact, sums fp32; the softmax weights are
+// rounded to bf16 for the product with the values (an error of 2^-9 of each weight
+// at most, random over the keys, where the output's own rounding is 2^-9 of the
+// result); l sums them before that rounding.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -46,81 +51,135 @@ namespace {
 
 using namespace hsq_tc;
 
-constexpr int kFewRows = 16;                    // rows (tokens x r) of a request up to which the few-rows kernel takes it
 constexpr int kTileRows = 128, kTileKeys = 128;
-constexpr float kRaise = 8.f;                   // log2 units a logit may exceed the running maximum by before o is rescaled
-constexpr float kTileSum = 65536.f;             // sum of a tile's 128 weights from which the maximum is taken anew
+constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which the maximum is taken anew
+// Cost of a key tile, per key: two row tiles (tensor cores), one row tile (A: tensor cores and loads; B: loads); and
+// what an item costs beside its tiles, in keys.
+constexpr int kCostPair = 8, kCostOne = 6, kCostOwn = 6, kItemKeys = 96;
+
+struct PlanHead {
+    long long work, work_a, work_c;  // the line: [A | C | B]
+    long long head_a;                // A's cost for one KV head
+    int tokens, tiles, pairs;        // of the short requests
+    int dense;                       // 1: the short requests' tokens are the rows [base, base + tokens)
+    int base;
+    int runs;                        // CTAs with work: no run shorter than a tile, so that every run inside an item holds one
+};
 
 struct SharedArgs {
-    const uint16_t *q, *pk, *pv;
     const int32_t *q_start, *lens, *table, *prefix;
+    const uint16_t* q;
     uint16_t* out; float* lse;
-    int rows, B, width, prefix_len, max_new, n_pages, page_n, page_shift, Hq, Hkv, r;
-    int tpt;       // tokens of a row tile: 128 / r
-    int runs;      // CTAs of the prefix kernel
-    float* part_o;   // [slot][2 streams][128 rows][128]
-    float2* part_ml; // [slot][2 streams][128 rows]: maximum (of q.k, unscaled), sum
+    int rows, B, width, prefix_len, prefix_tiles, max_new, n_pages, page_n, page_shift, Hq, Hkv, r;
+    int tpt;   // tokens of a row tile: 128 / r
+    int runs;  // CTAs of the main kernel: an SM each
+    int own_rows;  // rows that a B item's parts have room for
+    // workspace
+    PlanHead* head;
+    int4* req;              // [B] first row, rows, own tokens (checked), short tokens before it
+    long long *c_at, *b_at; // [B + 1] cost of the C and B items before request b
+    int* cut;               // [runs][16 ints] the C item that run c is the second to work on (see CutRecord)
+    // parts: o [slot][2 streams][128 dims][rows], ml [slot][2 streams][rows] (maximum of q.k, unscaled; sum)
+    float *a_o, *b_o, *c_o;
+    float2 *a_ml, *b_ml, *c_ml;
     int* err;
 };
 
-// Request b's rows and own tokens, checked: rows [first, first + n), own tokens [0, len).
-struct Request { int first, n, len; };
+// the run that holds place w of the line, and where run c begins
+__device__ __forceinline__ int run_of(const PlanHead& p, long long w) { return (int)(((w + 1) * p.runs - 1) / p.work); }
+__device__ __forceinline__ long long run_begin(const PlanHead& p, int c) { return p.work * min(c, p.runs) / p.runs; }
 
-__device__ __forceinline__ Request request_of(const SharedArgs& a, int b, int& bad) {
-    Request r;
-    const int s = a.q_start[b], e = a.q_start[b + 1];
-    r.first = s;
-    r.n = e - s;
-    if (s < 0 || e < s || e > a.rows || r.n > a.max_new) {
-        bad |= HSQ_DEVERR_LEN;
-        r.first = r.n = 0;
+// virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostPair a key
+__device__ __forceinline__ long long unit_base(const SharedArgs& a, int n, int len) {
+    return (long long)a.prefix_tiles * kTileKeys + max(len - n, 0);
+}
+// cost of the units before u (u < number of units), D tokens each
+__device__ __forceinline__ long long units_before(long long base, int D, long long u) {
+    return kCostPair * (u * base + D * (u * (u + 1) / 2));
+}
+
+// ---------------------------------------------------------------------------------------
+// Plan: one CTA scans the requests.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 512;
+
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ SharedArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ long long s_w[3][kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int bad = 0;
+    long long before[3] = {0, 0, 0};  // short tokens, C cost, B cost
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int first = 0, n = 0, len = 0;
+        if (b < a.B) {
+            const int s = a.q_start[b], e = a.q_start[b + 1], l = a.lens[b];
+            first = s;
+            n = e - s;
+            if (s < 0 || e < s || e > a.rows || n > a.max_new) {
+                bad |= HSQ_DEVERR_LEN;
+                first = n = 0;
+            }
+            len = (int)min((long long)max(l, 0), (long long)a.width << a.page_shift);
+            if (len != l || len < n) bad |= HSQ_DEVERR_LEN;
+        }
+        const bool brief = n <= a.tpt;
+        long long x[3] = {brief ? n : 0, 0, 0}, own[3];
+        if (n > 0 && brief && len > 0) x[2] = (long long)a.Hkv * (len + kItemKeys) * kCostOwn;
+        if (!brief) {
+            const int D = 2 * a.tpt, units = (n + D - 1) / D;
+            const long long base = unit_base(a, n, len);
+            x[1] = a.Hkv * (units_before(base, D, units - 1) + kCostPair * (base + n));
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            own[k] = x[k];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(kFull, x[k], o);
+                if (lane >= o) x[k] += u;
+            }
+            if (lane == 31) s_w[k][warp] = x[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            long long t = before[k], mine = 0;
+            for (int w = 0; w < kPlanThreads / 32; ++w) {
+                if (w == warp) mine = t;
+                t += s_w[k][w];
+            }
+            before[k] = t;
+            x[k] += mine - own[k];
+        }
+        if (b < a.B) {
+            a.req[b] = make_int4(first, n, len, (int)x[0]);
+            a.c_at[b] = x[1];
+            a.b_at[b] = x[2];
+        }
+        __syncthreads();
     }
-    const int len = a.lens[b];
-    const long long cap = (long long)a.width << a.page_shift;
-    r.len = (int)min((long long)max(len, 0), cap);
-    if (len != r.len || r.len < r.n) bad |= HSQ_DEVERR_LEN;
-    return r;
-}
-
-// ---- the prefix's work: key tiles of (KV head, pair of row tiles), cut into equal runs ----
-
-struct PrefixPlan {
-    int tiles, pairs, steps;  // row tiles in use, pairs of them, key tiles
-    long long work;           // Hkv * pairs * steps
-};
-
-__device__ __forceinline__ PrefixPlan prefix_plan(const SharedArgs& a) {
-    PrefixPlan p;
-    const int live = min(max(a.q_start[a.B], 0), a.rows);
-    p.tiles = (live + a.tpt - 1) / a.tpt;
-    p.pairs = (p.tiles + 1) >> 1;
-    p.steps = (a.prefix_len + kTileKeys - 1) / kTileKeys;
-    p.work = (long long)a.Hkv * p.pairs * p.steps;
-    return p;
-}
-
-// run c covers the steps [c work / runs, (c + 1) work / runs); an item's segment in run c keeps its
-// parts in slot item + c (segments in order raise one of the two by one, so slots are unique)
-__device__ __forceinline__ long long run_begin(const PrefixPlan& p, int runs, int c) { return p.work * c / runs; }
-__device__ __forceinline__ int run_of(const PrefixPlan& p, int runs, long long w) {
-    return (int)(((w + 1) * runs - 1) / p.work);
-}
-
-// The parts of one row (token, head jj of KV head h): indices [at + k * step], k < n, of part_ml rows
-struct RowParts { size_t at; size_t step; int n; };
-
-__device__ __forceinline__ RowParts row_parts(const SharedArgs& a, const PrefixPlan& p, int h, int token, int jj) {
-    const int tile = token / a.tpt, pair = tile >> 1, stream = tile & 1;
-    const int row = (token - tile * a.tpt) * a.r + jj;
-    const long long item = (long long)h * p.pairs + pair, w0 = item * p.steps;
-    const int c0 = run_of(p, a.runs, w0), c1 = run_of(p, a.runs, w0 + p.steps - 1);
-    // a pair of one tile has its key tiles dealt to both streams
-    const bool split = tile == p.tiles - 1 && !(tile & 1);
-    RowParts x;
-    x.at = ((size_t)(item + c0) * 2 + stream) * kTileRows + row;
-    x.step = split ? kTileRows : 2 * kTileRows;
-    x.n = (c1 - c0 + 1) * (split ? 2 : 1);
-    return x;
+    if (bad) atomicOr(a.err, bad);
+    const int any_bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        PlanHead h;
+        h.tokens = (int)before[0];
+        h.tiles = (h.tokens + a.tpt - 1) / a.tpt;
+        h.pairs = (h.tiles + 1) >> 1;
+        const long long keys = (long long)a.prefix_tiles * kTileKeys;
+        h.head_a = (h.tiles >> 1) * keys * kCostPair + (h.tiles & 1) * keys * kCostOne;
+        h.work_a = a.Hkv * h.head_a;
+        h.work_c = before[1];
+        h.work = h.work_a + h.work_c + before[2];
+        h.base = a.q_start[0];
+        const int most = (h.tiles > 1 || h.work_c > 0 ? kCostPair : max(kCostOne, kCostOwn)) * kTileKeys;
+        h.runs = (int)max(1LL, min((long long)a.runs, h.work / most));
+        h.dense = !any_bad && before[1] == 0;
+        *a.head = h;
+        a.c_at[a.B] = before[1];
+        a.b_at[a.B] = before[2];
+    }
 }
 
 // One arrival for the whole warp, after every lane's writes.
@@ -155,56 +214,232 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Tensor-core kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7
-// (stream 1), warp 8 loads, warp 9 issues the MMAs (10 and 11 only give their registers away:
-// 168 a thread at launch, then 184 for the softmax warps, whose row of 128 logits
-// lives in registers, and 136 for the others).  A stream is a 128-row query tile with
-// its S / P and O in tensor memory.  The two streams either hold two row tiles and share every
-// key tile (so keys and values are loaded once for 256 rows), or, when only one row tile is
-// left, hold the same rows and take the key tiles in turn.  While one stream's softmax
-// runs, the tensor cores work for the other.
+// Main kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7 (stream 1),
+// warp 8 walks the run and loads keys and values, warp 9 issues the MMAs, warp 10 loads the queries
+// (11 only gives its registers away: 168 a thread at launch, then 184 for the softmax
+// warps, whose row of logits lives in registers, and 136 for the others).
+// A stream is a 128-row query tile with its S / P and O in tensor memory.  The two streams
+// either hold two row tiles and share every key tile (so keys and values are loaded once
+// for 256 rows), or (split) hold the same rows and take the key tiles in turn.  While
+// one stream's softmax runs, the tensor cores work for the other.
 //   shared memory: ring of five 32 KB tiles K0 V0 K1 V1 ... (TMA, 128-byte swizzle), two Q tiles;
 //   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kTcThreads = 384, kStages = 5;
+constexpr int kTcThreads = 384, kStages = 5, kQueue = 4;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = kStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
-// barriers: full[5] | empty[5] | q_full[2] | s_full[2] | p_full[2] | o_full[2] | tail | x_full
-constexpr int kTcBars = 2 * kStages + 10;
-constexpr uint32_t kOffMask = kOffBars + 8 * (kTcBars + 1);        // [8] pages of a key tile that lie in the pool
-constexpr uint32_t kTcSmem = kOffMask + 32 + 16 + 1024;      // + TMEM address, alignment
+// barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | seg_full[4] | seg_empty[4]
+constexpr int kTcBars = 2 * kStages + 11 + 2 * kQueue;
+constexpr uint32_t kOffMask = kOffBars + 8 * (kTcBars + 1);  // [8] pages of a key tile that lie in the pool
+constexpr uint32_t kOffSeg = kOffMask + 32;                  // [4] segments of the run
+constexpr uint32_t kSegBytes = 96;
+constexpr uint32_t kTcSmem = kOffSeg + kQueue * kSegBytes + 16 + 1024;  // + TMEM address, alignment
+constexpr int kSegReaders = 10;                              // 8 softmax warps, the MMA thread, the query loader
+
+// The key tiles [n0, n1) of an item that lie in this CTA's run.
+enum : int { kEnd = -1, kPrefixItem = 0, kOwnItem = 1, kWholeItem = 2, kCutItem = 3 };
+struct alignas(16) Segment {
+    int kind, h;
+    int tok0, tok1, toks0, toks1;  // each stream's tile: first token (A: of the packed ones), tokens
+    int n0, n1, end0, end1;        // a stream works on [n0, end)
+    int split;
+    int ptiles;                    // the item's tiles that are the prefix's
+    int olen, obase, first;        // own keys; token t sees min(olen, obase + t - first) of them
+    int b, slot, pad[3];
+};
+
+__device__ __forceinline__ int tiles_of(const Segment& s, int st) {
+    return s.split ? (s.n1 - s.n0 + 1 - st) >> 1 : (st ? s.end1 : s.end0) - s.n0;
+}
+// keys of tile n that are loaded
+__device__ __forceinline__ int keys_of(const SharedArgs& a, const Segment& s, int n) {
+    return min(kTileKeys, n < s.ptiles ? a.prefix_len - n * kTileKeys : s.olen - (n - s.ptiles) * kTileKeys);
+}
+
+// What the join has to know of a C item that run c is the second to work on.
+struct CutRecord { int valid, h, tok0, tok1, toks0, toks1, c0, c1; };
 
 // A place in the ring of stages, and the parity of its barriers' phase.
 struct Ring {
     uint32_t stage, phase;
-    __device__ __forceinline__ void advance(uint32_t by) {
+    __device__ __forceinline__ void advance(uint32_t by, uint32_t size = kStages) {
         stage += by;
-        if (stage >= kStages) {
-            stage -= kStages;
+        if (stage >= size) {
+            stage -= size;
             phase ^= 1;
         }
     }
 };
 
-// One run of key tiles [n0, n1) of an item.
-struct Segment {
-    int h, item;
-    int tok0, tok1;    // first token of each stream's tile
-    int toks0, toks1;  // its tokens
-    int n0, n1, end0, end1;
-    bool split;
-    int klen;          // keys in all
-    const int32_t* ids;  // page ids
-};
-
-// keys that token `t` of the request sees (own), or all (prefix)
-template <bool kOwn>
-__device__ __forceinline__ int key_limit(const Request& rq, int klen, int t) {
-    return kOwn ? min(klen, rq.len - rq.n + (t - rq.first) + 1) : klen;
+// The last b with at[b] <= x (at ascending, at[0] = 0, n entries), by a whole warp: 32 probes a step.
+__device__ __forceinline__ int warp_find(const long long* at, int n, long long x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int step = (len + 31) / 32, i = lo + lane * step;
+        const bool le = lane * step < len && at[i] <= x;
+        const int k = max(__popc(__ballot_sync(kFull, le)) - 1, 0);
+        len = min(step, len - k * step);
+        lo += k * step;
+    }
+    return lo;
 }
 
-template <bool kOwn>
+// Walks the CTA's run of the line (a whole warp, uniformly).
+struct Walker {
+    const SharedArgs& a;
+    const PlanHead& p;
+    long long at, end;      // the run
+    long long w0;           // where the current item begins
+    int zone, b, h, u, n, len, first;  // the item: A (h, u = pair), C (b, h, unit u), B (b, h)
+    long long cost;         // the item's
+    bool more;
+
+    __device__ __forceinline__ void load_request() {
+        const int4 q = a.req[b];
+        first = q.x;
+        n = q.y;
+        len = q.z;
+    }
+    __device__ __forceinline__ int units() const { return (n + 2 * a.tpt - 1) / (2 * a.tpt); }
+    __device__ __forceinline__ void set_cost() {
+        if (zone == 0) {
+            const bool one = u == p.pairs - 1 && (p.tiles & 1);
+            cost = (long long)a.prefix_tiles * kTileKeys * (one ? kCostOne : kCostPair);
+        } else if (zone == 1) {
+            const long long base = unit_base(a, n, len);
+            cost = kCostPair * (base + min(n, (u + 1) * 2 * a.tpt));
+        } else {
+            cost = (long long)(len + kItemKeys) * kCostOwn;
+        }
+    }
+    // the item that holds place x of the line
+    __device__ void locate(long long x) {
+        if (x >= p.work) {
+            more = false;
+            return;
+        }
+        if (x < p.work_a) {
+            zone = 0;
+            h = (int)(x / p.head_a);
+            const long long pair = (long long)a.prefix_tiles * kTileKeys * kCostPair;
+            u = min((int)((x - h * p.head_a) / pair), p.pairs - 1);
+            w0 = h * p.head_a + u * pair;
+        } else if (x < p.work_a + p.work_c) {
+            zone = 1;
+            const long long y = x - p.work_a;
+            b = warp_find(a.c_at, a.B, y);
+            load_request();
+            const long long per = (a.c_at[b + 1] - a.c_at[b]) / a.Hkv, z = y - a.c_at[b];
+            h = (int)(z / per);
+            const long long rem = z - h * per, base = unit_base(a, n, len);
+            const int D = 2 * a.tpt;
+            // units_before(u) <= rem: the quadratic's root, then exactly
+            const double bq = base + 0.5 * D;
+            u = (int)((sqrt(bq * bq + 2.0 * D * (double)rem / kCostPair) - bq) / D);
+            u = min(max(u, 0), units() - 1);
+            while (u > 0 && units_before(base, D, u) > rem) --u;
+            while (u + 1 < units() && units_before(base, D, u + 1) <= rem) ++u;
+            w0 = p.work_a + a.c_at[b] + h * per + units_before(base, D, u);
+        } else {
+            zone = 2;
+            const long long y = x - p.work_a - p.work_c;
+            b = warp_find(a.b_at, a.B, y);
+            load_request();
+            set_cost();
+            h = (int)((y - a.b_at[b]) / cost);
+            w0 = p.work_a + p.work_c + a.b_at[b] + h * cost;
+        }
+        set_cost();
+    }
+    __device__ void start(int c) {
+        at = run_begin(p, c);
+        end = run_begin(p, c + 1);
+        more = at < end;
+        if (more) locate(at);
+    }
+    __device__ void step() {  // to the next item
+        const long long w1 = w0 + cost;
+        if (w1 >= end) {
+            more = false;
+            return;
+        }
+        if (zone == 0 && u + 1 < p.pairs) { ++u; w0 = w1; set_cost(); return; }
+        if (zone == 0 && h + 1 < a.Hkv) { ++h; u = 0; w0 = w1; set_cost(); return; }
+        if (zone == 1 && u + 1 < units()) { ++u; w0 = w1; set_cost(); return; }
+        if (zone == 1 && h + 1 < a.Hkv) { ++h; u = 0; w0 = w1; set_cost(); return; }
+        if (zone == 2 && h + 1 < a.Hkv) { ++h; w0 = w1; return; }
+        locate(w1);
+    }
+    // The item's tiles in the run; false when none begins there (tile k lies at w0 + 128 k rate).
+    __device__ bool segment(Segment& s, CutRecord& cut, int c) {
+        const int rate = (zone == 0 ? (u == p.pairs - 1 && (p.tiles & 1) ? kCostOne : kCostPair) : zone == 1 ? kCostPair : kCostOwn) * kTileKeys;
+        s.h = h;
+        s.b = b;
+        s.obase = s.first = 0;
+        int tiles;
+        if (zone == 0) {
+            s.kind = kPrefixItem;
+            s.split = u == p.pairs - 1 && (p.tiles & 1);
+            s.tok0 = 2 * u * a.tpt;
+            s.tok1 = s.split ? s.tok0 : s.tok0 + a.tpt;
+            s.toks0 = min(a.tpt, p.tokens - s.tok0);
+            s.toks1 = min(a.tpt, p.tokens - s.tok1);
+            s.ptiles = tiles = a.prefix_tiles;
+            s.olen = 0;
+            s.end0 = s.end1 = tiles;
+        } else if (zone == 1) {
+            const int left = n - u * 2 * a.tpt;  // tokens from this pair's first on
+            s.split = 0;
+            s.toks0 = left > a.tpt ? a.tpt : 0;   // (a single tile goes to stream 1)
+            s.toks1 = left > a.tpt ? min(left - a.tpt, a.tpt) : left;
+            s.tok0 = first + u * 2 * a.tpt;
+            s.tok1 = s.tok0 + s.toks0;
+            s.ptiles = a.prefix_tiles;
+            s.first = first;
+            s.obase = len - n + 1;
+            s.olen = min(len, max(0, s.obase + s.tok1 + s.toks1 - 1 - first));
+            tiles = s.ptiles + (s.olen + kTileKeys - 1) / kTileKeys;
+            const int l0 = min(s.olen, max(0, s.obase + s.tok0 + s.toks0 - 1 - first));
+            s.end0 = s.toks0 ? s.ptiles + (l0 + kTileKeys - 1) / kTileKeys : 0;
+            s.end1 = tiles;
+        } else {
+            s.kind = kOwnItem;
+            s.split = 1;
+            s.tok0 = s.tok1 = s.first = first;
+            s.toks0 = s.toks1 = n;
+            s.ptiles = 0;
+            s.obase = len - n + 1;
+            s.olen = len;
+            s.end0 = s.end1 = tiles = (len + kTileKeys - 1) / kTileKeys;
+        }
+        s.n0 = at <= w0 ? 0 : (int)((at - w0 + rate - 1) / rate);
+        s.n1 = (int)min((long long)tiles, (end - w0 + rate - 1) / rate);
+        if (tiles == 0) {  // (C only: rows that see nothing are written all the same, where the item begins)
+            if (at > w0) return false;
+            s.n0 = s.n1 = 0;
+        } else if (s.n0 >= s.n1) {
+            return false;
+        }
+        s.end0 = min(max(s.end0, s.n0), s.n1);
+        s.end1 = min(max(s.end1, s.n0), s.n1);
+        if (zone == 0) {
+            s.slot = h * p.pairs + u + c;  // (segments in order raise item or run by one: each slot has one)
+        } else if (zone == 2) {
+            s.slot = b * a.Hkv + h + c;
+        } else {
+            s.kind = s.n0 == 0 && s.n1 == tiles ? kWholeItem : kCutItem;
+            s.slot = 2 * c + (s.n0 == 0);  // the run's first segment, or its last
+            if (s.kind == kCutItem && s.n0 > 0) {
+                const int c0 = run_of(p, w0);
+                if (c0 == c - 1) cut = CutRecord{1, h, s.tok0, s.tok1, s.toks0, s.toks1, c0, run_of(p, w0 + (long long)(tiles - 1) * rate)};
+            }
+        }
+        return true;
+    }
+};
+
 __global__ void __launch_bounds__(kTcThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ SharedArgs a) {
@@ -212,92 +447,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t raw = smem_addr(tc_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = tc_raw + (base - raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t full = base + kOffBars, empty = full + 8 * kStages, q_full = empty + 8 * kStages;
-    const uint32_t s_full = q_full + 16, p_full = s_full + 16, o_full = p_full + 16, tail = o_full + 16, x_full = tail + 8;
+    const uint32_t full = base + kOffBars, empty = full + 8 * kStages, q_full = empty + 8 * kStages, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_full = p_full + 16, tail = o_full + 16;
+    const uint32_t seg_full = tail + 8, seg_empty = seg_full + 8 * kQueue;
     volatile uint32_t* s_mask = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask);
-    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask + 32);
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffSeg + kQueue * kSegBytes);
     int bad = 0;
-
-    // ---- what this CTA works on ----
-    Request rq{0, 0, 0};
-    PrefixPlan plan = prefix_plan(a);
-    long long w = 0, w_end = 0;
-    int unit = 0;
-    const int32_t* own_ids = nullptr;
-    bool have = true;
-    if (kOwn) {
-        // pair ids: request b's start at q_start[b] / (2 tpt) + b, which leaves room for all of them; the last ids first
-        // (later tokens see more keys)
-        const int two = 2 * a.tpt, id = (int)(gridDim.y - 1 - blockIdx.y);
-        int below = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kTcThreads) {
-            const int b = b0 + tid;
-            below += __syncthreads_count(b < a.B && max(a.q_start[b], 0) / two + b <= id);
-        }
-        const int b = max(below - 1, 0);
-        rq = request_of(a, b, bad);
-        unit = id - (max(a.q_start[b], 0) / two + b);
-        have = below > 0 && rq.n * a.r > kFewRows && unit * two < rq.n;
-        own_ids = a.table + (size_t)b * a.width;
-    } else {
-        w = run_begin(plan, a.runs, blockIdx.x);
-        w_end = run_begin(plan, a.runs, blockIdx.x + 1);
-        have = w < w_end;
-    }
-    if (!kOwn) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (!have) {
-        if (kOwn) {
-            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // (a grid that ends has seen its predecessor end)
-        }
-        return;
-    }
-
-    // the next segment; false when there is none
-    auto next = [&](long long& w, Segment& s) {
-        if (w >= w_end) return false;
-        if (kOwn) {
-            s.h = blockIdx.x;
-            s.item = 0;
-            const int left = rq.n - unit * 2 * a.tpt;  // tokens from this pair's first on
-            s.split = left <= a.tpt;
-            s.toks0 = min(left, a.tpt);
-            s.toks1 = s.split ? s.toks0 : min(left - a.tpt, a.tpt);
-            s.tok0 = rq.first + unit * 2 * a.tpt;
-            s.tok1 = s.split ? s.tok0 : s.tok0 + a.tpt;
-            s.klen = max(0, key_limit<true>(rq, rq.len, s.tok1 + s.toks1 - 1));
-            s.ids = own_ids;
-            s.n0 = 0;
-            s.n1 = (s.klen + kTileKeys - 1) / kTileKeys;
-            const int l0 = max(0, key_limit<true>(rq, s.klen, s.tok0 + s.toks0 - 1));
-            s.end0 = (l0 + kTileKeys - 1) / kTileKeys;
-            s.end1 = s.n1;
-            w = w_end;
-        } else {
-            s.item = (int)(w / plan.steps);
-            s.h = s.item / plan.pairs;
-            const int pair = s.item - s.h * plan.pairs;
-            s.split = 2 * pair + 1 == plan.tiles;
-            const int live = min(max(a.q_start[a.B], 0), a.rows);
-            s.tok0 = 2 * pair * a.tpt;
-            s.tok1 = s.split ? s.tok0 : s.tok0 + a.tpt;
-            s.toks0 = min(a.tpt, live - s.tok0);
-            s.toks1 = min(a.tpt, live - s.tok1);
-            s.klen = a.prefix_len;
-            s.ids = a.prefix;
-            s.n0 = (int)(w - (long long)s.item * plan.steps);
-            s.n1 = (int)min((long long)plan.steps, s.n0 + (w_end - w));
-            s.end0 = s.end1 = s.n1;
-            w += s.n1 - s.n0;
-        }
-        return true;
-    };
-    if (kOwn) w_end = 1;
-    // key tiles that stream s takes in a segment
-    auto tiles_of = [](const Segment& s, int st) {
-        if (!s.split) return (st ? s.end1 : s.end0) - s.n0;
-        return (s.n1 - s.n0 + 1 - st) >> 1;
-    };
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -306,12 +462,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_empty + 8 * i, 1);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_full + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
         }
         mbar_init(tail, 1);
-        mbar_init(x_full, 4);
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(seg_full + 8 * i, 1);
+            mbar_init(seg_empty + 8 * i, kSegReaders);
+        }
         mbar_init_fence();
     }
     if (warp == 9) {
@@ -325,20 +485,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool failed = false;
     Segment s;
 
+    // the next segment of the queue, read by one thread or by a warp
+    auto receive = [&](Ring& q, bool release) {
+        mbar_wait_fast(seg_full + 8 * q.stage, q.phase, failed);
+        const int4* src = reinterpret_cast<const int4*>(gbase + kOffSeg + q.stage * kSegBytes);
+        int4* dst = reinterpret_cast<int4*>(&s);
+        if (failed) {
+            s.kind = kEnd;
+            return false;
+        }
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Segment) / 16); ++i) dst[i] = src[i];
+        if (release) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_empty + 8 * q.stage);
+        } else {
+            mbar_arrive(seg_empty + 8 * q.stage);
+        }
+        q.advance(1, kQueue);
+        return s.kind != kEnd;
+    };
+
     // (128 x 168 x 3 registers at launch: 2 x 128 x 184 + 128 x 136)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 136;\n");
         if (warp == 8) {
-            // ---- loads: per key tile the K pages, then the V pages (lane i: page i of the tile) ----
-            Ring ring{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
+            // ---- the run's segments, and per key tile the K pages, then the V pages (lane i: page i of the tile) ----
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            Ring ring{0, 1}, queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
             uint32_t step = 0, tail_par = 0;
             const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
-            while (next(w, s)) {
+            const PlanHead plan = *a.head;
+            Walker walk{a, plan};
+            walk.start(blockIdx.x);
+            CutRecord cut{0, 0, 0, 0, 0, 0, 0, 0};
+            auto send = [&] {
+                mbar_wait_fast(seg_empty + 8 * queue.stage, queue.phase, failed);
+                failed = __any_sync(kFull, failed);
+                if (lane == 0) {
+                    *reinterpret_cast<Segment*>(gbase + kOffSeg + queue.stage * kSegBytes) = s;
+                    mbar_arrive(seg_full + 8 * queue.stage);
+                }
+                __syncwarp();
+                queue.advance(1, kQueue);
+            };
+            for (; walk.more && !failed; walk.step()) {
+                if (!walk.segment(s, cut, blockIdx.x)) continue;
+                send();
+                const int32_t* own = a.table + (size_t)s.b * a.width;
 #pragma unroll 1
-                for (int n = s.n0; n < s.n1; ++n, ++step) {
-                    const int nk = min(kTileKeys, s.klen - n * kTileKeys), np = (nk + a.page_n - 1) >> a.page_shift;
+                for (int n = s.n0; n < s.n1 && !failed; ++n, ++step) {
+                    const bool pre = n < s.ptiles;
+                    const int nk = keys_of(a, s, n), np = (nk + a.page_n - 1) >> a.page_shift;
                     int id = -1;
-                    if (lane < np) id = s.ids[((n * kTileKeys) >> a.page_shift) + lane];
+                    if (lane < np)
+                        id = (pre ? a.prefix : own)[((pre ? n : n - s.ptiles) * kTileKeys >> a.page_shift) + lane];
                     const bool in = lane < np && id >= 0 && id < a.n_pages;
                     const uint32_t mask = __ballot_sync(kFull, in);
                     if (mask != (1u << np) - 1u) bad |= HSQ_DEVERR_PAGE;
@@ -355,7 +556,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const bool ragged = kv && (nk & 15);
                         const uint32_t lands = ragged ? tail : bar;
                         if (lane == 0) {
-                            if (!kv) s_mask[step & 7] = mask;
+                            if (!kv) s_mask[step & 7] = mask == (1u << np) - 1u ? ~0u : mask;
                             mbar_expect_tx(lands, np * page_bytes);
                         }
                         __syncwarp();
@@ -378,31 +579,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         ring.advance(1);
                     }
-                    if (failed) break;
                 }
-                if (failed) break;
             }
-            if (failed) {  // see the copies in flight land before the CTA ends
-                for (int i = 0; i < kStages; ++i) mbar_wait(full + 8 * i, i < (int)ring.stage ? ring.phase ^ 1 : ring.phase);
-            }
+            s.kind = kEnd;
+            send();
+            if (lane == 0) *reinterpret_cast<CutRecord*>(a.cut + 16 * blockIdx.x) = cut;
+            if (failed)  // see the copies in flight land before the CTA ends
+                for (int i = 0; i < kStages; ++i) mbar_wait(full + 8 * i, i < (int)ring.stage ? ring.phase ^ 1 : ring.phase, 1 << 12);
         } else if (warp == 9 && elect_one()) {
             // ---- MMAs, one thread ----
-            // Straight code: per pair of key tiles three waits, each one poll; the tensor pipe takes an MMA every 64
+            // Straight code: per pair of key tiles four waits, each one poll; the tensor pipe takes an MMA every 64
             // cycles and holds only one or two more, so what the thread does in between shows.
-            const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
             constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128), idFull = idesc_bf16_f32(128, 128);
-            Ring kr{0, 0}, vr{1, 0};
+            Ring kr{0, 0}, vr{1, 0}, queue{0, 0};
             uint32_t q_par = 0, p_par = 0;  // a bit for each stream
-            auto load_q = [&](int st, int tok) {
-                const uint32_t dst = base + kOffQ + st * kTileBytes, bar = q_full + 8 * st;
-                mbar_expect_tx(bar, q_bytes);
-                tma_3d(dst, &mq, 0, s.h * a.r, tok, bar);
-                tma_3d(dst + kHalfBytes, &mq, 64, s.h * a.r, tok, bar);
-            };
-            auto load_both = [&] {
-                if (tiles_of(s, 0) > 0) load_q(0, s.tok0);
-                if (tiles_of(s, 1) > 0) load_q(1, s.tok1);
-            };
             auto scores = [&](int st, uint32_t idS) {  // S = Q K^T of the tile at kr
                 const uint32_t dS = tmem + 128 * st;
                 const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + kr.stage * kTileBytes);
@@ -423,7 +613,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int k = 1; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
             };
-            auto product_last = [&](int st, int ks16, uint32_t begun) {  // the same of an item's last tile: ks16 groups of 16 keys
+            auto product_n = [&](int st, int ks16, uint32_t begun) {  // the same of a tile of ks16 groups of 16 keys
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
                 const uint64_t dv = sw128_mn_desc(base + vr.stage * kTileBytes, kHalfBytes);
                 mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
@@ -432,86 +622,144 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int k = 0; k < ks16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
             };
-            bool more = next(w, s);
-            if (more) load_both();
-            while (more) {
-                const int n_last = s.n1 - 1, nk_last = s.klen - n_last * kTileKeys;
-                const uint32_t id_last = nk_last < kTileKeys ? idesc_bf16_f32(128, (nk_last + 15) & ~15) : idFull;
-                const int ks_last = min(8, (nk_last + 15) >> 4);
-                if (tiles_of(s, 0) > 0) { mbar_wait_fast(q_full, q_par & 1, failed); q_par ^= 1; }
-                if (tiles_of(s, 1) > 0) { mbar_wait_fast(q_full + 8, (q_par >> 1) & 1, failed); q_par ^= 2; }
+            auto k_wait = [&] { mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed); };
+            auto v_wait = [&] { mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed); };
+            auto k_done = [&] { mma_commit(empty + 8 * kr.stage); kr.advance(2); };
+            auto v_done = [&] { mma_commit(empty + 8 * vr.stage); vr.advance(2); };
+            auto groups = [&](int n) { return (keys_of(a, s, n) + 15) >> 4; };
+            while (receive(queue, false)) {
+                const bool has0 = tiles_of(s, 0) > 0, has1 = tiles_of(s, 1) > 0;
+                if (has0) { mbar_wait_fast(q_full, q_par & 1, failed); q_par ^= 1; }
+                if (has1) { mbar_wait_fast(q_full + 8, (q_par >> 1) & 1, failed); q_par ^= 2; }
+                const int n0 = s.n0, n1 = s.n1, end0 = s.end0;
                 if (!s.split) {
-                    const int n0 = s.n0, n1 = s.n1, end0 = s.end0;
                     if (n1 > n0) {
-                        mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
-                        if (n0 < end0) scores(0, n0 == n_last ? id_last : idFull);
-                        scores(1, n0 == n_last ? id_last : idFull);
-                        mma_commit(empty + 8 * kr.stage);
-                        kr.advance(2);
+                        // the tiles that are not whole: the prefix's last and the item's last
+                        const int r1 = (a.prefix_len & 127) ? s.ptiles - 1 : -2, both = min(end0, n1 - 1);
+                        k_wait();
+                        if (n0 < end0) scores(0, idesc_bf16_f32(128, 16 * groups(n0)));
+                        scores(1, idesc_bf16_f32(128, 16 * groups(n0)));
+                        k_done();
                         int n = n0 + 1;
-                        const int both = min(end0, n_last);
+                        while (n < n1) {
+                            const int to = r1 >= n ? min(both, r1) : both;
+                            if (n - 1 != r1) {
 #pragma unroll 1
-                        for (; n < both; ++n) {  // P V of tile n - 1 and S of tile n, all tiles whole
-                            mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
-                            mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
-                            product(0, n > n0 + 1);
-                            scores(0, idFull);
-                            product(1, n > n0 + 1);
-                            mma_commit(empty + 8 * vr.stage);
-                            vr.advance(2);
-                            scores(1, idFull);
-                            mma_commit(empty + 8 * kr.stage);
-                            kr.advance(2);
+                                for (; n < to; ++n) {  // P V of tile n - 1 and S of tile n, both whole
+                                    k_wait();
+                                    v_wait();
+                                    product(0, n > n0 + 1);
+                                    scores(0, idFull);
+                                    product(1, n > n0 + 1);
+                                    v_done();
+                                    scores(1, idFull);
+                                    k_done();
+                                }
+                            }
+                            if (n < n1) {  // stream 0 at its end, or a tile that is not whole
+                                const uint32_t idS = idesc_bf16_f32(128, 16 * groups(n));
+                                const int gp = groups(n - 1);
+                                k_wait();
+                                v_wait();
+                                if (n <= end0) product_n(0, gp, n > n0 + 1);
+                                if (n < end0) scores(0, idS);
+                                product_n(1, gp, n > n0 + 1);
+                                v_done();
+                                scores(1, idS);
+                                k_done();
+                                ++n;
+                            }
                         }
-#pragma unroll 1
-                        for (; n < n1; ++n) {  // stream 0 ends before stream 1, or the last tile
-                            const uint32_t idS = n == n_last ? id_last : idFull;
-                            mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
-                            mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
-                            if (n <= end0) product_last(0, 8, n > n0 + 1);
-                            if (n < end0) scores(0, idS);
-                            product_last(1, 8, n > n0 + 1);
-                            mma_commit(empty + 8 * vr.stage);
-                            vr.advance(2);
-                            scores(1, idS);
-                            mma_commit(empty + 8 * kr.stage);
-                            kr.advance(2);
-                        }
-                        mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
-                        if (end0 == n1) product_last(0, ks_last, n_last > n0);
-                        if (end0 > n0) mma_commit(o_full);
-                        product_last(1, ks_last, n_last > n0);
+                        if (has0) mma_commit(q_empty);
+                        mma_commit(q_empty + 8);
+                        const int gp = groups(n1 - 1);
+                        v_wait();
+                        if (end0 == n1) product_n(0, gp, n1 - 1 > n0);
+                        if (has0) mma_commit(o_full);
+                        product_n(1, gp, n1 - 1 > n0);
                         mma_commit(o_full + 8);
-                        mma_commit(empty + 8 * vr.stage);
-                        vr.advance(2);
+                        v_done();
                     }
                 } else {
 #pragma unroll 1
-                    for (int n = s.n0; n < s.n1 + 2; ++n) {
-                        const int st = (n - s.n0) & 1, np = n - 2;
-                        if (np >= s.n0) {
-                            mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed);
-                            product_last(st, np == n_last ? ks_last : 8, np > s.n0 + 1);
-                            mma_commit(empty + 8 * vr.stage);
-                            vr.advance(2);
-                            if (n >= s.n1) mma_commit(o_full + 8 * st);
+                    for (int n = n0; n < n1 + 2; ++n) {
+                        const int st = (n - n0) & 1, np = n - 2;
+                        if (np >= n0) {
+                            v_wait();
+                            const int gp = groups(np);
+                            if (gp == 8) product(st, np > n0 + 1);
+                            else product_n(st, gp, np > n0 + 1);
+                            v_done();
+                            if (n >= n1) mma_commit(o_full + 8 * st);
                         }
-                        if (n < s.n1) {
-                            mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed);
-                            scores(st, n == n_last ? id_last : idFull);
-                            mma_commit(empty + 8 * kr.stage);
-                            kr.advance(2);
+                        if (n < n1) {
+                            k_wait();
+                            scores(st, idesc_bf16_f32(128, 16 * groups(n)));
+                            k_done();
+                            if (n + 2 >= n1) mma_commit(q_empty + 8 * st);  // (the stream's last S of the segment)
                         }
                     }
                 }
+            }
+        } else if (warp == 10) {
+            // ---- queries of the segments' streams ----
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            Ring queue{0, 0};
+            uint32_t q_par = 3;  // (the buffers start empty)
+            const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
+            const PlanHead plan = *a.head;
+            while (receive(queue, true)) {
+#pragma unroll 1
+                for (int st = 0; st < 2; ++st) {
+                    if (tiles_of(s, st) <= 0) continue;
+                    const uint32_t dst = base + kOffQ + st * kTileBytes, bar = q_full + 8 * st;
+                    const int tok = st ? s.tok1 : s.tok0, toks = st ? s.toks1 : s.toks0;
+                    mbar_wait_fast(q_empty + 8 * st, (q_par >> st) & 1, failed);
+                    failed = __any_sync(kFull, failed);
+                    q_par ^= 1u << st;
+                    if (s.kind != kPrefixItem || plan.dense) {  // tokens side by side
+                        const int row = s.kind == kPrefixItem ? plan.base + tok : tok;
+                        if (lane == 0) {
+                            mbar_expect_tx(bar, q_bytes);
+                            tma_3d(dst, &mq, 0, s.h * a.r, row, bar);
+                            tma_3d(dst + kHalfBytes, &mq, 64, s.h * a.r, row, bar);
+                        }
+                        __syncwarp();
+                    } else {  // the short requests' tokens among others: row by row, into the swizzled layout
+#pragma unroll 1
+                        for (int i0 = 0; i0 < toks; i0 += 32) {
+                            int row = -1;
+                            if (i0 + lane < toks) {  // the request of packed token tok + i: the last that begins at or before it
+                                int lo = 0, hi = a.B;
+                                while (hi - lo > 1) {
+                                    const int mid = (lo + hi) >> 1;
+                                    if (a.req[mid].w <= tok + i0 + lane) lo = mid; else hi = mid;
+                                }
+                                const int4 q = a.req[lo];
+                                row = q.x + tok + i0 + lane - q.w;
+                            }
+                            const int chunks = min(32, toks - i0) * a.r * 16;
+#pragma unroll 4
+                            for (int e0 = 0; e0 < chunks; e0 += 32) {
+                                const int e = e0 + lane, hr = e >> 4, c = e & 15, i = min(hr / a.r, 31), jj = hr - (hr / a.r) * a.r;
+                                const int from = __shfl_sync(kFull, row, i);
+                                if (e < chunks) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(a.q + ((size_t)from * a.Hq + s.h * a.r + jj) * 128 + 8 * c);
+                                    const int rt = (i0 + i) * a.r + jj;
+                                    *reinterpret_cast<uint4*>(gbase + (dst - base) + (c >> 3) * kHalfBytes + rt * 128 +
+                                                              (((c & 7) ^ (rt & 7)) << 4)) = v;
+                                }
+                            }
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar);
+                    }
+                }
                 if (failed) break;
-                more = next(w, s);
-                if (more) load_both();  // (every S of the segment is done: its P has been seen)
             }
-            if (failed) {  // query tiles in flight land before the CTA ends
-                mbar_wait(q_full, q_par & 1, 1 << 12);
-                mbar_wait(q_full + 8, (q_par >> 1) & 1, 1 << 12);
-            }
+            if (failed)  // query tiles in flight land before the CTA ends
+                for (int st = 0; st < 2; ++st) mbar_wait(q_full + 8 * st, (q_par >> st) & 1, 1 << 12);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
@@ -520,16 +768,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + 128 * st, tO = tmem + lanes + 256 + 128 * st;
         uint32_t s_par = 0, o_par = 0;
+        Ring queue{0, 0};
         int step0 = 0;
-        while (next(w, s)) {
-            const int own_token = row / a.r;
-            const bool live = own_token < (st ? s.toks1 : s.toks0);
-            const bool idle = 32 * (warp & 3) >= (st ? s.toks1 : s.toks0) * a.r;  // (warp-uniform) no row of this warp in use
-            const int lim = live ? key_limit<kOwn>(rq, s.klen, (st ? s.tok1 : s.tok0) + own_token) : 0;
-            const int lim_min = key_limit<kOwn>(rq, s.klen, (st ? s.tok1 : s.tok0));
+        const int row_token = row / a.r;
+        while (receive(queue, true)) {
+            const int toks = st ? s.toks1 : s.toks0, tok = st ? s.tok1 : s.tok0, stop = st ? s.end1 : s.end0;
+            const bool live = row_token < toks;
+            const bool idle = 32 * (warp & 3) >= toks * a.r;  // (warp-uniform) no row of this warp in use
+            const int own_min = min(s.olen, s.obase + tok - s.first);             // own keys that the tile's first row sees
+            const int own_lim = min(s.olen, s.obase + tok - s.first + row_token); // and this row
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int n = s.n0 + (s.split ? st : 0); n < (st ? s.end1 : s.end0); n += s.split ? 2 : 1) {
+            for (int n = s.n0 + (s.split ? st : 0); n < stop; n += s.split ? 2 : 1) {
                 mbar_wait_fast(s_full + 8 * st, s_par, failed);
                 s_par ^= 1;
                 if (!idle) {
@@ -538,18 +788,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // where the tile's sum shows that the logits have outgrown m by far; every other tile goes without
                     // (a third of the softmax's time).
                     tc_fence_after();
-                    const int nk = min(kTileKeys, s.klen - n * kTileKeys), np = (nk + a.page_n - 1) >> a.page_shift;
+                    const int begin = (n < s.ptiles ? n : n - s.ptiles) * kTileKeys;
                     const uint32_t mask = s_mask[(step0 + n - s.n0) & 7];
-                    if ((n + 1) * kTileKeys > lim_min || mask != (1u << np) - 1u) {
+                    if (begin + kTileKeys > (n < s.ptiles ? a.prefix_len : own_min) || mask != ~0u) {
                         // keys past the row's limit or of no page: hidden in S itself, so that the code below (and the
                         // instruction cache) knows whole tiles only
+                        const int lim = !live ? 0 : (n < s.ptiles ? a.prefix_len : own_lim) - begin;
 #pragma unroll 1
                         for (int c0 = 0; c0 < 128; c0 += 32) {
                             float x[32];
                             tmem_ld32(tS + c0, x);
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (n * kTileKeys + c0 + c >= lim || !((mask >> ((c0 + c) >> a.page_shift)) & 1u)) x[c] = -INFINITY;
+                                if (c0 + c >= lim || !((mask >> ((c0 + c) >> a.page_shift)) & 1u)) x[c] = -INFINITY;
                             tmem_st32(tS + c0, x);
                         }
                     }
@@ -622,131 +873,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 mbar_wait_fast(o_full + 8 * st, o_par, failed);
                 o_par ^= 1;
             }
-            // (the join writes to the ring: the other stream's products first)
-            if (kOwn && tiles_of(s, 1 - st) > 0) mbar_wait_fast(o_full + 8 * (1 - st), 0, failed);
             failed = __any_sync(kFull, failed);
             if (failed) break;
             tc_fence_after();
-            if (!kOwn) {
-                const size_t at = ((size_t)(s.item + blockIdx.x) * 2 + st) * kTileRows + row;
-                if (live) a.part_ml[at] = make_float2(m, l);
-                if (any && !idle) {
+            if (s.kind == kWholeItem) {  // the result
+                const float inv = l > 0.f ? 1.0f / l : 0.f;
+                const size_t to = (size_t)(tok + row_token) * a.Hq + s.h * a.r + (row - row_token * a.r);
+                if (live && a.lse) a.lse[to] = l > 0.f ? m * kRsqrtD + logf(l) : -INFINITY;
+                if (!idle) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 128; c0 += 32) {
+                        float o[32];
+                        if (any) tmem_ld32(tO + c0, o);
+                        if (live) {
+                            uint4* dst = reinterpret_cast<uint4*>(a.out + to * 128 + c0);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 8)
+                                dst[c >> 3] = l > 0.f ? make_uint4(pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
+                                                                   pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv))
+                                                      : make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
+            } else if (!idle) {  // a part: dims apart, rows side by side, so that a warp writes whole lines
+                const int pitch = s.kind == kOwnItem ? a.own_rows : kTileRows;
+                const size_t at = (size_t)s.slot * 2 + st;
+                float* o_to = (s.kind == kPrefixItem ? a.a_o : s.kind == kOwnItem ? a.b_o : a.c_o) + at * 128 * pitch + row;
+                float2* ml_to = (s.kind == kPrefixItem ? a.a_ml : s.kind == kOwnItem ? a.b_ml : a.c_ml) + at * pitch + row;
+                if (live) *ml_to = make_float2(m, l);
+                if (any) {
 #pragma unroll 1
                     for (int c0 = 0; c0 < 128; c0 += 32) {
                         float o[32];
                         tmem_ld32(tO + c0, o);
                         if (live) {
-                            float4* dst = reinterpret_cast<float4*>(a.part_o + at * 128 + c0);
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) dst[c >> 2] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                            for (int c = 0; c < 32; ++c) o_to[(size_t)(c0 + c) * pitch] = o[c];
                         }
-                    }
-                }
-            } else {
-                // Join: the two streams of a split pair, then the prefix's parts.  A thread has its row's statistics; the
-                // sums go through shared memory (the ring is at rest), where the warp takes its 32 rows one after
-                // another, a lane four dims, so that parts are read and results written in whole lines (thread by
-                // thread, row by row, this took 25 us of a CTA's 35).
-                constexpr int kPitch = 132;  // floats: 16-byte columns of 8 rows fall into different banks
-                float* mine = reinterpret_cast<float*>(gbase) + warp * 32 * kPitch;
-                const float* other = mine + 4 * 32 * kPitch;
-                float2* xml = reinterpret_cast<float2*>(gbase + 8 * 32 * kPitch * 4);
-                float M = m, L = l, w_me = 1.f, w_ot = 0.f;
-                auto put = [&](float scale) {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < 128; c0 += 32) {
-                        float o[32];
-                        if (any) tmem_ld32(tO + c0, o);
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4)
-                            *reinterpret_cast<float4*>(mine + lane * kPitch + c0 + c) =
-                                any && scale > 0.f ? make_float4(o[c] * scale, o[c + 1] * scale, o[c + 2] * scale, o[c + 3] * scale)
-                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                };
-                if (s.split) {
-                    if (st == 1) {
-                        xml[row] = make_float2(m, l);
-                        put(1.f);
-                        warp_arrive(x_full);
-                        break;
-                    }
-                    mbar_wait_fast(x_full, 0, failed);
-                    failed = __any_sync(kFull, failed);
-                    if (failed) break;
-                    const float2 ot = xml[row];
-                    M = fmaxf(m, ot.x);
-                    w_me = m == -INFINITY ? 0.f : ex2_approx((m - M) * kLogitScaleLog2);
-                    w_ot = ot.x == -INFINITY ? 0.f : ex2_approx((ot.x - M) * kLogitScaleLog2);
-                    L = l * w_me + ot.y * w_ot;
-                }
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                const int token = (st ? s.tok1 : s.tok0) + own_token, jj = row - own_token * a.r;
-                RowParts rp{0, 0, 0};
-                if (live && plan.work > 0) rp = row_parts(a, plan, s.h, token, jj);
-                float Mall = M;
-                for (int k = 0; k < rp.n; ++k) Mall = fmaxf(Mall, __ldcg(&a.part_ml[rp.at + k * rp.step]).x);
-                const float wm = M == -INFINITY ? 0.f : ex2_approx((M - Mall) * kLogitScaleLog2);
-                w_me *= wm;
-                w_ot *= wm;
-                L *= wm;
-                for (int k = 0; k < rp.n; ++k) {
-                    const float2 ml = __ldcg(&a.part_ml[rp.at + k * rp.step]);
-                    if (ml.y > 0.f) L += ml.y * ex2_approx((ml.x - Mall) * kLogitScaleLog2);
-                }
-                const float inv = L > 0.f ? 1.0f / L : 0.f;
-                const size_t to = (size_t)token * a.Hq + s.h * a.r + jj;
-                if (live && a.lse) a.lse[to] = L > 0.f ? Mall * kRsqrtD + logf(L) : -INFINITY;
-                put(w_me);
-                __syncwarp();
-                const int count = min(32, (st ? s.toks1 : s.toks0) * a.r - 32 * (warp & 3));  // rows of this warp in use
-#pragma unroll 1
-                for (int i0 = 0; i0 < count; i0 += 4) {
-                    float4 x[4];
-                    int n[4], most = 0;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int i = i0 + u;  // (rows past count: computed from what lies there, not written)
-                        x[u] = *reinterpret_cast<const float4*>(mine + i * kPitch + 4 * lane);
-                        const float wo = __shfl_sync(kFull, w_ot, i);
-                        if (wo > 0.f) {
-                            const float4 y = *reinterpret_cast<const float4*>(other + i * kPitch + 4 * lane);
-                            x[u] = make_float4(fmaf(y.x, wo, x[u].x), fmaf(y.y, wo, x[u].y), fmaf(y.z, wo, x[u].z), fmaf(y.w, wo, x[u].w));
-                        }
-                        n[u] = __shfl_sync(kFull, rp.n, i);
-                        most = max(most, n[u]);
-                    }
-#pragma unroll 1
-                    for (int k = 0; k < most; ++k) {
-                        float2 ml[4];
-                        float4 v[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const size_t at = __shfl_sync(kFull, (unsigned long long)(rp.at + k * rp.step), i0 + u);
-                            ml[u] = make_float2(0.f, 0.f);
-                            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (k < n[u]) {
-                                ml[u] = __ldcg(&a.part_ml[at]);
-                                v[u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * 128) + lane);
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float Mu = __shfl_sync(kFull, Mall, i0 + u);
-                            if (ml[u].y > 0.f) {
-                                const float wp = ex2_approx((ml[u].x - Mu) * kLogitScaleLog2);
-                                x[u] = make_float4(fmaf(v[u].x, wp, x[u].x), fmaf(v[u].y, wp, x[u].y), fmaf(v[u].z, wp, x[u].z),
-                                                   fmaf(v[u].w, wp, x[u].w));
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float iu = __shfl_sync(kFull, inv, i0 + u);
-                        const size_t tu = __shfl_sync(kFull, (unsigned long long)to, i0 + u);
-                        if (i0 + u < count)
-                            *reinterpret_cast<uint2*>(a.out + tu * 128 + 4 * lane) =
-                                make_uint2(pack_bf16(x[u].x * iu, x[u].y * iu), pack_bf16(x[u].z * iu, x[u].w * iu));
                     }
                 }
             }
@@ -758,10 +921,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (bad) atomicOr(a.err, bad);
     tc_fence_before();
     __syncthreads();
-    if (kOwn) {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // (every thread: a grid that ends has seen its predecessor end)
-    }
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -769,302 +928,117 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// Few rows: one cluster per (request, KV head), NT tiles of 8 rows (tokens x heads).  The
-// cluster's warps take groups of 16 keys in turn; a warp's fragments come straight from the
-// pages in 16-byte loads, without shared memory or barriers:
-//   S^T (16 keys x 8 rows) = K (A operand, 16 x 16) Q^T: the product over the 128 dims
-//     may take them in any order, so lane (g, t) reads dims [32 j + 8 t, + 8) of keys g and
-//     g + 8 (j = 0..3) and feeds two k-steps from each load; Q is read the same way;
-//   O^T (dims x 8 rows) += V^T (A) P^T (B): lane (g, t) reads dims [64 c + 8 g, + 8) of keys
-//     2t, 2t + 1, 2t + 8, 2t + 9 and interleaves pairs of keys with byte permutes; row g
-//     of MMA i is dim 8 g + i, row g + 8 dim 64 + 8 g + i.  P^T comes from S^T by two 8 x 8
-//     transposes (movmatrix).
-// So 16 rows cost two MMAs where 8 cost one, and a warp's bytes in flight are its
-// registers: the next group's keys are on their way while this one's values arrive.
-// Bound by HBM.
+// Join.  A CTA takes 32 rows: of a tile of the short requests' tokens (parts of A and B), or of a row tile of a
+// C item that a cut divides.  Lane = row, a warp eight dims: parts are read in whole lines, weights
+// are the lane's own, and the parts' loads do not wait for one another.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kFewWarps = 4, kFewThreads = 32 * kFewWarps;
+constexpr int kJoinWarps = 16, kJoinDims = 128 / kJoinWarps;
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};\n"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
-
-template <int NT>
-__global__ void __launch_bounds__(kFewThreads) shared_few_kernel(const __grid_constant__ SharedArgs a) {
-    constexpr int kRows = 8 * NT;
-    __shared__ float s_o[kFewWarps][kRows][128];
-    __shared__ float2 s_ml[kFewWarps][kRows];
-    __shared__ float2 s_cta[kRows];
-    __shared__ float4 s_x[kFewWarps][32];
-    namespace cg = cooperative_groups;
-    cg::cluster_group cl = cg::this_cluster();
-    const int rank = blockIdx.x, splits = gridDim.x, h = blockIdx.y, b = blockIdx.z;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    int bad = 0;
-    const Request rq = request_of(a, b, bad);
-    const int rows = rq.n * a.r;
-    if (rows == 0 || rows > kFewRows) {  // (the same for the whole cluster)
-        if (bad && tid == 0) atomicOr(a.err, bad);
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
-    }
-    const int32_t* ids = a.table + (size_t)b * a.width;
-    const int groups = (rq.len + 15) >> 4, stride = splits * kFewWarps;
-
-    uint32_t qf[NT][8][2];
-    int lim[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int row = 8 * nt + g;
-        const bool in = row < rows;
-        const uint16_t* src = a.q + ((size_t)(rq.first + (in ? row / a.r : 0)) * a.Hq + h * a.r + (in ? row % a.r : 0)) * 128 + 8 * t;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint4 x = in ? *reinterpret_cast<const uint4*>(src + 32 * j) : make_uint4(0, 0, 0, 0);
-            qf[nt][2 * j][0] = x.x;
-            qf[nt][2 * j][1] = x.y;
-            qf[nt][2 * j + 1][0] = x.z;
-            qf[nt][2 * j + 1][1] = x.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int rr = 8 * nt + 2 * t + e;
-            lim[nt][e] = rr < rows ? min(rq.len, rq.len - rq.n + rr / a.r + 1) : 0;
-        }
-    }
-    float o[NT][8][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-    }
-    // offset of key 16 s in the pool, or -1 (no page there)
-    auto place = [&](int s) -> long long {
-        if (s >= groups) return -1;
-        const int id = ids[(16 * s) >> a.page_shift];
-        if (id < 0 || id >= a.n_pages) {
-            bad |= HSQ_DEVERR_PAGE;
-            return -1;
-        }
-        return ((((long long)id * a.Hkv + h) << a.page_shift) + ((16 * s) & (a.page_n - 1))) * 128;
-    };
-    uint4 kf[2][4];
-    // keys past the length (and of no page) read as zero, so that nothing stale enters a product
-    auto load_k = [&](int s, long long at) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const bool in = at >= 0 && 16 * s + g + 8 * e < rq.len;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                kf[e][j] = in ? __ldcs(reinterpret_cast<const uint4*>(a.pk + at + (g + 8 * e) * 128 + 32 * j + 8 * t))
-                              : make_uint4(0, 0, 0, 0);
-        }
-    };
-    int s = rank * kFewWarps + warp;
-    long long at = place(s);
-    if (s < groups) load_k(s, at);
-#pragma unroll 1
-    for (; s < groups; s += stride) {
-        const long long ahead = place(s + stride);
-        uint4 vf[4][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int key = 2 * t + (e & 1) + 8 * (e >> 1);
-            const bool in = at >= 0 && 16 * s + key < rq.len;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                vf[e][c] = in ? __ldcs(reinterpret_cast<const uint4*>(a.pv + at + key * 128 + 64 * c + 8 * g))
-                              : make_uint4(0, 0, 0, 0);
-        }
-        float x[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(x[nt], kf[0][j].x, kf[1][j].x, kf[0][j].y, kf[1][j].y, qf[nt][2 * j][0], qf[nt][2 * j][1]);
-                mma_16816(x[nt], kf[0][j].z, kf[1][j].z, kf[0][j].w, kf[1][j].w, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
-            }
-        if (s + stride < groups) load_k(s + stride, ahead);
-        bool raise = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // key g + 8 (e >> 1), row 2 t + (e & 1)
-                if (at < 0 || 16 * s + g + 8 * (e >> 1) >= lim[nt][e & 1]) x[nt][e] = -INFINITY;
-                raise |= x[nt][e] * kLogitScaleLog2 > m[nt][e & 1] * kLogitScaleLog2 + kRaise;
-            }
-        if (__any_sync(kFull, raise)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(m[nt][e], fmaxf(x[nt][e], x[nt][e + 2]));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
-                    const float alpha = mx == -INFINITY ? 1.f : ex2_approx((m[nt][e] - mx) * kLogitScaleLog2);
-                    m[nt][e] = mx;
-                    l[nt][e] *= alpha;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        o[nt][i][e] *= alpha;
-                        o[nt][i][e + 2] *= alpha;
-                    }
-                }
-        }
-        uint32_t pf[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float off = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1] * kLogitScaleLog2;
-                p[e] = ex2_approx(fmaf(x[nt][e], kLogitScaleLog2, -off));
-                l[nt][e & 1] += p[e];
-            }
-            pf[nt][0] = transpose_8x8(pack_bf16(p[0], p[1]));
-            pf[nt][1] = transpose_8x8(pack_bf16(p[2], p[3]));
-        }
-        const uint32_t* v[4][2];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) v[e][c] = reinterpret_cast<const uint32_t*>(&vf[e][c]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
-            const uint32_t a0 = __byte_perm(v[0][0][i >> 1], v[1][0][i >> 1], sel);
-            const uint32_t a1 = __byte_perm(v[0][1][i >> 1], v[1][1][i >> 1], sel);
-            const uint32_t a2 = __byte_perm(v[2][0][i >> 1], v[3][0][i >> 1], sel);
-            const uint32_t a3 = __byte_perm(v[2][1][i >> 1], v[3][1][i >> 1], sel);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-        }
-        at = ahead;
-    }
-
-    // ---- join: the CTA's warps, the cluster's CTAs, the prefix's parts ----
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], d);
-            const int row = 8 * nt + 2 * t + e;
-            if (g == 0) s_ml[warp][row] = make_float2(m[nt][e], l[nt][e]);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float4* dst = reinterpret_cast<float4*>(&s_o[warp][row][64 * c + 8 * g]);
-                dst[0] = make_float4(o[nt][0][e + 2 * c], o[nt][1][e + 2 * c], o[nt][2][e + 2 * c], o[nt][3][e + 2 * c]);
-                dst[1] = make_float4(o[nt][4][e + 2 * c], o[nt][5][e + 2 * c], o[nt][6][e + 2 * c], o[nt][7][e + 2 * c]);
-            }
-        }
-    }
-    if (bad) atomicOr(a.err, bad);
-    __syncthreads();
-    for (int row = 0; row < rows; ++row) {  // thread = dim
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, s_ml[w][row].x);
-        float L = 0.f, x = 0.f;
-#pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
-            const float2 ml = s_ml[w][row];
-            if (ml.y > 0.f) {
-                const float c = ex2_approx((ml.x - M) * kLogitScaleLog2);
-                L = fmaf(ml.y, c, L);
-                x = fmaf(s_o[w][row][tid], c, x);
-            }
-        }
-        s_o[0][row][tid] = x;  // (this thread alone reads and writes the column)
-        if (tid == 0) s_cta[row] = make_float2(M, L);
-    }
-    if (splits > 1) cl.sync(); else __syncthreads();
+__global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __grid_constant__ SharedArgs a, int short_ctas) {
+    __shared__ int s_short[HSQ_MAX_REQUESTS];
+    __shared__ __align__(16) uint16_t s_out[32][136];
+    __shared__ long long s_to[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d0 = warp * kJoinDims;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // This CTA's rows (every splits-th), one warp a row, or two or four warps where there are
-    // that few rows: lane k holds the weights of parts k, k + 32, ..., then the warp adds
-    // the parts up, a lane four dims.  Loads do not wait for one another but for that one step.
-    const PrefixPlan plan = prefix_plan(a);
-    const int mine = (rows - rank + splits - 1) / splits;                  // (rows > rank, or none)
-    const int per = mine == 1 ? kFewWarps : mine == 2 ? kFewWarps / 2 : 1;  // warps a row
-    for (int i0 = 0; i0 < mine; i0 += kFewWarps / per) {
-        const int i = i0 + warp / per, sub = warp % per;
-        const bool live = i < mine;
-        const int row = rank + (live ? i : 0) * splits, token = rq.first + row / a.r, jj = row % a.r;
-        RowParts rp{0, 0, 0};
-        if (live && plan.work > 0) rp = row_parts(a, plan, h, token, jj);
-        // parts: the cluster's CTAs 0 .. splits - 1, then the prefix's
-        const int n = live ? splits + rp.n : 0;
-        float M = -INFINITY;
-        for (int k = lane; k < n; k += 32)
-            M = fmaxf(M, k < splits ? cl.map_shared_rank(s_cta, k)[row].x : __ldcg(&a.part_ml[rp.at + (k - splits) * rp.step]).x);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, d));
-        float L = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < n; k0 += 32) {
-            float wt = 0.f;  // weight of part k0 + lane
-            if (k0 + lane < n) {
-                const int k = k0 + lane;
-                const float2 ml = k < splits ? cl.map_shared_rank(s_cta, k)[row] : __ldcg(&a.part_ml[rp.at + (k - splits) * rp.step]);
-                if (ml.y > 0.f) {
-                    wt = ex2_approx((ml.x - M) * kLogitScaleLog2);
-                    L = fmaf(ml.y, wt, L);
-                }
-            }
-            const int stop = min(32, n - k0);
-#pragma unroll 8
-            for (int e = sub; e < stop; e += per) {
-                const float wk = __shfl_sync(kFull, wt, e);
-                const int k = k0 + e;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (wk > 0.f)
-                    v = k < splits ? *reinterpret_cast<const float4*>(cl.map_shared_rank(&s_o[0][row][4 * lane], k))
-                                   : __ldcg(reinterpret_cast<const float4*>(a.part_o + (rp.at + (k - splits) * rp.step) * 128) + lane);
-                x.x = fmaf(v.x, wk, x.x);
-                x.y = fmaf(v.y, wk, x.y);
-                x.z = fmaf(v.z, wk, x.z);
-                x.w = fmaf(v.w, wk, x.w);
-            }
+    const PlanHead p = *a.head;
+    struct Parts { const float* o; const float2* ml; long long step; int n, pitch; };  // n parts, `step` part rows apart
+    Parts list[2] = {{nullptr, nullptr, 0, 0, 1}, {nullptr, nullptr, 0, 0, 1}};
+    bool live;
+    int h, token = 0, jj = 0;
+    if ((int)blockIdx.x < short_ctas) {
+        h = blockIdx.x % a.Hkv;
+        const int grp = blockIdx.x / a.Hkv, tile = grp >> 2, row = (grp & 3) * 32 + lane;
+        const int rows = min(a.tpt, p.tokens - tile * a.tpt) * a.r;
+        if ((grp & 3) * 32 >= rows) return;
+        for (int i = tid; i < a.B; i += 32 * kJoinWarps) s_short[i] = a.req[i].w;
+        __syncthreads();
+        live = row < rows;
+        const int at = tile * a.tpt + (live ? row : 0) / a.r;
+        jj = (live ? row : 0) % a.r;
+        int lo = 0, hi = a.B;  // the request: the last that begins at or before the token
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_short[mid] <= at) lo = mid; else hi = mid;
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(kFull, L, d);
-        if (per > 1) {
-            s_x[warp][lane] = x;
-            __syncthreads();
-            for (int w = 1; w < per; ++w) {
-                const float4 v = s_x[warp - sub + (sub + w) % per][lane];
-                x.x += v.x;
-                x.y += v.y;
-                x.z += v.z;
-                x.w += v.w;
-            }
+        const int4 q = a.req[lo];
+        token = q.x + at - q.w;
+        if (p.work_a > 0) {
+            const int pair = tile >> 1, stream = tile & 1;
+            const bool split = tile == p.tiles - 1 && !stream;  // (a pair of one tile has its key tiles dealt to both streams)
+            const long long keys = (long long)a.prefix_tiles * kTileKeys;
+            const int rate = (split ? kCostOne : kCostPair) * kTileKeys;
+            const long long w0 = h * p.head_a + pair * keys * kCostPair;
+            const int c0 = run_of(p, w0), c1 = run_of(p, w0 + (long long)(a.prefix_tiles - 1) * rate);
+            const size_t slot = ((size_t)h * p.pairs + pair + c0) * 2 + stream;
+            list[0] = {a.a_o + slot * 128 * kTileRows + row, a.a_ml + slot * kTileRows + row, split ? 1 : 2,
+                       (c1 - c0 + 1) * (split ? 2 : 1), kTileRows};
         }
-        if (live && sub == 0) {
-            const size_t to = (size_t)token * a.Hq + h * a.r + jj;
-            const float inv = L > 0.f ? 1.0f / L : 0.f;
-            *reinterpret_cast<uint2*>(a.out + to * 128 + 4 * lane) =
-                make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-            if (a.lse && lane == 0) a.lse[to] = L > 0.f ? M * kRsqrtD + logf(L) : -INFINITY;
+        if (q.z > 0) {
+            const long long cost = (long long)(q.z + kItemKeys) * kCostOwn;
+            const long long w0 = p.work_a + p.work_c + a.b_at[lo] + h * cost;
+            const int tiles = (q.z + kTileKeys - 1) / kTileKeys;
+            const int c0 = run_of(p, w0), c1 = run_of(p, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
+            const size_t slot = ((size_t)lo * a.Hkv + h + c0) * 2;
+            const int orow = (at - q.w) * a.r + jj;
+            list[1] = {a.b_o + slot * 128 * a.own_rows + orow, a.b_ml + slot * a.own_rows + orow, 1, 2 * (c1 - c0 + 1), a.own_rows};
+        }
+    } else {
+        const int e = blockIdx.x - short_ctas, c = 1 + (e >> 3), st = (e >> 2) & 1, row = (e & 3) * 32 + lane;
+        const CutRecord cut = *reinterpret_cast<const CutRecord*>(a.cut + 16 * c);
+        const int rows = (st ? cut.toks1 : cut.toks0) * a.r;
+        if (!cut.valid || (e & 3) * 32 >= rows) return;
+        live = row < rows;
+        h = cut.h;
+        token = (st ? cut.tok1 : cut.tok0) + (live ? row : 0) / a.r;
+        jj = (live ? row : 0) % a.r;
+        // slot 2 c0 + 1, then 2 c0 + 2, 2 c0 + 4, ...
+        const size_t s0 = (2 * (size_t)cut.c0 + 1) * 2 + st, s1 = (2 * (size_t)cut.c0 + 2) * 2 + st;
+        list[0] = {a.c_o + s0 * 128 * kTileRows + row, a.c_ml + s0 * kTileRows + row, 1, 1, kTileRows};
+        list[1] = {a.c_o + s1 * 128 * kTileRows + row, a.c_ml + s1 * kTileRows + row, 4, cut.c1 - cut.c0, kTileRows};
+    }
+    if (!live) list[0].n = list[1].n = 0;
+    float M = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll 4
+        for (int k = 0; k < list[e].n; ++k) M = fmaxf(M, __ldcg(list[e].ml + k * list[e].step * list[e].pitch).x);
+    }
+    float L = 0.f, x[kJoinDims];
+#pragma unroll
+    for (int d = 0; d < kJoinDims; ++d) x[d] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const Parts& q = list[e];
+#pragma unroll 4
+        for (int k = 0; k < q.n; ++k) {
+            const float2 ml = __ldcg(q.ml + k * q.step * q.pitch);
+            const float* o = q.o + (k * q.step * 128 + d0) * q.pitch;
+            float v[kJoinDims];
+#pragma unroll
+            for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + (size_t)d * q.pitch);
+            if (ml.y > 0.f) {  // (a part without a key has no o)
+                const float w = ex2_approx((ml.x - M) * kLogitScaleLog2);
+                L = fmaf(ml.y, w, L);
+#pragma unroll
+                for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(v[d], w, x[d]);
+            }
         }
     }
-    if (splits > 1) cl.sync();  // (the others may still read this CTA's part)
+    const float inv = L > 0.f ? 1.0f / L : 0.f;
+    uint32_t y[kJoinDims / 2];
+#pragma unroll
+    for (int d = 0; d < kJoinDims; d += 2) y[d / 2] = pack_bf16(x[d] * inv, x[d + 1] * inv);
+    *reinterpret_cast<uint4*>(&s_out[lane][d0]) = make_uint4(y[0], y[1], y[2], y[3]);
+    const long long to = (long long)token * a.Hq + h * a.r + jj;
+    if (warp == 0) {
+        s_to[lane] = live ? to : -1;
+        if (live && a.lse) a.lse[to] = L > 0.f ? M * kRsqrtD + logf(L) : -INFINITY;
+    }
+    __syncthreads();
+    const int orow = tid >> 4, c = tid & 15;  // 32 rows x 16 chunks of 16 bytes
+    if (s_to[orow] >= 0)
+        *reinterpret_cast<uint4*>(a.out + s_to[orow] * 128 + 8 * c) = *reinterpret_cast<const uint4*>(&s_out[orow][8 * c]);
 }
 
 // ---- host side --------------------------------------------------------------------------
@@ -1103,44 +1077,49 @@ bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint3
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// workspace: part_o, then part_ml, of Hkv * pairs + runs slots
-struct Parts { long long slots; size_t o_bytes, bytes; int runs; };
+// The workspace's pieces and their offsets.
+struct Layout { size_t head, req, c_at, b_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, bytes; int runs, own_rows; };
 
-Parts parts_of(const hsq_ctx* ctx, int rows, int prefix_len) {
-    Parts p{0, 0, 256, 0};
-    if (prefix_len == 0) return p;
-    const int tpt = kTileRows / ctx->r, tiles = (rows + tpt - 1) / tpt, pairs = (tiles + 1) / 2;
-    const long long items = (long long)ctx->cfg.n_kv_heads * pairs;
-    const long long work = items * ((prefix_len + kTileKeys - 1) / kTileKeys);
-    p.runs = (int)std::min<long long>(ctx->num_sms, work);
-    p.slots = items + p.runs;
-    p.o_bytes = (size_t)p.slots * 2 * kTileRows * 128 * 4;
-    p.bytes = p.o_bytes + (size_t)p.slots * 2 * kTileRows * 8;
-    return p;
+Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new) {
+    Layout x{};
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255) / 256 * 256;
+        return here;
+    };
+    const size_t Hkv = ctx->cfg.n_kv_heads, r = ctx->r, tpt = kTileRows / r;
+    x.runs = ctx->num_sms;
+    x.own_rows = (int)((std::min<size_t>(max_new, tpt) * r + 3) / 4 * 4);
+    x.head = take(sizeof(PlanHead));
+    x.req = take((size_t)B * 16);
+    x.c_at = take((size_t)(B + 1) * 8);
+    x.b_at = take((size_t)(B + 1) * 8);
+    x.cut = take((size_t)x.runs * 64);
+    const size_t tokens = std::min<size_t>(rows, (size_t)B * tpt), tiles = (tokens + tpt - 1) / tpt;
+    const size_t a = prefix_len > 0 ? Hkv * ((tiles + 1) / 2) + x.runs : 0, b = (size_t)B * Hkv + x.runs;
+    const size_t c = (size_t)max_new > tpt ? 2 * (size_t)x.runs : 0;
+    x.a_o = take(a * 2 * 128 * kTileRows * 4);
+    x.a_ml = take(a * 2 * kTileRows * 8);
+    x.b_o = take(b * 2 * 128 * x.own_rows * 4);
+    x.b_ml = take(b * 2 * x.own_rows * 8);
+    x.c_o = take(c * 2 * 128 * kTileRows * 4);
+    x.c_ml = take(c * 2 * kTileRows * 8);
+    x.bytes = at;
+    return x;
 }
 
-cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster, bool after,
-                   void** args) {
+cudaError_t launch(const void* fn, int grid, int threads, size_t smem, cudaStream_t st, bool after, void** args) {
     cudaLaunchConfig_t lc{};
-    lc.gridDim = grid;
+    lc.gridDim = dim3(grid);
     lc.blockDim = dim3(threads);
     lc.dynamicSmemBytes = smem;
     lc.stream = st;
-    cudaLaunchAttribute at[2];
-    int n = 0;
-    if (cluster > 1) {
-        at[n].id = cudaLaunchAttributeClusterDimension;
-        at[n].val.clusterDim.x = cluster;
-        at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (after) {
-        at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
-    lc.numAttrs = n;
+    lc.numAttrs = after ? 1 : 0;
     return cudaLaunchKernelExC(&lc, fn, args);
 }
 
@@ -1151,9 +1130,9 @@ extern "C" {
 hsq_status hsq_shared_attn_workspace_size(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new,
                                           size_t* bytes) {
     if (!ctx || !bytes) return hsq::fail(nullptr, HSQ_ERR_INVALID, "ctx or bytes is NULL");
-    if (rows < 1 || B < 1 || prefix_len < 0 || max_new < 1)
-        return hsq::fail(nullptr, HSQ_ERR_INVALID, "rows, B and max_new must be positive, prefix_len not negative");
-    *bytes = parts_of(ctx, rows, prefix_len).bytes;
+    if (rows < 1 || B < 1 || B > HSQ_MAX_REQUESTS || prefix_len < 0 || max_new < 1)
+        return hsq::fail(nullptr, HSQ_ERR_INVALID, "rows, B (up to HSQ_MAX_REQUESTS) and max_new must be positive, prefix_len not negative");
+    *bytes = layout_of(ctx, rows, B, prefix_len, max_new).bytes;
     return HSQ_OK;
 }
 
@@ -1167,70 +1146,60 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
         return hsq::fail(ctx, HSQ_ERR_INVALID, "an argument of hsq_shared_attn is NULL");
     if (B < 1 || B > ctx->cfg.max_batch || B > HSQ_MAX_REQUESTS)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "B outside [1, min(max_batch, HSQ_MAX_REQUESTS)]");
-    if (rows < 1 || width < 1 || max_new < 1 || prefix_len < 0)
-        return hsq::fail(ctx, HSQ_ERR_INVALID, "rows, width and max_new must be positive, prefix_len not negative");
+    if (rows < 1 || width < 1 || max_new < 1 || prefix_len < 0 || prefix_len > (1 << 30))
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "rows, width and max_new must be positive, prefix_len in [0, 2^30]");
+    if ((long long)width * pages->page_n > (1 << 30)) return hsq::fail(ctx, HSQ_ERR_INVALID, "width * page_n above 2^30");
     if (prefix_len > 0 && !prefix) return hsq::fail(ctx, HSQ_ERR_INVALID, "prefix is NULL with prefix_len > 0");
     if (((uintptr_t)q | (uintptr_t)out) & 15u)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "q and out must be 16-byte aligned");
     if ((uintptr_t)workspace & 255u) return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace must be 256-byte aligned");
-    const Parts parts = parts_of(ctx, rows, prefix_len);
-    if (workspace_bytes < parts.bytes)
+    const Layout x = layout_of(ctx, rows, B, prefix_len, max_new);
+    if (workspace_bytes < x.bytes)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace smaller than hsq_shared_attn_workspace_size");
     if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
     const int r = ctx->r, Hkv = ctx->cfg.n_kv_heads, tpt = kTileRows / r;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     SharedArgs a{};
     a.q = static_cast<const uint16_t*>(q);
-    a.pk = static_cast<const uint16_t*>(pages->k);
-    a.pv = static_cast<const uint16_t*>(pages->v);
     a.q_start = q_start; a.lens = lens; a.table = table; a.prefix = prefix;
     a.out = static_cast<uint16_t*>(out);
     a.lse = lse_opt;
     a.rows = rows; a.B = B; a.width = width; a.prefix_len = prefix_len; a.max_new = max_new;
+    a.prefix_tiles = (prefix_len + kTileKeys - 1) / kTileKeys;
     a.n_pages = pages->n_pages; a.page_n = pages->page_n;
     a.page_shift = pages->page_n == 16 ? 4 : pages->page_n == 32 ? 5 : pages->page_n == 64 ? 6 : 7;
-    a.Hq = ctx->cfg.n_q_heads; a.Hkv = Hkv; a.r = r; a.tpt = tpt; a.runs = parts.runs;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + parts.o_bytes);
+    a.Hq = ctx->cfg.n_q_heads; a.Hkv = Hkv; a.r = r; a.tpt = tpt; a.runs = x.runs; a.own_rows = x.own_rows;
+    a.head = reinterpret_cast<PlanHead*>(ws + x.head);
+    a.req = reinterpret_cast<int4*>(ws + x.req);
+    a.c_at = reinterpret_cast<long long*>(ws + x.c_at);
+    a.b_at = reinterpret_cast<long long*>(ws + x.b_at);
+    a.cut = reinterpret_cast<int*>(ws + x.cut);
+    a.a_o = reinterpret_cast<float*>(ws + x.a_o); a.a_ml = reinterpret_cast<float2*>(ws + x.a_ml);
+    a.b_o = reinterpret_cast<float*>(ws + x.b_o); a.b_ml = reinterpret_cast<float2*>(ws + x.b_ml);
+    a.c_o = reinterpret_cast<float*>(ws + x.c_o); a.c_ml = reinterpret_cast<float2*>(ws + x.c_ml);
     a.err = ctx->d_err;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool many = (long long)max_new * r > kFewRows;
     CUtensorMap mq, mk, mv;
-    if (prefix_len > 0 || many) {
-        if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-        const uint64_t n = (uint64_t)pages->n_pages * Hkv * pages->page_n;
-        if (!encode_q(&mq, q, rows, a.Hq, r, tpt) || !encode_rows(&mk, pages->k, n, pages->page_n) ||
-            !encode_rows(&mv, pages->v, n, pages->page_n))
-            return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
-    }
-    cudaError_t e = cudaSuccess;
-    bool after = false;
+    if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const uint64_t n = (uint64_t)pages->n_pages * Hkv * pages->page_n;
+    if (!encode_q(&mq, q, rows, a.Hq, r, tpt) || !encode_rows(&mk, pages->k, n, pages->page_n) ||
+        !encode_rows(&mv, pages->v, n, pages->page_n))
+        return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int tiles = (int)((std::min<long long>(rows, (long long)B * tpt) + tpt - 1) / tpt);
+    int short_ctas = 4 * tiles * Hkv;
+    const int cut_ctas = max_new > tpt ? 8 * (x.runs - 1) : 0;
+    void* plan_args[] = {&a};
     void* tc_args[] = {&mq, &mk, &mv, &a};
-    void* few_args[] = {&a};
-    if (prefix_len > 0) {
-        const void* fn = (const void*)shared_tc_kernel<false>;
-        if ((e = hsq::raise_smem_limit(fn, ctx->device, kTcSmem)) != cudaSuccess)
-            return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(shared_attn)");
-        e = launch(fn, dim3(parts.runs), kTcThreads, kTcSmem, s, 1, false, tc_args);
-        if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn prefix");
-        after = true;
-    }
-    if (many) {
-        const void* fn = (const void*)shared_tc_kernel<true>;
-        if ((e = hsq::raise_smem_limit(fn, ctx->device, kTcSmem)) != cudaSuccess)
-            return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(shared_attn)");
-        const int ids = rows / (2 * tpt) + B;
-        if (ids > 65535) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
-        e = launch(fn, dim3(Hkv, ids), kTcThreads, kTcSmem, s, 1, after, tc_args);
-        if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn rows");
-        after = true;
-    }
-    int splits = 1;
-    while (splits < 8 && (long long)B * Hkv * splits < 3 * ctx->num_sms &&
-           (long long)width * pages->page_n > 16LL * kFewWarps * 4 * splits)
-        splits *= 2;
-    const void* fn = many || max_new * r > 8 ? (const void*)shared_few_kernel<2> : (const void*)shared_few_kernel<1>;
-    e = launch(fn, dim3(splits, Hkv, B), kFewThreads, 0, s, splits, after, few_args);
-    if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn few");
+    void* join_args[] = {&a, &short_ctas};
+    const void* fn = (const void*)shared_tc_kernel;
+    cudaError_t e = hsq::raise_smem_limit(fn, ctx->device, kTcSmem);
+    if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(shared_attn)");
+    if ((e = launch((const void*)shared_plan_kernel, 1, kPlanThreads, 0, s, false, plan_args)) != cudaSuccess)
+        return hsq::cuda_fail(ctx, e, "shared_attn plan");
+    if ((e = launch(fn, x.runs, kTcThreads, kTcSmem, s, true, tc_args)) != cudaSuccess)
+        return hsq::cuda_fail(ctx, e, "shared_attn");
+    e = launch((const void*)shared_join_kernel, short_ctas + cut_ctas, 32 * kJoinWarps, 0, s, true, join_args);
+    if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn join");
     return HSQ_OK;
 }
 
