@@ -222,11 +222,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // either hold two row tiles and share every key tile (so keys and values are loaded once
 // for 256 rows), or (split) hold the same rows and take the key tiles in turn.  While
 // one stream's softmax runs, the tensor cores work for the other.
-//   shared memory: ring of five 32 KB tiles K0 V0 K1 V1 ... (TMA, 128-byte swizzle), two Q tiles;
+//   shared memory: a ring of three K tiles and one of two V tiles, 32 KB each (TMA, 128-byte swizzle; in
+//     one ring of five a key tile had to wait for the P V of three tiles before), two Q tiles;
 //   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kTcThreads = 384, kStages = 5, kQueue = 4;
+constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kStages = kKeyStages + kValueStages, kQueue = 4;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = kStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
 // barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | seg_full[4] | seg_empty[4]
@@ -246,11 +247,13 @@ struct alignas(16) Segment {
     int split;
     int ptiles;                    // the item's tiles that are the prefix's
     int olen, obase, first;        // own keys; token t sees min(olen, obase + t - first) of them
-    int b, slot, pad[3];
+    int b, slot;
+    int flip;                      // split: the stream of the first tile
+    int pad[2];
 };
 
 __device__ __forceinline__ int tiles_of(const Segment& s, int st) {
-    return s.split ? (s.n1 - s.n0 + 1 - st) >> 1 : (st ? s.end1 : s.end0) - s.n0;
+    return s.split ? (s.n1 - s.n0 + 1 - (st ^ s.flip)) >> 1 : (st ? s.end1 : s.end0) - s.n0;
 }
 // keys of tile n that are loaded
 __device__ __forceinline__ int keys_of(const SharedArgs& a, const Segment& s, int n) {
@@ -260,17 +263,19 @@ __device__ __forceinline__ int keys_of(const SharedArgs& a, const Segment& s, in
 // What the join has to know of a C item that run c is the second to work on.
 struct CutRecord { int valid, h, tok0, tok1, toks0, toks1, c0, c1; };
 
-// A place in the ring of stages, and the parity of its barriers' phase.
+// A place in a ring of N stages, and the parity of its barriers' phase.
+template <uint32_t N>
 struct Ring {
     uint32_t stage, phase;
-    __device__ __forceinline__ void advance(uint32_t by, uint32_t size = kStages) {
-        stage += by;
-        if (stage >= size) {
-            stage -= size;
+    __device__ __forceinline__ void advance() {
+        if (++stage == N) {
+            stage = 0;
             phase ^= 1;
         }
     }
 };
+using KeyRing = Ring<kKeyStages>;      // stages 0, 1, 2 of `full` and `empty`
+using ValueRing = Ring<kValueStages>;  // stages 3, 4
 
 // The last b with at[b] <= x (at ascending, at[0] = 0, n entries), by a whole warp: 32 probes a step.
 __device__ __forceinline__ int warp_find(const long long* at, int n, long long x) {
@@ -415,7 +420,7 @@ struct Walker {
             s.end0 = s.end1 = tiles = (len + kTileKeys - 1) / kTileKeys;
         }
         s.n0 = at <= w0 ? 0 : (int)((at - w0 + rate - 1) / rate);
-        s.n1 = (int)min((long long)tiles, (end - w0 + rate - 1) / rate);
+        s.n1 = w0 + (long long)tiles * rate <= end ? tiles : (int)min((long long)tiles, (end - w0 + rate - 1) / rate);
         if (tiles == 0) {  // (C only: rows that see nothing are written all the same, where the item begins)
             if (at > w0) return false;
             s.n0 = s.n1 = 0;
@@ -486,7 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Segment s;
 
     // the next segment of the queue, read by one thread or by a warp
-    auto receive = [&](Ring& q, bool release) {
+    auto receive = [&](Ring<kQueue>& q, bool release) {
         mbar_wait_fast(seg_full + 8 * q.stage, q.phase, failed);
         const int4* src = reinterpret_cast<const int4*>(gbase + kOffSeg + q.stage * kSegBytes);
         int4* dst = reinterpret_cast<int4*>(&s);
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         } else {
             mbar_arrive(seg_empty + 8 * q.stage);
         }
-        q.advance(1, kQueue);
+        q.advance();
         return s.kind != kEnd;
     };
 
@@ -512,13 +517,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (warp == 8) {
             // ---- the run's segments, and per key tile the K pages, then the V pages (lane i: page i of the tile) ----
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            Ring ring{0, 1}, queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
+            KeyRing kr{0, 1};
+            ValueRing vr{0, 1};
+            Ring<kQueue> queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
             uint32_t step = 0, tail_par = 0;
             const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
             const PlanHead plan = *a.head;
             Walker walk{a, plan};
             walk.start(blockIdx.x);
             CutRecord cut{0, 0, 0, 0, 0, 0, 0, 0};
+            int flip = 0;
             auto send = [&] {
                 mbar_wait_fast(seg_empty + 8 * queue.stage, queue.phase, failed);
                 failed = __any_sync(kFull, failed);
@@ -527,28 +535,55 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mbar_arrive(seg_full + 8 * queue.stage);
                 }
                 __syncwarp();
-                queue.advance(1, kQueue);
+                queue.advance();
             };
-            for (; walk.more && !failed; walk.step()) {
-                if (!walk.segment(s, cut, blockIdx.x)) continue;
-                send();
-                const int32_t* own = a.table + (size_t)s.b * a.width;
-#pragma unroll 1
-                for (int n = s.n0; n < s.n1 && !failed; ++n, ++step) {
-                    const bool pre = n < s.ptiles;
-                    const int nk = keys_of(a, s, n), np = (nk + a.page_n - 1) >> a.page_shift;
-                    int id = -1;
-                    if (lane < np)
-                        id = (pre ? a.prefix : own)[((pre ? n : n - s.ptiles) * kTileKeys >> a.page_shift) + lane];
-                    const bool in = lane < np && id >= 0 && id < a.n_pages;
+            // A key tile to load.  It is looked up (segment, page ids) while the one before it is issued: the ids' way
+            // from memory would otherwise stand before every tile's own.
+            struct Tile { int n, np, nk, id, h, first; };
+            bool fresh = true;  // the walker stands on an item not yet taken
+            int n_next = 0;
+            auto fetch = [&](Tile& u) {
+                u.first = 0;
+                if (fresh || n_next >= s.n1) {
+                    if (!fresh) walk.step();
+                    fresh = false;
+                    while (walk.more && !walk.segment(s, cut, blockIdx.x)) walk.step();
+                    if (!walk.more) return false;
+                    s.flip = s.split ? flip : 0;  // (items of one tile in turn on both streams)
+                    if (s.split) flip ^= (s.n1 - s.n0) & 1;
+                    n_next = s.n0;
+                    u.first = 1;
+                }
+                u.n = n_next++;
+                u.h = s.h;
+                u.np = 0;
+                if (u.n >= s.n1) return true;  // (an item without a tile)
+                const bool pre = u.n < s.ptiles;
+                u.nk = keys_of(a, s, u.n);
+                u.np = (u.nk + a.page_n - 1) >> a.page_shift;
+                u.id = -1;
+                if (lane < u.np)
+                    u.id = pre ? a.prefix[(u.n * kTileKeys >> a.page_shift) + lane]
+                               : a.table[(size_t)s.b * a.width + ((u.n - s.ptiles) * kTileKeys >> a.page_shift) + lane];
+                return true;
+            };
+            Tile now, then;
+            bool have = fetch(now);
+            while (have && !failed) {
+                if (now.first) send();
+                have = fetch(then);
+                const int np = now.np, nk = now.nk;
+                if (np > 0) {
+                    const bool in = lane < np && now.id >= 0 && now.id < a.n_pages;
                     const uint32_t mask = __ballot_sync(kFull, in);
                     if (mask != (1u << np) - 1u) bad |= HSQ_DEVERR_PAGE;
                     // (a page outside the pool is read past the map's extent: zeros, masked in the softmax)
-                    const int y = in ? (id * a.Hkv + s.h) << a.page_shift : (a.n_pages * a.Hkv) << a.page_shift;
+                    const int y = in ? (now.id * a.Hkv + now.h) << a.page_shift : (a.n_pages * a.Hkv) << a.page_shift;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t stage = base + ring.stage * kTileBytes, bar = full + 8 * ring.stage;
-                        mbar_wait_fast(empty + 8 * ring.stage, ring.phase, failed);
+                        const uint32_t slot = kv ? kKeyStages + vr.stage : kr.stage;
+                        const uint32_t stage = base + slot * kTileBytes, bar = full + 8 * slot;
+                        mbar_wait_fast(empty + 8 * slot, kv ? vr.phase : kr.phase, failed);
                         failed = __any_sync(kFull, failed);
                         // The values of a tile that does not end on a multiple of 16 keys: the rows up to there
                         // hold what the page holds; their weights are 0, so they have to be finite.  Cleared
@@ -577,21 +612,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar);
                         }
-                        ring.advance(1);
+                        if (kv) vr.advance(); else kr.advance();
                     }
+                    ++step;
                 }
+                now = then;
             }
             s.kind = kEnd;
             send();
             if (lane == 0) *reinterpret_cast<CutRecord*>(a.cut + 16 * blockIdx.x) = cut;
             if (failed)  // see the copies in flight land before the CTA ends
-                for (int i = 0; i < kStages; ++i) mbar_wait(full + 8 * i, i < (int)ring.stage ? ring.phase ^ 1 : ring.phase, 1 << 12);
+                for (int i = 0; i < kStages; ++i) {
+                    const bool lap = i < kKeyStages ? i < (int)kr.stage : i - kKeyStages < (int)vr.stage;
+                    mbar_wait(full + 8 * i, (i < kKeyStages ? kr.phase : vr.phase) ^ (lap ? 1u : 0u), 1 << 12);
+                }
         } else if (warp == 9 && elect_one()) {
             // ---- MMAs, one thread ----
             // Straight code: per pair of key tiles four waits, each one poll; the tensor pipe takes an MMA every 64
             // cycles and holds only one or two more, so what the thread does in between shows.
             constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128), idFull = idesc_bf16_f32(128, 128);
-            Ring kr{0, 0}, vr{1, 0}, queue{0, 0};
+            KeyRing kr{0, 0};
+            ValueRing vr{0, 0};
+            Ring<kQueue> queue{0, 0};
             uint32_t q_par = 0, p_par = 0;  // a bit for each stream
             auto scores = [&](int st, uint32_t idS) {  // S = Q K^T of the tile at kr
                 const uint32_t dS = tmem + 128 * st;
@@ -605,7 +647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             auto product = [&](int st, uint32_t begun) {  // O += P V of the whole tile at vr
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
-                const uint64_t dv = sw128_mn_desc(base + vr.stage * kTileBytes, kHalfBytes);
+                const uint64_t dv = sw128_mn_desc(base + (kKeyStages + vr.stage) * kTileBytes, kHalfBytes);
                 mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
                 p_par ^= 1u << st;
                 tc_fence_after();
@@ -615,7 +657,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             auto product_n = [&](int st, int ks16, uint32_t begun) {  // the same of a tile of ks16 groups of 16 keys
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
-                const uint64_t dv = sw128_mn_desc(base + vr.stage * kTileBytes, kHalfBytes);
+                const uint64_t dv = sw128_mn_desc(base + (kKeyStages + vr.stage) * kTileBytes, kHalfBytes);
                 mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
                 p_par ^= 1u << st;
                 tc_fence_after();
@@ -623,88 +665,106 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int k = 0; k < ks16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
             };
             auto k_wait = [&] { mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed); };
-            auto v_wait = [&] { mbar_wait_fast(full + 8 * vr.stage, vr.phase, failed); };
-            auto k_done = [&] { mma_commit(empty + 8 * kr.stage); kr.advance(2); };
-            auto v_done = [&] { mma_commit(empty + 8 * vr.stage); vr.advance(2); };
+            auto v_wait = [&] { mbar_wait_fast(full + 8 * (kKeyStages + vr.stage), vr.phase, failed); };
+            auto k_done = [&] { mma_commit(empty + 8 * kr.stage); kr.advance(); };
+            auto v_done = [&] { mma_commit(empty + 8 * (kKeyStages + vr.stage)); vr.advance(); };
             auto groups = [&](int n) { return (keys_of(a, s, n) + 15) >> 4; };
+            // split segments: the product of a stream's tile waits here until the stream's next S, so that the
+            // streams go on from one item to the next without a gap (bit 0: there is one, 1: of the segment's first tile
+            // of the stream, 2: of its last, from 8 on: its groups of 16 keys)
+            uint32_t due0 = 0, due1 = 0;
+            auto settle = [&](int st) {
+                const uint32_t due = st ? due1 : due0;
+                if (!(due & 1)) return;
+                v_wait();
+                if ((due >> 8) == 8) product(st, !(due & 2));
+                else product_n(st, due >> 8, !(due & 2));
+                v_done();
+                if (due & 4) mma_commit(o_full + 8 * st);
+                if (st) due1 = 0; else due0 = 0;
+            };
+            int turn = 0;  // the stream of the next tile of a split segment: the one whose product is older
             while (receive(queue, false)) {
+                const int n0 = s.n0, n1 = s.n1, end0 = s.end0;
+                if (s.split) {
+#pragma unroll 1
+                    for (int n = n0; n < n1; ++n) {
+                        const int st = (n - n0 + s.flip) & 1;
+                        turn = st ^ 1;
+                        settle(st);
+                        if (n - n0 < 2) {
+                            mbar_wait_fast(q_full + 8 * st, (q_par >> st) & 1, failed);
+                            q_par ^= 1u << st;
+                        }
+                        const int g = groups(n);
+                        k_wait();
+                        scores(st, idesc_bf16_f32(128, 16 * g));
+                        k_done();
+                        if (n + 2 >= n1) mma_commit(q_empty + 8 * st);  // (the stream's last S of the segment)
+                        const uint32_t due = 1u | (n - n0 < 2 ? 2u : 0u) | (n + 2 >= n1 ? 4u : 0u) | ((uint32_t)g << 8);
+                        if (st) due1 = due; else due0 = due;
+                    }
+                    continue;
+                }
+                settle(turn);
+                settle(turn ^ 1);
                 const bool has0 = tiles_of(s, 0) > 0, has1 = tiles_of(s, 1) > 0;
                 if (has0) { mbar_wait_fast(q_full, q_par & 1, failed); q_par ^= 1; }
                 if (has1) { mbar_wait_fast(q_full + 8, (q_par >> 1) & 1, failed); q_par ^= 2; }
-                const int n0 = s.n0, n1 = s.n1, end0 = s.end0;
-                if (!s.split) {
-                    if (n1 > n0) {
-                        // the tiles that are not whole: the prefix's last and the item's last
-                        const int r1 = (a.prefix_len & 127) ? s.ptiles - 1 : -2, both = min(end0, n1 - 1);
-                        k_wait();
-                        if (n0 < end0) scores(0, idesc_bf16_f32(128, 16 * groups(n0)));
-                        scores(1, idesc_bf16_f32(128, 16 * groups(n0)));
-                        k_done();
-                        int n = n0 + 1;
-                        while (n < n1) {
-                            const int to = r1 >= n ? min(both, r1) : both;
-                            if (n - 1 != r1) {
+                if (n1 > n0) {
+                    // the tiles that are not whole: the prefix's last and the item's last
+                    const int r1 = (a.prefix_len & 127) ? s.ptiles - 1 : -2, both = min(end0, n1 - 1);
+                    k_wait();
+                    if (n0 < end0) scores(0, idesc_bf16_f32(128, 16 * groups(n0)));
+                    scores(1, idesc_bf16_f32(128, 16 * groups(n0)));
+                    k_done();
+                    int n = n0 + 1;
+                    while (n < n1) {
+                        const int to = r1 >= n ? min(both, r1) : both;
+                        if (n - 1 != r1) {
 #pragma unroll 1
-                                for (; n < to; ++n) {  // P V of tile n - 1 and S of tile n, both whole
-                                    k_wait();
-                                    v_wait();
-                                    product(0, n > n0 + 1);
-                                    scores(0, idFull);
-                                    product(1, n > n0 + 1);
-                                    v_done();
-                                    scores(1, idFull);
-                                    k_done();
-                                }
-                            }
-                            if (n < n1) {  // stream 0 at its end, or a tile that is not whole
-                                const uint32_t idS = idesc_bf16_f32(128, 16 * groups(n));
-                                const int gp = groups(n - 1);
+                            for (; n < to; ++n) {  // P V of tile n - 1 and S of tile n, both whole
                                 k_wait();
                                 v_wait();
-                                if (n <= end0) product_n(0, gp, n > n0 + 1);
-                                if (n < end0) scores(0, idS);
-                                product_n(1, gp, n > n0 + 1);
+                                product(0, n > n0 + 1);
+                                scores(0, idFull);
+                                product(1, n > n0 + 1);
                                 v_done();
-                                scores(1, idS);
+                                scores(1, idFull);
                                 k_done();
-                                ++n;
                             }
                         }
-                        if (has0) mma_commit(q_empty);
-                        mma_commit(q_empty + 8);
-                        const int gp = groups(n1 - 1);
-                        v_wait();
-                        if (end0 == n1) product_n(0, gp, n1 - 1 > n0);
-                        if (has0) mma_commit(o_full);
-                        product_n(1, gp, n1 - 1 > n0);
-                        mma_commit(o_full + 8);
-                        v_done();
-                    }
-                } else {
-#pragma unroll 1
-                    for (int n = n0; n < n1 + 2; ++n) {
-                        const int st = (n - n0) & 1, np = n - 2;
-                        if (np >= n0) {
-                            v_wait();
-                            const int gp = groups(np);
-                            if (gp == 8) product(st, np > n0 + 1);
-                            else product_n(st, gp, np > n0 + 1);
-                            v_done();
-                            if (n >= n1) mma_commit(o_full + 8 * st);
-                        }
-                        if (n < n1) {
+                        if (n < n1) {  // stream 0 at its end, or a tile that is not whole
+                            const uint32_t idS = idesc_bf16_f32(128, 16 * groups(n));
+                            const int gp = groups(n - 1);
                             k_wait();
-                            scores(st, idesc_bf16_f32(128, 16 * groups(n)));
+                            v_wait();
+                            if (n <= end0) product_n(0, gp, n > n0 + 1);
+                            if (n < end0) scores(0, idS);
+                            product_n(1, gp, n > n0 + 1);
+                            v_done();
+                            scores(1, idS);
                             k_done();
-                            if (n + 2 >= n1) mma_commit(q_empty + 8 * st);  // (the stream's last S of the segment)
+                            ++n;
                         }
                     }
+                    if (has0) mma_commit(q_empty);
+                    mma_commit(q_empty + 8);
+                    const int gp = groups(n1 - 1);
+                    v_wait();
+                    if (end0 == n1) product_n(0, gp, n1 - 1 > n0);
+                    if (has0) mma_commit(o_full);
+                    product_n(1, gp, n1 - 1 > n0);
+                    mma_commit(o_full + 8);
+                    v_done();
                 }
             }
+            settle(turn);
+            settle(turn ^ 1);
         } else if (warp == 10) {
             // ---- queries of the segments' streams ----
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            Ring queue{0, 0};
+            Ring<kQueue> queue{0, 0};
             uint32_t q_par = 3;  // (the buffers start empty)
             const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
             const PlanHead plan = *a.head;
@@ -768,7 +828,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + 128 * st, tO = tmem + lanes + 256 + 128 * st;
         uint32_t s_par = 0, o_par = 0;
-        Ring queue{0, 0};
+        Ring<kQueue> queue{0, 0};
         int step0 = 0;
         const int row_token = row / a.r;
         while (receive(queue, true)) {
@@ -779,7 +839,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int own_lim = min(s.olen, s.obase + tok - s.first + row_token); // and this row
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int n = s.n0 + (s.split ? st : 0); n < stop; n += s.split ? 2 : 1) {
+            for (int n = s.n0 + (s.split ? st ^ s.flip : 0); n < stop; n += s.split ? 2 : 1) {
                 mbar_wait_fast(s_full + 8 * st, s_par, failed);
                 s_par ^= 1;
                 if (!idle) {
@@ -929,29 +989,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---------------------------------------------------------------------------------------
 // Join.  A CTA takes 32 rows: of a tile of the short requests' tokens (parts of A and B), or of a row tile of a
-// C item that a cut divides.  Lane = row, a warp eight dims: parts are read in whole lines, weights
-// are the lane's own, and the parts' loads do not wait for one another.
+// C item that a cut divides.  Lane = row; four groups of warps deal the parts among them, a warp of a group
+// takes 32 dims: parts are read in whole lines, 32 loads at a time, weights are the lane's own.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kJoinWarps = 16, kJoinDims = 128 / kJoinWarps;
+constexpr int kJoinWarps = 16, kJoinGroups = 4, kJoinDims = 128 / (kJoinWarps / kJoinGroups);
 
 __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __grid_constant__ SharedArgs a, int short_ctas) {
-    __shared__ int s_short[HSQ_MAX_REQUESTS];
-    __shared__ __align__(16) uint16_t s_out[32][136];
-    __shared__ long long s_to[32];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d0 = warp * kJoinDims;
+    __shared__ __align__(16) float s_x[2][128][32];  // (first the requests' offsets: 4096 ints)
+    __shared__ float2 s_ml[kJoinGroups][32];
+    int* s_short = reinterpret_cast<int*>(&s_x[0][0][0]);
+    static_assert(sizeof(s_x) >= HSQ_MAX_REQUESTS * sizeof(int), "the offsets fit");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = warp % kJoinGroups, d0 = warp / kJoinGroups * kJoinDims;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PlanHead p = *a.head;
-    struct Parts { const float* o; const float2* ml; long long step; int n, pitch; };  // n parts, `step` part rows apart
-    Parts list[2] = {{nullptr, nullptr, 0, 0, 1}, {nullptr, nullptr, 0, 0, 1}};
+    // the row's parts: n0 at o0 / ml0, n1 at o1 / ml1, `step` part rows apart
+    const float *o0 = nullptr, *o1 = nullptr;
+    const float2 *ml0 = nullptr, *ml1 = nullptr;
+    int n0 = 0, n1 = 0, step0 = 1, step1 = 1, pitch1 = kTileRows;
     bool live;
     int h, token = 0, jj = 0;
-    if ((int)blockIdx.x < short_ctas) {
+    const bool brief = (int)blockIdx.x < short_ctas;
+    if (brief) {
         h = blockIdx.x % a.Hkv;
         const int grp = blockIdx.x / a.Hkv, tile = grp >> 2, row = (grp & 3) * 32 + lane;
+        for (int i = tid; i < a.B; i += 32 * kJoinWarps) s_short[i] = a.req[i].w;
         const int rows = min(a.tpt, p.tokens - tile * a.tpt) * a.r;
         if ((grp & 3) * 32 >= rows) return;
-        for (int i = tid; i < a.B; i += 32 * kJoinWarps) s_short[i] = a.req[i].w;
         __syncthreads();
         live = row < rows;
         const int at = tile * a.tpt + (live ? row : 0) / a.r;
@@ -961,7 +1026,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             const int mid = (lo + hi) >> 1;
             if (s_short[mid] <= at) lo = mid; else hi = mid;
         }
+        __syncthreads();
         const int4 q = a.req[lo];
+        const long long b_at = a.b_at[lo];
         token = q.x + at - q.w;
         if (p.work_a > 0) {
             const int pair = tile >> 1, stream = tile & 1;
@@ -971,74 +1038,109 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             const long long w0 = h * p.head_a + pair * keys * kCostPair;
             const int c0 = run_of(p, w0), c1 = run_of(p, w0 + (long long)(a.prefix_tiles - 1) * rate);
             const size_t slot = ((size_t)h * p.pairs + pair + c0) * 2 + stream;
-            list[0] = {a.a_o + slot * 128 * kTileRows + row, a.a_ml + slot * kTileRows + row, split ? 1 : 2,
-                       (c1 - c0 + 1) * (split ? 2 : 1), kTileRows};
+            o0 = a.a_o + slot * 128 * kTileRows + row;
+            ml0 = a.a_ml + slot * kTileRows + row;
+            step0 = split ? 1 : 2;
+            n0 = (c1 - c0 + 1) * (split ? 2 : 1);
         }
         if (q.z > 0) {
             const long long cost = (long long)(q.z + kItemKeys) * kCostOwn;
-            const long long w0 = p.work_a + p.work_c + a.b_at[lo] + h * cost;
+            const long long w0 = p.work_a + p.work_c + b_at + h * cost;
             const int tiles = (q.z + kTileKeys - 1) / kTileKeys;
             const int c0 = run_of(p, w0), c1 = run_of(p, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
             const size_t slot = ((size_t)lo * a.Hkv + h + c0) * 2;
             const int orow = (at - q.w) * a.r + jj;
-            list[1] = {a.b_o + slot * 128 * a.own_rows + orow, a.b_ml + slot * a.own_rows + orow, 1, 2 * (c1 - c0 + 1), a.own_rows};
+            pitch1 = a.own_rows;
+            o1 = a.b_o + slot * 128 * pitch1 + orow;
+            ml1 = a.b_ml + slot * pitch1 + orow;
+            n1 = 2 * (c1 - c0 + 1);
         }
     } else {
-        const int e = blockIdx.x - short_ctas, c = 1 + (e >> 3), st = (e >> 2) & 1, row = (e & 3) * 32 + lane;
+        // (few parts: the groups of warps take 32 rows each instead)
+        const int e = blockIdx.x - short_ctas, c = 1 + (e >> 1), st = e & 1, row = group * 32 + lane;
         const CutRecord cut = *reinterpret_cast<const CutRecord*>(a.cut + 16 * c);
         const int rows = (st ? cut.toks1 : cut.toks0) * a.r;
-        if (!cut.valid || (e & 3) * 32 >= rows) return;
+        if (!cut.valid) return;
         live = row < rows;
         h = cut.h;
         token = (st ? cut.tok1 : cut.tok0) + (live ? row : 0) / a.r;
         jj = (live ? row : 0) % a.r;
         // slot 2 c0 + 1, then 2 c0 + 2, 2 c0 + 4, ...
         const size_t s0 = (2 * (size_t)cut.c0 + 1) * 2 + st, s1 = (2 * (size_t)cut.c0 + 2) * 2 + st;
-        list[0] = {a.c_o + s0 * 128 * kTileRows + row, a.c_ml + s0 * kTileRows + row, 1, 1, kTileRows};
-        list[1] = {a.c_o + s1 * 128 * kTileRows + row, a.c_ml + s1 * kTileRows + row, 4, cut.c1 - cut.c0, kTileRows};
+        o0 = a.c_o + s0 * 128 * kTileRows + row;
+        ml0 = a.c_ml + s0 * kTileRows + row;
+        n0 = 1;
+        o1 = a.c_o + s1 * 128 * kTileRows + row;
+        ml1 = a.c_ml + s1 * kTileRows + row;
+        step1 = 4;
+        n1 = cut.c1 - cut.c0;
     }
-    if (!live) list[0].n = list[1].n = 0;
-    float M = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll 4
-        for (int k = 0; k < list[e].n; ++k) M = fmaxf(M, __ldcg(list[e].ml + k * list[e].step * list[e].pitch).x);
-    }
-    float L = 0.f, x[kJoinDims];
+    const int n = live ? n0 + n1 : 0;
+    float M = -INFINITY, L = 0.f, x[kJoinDims];
 #pragma unroll
     for (int d = 0; d < kJoinDims; ++d) x[d] = 0.f;
+#pragma unroll 2
+    for (int k = brief ? group : 0; k < n; k += brief ? kJoinGroups : 1) {
+        const bool second = k >= n0;
+        const size_t at = second ? (size_t)(k - n0) * step1 : (size_t)k * step0, pitch = second ? pitch1 : kTileRows;
+        const float2 ml = __ldcg((second ? ml1 : ml0) + at * pitch);
+        const float* o = (second ? o1 : o0) + (at * 128 + d0) * pitch;
+        float v[kJoinDims];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const Parts& q = list[e];
-#pragma unroll 4
-        for (int k = 0; k < q.n; ++k) {
-            const float2 ml = __ldcg(q.ml + k * q.step * q.pitch);
-            const float* o = q.o + (k * q.step * 128 + d0) * q.pitch;
-            float v[kJoinDims];
+        for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + d * pitch);
+        if (ml.y > 0.f) {  // (a part without a key has no o)
+            const float to = fmaxf(M, ml.x);
+            const float was = M == -INFINITY ? 0.f : ex2_approx((M - to) * kLogitScaleLog2), w = ex2_approx((ml.x - to) * kLogitScaleLog2);
+            M = to;
+            L = fmaf(ml.y, w, L * was);
 #pragma unroll
-            for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + (size_t)d * q.pitch);
-            if (ml.y > 0.f) {  // (a part without a key has no o)
-                const float w = ex2_approx((ml.x - M) * kLogitScaleLog2);
-                L = fmaf(ml.y, w, L);
-#pragma unroll
-                for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(v[d], w, x[d]);
-            }
+            for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(v[d], w, x[d] * was);
         }
     }
-    const float inv = L > 0.f ? 1.0f / L : 0.f;
-    uint32_t y[kJoinDims / 2];
+    float Mall = M, Lall = L;
+    if (brief) {
+        if (d0 == 0) s_ml[group][lane] = make_float2(M, L);
+        __syncthreads();
+        Mall = -INFINITY;
+        Lall = 0.f;
 #pragma unroll
-    for (int d = 0; d < kJoinDims; d += 2) y[d / 2] = pack_bf16(x[d] * inv, x[d + 1] * inv);
-    *reinterpret_cast<uint4*>(&s_out[lane][d0]) = make_uint4(y[0], y[1], y[2], y[3]);
-    const long long to = (long long)token * a.Hq + h * a.r + jj;
-    if (warp == 0) {
-        s_to[lane] = live ? to : -1;
-        if (live && a.lse) a.lse[to] = L > 0.f ? M * kRsqrtD + logf(L) : -INFINITY;
+        for (int g = 0; g < kJoinGroups; ++g) Mall = fmaxf(Mall, s_ml[g][lane].x);
+#pragma unroll
+        for (int g = 0; g < kJoinGroups; ++g) {
+            const float2 ml = s_ml[g][lane];
+            if (ml.y > 0.f) Lall = fmaf(ml.y, ex2_approx((ml.x - Mall) * kLogitScaleLog2), Lall);
+        }
+        const float w = M == -INFINITY ? 0.f : ex2_approx((M - Mall) * kLogitScaleLog2);
+#pragma unroll
+        for (int d = 0; d < kJoinDims; ++d) x[d] *= w;
+        // groups 1 and 3 to 0 and 2, then 2 to 0
+        if (group & 1)
+            for (int d = 0; d < kJoinDims; ++d) s_x[group >> 1][d0 + d][lane] = x[d];
+        __syncthreads();
+        if (!(group & 1))
+#pragma unroll
+            for (int d = 0; d < kJoinDims; ++d) x[d] += s_x[group >> 1][d0 + d][lane];
+        __syncthreads();
+        if (group == 2)
+#pragma unroll
+            for (int d = 0; d < kJoinDims; ++d) s_x[0][d0 + d][lane] = x[d];
+        __syncthreads();
+        if (group == 0)
+#pragma unroll
+            for (int d = 0; d < kJoinDims; ++d) x[d] += s_x[0][d0 + d][lane];
     }
-    __syncthreads();
-    const int orow = tid >> 4, c = tid & 15;  // 32 rows x 16 chunks of 16 bytes
-    if (s_to[orow] >= 0)
-        *reinterpret_cast<uint4*>(a.out + s_to[orow] * 128 + 8 * c) = *reinterpret_cast<const uint4*>(&s_out[orow][8 * c]);
+    if ((group == 0 || !brief) && live) {
+        const float inv = Lall > 0.f ? 1.0f / Lall : 0.f;
+        const size_t to = (size_t)token * a.Hq + h * a.r + jj;
+#pragma unroll
+        for (int d = 0; d < kJoinDims; ++d) x[d] *= inv;
+        uint4* dst = reinterpret_cast<uint4*>(a.out + to * 128 + d0);
+#pragma unroll
+        for (int d = 0; d < kJoinDims; d += 8)
+            dst[d >> 3] = make_uint4(pack_bf16(x[d], x[d + 1]), pack_bf16(x[d + 2], x[d + 3]), pack_bf16(x[d + 4], x[d + 5]),
+                                     pack_bf16(x[d + 6], x[d + 7]));
+        if (d0 == 0 && a.lse) a.lse[to] = Lall > 0.f ? Mall * kRsqrtD + logf(Lall) : -INFINITY;
+    }
 }
 
 // ---- host side --------------------------------------------------------------------------
@@ -1187,7 +1289,7 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int tiles = (int)((std::min<long long>(rows, (long long)B * tpt) + tpt - 1) / tpt);
     int short_ctas = 4 * tiles * Hkv;
-    const int cut_ctas = max_new > tpt ? 8 * (x.runs - 1) : 0;
+    const int cut_ctas = max_new > tpt ? 2 * (x.runs - 1) : 0;
     void* plan_args[] = {&a};
     void* tc_args[] = {&mq, &mk, &mv, &a};
     void* join_args[] = {&a, &short_ctas};
