@@ -17,14 +17,15 @@
 // Work.  A request is short when its new tokens fit one tile (n <= 128 / r: decode,
 // proposals), else long (a prompt's chunk).  Three kinds of items:
 //   A  (KV head, pair of row tiles of the short requests' tokens, packed): the prefix;
-//   B  (short request, KV head): its own tokens;
+//   B  (short request of more than 16 rows, n r > 16, KV head): its own tokens;
 //   C  (long request, KV head, pair of its row tiles): the prefix, then its own
-//      tokens up to the pair's last.
-// An item is a run of 128-key tiles with a cost per tile; the items one after
-// another make one line of cost, cut into as many equal runs as the GPU has SMs:
-// a persistent CTA each.  Decode's A is bound by the tensor cores and its B by HBM, and since
-// they lie at different places of the line, different SMs work on either at
-// any time and both are in use throughout.
+//      tokens up to the pair's last;
+//   D  (request of up to 16 rows, KV head): its own tokens, by single warps.
+// An item is a run of key tiles (D: of groups of 16 keys) with a cost each; the
+// items one after another make one line of cost, cut into as many equal runs as the
+// GPU has SMs: a persistent CTA each.  Decode's A is bound by the tensor cores and its D
+// by HBM, and since they lie at different places of the line, different SMs work on
+// either at any time and both are in use throughout.
 //
 // Three kernels, the later two launched with programmatic serialization (their set-up
 // runs while the one before ends):
@@ -56,9 +57,11 @@ constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which t
 // Cost of a key tile, per key: two row tiles (tensor cores), one row tile (A: tensor cores and loads; B: loads); and
 // what an item costs beside its tiles, in keys.
 constexpr int kCostPair = 8, kCostOne = 6, kCostOwn = 6, kItemKeys = 96;
+// D: requests of up to kFewRows rows; a group is 16 keys of one warp, kFewWarps warps share a CTA's run
+constexpr int kFewRows = 16, kFewWarps = 8, kCostFew = 6, kFewItemKeys = 64;
 
 struct PlanHead {
-    long long work, work_a, work_c;  // the line: [A | C | B]
+    long long work, work_a, work_c, work_t;  // the line: [A | C | B | D], work_t where D begins
     long long head_a;                // A's cost for one KV head
     int tokens, tiles, pairs;        // of the short requests
     int dense;                       // 1: the short requests' tokens are the rows [base, base + tokens)
@@ -77,17 +80,39 @@ struct SharedArgs {
     // workspace
     PlanHead* head;
     int4* req;              // [B] first row, rows, own tokens (checked), short tokens before it
-    long long *c_at, *b_at; // [B + 1] cost of the C and B items before request b
+    long long *c_at, *b_at, *d_at; // [B + 1] cost of the C, B and D items before request b
     int* cut;               // [runs][16 ints] the C item that run c is the second to work on (see CutRecord)
     // parts: o [slot][2 streams][128 dims][rows], ml [slot][2 streams][rows] (maximum of q.k, unscaled; sum)
     float *a_o, *b_o, *c_o;
     float2 *a_ml, *b_ml, *c_ml;
+    // D's: o [slot][rows][128], ml [slot][rows]
+    float* d_o;
+    float2* d_ml;
+    int few_rows;  // 8 or 16
     int* err;
 };
 
 // the run that holds place w of the line, and where run c begins
 __device__ __forceinline__ int run_of(const PlanHead& p, long long w) { return (int)(((w + 1) * p.runs - 1) / p.work); }
 __device__ __forceinline__ long long run_begin(const PlanHead& p, int c) { return p.work * min(c, p.runs) / p.runs; }
+
+__device__ __forceinline__ long long few_cost(int len) { return (long long)(((len + 15) >> 4) * 16 + kFewItemKeys) * kCostFew; }
+
+// D: the warp (of all CTAs' warps) that takes the group at place x: a CTA's share of D is cut into eight equal parts
+// (into as many as it has groups, the last ones of the eight, where D begins inside its run)
+struct FewShare { long long lo, hi; int parts; };
+__device__ __forceinline__ FewShare few_share(const PlanHead& p, int c) {
+    FewShare s;
+    s.lo = max(run_begin(p, c), p.work_t);
+    s.hi = run_begin(p, c + 1);
+    s.parts = (int)max(1LL, min((long long)kFewWarps, (s.hi - s.lo) / (16 * kCostFew)));
+    return s;
+}
+__device__ __forceinline__ int few_warp_of(const PlanHead& p, long long x) {
+    const int c = run_of(p, x);
+    const FewShare s = few_share(p, c);
+    return c * kFewWarps + kFewWarps - s.parts + (int)(((x - s.lo + 1) * s.parts - 1) / (s.hi - s.lo));
+}
 
 // virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostPair a key
 __device__ __forceinline__ long long unit_base(const SharedArgs& a, int n, int len) {
@@ -106,10 +131,10 @@ constexpr int kPlanThreads = 512;
 
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ SharedArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ long long s_w[3][kPlanThreads / 32];
+    __shared__ long long s_w[4][kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int bad = 0;
-    long long before[3] = {0, 0, 0};  // short tokens, C cost, B cost
+    long long before[4] = {0, 0, 0, 0};  // short tokens, C, B and D cost
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int first = 0, n = 0, len = 0;
@@ -125,15 +150,18 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
             if (len != l || len < n) bad |= HSQ_DEVERR_LEN;
         }
         const bool brief = n <= a.tpt;
-        long long x[3] = {brief ? n : 0, 0, 0}, own[3];
-        if (n > 0 && brief && len > 0) x[2] = (long long)a.Hkv * (len + kItemKeys) * kCostOwn;
+        long long x[4] = {brief ? n : 0, 0, 0, 0}, own[4];
+        if (n > 0 && brief && len > 0) {
+            if (n * a.r > kFewRows) x[2] = (long long)a.Hkv * (len + kItemKeys) * kCostOwn;
+            else x[3] = a.Hkv * few_cost(len);
+        }
         if (!brief) {
             const int D = 2 * a.tpt, units = (n + D - 1) / D;
             const long long base = unit_base(a, n, len);
             x[1] = a.Hkv * (units_before(base, D, units - 1) + kCostPair * (base + n));
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < 4; ++k) {
             own[k] = x[k];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -144,7 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
+        for (int k = 0; k < 4; ++k) {
             long long t = before[k], mine = 0;
             for (int w = 0; w < kPlanThreads / 32; ++w) {
                 if (w == warp) mine = t;
@@ -157,6 +185,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
             a.req[b] = make_int4(first, n, len, (int)x[0]);
             a.c_at[b] = x[1];
             a.b_at[b] = x[2];
+            a.d_at[b] = x[3];
         }
         __syncthreads();
     }
@@ -171,14 +200,16 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         h.head_a = (h.tiles >> 1) * keys * kCostPair + (h.tiles & 1) * keys * kCostOne;
         h.work_a = a.Hkv * h.head_a;
         h.work_c = before[1];
-        h.work = h.work_a + h.work_c + before[2];
+        h.work_t = h.work_a + h.work_c + before[2];
+        h.work = h.work_t + before[3];
         h.base = a.q_start[0];
-        const int most = (h.tiles > 1 || h.work_c > 0 ? kCostPair : max(kCostOne, kCostOwn)) * kTileKeys;
+        const int most = (h.tiles > 1 || h.work_c > 0 ? kCostPair : max(max(kCostOne, kCostOwn), kCostFew)) * kTileKeys;
         h.runs = (int)max(1LL, min((long long)a.runs, h.work / most));
         h.dense = !any_bad && before[1] == 0;
         *a.head = h;
         a.c_at[a.B] = before[1];
         a.b_at[a.B] = before[2];
+        a.d_at[a.B] = before[3];
     }
 }
 
@@ -235,7 +266,8 @@ constexpr int kTcBars = 2 * kStages + 11 + 2 * kQueue;
 constexpr uint32_t kOffMask = kOffBars + 8 * (kTcBars + 1);  // [8] pages of a key tile that lie in the pool
 constexpr uint32_t kOffSeg = kOffMask + 32;                  // [4] segments of the run
 constexpr uint32_t kSegBytes = 96;
-constexpr uint32_t kTcSmem = kOffSeg + kQueue * kSegBytes + 16 + 1024;  // + TMEM address, alignment
+constexpr uint32_t kOffFew = kOffSeg + kQueue * kSegBytes + 16;  // (+ TMEM address) D's barriers, three a warp
+constexpr uint32_t kTcSmem = kOffFew + 8 * 8 * 3 + 1024;         // + alignment
 constexpr int kSegReaders = 10;                              // 8 softmax warps, the MMA thread, the query loader
 
 // The key tiles [n0, n1) of an item that lie in this CTA's run.
@@ -321,7 +353,7 @@ struct Walker {
     }
     // the item that holds place x of the line
     __device__ void locate(long long x) {
-        if (x >= p.work) {
+        if (x >= p.work_t) {
             more = false;
             return;
         }
@@ -360,7 +392,7 @@ struct Walker {
     }
     __device__ void start(int c) {
         at = run_begin(p, c);
-        end = run_begin(p, c + 1);
+        end = min(run_begin(p, c + 1), p.work_t);
         more = at < end;
         if (more) locate(at);
     }
@@ -445,9 +477,266 @@ struct Walker {
     }
 };
 
+// ---- D: few rows, single warps -----------------------------------------------------------
+// NT tiles of 8 rows (tokens x heads).  A warp takes groups of 16 keys one after another, loaded three groups
+// ahead (TMA, 128-byte swizzle) into 24 KB of the ring that the CTA's other work no longer needs, on from one
+// item to the next.
+//   S^T (16 keys x 8 rows) = K (A operand, by ldmatrix) Q^T (B);
+//   O^T (128 dims x 8 rows) += V^T (A, by transposing ldmatrix) P^T (B); P^T comes from S^T by two 8 x 8
+//     transposes (movmatrix).
+// So no lane exchanges logits but for a new maximum, and up to 192 KB an SM are in flight.  Bound by HBM.  (On
+// the tensor cores' path a request of 4 rows costs what one of 128 does: 1.4 us a 128-key tile and as much
+// an item; with the fragments loaded straight into registers, 8 KB a warp in flight, a group took 1.8 us.)
+
+constexpr int kFewStages = 3;
+constexpr uint32_t kFewStageBytes = 16 * 256 * 2, kFewWarpBytes = kFewStages * kFewStageBytes;
+static_assert(kFewWarps * kFewWarpBytes <= kOffBars, "the warps' stages fit the ring and the query tiles");
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};\n"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix(uint32_t (&x)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_trans(uint32_t (&x)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Walks a warp's share of D, item by item: groups [s, s1) of (request b, KV head h).
+struct FewWalk {
+    const SharedArgs& a;
+    const PlanHead& p;
+    long long at, end, w0;
+    int b, h, s, s1, first, n, len;
+    bool more;
+
+    __device__ __forceinline__ void find(long long x) {
+        b = warp_find(a.d_at, a.B, x - p.work_t);
+        const int4 q = a.req[b];
+        first = q.x;
+        n = q.y;
+        len = q.z;
+        const long long z = x - p.work_t - a.d_at[b], cost = few_cost(len);
+        h = (int)(z / cost);
+        w0 = x - z + h * cost;
+    }
+    __device__ __forceinline__ void take() {  // the item's groups, or the next item's that has some
+        constexpr int rate = 16 * kCostFew;
+        while (true) {
+            const int groups = (len + 15) >> 4;
+            s = at <= w0 ? 0 : (int)((at - w0 + rate - 1) / rate);
+            s1 = w0 + (long long)groups * rate <= end ? groups : (int)min((long long)groups, (end - w0 + rate - 1) / rate);
+            if (s < s1) return;
+            if (!step()) return;
+        }
+    }
+    __device__ __forceinline__ bool step() {
+        const long long w1 = w0 + few_cost(len);
+        if (w1 >= end) return more = false;
+        if (h + 1 < a.Hkv) {
+            ++h;
+            w0 = w1;
+        } else {
+            find(w1);
+        }
+        return true;
+    }
+    __device__ __forceinline__ void next_item() {
+        if (step()) take();
+    }
+};
+
+template <int NT>
+__device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, const PlanHead& p,
+                                         int c, int warp, uint32_t stages, uint8_t* stages_g, uint32_t bars, bool& failed,
+                                         int& bad) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const FewShare share = few_share(p, c);
+    if (share.hi <= share.lo) return;
+    const int sub = warp - (kFewWarps - share.parts);
+    if (sub < 0) return;
+    FewWalk ask{a, p};  // what is loaded next
+    ask.at = share.lo + (share.hi - share.lo) * sub / share.parts;
+    ask.end = share.lo + (share.hi - share.lo) * (sub + 1) / share.parts;
+    ask.more = ask.at < ask.end;
+    if (!ask.more) return;
+    ask.find(ask.at);
+    ask.take();
+    if (!ask.more) return;
+    FewWalk now = ask;  // what is worked on
+    Ring<kFewStages> in{0, 0}, out{0, 0};
+    uint32_t missing = 0;  // a bit for each stage: its page is not in the pool
+    auto id_of = [&] { return a.table[(size_t)ask.b * a.width + ((16 * ask.s) >> a.page_shift)]; };
+    int id = id_of();
+    auto load = [&] {  // the next group into stage in
+        if (!ask.more) return;
+        const bool have = id >= 0 && id < a.n_pages;
+        if (!have) bad |= HSQ_DEVERR_PAGE;
+        missing = (missing & ~(1u << in.stage)) | (have ? 0u : 1u << in.stage);
+        if (lane == 0) {
+            const uint32_t dst = stages + in.stage * kFewStageBytes, bar = bars + 8 * in.stage;
+            // (a page outside the pool is read past the map's extent: zeros, masked below)
+            const int y = have ? ((id * a.Hkv + ask.h) << a.page_shift) + ((16 * ask.s) & (a.page_n - 1)) : (a.n_pages * a.Hkv) << a.page_shift;
+            mbar_expect_tx(bar, kFewStageBytes);
+            tma_2d(dst, &mk, 0, y, bar);
+            tma_2d(dst + 2048, &mk, 64, y, bar);
+            tma_2d(dst + 4096, &mv, 0, y, bar);
+            tma_2d(dst + 6144, &mv, 64, y, bar);
+        }
+        __syncwarp();
+        in.advance();
+        if (++ask.s == ask.s1) ask.next_item();
+        if (ask.more) id = id_of();
+    };
+    for (int i = 0; i < kFewStages; ++i) load();
+    // lane's row of the 8 x 8 matrices that ldmatrix takes: K: keys (lane & 15), chunks 2 kk + (lane >> 4);
+    // V: keys (lane & 7) + 8 (lane >> 4), chunks 2 i + ((lane >> 3) & 1)
+    const uint32_t k_row = (lane & 15) * 128, k_x = lane & 7, k_c = lane >> 4;
+    const uint32_t v_row = ((lane & 7) + 8 * (lane >> 4)) * 128, v_c = (lane >> 3) & 1;
+    while (now.more && !failed) {
+        const int rows = now.n * a.r;
+        uint32_t qf[NT][8][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = 8 * nt + g;
+            const bool in_use = row < rows;
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                a.q + ((size_t)(now.first + (in_use ? row / a.r : 0)) * a.Hq + now.h * a.r + (in_use ? row % a.r : 0)) * 128 + 2 * t);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                qf[nt][kk][0] = in_use ? src[8 * kk] : 0u;
+                qf[nt][kk][1] = in_use ? src[8 * kk + 4] : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int rr = 8 * nt + 2 * t + e;
+                lim[nt][e] = rr < rows ? min(now.len, now.len - now.n + rr / a.r + 1) : 0;
+            }
+        }
+        float o[NT][8][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+#pragma unroll 1
+        for (int s = now.s; s < now.s1; ++s) {
+            const uint32_t kb = stages + out.stage * kFewStageBytes, vb = kb + 4096;
+            mbar_wait_fast(bars + 8 * out.stage, out.phase, failed);
+            const bool gone = (missing >> out.stage) & 1u;
+            const int valid = now.len - 16 * s;  // keys of the group that the request has
+            if (valid < 16) {  // the rest of the page is stale: weight 0, but it has to be finite
+                for (int i = lane; i < (16 - valid) * 16; i += 32)
+                    *reinterpret_cast<uint4*>(stages_g + out.stage * kFewStageBytes + 4096 + ((i >> 3) & 1) * 2048 + (valid + (i >> 4)) * 128 +
+                                              (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+            float x[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                uint32_t k[4];
+                ldmatrix(k, kb + (kk >> 2) * 2048 + k_row + ((((2 * kk + k_c) & 7) ^ k_x) << 4));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_16816(x[nt], k, qf[nt][kk][0], qf[nt][kk][1]);
+            }
+            bool look = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // key g + 8 (e >> 1), row 2 t + (e & 1)
+                    if (gone || 16 * s + g + 8 * (e >> 1) >= lim[nt][e & 1]) x[nt][e] = -INFINITY;
+                    look |= x[nt][e] * kLogitScaleLog2 > m[nt][e & 1] * kLogitScaleLog2 + 8.f;  // (the first key raises from -inf)
+                }
+            if (__any_sync(kFull, look)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(m[nt][e], fmaxf(x[nt][e], x[nt][e + 2]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+                        const float alpha = mx == -INFINITY ? 1.f : ex2_approx((m[nt][e] - mx) * kLogitScaleLog2);
+                        m[nt][e] = mx;
+                        l[nt][e] *= alpha;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            o[nt][i][e] *= alpha;
+                            o[nt][i][e + 2] *= alpha;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float pr[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float off = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1] * kLogitScaleLog2;
+                    pr[e] = ex2_approx(fmaf(x[nt][e], kLogitScaleLog2, -off));
+                    l[nt][e & 1] += pr[e];
+                }
+                pf[nt][0] = transpose_8x8(pack_bf16(pr[0], pr[1]));
+                pf[nt][1] = transpose_8x8(pack_bf16(pr[2], pr[3]));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t v[4];
+                ldmatrix_trans(v, vb + (i >> 2) * 2048 + v_row + ((((2 * i + v_c) & 7) ^ k_x) << 4));
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], v, pf[nt][0], pf[nt][1]);
+            }
+            __syncwarp();  // (every lane has read the stage)
+            out.advance();
+            load();
+        }
+        const size_t slot = (size_t)now.b * a.Hkv + now.h + c * kFewWarps + warp;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], d);
+                const int row = 8 * nt + 2 * t + e;
+                if (row < rows) {
+                    const size_t to = slot * (8 * NT) + row;
+                    if (g == 0) a.d_ml[to] = make_float2(m[nt][e], l[nt][e]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a.d_o[to * 128 + 16 * i + g] = o[nt][i][e];
+                        a.d_o[to * 128 + 16 * i + 8 + g] = o[nt][i][e + 2];
+                    }
+                }
+            }
+        now.next_item();
+    }
+    if (failed)  // see the copies in flight land before the CTA ends
+        for (int i = 0; i < kFewStages; ++i)
+            mbar_wait(bars + 8 * i, i < (int)in.stage ? in.phase : in.phase ^ 1, 1 << 12);
+}
+
+template <int NT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     shared_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ SharedArgs a) {
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mk16,
+                     const __grid_constant__ CUtensorMap mv16, const __grid_constant__ SharedArgs a) {
     extern __shared__ uint8_t tc_raw[];
     const uint32_t raw = smem_addr(tc_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* gbase = tc_raw + (base - raw);
@@ -477,6 +766,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(seg_full + 8 * i, 1);
             mbar_init(seg_empty + 8 * i, kSegReaders);
         }
+        for (int i = 0; i < kFewWarps * kFewStages; ++i) mbar_init(base + kOffFew + 8 * i, 1);
         mbar_init_fence();
     }
     if (warp == 9) {
@@ -831,7 +1121,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         Ring<kQueue> queue{0, 0};
         int step0 = 0;
         const int row_token = row / a.r;
-        while (receive(queue, true)) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const PlanHead plan = *a.head;
+        const bool tiles = run_begin(plan, blockIdx.x) < plan.work_t;  // (a run of D alone does not wait for the queue)
+        while (tiles && receive(queue, true)) {
             const int toks = st ? s.toks1 : s.toks0, tok = st ? s.tok1 : s.tok0, stop = st ? s.end1 : s.end0;
             const bool live = row_token < toks;
             const bool idle = 32 * (warp & 3) >= toks * a.r;  // (warp-uniform) no row of this warp in use
@@ -976,6 +1269,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_before();  // (O has been read: the next segment's first P releases it)
             step0 += s.n1 - s.n0;
         }
+        // D: every stream's work of this CTA is done, its memory free
+        named_bar_sync(1, 256);
+        if (!failed)
+            few_rows<NT>(a, mk16, mv16, plan, blockIdx.x, warp, base + warp * kFewWarpBytes, gbase + warp * kFewWarpBytes,
+                         base + kOffFew + 8 * kFewStages * warp, failed, bad);
     }
     if (failed) bad |= HSQ_DEVERR_WAIT;
     if (bad) atomicOr(a.err, bad);
@@ -1008,7 +1306,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const float *o0 = nullptr, *o1 = nullptr;
     const float2 *ml0 = nullptr, *ml1 = nullptr;
     int n0 = 0, n1 = 0, step0 = 1, step1 = 1, pitch1 = kTileRows;
-    bool live;
+    bool live, by_row = false;  // by_row: the second parts' o has a row's dims side by side (D's)
     int h, token = 0, jj = 0;
     const bool brief = (int)blockIdx.x < short_ctas;
     if (brief) {
@@ -1028,7 +1326,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         }
         __syncthreads();
         const int4 q = a.req[lo];
-        const long long b_at = a.b_at[lo];
+        const bool few = q.y * a.r <= kFewRows;
+        const long long at0 = few ? p.work_t + a.d_at[lo] : p.work_a + p.work_c + a.b_at[lo];
         token = q.x + at - q.w;
         if (p.work_a > 0) {
             const int pair = tile >> 1, stream = tile & 1;
@@ -1043,13 +1342,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             step0 = split ? 1 : 2;
             n0 = (c1 - c0 + 1) * (split ? 2 : 1);
         }
-        if (q.z > 0) {
+        const int orow = (at - q.w) * a.r + jj;
+        if (q.z > 0 && few) {
+            const long long w0 = at0 + h * few_cost(q.z);
+            const int v0 = few_warp_of(p, w0), v1 = few_warp_of(p, w0 + (long long)(((q.z + 15) >> 4) - 1) * 16 * kCostFew);
+            const size_t slot = (size_t)lo * a.Hkv + h + v0;
+            by_row = true;
+            pitch1 = a.few_rows;
+            o1 = a.d_o + (slot * a.few_rows + orow) * 128;
+            ml1 = a.d_ml + slot * a.few_rows + orow;
+            n1 = v1 - v0 + 1;
+        } else if (q.z > 0) {
             const long long cost = (long long)(q.z + kItemKeys) * kCostOwn;
-            const long long w0 = p.work_a + p.work_c + b_at + h * cost;
+            const long long w0 = at0 + h * cost;
             const int tiles = (q.z + kTileKeys - 1) / kTileKeys;
             const int c0 = run_of(p, w0), c1 = run_of(p, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
             const size_t slot = ((size_t)lo * a.Hkv + h + c0) * 2;
-            const int orow = (at - q.w) * a.r + jj;
             pitch1 = a.own_rows;
             o1 = a.b_o + slot * 128 * pitch1 + orow;
             ml1 = a.b_ml + slot * pitch1 + orow;
@@ -1084,10 +1392,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         const bool second = k >= n0;
         const size_t at = second ? (size_t)(k - n0) * step1 : (size_t)k * step0, pitch = second ? pitch1 : kTileRows;
         const float2 ml = __ldcg((second ? ml1 : ml0) + at * pitch);
-        const float* o = (second ? o1 : o0) + (at * 128 + d0) * pitch;
         float v[kJoinDims];
+        if (second && by_row) {
+            const float4* o = reinterpret_cast<const float4*>(o1 + at * pitch * 128 + d0);
 #pragma unroll
-        for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + d * pitch);
+            for (int d = 0; d < kJoinDims; d += 4) {
+                const float4 y = __ldcg(o + (d >> 2));
+                v[d] = y.x;
+                v[d + 1] = y.y;
+                v[d + 2] = y.z;
+                v[d + 3] = y.w;
+            }
+        } else {
+            const float* o = (second ? o1 : o0) + (at * 128 + d0) * pitch;
+#pragma unroll
+            for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + d * pitch);
+        }
         if (ml.y > 0.f) {  // (a part without a key has no o)
             const float to = fmaxf(M, ml.x);
             const float was = M == -INFINITY ? 0.f : ex2_approx((M - to) * kLogitScaleLog2), w = ex2_approx((ml.x - to) * kLogitScaleLog2);
@@ -1180,7 +1500,7 @@ bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint3
 }
 
 // The workspace's pieces and their offsets.
-struct Layout { size_t head, req, c_at, b_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, bytes; int runs, own_rows; };
+struct Layout { size_t head, req, c_at, b_at, d_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, d_o, d_ml, bytes; int runs, own_rows, few_rows; };
 
 Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new) {
     Layout x{};
@@ -1197,9 +1517,11 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     x.req = take((size_t)B * 16);
     x.c_at = take((size_t)(B + 1) * 8);
     x.b_at = take((size_t)(B + 1) * 8);
+    x.d_at = take((size_t)(B + 1) * 8);
+    x.few_rows = (size_t)max_new * r <= 8 ? 8 : 16;
     x.cut = take((size_t)x.runs * 64);
     const size_t tokens = std::min<size_t>(rows, (size_t)B * tpt), tiles = (tokens + tpt - 1) / tpt;
-    const size_t a = prefix_len > 0 ? Hkv * ((tiles + 1) / 2) + x.runs : 0, b = (size_t)B * Hkv + x.runs;
+    const size_t a = prefix_len > 0 ? Hkv * ((tiles + 1) / 2) + x.runs : 0, b = (size_t)max_new * r > kFewRows ? (size_t)B * Hkv + x.runs : 0;
     const size_t c = (size_t)max_new > tpt ? 2 * (size_t)x.runs : 0;
     x.a_o = take(a * 2 * 128 * kTileRows * 4);
     x.a_ml = take(a * 2 * kTileRows * 8);
@@ -1207,6 +1529,9 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     x.b_ml = take(b * 2 * x.own_rows * 8);
     x.c_o = take(c * 2 * 128 * kTileRows * 4);
     x.c_ml = take(c * 2 * kTileRows * 8);
+    const size_t d = (size_t)B * Hkv + (size_t)kFewWarps * x.runs;
+    x.d_o = take(d * x.few_rows * 128 * 4);
+    x.d_ml = take(d * x.few_rows * 8);
     x.bytes = at;
     return x;
 }
@@ -1275,25 +1600,29 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     a.req = reinterpret_cast<int4*>(ws + x.req);
     a.c_at = reinterpret_cast<long long*>(ws + x.c_at);
     a.b_at = reinterpret_cast<long long*>(ws + x.b_at);
+    a.d_at = reinterpret_cast<long long*>(ws + x.d_at);
     a.cut = reinterpret_cast<int*>(ws + x.cut);
     a.a_o = reinterpret_cast<float*>(ws + x.a_o); a.a_ml = reinterpret_cast<float2*>(ws + x.a_ml);
     a.b_o = reinterpret_cast<float*>(ws + x.b_o); a.b_ml = reinterpret_cast<float2*>(ws + x.b_ml);
     a.c_o = reinterpret_cast<float*>(ws + x.c_o); a.c_ml = reinterpret_cast<float2*>(ws + x.c_ml);
+    a.d_o = reinterpret_cast<float*>(ws + x.d_o); a.d_ml = reinterpret_cast<float2*>(ws + x.d_ml);
+    a.few_rows = x.few_rows;
     a.err = ctx->d_err;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mk16, mv16;
     if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const uint64_t n = (uint64_t)pages->n_pages * Hkv * pages->page_n;
     if (!encode_q(&mq, q, rows, a.Hq, r, tpt) || !encode_rows(&mk, pages->k, n, pages->page_n) ||
-        !encode_rows(&mv, pages->v, n, pages->page_n))
+        !encode_rows(&mv, pages->v, n, pages->page_n) || !encode_rows(&mk16, pages->k, n, 16) ||
+        !encode_rows(&mv16, pages->v, n, 16))
         return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int tiles = (int)((std::min<long long>(rows, (long long)B * tpt) + tpt - 1) / tpt);
     int short_ctas = 4 * tiles * Hkv;
     const int cut_ctas = max_new > tpt ? 2 * (x.runs - 1) : 0;
     void* plan_args[] = {&a};
-    void* tc_args[] = {&mq, &mk, &mv, &a};
+    void* tc_args[] = {&mq, &mk, &mv, &mk16, &mv16, &a};
     void* join_args[] = {&a, &short_ctas};
-    const void* fn = (const void*)shared_tc_kernel;
+    const void* fn = x.few_rows == 8 ? (const void*)shared_tc_kernel<1> : (const void*)shared_tc_kernel<2>;
     cudaError_t e = hsq::raise_smem_limit(fn, ctx->device, kTcSmem);
     if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(shared_attn)");
     if ((e = launch((const void*)shared_plan_kernel, 1, kPlanThreads, 0, s, false, plan_args)) != cudaSuccess)
