@@ -21,11 +21,13 @@
 //   C  (long request, KV head, pair of its row tiles): the prefix, then its own
 //      tokens up to the pair's last;
 //   D  (request of up to 16 rows, KV head): its own tokens, by single warps.
-// An item is a run of key tiles (D: of groups of 16 keys) with a cost each; the
-// items one after another make one line of cost, cut into as many equal runs as the
-// GPU has SMs: a persistent CTA each.  Decode's A is bound by the tensor cores and its D
-// by HBM, and since they lie at different places of the line, different SMs work on
-// either at any time and both are in use throughout.
+// An item is a run of key tiles (D: of groups of 16 keys) with a cost each.  The SMs (a
+// persistent CTA each) are dealt to A and to the rest by their costs; each side's items
+// one after another make a line of cost, cut into as many equal runs as it has CTAs.  So
+// some SMs work on A, bound by the tensor cores, while others stream D's pages, bound
+// by HBM, and both are in use throughout.  A's line is the prefix's keys, head by head; up
+// to four pairs of row tiles have a line each, cut alike, so that CTAs side by side read
+// the same key tiles at the same time and HBM gives them once.
 //
 // Three kernels, the later two launched with programmatic serialization (their set-up
 // runs while the one before ends):
@@ -61,13 +63,15 @@ constexpr int kCostPair = 8, kCostOne = 6, kCostOwn = 6, kItemKeys = 96;
 constexpr int kFewRows = 16, kFewWarps = 8, kCostFew = 6, kFewItemKeys = 64;
 
 struct PlanHead {
-    long long work, work_a, work_c, work_t;  // the line: [A | C | B | D], work_t where D begins
-    long long head_a;                // A's cost for one KV head
+    long long lane_a;                // A: length of a lane's line, and of one KV head's part of it
+    long long head_a;
+    long long work, work_c, work_t;  // the others' line: [C | B | D], work_t where D begins
+    int lanes, cuts_a, runs_a;       // A: lanes (1: the pairs one after another), runs of each, CTAs
     int tokens, tiles, pairs;        // of the short requests
     int dense;                       // 1: the short requests' tokens are the rows [base, base + tokens)
     int base;
-    int runs;                        // CTAs with work: no run shorter than a tile, so that every run inside an item holds one
-};
+    int runs;                        // the others' CTAs: runs_a and up
+};  // (no run is shorter than a tile, so that every run inside an item holds one)
 
 struct SharedArgs {
     const int32_t *q_start, *lens, *table, *prefix;
@@ -92,26 +96,26 @@ struct SharedArgs {
     int* err;
 };
 
-// the run that holds place w of the line, and where run c begins
-__device__ __forceinline__ int run_of(const PlanHead& p, long long w) { return (int)(((w + 1) * p.runs - 1) / p.work); }
-__device__ __forceinline__ long long run_begin(const PlanHead& p, int c) { return p.work * min(c, p.runs) / p.runs; }
+// the run that holds place w of a line, and where run i begins
+__device__ __forceinline__ int run_of(long long line, int runs, long long w) { return (int)(((w + 1) * runs - 1) / line); }
+__device__ __forceinline__ long long run_begin(long long line, int runs, int i) { return line * min(i, runs) / runs; }
 
 __device__ __forceinline__ long long few_cost(int len) { return (long long)(((len + 15) >> 4) * 16 + kFewItemKeys) * kCostFew; }
 
 // D: the warp (of all CTAs' warps) that takes the group at place x: a CTA's share of D is cut into eight equal parts
 // (into as many as it has groups, the last ones of the eight, where D begins inside its run)
 struct FewShare { long long lo, hi; int parts; };
-__device__ __forceinline__ FewShare few_share(const PlanHead& p, int c) {
+__device__ __forceinline__ FewShare few_share(const PlanHead& p, int i) {  // i: of the others' runs
     FewShare s;
-    s.lo = max(run_begin(p, c), p.work_t);
-    s.hi = run_begin(p, c + 1);
+    s.lo = max(run_begin(p.work, p.runs, i), p.work_t);
+    s.hi = run_begin(p.work, p.runs, i + 1);
     s.parts = (int)max(1LL, min((long long)kFewWarps, (s.hi - s.lo) / (16 * kCostFew)));
     return s;
 }
 __device__ __forceinline__ int few_warp_of(const PlanHead& p, long long x) {
-    const int c = run_of(p, x);
-    const FewShare s = few_share(p, c);
-    return c * kFewWarps + kFewWarps - s.parts + (int)(((x - s.lo + 1) * s.parts - 1) / (s.hi - s.lo));
+    const int i = run_of(p.work, p.runs, x);
+    const FewShare s = few_share(p, i);
+    return i * kFewWarps + kFewWarps - s.parts + (int)(((x - s.lo + 1) * s.parts - 1) / (s.hi - s.lo));
 }
 
 // virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostPair a key
@@ -197,15 +201,28 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         h.tiles = (h.tokens + a.tpt - 1) / a.tpt;
         h.pairs = (h.tiles + 1) >> 1;
         const long long keys = (long long)a.prefix_tiles * kTileKeys;
-        h.head_a = (h.tiles >> 1) * keys * kCostPair + (h.tiles & 1) * keys * kCostOne;
-        h.work_a = a.Hkv * h.head_a;
+        const long long full = h.tiles >> 1, one = h.tiles & 1;
+        h.lanes = h.pairs <= 4 ? max(h.pairs, 1) : 1;
+        // (lanes are cut alike, so a pair of one tile counts as a whole one there)
+        h.head_a = h.pairs == 0 ? 0 : h.lanes == 1 ? keys * (full * kCostPair + one * kCostOne) : keys * kCostPair;
+        h.lane_a = a.Hkv * h.head_a;
         h.work_c = before[1];
-        h.work_t = h.work_a + h.work_c + before[2];
+        h.work_t = h.work_c + before[2];
         h.work = h.work_t + before[3];
         h.base = a.q_start[0];
-        const int most = (h.tiles > 1 || h.work_c > 0 ? kCostPair : max(max(kCostOne, kCostOwn), kCostFew)) * kTileKeys;
-        h.runs = (int)max(1LL, min((long long)a.runs, h.work / most));
         h.dense = !any_bad && before[1] == 0;
+        const long long work_a = a.Hkv * keys * (full * kCostPair + one * kCostOne), all = work_a + h.work;
+        // CTAs for A, a multiple of the lanes; at least one for what there is of either
+        int ga = 0;
+        if (work_a > 0) {
+            ga = (int)((work_a * a.runs / h.lanes + all / 2) / all) * h.lanes;
+            ga = max(h.lanes, min(ga, (a.runs - (h.work > 0)) / h.lanes * h.lanes));
+        }
+        const int rate = (h.tiles > 1 ? kCostPair : kCostOne) * kTileKeys;
+        h.cuts_a = (int)min((long long)(ga / h.lanes), h.lane_a / rate);
+        h.runs_a = h.cuts_a * h.lanes;
+        const int most = max(max(kCostPair, kCostOwn), kCostFew) * kTileKeys;
+        h.runs = h.work > 0 ? (int)max(1LL, min((long long)(a.runs - ga), h.work / most)) : 0;
         *a.head = h;
         a.c_at[a.B] = before[1];
         a.b_at[a.B] = before[2];
@@ -327,9 +344,10 @@ __device__ __forceinline__ int warp_find(const long long* at, int n, long long x
 struct Walker {
     const SharedArgs& a;
     const PlanHead& p;
-    long long at, end;      // the run
+    long long at, end;      // the run, of A's lane or of the others' line
     long long w0;           // where the current item begins
     int zone, b, h, u, n, len, first;  // the item: A (h, u = pair), C (b, h, unit u), B (b, h)
+    int lane, run;          // A: the CTA's lane and run; else the run
     long long cost;         // the item's
     bool more;
 
@@ -340,10 +358,10 @@ struct Walker {
         len = q.z;
     }
     __device__ __forceinline__ int units() const { return (n + 2 * a.tpt - 1) / (2 * a.tpt); }
+    __device__ __forceinline__ int a_rate() const { return p.lanes == 1 && u == p.pairs - 1 && (p.tiles & 1) ? kCostOne : kCostPair; }
     __device__ __forceinline__ void set_cost() {
         if (zone == 0) {
-            const bool one = u == p.pairs - 1 && (p.tiles & 1);
-            cost = (long long)a.prefix_tiles * kTileKeys * (one ? kCostOne : kCostPair);
+            cost = (long long)a.prefix_tiles * kTileKeys * a_rate();
         } else if (zone == 1) {
             const long long base = unit_base(a, n, len);
             cost = kCostPair * (base + min(n, (u + 1) * 2 * a.tpt));
@@ -353,22 +371,19 @@ struct Walker {
     }
     // the item that holds place x of the line
     __device__ void locate(long long x) {
-        if (x >= p.work_t) {
+        if (zone == 0) {
+            const long long pair = (long long)a.prefix_tiles * kTileKeys * kCostPair;
+            h = (int)(x / p.head_a);
+            u = p.lanes > 1 ? lane : min((int)((x - h * p.head_a) / pair), p.pairs - 1);
+            w0 = h * p.head_a + (p.lanes > 1 ? 0 : u * pair);
+        } else if (x >= p.work_t) {
             more = false;
             return;
-        }
-        if (x < p.work_a) {
-            zone = 0;
-            h = (int)(x / p.head_a);
-            const long long pair = (long long)a.prefix_tiles * kTileKeys * kCostPair;
-            u = min((int)((x - h * p.head_a) / pair), p.pairs - 1);
-            w0 = h * p.head_a + u * pair;
-        } else if (x < p.work_a + p.work_c) {
+        } else if (x < p.work_c) {
             zone = 1;
-            const long long y = x - p.work_a;
-            b = warp_find(a.c_at, a.B, y);
+            b = warp_find(a.c_at, a.B, x);
             load_request();
-            const long long per = (a.c_at[b + 1] - a.c_at[b]) / a.Hkv, z = y - a.c_at[b];
+            const long long per = (a.c_at[b + 1] - a.c_at[b]) / a.Hkv, z = x - a.c_at[b];
             h = (int)(z / per);
             const long long rem = z - h * per, base = unit_base(a, n, len);
             const int D = 2 * a.tpt;
@@ -378,21 +393,33 @@ struct Walker {
             u = min(max(u, 0), units() - 1);
             while (u > 0 && units_before(base, D, u) > rem) --u;
             while (u + 1 < units() && units_before(base, D, u + 1) <= rem) ++u;
-            w0 = p.work_a + a.c_at[b] + h * per + units_before(base, D, u);
+            w0 = a.c_at[b] + h * per + units_before(base, D, u);
         } else {
             zone = 2;
-            const long long y = x - p.work_a - p.work_c;
+            const long long y = x - p.work_c;
             b = warp_find(a.b_at, a.B, y);
             load_request();
             set_cost();
             h = (int)((y - a.b_at[b]) / cost);
-            w0 = p.work_a + p.work_c + a.b_at[b] + h * cost;
+            w0 = p.work_c + a.b_at[b] + h * cost;
         }
         set_cost();
     }
     __device__ void start(int c) {
-        at = run_begin(p, c);
-        end = min(run_begin(p, c + 1), p.work_t);
+        zone = c < p.runs_a ? 0 : 1;
+        if (zone == 0) {
+            lane = c % p.lanes;
+            run = c / p.lanes;
+            at = run_begin(p.lane_a, p.cuts_a, run);
+            end = run_begin(p.lane_a, p.cuts_a, run + 1);
+        } else {
+            run = c - p.runs_a;
+            at = end = 0;
+            if (run < p.runs) {
+                at = run_begin(p.work, p.runs, run);
+                end = min(run_begin(p.work, p.runs, run + 1), p.work_t);
+            }
+        }
         more = at < end;
         if (more) locate(at);
     }
@@ -402,16 +429,25 @@ struct Walker {
             more = false;
             return;
         }
-        if (zone == 0 && u + 1 < p.pairs) { ++u; w0 = w1; set_cost(); return; }
-        if (zone == 0 && h + 1 < a.Hkv) { ++h; u = 0; w0 = w1; set_cost(); return; }
+        if (zone == 0) {
+            if (p.lanes > 1 || u + 1 == p.pairs) {
+                ++h;
+                u = p.lanes > 1 ? lane : 0;
+            } else {
+                ++u;
+            }
+            w0 = w1;
+            set_cost();
+            return;
+        }
         if (zone == 1 && u + 1 < units()) { ++u; w0 = w1; set_cost(); return; }
         if (zone == 1 && h + 1 < a.Hkv) { ++h; u = 0; w0 = w1; set_cost(); return; }
         if (zone == 2 && h + 1 < a.Hkv) { ++h; w0 = w1; return; }
         locate(w1);
     }
     // The item's tiles in the run; false when none begins there (tile k lies at w0 + 128 k rate).
-    __device__ bool segment(Segment& s, CutRecord& cut, int c) {
-        const int rate = (zone == 0 ? (u == p.pairs - 1 && (p.tiles & 1) ? kCostOne : kCostPair) : zone == 1 ? kCostPair : kCostOwn) * kTileKeys;
+    __device__ bool segment(Segment& s, CutRecord& cut) {
+        const int rate = (zone == 0 ? a_rate() : zone == 1 ? kCostPair : kCostOwn) * kTileKeys;
         s.h = h;
         s.b = b;
         s.obase = s.first = 0;
@@ -461,16 +497,17 @@ struct Walker {
         }
         s.end0 = min(max(s.end0, s.n0), s.n1);
         s.end1 = min(max(s.end1, s.n0), s.n1);
-        if (zone == 0) {
-            s.slot = h * p.pairs + u + c;  // (segments in order raise item or run by one: each slot has one)
+        if (zone == 0) {  // (segments of a lane in order raise item or run by one: each slot has one)
+            s.slot = ((p.lanes > 1 ? h : h * p.pairs + u) + run) * p.lanes + lane;
         } else if (zone == 2) {
-            s.slot = b * a.Hkv + h + c;
+            s.slot = b * a.Hkv + h + run;
         } else {
             s.kind = s.n0 == 0 && s.n1 == tiles ? kWholeItem : kCutItem;
-            s.slot = 2 * c + (s.n0 == 0);  // the run's first segment, or its last
+            s.slot = 2 * run + (s.n0 == 0);  // the run's first segment, or its last
             if (s.kind == kCutItem && s.n0 > 0) {
-                const int c0 = run_of(p, w0);
-                if (c0 == c - 1) cut = CutRecord{1, h, s.tok0, s.tok1, s.toks0, s.toks1, c0, run_of(p, w0 + (long long)(tiles - 1) * rate)};
+                const int c0 = run_of(p.work, p.runs, w0);
+                if (c0 == run - 1)
+                    cut = CutRecord{1, h, s.tok0, s.tok1, s.toks0, s.toks1, c0, run_of(p.work, p.runs, w0 + (long long)(tiles - 1) * rate)};
             }
         }
         return true;
@@ -558,10 +595,11 @@ struct FewWalk {
 
 template <int NT>
 __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, const PlanHead& p,
-                                         int c, int warp, uint32_t stages, uint8_t* stages_g, uint32_t bars, bool& failed,
+                                         int run, int warp, uint32_t stages, uint8_t* stages_g, uint32_t bars, bool& failed,
                                          int& bad) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const FewShare share = few_share(p, c);
+    if (run < 0 || run >= p.runs) return;
+    const FewShare share = few_share(p, run);
     if (share.hi <= share.lo) return;
     const int sub = warp - (kFewWarps - share.parts);
     if (sub < 0) return;
@@ -707,7 +745,7 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
             out.advance();
             load();
         }
-        const size_t slot = (size_t)now.b * a.Hkv + now.h + c * kFewWarps + warp;
+        const size_t slot = (size_t)now.b * a.Hkv + now.h + run * kFewWarps + warp;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -837,7 +875,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (fresh || n_next >= s.n1) {
                     if (!fresh) walk.step();
                     fresh = false;
-                    while (walk.more && !walk.segment(s, cut, blockIdx.x)) walk.step();
+                    while (walk.more && !walk.segment(s, cut)) walk.step();
                     if (!walk.more) return false;
                     s.flip = s.split ? flip : 0;  // (items of one tile in turn on both streams)
                     if (s.split) flip ^= (s.n1 - s.n0) & 1;
@@ -910,7 +948,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             s.kind = kEnd;
             send();
-            if (lane == 0) *reinterpret_cast<CutRecord*>(a.cut + 16 * blockIdx.x) = cut;
+            if (lane == 0 && blockIdx.x >= plan.runs_a) *reinterpret_cast<CutRecord*>(a.cut + 16 * walk.run) = cut;
             if (failed)  // see the copies in flight land before the CTA ends
                 for (int i = 0; i < kStages; ++i) {
                     const bool lap = i < kKeyStages ? i < (int)kr.stage : i - kKeyStages < (int)vr.stage;
@@ -1123,7 +1161,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int row_token = row / a.r;
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const PlanHead plan = *a.head;
-        const bool tiles = run_begin(plan, blockIdx.x) < plan.work_t;  // (a run of D alone does not wait for the queue)
+        // (a run of D alone does not wait for the queue)
+        const int other = (int)blockIdx.x - plan.runs_a;
+        const bool tiles = other < 0 || (other < plan.runs && run_begin(plan.work, plan.runs, other) < plan.work_t);
         while (tiles && receive(queue, true)) {
             const int toks = st ? s.toks1 : s.toks0, tok = st ? s.tok1 : s.tok0, stop = st ? s.end1 : s.end0;
             const bool live = row_token < toks;
@@ -1272,7 +1312,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // D: every stream's work of this CTA is done, its memory free
         named_bar_sync(1, 256);
         if (!failed)
-            few_rows<NT>(a, mk16, mv16, plan, blockIdx.x, warp, base + warp * kFewWarpBytes, gbase + warp * kFewWarpBytes,
+            few_rows<NT>(a, mk16, mv16, plan, (int)blockIdx.x - plan.runs_a, warp, base + warp * kFewWarpBytes, gbase + warp * kFewWarpBytes,
                          base + kOffFew + 8 * kFewStages * warp, failed, bad);
     }
     if (failed) bad |= HSQ_DEVERR_WAIT;
@@ -1302,10 +1342,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     const int group = warp % kJoinGroups, d0 = warp / kJoinGroups * kJoinDims;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PlanHead p = *a.head;
-    // the row's parts: n0 at o0 / ml0, n1 at o1 / ml1, `step` part rows apart
+    // the row's parts: n0 at o0 / ml0, n1 at o1 / ml1, step1 part rows apart
     const float *o0 = nullptr, *o1 = nullptr;
     const float2 *ml0 = nullptr, *ml1 = nullptr;
-    int n0 = 0, n1 = 0, step0 = 1, step1 = 1, pitch1 = kTileRows;
+    int n0 = 0, n1 = 0, step1 = 1, pitch1 = kTileRows;
+    bool both = false;  // the first parts are two streams' (of a pair of one tile)
+    int apart0 = 2;     // part rows between one run's first part and the next's
     bool live, by_row = false;  // by_row: the second parts' o has a row's dims side by side (D's)
     int h, token = 0, jj = 0;
     const bool brief = (int)blockIdx.x < short_ctas;
@@ -1327,20 +1369,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         __syncthreads();
         const int4 q = a.req[lo];
         const bool few = q.y * a.r <= kFewRows;
-        const long long at0 = few ? p.work_t + a.d_at[lo] : p.work_a + p.work_c + a.b_at[lo];
+        const long long at0 = few ? p.work_t + a.d_at[lo] : p.work_c + a.b_at[lo];
         token = q.x + at - q.w;
-        if (p.work_a > 0) {
+        if (p.lane_a > 0) {
             const int pair = tile >> 1, stream = tile & 1;
-            const bool split = tile == p.tiles - 1 && !stream;  // (a pair of one tile has its key tiles dealt to both streams)
+            both = tile == p.tiles - 1 && !stream;  // (a pair of one tile has its key tiles dealt to both streams)
             const long long keys = (long long)a.prefix_tiles * kTileKeys;
-            const int rate = (split ? kCostOne : kCostPair) * kTileKeys;
-            const long long w0 = h * p.head_a + pair * keys * kCostPair;
-            const int c0 = run_of(p, w0), c1 = run_of(p, w0 + (long long)(a.prefix_tiles - 1) * rate);
-            const size_t slot = ((size_t)h * p.pairs + pair + c0) * 2 + stream;
+            const int rate = (both && p.lanes == 1 ? kCostOne : kCostPair) * kTileKeys;
+            const long long w0 = h * p.head_a + (p.lanes > 1 ? 0 : pair * keys * kCostPair);
+            const int c0 = run_of(p.lane_a, p.cuts_a, w0), c1 = run_of(p.lane_a, p.cuts_a, w0 + (long long)(a.prefix_tiles - 1) * rate);
+            const int lane_of = p.lanes > 1 ? pair : 0;
+            const size_t slot = (((p.lanes > 1 ? h : (size_t)h * p.pairs + pair) + c0) * p.lanes + lane_of) * 2 + stream;
             o0 = a.a_o + slot * 128 * kTileRows + row;
             ml0 = a.a_ml + slot * kTileRows + row;
-            step0 = split ? 1 : 2;
-            n0 = (c1 - c0 + 1) * (split ? 2 : 1);
+            apart0 = 2 * p.lanes;
+            n0 = (c1 - c0 + 1) * (both ? 2 : 1);
         }
         const int orow = (at - q.w) * a.r + jj;
         if (q.z > 0 && few) {
@@ -1356,7 +1399,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             const long long cost = (long long)(q.z + kItemKeys) * kCostOwn;
             const long long w0 = at0 + h * cost;
             const int tiles = (q.z + kTileKeys - 1) / kTileKeys;
-            const int c0 = run_of(p, w0), c1 = run_of(p, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
+            const int c0 = run_of(p.work, p.runs, w0), c1 = run_of(p.work, p.runs, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
             const size_t slot = ((size_t)lo * a.Hkv + h + c0) * 2;
             pitch1 = a.own_rows;
             o1 = a.b_o + slot * 128 * pitch1 + orow;
@@ -1366,6 +1409,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     } else {
         // (few parts: the groups of warps take 32 rows each instead)
         const int e = blockIdx.x - short_ctas, c = 1 + (e >> 1), st = e & 1, row = group * 32 + lane;
+        if (c >= p.runs) return;
         const CutRecord cut = *reinterpret_cast<const CutRecord*>(a.cut + 16 * c);
         const int rows = (st ? cut.toks1 : cut.toks0) * a.r;
         if (!cut.valid) return;
@@ -1390,7 +1434,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
 #pragma unroll 2
     for (int k = brief ? group : 0; k < n; k += brief ? kJoinGroups : 1) {
         const bool second = k >= n0;
-        const size_t at = second ? (size_t)(k - n0) * step1 : (size_t)k * step0, pitch = second ? pitch1 : kTileRows;
+        const size_t at = second ? (size_t)(k - n0) * step1 : both ? (size_t)(k >> 1) * apart0 + (k & 1) : (size_t)k * apart0, pitch = second ? pitch1 : kTileRows;
         const float2 ml = __ldcg((second ? ml1 : ml0) + at * pitch);
         float v[kJoinDims];
         if (second && by_row) {
