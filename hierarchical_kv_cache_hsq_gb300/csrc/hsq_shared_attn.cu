@@ -58,9 +58,9 @@ constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which the maximum is taken anew
 // Cost of a key tile, per key: two row tiles (tensor cores), one row tile (A: tensor cores and loads; B: loads); and
 // what an item costs beside its tiles, in keys.
-constexpr int kCostPair = 8, kCostOne = 6, kCostOwn = 6, kItemKeys = 96;
+constexpr int kCostPair = 10, kCostOne = 8, kCostLong = 7, kCostOwn = 6, kItemKeys = 96;
 // D: requests of up to kFewRows rows; a group is 16 keys of one warp, kFewWarps warps share a CTA's run
-constexpr int kFewRows = 16, kFewWarps = 8, kCostFew = 6, kFewItemKeys = 64;
+constexpr int kFewRows = 16, kFewWarps = 8, kCostFew = 4, kFewItemKeys = 64;
 
 struct PlanHead {
     long long lane_a;                // A: length of a lane's line, and of one KV head's part of it
@@ -81,9 +81,13 @@ struct SharedArgs {
     int tpt;   // tokens of a row tile: 128 / r
     int runs;  // CTAs of the main kernel: an SM each
     int own_rows;  // rows that a B item's parts have room for
+    int tokens_cap;  // most tokens that short requests can have
     // workspace
     PlanHead* head;
     int4* req;              // [B] first row, rows, own tokens (checked), short tokens before it
+    int* of;                // [short tokens] their requests
+    int2 *a_dir, *b_dir;    // [item of A], [request, KV head]: first part row of the item's parts (A: in units of 128, others
+                            // of their slot's rows), number of parts; by the run with the item's last tile
     long long *c_at, *b_at, *d_at; // [B + 1] cost of the C, B and D items before request b
     int* cut;               // [runs][16 ints] the C item that run c is the second to work on (see CutRecord)
     // parts: o [slot][2 streams][128 dims][rows], ml [slot][2 streams][rows] (maximum of q.k, unscaled; sum)
@@ -118,13 +122,13 @@ __device__ __forceinline__ int few_warp_of(const PlanHead& p, long long x) {
     return i * kFewWarps + kFewWarps - s.parts + (int)(((x - s.lo + 1) * s.parts - 1) / (s.hi - s.lo));
 }
 
-// virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostPair a key
+// virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostLong a key
 __device__ __forceinline__ long long unit_base(const SharedArgs& a, int n, int len) {
     return (long long)a.prefix_tiles * kTileKeys + max(len - n, 0);
 }
 // cost of the units before u (u < number of units), D tokens each
 __device__ __forceinline__ long long units_before(long long base, int D, long long u) {
-    return kCostPair * (u * base + D * (u * (u + 1) / 2));
+    return kCostLong * (u * base + D * (u * (u + 1) / 2));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         if (!brief) {
             const int D = 2 * a.tpt, units = (n + D - 1) / D;
             const long long base = unit_base(a, n, len);
-            x[1] = a.Hkv * (units_before(base, D, units - 1) + kCostPair * (base + n));
+            x[1] = a.Hkv * (units_before(base, D, units - 1) + kCostLong * (base + n));
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -187,6 +191,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         }
         if (b < a.B) {
             a.req[b] = make_int4(first, n, len, (int)x[0]);
+            for (int i = 0; i < own[0]; ++i) a.of[x[0] + i] = b;
             a.c_at[b] = x[1];
             a.b_at[b] = x[2];
             a.d_at[b] = x[3];
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         const int rate = (h.tiles > 1 ? kCostPair : kCostOne) * kTileKeys;
         h.cuts_a = (int)min((long long)(ga / h.lanes), h.lane_a / rate);
         h.runs_a = h.cuts_a * h.lanes;
-        const int most = max(max(kCostPair, kCostOwn), kCostFew) * kTileKeys;
+        const int most = max(max(kCostLong, kCostOwn), kCostFew) * kTileKeys;
         h.runs = h.work > 0 ? (int)max(1LL, min((long long)(a.runs - ga), h.work / most)) : 0;
         *a.head = h;
         a.c_at[a.B] = before[1];
@@ -364,7 +369,7 @@ struct Walker {
             cost = (long long)a.prefix_tiles * kTileKeys * a_rate();
         } else if (zone == 1) {
             const long long base = unit_base(a, n, len);
-            cost = kCostPair * (base + min(n, (u + 1) * 2 * a.tpt));
+            cost = kCostLong * (base + min(n, (u + 1) * 2 * a.tpt));
         } else {
             cost = (long long)(len + kItemKeys) * kCostOwn;
         }
@@ -389,7 +394,7 @@ struct Walker {
             const int D = 2 * a.tpt;
             // units_before(u) <= rem: the quadratic's root, then exactly
             const double bq = base + 0.5 * D;
-            u = (int)((sqrt(bq * bq + 2.0 * D * (double)rem / kCostPair) - bq) / D);
+            u = (int)((sqrt(bq * bq + 2.0 * D * (double)rem / kCostLong) - bq) / D);
             u = min(max(u, 0), units() - 1);
             while (u > 0 && units_before(base, D, u) > rem) --u;
             while (u + 1 < units() && units_before(base, D, u + 1) <= rem) ++u;
@@ -447,7 +452,7 @@ struct Walker {
     }
     // The item's tiles in the run; false when none begins there (tile k lies at w0 + 128 k rate).
     __device__ bool segment(Segment& s, CutRecord& cut) {
-        const int rate = (zone == 0 ? a_rate() : zone == 1 ? kCostPair : kCostOwn) * kTileKeys;
+        const int rate = (zone == 0 ? a_rate() : zone == 1 ? kCostLong : kCostOwn) * kTileKeys;
         s.h = h;
         s.b = b;
         s.obase = s.first = 0;
@@ -497,10 +502,20 @@ struct Walker {
         }
         s.end0 = min(max(s.end0, s.n0), s.n1);
         s.end1 = min(max(s.end1, s.n0), s.n1);
+        const bool last = s.n1 == tiles && (threadIdx.x & 31) == 0;
         if (zone == 0) {  // (segments of a lane in order raise item or run by one: each slot has one)
-            s.slot = ((p.lanes > 1 ? h : h * p.pairs + u) + run) * p.lanes + lane;
+            const int item = p.lanes > 1 ? h : h * p.pairs + u;
+            s.slot = (item + run) * p.lanes + lane;
+            if (last) {
+                const int c0 = run_of(p.lane_a, p.cuts_a, w0);
+                a.a_dir[h * p.pairs + u] = make_int2(((item + c0) * p.lanes + lane) * 2, (run - c0 + 1) * (s.split ? 2 : 1));
+            }
         } else if (zone == 2) {
             s.slot = b * a.Hkv + h + run;
+            if (last) {
+                const int c0 = run_of(p.work, p.runs, w0);
+                a.b_dir[b * a.Hkv + h] = make_int2((b * a.Hkv + h + c0) * 2, 2 * (run - c0 + 1));
+            }
         } else {
             s.kind = s.n0 == 0 && s.n1 == tiles ? kWholeItem : kCutItem;
             s.slot = 2 * run + (s.n0 == 0);  // the run's first segment, or its last
@@ -763,6 +778,10 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
                     }
                 }
             }
+        if (lane == 0 && now.s1 == (now.len + 15) >> 4) {
+            const int v0 = few_warp_of(p, now.w0);
+            a.b_dir[now.b * a.Hkv + now.h] = make_int2(now.b * a.Hkv + now.h + v0, run * kFewWarps + warp - v0 + 1);
+        }
         now.next_item();
     }
     if (failed)  // see the copies in flight land before the CTA ends
@@ -1117,13 +1136,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                         for (int i0 = 0; i0 < toks; i0 += 32) {
                             int row = -1;
-                            if (i0 + lane < toks) {  // the request of packed token tok + i: the last that begins at or before it
-                                int lo = 0, hi = a.B;
-                                while (hi - lo > 1) {
-                                    const int mid = (lo + hi) >> 1;
-                                    if (a.req[mid].w <= tok + i0 + lane) lo = mid; else hi = mid;
-                                }
-                                const int4 q = a.req[lo];
+                            if (i0 + lane < toks) {
+                                const int4 q = a.req[a.of[tok + i0 + lane]];
                                 row = q.x + tok + i0 + lane - q.w;
                             }
                             const int chunks = min(32, toks - i0) * a.r * 16;
@@ -1326,97 +1340,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------------
-// Join.  A CTA takes 32 rows: of a tile of the short requests' tokens (parts of A and B), or of a row tile of a
-// C item that a cut divides.  Lane = row; four groups of warps deal the parts among them, a warp of a group
-// takes 32 dims: parts are read in whole lines, 32 loads at a time, weights are the lane's own.
+// Join.  A CTA takes 32 dims of 32 rows of a tile of the short requests' tokens (parts of A, and of B or D), or of
+// the 128 rows of a tile of a C item that a cut divides.  Lane = row; the warps deal the parts among them (for a
+// cut item, of few parts, the rows too), so that what a CTA waits for is the chain of its lookups and one or two
+// parts.  A's, B's and C's parts are read in whole lines.  Bound by latency.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kJoinWarps = 16, kJoinGroups = 4, kJoinDims = 128 / (kJoinWarps / kJoinGroups);
+constexpr int kJoinWarps = 16, kJoinGroups = 8, kJoinDims = 16;  // two warps of 16 dims a group
 
 __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __grid_constant__ SharedArgs a, int short_ctas) {
-    __shared__ __align__(16) float s_x[2][128][32];  // (first the requests' offsets: 4096 ints)
+    __shared__ float s_x[kJoinGroups][32][33];
     __shared__ float2 s_ml[kJoinGroups][32];
-    int* s_short = reinterpret_cast<int*>(&s_x[0][0][0]);
-    static_assert(sizeof(s_x) >= HSQ_MAX_REQUESTS * sizeof(int), "the offsets fit");
+    __shared__ long long s_to[4][32];
+    __shared__ float s_inv[4][32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int group = warp % kJoinGroups, d0 = warp / kJoinGroups * kJoinDims;
+    const int group = warp >> 1, quarter = blockIdx.x & 3, cta = blockIdx.x >> 2;
+    const int d_cta = 32 * quarter, d_warp = 16 * (warp & 1), d0 = d_cta + d_warp;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const PlanHead p = *a.head;
-    // the row's parts: n0 at o0 / ml0, n1 at o1 / ml1, step1 part rows apart
+    // row groups of 32 that the CTA has, and which this group of warps takes; of its parts it takes k0, k0 + dk, ...
+    const bool brief = cta < short_ctas;
+    const int row_groups = brief ? 1 : 4, mine = group % row_groups, k0 = group / row_groups, dk = kJoinGroups / row_groups;
+    // the row's parts: n0 at o0 / ml0 (128 rows a slot), n1 at o1 / ml1, step part rows apart
     const float *o0 = nullptr, *o1 = nullptr;
     const float2 *ml0 = nullptr, *ml1 = nullptr;
-    int n0 = 0, n1 = 0, step1 = 1, pitch1 = kTileRows;
-    bool both = false;  // the first parts are two streams' (of a pair of one tile)
-    int apart0 = 2;     // part rows between one run's first part and the next's
-    bool live, by_row = false;  // by_row: the second parts' o has a row's dims side by side (D's)
-    int h, token = 0, jj = 0;
-    const bool brief = (int)blockIdx.x < short_ctas;
+    int n0 = 0, n1 = 0, apart0 = 1, step1 = 1, pitch1 = kTileRows;
+    bool both = false, by_row = false;  // both: the first parts are two streams'; by_row: a row's dims lie side by side in o1
+    bool live;
+    size_t to = 0;
     if (brief) {
-        h = blockIdx.x % a.Hkv;
-        const int grp = blockIdx.x / a.Hkv, tile = grp >> 2, row = (grp & 3) * 32 + lane;
-        for (int i = tid; i < a.B; i += 32 * kJoinWarps) s_short[i] = a.req[i].w;
-        const int rows = min(a.tpt, p.tokens - tile * a.tpt) * a.r;
-        if ((grp & 3) * 32 >= rows) return;
-        __syncthreads();
-        live = row < rows;
-        const int at = tile * a.tpt + (live ? row : 0) / a.r;
-        jj = (live ? row : 0) % a.r;
-        int lo = 0, hi = a.B;  // the request: the last that begins at or before the token
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_short[mid] <= at) lo = mid; else hi = mid;
-        }
-        __syncthreads();
-        const int4 q = a.req[lo];
-        const bool few = q.y * a.r <= kFewRows;
-        const long long at0 = few ? p.work_t + a.d_at[lo] : p.work_c + a.b_at[lo];
-        token = q.x + at - q.w;
+        const int h = cta % a.Hkv, grp = cta / a.Hkv, tile = grp >> 2, row = (grp & 3) * 32 + lane;
+        const int at = tile * a.tpt + row / a.r;
+        const bool room = row < a.tpt * a.r;
+        const int b_any = a.of[min(at, a.tokens_cap - 1)];  // (looked up before it is known whether the row is in use)
+        const PlanHead p = *a.head;
+        live = room && at < p.tokens;
+        if (!__any_sync(kFull, live)) return;  // (the same for every warp)
+        const int b = live ? b_any : 0;
+        const int4 q = a.req[b];
+        const int2 own = a.b_dir[b * a.Hkv + h];
+        const int orow = live ? row - (q.w - tile * a.tpt) * a.r : 0;  // row among the request's
         if (p.lane_a > 0) {
-            const int pair = tile >> 1, stream = tile & 1;
+            const int2 x = a.a_dir[h * p.pairs + (tile >> 1)];
+            const int stream = tile & 1;
             both = tile == p.tiles - 1 && !stream;  // (a pair of one tile has its key tiles dealt to both streams)
-            const long long keys = (long long)a.prefix_tiles * kTileKeys;
-            const int rate = (both && p.lanes == 1 ? kCostOne : kCostPair) * kTileKeys;
-            const long long w0 = h * p.head_a + (p.lanes > 1 ? 0 : pair * keys * kCostPair);
-            const int c0 = run_of(p.lane_a, p.cuts_a, w0), c1 = run_of(p.lane_a, p.cuts_a, w0 + (long long)(a.prefix_tiles - 1) * rate);
-            const int lane_of = p.lanes > 1 ? pair : 0;
-            const size_t slot = (((p.lanes > 1 ? h : (size_t)h * p.pairs + pair) + c0) * p.lanes + lane_of) * 2 + stream;
-            o0 = a.a_o + slot * 128 * kTileRows + row;
-            ml0 = a.a_ml + slot * kTileRows + row;
+            o0 = a.a_o + (size_t)(x.x + stream) * 128 * kTileRows + row;
+            ml0 = a.a_ml + (size_t)(x.x + stream) * kTileRows + row;
             apart0 = 2 * p.lanes;
-            n0 = (c1 - c0 + 1) * (both ? 2 : 1);
+            n0 = x.y;
         }
-        const int orow = (at - q.w) * a.r + jj;
-        if (q.z > 0 && few) {
-            const long long w0 = at0 + h * few_cost(q.z);
-            const int v0 = few_warp_of(p, w0), v1 = few_warp_of(p, w0 + (long long)(((q.z + 15) >> 4) - 1) * 16 * kCostFew);
-            const size_t slot = (size_t)lo * a.Hkv + h + v0;
-            by_row = true;
-            pitch1 = a.few_rows;
-            o1 = a.d_o + (slot * a.few_rows + orow) * 128;
-            ml1 = a.d_ml + slot * a.few_rows + orow;
-            n1 = v1 - v0 + 1;
-        } else if (q.z > 0) {
-            const long long cost = (long long)(q.z + kItemKeys) * kCostOwn;
-            const long long w0 = at0 + h * cost;
-            const int tiles = (q.z + kTileKeys - 1) / kTileKeys;
-            const int c0 = run_of(p.work, p.runs, w0), c1 = run_of(p.work, p.runs, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
-            const size_t slot = ((size_t)lo * a.Hkv + h + c0) * 2;
-            pitch1 = a.own_rows;
-            o1 = a.b_o + slot * 128 * pitch1 + orow;
-            ml1 = a.b_ml + slot * pitch1 + orow;
-            n1 = 2 * (c1 - c0 + 1);
+        if (live && q.z > 0) {
+            by_row = q.y * a.r <= kFewRows;
+            pitch1 = by_row ? a.few_rows : a.own_rows;
+            o1 = by_row ? a.d_o + ((size_t)own.x * pitch1 + orow) * 128 : a.b_o + (size_t)own.x * 128 * pitch1 + orow;
+            ml1 = (by_row ? a.d_ml : a.b_ml) + (size_t)own.x * pitch1 + orow;
+            n1 = own.y;
         }
+        to = (size_t)(q.x + orow / a.r) * a.Hq + h * a.r + orow % a.r;
     } else {
-        // (few parts: the groups of warps take 32 rows each instead)
-        const int e = blockIdx.x - short_ctas, c = 1 + (e >> 1), st = e & 1, row = group * 32 + lane;
-        if (c >= p.runs) return;
+        const int e = cta - short_ctas, c = 1 + (e >> 1), st = e & 1, row = mine * 32 + lane;
+        if (c >= a.head->runs) return;
         const CutRecord cut = *reinterpret_cast<const CutRecord*>(a.cut + 16 * c);
-        const int rows = (st ? cut.toks1 : cut.toks0) * a.r;
         if (!cut.valid) return;
-        live = row < rows;
-        h = cut.h;
-        token = (st ? cut.tok1 : cut.tok0) + (live ? row : 0) / a.r;
-        jj = (live ? row : 0) % a.r;
+        live = row < (st ? cut.toks1 : cut.toks0) * a.r;
         // slot 2 c0 + 1, then 2 c0 + 2, 2 c0 + 4, ...
         const size_t s0 = (2 * (size_t)cut.c0 + 1) * 2 + st, s1 = (2 * (size_t)cut.c0 + 2) * 2 + st;
         o0 = a.c_o + s0 * 128 * kTileRows + row;
@@ -1426,15 +1411,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         ml1 = a.c_ml + s1 * kTileRows + row;
         step1 = 4;
         n1 = cut.c1 - cut.c0;
+        to = (size_t)((st ? cut.tok1 : cut.tok0) + row / a.r) * a.Hq + cut.h * a.r + row % a.r;
     }
     const int n = live ? n0 + n1 : 0;
     float M = -INFINITY, L = 0.f, x[kJoinDims];
 #pragma unroll
     for (int d = 0; d < kJoinDims; ++d) x[d] = 0.f;
 #pragma unroll 2
-    for (int k = brief ? group : 0; k < n; k += brief ? kJoinGroups : 1) {
+    for (int k = k0; k < n; k += dk) {
         const bool second = k >= n0;
-        const size_t at = second ? (size_t)(k - n0) * step1 : both ? (size_t)(k >> 1) * apart0 + (k & 1) : (size_t)k * apart0, pitch = second ? pitch1 : kTileRows;
+        const size_t at = second ? (size_t)(k - n0) * step1 : both ? (size_t)(k >> 1) * apart0 + (k & 1) : (size_t)k * apart0;
+        const size_t pitch = second ? pitch1 : kTileRows;
         const float2 ml = __ldcg((second ? ml1 : ml0) + at * pitch);
         float v[kJoinDims];
         if (second && by_row) {
@@ -1453,57 +1440,41 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
             for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + d * pitch);
         }
         if (ml.y > 0.f) {  // (a part without a key has no o)
-            const float to = fmaxf(M, ml.x);
-            const float was = M == -INFINITY ? 0.f : ex2_approx((M - to) * kLogitScaleLog2), w = ex2_approx((ml.x - to) * kLogitScaleLog2);
-            M = to;
+            const float top = fmaxf(M, ml.x);
+            const float was = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2), w = ex2_approx((ml.x - top) * kLogitScaleLog2);
+            M = top;
             L = fmaf(ml.y, w, L * was);
 #pragma unroll
             for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(v[d], w, x[d] * was);
         }
     }
-    float Mall = M, Lall = L;
-    if (brief) {
-        if (d0 == 0) s_ml[group][lane] = make_float2(M, L);
-        __syncthreads();
-        Mall = -INFINITY;
-        Lall = 0.f;
-#pragma unroll
-        for (int g = 0; g < kJoinGroups; ++g) Mall = fmaxf(Mall, s_ml[g][lane].x);
-#pragma unroll
-        for (int g = 0; g < kJoinGroups; ++g) {
-            const float2 ml = s_ml[g][lane];
-            if (ml.y > 0.f) Lall = fmaf(ml.y, ex2_approx((ml.x - Mall) * kLogitScaleLog2), Lall);
-        }
-        const float w = M == -INFINITY ? 0.f : ex2_approx((M - Mall) * kLogitScaleLog2);
-#pragma unroll
-        for (int d = 0; d < kJoinDims; ++d) x[d] *= w;
-        // groups 1 and 3 to 0 and 2, then 2 to 0
-        if (group & 1)
-            for (int d = 0; d < kJoinDims; ++d) s_x[group >> 1][d0 + d][lane] = x[d];
-        __syncthreads();
-        if (!(group & 1))
-#pragma unroll
-            for (int d = 0; d < kJoinDims; ++d) x[d] += s_x[group >> 1][d0 + d][lane];
-        __syncthreads();
-        if (group == 2)
-#pragma unroll
-            for (int d = 0; d < kJoinDims; ++d) s_x[0][d0 + d][lane] = x[d];
-        __syncthreads();
-        if (group == 0)
-#pragma unroll
-            for (int d = 0; d < kJoinDims; ++d) x[d] += s_x[0][d0 + d][lane];
+    if (d_warp == 0) s_ml[group][lane] = make_float2(M, L);
+    __syncthreads();
+    float top = -INFINITY, sum = 0.f;
+    for (int g = mine; g < kJoinGroups; g += row_groups) top = fmaxf(top, s_ml[g][lane].x);
+    for (int g = mine; g < kJoinGroups; g += row_groups) {
+        const float2 ml = s_ml[g][lane];
+        if (ml.y > 0.f) sum = fmaf(ml.y, ex2_approx((ml.x - top) * kLogitScaleLog2), sum);
     }
-    if ((group == 0 || !brief) && live) {
-        const float inv = Lall > 0.f ? 1.0f / Lall : 0.f;
-        const size_t to = (size_t)token * a.Hq + h * a.r + jj;
+    const float w = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2);
 #pragma unroll
-        for (int d = 0; d < kJoinDims; ++d) x[d] *= inv;
-        uint4* dst = reinterpret_cast<uint4*>(a.out + to * 128 + d0);
-#pragma unroll
-        for (int d = 0; d < kJoinDims; d += 8)
-            dst[d >> 3] = make_uint4(pack_bf16(x[d], x[d + 1]), pack_bf16(x[d + 2], x[d + 3]), pack_bf16(x[d + 4], x[d + 5]),
-                                     pack_bf16(x[d + 6], x[d + 7]));
-        if (d0 == 0 && a.lse) a.lse[to] = Lall > 0.f ? Mall * kRsqrtD + logf(Lall) : -INFINITY;
+    for (int d = 0; d < kJoinDims; ++d) s_x[group][lane][d_warp + d] = x[d] * w;
+    if (k0 == 0 && d_warp == 0) {
+        s_to[mine][lane] = live ? (long long)to : -1;
+        s_inv[mine][lane] = sum > 0.f ? 1.0f / sum : 0.f;
+        if (live && a.lse && quarter == 0) a.lse[to] = sum > 0.f ? top * kRsqrtD + logf(sum) : -INFINITY;
+    }
+    __syncthreads();
+    const int row = tid >> 4, d = 2 * (tid & 15);
+    for (int i = 0; i < row_groups; ++i) {
+        float y0 = 0.f, y1 = 0.f;
+        for (int g = i; g < kJoinGroups; g += row_groups) {
+            y0 += s_x[g][row][d];
+            y1 += s_x[g][row][d + 1];
+        }
+        const float inv = s_inv[i][row];
+        if (s_to[i][row] >= 0)
+            *reinterpret_cast<uint32_t*>(a.out + s_to[i][row] * 128 + d_cta + d) = pack_bf16(y0 * inv, y1 * inv);
     }
 }
 
@@ -1544,7 +1515,7 @@ bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint3
 }
 
 // The workspace's pieces and their offsets.
-struct Layout { size_t head, req, c_at, b_at, d_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, d_o, d_ml, bytes; int runs, own_rows, few_rows; };
+struct Layout { size_t head, req, of, a_dir, b_dir, c_at, b_at, d_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, d_o, d_ml, bytes; int runs, own_rows, few_rows, tokens; };
 
 Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new) {
     Layout x{};
@@ -1565,6 +1536,10 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     x.few_rows = (size_t)max_new * r <= 8 ? 8 : 16;
     x.cut = take((size_t)x.runs * 64);
     const size_t tokens = std::min<size_t>(rows, (size_t)B * tpt), tiles = (tokens + tpt - 1) / tpt;
+    x.tokens = (int)tokens;
+    x.of = take(tokens * 4);
+    x.a_dir = take(Hkv * ((tiles + 1) / 2) * 8);
+    x.b_dir = take((size_t)B * Hkv * 8);
     const size_t a = prefix_len > 0 ? Hkv * ((tiles + 1) / 2) + x.runs : 0, b = (size_t)max_new * r > kFewRows ? (size_t)B * Hkv + x.runs : 0;
     const size_t c = (size_t)max_new > tpt ? 2 * (size_t)x.runs : 0;
     x.a_o = take(a * 2 * 128 * kTileRows * 4);
@@ -1646,6 +1621,10 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     a.b_at = reinterpret_cast<long long*>(ws + x.b_at);
     a.d_at = reinterpret_cast<long long*>(ws + x.d_at);
     a.cut = reinterpret_cast<int*>(ws + x.cut);
+    a.of = reinterpret_cast<int*>(ws + x.of);
+    a.a_dir = reinterpret_cast<int2*>(ws + x.a_dir);
+    a.b_dir = reinterpret_cast<int2*>(ws + x.b_dir);
+    a.tokens_cap = x.tokens;
     a.a_o = reinterpret_cast<float*>(ws + x.a_o); a.a_ml = reinterpret_cast<float2*>(ws + x.a_ml);
     a.b_o = reinterpret_cast<float*>(ws + x.b_o); a.b_ml = reinterpret_cast<float2*>(ws + x.b_ml);
     a.c_o = reinterpret_cast<float*>(ws + x.c_o); a.c_ml = reinterpret_cast<float2*>(ws + x.c_ml);
@@ -1660,7 +1639,7 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
         !encode_rows(&mv16, pages->v, n, 16))
         return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int tiles = (int)((std::min<long long>(rows, (long long)B * tpt) + tpt - 1) / tpt);
+    const int tiles = (x.tokens + tpt - 1) / tpt;
     int short_ctas = 4 * tiles * Hkv;
     const int cut_ctas = max_new > tpt ? 2 * (x.runs - 1) : 0;
     void* plan_args[] = {&a};
@@ -1673,7 +1652,7 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
         return hsq::cuda_fail(ctx, e, "shared_attn plan");
     if ((e = launch(fn, x.runs, kTcThreads, kTcSmem, s, true, tc_args)) != cudaSuccess)
         return hsq::cuda_fail(ctx, e, "shared_attn");
-    e = launch((const void*)shared_join_kernel, short_ctas + cut_ctas, 32 * kJoinWarps, 0, s, true, join_args);
+    e = launch((const void*)shared_join_kernel, 4 * (short_ctas + cut_ctas), 32 * kJoinWarps, 0, s, true, join_args);
     if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn join");
     return HSQ_OK;
 }
