@@ -180,9 +180,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4; ++k) {  // (warps past the last request have nothing to add)
             long long t = before[k], mine = 0;
-            for (int w = 0; w < kPlanThreads / 32; ++w) {
+            for (int w = 0; w < min(kPlanThreads / 32, (a.B - b0 + 31) / 32); ++w) {
                 if (w == warp) mine = t;
                 t += s_w[k][w];
             }
@@ -829,6 +829,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == 9) {
         tmem_alloc(smem_addr((const void*)s_tmem), 512);
         tmem_relinquish();
+    }
+    if (warp == 11) {
+        // what the first copies will need, on its way while the plan is made (the page ids are not the plan kernel's)
+        if (lane < 5) {
+            const CUtensorMap* map = lane == 0 ? &mq : lane == 1 ? &mk : lane == 2 ? &mv : lane == 3 ? &mk16 : &mv16;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+        }
+        const int ahead = (a.prefix_len + a.page_n - 1) >> a.page_shift;
+        const long long lines_p = (ahead + 31) / 32, lines = lines_p + ((long long)a.B * a.width + 31) / 32;
+        for (long long i = blockIdx.x * 32 + lane, k = 0; i < lines && k < 4; i += gridDim.x * 32, ++k) {
+            const int32_t* at = i < lines_p ? a.prefix + 32 * i : a.table + 32 * (i - lines_p);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+        }
     }
     tc_fence_before();
     __syncthreads();
