@@ -493,9 +493,16 @@ def allocate_pages(ctx: Context, n_pages: int, page_n: int, device=None) -> Page
 
 def _need(pool: PagePool, dtype, **tensors):
     """Every tensor given is contiguous, of this type and on the pool's device."""
+    index = pool.index
     for name, x in tensors.items():
-        if x.dtype != dtype or x.get_device() != pool.index or not x.is_contiguous():
+        if x.dtype is not dtype or x.get_device() != index or not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous {dtype} on the pool's device")
+
+
+def _stream_on(pool: PagePool, stream) -> int:
+    """The given stream's handle, or the current one's of the pool's device."""
+    import torch
+    return torch.cuda.current_stream(pool.index).cuda_stream if stream is None else stream.cuda_stream
 
 
 def _need_heads(ctx: Context, pool: PagePool):
@@ -524,7 +531,7 @@ def hsq_page_tables(ctx: Context, pool: PagePool, cached, fresh, free_ids, used,
     st = ctx.lib.hsq_page_tables(ctx.handle, pool.ref, B, table.shape[1], rows, free_ids.numel(), base,
                                  cached.data_ptr(), fresh.data_ptr(), free_ids.data_ptr(), used.data_ptr(),
                                  table.data_ptr(), slots.data_ptr(), pos.data_ptr(), q_start.data_ptr(),
-                                 lens.data_ptr(), used_out.data_ptr(), _stream_handle(stream))
+                                 lens.data_ptr(), used_out.data_ptr(), _stream_on(pool, stream))
     if st:
         _check(st, ctx.handle)
 
@@ -564,7 +571,7 @@ def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, str
     st = ctx.lib.hsq_page_write(ctx.handle, pool.ref, rows, _ptr(q), k.data_ptr(), v.data_ptr(),
                                 0 if q is None else ctx.cfg.n_q_heads * 128 if one else q.stride(0),
                                 Hkv * 128 if one else k.stride(0), Hkv * 128 if one else v.stride(0), dt,
-                                pos.data_ptr(), slots.data_ptr(), _ptr(q_out), _stream_handle(stream))
+                                pos.data_ptr(), slots.data_ptr(), _ptr(q_out), _stream_on(pool, stream))
     if st:
         _check(st, ctx.handle)
 
@@ -610,7 +617,7 @@ def hsq_shared_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, out, 
                                  q_start.data_ptr(), lens.data_ptr(), table.data_ptr(),
                                  prefix.data_ptr() if prefix_len > 0 else None, out.data_ptr(), _ptr(lse),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                 _stream_handle(stream))
+                                 _stream_on(pool, stream))
     if st:
         _check(st, ctx.handle)
 

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "hsq_ctx.h"
 #include "hsq_device.cuh"
@@ -21,23 +22,26 @@ struct TablesArgs {
     int* err;
 };
 
-// Every CTA scans the lengths itself (B <= 4096: two loads and ten shuffles a
-// thread and round) and keeps both prefix sums -- rows, pages taken -- in
-// shared memory; then the grid strides over the rows and the new table entries,
-// each found by a binary search in them.  So one launch does without any
-// exchange between CTAs: nothing that one CTA reads is written by another (a
-// token's page is either an old entry of the table or, for a page taken in this
-// call, read from the free list itself).  Bound by its latency: launch, length
-// loads, scan, search.
+// Every CTA scans the lengths itself (B <= 4096: a round of 512 is two loads and ten
+// shuffles a thread) and keeps both prefix sums -- rows, pages taken -- and the cached
+// lengths in shared memory; then the grid strides over the rows and the new table
+// entries, each found by a binary search in them.  So one launch does without any
+// exchange between CTAs: nothing that one CTA reads is written by another (a token's
+// page is either an old entry of the table or, for a page taken in this call, read
+// from the free list itself).  Bound by its latency: launch, length loads, scan,
+// search, one more load.
 __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) {
     extern __shared__ int tab_sm[];
-    int* s_row = tab_sm;              // [B + 1] rows before request b
-    int* s_page = tab_sm + a.B + 1;   // [B + 1] pages taken before request b
-    __shared__ int s_wr[kTabThreads / 32], s_wp[kTabThreads / 32];
+    int* s_row = tab_sm;                 // [B + 1] rows before request b
+    int* s_page = s_row + a.B + 1;       // [B + 1] pages taken before request b
+    int* s_cached = s_page + a.B + 1;    // [B] cached lengths, checked
+    __shared__ int2 s_w[kTabThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int shift = __ffs(a.page_n) - 1;
     const bool first = blockIdx.x == 0;
-    int bad = 0, row0 = 0, page0 = 0;
+    int used = *a.used;
+    int bad = 0;
+    long long row0 = 0, page0 = 0;  // (before the round: saturating below, no sum wraps)
     for (int b0 = 0; b0 < a.B; b0 += kTabThreads) {
         const int b = b0 + tid;
         int c = 0, f = 0;
@@ -48,56 +52,66 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
             c = min(max(c, 0), kMaxLen);
             f = min(max(f, 0), kMaxLen - c);
             if ((c + f + a.page_n - 1) >> shift > a.width) bad |= HSQ_DEVERR_LEN;
+            s_cached[b] = c;
             if (first) a.lens[b] = c + f;
         }
-        // (no page is taken past the table's width; a request's rows saturate at the rows there are)
+        // No page is taken past the table's width; a request's rows saturate at the rows there are.  (A warp's sums
+        // saturate at 2^30, past which neither rows nor pages of a valid call reach.)
         const int xi = min(f, a.rows);
         const int yi = min((c + f + a.page_n - 1) >> shift, a.width) - min((c + a.page_n - 1) >> shift, a.width);
-        long long X = xi, Y = yi;
+        int x = xi, y = yi;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(kFull, X, o), w = __shfl_up_sync(kFull, Y, o);
-            if (lane >= o) { X += u; Y += w; }
+            const int u = __shfl_up_sync(kFull, x, o), w = __shfl_up_sync(kFull, y, o);
+            if (lane >= o) {
+                x = (int)min((long long)x + u, (long long)kMaxLen);
+                y = (int)min((long long)y + w, (long long)kMaxLen);
+            }
         }
-        if (lane == 31) {
-            s_wr[warp] = (int)min(X, (long long)INT_MAX);
-            s_wp[warp] = (int)min(Y, (long long)INT_MAX);
-        }
+        if (lane == 31) s_w[warp] = make_int2(x, y);
         __syncthreads();
-        long long tr = row0, tp = page0;
-        for (int w = 0; w < kTabThreads / 32; ++w) {
-            if (w == warp) { X += tr; Y += tp; }
-            tr += s_wr[w];
-            tp += s_wp[w];
+        long long tr = row0, tp = page0, X = x, Y = y;
+        const int warps = min(kTabThreads, a.B - b0 + 31) >> 5;
+        for (int w = 0; w < warps; ++w) {
+            if (w == warp) {
+                X += tr;
+                Y += tp;
+            }
+            const int2 v = s_w[w];
+            tr += v.x;
+            tp += v.y;
         }
         if (b < a.B) {
-            s_row[b] = (int)min(X - xi, (long long)a.rows);
-            s_page[b] = (int)min(Y - yi, (long long)INT_MAX);
+            s_row[b] = (int)min(max(X - xi, 0LL), (long long)a.rows);
+            s_page[b] = (int)min(max(Y - yi, 0LL), (long long)INT_MAX);
             if (X > a.rows) bad |= HSQ_DEVERR_LEN;
         }
-        row0 = (int)min(tr, (long long)a.rows);
-        page0 = (int)min(tp, (long long)INT_MAX);
+        row0 = min(tr, (long long)a.rows);
+        page0 = min(tp, (long long)INT_MAX);
         __syncthreads();
     }
+    const int rows = (int)row0, pages = (int)page0;
     if (tid == 0) {
-        s_row[a.B] = row0;
-        s_page[a.B] = page0;
+        s_row[a.B] = rows;
+        s_page[a.B] = pages;
     }
-    int used = *a.used;
     if (used < 0 || used > a.n_free) bad |= HSQ_DEVERR_LEN;
     used = min(max(used, 0), a.n_free);
-    if (page0 > a.n_free - used) bad |= HSQ_DEVERR_PAGE;
+    if (pages > a.n_free - used) bad |= HSQ_DEVERR_PAGE;
     __syncthreads();
     if (first) {
         for (int b = tid; b <= a.B; b += kTabThreads) a.q_start[b] = s_row[b];
-        if (tid == 0) *a.used_out = used + min(page0, a.n_free - used);
+        if (tid == 0) *a.used_out = used + min(pages, a.n_free - used);
     }
     // id of the e-th page taken in this call, -1 when the list is at its end or holds no page of the pool
     auto taken = [&](int e) {
         int id = -1;
         if (e < a.n_free - used) {
             id = a.free_ids[used + e];
-            if (id < 0 || id >= a.n_pages) { id = -1; bad |= HSQ_DEVERR_PAGE; }
+            if (id < 0 || id >= a.n_pages) {
+                id = -1;
+                bad |= HSQ_DEVERR_PAGE;
+            }
         }
         return id;
     };
@@ -110,18 +124,17 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
         return lo;
     };
     const int stride = gridDim.x * kTabThreads, at = blockIdx.x * kTabThreads + tid;
-    for (int e = at; e < page0; e += stride) {
+    for (int e = at; e < pages; e += stride) {
         const int b = find(s_page, e);
-        const int c = min(max(a.cached[b], 0), kMaxLen);
-        const int col = ((c + a.page_n - 1) >> shift) + e - s_page[b];
+        const int col = ((s_cached[b] + a.page_n - 1) >> shift) + e - s_page[b];
         if (col < a.width) a.table[(size_t)b * a.width + col] = taken(e);
     }
     for (int i = at; i < a.rows; i += stride) {
         long long slot = -1;
         int pos = -1;
-        if (i < row0) {
+        if (i < rows) {
             const int b = find(s_row, i);
-            const int c = min(max(a.cached[b], 0), kMaxLen);
+            const int c = s_cached[b];
             const int p = c + i - s_row[b], col = p >> shift, have = (c + a.page_n - 1) >> shift;
             int id = -1;
             if (col < a.width) {
@@ -129,7 +142,10 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
                     id = taken(s_page[b] + col - have);
                 } else {
                     id = a.table[(size_t)b * a.width + col];
-                    if (id < 0 || id >= a.n_pages) { id = -1; bad |= HSQ_DEVERR_PAGE; }
+                    if (id < 0 || id >= a.n_pages) {
+                        id = -1;
+                        bad |= HSQ_DEVERR_PAGE;
+                    }
                 }
             }
             pos = a.base + p;
@@ -141,14 +157,14 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
     if (bad) atomicOr(a.err, bad);
 }
 
-constexpr int kWriteHeads = 8;  // vectors of one row that a half-warp rotates with one set of angles
-
 struct WriteArgs {
     const void *q, *k, *v;
     long long qs, ks, vs;  // elements between rows
     const int32_t* pos; const int64_t* slots;
     uint16_t *q_out, *pk, *pv;
-    int rows, Hq, Hkv, n_pages, page_n, units;  // units: groups of kWriteHeads vectors of a row
+    int rows, Hq, Hkv, page_n, page_shift;
+    long long n_slots;
+    unsigned units;  // groups of V vectors of a row
     int* err;
 };
 
@@ -162,43 +178,76 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, const float v[8]) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d));
 }
 
-// One half-warp per (row, up to 8 of its Hq + 2 Hkv vectors): the row's cos / sin
-// once, then load, rotate, round, store.  Bound by HBM.
-template <bool BF>
+// One half-warp per (row, V of its Hq + 2 Hkv vectors): all V vectors' loads first,
+// then the row's position, slot, cos and sin (one set for the V vectors), then
+// rotate, round, store.  Bound by HBM for many rows: what is in flight decides, so V
+// is as many as registers hold; for few rows by latency, and V = 1 spreads them over the SMs.
+template <bool BF, int V>
 __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Tables tb) {
+    using Raw = typename std::conditional<BF, uint2, float4>::type;  // a lane's dims 4 l .. and 64 + 4 l ..
     const int l = hlane();
-    const long long unit = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4;
-    const int row = (int)(unit / a.units), g = (int)(unit % a.units);
+    const unsigned unit = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
+    const int row = (int)(unit / a.units), i0 = (int)(unit % a.units) * V;
     if (row >= a.rows) return;
+    const int H = a.Hq + 2 * a.Hkv;
+    Raw raw[V][2];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = i0 + j;
+        if (i < H) {
+            const bool is_q = i < a.Hq, is_v = i >= a.Hq + a.Hkv;
+            const int h = is_q ? i : is_v ? i - a.Hq - a.Hkv : i - a.Hq;
+            const long long at = (long long)row * (is_q ? a.qs : is_v ? a.vs : a.ks) + h * kDim;
+            const char* src = static_cast<const char*>(is_q ? a.q : is_v ? a.v : a.k) + at * (BF ? 2 : 4);
+            raw[j][0] = __ldcs(reinterpret_cast<const Raw*>(src) + l);
+            raw[j][1] = __ldcs(reinterpret_cast<const Raw*>(src + 64 * (BF ? 2 : 4)) + l);
+        }
+    }
     int p = a.pos[row];
+    long long slot = a.slots[row];
     if (p < 0) return;
     if (p >= tb.max_pos) {
         p = tb.max_pos - 1;
         if (l == 0) atomicOr(a.err, HSQ_DEVERR_POS);
     }
-    const int H = a.Hq + 2 * a.Hkv;
-    long long slot = a.slots[row];
-    if (slot >= (long long)a.n_pages * a.page_n) {
+    if (slot >= a.n_slots) {
         slot = -1;
         if (l == 0) atomicOr(a.err, HSQ_DEVERR_PAGE);
     }
     const RopeRows rr = rope_rows(p, tb);
-    const long long page = slot / a.page_n, off = slot % a.page_n;
-#pragma unroll 2
-    for (int i = g * kWriteHeads; i < min(H, (g + 1) * kWriteHeads); ++i) {
+    const size_t page = (size_t)(slot >> a.page_shift), off = (size_t)(slot & (a.page_n - 1));
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int i = i0 + j;
         const bool is_q = i < a.Hq, is_v = i >= a.Hq + a.Hkv;
-        if (!is_q && slot < 0) continue;
+        if (i >= H || (!is_q && slot < 0)) continue;
         const int h = is_q ? i : is_v ? i - a.Hq - a.Hkv : i - a.Hq;
-        const void* src = is_q ? a.q : is_v ? a.v : a.k;
-        const long long at = (long long)row * (is_q ? a.qs : is_v ? a.vs : a.ks) + (long long)h * kDim;
         float x[8];
-        if (BF) load_bf16x8(static_cast<const uint16_t*>(src) + at, x);
-        else load_f32x8(static_cast<const float*>(src) + at, x);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if constexpr (BF) {
+                x[4 * e] = __uint_as_float(raw[j][e].x << 16);
+                x[4 * e + 1] = __uint_as_float(raw[j][e].x & 0xFFFF0000u);
+                x[4 * e + 2] = __uint_as_float(raw[j][e].y << 16);
+                x[4 * e + 3] = __uint_as_float(raw[j][e].y & 0xFFFF0000u);
+            } else {
+                x[4 * e] = raw[j][e].x;
+                x[4 * e + 1] = raw[j][e].y;
+                x[4 * e + 2] = raw[j][e].z;
+                x[4 * e + 3] = raw[j][e].w;
+            }
+        }
         if (!is_v) rope_apply(x, rr);
-        uint16_t* dst = is_q ? a.q_out + ((size_t)row * a.Hq + h) * kDim
-                             : (is_v ? a.pv : a.pk) + (((size_t)page * a.Hkv + h) * a.page_n + off) * kDim;
-        store_bf16x8(dst, x);
+        store_bf16x8(is_q ? a.q_out + ((size_t)row * a.Hq + h) * kDim
+                          : (is_v ? a.pv : a.pk) + ((page * a.Hkv + h) * a.page_n + off) * kDim, x);
     }
+}
+
+template <bool BF, int V>
+void launch_write(WriteArgs a, const Tables& tb, cudaStream_t s) {
+    a.units = (a.Hq + 2 * a.Hkv + V - 1) / V;
+    const unsigned ctas = (unsigned)(((unsigned long long)a.rows * a.units + kHalves - 1) / kHalves);
+    page_write_kernel<BF, V><<<ctas, kThreads, 0, s>>>(a, tb);
 }
 
 }  // namespace
@@ -253,8 +302,11 @@ hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int widt
     TablesArgs a{cached, fresh, free_ids, used, table, slots, pos, q_start, lens, used_out,
                  B, width, rows, n_free, base, pages->n_pages, pages->page_n, ctx->d_err};
     const int grid = std::min(2 * ctx->num_sms, (rows + kTabThreads - 1) / kTabThreads);
-    page_tables_kernel<<<grid, kTabThreads, 8 * (B + 1), reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const size_t smem = 4 * (3 * (size_t)B + 2);
+    cudaError_t e = hsq::raise_smem_limit((const void*)page_tables_kernel, ctx->device, smem);
+    if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(page_tables)");
+    page_tables_kernel<<<grid, kTabThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    e = cudaGetLastError();
     return e == cudaSuccess ? HSQ_OK : hsq::cuda_fail(ctx, e, "page_tables");
 }
 
@@ -275,15 +327,23 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
         (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 15u))
         return hsq::fail(ctx, HSQ_ERR_INVALID, "rows of q, k, v and q_out must be 16-byte aligned");
     if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
-    const int units = (Hq + 2 * Hkv + kWriteHeads - 1) / kWriteHeads;
-    const long long ctas = ((long long)rows * units + kHalves - 1) / kHalves;
-    if (ctas > INT_MAX) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
+    const long long vectors = (long long)rows * (Hq + 2 * Hkv);
+    if (vectors >= (1LL << 31)) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
+    const int shift = pages->page_n == 16 ? 4 : pages->page_n == 32 ? 5 : pages->page_n == 64 ? 6 : 7;
     WriteArgs a{q, k, v, q_stride, k_stride, v_stride, pos, slots, static_cast<uint16_t*>(q_out),
-                static_cast<uint16_t*>(pages->k), static_cast<uint16_t*>(pages->v), rows, Hq, Hkv, pages->n_pages,
-                pages->page_n, units, ctx->d_err};
+                static_cast<uint16_t*>(pages->k), static_cast<uint16_t*>(pages->v), rows, Hq, Hkv, pages->page_n, shift,
+                (long long)pages->n_pages * pages->page_n, 0, ctx->d_err};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == HSQ_DTYPE_BF16) page_write_kernel<true><<<(int)ctas, kThreads, 0, s>>>(a, make_tables(ctx));
-    else page_write_kernel<false><<<(int)ctas, kThreads, 0, s>>>(a, make_tables(ctx));
+    const Tables tb = make_tables(ctx);
+    // one vector a half-warp until the GPU's warps (32 a SM) are all in use, then as many as fit its registers
+    const bool few = vectors <= 64LL * ctx->num_sms;
+    if (dtype == HSQ_DTYPE_BF16) {
+        if (few) launch_write<true, 1>(a, tb, s);
+        else launch_write<true, 8>(a, tb, s);
+    } else {
+        if (few) launch_write<false, 1>(a, tb, s);
+        else launch_write<false, 4>(a, tb, s);
+    }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HSQ_OK : hsq::cuda_fail(ctx, e, "page_write");
 }
