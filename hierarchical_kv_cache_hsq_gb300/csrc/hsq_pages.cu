@@ -164,7 +164,8 @@ struct WriteArgs {
     uint16_t *q_out, *pk, *pv;
     int rows, Hq, Hkv, page_n, page_shift;
     long long n_slots;
-    unsigned units;  // groups of V vectors of a row
+    unsigned units;          // units of a row: V heads each, of the queries, then keys, then values
+    int units_q, units_k;
     int* err;
 };
 
@@ -178,29 +179,32 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, const float v[8]) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d));
 }
 
-// One half-warp per (row, V of its Hq + 2 Hkv vectors): all V vectors' loads first,
-// then the row's position, slot, cos and sin (one set for the V vectors), then
-// rotate, round, store.  Bound by HBM for many rows: what is in flight decides, so V
-// is as many as registers hold; for few rows by latency, and V = 1 spreads them over the SMs.
+// One half-warp per (row, V neighbouring heads of its queries, keys or values): all V
+// vectors' loads first, then the row's position, slot, cos and sin (one set for the V
+// vectors), then rotate, round, store.  A unit has one kind of vectors, so that its
+// pointers are two bases and two strides (with the kind chosen vector by vector, address arithmetic
+// took half of the issue slots).  Bound by HBM for many rows, where reads and writes in flight
+// decide; for few rows by latency, and V = 1 spreads them over the SMs.
 template <bool BF, int V>
 __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Tables tb) {
     using Raw = typename std::conditional<BF, uint2, float4>::type;  // a lane's dims 4 l .. and 64 + 4 l ..
+    constexpr int kSize = BF ? 2 : 4;
     const int l = hlane();
     const unsigned unit = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
-    const int row = (int)(unit / a.units), i0 = (int)(unit % a.units) * V;
+    const unsigned row_u = unit / a.units;
+    const int row = (int)row_u, u = (int)(unit - row_u * a.units);
     if (row >= a.rows) return;
-    const int H = a.Hq + 2 * a.Hkv;
+    const bool is_q = u < a.units_q, is_v = u >= a.units_q + a.units_k;
+    const int h0 = (is_q ? u : is_v ? u - a.units_q - a.units_k : u - a.units_q) * V;
+    const int count = min(V, (is_q ? a.Hq : a.Hkv) - h0);
+    const char* src = static_cast<const char*>(is_q ? a.q : is_v ? a.v : a.k) +
+                      ((long long)row * (is_q ? a.qs : is_v ? a.vs : a.ks) + h0 * kDim) * kSize + l * sizeof(Raw);
     Raw raw[V][2];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int i = i0 + j;
-        if (i < H) {
-            const bool is_q = i < a.Hq, is_v = i >= a.Hq + a.Hkv;
-            const int h = is_q ? i : is_v ? i - a.Hq - a.Hkv : i - a.Hq;
-            const long long at = (long long)row * (is_q ? a.qs : is_v ? a.vs : a.ks) + h * kDim;
-            const char* src = static_cast<const char*>(is_q ? a.q : is_v ? a.v : a.k) + at * (BF ? 2 : 4);
-            raw[j][0] = __ldcs(reinterpret_cast<const Raw*>(src) + l);
-            raw[j][1] = __ldcs(reinterpret_cast<const Raw*>(src + 64 * (BF ? 2 : 4)) + l);
+        if (j < count) {
+            raw[j][0] = __ldg(reinterpret_cast<const Raw*>(src + j * (kDim * kSize)));
+            raw[j][1] = __ldg(reinterpret_cast<const Raw*>(src + j * (kDim * kSize) + 64 * kSize));
         }
     }
     int p = a.pos[row];
@@ -214,14 +218,26 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Table
         slot = -1;
         if (l == 0) atomicOr(a.err, HSQ_DEVERR_PAGE);
     }
-    const RopeRows rr = rope_rows(p, tb);
-    const size_t page = (size_t)(slot >> a.page_shift), off = (size_t)(slot & (a.page_n - 1));
+    if (!is_q && slot < 0) return;
+    uint16_t* dst;
+    int step = kDim;  // elements between the unit's heads
+    if (is_q) {
+        dst = a.q_out + ((size_t)row * a.Hq + h0) * kDim;
+    } else {
+        step = a.page_n * kDim;
+        dst = (is_v ? a.pv : a.pk) +
+              (((size_t)(slot >> a.page_shift) * a.Hkv + h0) * a.page_n + (size_t)(slot & (a.page_n - 1))) * kDim;
+    }
+    RopeRows rr;
+    if (!is_v) rr = rope_rows(p, tb);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int i = i0 + j;
-        const bool is_q = i < a.Hq, is_v = i >= a.Hq + a.Hkv;
-        if (i >= H || (!is_q && slot < 0)) continue;
-        const int h = is_q ? i : is_v ? i - a.Hq - a.Hkv : i - a.Hq;
+        if (j >= count) break;
+        if (BF && is_v) {
+            reinterpret_cast<Raw*>(dst + (size_t)j * step)[l] = raw[j][0];
+            reinterpret_cast<Raw*>(dst + (size_t)j * step + 64)[l] = raw[j][1];
+            continue;
+        }
         float x[8];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -238,14 +254,15 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Table
             }
         }
         if (!is_v) rope_apply(x, rr);
-        store_bf16x8(is_q ? a.q_out + ((size_t)row * a.Hq + h) * kDim
-                          : (is_v ? a.pv : a.pk) + ((page * a.Hkv + h) * a.page_n + off) * kDim, x);
+        store_bf16x8(dst + (size_t)j * step, x);
     }
 }
 
 template <bool BF, int V>
 void launch_write(WriteArgs a, const Tables& tb, cudaStream_t s) {
-    a.units = (a.Hq + 2 * a.Hkv + V - 1) / V;
+    a.units_q = (a.Hq + V - 1) / V;
+    a.units_k = (a.Hkv + V - 1) / V;
+    a.units = a.units_q + 2 * a.units_k;
     const unsigned ctas = (unsigned)(((unsigned long long)a.rows * a.units + kHalves - 1) / kHalves);
     page_write_kernel<BF, V><<<ctas, kThreads, 0, s>>>(a, tb);
 }
@@ -332,7 +349,7 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
     const int shift = pages->page_n == 16 ? 4 : pages->page_n == 32 ? 5 : pages->page_n == 64 ? 6 : 7;
     WriteArgs a{q, k, v, q_stride, k_stride, v_stride, pos, slots, static_cast<uint16_t*>(q_out),
                 static_cast<uint16_t*>(pages->k), static_cast<uint16_t*>(pages->v), rows, Hq, Hkv, pages->page_n, shift,
-                (long long)pages->n_pages * pages->page_n, 0, ctx->d_err};
+                (long long)pages->n_pages * pages->page_n, 0, 0, 0, ctx->d_err};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Tables tb = make_tables(ctx);
     // one vector a half-warp until the GPU's warps (32 a SM) are all in use, then as many as fit its registers
