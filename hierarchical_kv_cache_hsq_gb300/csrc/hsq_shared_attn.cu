@@ -86,8 +86,6 @@ struct SharedArgs {
     PlanHead* head;
     int4* req;              // [B] first row, rows, own tokens (checked), short tokens before it
     int* of;                // [short tokens] their requests
-    int2 *a_dir, *b_dir;    // [item of A], [request, KV head]: first part row of the item's parts (A: in units of 128, others
-                            // of their slot's rows), number of parts; by the run with the item's last tile
     long long *c_at, *b_at, *d_at; // [B + 1] cost of the C, B and D items before request b
     int* cut;               // [runs][16 ints] the C item that run c is the second to work on (see CutRecord)
     // parts: o [slot][2 streams][128 dims][rows], ml [slot][2 streams][rows] (maximum of q.k, unscaled; sum)
@@ -502,20 +500,10 @@ struct Walker {
         }
         s.end0 = min(max(s.end0, s.n0), s.n1);
         s.end1 = min(max(s.end1, s.n0), s.n1);
-        const bool last = s.n1 == tiles && (threadIdx.x & 31) == 0;
         if (zone == 0) {  // (segments of a lane in order raise item or run by one: each slot has one)
-            const int item = p.lanes > 1 ? h : h * p.pairs + u;
-            s.slot = (item + run) * p.lanes + lane;
-            if (last) {
-                const int c0 = run_of(p.lane_a, p.cuts_a, w0);
-                a.a_dir[h * p.pairs + u] = make_int2(((item + c0) * p.lanes + lane) * 2, (run - c0 + 1) * (s.split ? 2 : 1));
-            }
+            s.slot = ((p.lanes > 1 ? h : h * p.pairs + u) + run) * p.lanes + lane;
         } else if (zone == 2) {
             s.slot = b * a.Hkv + h + run;
-            if (last) {
-                const int c0 = run_of(p.work, p.runs, w0);
-                a.b_dir[b * a.Hkv + h] = make_int2((b * a.Hkv + h + c0) * 2, 2 * (run - c0 + 1));
-            }
         } else {
             s.kind = s.n0 == 0 && s.n1 == tiles ? kWholeItem : kCutItem;
             s.slot = 2 * run + (s.n0 == 0);  // the run's first segment, or its last
@@ -778,10 +766,6 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
                     }
                 }
             }
-        if (lane == 0 && now.s1 == (now.len + 15) >> 4) {
-            const int v0 = few_warp_of(p, now.w0);
-            a.b_dir[now.b * a.Hkv + now.h] = make_int2(now.b * a.Hkv + now.h + v0, run * kFewWarps + warp - v0 + 1);
-        }
         now.next_item();
     }
     if (failed)  // see the copies in flight land before the CTA ends
@@ -804,7 +788,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile uint32_t* s_mask = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask);
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffSeg + kQueue * kSegBytes);
     int bad = 0;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -877,6 +860,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (warp == 8) {
             // ---- the run's segments, and per key tile the K pages, then the V pages (lane i: page i of the tile) ----
             asm volatile("griddepcontrol.wait;" ::: "memory");
+            // (only now: so the join kernel, when it is scheduled, finds the plan complete)
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             KeyRing kr{0, 1};
             ValueRing vr{0, 1};
             Ring<kQueue> queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
@@ -1359,20 +1344,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // parts.  A's, B's and C's parts are read in whole lines.  Bound by latency.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kJoinWarps = 16, kJoinGroups = 8, kJoinDims = 16;  // two warps of 16 dims a group
+constexpr int kJoinDims = 16;  // of a warp; two warps a group
 
-__global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __grid_constant__ SharedArgs a, int short_ctas) {
-    __shared__ float s_x[kJoinGroups][32][33];
-    __shared__ float2 s_ml[kJoinGroups][32];
+// G groups of warps: 8, with the loads of two parts at once, where all CTAs are resident together; 4, four CTAs an
+// SM, where they are not (a second wave costs more than a third part: 16 requests 37 us with G = 8 and 40 with
+// 4, 128 requests 121 and 113).
+template <int G>
+__global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(const __grid_constant__ SharedArgs a, int short_ctas) {
+    __shared__ float s_x[G][32][33];
+    __shared__ float2 s_ml[G][32];
     __shared__ long long s_to[4][32];
     __shared__ float s_inv[4][32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = warp >> 1, quarter = blockIdx.x & 3, cta = blockIdx.x >> 2;
     const int d_cta = 32 * quarter, d_warp = 16 * (warp & 1), d0 = d_cta + d_warp;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // row groups of 32 that the CTA has, and which this group of warps takes; of its parts it takes k0, k0 + dk, ...
     const bool brief = cta < short_ctas;
-    const int row_groups = brief ? 1 : 4, mine = group % row_groups, k0 = group / row_groups, dk = kJoinGroups / row_groups;
+    const int row_groups = brief ? 1 : 4, mine = group % row_groups, k0 = group / row_groups, dk = G / row_groups;
     // the row's parts: n0 at o0 / ml0 (128 rows a slot), n1 at o1 / ml1, step part rows apart
     const float *o0 = nullptr, *o1 = nullptr;
     const float2 *ml0 = nullptr, *ml1 = nullptr;
@@ -1380,36 +1368,58 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     bool both = false, by_row = false;  // both: the first parts are two streams'; by_row: a row's dims lie side by side in o1
     bool live;
     size_t to = 0;
-    if (brief) {
+    if (brief) {  // (of the plan alone, complete before this kernel begins: looked up while the main kernel ends)
         const int h = cta % a.Hkv, grp = cta / a.Hkv, tile = grp >> 2, row = (grp & 3) * 32 + lane;
         const int at = tile * a.tpt + row / a.r;
         const bool room = row < a.tpt * a.r;
-        const int b_any = a.of[min(at, a.tokens_cap - 1)];  // (looked up before it is known whether the row is in use)
+        const int b_any = __ldcg(a.of + min(at, a.tokens_cap - 1));  // (before it is known whether the row is in use)
         const PlanHead p = *a.head;
         live = room && at < p.tokens;
-        if (!__any_sync(kFull, live)) return;  // (the same for every warp)
+        if (!__any_sync(kFull, live)) {  // (the same for every warp)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            return;
+        }
         const int b = live ? b_any : 0;
-        const int4 q = a.req[b];
-        const int2 own = a.b_dir[b * a.Hkv + h];
+        const int4 q = __ldcg(a.req + b);
+        const bool few = q.y * a.r <= kFewRows;
+        const long long at1 = few ? p.work_t + __ldcg(a.d_at + b) : p.work_c + __ldcg(a.b_at + b);
         const int orow = live ? row - (q.w - tile * a.tpt) * a.r : 0;  // row among the request's
         if (p.lane_a > 0) {
-            const int2 x = a.a_dir[h * p.pairs + (tile >> 1)];
-            const int stream = tile & 1;
+            const int pair = tile >> 1, stream = tile & 1;
             both = tile == p.tiles - 1 && !stream;  // (a pair of one tile has its key tiles dealt to both streams)
-            o0 = a.a_o + (size_t)(x.x + stream) * 128 * kTileRows + row;
-            ml0 = a.a_ml + (size_t)(x.x + stream) * kTileRows + row;
+            const long long keys = (long long)a.prefix_tiles * kTileKeys;
+            const int rate = (both && p.lanes == 1 ? kCostOne : kCostPair) * kTileKeys;
+            const long long w0 = h * p.head_a + (p.lanes > 1 ? 0 : pair * keys * kCostPair);
+            const int c0 = run_of(p.lane_a, p.cuts_a, w0), c1 = run_of(p.lane_a, p.cuts_a, w0 + (long long)(a.prefix_tiles - 1) * rate);
+            const size_t slot = (((p.lanes > 1 ? h : (size_t)h * p.pairs + pair) + c0) * p.lanes + (p.lanes > 1 ? pair : 0)) * 2 + stream;
+            o0 = a.a_o + slot * 128 * kTileRows + row;
+            ml0 = a.a_ml + slot * kTileRows + row;
             apart0 = 2 * p.lanes;
-            n0 = x.y;
+            n0 = (c1 - c0 + 1) * (both ? 2 : 1);
         }
-        if (live && q.z > 0) {
-            by_row = q.y * a.r <= kFewRows;
-            pitch1 = by_row ? a.few_rows : a.own_rows;
-            o1 = by_row ? a.d_o + ((size_t)own.x * pitch1 + orow) * 128 : a.b_o + (size_t)own.x * 128 * pitch1 + orow;
-            ml1 = (by_row ? a.d_ml : a.b_ml) + (size_t)own.x * pitch1 + orow;
-            n1 = own.y;
+        if (live && q.z > 0 && few) {
+            const long long w0 = at1 + h * few_cost(q.z);
+            const int v0 = few_warp_of(p, w0), v1 = few_warp_of(p, w0 + (long long)(((q.z + 15) >> 4) - 1) * 16 * kCostFew);
+            const size_t slot = (size_t)b * a.Hkv + h + v0;
+            by_row = true;
+            pitch1 = a.few_rows;
+            o1 = a.d_o + (slot * a.few_rows + orow) * 128;
+            ml1 = a.d_ml + slot * a.few_rows + orow;
+            n1 = v1 - v0 + 1;
+        } else if (live && q.z > 0) {
+            const long long w0 = at1 + h * ((long long)(q.z + kItemKeys) * kCostOwn);
+            const int tiles = (q.z + kTileKeys - 1) / kTileKeys;
+            const int c0 = run_of(p.work, p.runs, w0), c1 = run_of(p.work, p.runs, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
+            const size_t slot = ((size_t)b * a.Hkv + h + c0) * 2;
+            pitch1 = a.own_rows;
+            o1 = a.b_o + slot * 128 * pitch1 + orow;
+            ml1 = a.b_ml + slot * pitch1 + orow;
+            n1 = 2 * (c1 - c0 + 1);
         }
         to = (size_t)(q.x + orow / a.r) * a.Hq + h * a.r + orow % a.r;
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         const int e = cta - short_ctas, c = 1 + (e >> 1), st = e & 1, row = mine * 32 + lane;
         if (c >= a.head->runs) return;
         const CutRecord cut = *reinterpret_cast<const CutRecord*>(a.cut + 16 * c);
@@ -1430,13 +1440,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
     float M = -INFINITY, L = 0.f, x[kJoinDims];
 #pragma unroll
     for (int d = 0; d < kJoinDims; ++d) x[d] = 0.f;
-#pragma unroll 2
-    for (int k = k0; k < n; k += dk) {
+    auto place = [&](int k, size_t& at, size_t& pitch) {
         const bool second = k >= n0;
-        const size_t at = second ? (size_t)(k - n0) * step1 : both ? (size_t)(k >> 1) * apart0 + (k & 1) : (size_t)k * apart0;
-        const size_t pitch = second ? pitch1 : kTileRows;
-        const float2 ml = __ldcg((second ? ml1 : ml0) + at * pitch);
-        float v[kJoinDims];
+        at = second ? (size_t)(k - n0) * step1 : both ? (size_t)(k >> 1) * apart0 + (k & 1) : (size_t)k * apart0;
+        pitch = second ? pitch1 : kTileRows;
+        return second;
+    };
+    auto fetch = [&](int k, float2& ml, float (&v)[kJoinDims]) {
+        size_t at, pitch;
+        const bool second = place(k, at, pitch);
+        ml = __ldcg((second ? ml1 : ml0) + at * pitch);
         if (second && by_row) {
             const float4* o = reinterpret_cast<const float4*>(o1 + at * pitch * 128 + d0);
 #pragma unroll
@@ -1452,20 +1465,38 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
 #pragma unroll
             for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + d * pitch);
         }
-        if (ml.y > 0.f) {  // (a part without a key has no o)
-            const float top = fmaxf(M, ml.x);
-            const float was = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2), w = ex2_approx((ml.x - top) * kLogitScaleLog2);
-            M = top;
-            L = fmaf(ml.y, w, L * was);
+    };
+    auto add = [&](float2 ml, const float (&v)[kJoinDims]) {
+        if (!(ml.y > 0.f)) return;  // (a part without a key has no o)
+        const float top = fmaxf(M, ml.x);
+        const float was = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2), w = ex2_approx((ml.x - top) * kLogitScaleLog2);
+        M = top;
+        L = fmaf(ml.y, w, L * was);
 #pragma unroll
-            for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(v[d], w, x[d] * was);
+        for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(v[d], w, x[d] * was);
+    };
+    if constexpr (G == 8) {
+        for (int k = k0; k < n; k += 2 * dk) {
+            float2 ml_a, ml_b = make_float2(0.f, 0.f);
+            float v_a[kJoinDims], v_b[kJoinDims];
+            fetch(k, ml_a, v_a);
+            if (k + dk < n) fetch(k + dk, ml_b, v_b);
+            add(ml_a, v_a);
+            add(ml_b, v_b);
+        }
+    } else {
+        for (int k = k0; k < n; k += dk) {
+            float2 ml;
+            float v[kJoinDims];
+            fetch(k, ml, v);
+            add(ml, v);
         }
     }
     if (d_warp == 0) s_ml[group][lane] = make_float2(M, L);
     __syncthreads();
     float top = -INFINITY, sum = 0.f;
-    for (int g = mine; g < kJoinGroups; g += row_groups) top = fmaxf(top, s_ml[g][lane].x);
-    for (int g = mine; g < kJoinGroups; g += row_groups) {
+    for (int g = mine; g < G; g += row_groups) top = fmaxf(top, s_ml[g][lane].x);
+    for (int g = mine; g < G; g += row_groups) {
         const float2 ml = s_ml[g][lane];
         if (ml.y > 0.f) sum = fmaf(ml.y, ex2_approx((ml.x - top) * kLogitScaleLog2), sum);
     }
@@ -1478,10 +1509,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const __gr
         if (live && a.lse && quarter == 0) a.lse[to] = sum > 0.f ? top * kRsqrtD + logf(sum) : -INFINITY;
     }
     __syncthreads();
-    const int row = tid >> 4, d = 2 * (tid & 15);
-    for (int i = 0; i < row_groups; ++i) {
+    const int d = 2 * (tid & 15);
+    for (int e = tid >> 4; e < 32 * row_groups; e += 4 * G) {
+        const int i = e >> 5, row = e & 31;
         float y0 = 0.f, y1 = 0.f;
-        for (int g = i; g < kJoinGroups; g += row_groups) {
+        for (int g = i; g < G; g += row_groups) {
             y0 += s_x[g][row][d];
             y1 += s_x[g][row][d + 1];
         }
@@ -1528,7 +1560,7 @@ bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint3
 }
 
 // The workspace's pieces and their offsets.
-struct Layout { size_t head, req, of, a_dir, b_dir, c_at, b_at, d_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, d_o, d_ml, bytes; int runs, own_rows, few_rows, tokens; };
+struct Layout { size_t head, req, of, c_at, b_at, d_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, d_o, d_ml, bytes; int runs, own_rows, few_rows, tokens; };
 
 Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new) {
     Layout x{};
@@ -1551,8 +1583,6 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     const size_t tokens = std::min<size_t>(rows, (size_t)B * tpt), tiles = (tokens + tpt - 1) / tpt;
     x.tokens = (int)tokens;
     x.of = take(tokens * 4);
-    x.a_dir = take(Hkv * ((tiles + 1) / 2) * 8);
-    x.b_dir = take((size_t)B * Hkv * 8);
     const size_t a = prefix_len > 0 ? Hkv * ((tiles + 1) / 2) + x.runs : 0, b = (size_t)max_new * r > kFewRows ? (size_t)B * Hkv + x.runs : 0;
     const size_t c = (size_t)max_new > tpt ? 2 * (size_t)x.runs : 0;
     x.a_o = take(a * 2 * 128 * kTileRows * 4);
@@ -1635,8 +1665,6 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     a.d_at = reinterpret_cast<long long*>(ws + x.d_at);
     a.cut = reinterpret_cast<int*>(ws + x.cut);
     a.of = reinterpret_cast<int*>(ws + x.of);
-    a.a_dir = reinterpret_cast<int2*>(ws + x.a_dir);
-    a.b_dir = reinterpret_cast<int2*>(ws + x.b_dir);
     a.tokens_cap = x.tokens;
     a.a_o = reinterpret_cast<float*>(ws + x.a_o); a.a_ml = reinterpret_cast<float2*>(ws + x.a_ml);
     a.b_o = reinterpret_cast<float*>(ws + x.b_o); a.b_ml = reinterpret_cast<float2*>(ws + x.b_ml);
@@ -1665,7 +1693,9 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
         return hsq::cuda_fail(ctx, e, "shared_attn plan");
     if ((e = launch(fn, x.runs, kTcThreads, kTcSmem, s, true, tc_args)) != cudaSuccess)
         return hsq::cuda_fail(ctx, e, "shared_attn");
-    e = launch((const void*)shared_join_kernel, 4 * (short_ctas + cut_ctas), 32 * kJoinWarps, 0, s, true, join_args);
+    const int join_ctas = 4 * (short_ctas + cut_ctas);
+    e = join_ctas <= ctx->num_sms ? launch((const void*)shared_join_kernel<8>, join_ctas, 512, 0, s, true, join_args)
+                                  : launch((const void*)shared_join_kernel<4>, join_ctas, 256, 0, s, true, join_args);
     if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn join");
     return HSQ_OK;
 }
