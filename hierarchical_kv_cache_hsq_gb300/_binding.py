@@ -500,8 +500,11 @@ def _need(pool: PagePool, dtype, **tensors):
 
 
 def _stream_on(pool: PagePool, stream) -> int:
-    """The given stream's handle, or the current one's of the pool's device."""
+    """The given stream's handle, or the current one's; the pool has to be on the current device (as the
+    library holds the context to it)."""
     import torch
+    if torch.cuda.current_device() != pool.index:
+        raise ValueError("the pool is not on the current device")
     return torch.cuda.current_stream(pool.index).cuda_stream if stream is None else stream.cuda_stream
 
 

@@ -308,8 +308,8 @@ hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int widt
         return hsq::fail(ctx, HSQ_ERR_INVALID, "an argument of hsq_page_tables is NULL");
     if (B < 1 || B > ctx->cfg.max_batch || B > HSQ_MAX_REQUESTS)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "B outside [1, min(max_batch, HSQ_MAX_REQUESTS)]");
-    if (width < 1 || rows < 1 || n_free < 1 || base < 0)
-        return hsq::fail(ctx, HSQ_ERR_INVALID, "width, rows and n_free must be positive, base not negative");
+    if (width < 1 || rows < 1 || n_free < 1 || base < 0 || base >= kMaxLen)
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "width, rows and n_free must be positive, base in [0, 2^30)");
     const void* ins[] = {cached, fresh, free_ids, used};
     const void* outs[] = {table, slots, pos, q_start, lens, used_out};
     for (const void* i : ins)
@@ -336,6 +336,7 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
     if (!q != !q_out) return hsq::fail(ctx, HSQ_ERR_INVALID, "q and q_out go together");
     if (dtype != HSQ_DTYPE_F32 && dtype != HSQ_DTYPE_BF16) return hsq::fail(ctx, HSQ_ERR_INVALID, "bad dtype");
     if (rows < 1) return hsq::fail(ctx, HSQ_ERR_INVALID, "rows must be positive");
+    if (q && (q_out == q || q_out == k || q_out == v)) return hsq::fail(ctx, HSQ_ERR_INVALID, "q_out is an input");
     const int Hq = q ? ctx->cfg.n_q_heads : 0, Hkv = ctx->cfg.n_kv_heads;
     const int64_t unit = dtype == HSQ_DTYPE_BF16 ? 8 : 4;  // elements of 16 bytes
     if ((q && q_stride < (int64_t)Hq * 128) || k_stride < (int64_t)Hkv * 128 || v_stride < (int64_t)Hkv * 128)

@@ -139,19 +139,28 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ long long s_w[4][kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int bad = 0;
+    int bad = 0, disorder = 0;
     long long before[4] = {0, 0, 0, 0};  // short tokens, C, B and D cost
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
-        int first = 0, n = 0, len = 0;
+        int first = 0, n = 0, len = 0, l = 0;
+        bool wrong = false;
         if (b < a.B) {
-            const int s = a.q_start[b], e = a.q_start[b + 1], l = a.lens[b];
+            const int s = a.q_start[b], e = a.q_start[b + 1];
+            l = a.lens[b];
             first = s;
             n = e - s;
-            if (s < 0 || e < s || e > a.rows || n > a.max_new) {
-                bad |= HSQ_DEVERR_LEN;
-                first = n = 0;
-            }
+            wrong = s < 0 || e < s || e > a.rows || n > a.max_new;
+        }
+        // (no row may belong to two requests: the workspace has room for each row once)
+        if (disorder |= __syncthreads_or(wrong)) {
+            for (int c = 0; c < b && b < a.B; ++c) wrong |= a.q_start[c] > first && a.q_start[c] <= a.rows;
+        }
+        if (wrong) {
+            bad |= HSQ_DEVERR_LEN;
+            first = n = 0;
+        }
+        if (b < a.B) {
             len = (int)min((long long)max(l, 0), (long long)a.width << a.page_shift);
             if (len != l || len < n) bad |= HSQ_DEVERR_LEN;
         }
@@ -766,6 +775,7 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
                     }
                 }
             }
+        failed = __any_sync(kFull, failed);
         now.next_item();
     }
     if (failed)  // see the copies in flight land before the CTA ends
@@ -838,6 +848,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait_fast(seg_full + 8 * q.stage, q.phase, failed);
         const int4* src = reinterpret_cast<const int4*>(gbase + kOffSeg + q.stage * kSegBytes);
         int4* dst = reinterpret_cast<int4*>(&s);
+        if (release) failed = __any_sync(kFull, failed);  // (a warp stays together)
         if (failed) {
             s.kind = kEnd;
             return false;
@@ -1282,9 +1293,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (failed) break;
             tc_fence_after();
             if (s.kind == kWholeItem) {  // the result
-                const float inv = l > 0.f ? 1.0f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.0f / l;  // (a sum that is not a number shows in the result)
                 const size_t to = (size_t)(tok + row_token) * a.Hq + s.h * a.r + (row - row_token * a.r);
-                if (live && a.lse) a.lse[to] = l > 0.f ? m * kRsqrtD + logf(l) : -INFINITY;
+                if (live && a.lse) a.lse[to] = l == 0.f ? -INFINITY : m * kRsqrtD + logf(l);
                 if (!idle) {
 #pragma unroll 1
                     for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -1294,9 +1305,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             uint4* dst = reinterpret_cast<uint4*>(a.out + to * 128 + c0);
 #pragma unroll
                             for (int c = 0; c < 32; c += 8)
-                                dst[c >> 3] = l > 0.f ? make_uint4(pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
-                                                                   pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv))
-                                                      : make_uint4(0, 0, 0, 0);
+                                dst[c >> 3] = l == 0.f ? make_uint4(0, 0, 0, 0)
+                                                       : make_uint4(pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
+                                                                    pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv));
                         }
                     }
                 }
@@ -1467,7 +1478,7 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
         }
     };
     auto add = [&](float2 ml, const float (&v)[kJoinDims]) {
-        if (!(ml.y > 0.f)) return;  // (a part without a key has no o)
+        if (ml.y == 0.f) return;  // (a part without a key has no o)
         const float top = fmaxf(M, ml.x);
         const float was = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2), w = ex2_approx((ml.x - top) * kLogitScaleLog2);
         M = top;
@@ -1498,15 +1509,15 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
     for (int g = mine; g < G; g += row_groups) top = fmaxf(top, s_ml[g][lane].x);
     for (int g = mine; g < G; g += row_groups) {
         const float2 ml = s_ml[g][lane];
-        if (ml.y > 0.f) sum = fmaf(ml.y, ex2_approx((ml.x - top) * kLogitScaleLog2), sum);
+        if (ml.y != 0.f) sum = fmaf(ml.y, ex2_approx((ml.x - top) * kLogitScaleLog2), sum);
     }
     const float w = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2);
 #pragma unroll
     for (int d = 0; d < kJoinDims; ++d) s_x[group][lane][d_warp + d] = x[d] * w;
     if (k0 == 0 && d_warp == 0) {
         s_to[mine][lane] = live ? (long long)to : -1;
-        s_inv[mine][lane] = sum > 0.f ? 1.0f / sum : 0.f;
-        if (live && a.lse && quarter == 0) a.lse[to] = sum > 0.f ? top * kRsqrtD + logf(sum) : -INFINITY;
+        s_inv[mine][lane] = sum == 0.f ? 0.f : 1.0f / sum;
+        if (live && a.lse && quarter == 0) a.lse[to] = sum == 0.f ? -INFINITY : top * kRsqrtD + logf(sum);
     }
     __syncthreads();
     const int d = 2 * (tid & 15);
@@ -1619,8 +1630,9 @@ extern "C" {
 hsq_status hsq_shared_attn_workspace_size(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new,
                                           size_t* bytes) {
     if (!ctx || !bytes) return hsq::fail(nullptr, HSQ_ERR_INVALID, "ctx or bytes is NULL");
-    if (rows < 1 || B < 1 || B > HSQ_MAX_REQUESTS || prefix_len < 0 || max_new < 1)
-        return hsq::fail(nullptr, HSQ_ERR_INVALID, "rows, B (up to HSQ_MAX_REQUESTS) and max_new must be positive, prefix_len not negative");
+    if (rows < 1 || B < 1 || B > HSQ_MAX_REQUESTS || prefix_len < 0 || prefix_len > (1 << 30) || max_new < 1)
+        return hsq::fail(nullptr, HSQ_ERR_INVALID,
+                         "rows, B (up to HSQ_MAX_REQUESTS) and max_new must be positive, prefix_len in [0, 2^30]");
     *bytes = layout_of(ctx, rows, B, prefix_len, max_new).bytes;
     return HSQ_OK;
 }

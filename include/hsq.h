@@ -546,7 +546,7 @@ enum { HSQ_MAX_REQUESTS = 4096 };  /* largest B of the paged calls */
  *   (taken as that), tokens past the table's width (slot -1) or past `rows`
  *   (not listed: q_start stops at `rows`), *used outside [0, n_free].
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
- *   HSQ_MAX_REQUESTS)], width, rows or n_free < 1, base < 0, an
+ *   HSQ_MAX_REQUESTS)], width, rows or n_free < 1, base outside [0, 2^30), an
  *   output that is an input, another current device than the context's),
  *   HSQ_ERR_CUDA.
  */
@@ -563,11 +563,12 @@ hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int widt
  *   skipped whole.  A slot must not occur twice: it then holds parts of both rows.
  *   q: [rows][Hq][128] or NULL with q_out NULL; k, v: [rows][Hkv][128], of dtype,
  *   device memory, rows q_stride, k_stride, v_stride elements apart (views of one fused
- *   projection), 16-byte aligned rows.  q_out: [rows][Hq][128] bf16, 16-byte aligned.
+ *   projection), 16-byte aligned rows.  q_out: [rows][Hq][128] bf16, 16-byte aligned;
+ *   neither it nor the pool may overlap q, k or v.
  *   HSQ_DEVERR_POS: a position >= max_pos (clamped); HSQ_DEVERR_PAGE: a slot
  *   outside the pool (not stored).
- *   Errors: HSQ_ERR_INVALID (NULL, rows < 1, a stride below a row's length or
- *   alignment, another current device than the context's), HSQ_ERR_CUDA.
+ *   Errors: HSQ_ERR_INVALID (NULL, rows < 1, rows * (Hq + 2 Hkv) >= 2^31, a stride below
+ *   a row's length or alignment, q_out an input, another current device than the context's), HSQ_ERR_CUDA.
  */
 hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const void* q, const void* k, const void* v,
                           int64_t q_stride, int64_t k_stride, int64_t v_stride, hsq_dtype dtype,
@@ -591,16 +592,17 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
  *   aligned, caller-owned; its contents are not needed before or after, but calls that may run at the
  *   same time need one each.  Products are bf16 with fp32 accumulation; softmax
  *   weights are rounded to bf16 for the product with the values, sums and statistics are fp32.
- *   Keys and values of the tokens seen are expected finite: a value that is not may
- *   reach every row of its request (of the batch, when in the prefix).  What
- *   the pages hold past a request's length does not matter.
+ *   What the pages hold past a request's length does not matter.  Keys and values before
+ *   it are expected finite: a value that is not makes results of the rows that see it NaN, and may do so for every
+ *   row of its request (weights of 0 times infinity).  A logit of NaN gives a row of NaN.
  *   HSQ_DEVERR_PAGE: a page id outside the pool (its tokens are not attended to);
- *   HSQ_DEVERR_LEN: lens[b] above width * P, negative or below n_b (clamped), q_start not
- *   ascending in [0, rows] or n_b above max_new (that request's rows are not
- *   written); HSQ_DEVERR_WAIT as for hsq_prefill.
+ *   HSQ_DEVERR_LEN: lens[b] above width * P, negative (both clamped) or below n_b (the first rows see
+ *   the prefix only), q_start[b] .. q_start[b + 1] not ascending in [0, rows], below an earlier
+ *   offset or more than max_new rows (that request's rows are not written);
+ *   HSQ_DEVERR_WAIT: a bounded wait ran out, the results of the call are undefined.
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
- *   HSQ_MAX_REQUESTS)], rows, width or max_new < 1, prefix_len < 0, alignment, a
- *   small workspace, another current device than the context's), HSQ_ERR_CUDA.
+ *   HSQ_MAX_REQUESTS)], rows, width or max_new < 1, prefix_len outside [0, 2^30], width * P above
+ *   2^30, alignment, a small workspace, another current device than the context's), HSQ_ERR_CUDA.
  */
 hsq_status hsq_shared_attn_workspace_size(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new,
                                           size_t* bytes);
