@@ -71,6 +71,8 @@ struct PlanHead {
     int dense;                       // 1: the short requests' tokens are the rows [base, base + tokens)
     int base;
     int runs;                        // the others' CTAs: runs_a and up
+    long long each_a, each_w;        // lane_a / cuts_a, work / runs
+    int rest_a, rest_w;              // and their remainders
 };  // (no run is shorter than a tile, so that every run inside an item holds one)
 
 struct SharedArgs {
@@ -98,9 +100,23 @@ struct SharedArgs {
     int* err;
 };
 
-// the run that holds place w of a line, and where run i begins
-__device__ __forceinline__ int run_of(long long line, int runs, long long w) { return (int)(((w + 1) * runs - 1) / line); }
-__device__ __forceinline__ long long run_begin(long long line, int runs, int i) { return line * min(i, runs) / runs; }
+// n / d (n >= 0, d > 0) where the quotient is below 2^16: in float within one of it, then exactly.  (A 64-bit division
+// is some hundred instructions; the lookups here and in the join have a dozen of them.)
+__device__ __forceinline__ int small_quotient(long long n, long long d) {
+    const int q = (int)__fdividef((float)n, (float)d);
+    const long long rest = n - q * d;
+    return q + (rest >= d) - (rest < 0);
+}
+
+// A line cut into equal runs: the run that holds place w, and where run i begins (floor(line i / runs), from the
+// quotient and the remainder of line / runs).
+__device__ __forceinline__ int run_of(long long line, int runs, long long w) { return small_quotient((w + 1) * runs - 1, line); }
+__device__ __forceinline__ long long run_begin(long long each, int rest, int runs, int i) {
+    i = min(i, runs);
+    return each * i + (unsigned)(rest * i) / (unsigned)runs;
+}
+__device__ __forceinline__ long long a_begin(const PlanHead& p, int i) { return run_begin(p.each_a, p.rest_a, p.cuts_a, i); }
+__device__ __forceinline__ long long w_begin(const PlanHead& p, int i) { return run_begin(p.each_w, p.rest_w, p.runs, i); }
 
 __device__ __forceinline__ long long few_cost(int len) { return (long long)(((len + 15) >> 4) * 16 + kFewItemKeys) * kCostFew; }
 
@@ -109,15 +125,20 @@ __device__ __forceinline__ long long few_cost(int len) { return (long long)(((le
 struct FewShare { long long lo, hi; int parts; };
 __device__ __forceinline__ FewShare few_share(const PlanHead& p, int i) {  // i: of the others' runs
     FewShare s;
-    s.lo = max(run_begin(p.work, p.runs, i), p.work_t);
-    s.hi = run_begin(p.work, p.runs, i + 1);
-    s.parts = (int)max(1LL, min((long long)kFewWarps, (s.hi - s.lo) / (16 * kCostFew)));
+    s.lo = max(w_begin(p, i), p.work_t);
+    s.hi = w_begin(p, i + 1);
+    s.parts = max(1, (int)min((long long)kFewWarps, max(s.hi - s.lo, 0LL) / (16u * kCostFew)));
     return s;
+}
+// where part j begins: floor(length j / parts)
+__device__ __forceinline__ long long few_begin(const FewShare& s, int j) {
+    const long long n = s.hi - s.lo;  // (fewer parts than kFewWarps: the length is small)
+    return s.lo + (s.parts == kFewWarps ? n * j / kFewWarps : (long long)((unsigned)n * j / (unsigned)s.parts));
 }
 __device__ __forceinline__ int few_warp_of(const PlanHead& p, long long x) {
     const int i = run_of(p.work, p.runs, x);
     const FewShare s = few_share(p, i);
-    return i * kFewWarps + kFewWarps - s.parts + (int)(((x - s.lo + 1) * s.parts - 1) / (s.hi - s.lo));
+    return i * kFewWarps + kFewWarps - s.parts + small_quotient((x - s.lo + 1) * s.parts - 1, s.hi - s.lo);
 }
 
 // virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostLong a key
@@ -235,6 +256,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         h.runs_a = h.cuts_a * h.lanes;
         const int most = max(max(kCostLong, kCostOwn), kCostFew) * kTileKeys;
         h.runs = h.work > 0 ? (int)max(1LL, min((long long)(a.runs - ga), h.work / most)) : 0;
+        h.each_a = h.cuts_a ? h.lane_a / h.cuts_a : 0;
+        h.rest_a = h.cuts_a ? (int)(h.lane_a - h.each_a * h.cuts_a) : 0;
+        h.each_w = h.runs ? h.work / h.runs : 0;
+        h.rest_w = h.runs ? (int)(h.work - h.each_w * h.runs) : 0;
         *a.head = h;
         a.c_at[a.B] = before[1];
         a.b_at[a.B] = before[2];
@@ -385,7 +410,7 @@ struct Walker {
     __device__ void locate(long long x) {
         if (zone == 0) {
             const long long pair = (long long)a.prefix_tiles * kTileKeys * kCostPair;
-            h = (int)(x / p.head_a);
+            h = small_quotient(x, p.head_a);
             u = p.lanes > 1 ? lane : min((int)((x - h * p.head_a) / pair), p.pairs - 1);
             w0 = h * p.head_a + (p.lanes > 1 ? 0 : u * pair);
         } else if (x >= p.work_t) {
@@ -396,7 +421,7 @@ struct Walker {
             b = warp_find(a.c_at, a.B, x);
             load_request();
             const long long per = (a.c_at[b + 1] - a.c_at[b]) / a.Hkv, z = x - a.c_at[b];
-            h = (int)(z / per);
+            h = small_quotient(z, per);
             const long long rem = z - h * per, base = unit_base(a, n, len);
             const int D = 2 * a.tpt;
             // units_before(u) <= rem: the quadratic's root, then exactly
@@ -412,7 +437,7 @@ struct Walker {
             b = warp_find(a.b_at, a.B, y);
             load_request();
             set_cost();
-            h = (int)((y - a.b_at[b]) / cost);
+            h = small_quotient(y - a.b_at[b], cost);
             w0 = p.work_c + a.b_at[b] + h * cost;
         }
         set_cost();
@@ -422,14 +447,14 @@ struct Walker {
         if (zone == 0) {
             lane = c % p.lanes;
             run = c / p.lanes;
-            at = run_begin(p.lane_a, p.cuts_a, run);
-            end = run_begin(p.lane_a, p.cuts_a, run + 1);
+            at = a_begin(p, run);
+            end = a_begin(p, run + 1);
         } else {
             run = c - p.runs_a;
             at = end = 0;
             if (run < p.runs) {
-                at = run_begin(p.work, p.runs, run);
-                end = min(run_begin(p.work, p.runs, run + 1), p.work_t);
+                at = w_begin(p, run);
+                end = min(w_begin(p, run + 1), p.work_t);
             }
         }
         more = at < end;
@@ -460,6 +485,11 @@ struct Walker {
     // The item's tiles in the run; false when none begins there (tile k lies at w0 + 128 k rate).
     __device__ bool segment(Segment& s, CutRecord& cut) {
         const int rate = (zone == 0 ? a_rate() : zone == 1 ? kCostLong : kCostOwn) * kTileKeys;
+        auto tiles_from = [&](long long x) {  // ceil(x / rate), x > 0: divisions by constants
+            const unsigned long long y = x + rate - 1;
+            return (long long)(zone == 1 ? y / (kCostLong * kTileKeys) : zone == 2 ? y / (kCostOwn * kTileKeys)
+                               : rate == kCostPair * kTileKeys ? y / (kCostPair * kTileKeys) : y / (kCostOne * kTileKeys));
+        };
         s.h = h;
         s.b = b;
         s.obase = s.first = 0;
@@ -499,8 +529,8 @@ struct Walker {
             s.olen = len;
             s.end0 = s.end1 = tiles = (len + kTileKeys - 1) / kTileKeys;
         }
-        s.n0 = at <= w0 ? 0 : (int)((at - w0 + rate - 1) / rate);
-        s.n1 = w0 + (long long)tiles * rate <= end ? tiles : (int)min((long long)tiles, (end - w0 + rate - 1) / rate);
+        s.n0 = at <= w0 ? 0 : (int)tiles_from(at - w0);
+        s.n1 = w0 + (long long)tiles * rate <= end ? tiles : (int)min((long long)tiles, tiles_from(end - w0));
         if (tiles == 0) {  // (C only: rows that see nothing are written all the same, where the item begins)
             if (at > w0) return false;
             s.n0 = s.n1 = 0;
@@ -576,7 +606,7 @@ struct FewWalk {
         n = q.y;
         len = q.z;
         const long long z = x - p.work_t - a.d_at[b], cost = few_cost(len);
-        h = (int)(z / cost);
+        h = small_quotient(z, cost);
         w0 = x - z + h * cost;
     }
     __device__ __forceinline__ void take() {  // the item's groups, or the next item's that has some
@@ -616,8 +646,8 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
     const int sub = warp - (kFewWarps - share.parts);
     if (sub < 0) return;
     FewWalk ask{a, p};  // what is loaded next
-    ask.at = share.lo + (share.hi - share.lo) * sub / share.parts;
-    ask.end = share.lo + (share.hi - share.lo) * (sub + 1) / share.parts;
+    ask.at = few_begin(share, sub);
+    ask.end = few_begin(share, sub + 1);
     ask.more = ask.at < ask.end;
     if (!ask.more) return;
     ask.find(ask.at);
@@ -1186,7 +1216,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const PlanHead plan = *a.head;
         // (a run of D alone does not wait for the queue)
         const int other = (int)blockIdx.x - plan.runs_a;
-        const bool tiles = other < 0 || (other < plan.runs && run_begin(plan.work, plan.runs, other) < plan.work_t);
+        const bool tiles = other < 0 || (other < plan.runs && w_begin(plan, other) < plan.work_t);
         while (tiles && receive(queue, true)) {
             const int toks = st ? s.toks1 : s.toks0, tok = st ? s.tok1 : s.tok0, stop = st ? s.end1 : s.end0;
             const bool live = row_token < toks;
