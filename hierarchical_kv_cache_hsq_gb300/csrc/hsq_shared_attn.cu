@@ -58,7 +58,7 @@ constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which the maximum is taken anew
 // Cost of a key tile, per key: two row tiles (tensor cores), one row tile (A: tensor cores and loads; B: loads); and
 // what an item costs beside its tiles, in keys.
-constexpr int kCostPair = 10, kCostOne = 8, kCostLong = 7, kCostOwn = 6, kItemKeys = 96;
+constexpr int kCostPair = 10, kCostOne = 8, kCostLong = 7, kCostOwn = 6, kItemKeys = 96, kItemKeysA = 128;
 // D: requests of up to kFewRows rows; a group is 16 keys of one warp, kFewWarps warps share a CTA's run
 constexpr int kFewRows = 16, kFewWarps = 8, kCostFew = 4, kFewItemKeys = 64;
 
@@ -144,6 +144,10 @@ __device__ __forceinline__ int few_warp_of(const PlanHead& p, long long x) {
 // virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostLong a key
 __device__ __forceinline__ long long unit_base(const SharedArgs& a, int n, int len) {
     return (long long)a.prefix_tiles * kTileKeys + max(len - n, 0);
+}
+// virtual keys of an item of A (0: there is none)
+__device__ __forceinline__ long long a_keys(const SharedArgs& a) {
+    return a.prefix_tiles ? (long long)a.prefix_tiles * kTileKeys + kItemKeysA : 0;
 }
 // cost of the units before u (u < number of units), D tokens each
 __device__ __forceinline__ long long units_before(long long base, int D, long long u) {
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         h.tokens = (int)before[0];
         h.tiles = (h.tokens + a.tpt - 1) / a.tpt;
         h.pairs = (h.tiles + 1) >> 1;
-        const long long keys = (long long)a.prefix_tiles * kTileKeys;
+        const long long keys = a_keys(a);
         const long long full = h.tiles >> 1, one = h.tiles & 1;
         h.lanes = h.pairs <= 4 ? max(h.pairs, 1) : 1;
         // (lanes are cut alike, so a pair of one tile counts as a whole one there)
@@ -398,7 +402,7 @@ struct Walker {
     __device__ __forceinline__ int a_rate() const { return p.lanes == 1 && u == p.pairs - 1 && (p.tiles & 1) ? kCostOne : kCostPair; }
     __device__ __forceinline__ void set_cost() {
         if (zone == 0) {
-            cost = (long long)a.prefix_tiles * kTileKeys * a_rate();
+            cost = a_keys(a) * a_rate();
         } else if (zone == 1) {
             const long long base = unit_base(a, n, len);
             cost = kCostLong * (base + min(n, (u + 1) * 2 * a.tpt));
@@ -409,7 +413,7 @@ struct Walker {
     // the item that holds place x of the line
     __device__ void locate(long long x) {
         if (zone == 0) {
-            const long long pair = (long long)a.prefix_tiles * kTileKeys * kCostPair;
+            const long long pair = a_keys(a) * kCostPair;
             h = small_quotient(x, p.head_a);
             u = p.lanes > 1 ? lane : min((int)((x - h * p.head_a) / pair), p.pairs - 1);
             w0 = h * p.head_a + (p.lanes > 1 ? 0 : u * pair);
@@ -420,17 +424,18 @@ struct Walker {
             zone = 1;
             b = warp_find(a.c_at, a.B, x);
             load_request();
-            const long long per = (a.c_at[b + 1] - a.c_at[b]) / a.Hkv, z = x - a.c_at[b];
-            h = small_quotient(z, per);
-            const long long rem = z - h * per, base = unit_base(a, n, len);
             const int D = 2 * a.tpt;
-            // units_before(u) <= rem: the quadratic's root, then exactly
-            const double bq = base + 0.5 * D;
-            u = (int)((sqrt(bq * bq + 2.0 * D * (double)rem / kCostLong) - bq) / D);
+            const long long base = unit_base(a, n, len), at_b = a.c_at[b], z = x - at_b;
+            const long long per = units_before(base, D, units() - 1) + kCostLong * (base + n);  // a KV head's
+            h = small_quotient(z, per);
+            const long long rem = z - h * per;
+            // units_before(u) <= rem: the quadratic's root (as 2 c / (sqrt(b^2 + 2 D c) + b), which cancels nothing), then exactly
+            const float bq = (float)base + 0.5f * D, c = (float)rem / kCostLong;
+            u = (int)(2.f * c / (sqrtf(bq * bq + 2.f * D * c) + bq));
             u = min(max(u, 0), units() - 1);
             while (u > 0 && units_before(base, D, u) > rem) --u;
             while (u + 1 < units() && units_before(base, D, u + 1) <= rem) ++u;
-            w0 = a.c_at[b] + h * per + units_before(base, D, u);
+            w0 = at_b + h * per + units_before(base, D, u);
         } else {
             zone = 2;
             const long long y = x - p.work_c;
@@ -1386,16 +1391,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // ---------------------------------------------------------------------------------------
 
 constexpr int kJoinDims = 16;  // of a warp; two warps a group
+// A warp's part in flight: 16 dims of 32 rows, 2 KB (A, C: by dims, 128 bytes each; B, D: by rows, 64 bytes each, the
+// 16-byte chunks exchanged so that the lanes' reads meet no bank twice), and the rows' (m, l).
+constexpr int kJoinStage = 32 * kJoinDims * 4 + 32 * 8;
+template <int G> constexpr int kJoinStages = G == 8 ? 5 : 3;
+template <int G> constexpr int kJoinSmem = 2 * G * kJoinStages<G> * kJoinStage;
 
-// G groups of warps: 8, with the loads of two parts at once, where all CTAs are resident together; 4, four CTAs an
-// SM, where they are not (a second wave costs more than a third part: 16 requests 37 us with G = 8 and 40 with
-// 4, 128 requests 121 and 113).
+template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+
+// G groups of warps: 8 where all CTAs are resident together; 4, four CTAs an SM, where they are not.
 template <int G>
 __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(const __grid_constant__ SharedArgs a, int short_ctas) {
-    __shared__ float s_x[G][32][33];
-    __shared__ float2 s_ml[G][32];
-    __shared__ long long s_to[4][32];
-    __shared__ float s_inv[4][32];
+    constexpr int S = kJoinStages<G>;
+    extern __shared__ __align__(16) uint8_t join_sm[];
+    // (over the stages, when they have been read)
+    struct Reduce { float x[G][32][33]; float2 ml[G][32]; long long to[4][32]; float inv[4][32]; };
+    static_assert(sizeof(Reduce) <= kJoinSmem<G>, "the reduction fits the stages");
+    Reduce& sm = *reinterpret_cast<Reduce*>(join_sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = warp >> 1, quarter = blockIdx.x & 3, cta = blockIdx.x >> 2;
     const int d_cta = 32 * quarter, d_warp = 16 * (warp & 1), d0 = d_cta + d_warp;
@@ -1428,7 +1443,7 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
         if (p.lane_a > 0) {
             const int pair = tile >> 1, stream = tile & 1;
             both = tile == p.tiles - 1 && !stream;  // (a pair of one tile has its key tiles dealt to both streams)
-            const long long keys = (long long)a.prefix_tiles * kTileKeys;
+            const long long keys = a_keys(a);
             const int rate = (both && p.lanes == 1 ? kCostOne : kCostPair) * kTileKeys;
             const long long w0 = h * p.head_a + (p.lanes > 1 ? 0 : pair * keys * kCostPair);
             const int c0 = run_of(p.lane_a, p.cuts_a, w0), c1 = run_of(p.lane_a, p.cuts_a, w0 + (long long)(a.prefix_tiles - 1) * rate);
@@ -1477,76 +1492,98 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
         n1 = cut.c1 - cut.c0;
         to = (size_t)((st ? cut.tok1 : cut.tok0) + row / a.r) * a.Hq + cut.h * a.r + row % a.r;
     }
-    const int n = live ? n0 + n1 : 0;
+    if (!live) n1 = 0;
+    const int n = __reduce_max_sync(kFull, n0 + n1);  // (n0 is one for the tile)
+    const uint64_t o1_at = reinterpret_cast<uint64_t>(o1);
+    uint8_t* mine_g = join_sm + warp * S * kJoinStage;
+    const uint32_t mine_s = smem_addr(mine_g);
+    auto swizzled = [](int row, int chunk) { return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4); };
+    auto fetch = [&](int k, int stage) {  // part k on its way
+        const uint32_t dst = mine_s + stage * kJoinStage;
+        const bool first = k < n0;
+        const size_t at = !first ? (size_t)(k - n0) * step1 : both ? (size_t)(k >> 1) * apart0 + (k & 1) : (size_t)k * apart0;
+        if (first || !brief) {
+            const float* src = (first ? o0 : o1) - lane + (at * 128 + d0) * kTileRows;  // (of row 0 of the 32)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int dim = 4 * i + (lane >> 3), rows4 = 4 * (lane & 7);
+                copy_async<16>(dst + (dim * 32 + rows4) * 4, src + dim * kTileRows + rows4);
+            }
+            copy_async<8>(dst + 2048 + 8 * lane, (first ? ml0 : ml1) + at * kTileRows);
+            return;
+        }
+        const int rows_n = by_row ? n1 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2), chunk = lane & 3;
+            const float* src = reinterpret_cast<const float*>(__shfl_sync(kFull, o1_at, row)) + at * a.few_rows * 128 + d0 + 4 * chunk;
+            if (k - n0 < __shfl_sync(kFull, rows_n, row)) copy_async<16>(dst + swizzled(row, chunk), src);
+        }
+        if (k - n0 >= n1) return;
+        if (!by_row) {
+            const float* src = o1 + (at * 128 + d0) * pitch1;
+#pragma unroll
+            for (int d = 0; d < kJoinDims; ++d) copy_async<4>(dst + swizzled(lane, d >> 2) + 4 * (d & 3), src + d * pitch1);
+        }
+        copy_async<8>(dst + 2048 + 8 * lane, ml1 + at * pitch1);
+    };
     float M = -INFINITY, L = 0.f, x[kJoinDims];
 #pragma unroll
     for (int d = 0; d < kJoinDims; ++d) x[d] = 0.f;
-    auto place = [&](int k, size_t& at, size_t& pitch) {
-        const bool second = k >= n0;
-        at = second ? (size_t)(k - n0) * step1 : both ? (size_t)(k >> 1) * apart0 + (k & 1) : (size_t)k * apart0;
-        pitch = second ? pitch1 : kTileRows;
-        return second;
-    };
-    auto fetch = [&](int k, float2& ml, float (&v)[kJoinDims]) {
-        size_t at, pitch;
-        const bool second = place(k, at, pitch);
-        ml = __ldcg((second ? ml1 : ml0) + at * pitch);
-        if (second && by_row) {
-            const float4* o = reinterpret_cast<const float4*>(o1 + at * pitch * 128 + d0);
-#pragma unroll
-            for (int d = 0; d < kJoinDims; d += 4) {
-                const float4 y = __ldcg(o + (d >> 2));
-                v[d] = y.x;
-                v[d + 1] = y.y;
-                v[d + 2] = y.z;
-                v[d + 3] = y.w;
-            }
-        } else {
-            const float* o = (second ? o1 : o0) + (at * 128 + d0) * pitch;
-#pragma unroll
-            for (int d = 0; d < kJoinDims; ++d) v[d] = __ldcg(o + d * pitch);
-        }
-    };
-    auto add = [&](float2 ml, const float (&v)[kJoinDims]) {
+    auto add = [&](int k, int stage) {
+        const uint8_t* src = mine_g + stage * kJoinStage;
+        const bool first = k < n0;
+        if (!live || (!first && k - n0 >= n1)) return;
+        const float2 ml = reinterpret_cast<const float2*>(src + 2048)[lane];
         if (ml.y == 0.f) return;  // (a part without a key has no o)
         const float top = fmaxf(M, ml.x);
         const float was = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2), w = ex2_approx((ml.x - top) * kLogitScaleLog2);
         M = top;
         L = fmaf(ml.y, w, L * was);
+        if (first || !brief) {
 #pragma unroll
-        for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(v[d], w, x[d] * was);
+            for (int d = 0; d < kJoinDims; ++d) x[d] = fmaf(reinterpret_cast<const float*>(src)[32 * d + lane], w, x[d] * was);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kJoinDims / 4; ++c) {
+                const float4 y = *reinterpret_cast<const float4*>(src + swizzled(lane, c));
+                x[4 * c] = fmaf(y.x, w, x[4 * c] * was);
+                x[4 * c + 1] = fmaf(y.y, w, x[4 * c + 1] * was);
+                x[4 * c + 2] = fmaf(y.z, w, x[4 * c + 2] * was);
+                x[4 * c + 3] = fmaf(y.w, w, x[4 * c + 3] * was);
+            }
+        }
     };
-    if constexpr (G == 8) {
-        for (int k = k0; k < n; k += 2 * dk) {
-            float2 ml_a, ml_b = make_float2(0.f, 0.f);
-            float v_a[kJoinDims], v_b[kJoinDims];
-            fetch(k, ml_a, v_a);
-            if (k + dk < n) fetch(k + dk, ml_b, v_b);
-            add(ml_a, v_a);
-            add(ml_b, v_b);
-        }
-    } else {
-        for (int k = k0; k < n; k += dk) {
-            float2 ml;
-            float v[kJoinDims];
-            fetch(k, ml, v);
-            add(ml, v);
-        }
+    // S parts in flight a warp: their way from L2 is what the join waits for
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        if (k0 + i * dk < n) fetch(k0 + i * dk, i);
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
-    if (d_warp == 0) s_ml[group][lane] = make_float2(M, L);
+    for (int k = k0, stage = 0; k < n; k += dk) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(S - 1) : "memory");
+        __syncwarp();
+        add(k, stage);
+        __syncwarp();
+        if (k + S * dk < n) fetch(k + S * dk, stage);
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+        if (++stage == S) stage = 0;
+    }
+    __syncthreads();
+    if (d_warp == 0) sm.ml[group][lane] = make_float2(M, L);
     __syncthreads();
     float top = -INFINITY, sum = 0.f;
-    for (int g = mine; g < G; g += row_groups) top = fmaxf(top, s_ml[g][lane].x);
+    for (int g = mine; g < G; g += row_groups) top = fmaxf(top, sm.ml[g][lane].x);
     for (int g = mine; g < G; g += row_groups) {
-        const float2 ml = s_ml[g][lane];
+        const float2 ml = sm.ml[g][lane];
         if (ml.y != 0.f) sum = fmaf(ml.y, ex2_approx((ml.x - top) * kLogitScaleLog2), sum);
     }
     const float w = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLogitScaleLog2);
 #pragma unroll
-    for (int d = 0; d < kJoinDims; ++d) s_x[group][lane][d_warp + d] = x[d] * w;
+    for (int d = 0; d < kJoinDims; ++d) sm.x[group][lane][d_warp + d] = x[d] * w;
     if (k0 == 0 && d_warp == 0) {
-        s_to[mine][lane] = live ? (long long)to : -1;
-        s_inv[mine][lane] = sum == 0.f ? 0.f : 1.0f / sum;
+        sm.to[mine][lane] = live ? (long long)to : -1;
+        sm.inv[mine][lane] = sum == 0.f ? 0.f : 1.0f / sum;
         if (live && a.lse && quarter == 0) a.lse[to] = sum == 0.f ? -INFINITY : top * kRsqrtD + logf(sum);
     }
     __syncthreads();
@@ -1555,12 +1592,12 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
         const int i = e >> 5, row = e & 31;
         float y0 = 0.f, y1 = 0.f;
         for (int g = i; g < G; g += row_groups) {
-            y0 += s_x[g][row][d];
-            y1 += s_x[g][row][d + 1];
+            y0 += sm.x[g][row][d];
+            y1 += sm.x[g][row][d + 1];
         }
-        const float inv = s_inv[i][row];
-        if (s_to[i][row] >= 0)
-            *reinterpret_cast<uint32_t*>(a.out + s_to[i][row] * 128 + d_cta + d) = pack_bf16(y0 * inv, y1 * inv);
+        const float inv = sm.inv[i][row];
+        if (sm.to[i][row] >= 0)
+            *reinterpret_cast<uint32_t*>(a.out + sm.to[i][row] * 128 + d_cta + d) = pack_bf16(y0 * inv, y1 * inv);
     }
 }
 
@@ -1736,8 +1773,11 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     if ((e = launch(fn, x.runs, kTcThreads, kTcSmem, s, true, tc_args)) != cudaSuccess)
         return hsq::cuda_fail(ctx, e, "shared_attn");
     const int join_ctas = 4 * (short_ctas + cut_ctas);
-    e = join_ctas <= ctx->num_sms ? launch((const void*)shared_join_kernel<8>, join_ctas, 512, 0, s, true, join_args)
-                                  : launch((const void*)shared_join_kernel<4>, join_ctas, 256, 0, s, true, join_args);
+    const bool wide = join_ctas <= ctx->num_sms;
+    fn = wide ? (const void*)shared_join_kernel<8> : (const void*)shared_join_kernel<4>;
+    const size_t smem = wide ? kJoinSmem<8> : kJoinSmem<4>;
+    if ((e = hsq::raise_smem_limit(fn, ctx->device, smem)) == cudaSuccess)
+        e = launch(fn, join_ctas, wide ? 512 : 256, smem, s, true, join_args);
     if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "shared_attn join");
     return HSQ_OK;
 }
