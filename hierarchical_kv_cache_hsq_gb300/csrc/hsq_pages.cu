@@ -29,7 +29,7 @@ struct TablesArgs {
 // exchange between CTAs: nothing that one CTA reads is written by another (a token's
 // page is either an old entry of the table or, for a page taken in this call, read
 // from the free list itself).  Bound by its latency: launch, length loads, scan,
-// search, one more load.
+// search, one more load (6.2 us for 16 decodes, 8.3 us for 256 requests with some prompts among them).
 __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) {
     extern __shared__ int tab_sm[];
     int* s_row = tab_sm;                 // [B + 1] rows before request b
@@ -184,7 +184,9 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, const float v[8]) {
 // vectors), then rotate, round, store.  A unit has one kind of vectors, so that its
 // pointers are two bases and two strides (with the kind chosen vector by vector, address arithmetic
 // took half of the issue slots).  Bound by HBM for many rows, where reads and writes in flight
-// decide; for few rows by latency, and V = 1 spreads them over the SMs.
+// decide: a prompt of 32K tokens (32/8 heads, bf16, 806 MB) takes 121 us, 6.7 TB/s, 99 % of a plain copy's rate; with V = 1,
+// fewer loads in flight, 185.  For few rows by latency, and V = 1 spreads them over the SMs: 16 rows 4.2 us, with
+// V = 8 5.5.  (2531 float32 rows: 25.2 with V = 1, 23.7 with V = 4.)
 template <bool BF, int V>
 __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Tables tb) {
     using Raw = typename std::conditional<BF, uint2, float4>::type;  // a lane's dims 4 l .. and 64 + 4 l ..

@@ -56,8 +56,12 @@ using namespace hsq_tc;
 
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which the maximum is taken anew
-// Cost of a key tile, per key: two row tiles (tensor cores), one row tile (A: tensor cores and loads; B: loads); and
-// what an item costs beside its tiles, in keys.
+// Cost of a key tile, per key: of A for two row tiles (tensor cores) and for one (tensor cores and loads), of C, of
+// B (loads); and what an item of B or A costs beside its tiles, in keys (its epilogue; the start of its loads).  Set by
+// timing; one up or down, in us: pairs 112.8 / 107.6 / 109.0 (9, 10, 11) and D's groups below 114.3 / 107.6 / 116.4 (3, 4,
+// 5) for 128 requests over a prefix of 32K; one tile 97.5 instead of 91.9 (9, 8) for 8 requests with a chunk of 1000
+// among them; C 93.8 / 92.0 / 91.3 (6, 7, 8) for those and 361 / 359 / 359.5 for four prompts of 1024; A's items
+// without the 128 keys 38.1 instead of 36.4 for 16 requests over 8K.  (Runs of one build differ by 3 %.)
 constexpr int kCostPair = 10, kCostOne = 8, kCostLong = 7, kCostOwn = 6, kItemKeys = 96, kItemKeysA = 128;
 // D: requests of up to kFewRows rows; a group is 16 keys of one warp, kFewWarps warps share a CTA's run
 constexpr int kFewRows = 16, kFewWarps = 8, kCostFew = 4, kFewItemKeys = 64;
@@ -304,9 +308,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 
 // ---------------------------------------------------------------------------------------
 // Main kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7 (stream 1),
-// warp 8 walks the run and loads keys and values, warp 9 issues the MMAs, warp 10 loads the queries
-// (11 only gives its registers away: 168 a thread at launch, then 184 for the softmax
-// warps, whose row of logits lives in registers, and 136 for the others).
+// warp 8 walks the run and loads keys and values, warp 9 issues the MMAs (one elected thread), warp 10 loads
+// the queries, warp 11 fetches tensor maps and page ids ahead (168 registers a thread at launch, then 184 for the
+// softmax warps, whose row of logits lives in registers, and 136 for the others).
 // A stream is a 128-row query tile with its S / P and O in tensor memory.  The two streams
 // either hold two row tiles and share every key tile (so keys and values are loaded once
 // for 256 rows), or (split) hold the same rows and take the key tiles in turn.  While
@@ -314,6 +318,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 //   shared memory: a ring of three K tiles and one of two V tiles, 32 KB each (TMA, 128-byte swizzle; in
 //     one ring of five a key tile had to wait for the P V of three tiles before), two Q tiles;
 //   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
+// What it reaches: four prompts of 1024 over a prefix of 8192 (32/8 heads, 0.58 TFLOP) 343 us of the call's 358,
+// 1.70 PFLOP/s, the tensor pipe 75 % of the time active; bound by the pipe and by what a key tile costs beside it (a
+// 128 x 128 x 16 MMA takes 64 cycles in any of the forms used here, so a key tile of two row tiles 2048, 1.07 us at 1.9
+// GHz; it takes 1.43).  128 requests over 32K: 98 us for 500 MB, 5.1 TB/s, bound by HBM with some 25 us
+// of start and end.  Few requests (16 over 8K, 79 MB, 25 us): bound by the latencies of start, first loads and end.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kStages = kKeyStages + kValueStages, kQueue = 4;
@@ -570,7 +579,7 @@ struct Walker {
 //     transposes (movmatrix).
 // So no lane exchanges logits but for a new maximum, and up to 192 KB an SM are in flight.  Bound by HBM.  (On
 // the tensor cores' path a request of 4 rows costs what one of 128 does: 1.4 us a 128-key tile and as much
-// an item; with the fragments loaded straight into registers, 8 KB a warp in flight, a group took 1.8 us.)
+// an item, and 128 requests over 32K took 171 us instead of 142; with the fragments loaded straight into registers, 8 KB a warp in flight, a group took 1.8 us.)
 
 constexpr int kFewStages = 3;
 constexpr uint32_t kFewStageBytes = 16 * 256 * 2, kFewWarpBytes = kFewStages * kFewStageBytes;
@@ -1386,8 +1395,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // ---------------------------------------------------------------------------------------
 // Join.  A CTA takes 32 dims of 32 rows of a tile of the short requests' tokens (parts of A, and of B or D), or of
 // the 128 rows of a tile of a C item that a cut divides.  Lane = row; the warps deal the parts among them (for a
-// cut item, of few parts, the rows too), so that what a CTA waits for is the chain of its lookups and one or two
-// parts.  A's, B's and C's parts are read in whole lines.  Bound by latency.
+// cut item, of few parts, the rows too), each with several parts on their way by asynchronous copies, so that what a
+// CTA waits for is one or two ways from L2 (one part at a time in registers: 16 requests over 8K 38.5 us instead of 36.9, verification of 32 x 3
+// rows 48.8 instead of 48.0).  A's, B's and C's parts are read in whole lines.  Bound by latency: 5 to 10 us of a call.
+// (Joined by the CTA in which the item begins, where the other part is there by then: four prompts 384 us instead of
+// 357, the softmax's registers spilt.)
 // ---------------------------------------------------------------------------------------
 
 constexpr int kJoinDims = 16;  // of a warp; two warps a group
@@ -1402,7 +1414,8 @@ template <int N> __device__ __forceinline__ void copy_async(uint32_t dst, const 
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 
-// G groups of warps: 8 where all CTAs are resident together; 4, four CTAs an SM, where they are not.
+// G groups of warps: 8 where all CTAs are resident together, one an SM; 4, four CTAs an SM, where they are not (us with
+// G = 8 and 4: 4 requests over 1K 18.3 and 20.7, 16 over 8K 37 and 41; 61 over 5K 51 and 45, 128 over 32K 119 and 107).
 template <int G>
 __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(const __grid_constant__ SharedArgs a, int short_ctas) {
     constexpr int S = kJoinStages<G>;
