@@ -491,11 +491,12 @@ def allocate_pages(ctx: Context, n_pages: int, page_n: int, device=None) -> Page
                     torch.zeros(shape, dtype=torch.bfloat16, device=dev))
 
 
-def _need(pool: PagePool, dtype, **tensors):
-    """Every tensor given is contiguous, of this type and on the pool's device."""
+def _need(pool: PagePool, dtype, names: str, *tensors):
+    """Every tensor given is contiguous, of this type and on the pool's device (names: theirs, in order)."""
     index = pool.index
-    for name, x in tensors.items():
+    for x in tensors:
         if x.dtype is not dtype or x.get_device() != index or not x.is_contiguous():
+            name = next(n for n, y in zip(names.split(), tensors) if y is x)
             raise ValueError(f"{name} must be contiguous {dtype} on the pool's device")
 
 
@@ -505,7 +506,8 @@ def _stream_on(pool: PagePool, stream) -> int:
     import torch
     if torch.cuda.current_device() != pool.index:
         raise ValueError("the pool is not on the current device")
-    return torch.cuda.current_stream(pool.index).cuda_stream if stream is None else stream.cuda_stream
+    # (the handle alone: a Stream object around it takes 1 us of a call's 11)
+    return torch._C._cuda_getCurrentRawStream(pool.index) if stream is None else stream.cuda_stream
 
 
 def _need_heads(ctx: Context, pool: PagePool):
@@ -522,9 +524,9 @@ def hsq_page_tables(ctx: Context, pool: PagePool, cached, fresh, free_ids, used,
     q_start int32 [B + 1], lens int32 [B] and used_out int32 [1].  base: the
     position of a request's first own token (the shared prefix's length)."""
     import torch
-    _need(pool, torch.int32, cached=cached, fresh=fresh, free_ids=free_ids, used=used, table=table, pos=pos,
-          q_start=q_start, lens=lens, used_out=used_out)
-    _need(pool, torch.int64, slots=slots)
+    _need(pool, torch.int32, "cached fresh free_ids used table pos q_start lens used_out", cached, fresh, free_ids, used,
+          table, pos, q_start, lens, used_out)
+    _need(pool, torch.int64, "slots", slots)
     B = cached.numel()
     if fresh.numel() != B or lens.numel() != B or q_start.numel() != B + 1 or table.dim() != 2 or table.shape[0] != B:
         raise ValueError("fresh, lens [B], q_start [B + 1] and table [B, width] must agree with cached [B]")
@@ -546,8 +548,8 @@ def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, str
     (q and q_out may both be None).  Rows with pos < 0 are skipped; a slot < 0 stores nothing."""
     import torch
     _need_heads(ctx, pool)
-    _need(pool, torch.int32, pos=pos)
-    _need(pool, torch.int64, slots=slots)
+    _need(pool, torch.int32, "pos", pos)
+    _need(pool, torch.int64, "slots", slots)
     if k.dtype == torch.bfloat16:
         dt = HSQ_DTYPE_BF16
     elif k.dtype == torch.float32:
@@ -567,7 +569,7 @@ def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, str
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        _need(pool, torch.bfloat16, q_out=q_out)
+        _need(pool, torch.bfloat16, "q_out", q_out)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
     one = rows == 1  # (the row stride of a single row says nothing)
@@ -597,8 +599,8 @@ def hsq_shared_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, out, 
     hsq_shared_attn_workspace_size bytes, one for each call that may run at the same time."""
     import torch
     _need_heads(ctx, pool)
-    _need(pool, torch.bfloat16, q=q, out=out)
-    _need(pool, torch.int32, q_start=q_start, lens=lens, table=table)
+    _need(pool, torch.bfloat16, "q out", q, out)
+    _need(pool, torch.int32, "q_start lens table", q_start, lens, table)
     B, rows = lens.numel(), q.shape[0]
     if q.shape[1:] != (ctx.cfg.n_q_heads, 128) or out.shape != q.shape:
         raise ValueError("q and out must be [rows, Hq, 128]")
@@ -607,11 +609,11 @@ def hsq_shared_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, out, 
     if prefix_len > 0:
         if prefix is None:
             raise ValueError("prefix is None with prefix_len > 0")
-        _need(pool, torch.int32, prefix=prefix)
+        _need(pool, torch.int32, "prefix", prefix)
         if prefix.numel() * pool.page_n < prefix_len:
             raise ValueError("prefix has too few pages for prefix_len")
     if lse is not None:
-        _need(pool, torch.float32, lse=lse)
+        _need(pool, torch.float32, "lse", lse)
         if lse.shape != q.shape[:2]:
             raise ValueError("lse must be [rows, Hq]")
     if workspace.get_device() != pool.index or not workspace.is_contiguous():
