@@ -1733,6 +1733,8 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     if (prefix_len > 0 && !prefix) return hsq::fail(ctx, HSQ_ERR_INVALID, "prefix is NULL with prefix_len > 0");
     if (((uintptr_t)q | (uintptr_t)out) & 15u)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "q and out must be 16-byte aligned");
+    if (q == out || out == workspace || q == workspace || lse_opt == out || lse_opt == workspace)
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "an output or the workspace of hsq_shared_attn is another argument");
     if ((uintptr_t)workspace & 255u) return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace must be 256-byte aligned");
     const Layout x = layout_of(ctx, rows, B, prefix_len, max_new);
     if (workspace_bytes < x.bytes)

@@ -588,6 +588,7 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
  *   same shape and type; lse: [rows][Hq] f32 or NULL; q_start [B + 1], lens [B],
  *   table [B][width], prefix [ceil(prefix_len / P)] (NULL with prefix_len 0):
  *   int32; all device memory.  max_new: the largest n_b of the step.
+ *   out, lse and the workspace overlap neither each other nor an input.
  *   workspace: device memory of hsq_shared_attn_workspace_size bytes, 256-byte
  *   aligned, caller-owned; its contents are not needed before or after, but calls that may run at the
  *   same time need one each.  Products are bf16 with fp32 accumulation; softmax
@@ -602,7 +603,7 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
  *   HSQ_DEVERR_WAIT: a bounded wait ran out, the results of the call are undefined.
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
  *   HSQ_MAX_REQUESTS)], rows, width or max_new < 1, prefix_len outside [0, 2^30], width * P above
- *   2^30, alignment, a small workspace, another current device than the context's), HSQ_ERR_CUDA.
+ *   2^30, alignment, a small workspace, out or the workspace given twice, another current device than the context's), HSQ_ERR_CUDA.
  */
 hsq_status hsq_shared_attn_workspace_size(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new,
                                           size_t* bytes);

@@ -207,6 +207,10 @@ def test_more_refusals(monkeypatch):
         H.hsq_page_write(ctx, pool, **dict(w, q_out=w["q"]))
     with pytest.raises(H.HSQError):
         H.hsq_page_tables(ctx, pool, **t, base=1 << 30)
+    big = torch.zeros(ws.numel(), dtype=torch.bfloat16, device="cuda")
+    for change in (dict(out=a["q"]), dict(workspace=big, out=big[: 3 * 8 * 128].view(3, 8, 128))):
+        with pytest.raises(H.HSQError):
+            H.hsq_shared_attn(ctx, pool, **dict(a, **change))
     index = pool.index
     monkeypatch.setattr(torch.cuda, "current_device", lambda: index + 1)
     for call in (lambda: H.hsq_shared_attn(ctx, pool, **a), lambda: H.hsq_page_write(ctx, pool, **w),
@@ -215,3 +219,34 @@ def test_more_refusals(monkeypatch):
             call()
     monkeypatch.undo()
     assert word(ctx) == set()
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """Nothing that a call does once (limits, entry points, modules) breaks a capture."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import numpy as np, torch
+from test_gpu_paged import attn_inputs, check_attn, host, i32, make
+import hierarchical_kv_cache_hsq_gb300 as H
+x = attn_inputs(8, 2, 16, 300, [40, 9, 130], [1, 2, 100], seed=50)
+ctx = make(8, 2, 3)
+pool = H.PagePool(x["k"], x["v"])
+out, lse = torch.zeros_like(x["q"]), torch.zeros(x["q"].shape[:2], device="cuda")
+n = H.hsq_shared_attn_workspace_size(ctx, x["q"].shape[0], 3, 300, 100)
+args = (i32(x["q_start"]), i32(x["lens"]), i32(x["table"]), out, torch.empty(n, dtype=torch.uint8, device="cuda"))
+prefix = i32(x["prefix"])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    H.hsq_shared_attn(ctx, pool, x["q"], *args, prefix=prefix, prefix_len=300, max_new=100, lse=lse)
+g.replay()
+torch.cuda.synchronize()
+assert H.hsq_sync_status(ctx) == 0
+check_attn(x, host(out), host(lse))
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(here), capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)])))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
