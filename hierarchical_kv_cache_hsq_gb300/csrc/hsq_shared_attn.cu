@@ -309,8 +309,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // ---------------------------------------------------------------------------------------
 // Main kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7 (stream 1),
 // warp 8 walks the run and loads keys and values, warp 9 issues the MMAs (one elected thread), warp 10 loads
-// the queries, warp 11 fetches tensor maps and page ids ahead (168 registers a thread at launch, then 184 for the
-// softmax warps, whose row of logits lives in registers, and 136 for the others).
+// the queries, warp 11 fetches tensor maps and page ids ahead (168 registers a thread at launch, then 176 for the
+// softmax warps, whose row of logits lives in registers, and 152 for the others; four prompts 349 us, with 168 for all 357,
+// with 184 and 136, where the warps of 136 spill, 357).
 // A stream is a 128-row query tile with its S / P and O in tensor memory.  The two streams
 // either hold two row tiles and share every key tile (so keys and values are loaded once
 // for 256 rows), or (split) hold the same rows and take the key tiles in turn.  While
@@ -318,10 +319,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 //   shared memory: a ring of three K tiles and one of two V tiles, 32 KB each (TMA, 128-byte swizzle; in
 //     one ring of five a key tile had to wait for the P V of three tiles before), two Q tiles;
 //   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
-// What it reaches: four prompts of 1024 over a prefix of 8192 (32/8 heads, 0.58 TFLOP) 343 us of the call's 358,
-// 1.70 PFLOP/s, the tensor pipe 75 % of the time active; bound by the pipe and by what a key tile costs beside it (a
+// What it reaches: four prompts of 1024 over a prefix of 8192 (32/8 heads, 0.58 TFLOP) 335 us of the call's 349,
+// 1.74 PFLOP/s, the tensor pipe three quarters of the time active; bound by the pipe and by what a key tile costs beside it (a
 // 128 x 128 x 16 MMA takes 64 cycles in any of the forms used here, so a key tile of two row tiles 2048, 1.07 us at 1.9
-// GHz; it takes 1.43).  128 requests over 32K: 98 us for 500 MB, 5.1 TB/s, bound by HBM with some 25 us
+// GHz; it takes 1.4).  128 requests over 32K: 98 us for 500 MB, 5.1 TB/s, bound by HBM with some 25 us
 // of start and end.  Few requests (16 over 8K, 79 MB, 25 us): bound by the latencies of start, first loads and end.
 // ---------------------------------------------------------------------------------------
 
@@ -909,9 +910,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return s.kind != kEnd;
     };
 
-    // (128 x 168 x 3 registers at launch: 2 x 128 x 184 + 128 x 136)
+    // (128 x 168 x 3 registers at launch: 2 x 128 x 176 + 128 x 152)
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 136;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 152;\n");
         if (warp == 8) {
             // ---- the run's segments, and per key tile the K pages, then the V pages (lane i: page i of the tile) ----
             asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1217,7 +1218,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int st = 0; st < 2; ++st) mbar_wait(q_full + 8 * st, (q_par >> st) & 1, 1 << 12);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
         // ---- softmax: thread = row of its stream's tile ----
         const int st = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
