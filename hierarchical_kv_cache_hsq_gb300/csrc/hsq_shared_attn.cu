@@ -319,8 +319,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 //   shared memory: a ring of three K tiles and one of two V tiles, 32 KB each (TMA, 128-byte swizzle; in
 //     one ring of five a key tile had to wait for the P V of three tiles before), two Q tiles;
 //   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
-// What it reaches: four prompts of 1024 over a prefix of 8192 (32/8 heads, 0.58 TFLOP) 335 us of the call's 349,
-// 1.74 PFLOP/s, the tensor pipe three quarters of the time active; bound by the pipe and by what a key tile costs beside it (a
+// What it reaches: four prompts of 1024 over a prefix of 8192 (32/8 heads, 0.58 TFLOP) 340 us of the call's 349
+// to 359, 1.7 PFLOP/s, the tensor pipe 77 % of the time active; bound by the pipe and by what a key tile costs beside it (a
 // 128 x 128 x 16 MMA takes 64 cycles in any of the forms used here, so a key tile of two row tiles 2048, 1.07 us at 1.9
 // GHz; it takes 1.4).  128 requests over 32K: 98 us for 500 MB, 5.1 TB/s, bound by HBM with some 25 us
 // of start and end.  Few requests (16 over 8K, 79 MB, 25 us): bound by the latencies of start, first loads and end.
