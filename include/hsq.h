@@ -77,9 +77,9 @@ enum {
     HSQ_DEVERR_SEL = 1,       /* selection entry out of range or not ascending: treated as -1 */
     HSQ_DEVERR_POS = 2,       /* position outside [0, max_pos): clamped */
     HSQ_DEVERR_L1_OVER = 4,   /* more L1 tokens than max_l1: extra tokens dropped from L1 */
-    HSQ_DEVERR_WAIT = 8,      /* a bounded wait of the prefill attention kernel (on its bulk
-                                 copies or its tensor-core work) ran out: its output is not
-                                 written */
+    HSQ_DEVERR_WAIT = 8,      /* a bounded wait (on copies or tensor-core work) ran out: of the
+                                 prefill attention kernel, whose output is then not written, or
+                                 of hsq_shared_attn, whose results are then undefined */
     HSQ_DEVERR_GROW = 16,     /* hsq_append: the token leaving the recent window was not in L1
                                  (the cache was not encoded with that window): L1 left as is */
     HSQ_DEVERR_PAGE = 32,     /* paged calls: the free list ran out, or a page id or slot lies outside

@@ -19,6 +19,16 @@ def ensure_built():
         build.build()
 
 
+def waits_checked(read_word):
+    """hsq_sync_status that fails where the word says that a bounded wait ran out."""
+    def checked(ctx, stream=None):
+        import hierarchical_kv_cache_hsq_gb300 as H
+        w = read_word(ctx, stream)
+        assert not w & H.HSQ_DEVERR_WAIT, f"a bounded wait ran out (device error word {w})"
+        return w
+    return checked
+
+
 def make_ctx(w: W.Workload, beta: Optional[int] = None, max_l1: Optional[int] = None, n_splits: int = 0,
              steps: Optional[int] = None, B: Optional[int] = None):
     import hierarchical_kv_cache_hsq_gb300 as H
