@@ -310,8 +310,9 @@ hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int widt
         return hsq::fail(ctx, HSQ_ERR_INVALID, "an argument of hsq_page_tables is NULL");
     if (B < 1 || B > ctx->cfg.max_batch || B > HSQ_MAX_REQUESTS)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "B outside [1, min(max_batch, HSQ_MAX_REQUESTS)]");
-    if (width < 1 || rows < 1 || n_free < 1 || base < 0 || base >= kMaxLen)
-        return hsq::fail(ctx, HSQ_ERR_INVALID, "width, rows and n_free must be positive, base in [0, 2^30)");
+    // (past 2^30 the kernel's sums and its strides over rows and pages no longer fit 32 bits)
+    if (width < 1 || rows < 1 || rows >= kMaxLen || n_free < 1 || n_free >= kMaxLen || base < 0 || base >= kMaxLen)
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "width must be positive, rows and n_free in [1, 2^30), base in [0, 2^30)");
     const void* ins[] = {cached, fresh, free_ids, used};
     const void* outs[] = {table, slots, pos, q_start, lens, used_out};
     for (const void* i : ins)

@@ -546,7 +546,7 @@ enum { HSQ_MAX_REQUESTS = 4096 };  /* largest B of the paged calls */
  *   (taken as that), tokens past the table's width (slot -1) or past `rows`
  *   (not listed: q_start stops at `rows`), *used outside [0, n_free].
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
- *   HSQ_MAX_REQUESTS)], width, rows or n_free < 1, base outside [0, 2^30), an
+ *   HSQ_MAX_REQUESTS)], width < 1, rows or n_free outside [1, 2^30), base outside [0, 2^30), an
  *   output that is an input, another current device than the context's),
  *   HSQ_ERR_CUDA.
  */
