@@ -55,9 +55,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
             s_cached[b] = c;
             if (first) a.lens[b] = c + f;
         }
-        // No page is taken past the table's width; a request's rows saturate at the rows there are.  (A warp's sums
-        // saturate at 2^30, past which neither rows nor pages of a valid call reach.)
-        const int xi = min(f, a.rows);
+        // No page is taken past the table's width; a request's rows saturate just past the rows there are.  (A warp's
+        // sums saturate at 2^30, past which neither rows nor pages of a valid call reach.)
+        const int xi = min(f, a.rows + 1);
         const int yi = min((c + f + a.page_n - 1) >> shift, a.width) - min((c + a.page_n - 1) >> shift, a.width);
         int x = xi, y = yi;
 #pragma unroll

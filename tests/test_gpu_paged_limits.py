@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 from hsq_harness import ensure_built
-from test_gpu_paged import i32, i64, make, word
+from oracle import paged as P
+from test_gpu_paged import i32, i64, make, run_tables, word
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,13 @@ def test_tables_refuse_sizes_past_their_sums():
     for rows, n_free in ((1 << 30, 2), (2 ** 31 - 1, 2), (2, 1 << 30), (2, 2 ** 31 - 1), (0, 2), (2, 0)):
         assert call(rows, n_free) == 1, (rows, n_free)
     assert call(2, 2) == 0 and word(ctx) == set() and t[5].tolist() == [0, 16]
+
+
+@pytest.mark.parametrize("cached,fresh,rows", [([3], [50], 40), ([0, 7], [0, 41], 40), ([16, 1, 2], [50, 0, 0], 1), ([5, 6], [40, 1], 40)])
+def test_a_request_of_more_rows_than_there_are_is_flagged(cached, fresh, rows):
+    table = np.full((len(cached), 6), 2, np.int32)
+    want = P.page_tables(cached, fresh, np.arange(8), 3, table, rows, 16, 8)
+    got, err = run_tables(cached, fresh, np.arange(8), 3, table, rows, 16, 8)
+    assert err == want["err"] == {"LEN"}
+    for k in got:
+        np.testing.assert_array_equal(got[k].reshape(-1), np.asarray(want[k]).reshape(-1), err_msg=k)
