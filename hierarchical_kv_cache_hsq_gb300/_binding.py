@@ -522,7 +522,8 @@ def hsq_page_tables(ctx: Context, pool: PagePool, cached, fresh, free_ids, used,
     pool's free list and how much of it is taken.  Writes the new entries of table
     int32 [B, width], slots int64 and pos int32 [rows] (-1 behind the last row),
     q_start int32 [B + 1], lens int32 [B] and used_out int32 [1].  base: the
-    position of a request's first own token (the shared prefix's length)."""
+    position of a request's first own token (the shared prefix's length).
+    New tokens that find no row count as not brought (lens, table, used_out)."""
     import torch
     _need(pool, torch.int32, "cached fresh free_ids used table pos q_start lens used_out", cached, fresh, free_ids, used,
           table, pos, q_start, lens, used_out)

@@ -35,13 +35,15 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
     int* s_row = tab_sm;                 // [B + 1] rows before request b
     int* s_page = s_row + a.B + 1;       // [B + 1] pages taken before request b
     int* s_cached = s_page + a.B + 1;    // [B] cached lengths, checked
-    __shared__ int2 s_w[kTabThreads / 32];
+    __shared__ uint2 s_w[kTabThreads / 32];
+    __shared__ int s_cut, s_cut_pages;   // the request that the end of the rows cuts; pages taken up to its last listed row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int shift = __ffs(a.page_n) - 1;
     const bool first = blockIdx.x == 0;
     int used = *a.used;
     int bad = 0;
-    long long row0 = 0, page0 = 0;  // (before the round: saturating below, no sum wraps)
+    long long row0 = 0, page0 = 0;  // before the round
+    if (tid == 0) s_cut = a.B;
     for (int b0 = 0; b0 < a.B; b0 += kTabThreads) {
         const int b = b0 + tid;
         int c = 0, f = 0;
@@ -53,22 +55,21 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
             f = min(max(f, 0), kMaxLen - c);
             if ((c + f + a.page_n - 1) >> shift > a.width) bad |= HSQ_DEVERR_LEN;
             s_cached[b] = c;
-            if (first) a.lens[b] = c + f;
         }
         // No page is taken past the table's width; a request's rows saturate just past the rows there are.  (A warp's
-        // sums saturate at 2^30, past which neither rows nor pages of a valid call reach.)
+        // sums saturate at 2^31 - 1: with a.rows < 2^30 a start of at most a.rows is still exact, and any other stays above.)
         const int xi = min(f, a.rows + 1);
         const int yi = min((c + f + a.page_n - 1) >> shift, a.width) - min((c + a.page_n - 1) >> shift, a.width);
-        int x = xi, y = yi;
+        unsigned x = xi, y = yi;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, x, o), w = __shfl_up_sync(kFull, y, o);
+            const unsigned u = __shfl_up_sync(kFull, x, o), w = __shfl_up_sync(kFull, y, o);
             if (lane >= o) {
-                x = (int)min((long long)x + u, (long long)kMaxLen);
-                y = (int)min((long long)y + w, (long long)kMaxLen);
+                x = min(x + u, (unsigned)INT_MAX);
+                y = min(y + w, (unsigned)INT_MAX);
             }
         }
-        if (lane == 31) s_w[warp] = make_int2(x, y);
+        if (lane == 31) s_w[warp] = make_uint2(x, y);
         __syncthreads();
         long long tr = row0, tp = page0, X = x, Y = y;
         const int warps = min(kTabThreads, a.B - b0 + 31) >> 5;
@@ -77,20 +78,34 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(TablesArgs a) 
                 X += tr;
                 Y += tp;
             }
-            const int2 v = s_w[w];
+            const uint2 v = s_w[w];
             tr += v.x;
             tp += v.y;
         }
         if (b < a.B) {
-            s_row[b] = (int)min(max(X - xi, 0LL), (long long)a.rows);
-            s_page[b] = (int)min(max(Y - yi, 0LL), (long long)INT_MAX);
-            if (X > a.rows) bad |= HSQ_DEVERR_LEN;
+            // Where the rows end, a request is cut: what has no row counts neither as brought nor as stored (or the
+            // attention would take the last listed row for the request's last token, and read keys never written).
+            const int start = (int)min(X - xi, (long long)a.rows), listed = min(f, a.rows - start);
+            const int page = (int)min(Y - yi, (long long)INT_MAX);
+            s_row[b] = start;
+            s_page[b] = page;
+            if (first) a.lens[b] = c + listed;
+            if (listed < f) {
+                bad |= HSQ_DEVERR_LEN;
+                if (X - xi <= a.rows) {  // the first such request; none after it has a row or a new page
+                    const int more = min((c + listed + a.page_n - 1) >> shift, a.width) - min((c + a.page_n - 1) >> shift, a.width);
+                    s_cut = b;
+                    s_cut_pages = (int)min((long long)page + more, (long long)INT_MAX);
+                }
+            }
         }
-        row0 = min(tr, (long long)a.rows);
-        page0 = min(tp, (long long)INT_MAX);
+        row0 = tr;
+        page0 = tp;
         __syncthreads();
     }
-    const int rows = (int)row0, pages = (int)page0;
+    const int rows = (int)min(row0, (long long)a.rows), cut = s_cut;
+    const int pages = cut < a.B ? s_cut_pages : (int)min(page0, (long long)INT_MAX);
+    for (int b = cut + 1 + tid; b < a.B; b += kTabThreads) s_page[b] = pages;
     if (tid == 0) {
         s_row[a.B] = rows;
         s_page[a.B] = pages;

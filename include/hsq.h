@@ -530,7 +530,7 @@ enum { HSQ_MAX_REQUESTS = 4096 };  /* largest B of the paged calls */
  *   With P = page_n, lens = cached + fresh, have = min(ceil(cached / P), width)
  *   and need = min(ceil(lens / P), width):
  *     q_start[b] [B + 1]: rows of the requests before b (q_start[B] = rows in use);
- *     lens[b]    [B]: cached[b] + fresh[b];
+ *     lens[b]    [B]: cached[b] + fresh[b] (its tokens that have a row, see below);
  *     table[b][have .. need) = the next free_ids from index *used on, request by
  *       request; the other entries are left as they are;
  *     row i = q_start[b] + j: pos[i] = base + cached[b] + j and slots[i] =
@@ -542,9 +542,11 @@ enum { HSQ_MAX_REQUESTS = 4096 };  /* largest B of the paged calls */
  *   int32, slots int64; all device memory.
  *   Out of pages: the entries past the list are -1, and the slots of their
  *   tokens -1 (HSQ_DEVERR_PAGE); a page id outside the pool counts the same way.
- *   HSQ_DEVERR_LEN: a negative length (taken as 0), a length above 2^30
- *   (taken as that), tokens past the table's width (slot -1) or past `rows`
- *   (not listed: q_start stops at `rows`), *used outside [0, n_free].
+ *   More new tokens than `rows`: the requests get rows in their order until there
+ *   are none left; tokens without a row count as not brought (lens, table, *used_out), so
+ *   that the rows there are see their own tokens and a later step can bring the rest (HSQ_DEVERR_LEN).
+ *   HSQ_DEVERR_LEN as well: a negative length (taken as 0), a length above 2^30
+ *   (taken as that), tokens past the table's width (slot -1), *used outside [0, n_free].
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
  *   HSQ_MAX_REQUESTS)], width < 1, rows or n_free outside [1, 2^30), base outside [0, 2^30), an
  *   output that is an input, another current device than the context's),

@@ -28,6 +28,9 @@ def page_tables(cached, fresh, free_ids, used, table, rows, page_n, n_pages, bas
             err.add("LEN")
         c = min(max(c, 0), MAX_LEN)
         f = min(max(f, 0), MAX_LEN - c)
+        if f > rows - row:  # tokens without a row are not brought
+            err.add("LEN")
+            f = rows - row
         lens[b] = c + f
         have, need = -(-c // page_n), -(-(c + f) // page_n)
         if need > width:
@@ -44,9 +47,6 @@ def page_tables(cached, fresh, free_ids, used, table, rows, page_n, n_pages, bas
             table[b, col] = page
         q_start[b] = row
         for p in range(c, c + f):
-            if row == rows:
-                err.add("LEN")
-                break
             pos[row] = base + p
             if p // page_n < width:
                 page = int(table[b, p // page_n])

@@ -6,7 +6,7 @@ import pytest
 
 from hsq_harness import ensure_built
 from oracle import paged as P
-from test_gpu_paged import i32, i64, make, run_tables, word
+from test_gpu_paged import THETA, check_attn, host, i32, i64, make, run_tables, word
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,70 @@ def test_a_request_of_more_rows_than_there_are_is_flagged(cached, fresh, rows):
     assert err == want["err"] == {"LEN"}
     for k in got:
         np.testing.assert_array_equal(got[k].reshape(-1), np.asarray(want[k]).reshape(-1), err_msg=k)
+
+
+@pytest.mark.parametrize("cached,fresh,rows", [
+    ([5, 40, 0, 3], [1, 30, 4, 1], 20), ([0, 0], [16, 16], 16), ([0, 0, 0], [16, 33, 5], 40), ([17], [100], 15), ([3, 16, 2], [2, 40, 0], 18),
+    (list(range(700)), [2] * 700, 1001), (list(range(700)), [2] * 700, 1), (list(range(700)), [2] * 700, 1024)])
+def test_tokens_without_a_row_count_as_not_brought(cached, fresh, rows):
+    table = np.full((len(cached), 60), 2, np.int32)
+    n = 8 + sum(-(-(c + f) // 16) for c, f in zip(cached, fresh))
+    want = P.page_tables(cached, fresh, np.arange(n), 3, table, rows, 16, n)
+    listed = np.diff(want["q_start"])
+    assert listed.sum() == rows and (want["lens"] == np.asarray(cached) + listed).all()
+    got, err = run_tables(cached, fresh, np.arange(n), 3, table, rows, 16, n)
+    assert err == want["err"] == {"LEN"}
+    for k in got:
+        np.testing.assert_array_equal(got[k].reshape(-1), np.asarray(want[k]).reshape(-1), err_msg=k)
+
+
+def test_a_step_without_room_for_all_rows_attends_to_what_is_stored():
+    """Tables, write and attention with fewer rows than new tokens: each listed row sees the shared prefix and its
+    own tokens up to its own position; the next step brings the rest."""
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    rng = np.random.default_rng(3)
+    Hq, Hkv, page, B, shared, rows = 8, 2, 16, 3, 20, 30
+    ctx = make(Hq, Hkv, B, 512)
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda().bfloat16()  # noqa: E731
+    pool = H.PagePool(bf(24, Hkv, page, 128), bf(24, Hkv, page, 128))  # pages hold other tokens before they are written
+    free, used = i32(rng.permutation(24)), i32([2])
+    prefix = free[:2].contiguous()
+    total = np.array([9, 40, 5])
+    k, v = [bf(n, Hkv, 128) for n in total], [bf(n, Hkv, 128) for n in total]
+    table, cached = i32(np.full((B, 4), -1)), np.zeros(B, np.int64)
+    for step, listed in enumerate(([9, 21, 0], [0, 19, 5])):
+        fresh = total - cached
+        slots, pos, q_start, lens, used_out = i64([0] * rows), i32([0] * rows), i32([0] * (B + 1)), i32([0] * B), i32([0])
+        H.hsq_page_tables(ctx, pool, i32(cached), i32(fresh), free, used, table, slots, pos, q_start, lens, used_out, base=shared)
+        assert word(ctx) == ({"LEN"} if step == 0 else set())
+        assert np.diff(host(q_start)).tolist() == listed
+        # a program's rows: token cached[b] + j of request b, as q_start and pos say
+        at = [(b, int(cached[b]) + j) for b in range(B) for j in range(listed[b])]
+        ks, vs = torch.zeros(rows, Hkv, 128, device="cuda").bfloat16(), torch.zeros(rows, Hkv, 128, device="cuda").bfloat16()
+        for i, (b, t) in enumerate(at):
+            ks[i], vs[i] = k[b][t], v[b][t]
+        q, rot = bf(rows, Hq, 128), torch.zeros(rows, Hq, 128, device="cuda").bfloat16()
+        H.hsq_page_write(ctx, pool, q, ks, vs, pos, slots, rot)
+        out, lse = torch.full_like(q, 7.0), torch.full((rows, Hq), 7.0, device="cuda")
+        ws = torch.empty(H.hsq_shared_attn_workspace_size(ctx, rows, B, shared, rows), dtype=torch.uint8, device="cuda")
+        H.hsq_shared_attn(ctx, pool, rot, q_start, lens, table, out, ws, prefix=prefix, prefix_len=shared, max_new=rows, lse=lse)
+        assert word(ctx) == set()
+        # dense attention over each row's true tokens, from what a write of every token one by one gives
+        zero = np.zeros((24, Hkv, page, 128))
+        seen = cached + listed
+        for b in range(B):
+            ids = host(table)[b]
+            where = np.array([ids[t // page] * page + t % page for t in range(seen[b])], np.int64)
+            _, wk, wv = P.page_write(zero, zero, np.zeros((seen[b], Hq, 128)), host(k[b])[: seen[b]], host(v[b])[: seen[b]],
+                                     shared + np.arange(seen[b]), where, THETA, 512)
+            for t, s in enumerate(where):
+                assert np.abs(host(pool.k)[s // page, :, s % page] - wk[s // page, :, s % page]).max() < 2 ** -7 * 6
+                assert (host(pool.v)[s // page, :, s % page] == wv[s // page, :, s % page]).all()
+        x = dict(q=rot, k=pool.k, v=pool.v, table=host(table), prefix=host(prefix), prefix_len=shared,
+                 q_start=np.concatenate([[0], np.cumsum(listed)]), lens=seen, Hq=Hq, Hkv=Hkv)
+        check_attn(x, host(out), host(lse))
+        cached = host(lens).astype(np.int64)
+        assert (cached == seen).all()
+        used = used_out
+    assert (cached == total).all()
