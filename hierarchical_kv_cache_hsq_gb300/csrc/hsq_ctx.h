@@ -76,4 +76,24 @@ hsq_status prefill_attention(hsq_ctx* ctx, const PrefillImages& im, float* out, 
 hsq_status check_pages(hsq_ctx* ctx, const hsq_pages* pages, bool buffers);
 hsq_status check_device(hsq_ctx* ctx);
 
+// A call's buffer, and whether one of `outs` shares a byte with another or with one of `ins` (NULL: not given).
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+template <int NI, int NO>
+inline bool outputs_overlap(const Span (&ins)[NI], const Span (&outs)[NO]) {
+    auto meet = [](const Span& a, const Span& b) {
+        const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+        return x && y && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            if (meet(outs[o], ins[i])) return true;
+        for (int i = 0; i < o; ++i)
+            if (meet(outs[o], outs[i])) return true;
+    }
+    return false;
+}
+
 }  // namespace hsq

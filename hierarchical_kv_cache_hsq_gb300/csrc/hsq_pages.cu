@@ -328,11 +328,11 @@ hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int widt
     // (past 2^30 the kernel's sums and its strides over rows and pages no longer fit 32 bits)
     if (width < 1 || rows < 1 || rows >= kMaxLen || n_free < 1 || n_free >= kMaxLen || base < 0 || base >= kMaxLen)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "width must be positive, rows and n_free in [1, 2^30), base in [0, 2^30)");
-    const void* ins[] = {cached, fresh, free_ids, used};
-    const void* outs[] = {table, slots, pos, q_start, lens, used_out};
-    for (const void* i : ins)
-        for (const void* o : outs)
-            if (i == o) return hsq::fail(ctx, HSQ_ERR_INVALID, "an output of hsq_page_tables is one of its inputs");
+    const size_t n = 4 * (size_t)B;
+    const hsq::Span ins[] = {{cached, n}, {fresh, n}, {free_ids, 4 * (size_t)n_free}, {used, 4}};
+    const hsq::Span outs[] = {{table, n * width}, {slots, 8 * (size_t)rows}, {pos, 4 * (size_t)rows}, {q_start, n + 4}, {lens, n}, {used_out, 4}};
+    if (hsq::outputs_overlap(ins, outs))
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "an output of hsq_page_tables overlaps another argument");
     if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
     TablesArgs a{cached, fresh, free_ids, used, table, slots, pos, q_start, lens, used_out,
                  B, width, rows, n_free, base, pages->n_pages, pages->page_n, ctx->d_err};
@@ -354,7 +354,6 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
     if (!q != !q_out) return hsq::fail(ctx, HSQ_ERR_INVALID, "q and q_out go together");
     if (dtype != HSQ_DTYPE_F32 && dtype != HSQ_DTYPE_BF16) return hsq::fail(ctx, HSQ_ERR_INVALID, "bad dtype");
     if (rows < 1) return hsq::fail(ctx, HSQ_ERR_INVALID, "rows must be positive");
-    if (q && (q_out == q || q_out == k || q_out == v)) return hsq::fail(ctx, HSQ_ERR_INVALID, "q_out is an input");
     const int Hq = q ? ctx->cfg.n_q_heads : 0, Hkv = ctx->cfg.n_kv_heads;
     const int64_t unit = dtype == HSQ_DTYPE_BF16 ? 8 : 4;  // elements of 16 bytes
     if ((q && q_stride < (int64_t)Hq * 128) || k_stride < (int64_t)Hkv * 128 || v_stride < (int64_t)Hkv * 128)
@@ -362,9 +361,18 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
     if ((q && q_stride % unit) || k_stride % unit || v_stride % unit ||
         (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 15u))
         return hsq::fail(ctx, HSQ_ERR_INVALID, "rows of q, k, v and q_out must be 16-byte aligned");
-    if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
     const long long vectors = (long long)rows * (Hq + 2 * Hkv);
     if (vectors >= (1LL << 31)) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
+    const size_t size = dtype == HSQ_DTYPE_BF16 ? 2 : 4, pool = (size_t)pages->n_pages * Hkv * pages->page_n * 256;
+    auto strided = [&](const void* p, int64_t stride, int heads) {
+        return hsq::Span{p, ((size_t)(rows - 1) * stride + (size_t)heads * 128) * size};
+    };
+    const hsq::Span ins[] = {strided(q, q_stride, Hq), strided(k, k_stride, Hkv), strided(v, v_stride, Hkv),
+                             {pos, 4 * (size_t)rows}, {slots, 8 * (size_t)rows}};
+    const hsq::Span outs[] = {{q_out, (size_t)rows * Hq * 256}, {pages->k, pool}, {pages->v, pool}};
+    if (hsq::outputs_overlap(ins, outs))
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "q_out or the pool's k or v overlaps another argument of hsq_page_write");
+    if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
     const int shift = pages->page_n == 16 ? 4 : pages->page_n == 32 ? 5 : pages->page_n == 64 ? 6 : 7;
     WriteArgs a{q, k, v, q_stride, k_stride, v_stride, pos, slots, static_cast<uint16_t*>(q_out),
                 static_cast<uint16_t*>(pages->k), static_cast<uint16_t*>(pages->v), rows, Hq, Hkv, pages->page_n, shift,

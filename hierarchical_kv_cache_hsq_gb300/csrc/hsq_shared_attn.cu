@@ -1734,12 +1734,17 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     if (prefix_len > 0 && !prefix) return hsq::fail(ctx, HSQ_ERR_INVALID, "prefix is NULL with prefix_len > 0");
     if (((uintptr_t)q | (uintptr_t)out) & 15u)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "q and out must be 16-byte aligned");
-    if (q == out || out == workspace || q == workspace || lse_opt == out || lse_opt == workspace)
-        return hsq::fail(ctx, HSQ_ERR_INVALID, "an output or the workspace of hsq_shared_attn is another argument");
     if ((uintptr_t)workspace & 255u) return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace must be 256-byte aligned");
     const Layout x = layout_of(ctx, rows, B, prefix_len, max_new);
     if (workspace_bytes < x.bytes)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace smaller than hsq_shared_attn_workspace_size");
+    const size_t q_bytes = (size_t)rows * ctx->cfg.n_q_heads * 256, pool = (size_t)pages->n_pages * ctx->cfg.n_kv_heads * pages->page_n * 256;
+    const hsq::Span ins[] = {{q, q_bytes}, {q_start, 4 * ((size_t)B + 1)}, {lens, 4 * (size_t)B}, {table, 4 * (size_t)B * width},
+                             {prefix_len > 0 ? prefix : nullptr, 4 * (size_t)((prefix_len + pages->page_n - 1) / pages->page_n)},
+                             {pages->k, pool}, {pages->v, pool}};
+    const hsq::Span outs[] = {{out, q_bytes}, {lse_opt, (size_t)rows * ctx->cfg.n_q_heads * 4}, {workspace, x.bytes}};
+    if (hsq::outputs_overlap(ins, outs))
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "an output or the workspace of hsq_shared_attn overlaps another argument");
     if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
     const int r = ctx->r, Hkv = ctx->cfg.n_kv_heads, tpt = kTileRows / r;
     uint8_t* ws = static_cast<uint8_t*>(workspace);

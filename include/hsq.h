@@ -537,8 +537,8 @@ enum { HSQ_MAX_REQUESTS = 4096 };  /* largest B of the paged calls */
  *       table[b][p / P] * P + p mod P with p = cached[b] + j; rows from
  *       q_start[B] on: pos = slots = -1;
  *     *used_out = *used + the pages taken (at most n_free).
- *   Inputs are not written, so the call can be repeated; an output must
- *   not be an input.  free_ids [n_free], table [B][width], slots, pos [rows]:
+ *   Inputs are not written, so the call can be repeated; outputs overlap neither
+ *   inputs nor each other.  free_ids [n_free], table [B][width], slots, pos [rows]:
  *   int32, slots int64; all device memory.
  *   Out of pages: the entries past the list are -1, and the slots of their
  *   tokens -1 (HSQ_DEVERR_PAGE); a page id outside the pool counts the same way.
@@ -549,7 +549,7 @@ enum { HSQ_MAX_REQUESTS = 4096 };  /* largest B of the paged calls */
  *   (taken as that), tokens past the table's width (slot -1), *used outside [0, n_free].
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
  *   HSQ_MAX_REQUESTS)], width < 1, rows or n_free outside [1, 2^30), base outside [0, 2^30), an
- *   output that is an input, another current device than the context's),
+ *   output that overlaps another argument, another current device than the context's),
  *   HSQ_ERR_CUDA.
  */
 hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int width, int rows, int n_free, int base,
@@ -566,11 +566,11 @@ hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int widt
  *   q: [rows][Hq][128] or NULL with q_out NULL; k, v: [rows][Hkv][128], of dtype,
  *   device memory, rows q_stride, k_stride, v_stride elements apart (views of one fused
  *   projection), 16-byte aligned rows.  q_out: [rows][Hq][128] bf16, 16-byte aligned;
- *   neither it nor the pool may overlap q, k or v.
+ *   neither it nor the pool's k and v may overlap each other or an input.
  *   HSQ_DEVERR_POS: a position >= max_pos (clamped); HSQ_DEVERR_PAGE: a slot
  *   outside the pool (not stored).
  *   Errors: HSQ_ERR_INVALID (NULL, rows < 1, rows * (Hq + 2 Hkv) >= 2^31, a stride below
- *   a row's length or alignment, q_out an input, another current device than the context's), HSQ_ERR_CUDA.
+ *   a row's length or alignment, outputs that overlap, another current device than the context's), HSQ_ERR_CUDA.
  */
 hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const void* q, const void* k, const void* v,
                           int64_t q_stride, int64_t k_stride, int64_t v_stride, hsq_dtype dtype,
@@ -605,7 +605,7 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
  *   HSQ_DEVERR_WAIT: a bounded wait ran out, the results of the call are undefined.
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,
  *   HSQ_MAX_REQUESTS)], rows, width or max_new < 1, prefix_len outside [0, 2^30], width * P above
- *   2^30, alignment, a small workspace, out or the workspace given twice, another current device than the context's), HSQ_ERR_CUDA.
+ *   2^30, alignment, a small workspace, out, lse or the workspace over another argument, another current device than the context's), HSQ_ERR_CUDA.
  */
 hsq_status hsq_shared_attn_workspace_size(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_new,
                                           size_t* bytes);

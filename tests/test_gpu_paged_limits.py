@@ -108,3 +108,47 @@ def test_a_step_without_room_for_all_rows_attends_to_what_is_stored():
         assert (cached == seen).all()
         used = used_out
     assert (cached == total).all()
+
+
+def test_outputs_that_overlap_are_refused():
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    z = lambda n, dt=torch.int32: torch.zeros(n, dtype=dt, device="cuda")  # noqa: E731
+    b = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+
+    def refused(call, base, *changes):
+        call(**base)
+        for change in changes:
+            with pytest.raises(H.HSQError) as e:
+                call(**dict(base, **change))
+            assert e.value.status == 1 and "overlap" in str(e.value)
+    ctx = make(8, 2, 1, 512)
+    pool = H.allocate_pages(ctx, 4, 16)
+    t = dict(cached=z(1), fresh=z(1), free_ids=z(4), used=z(1), table=z((1, 2)), slots=z(1, torch.int64), pos=z(1),
+             q_start=z(2), lens=z(1), used_out=z(1))
+    both = z(8)
+    refused(lambda **k: H.hsq_page_tables(ctx, pool, **k), t,
+            dict(pos=t["lens"]), dict(used_out=t["lens"]), dict(pos=t["used_out"]), dict(lens=t["q_start"][1:]),
+            dict(free_ids=both[:4], q_start=both[3:5]), dict(table=both[:2].view(1, 2), used_out=both[1:2]), dict(used_out=t["fresh"]),
+            dict(slots=both[:2].view(torch.int64), lens=both[1:2]))
+    H.hsq_page_tables(ctx, pool, **dict(t, used=both[:1], used_out=both[1:2], lens=both[2:3], q_start=both[3:5]))  # side by side
+    w = dict(q=b(3, 8, 128), k=b(3, 2, 128), v=b(3, 2, 128), pos=z(3), slots=z(3, torch.int64) - 1, q_out=b(3, 8, 128))
+    wide = b(3, 12, 128)
+    rows = pool.k.view(-1)[: 3 * 8 * 128]
+    refused(lambda **k: H.hsq_page_write(ctx, pool, **k), w,
+            dict(q_out=w["q"]), dict(q=wide[:, :8], k=wide[:, 8:10], v=wide[:, 10:], q_out=wide.view(-1)[8 * 128: 8 * 128 + 3 * 1024].view(3, 8, 128)),
+            dict(q_out=rows.view(3, 8, 128)), dict(k=rows[: 3 * 256].view(3, 2, 128)), dict(v=pool.v.view(-1)[: 3 * 256].view(3, 2, 128)))
+    with pytest.raises(H.HSQError):  # keys and values in one place
+        H.hsq_page_write(ctx, H.PagePool(pool.k, pool.k), **w)
+    n = H.hsq_shared_attn_workspace_size(ctx, 3, 1, 20, 3)
+    big = torch.zeros(n + 3 * 8 * 128 * 2, dtype=torch.uint8, device="cuda")
+    a = dict(q=b(3, 8, 128), q_start=z(2), lens=z(1), table=z((1, 2)), out=b(3, 8, 128), workspace=big[:n], prefix=z(2), prefix_len=20,
+             max_new=3, lse=torch.zeros(3, 8, device="cuda"))
+    refused(lambda **k: H.hsq_shared_attn(ctx, pool, **k), a,
+            dict(out=a["q"]), dict(out=big[n - 256: n - 256 + 6144].view(torch.bfloat16).view(3, 8, 128)),
+            dict(lse=big[n - 96: n].view(torch.float32).view(3, 8)), dict(out=rows.view(3, 8, 128)),
+            dict(lse=a["out"].view(-1)[:48].view(torch.float32).view(1, 24).view(3, 8)),
+            dict(table=big[256: 264].view(torch.int32).view(1, 2)), dict(prefix=big[512: 520].view(torch.int32)))
+    both_kv = H.PagePool(pool.k, pool.k)  # read only: one tensor for keys and values is fine
+    H.hsq_shared_attn(ctx, both_kv, **a)
+    assert word(ctx) == set()
