@@ -510,6 +510,11 @@ def _stream_on(pool: PagePool, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(pool.index) if stream is None else stream.cuda_stream
 
 
+def _c_int(x: int) -> int:
+    """x as a C int; what does not fit one goes as -1, which the library refuses (ctypes would cut it off)."""
+    return x if -0x80000000 <= x <= 0x7FFFFFFF else -1
+
+
 def _need_heads(ctx: Context, pool: PagePool):
     if pool.k.shape[1] != ctx.cfg.n_kv_heads:
         raise ValueError("the pool's KV heads are not the context's")
@@ -534,7 +539,7 @@ def hsq_page_tables(ctx: Context, pool: PagePool, cached, fresh, free_ids, used,
     rows = slots.numel()
     if pos.numel() != rows or used.numel() != 1 or used_out.numel() != 1:
         raise ValueError("pos and slots must be [rows], used and used_out [1]")
-    st = ctx.lib.hsq_page_tables(ctx.handle, pool.ref, B, table.shape[1], rows, free_ids.numel(), base,
+    st = ctx.lib.hsq_page_tables(ctx.handle, pool.ref, _c_int(B), _c_int(table.shape[1]), _c_int(rows), _c_int(free_ids.numel()), _c_int(base),
                                  cached.data_ptr(), fresh.data_ptr(), free_ids.data_ptr(), used.data_ptr(),
                                  table.data_ptr(), slots.data_ptr(), pos.data_ptr(), q_start.data_ptr(),
                                  lens.data_ptr(), used_out.data_ptr(), _stream_on(pool, stream))
@@ -574,7 +579,7 @@ def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, str
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
     one = rows == 1  # (the row stride of a single row says nothing)
-    st = ctx.lib.hsq_page_write(ctx.handle, pool.ref, rows, _ptr(q), k.data_ptr(), v.data_ptr(),
+    st = ctx.lib.hsq_page_write(ctx.handle, pool.ref, _c_int(rows), _ptr(q), k.data_ptr(), v.data_ptr(),
                                 0 if q is None else ctx.cfg.n_q_heads * 128 if one else q.stride(0),
                                 Hkv * 128 if one else k.stride(0), Hkv * 128 if one else v.stride(0), dt,
                                 pos.data_ptr(), slots.data_ptr(), _ptr(q_out), _stream_on(pool, stream))
@@ -584,8 +589,8 @@ def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, str
 
 def hsq_shared_attn_workspace_size(ctx: Context, rows: int, B: int, prefix_len: int, max_new: int) -> int:
     n = ctypes.c_size_t(0)
-    _check(ctx.lib.hsq_shared_attn_workspace_size(ctx.handle, rows, B, prefix_len, max_new, ctypes.byref(n)),
-           ctx.handle)
+    _check(ctx.lib.hsq_shared_attn_workspace_size(ctx.handle, _c_int(rows), _c_int(B), _c_int(prefix_len), _c_int(max_new),
+                                                  ctypes.byref(n)), ctx.handle)
     return int(n.value)
 
 
@@ -619,7 +624,7 @@ def hsq_shared_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, out, 
             raise ValueError("lse must be [rows, Hq]")
     if workspace.get_device() != pool.index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the pool's device")
-    st = ctx.lib.hsq_shared_attn(ctx.handle, pool.ref, rows, B, table.shape[1], prefix_len, max_new, q.data_ptr(),
+    st = ctx.lib.hsq_shared_attn(ctx.handle, pool.ref, _c_int(rows), _c_int(B), _c_int(table.shape[1]), _c_int(prefix_len), _c_int(max_new), q.data_ptr(),
                                  q_start.data_ptr(), lens.data_ptr(), table.data_ptr(),
                                  prefix.data_ptr() if prefix_len > 0 else None, out.data_ptr(), _ptr(lse),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),

@@ -152,3 +152,30 @@ def test_outputs_that_overlap_are_refused():
     both_kv = H.PagePool(pool.k, pool.k)  # read only: one tensor for keys and values is fine
     H.hsq_shared_attn(ctx, both_kv, **a)
     assert word(ctx) == set()
+
+
+def test_numbers_that_no_c_int_holds_are_refused():
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    ctx = make(8, 2, 1, 512)
+    pool = H.allocate_pages(ctx, 4, 16)
+    z = lambda n, dt=torch.int32: torch.zeros(n, dtype=dt, device="cuda")  # noqa: E731
+    t = dict(cached=z(1), fresh=z(1), free_ids=z(4), used=z(1), table=z((1, 2)), slots=z(1, torch.int64), pos=z(1),
+             q_start=z(2), lens=z(1), used_out=z(1))
+    q = torch.zeros((3, 8, 128), dtype=torch.bfloat16, device="cuda")
+    a = dict(q=q, q_start=z(2), lens=z(1), table=z((1, 2)), out=torch.zeros_like(q), max_new=3,
+             workspace=torch.empty(H.hsq_shared_attn_workspace_size(ctx, 3, 1, 0, 3), dtype=torch.uint8, device="cuda"))
+    for big in (1 << 32, (1 << 32) + 3, -(1 << 32), 1 << 70):
+        for call in (lambda: H.hsq_page_tables(ctx, pool, **t, base=big),
+                     lambda: H.hsq_shared_attn(ctx, pool, **dict(a, max_new=big)),
+                     lambda: H.hsq_shared_attn_workspace_size(ctx, big, 1, 0, 3), lambda: H.hsq_shared_attn_workspace_size(ctx, 3, big, 0, 3),
+                     lambda: H.hsq_shared_attn_workspace_size(ctx, 3, 1, big, 3), lambda: H.hsq_shared_attn_workspace_size(ctx, 3, 1, 0, big)):
+            with pytest.raises(H.HSQError) as e:
+                call()
+            assert e.value.status == 1
+        if big < 0:
+            with pytest.raises(H.HSQError):
+                H.hsq_shared_attn(ctx, pool, **a, prefix_len=big)
+    H.hsq_page_tables(ctx, pool, **t, base=7)
+    H.hsq_shared_attn(ctx, pool, **a)
+    assert word(ctx) == set()
