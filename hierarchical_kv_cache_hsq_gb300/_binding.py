@@ -455,10 +455,11 @@ def hsq_route_noalloc(cfg: hsq_config, cache: CacheBuffers, q, pos, sel, stream=
 
 # -- paged serving ---------------------------------------------------------------------
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class PagePool:
     """The pages of one layer: k, v [n_pages, Hkv, page_n, 128] bfloat16 on one
-    device, keys RoPE'd.  page_n is 16, 32, 64 or 128."""
+    device, keys RoPE'd.  page_n is 16, 32, 64 or 128.  k and v are the pool's for
+    good (their addresses are taken once); other tensors make another pool."""
     k: "object"
     v: "object"
 
@@ -469,9 +470,9 @@ class PagePool:
                 raise ValueError("k and v must be contiguous bfloat16 [n_pages, Hkv, page_n, 128] on the GPU")
         if self.k.shape != self.v.shape or self.k.device != self.v.device:
             raise ValueError("k and v must have one shape and one device")
-        self.index = self.k.get_device()
-        self._c = hsq_pages(k=self.k.data_ptr(), v=self.v.data_ptr(), n_pages=self.k.shape[0], page_n=self.k.shape[2])
-        self.ref = ctypes.byref(self._c)
+        c = hsq_pages(k=self.k.data_ptr(), v=self.v.data_ptr(), n_pages=self.k.shape[0], page_n=self.k.shape[2])
+        for name, value in (("index", self.k.get_device()), ("_c", c), ("ref", ctypes.byref(c))):
+            object.__setattr__(self, name, value)
 
     @property
     def n_pages(self) -> int:

@@ -179,3 +179,15 @@ def test_numbers_that_no_c_int_holds_are_refused():
     H.hsq_page_tables(ctx, pool, **t, base=7)
     H.hsq_shared_attn(ctx, pool, **a)
     assert word(ctx) == set()
+
+
+def test_a_pool_keeps_its_tensors():
+    """The library holds their addresses: another tensor put in their place would go unread, the old one's memory being free."""
+    import dataclasses
+    import hierarchical_kv_cache_hsq_gb300 as H
+    pool = H.allocate_pages(make(8, 2), 4, 16)
+    for name in ("k", "v"):
+        with pytest.raises(dataclasses.FrozenInstanceError):
+            setattr(pool, name, pool.k.clone())
+    assert pool._c.k == pool.k.data_ptr() and pool._c.v == pool.v.data_ptr() and (pool.n_pages, pool.page_n) == (4, 16)
+    assert pool == pool and pool != H.PagePool(pool.k, pool.v)
