@@ -2,7 +2,7 @@
 //
 // For row i of request b (token j of its n new ones) and query head jq of KV head
 // h: one softmax, scale 1/sqrt(128), over the prefix's tokens and the request's own
-// tokens s <= len - n + j.  A softmax over the union of key sets is the weighted
+// tokens s <= len - n + j (of those that its table holds).  A softmax over the union of key sets is the weighted
 // sum of the softmaxes over each: with m, l, o a reference exponent, the sum of
 // exp(x - m) and the sum of exp(x - m) v of a part,
 //     out = sum_p exp(m_p - M) o_p / sum_p exp(m_p - M) l_p,   M = max_p m_p,
@@ -90,7 +90,9 @@ struct SharedArgs {
     int tokens_cap;  // most tokens that short requests can have
     // workspace
     PlanHead* head;
-    int4* req;              // [B] first row, rows, own tokens (checked), short tokens before it
+    // [B][2] first row, rows, own tokens (no more than its table holds), short tokens before it | own tokens before its first
+    // row: row j sees the first min(own tokens, that + j + 1)
+    int4* req;
     int* of;                // [short tokens] their requests
     long long *c_at, *b_at, *d_at; // [B + 1] cost of the C, B and D items before request b
     int* cut;               // [runs][16 ints] the C item that run c is the second to work on (see CutRecord)
@@ -146,8 +148,8 @@ __device__ __forceinline__ int few_warp_of(const PlanHead& p, long long x) {
 }
 
 // virtual keys of unit u of a long request (never fewer than the real ones): its cost is kCostLong a key
-__device__ __forceinline__ long long unit_base(const SharedArgs& a, int n, int len) {
-    return (long long)a.prefix_tiles * kTileKeys + max(len - n, 0);
+__device__ __forceinline__ long long unit_base(const SharedArgs& a, int ahead) {
+    return (long long)a.prefix_tiles * kTileKeys + max(ahead, 0);
 }
 // virtual keys of an item of A (0: there is none)
 __device__ __forceinline__ long long a_keys(const SharedArgs& a) {
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     long long before[4] = {0, 0, 0, 0};  // short tokens, C, B and D cost
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
-        int first = 0, n = 0, len = 0, l = 0;
+        int first = 0, n = 0, len = 0, ahead = 0, l = 0;
         bool wrong = false;
         if (b < a.B) {
             const int s = a.q_start[b], e = a.q_start[b + 1];
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         if (b < a.B) {
             len = (int)min((long long)max(l, 0), (long long)a.width << a.page_shift);
             if (len != l || len < n) bad |= HSQ_DEVERR_LEN;
+            ahead = min(max(l, 0) - n, len);  // (by the length given: a table too short for it hides keys, but moves no row)
         }
         const bool brief = n <= a.tpt;
         long long x[4] = {brief ? n : 0, 0, 0, 0}, own[4];
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         }
         if (!brief) {
             const int D = 2 * a.tpt, units = (n + D - 1) / D;
-            const long long base = unit_base(a, n, len);
+            const long long base = unit_base(a, ahead);
             x[1] = a.Hkv * (units_before(base, D, units - 1) + kCostLong * (base + n));
         }
 #pragma unroll
@@ -226,7 +229,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
             x[k] += mine - own[k];
         }
         if (b < a.B) {
-            a.req[b] = make_int4(first, n, len, (int)x[0]);
+            a.req[2 * b] = make_int4(first, n, len, (int)x[0]);
+            a.req[2 * b + 1] = make_int4(ahead, 0, 0, 0);
             for (int i = 0; i < own[0]; ++i) a.of[x[0] + i] = b;
             a.c_at[b] = x[1];
             a.b_at[b] = x[2];
@@ -397,13 +401,14 @@ struct Walker {
     const PlanHead& p;
     long long at, end;      // the run, of A's lane or of the others' line
     long long w0;           // where the current item begins
-    int zone, b, h, u, n, len, first;  // the item: A (h, u = pair), C (b, h, unit u), B (b, h)
+    int zone, b, h, u, n, len, first, ahead;  // the item: A (h, u = pair), C (b, h, unit u), B (b, h)
     int lane, run;          // A: the CTA's lane and run; else the run
     long long cost;         // the item's
     bool more;
 
     __device__ __forceinline__ void load_request() {
-        const int4 q = a.req[b];
+        const int4 q = a.req[2 * b];
+        ahead = a.req[2 * b + 1].x;
         first = q.x;
         n = q.y;
         len = q.z;
@@ -414,7 +419,7 @@ struct Walker {
         if (zone == 0) {
             cost = a_keys(a) * a_rate();
         } else if (zone == 1) {
-            const long long base = unit_base(a, n, len);
+            const long long base = unit_base(a, ahead);
             cost = kCostLong * (base + min(n, (u + 1) * 2 * a.tpt));
         } else {
             cost = (long long)(len + kItemKeys) * kCostOwn;
@@ -435,7 +440,7 @@ struct Walker {
             b = warp_find(a.c_at, a.B, x);
             load_request();
             const int D = 2 * a.tpt;
-            const long long base = unit_base(a, n, len), at_b = a.c_at[b], z = x - at_b;
+            const long long base = unit_base(a, ahead), at_b = a.c_at[b], z = x - at_b;
             const long long per = units_before(base, D, units() - 1) + kCostLong * (base + n);  // a KV head's
             h = small_quotient(z, per);
             const long long rem = z - h * per;
@@ -528,7 +533,7 @@ struct Walker {
             s.tok1 = s.tok0 + s.toks0;
             s.ptiles = a.prefix_tiles;
             s.first = first;
-            s.obase = len - n + 1;
+            s.obase = ahead + 1;
             s.olen = min(len, max(0, s.obase + s.tok1 + s.toks1 - 1 - first));
             tiles = s.ptiles + (s.olen + kTileKeys - 1) / kTileKeys;
             const int l0 = min(s.olen, max(0, s.obase + s.tok0 + s.toks0 - 1 - first));
@@ -540,7 +545,7 @@ struct Walker {
             s.tok0 = s.tok1 = s.first = first;
             s.toks0 = s.toks1 = n;
             s.ptiles = 0;
-            s.obase = len - n + 1;
+            s.obase = ahead + 1;
             s.olen = len;
             s.end0 = s.end1 = tiles = (len + kTileKeys - 1) / kTileKeys;
         }
@@ -611,12 +616,13 @@ struct FewWalk {
     const SharedArgs& a;
     const PlanHead& p;
     long long at, end, w0;
-    int b, h, s, s1, first, n, len;
+    int b, h, s, s1, first, n, len, ahead;
     bool more;
 
     __device__ __forceinline__ void find(long long x) {
         b = warp_find(a.d_at, a.B, x - p.work_t);
-        const int4 q = a.req[b];
+        const int4 q = a.req[2 * b];
+        ahead = a.req[2 * b + 1].x;
         first = q.x;
         n = q.y;
         len = q.z;
@@ -716,7 +722,7 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int rr = 8 * nt + 2 * t + e;
-                lim[nt][e] = rr < rows ? min(now.len, now.len - now.n + rr / a.r + 1) : 0;
+                lim[nt][e] = rr < rows ? min(now.len, now.ahead + rr / a.r + 1) : 0;
             }
         }
         float o[NT][8][4], m[NT][2], l[NT][2];
@@ -1191,7 +1197,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int i0 = 0; i0 < toks; i0 += 32) {
                             int row = -1;
                             if (i0 + lane < toks) {
-                                const int4 q = a.req[a.of[tok + i0 + lane]];
+                                const int4 q = a.req[2 * a.of[tok + i0 + lane]];
                                 row = q.x + tok + i0 + lane - q.w;
                             }
                             const int chunks = min(32, toks - i0) * a.r * 16;
@@ -1450,7 +1456,7 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
             return;
         }
         const int b = live ? b_any : 0;
-        const int4 q = __ldcg(a.req + b);
+        const int4 q = __ldcg(a.req + 2 * b);
         const bool few = q.y * a.r <= kFewRows;
         const long long at1 = few ? p.work_t + __ldcg(a.d_at + b) : p.work_c + __ldcg(a.b_at + b);
         const int orow = live ? row - (q.w - tile * a.tpt) * a.r : 0;  // row among the request's
@@ -1666,7 +1672,7 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     x.runs = ctx->num_sms;
     x.own_rows = (int)((std::min<size_t>(max_new, tpt) * r + 3) / 4 * 4);
     x.head = take(sizeof(PlanHead));
-    x.req = take((size_t)B * 16);
+    x.req = take((size_t)B * 32);
     x.c_at = take((size_t)(B + 1) * 8);
     x.b_at = take((size_t)(B + 1) * 8);
     x.d_at = take((size_t)(B + 1) * 8);

@@ -599,8 +599,8 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
  *   it are expected finite: a value that is not makes results of the rows that see it NaN, and may do so for every
  *   row of its request (weights of 0 times infinity).  A logit of NaN gives a row of NaN.
  *   HSQ_DEVERR_PAGE: a page id outside the pool (its tokens are not attended to);
- *   HSQ_DEVERR_LEN: lens[b] above width * P, negative (both clamped) or below n_b (the first rows see
- *   the prefix only), q_start[b] .. q_start[b + 1] not ascending in [0, rows], below an earlier
+ *   HSQ_DEVERR_LEN: lens[b] above width * P (no row sees a token past the table; each row's last token
+ *   goes by lens[b] as given), negative (taken as 0) or below n_b (the first rows see the prefix only), q_start[b] .. q_start[b + 1] not ascending in [0, rows], below an earlier
  *   offset or more than max_new rows (that request's rows are not written);
  *   HSQ_DEVERR_WAIT: a bounded wait ran out, the results of the call are undefined.
  *   Errors: HSQ_ERR_INVALID (NULL, B outside [1, min(max_batch,

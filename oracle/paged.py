@@ -89,7 +89,7 @@ def shared_attn(pages_k, pages_v, q, q_start, lens, table, prefix, prefix_len):
     """-> out [rows, Hq, 128], lse [rows, Hq], spread [rows, Hq, 128] (the weighted |values|) and
     mass [rows, Hq] (the largest sum of |q_d k_d| / sqrt(128) over the tokens seen): what error bounds
     are made of.  Rows that belong to no request: NaN."""
-    Hkv = pages_k.shape[1]
+    Hkv, P = pages_k.shape[1], pages_k.shape[2]
     rows, Hq, D = q.shape
     r = Hq // Hkv
     out, spread = np.full((rows, Hq, D), np.nan), np.full((rows, Hq, D), np.nan)
@@ -99,10 +99,11 @@ def shared_attn(pages_k, pages_v, q, q_start, lens, table, prefix, prefix_len):
         vp, _ = gather(pages_v, prefix, prefix_len, h)
         for b in range(len(lens)):
             s, e = int(q_start[b]), int(q_start[b + 1])
-            ko, oko = gather(pages_k, table[b], int(lens[b]), h)
-            vo, _ = gather(pages_v, table[b], int(lens[b]), h)
+            held = min(max(int(lens[b]), 0), len(table[b]) * P)  # tokens past the table are seen by no row
+            ko, oko = gather(pages_k, table[b], held, h)
+            vo, _ = gather(pages_v, table[b], held, h)
             for i in range(s, e):
-                own = min(max(int(lens[b]) - (e - s) + (i - s) + 1, 0), int(lens[b]))
+                own = min(max(max(int(lens[b]), 0) - (e - s) + (i - s) + 1, 0), held)
                 keep = np.concatenate([okp, oko[:own]])
                 k = np.concatenate([kp, ko[:own]])[keep]
                 v = np.concatenate([vp, vo[:own]])[keep]

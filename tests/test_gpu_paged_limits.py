@@ -6,7 +6,7 @@ import pytest
 
 from hsq_harness import ensure_built
 from oracle import paged as P
-from test_gpu_paged import THETA, check_attn, host, i32, i64, make, run_tables, word
+from test_gpu_paged import THETA, attn_inputs, check_attn, host, i32, i64, make, run_attn, run_tables, word
 
 pytestmark = pytest.mark.gpu
 
@@ -191,3 +191,19 @@ def test_a_pool_keeps_its_tensors():
             setattr(pool, name, pool.k.clone())
     assert pool._c.k == pool.k.data_ptr() and pool._c.v == pool.v.data_ptr() and (pool.n_pages, pool.page_n) == (4, 16)
     assert pool == pool and pool != H.PagePool(pool.k, pool.v)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (4, 4), (8, 1)])
+@pytest.mark.parametrize("own,new,width,lens", [
+    ([32, 20], [10, 1], 2, [40, 20]),         # request 0 has 30 tokens stored, two of the ten new ones fit
+    ([32, 20], [10, 4], 2, [70, 23]),         # none of its rows' own tokens fits
+    ([64, 64], [40, 3], 4, [70, 64]), ([64, 64], [40, 3], 4, [2 ** 31 - 1, 65]),
+    ([160, 16], [150, 1], 10, [170, 16]), ([160, 16], [150, 1], 10, [160 + 150, 16]), ([160, 16], [150, 1], 10, [2 ** 31 - 1, 2 ** 30 + 5])])
+def test_a_table_too_short_for_a_length_moves_no_row(own, new, width, lens, Hq, Hkv):
+    x = attn_inputs(Hq, Hkv, 16, 50, own, new, pad=1, seed=sum(own) + Hq, stale=0.25)
+    x["table"] = x["table"][:, :width].copy().clip(0)
+    x["lens"] = np.array(lens, np.int64).astype(np.int32)
+    out, lse, err = run_attn(x)
+    assert err == {"LEN"}
+    # (a length that puts every row past the table gives the same limits as any longer one; the bound of lse goes by it)
+    check_attn(dict(x, lens=np.minimum(lens, 16 * width + np.asarray(new))), out, lse)
