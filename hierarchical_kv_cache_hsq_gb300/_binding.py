@@ -26,6 +26,7 @@ HSQ_ERR_TIMEOUT, HSQ_ERR_DEVICE_CHECK, HSQ_ERR_UNSUPPORTED = 4, 5, 6
 HSQ_DTYPE_F32, HSQ_DTYPE_BF16 = 0, 1
 HSQ_ATTN_FROM_STAGING = 1
 HSQ_FAULT_ALLOC, HSQ_FAULT_FETCH = 1, 2
+HSQ_FAULT_WAIT_LOAD, HSQ_FAULT_WAIT_MMA, HSQ_FAULT_WAIT_QUERY, HSQ_FAULT_WAIT_SOFTMAX, HSQ_FAULT_WAIT_FEW = 4, 8, 16, 32, 64
 HSQ_DEVERR_SEL, HSQ_DEVERR_POS, HSQ_DEVERR_L1_OVER, HSQ_DEVERR_WAIT, HSQ_DEVERR_GROW = 1, 2, 4, 8, 16
 HSQ_DEVERR_PAGE, HSQ_DEVERR_LEN = 32, 64
 

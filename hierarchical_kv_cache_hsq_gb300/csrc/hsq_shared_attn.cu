@@ -103,6 +103,8 @@ struct SharedArgs {
     float* d_o;
     float2* d_ml;
     int few_rows;  // 8 or 16
+    int polls;     // of a wait, before it has run out
+    int fault;     // HSQ_FAULT_WAIT_*: the roles of the main kernel that give up at a certain wait (0 but in tests)
     int* err;
 };
 
@@ -333,9 +335,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kStages = kKeyStages + kValueStages, kQueue = 4;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = kStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
-// barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | seg_full[4] | seg_empty[4]
-constexpr int kTcBars = 2 * kStages + 11 + 2 * kQueue;
-constexpr uint32_t kOffMask = kOffBars + 8 * (kTcBars + 1);  // [8] pages of a key tile that lie in the pool
+// barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | drain | seg_full[4] | seg_empty[4]
+constexpr int kTcBars = 2 * kStages + 12 + 2 * kQueue;
+static_assert(kTcBars % 2 == 0, "segments lie on 16-byte boundaries");
+constexpr uint32_t kOffMask = kOffBars + 8 * kTcBars;  // [8] pages of a key tile that lie in the pool
 constexpr uint32_t kOffSeg = kOffMask + 32;                  // [4] segments of the run
 constexpr uint32_t kSegBytes = 96;
 constexpr uint32_t kOffFew = kOffSeg + kQueue * kSegBytes + 16;  // (+ TMEM address) D's barriers, three a warp
@@ -700,6 +703,7 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
         if (ask.more) id = id_of();
     };
     for (int i = 0; i < kFewStages; ++i) load();
+    failed |= (a.fault & HSQ_FAULT_WAIT_FEW) != 0;
     // lane's row of the 8 x 8 matrices that ldmatrix takes: K: keys (lane & 15), chunks 2 kk + (lane >> 4);
     // V: keys (lane & 7) + 8 (lane >> 4), chunks 2 i + ((lane >> 3) & 1)
     const uint32_t k_row = (lane & 15) * 128, k_x = lane & 7, k_c = lane >> 4;
@@ -738,7 +742,7 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
 #pragma unroll 1
         for (int s = now.s; s < now.s1; ++s) {
             const uint32_t kb = stages + out.stage * kFewStageBytes, vb = kb + 4096;
-            mbar_wait_fast(bars + 8 * out.stage, out.phase, failed);
+            mbar_wait_fast(bars + 8 * out.stage, out.phase, failed, a.polls);
             const bool gone = (missing >> out.stage) & 1u;
             const int valid = now.len - 16 * s;  // keys of the group that the request has
             if (valid < 16) {  // the rest of the page is stale: weight 0, but it has to be finite
@@ -758,7 +762,7 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma_16816(x[nt], k, qf[nt][kk][0], qf[nt][kk][1]);
             }
-            bool look = false;
+            bool look = failed;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -767,6 +771,8 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
                     look |= x[nt][e] * kLogitScaleLog2 > m[nt][e & 1] * kLogitScaleLog2 + 8.f;  // (the first key raises from -inf)
                 }
             if (__any_sync(kFull, look)) {
+                failed = __any_sync(kFull, failed);
+                if (failed) break;  // (a stage whose copy may still be under way is not asked for again)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -808,6 +814,7 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
             out.advance();
             load();
         }
+        if (failed) break;
         const size_t slot = (size_t)now.b * a.Hkv + now.h + run * kFewWarps + warp;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -826,10 +833,9 @@ __device__ __forceinline__ void few_rows(const SharedArgs& a, const CUtensorMap&
                     }
                 }
             }
-        failed = __any_sync(kFull, failed);
         now.next_item();
     }
-    if (failed)  // see the copies in flight land before the CTA ends
+    if (failed)  // see the copies in flight (one a stage at most) land before the CTA ends
         for (int i = 0; i < kFewStages; ++i)
             mbar_wait(bars + 8 * i, i < (int)in.stage ? in.phase : in.phase ^ 1, 1 << 12);
 }
@@ -845,7 +851,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t full = base + kOffBars, empty = full + 8 * kStages, q_full = empty + 8 * kStages, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_full = p_full + 16, tail = o_full + 16;
-    const uint32_t seg_full = tail + 8, seg_empty = seg_full + 8 * kQueue;
+    const uint32_t drain = tail + 8, seg_full = drain + 8, seg_empty = seg_full + 8 * kQueue;
     volatile uint32_t* s_mask = reinterpret_cast<volatile uint32_t*>(gbase + kOffMask);
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffSeg + kQueue * kSegBytes);
     int bad = 0;
@@ -863,6 +869,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(o_full + 8 * i, 1);
         }
         mbar_init(tail, 1);
+        mbar_init(drain, 1);
         for (int i = 0; i < kQueue; ++i) {
             mbar_init(seg_full + 8 * i, 1);
             mbar_init(seg_empty + 8 * i, kSegReaders);
@@ -893,10 +900,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t tmem = *s_tmem;
     bool failed = false;
     Segment s;
+    // A wait that runs out sets its warp's `failed`.  From there on the warp arms no barrier, starts no copy and writes no segment
+    // (a stage or a queue place may still be in use), sees what it has in flight to its end and stops; the others' waits then run
+    // out in turn.  The results are undefined, the error word says so, and the next call finds everything as it should be.
+    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_fast(bar, parity, failed, a.polls); };
 
     // the next segment of the queue, read by one thread or by a warp
     auto receive = [&](Ring<kQueue>& q, bool release) {
-        mbar_wait_fast(seg_full + 8 * q.stage, q.phase, failed);
+        wait(seg_full + 8 * q.stage, q.phase);
         const int4* src = reinterpret_cast<const int4*>(gbase + kOffSeg + q.stage * kSegBytes);
         int4* dst = reinterpret_cast<int4*>(&s);
         if (release) failed = __any_sync(kFull, failed);  // (a warp stays together)
@@ -928,6 +939,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ValueRing vr{0, 1};
             Ring<kQueue> queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
             uint32_t step = 0, tail_par = 0;
+            bool tail_due = false;
             const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
             const PlanHead plan = *a.head;
             Walker walk{a, plan};
@@ -935,8 +947,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             CutRecord cut{0, 0, 0, 0, 0, 0, 0, 0};
             int flip = 0;
             auto send = [&] {
-                mbar_wait_fast(seg_empty + 8 * queue.stage, queue.phase, failed);
+                wait(seg_empty + 8 * queue.stage, queue.phase);
                 failed = __any_sync(kFull, failed);
+                if (failed) return;
                 if (lane == 0) {
                     *reinterpret_cast<Segment*>(gbase + kOffSeg + queue.stage * kSegBytes) = s;
                     mbar_arrive(seg_full + 8 * queue.stage);
@@ -990,8 +1003,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int kv = 0; kv < 2; ++kv) {
                         const uint32_t slot = kv ? kKeyStages + vr.stage : kr.stage;
                         const uint32_t stage = base + slot * kTileBytes, bar = full + 8 * slot;
-                        mbar_wait_fast(empty + 8 * slot, kv ? vr.phase : kr.phase, failed);
+                        wait(empty + 8 * slot, kv ? vr.phase : kr.phase);
+                        if (kv) failed |= (a.fault & HSQ_FAULT_WAIT_LOAD) != 0;
                         failed = __any_sync(kFull, failed);
+                        if (failed) break;
                         // The values of a tile that does not end on a multiple of 16 keys: the rows up to there
                         // hold what the page holds; their weights are 0, so they have to be finite.  Cleared
                         // here before the tile is handed over.
@@ -1008,8 +1023,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tma_2d(stage + lane * half_page + kHalfBytes, map, 64, y, lands);
                         }
                         if (ragged) {
-                            mbar_wait_fast(tail, tail_par, failed);
+                            wait(tail, tail_par);
                             failed = __any_sync(kFull, failed);
+                            if (failed) {
+                                tail_due = true;
+                                break;
+                            }
                             tail_par ^= 1;
                             const int z = (16 - (nk & 15)) * 16;  // 16-byte chunks in both halves
                             for (int i = lane; i < z; i += 32)
@@ -1028,11 +1047,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             s.kind = kEnd;
             send();
             if (lane == 0 && blockIdx.x >= plan.runs_a) *reinterpret_cast<CutRecord*>(a.cut + 16 * walk.run) = cut;
-            if (failed)  // see the copies in flight land before the CTA ends
+            if (failed) {  // see the copies in flight land before the CTA ends
                 for (int i = 0; i < kStages; ++i) {
                     const bool lap = i < kKeyStages ? i < (int)kr.stage : i - kKeyStages < (int)vr.stage;
                     mbar_wait(full + 8 * i, (i < kKeyStages ? kr.phase : vr.phase) ^ (lap ? 1u : 0u), 1 << 12);
                 }
+                if (tail_due) mbar_wait(tail, tail_par, 1 << 12);
+            }
         } else if (warp == 9 && elect_one()) {
             // ---- MMAs, one thread ----
             // Straight code: per pair of key tiles four waits, each one poll; the tensor pipe takes an MMA every 64
@@ -1055,7 +1076,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             auto product = [&](int st, uint32_t begun) {  // O += P V of the whole tile at vr
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
                 const uint64_t dv = sw128_mn_desc(base + (kKeyStages + vr.stage) * kTileBytes, kHalfBytes);
-                mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
+                wait(p_full + 8 * st, (p_par >> st) & 1);
                 p_par ^= 1u << st;
                 tc_fence_after();
                 mma_bf16_ts(dO, pa, dv, idO, begun);
@@ -1065,14 +1086,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             auto product_n = [&](int st, int ks16, uint32_t begun) {  // the same of a tile of ks16 groups of 16 keys
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
                 const uint64_t dv = sw128_mn_desc(base + (kKeyStages + vr.stage) * kTileBytes, kHalfBytes);
-                mbar_wait_fast(p_full + 8 * st, (p_par >> st) & 1, failed);
+                wait(p_full + 8 * st, (p_par >> st) & 1);
                 p_par ^= 1u << st;
                 tc_fence_after();
 #pragma unroll 1
                 for (int k = 0; k < ks16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, begun | (k > 0));
             };
-            auto k_wait = [&] { mbar_wait_fast(full + 8 * kr.stage, kr.phase, failed); };
-            auto v_wait = [&] { mbar_wait_fast(full + 8 * (kKeyStages + vr.stage), vr.phase, failed); };
+            auto k_wait = [&] { wait(full + 8 * kr.stage, kr.phase); };
+            auto v_wait = [&] { wait(full + 8 * (kKeyStages + vr.stage), vr.phase); };
             auto k_done = [&] { mma_commit(empty + 8 * kr.stage); kr.advance(); };
             auto v_done = [&] { mma_commit(empty + 8 * (kKeyStages + vr.stage)); vr.advance(); };
             auto groups = [&](int n) { return (keys_of(a, s, n) + 15) >> 4; };
@@ -1086,88 +1107,104 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 v_wait();
                 if ((due >> 8) == 8) product(st, !(due & 2));
                 else product_n(st, due >> 8, !(due & 2));
+                if (__builtin_expect(failed, 0)) return;
                 v_done();
                 if (due & 4) mma_commit(o_full + 8 * st);
                 if (st) due1 = 0; else due0 = 0;
             };
             int turn = 0;  // the stream of the next tile of a split segment: the one whose product is older
-            while (receive(queue, false)) {
-                const int n0 = s.n0, n1 = s.n1, end0 = s.end0;
-                if (s.split) {
+            // (after a wait that ran out no stage is handed back: its copy may still be under way)
+            auto work = [&] {
+                while (receive(queue, false)) {
+                    const int n0 = s.n0, n1 = s.n1, end0 = s.end0;
+                    if (s.split) {
 #pragma unroll 1
-                    for (int n = n0; n < n1; ++n) {
-                        const int st = (n - n0 + s.flip) & 1;
-                        turn = st ^ 1;
-                        settle(st);
-                        if (n - n0 < 2) {
-                            mbar_wait_fast(q_full + 8 * st, (q_par >> st) & 1, failed);
-                            q_par ^= 1u << st;
+                        for (int n = n0; n < n1; ++n) {
+                            const int st = (n - n0 + s.flip) & 1;
+                            turn = st ^ 1;
+                            settle(st);
+                            if (n - n0 < 2) {
+                                wait(q_full + 8 * st, (q_par >> st) & 1);
+                                q_par ^= 1u << st;
+                            }
+                            const int g = groups(n);
+                            k_wait();
+                            if (__builtin_expect(failed, 0)) return;
+                            scores(st, idesc_bf16_f32(128, 16 * g));
+                            k_done();
+                            if (n + 2 >= n1) mma_commit(q_empty + 8 * st);  // (the stream's last S of the segment)
+                            const uint32_t due = 1u | (n - n0 < 2 ? 2u : 0u) | (n + 2 >= n1 ? 4u : 0u) | ((uint32_t)g << 8);
+                            if (st) due1 = due; else due0 = due;
                         }
-                        const int g = groups(n);
-                        k_wait();
-                        scores(st, idesc_bf16_f32(128, 16 * g));
-                        k_done();
-                        if (n + 2 >= n1) mma_commit(q_empty + 8 * st);  // (the stream's last S of the segment)
-                        const uint32_t due = 1u | (n - n0 < 2 ? 2u : 0u) | (n + 2 >= n1 ? 4u : 0u) | ((uint32_t)g << 8);
-                        if (st) due1 = due; else due0 = due;
+                        continue;
                     }
-                    continue;
-                }
-                settle(turn);
-                settle(turn ^ 1);
-                const bool has0 = tiles_of(s, 0) > 0, has1 = tiles_of(s, 1) > 0;
-                if (has0) { mbar_wait_fast(q_full, q_par & 1, failed); q_par ^= 1; }
-                if (has1) { mbar_wait_fast(q_full + 8, (q_par >> 1) & 1, failed); q_par ^= 2; }
-                if (n1 > n0) {
-                    // the tiles that are not whole: the prefix's last and the item's last
-                    const int r1 = (a.prefix_len & 127) ? s.ptiles - 1 : -2, both = min(end0, n1 - 1);
-                    k_wait();
-                    if (n0 < end0) scores(0, idesc_bf16_f32(128, 16 * groups(n0)));
-                    scores(1, idesc_bf16_f32(128, 16 * groups(n0)));
-                    k_done();
-                    int n = n0 + 1;
-                    while (n < n1) {
-                        const int to = r1 >= n ? min(both, r1) : both;
-                        if (n - 1 != r1) {
+                    settle(turn);
+                    settle(turn ^ 1);
+                    const bool has0 = tiles_of(s, 0) > 0, has1 = tiles_of(s, 1) > 0;
+                    if (has0) { wait(q_full, q_par & 1); q_par ^= 1; }
+                    if (has1) { wait(q_full + 8, (q_par >> 1) & 1); q_par ^= 2; }
+                    if (n1 > n0) {
+                        // the tiles that are not whole: the prefix's last and the item's last
+                        const int r1 = (a.prefix_len & 127) ? s.ptiles - 1 : -2, both = min(end0, n1 - 1);
+                        k_wait();
+                        if (__builtin_expect(failed, 0)) return;
+                        if (n0 < end0) scores(0, idesc_bf16_f32(128, 16 * groups(n0)));
+                        scores(1, idesc_bf16_f32(128, 16 * groups(n0)));
+                        k_done();
+                        failed |= (a.fault & HSQ_FAULT_WAIT_MMA) != 0;
+                        int n = n0 + 1;
+                        while (n < n1) {
+                            const int to = r1 >= n ? min(both, r1) : both;
+                            if (n - 1 != r1) {
 #pragma unroll 1
-                            for (; n < to; ++n) {  // P V of tile n - 1 and S of tile n, both whole
+                                for (; n < to; ++n) {  // P V of tile n - 1 and S of tile n, both whole
+                                    k_wait();
+                                    v_wait();
+                                    product(0, n > n0 + 1);
+                                    scores(0, idFull);
+                                    product(1, n > n0 + 1);
+                                    if (__builtin_expect(failed, 0)) return;
+                                    v_done();
+                                    scores(1, idFull);
+                                    k_done();
+                                }
+                            }
+                            if (n < n1) {  // stream 0 at its end, or a tile that is not whole
+                                const uint32_t idS = idesc_bf16_f32(128, 16 * groups(n));
+                                const int gp = groups(n - 1);
                                 k_wait();
                                 v_wait();
-                                product(0, n > n0 + 1);
-                                scores(0, idFull);
-                                product(1, n > n0 + 1);
+                                if (n <= end0) product_n(0, gp, n > n0 + 1);
+                                if (n < end0) scores(0, idS);
+                                product_n(1, gp, n > n0 + 1);
+                                if (__builtin_expect(failed, 0)) return;
                                 v_done();
-                                scores(1, idFull);
+                                scores(1, idS);
                                 k_done();
+                                ++n;
                             }
                         }
-                        if (n < n1) {  // stream 0 at its end, or a tile that is not whole
-                            const uint32_t idS = idesc_bf16_f32(128, 16 * groups(n));
-                            const int gp = groups(n - 1);
-                            k_wait();
-                            v_wait();
-                            if (n <= end0) product_n(0, gp, n > n0 + 1);
-                            if (n < end0) scores(0, idS);
-                            product_n(1, gp, n > n0 + 1);
-                            v_done();
-                            scores(1, idS);
-                            k_done();
-                            ++n;
-                        }
+                        if (has0) mma_commit(q_empty);
+                        mma_commit(q_empty + 8);
+                        const int gp = groups(n1 - 1);
+                        v_wait();
+                        if (end0 == n1) product_n(0, gp, n1 - 1 > n0);
+                        if (has0) mma_commit(o_full);
+                        product_n(1, gp, n1 - 1 > n0);
+                        if (__builtin_expect(failed, 0)) return;
+                        mma_commit(o_full + 8);
+                        v_done();
                     }
-                    if (has0) mma_commit(q_empty);
-                    mma_commit(q_empty + 8);
-                    const int gp = groups(n1 - 1);
-                    v_wait();
-                    if (end0 == n1) product_n(0, gp, n1 - 1 > n0);
-                    if (has0) mma_commit(o_full);
-                    product_n(1, gp, n1 - 1 > n0);
-                    mma_commit(o_full + 8);
-                    v_done();
                 }
+                if (failed) return;
+                settle(turn);
+                settle(turn ^ 1);
+            };
+            work();
+            if (failed) {  // what is in flight ends before its operands' and results' memory is given up
+                mma_commit(drain);
+                mbar_wait(drain, 0, 1 << 12);
             }
-            settle(turn);
-            settle(turn ^ 1);
         } else if (warp == 10) {
             // ---- queries of the segments' streams ----
             asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1181,8 +1218,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (tiles_of(s, st) <= 0) continue;
                     const uint32_t dst = base + kOffQ + st * kTileBytes, bar = q_full + 8 * st;
                     const int tok = st ? s.tok1 : s.tok0, toks = st ? s.toks1 : s.toks0;
-                    mbar_wait_fast(q_empty + 8 * st, (q_par >> st) & 1, failed);
+                    wait(q_empty + 8 * st, (q_par >> st) & 1);
+                    if (st) failed |= (a.fault & HSQ_FAULT_WAIT_QUERY) != 0;
                     failed = __any_sync(kFull, failed);
+                    if (failed) break;
                     q_par ^= 1u << st;
                     if (s.kind != kPrefixItem || plan.dense) {  // tokens side by side
                         const int row = s.kind == kPrefixItem ? plan.base + tok : tok;
@@ -1247,7 +1286,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int n = s.n0 + (s.split ? st ^ s.flip : 0); n < stop; n += s.split ? 2 : 1) {
-                mbar_wait_fast(s_full + 8 * st, s_par, failed);
+                wait(s_full + 8 * st, s_par);
                 s_par ^= 1;
                 if (!idle) {
                     // The running maximum need not be one: any m that keeps the sums in range gives the same
@@ -1337,9 +1376,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             const bool any = tiles_of(s, st) > 0;
             if (any) {
-                mbar_wait_fast(o_full + 8 * st, o_par, failed);
+                wait(o_full + 8 * st, o_par);
                 o_par ^= 1;
             }
+            failed |= (a.fault & HSQ_FAULT_WAIT_SOFTMAX) != 0;
             failed = __any_sync(kFull, failed);
             if (failed) break;
             tc_fence_after();
@@ -1383,8 +1423,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_before();  // (O has been read: the next segment's first P releases it)
             step0 += s.n1 - s.n0;
         }
-        // D: every stream's work of this CTA is done, its memory free
-        named_bar_sync(1, 256);
+        // D: every stream's work of this CTA is done, its memory free (where no wait ran out)
+        failed = named_bar_or(1, 256, failed);
         if (!failed)
             few_rows<NT>(a, mk16, mv16, plan, (int)blockIdx.x - plan.runs_a, warp, base + warp * kFewWarpBytes, gbase + warp * kFewWarpBytes,
                          base + kOffFew + 8 * kFewStages * warp, failed, bad);
@@ -1777,6 +1817,8 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     a.c_o = reinterpret_cast<float*>(ws + x.c_o); a.c_ml = reinterpret_cast<float2*>(ws + x.c_ml);
     a.d_o = reinterpret_cast<float*>(ws + x.d_o); a.d_ml = reinterpret_cast<float2*>(ws + x.d_ml);
     a.few_rows = x.few_rows;
+    a.fault = (int)hsq::fault_mask() & (HSQ_FAULT_WAIT_LOAD | HSQ_FAULT_WAIT_MMA | HSQ_FAULT_WAIT_QUERY | HSQ_FAULT_WAIT_SOFTMAX | HSQ_FAULT_WAIT_FEW);
+    a.polls = a.fault ? 1 << 8 : 1 << 20;
     a.err = ctx->d_err;
     CUtensorMap mq, mk, mv, mk16, mv16;
     if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");

@@ -54,8 +54,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int max
 
 // The same with the common case first: one poll and a branch that is not taken, where every taken
 // branch of a single running thread costs some 20 cycles of its issue.  A wait that runs out sets `failed`;
-// with `failed` set, waits return at once (the caller goes on without the data and ends soon).
-__device__ __forceinline__ void mbar_wait_fast(uint32_t bar, uint32_t parity, bool& failed) {
+// with `failed` set, waits return at once (the caller stops as soon as it can, and arms no barrier again).
+__device__ __forceinline__ void mbar_wait_fast(uint32_t bar, uint32_t parity, bool& failed, int max_polls) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
@@ -63,7 +63,7 @@ __device__ __forceinline__ void mbar_wait_fast(uint32_t bar, uint32_t parity, bo
         : "r"(bar), "r"(parity)
         : "memory");
     if (__builtin_expect(!done, 0)) {
-        if (!failed) failed = !mbar_wait(bar, parity);
+        if (!failed) failed = !mbar_wait(bar, parity, max_polls);
     }
 }
 
@@ -75,6 +75,17 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // barrier `id` (1..15) among `count` threads (a multiple of 32) of the CTA
 __device__ __forceinline__ void named_bar_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
+}
+
+// named_bar_sync that also tells whether `pred` was true in any of the threads
+__device__ __forceinline__ bool named_bar_or(int id, int count, bool pred) {
+    uint32_t any;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(any)
+        : "r"((uint32_t)pred), "r"(id), "r"(count)
+        : "memory");
+    return any != 0;
 }
 
 // ---- bulk copy (1-D, no tensor map): both addresses 16-byte aligned, size a multiple of 16

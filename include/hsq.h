@@ -94,11 +94,18 @@ enum {
                                  hsq_fetch_dequant) instead of gathering them from L3 */
 };
 
-/* Host-only fault injection (hsq_debug_set_fault). */
+/* Fault injection for tests (hsq_debug_set_fault). */
 enum {
     HSQ_FAULT_ALLOC = 1,      /* hsq_create fails with HSQ_ERR_NOMEM before any CUDA call */
-    HSQ_FAULT_FETCH = 2       /* hsq_fetch_dequant / hsq_decode_attn return HSQ_ERR_CUDA
+    HSQ_FAULT_FETCH = 2,      /* hsq_fetch_dequant / hsq_decode_attn return HSQ_ERR_CUDA
                                  without launching */
+    /* hsq_shared_attn: a part of its main kernel goes on as where a bounded wait has run out
+       (and all waits get a short bound): HSQ_DEVERR_WAIT, results undefined, the next call as ever */
+    HSQ_FAULT_WAIT_LOAD = 4,     /* the loads of keys and values, between the two */
+    HSQ_FAULT_WAIT_MMA = 8,      /* the issue of the products, behind a long request's first tile */
+    HSQ_FAULT_WAIT_QUERY = 16,   /* the loads of queries, between two row tiles */
+    HSQ_FAULT_WAIT_SOFTMAX = 32, /* the softmax, behind its first item */
+    HSQ_FAULT_WAIT_FEW = 64      /* requests of up to 16 rows, with their first loads under way */
 };
 
 typedef struct hsq_config {
@@ -617,7 +624,7 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
 /* hsq_last_error -- text of the last error of ctx (or of the process when ctx is NULL). */
 const char* hsq_last_error(const hsq_ctx* ctx);
 
-/* hsq_debug_set_fault -- process-wide host-side fault injection mask (HSQ_FAULT_*). */
+/* hsq_debug_set_fault -- process-wide fault injection mask (HSQ_FAULT_*), read by the host in each call. */
 hsq_status hsq_debug_set_fault(unsigned mask);
 
 /* hsq_version -- library version string. */
