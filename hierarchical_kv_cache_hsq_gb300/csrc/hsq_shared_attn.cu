@@ -86,17 +86,18 @@ struct SharedArgs {
     int rows, B, width, prefix_len, prefix_tiles, max_new, n_pages, page_n, page_shift, Hq, Hkv, r;
     int tpt;   // tokens of a row tile: 128 / r
     int runs;  // CTAs of the main kernel: an SM each
-    int own_rows;  // rows that a B item's parts have room for
+    int own_rows;  // most rows of a B item
     int tokens_cap;  // most tokens that short requests can have
     // workspace
     PlanHead* head;
     // [B][2] first row, rows, own tokens (no more than its table holds), short tokens before it | own tokens before its first
-    // row: row j sees the first min(own tokens, that + j + 1)
+    // row (row j sees the first min(own tokens, that + j + 1)), tokens of the B requests before it
     int4* req;
     int* of;                // [short tokens] their requests
     long long *c_at, *b_at, *d_at; // [B + 1] cost of the C, B and D items before request b
     int* cut;               // [runs][16 ints] the C item that run c is the second to work on (see CutRecord)
-    // parts: o [slot][2 streams][128 dims][rows], ml [slot][2 streams][rows] (maximum of q.k, unscaled; sum)
+    // parts: o [slot][2 streams][128 dims][rows], ml [slot][2 streams][rows] (maximum of q.k, unscaled; sum).  A slot of A and C has
+    // 128 rows, one of B as many as its item: they lie one item behind another, and own_rows further for each run (see own_slot).
     float *a_o, *b_o, *c_o;
     float2 *a_ml, *b_ml, *c_ml;
     // D's: o [slot][rows][128], ml [slot][rows]
@@ -157,6 +158,11 @@ __device__ __forceinline__ long long unit_base(const SharedArgs& a, int ahead) {
 __device__ __forceinline__ long long a_keys(const SharedArgs& a) {
     return a.prefix_tiles ? (long long)a.prefix_tiles * kTileKeys + kItemKeysA : 0;
 }
+// Rows before the part of a B item (KV head h of a request of n tokens, `before` tokens of B requests before it) that run i leaves:
+// from one part to the next either the item goes on by one, or the run does.
+__device__ __forceinline__ int own_slot(const SharedArgs& a, int before, int n, int h, int i) {
+    return (before * a.Hkv + h * n) * a.r + i * a.own_rows;
+}
 // cost of the units before u (u < number of units), D tokens each
 __device__ __forceinline__ long long units_before(long long base, int D, long long u) {
     return kCostLong * (u * base + D * (u * (u + 1) / 2));
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     __shared__ long long s_w[4][kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int bad = 0, disorder = 0;
-    long long before[4] = {0, 0, 0, 0};  // short tokens, C, B and D cost
+    long long before[4] = {0, 0, 0, 0};  // short tokens (and, from bit 32 on, those of B requests), C, B and D cost
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int first = 0, n = 0, len = 0, ahead = 0, l = 0;
@@ -201,8 +207,12 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         const bool brief = n <= a.tpt;
         long long x[4] = {brief ? n : 0, 0, 0, 0}, own[4];
         if (n > 0 && brief && len > 0) {
-            if (n * a.r > kFewRows) x[2] = (long long)a.Hkv * (len + kItemKeys) * kCostOwn;
-            else x[3] = a.Hkv * few_cost(len);
+            if (n * a.r > kFewRows) {
+                x[2] = (long long)a.Hkv * (len + kItemKeys) * kCostOwn;
+                x[0] |= (long long)n << 32;
+            } else {
+                x[3] = a.Hkv * few_cost(len);
+            }
         }
         if (!brief) {
             const int D = 2 * a.tpt, units = (n + D - 1) / D;
@@ -232,8 +242,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         }
         if (b < a.B) {
             a.req[2 * b] = make_int4(first, n, len, (int)x[0]);
-            a.req[2 * b + 1] = make_int4(ahead, 0, 0, 0);
-            for (int i = 0; i < own[0]; ++i) a.of[x[0] + i] = b;
+            a.req[2 * b + 1] = make_int4(ahead, (int)(x[0] >> 32), 0, 0);
+            for (int i = 0; i < (int)own[0]; ++i) a.of[(int)x[0] + i] = b;
             a.c_at[b] = x[1];
             a.b_at[b] = x[2];
             a.d_at[b] = x[3];
@@ -404,17 +414,18 @@ struct Walker {
     const PlanHead& p;
     long long at, end;      // the run, of A's lane or of the others' line
     long long w0;           // where the current item begins
-    int zone, b, h, u, n, len, first, ahead;  // the item: A (h, u = pair), C (b, h, unit u), B (b, h)
+    int zone, b, h, u, n, len, first, ahead, before;  // the item: A (h, u = pair), C (b, h, unit u), B (b, h)
     int lane, run;          // A: the CTA's lane and run; else the run
     long long cost;         // the item's
     bool more;
 
     __device__ __forceinline__ void load_request() {
-        const int4 q = a.req[2 * b];
-        ahead = a.req[2 * b + 1].x;
+        const int4 q = a.req[2 * b], e = a.req[2 * b + 1];
         first = q.x;
         n = q.y;
         len = q.z;
+        ahead = e.x;
+        before = e.y;
     }
     __device__ __forceinline__ int units() const { return (n + 2 * a.tpt - 1) / (2 * a.tpt); }
     __device__ __forceinline__ int a_rate() const { return p.lanes == 1 && u == p.pairs - 1 && (p.tiles & 1) ? kCostOne : kCostPair; }
@@ -565,7 +576,7 @@ struct Walker {
         if (zone == 0) {  // (segments of a lane in order raise item or run by one: each slot has one)
             s.slot = ((p.lanes > 1 ? h : h * p.pairs + u) + run) * p.lanes + lane;
         } else if (zone == 2) {
-            s.slot = b * a.Hkv + h + run;
+            s.slot = own_slot(a, before, n, h, run);
         } else {
             s.kind = s.n0 == 0 && s.n1 == tiles ? kWholeItem : kCutItem;
             s.slot = 2 * run + (s.n0 == 0);  // the run's first segment, or its last
@@ -1403,10 +1414,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
             } else if (!idle) {  // a part: dims apart, rows side by side, so that a warp writes whole lines
-                const int pitch = s.kind == kOwnItem ? a.own_rows : kTileRows;
-                const size_t at = (size_t)s.slot * 2 + st;
-                float* o_to = (s.kind == kPrefixItem ? a.a_o : s.kind == kOwnItem ? a.b_o : a.c_o) + at * 128 * pitch + row;
-                float2* ml_to = (s.kind == kPrefixItem ? a.a_ml : s.kind == kOwnItem ? a.b_ml : a.c_ml) + at * pitch + row;
+                const int pitch = s.kind == kOwnItem ? toks * a.r : kTileRows;
+                const size_t at = (size_t)s.slot * (s.kind == kOwnItem ? 2 : 2 * kTileRows) + st * pitch;  // rows before it
+                float* o_to = (s.kind == kPrefixItem ? a.a_o : s.kind == kOwnItem ? a.b_o : a.c_o) + at * 128 + row;
+                float2* ml_to = (s.kind == kPrefixItem ? a.a_ml : s.kind == kOwnItem ? a.b_ml : a.c_ml) + at + row;
                 if (live) *ml_to = make_float2(m, l);
                 if (any) {
 #pragma unroll 1
@@ -1497,6 +1508,7 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
         }
         const int b = live ? b_any : 0;
         const int4 q = __ldcg(a.req + 2 * b);
+        const int before = __ldcg(a.req + 2 * b + 1).y;
         const bool few = q.y * a.r <= kFewRows;
         const long long at1 = few ? p.work_t + __ldcg(a.d_at + b) : p.work_c + __ldcg(a.b_at + b);
         const int orow = live ? row - (q.w - tile * a.tpt) * a.r : 0;  // row among the request's
@@ -1526,10 +1538,10 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
             const long long w0 = at1 + h * ((long long)(q.z + kItemKeys) * kCostOwn);
             const int tiles = (q.z + kTileKeys - 1) / kTileKeys;
             const int c0 = run_of(p.work, p.runs, w0), c1 = run_of(p.work, p.runs, w0 + (long long)(tiles - 1) * kCostOwn * kTileKeys);
-            const size_t slot = ((size_t)b * a.Hkv + h + c0) * 2;
-            pitch1 = a.own_rows;
-            o1 = a.b_o + slot * 128 * pitch1 + orow;
-            ml1 = a.b_ml + slot * pitch1 + orow;
+            const size_t slot = (size_t)own_slot(a, before, q.y, h, c0) * 2;
+            pitch1 = q.y * a.r;
+            o1 = a.b_o + slot * 128 + orow;
+            ml1 = a.b_ml + slot + orow;
             n1 = 2 * (c1 - c0 + 1);
         }
         to = (size_t)(q.x + orow / a.r) * a.Hq + h * a.r + orow % a.r;
@@ -1580,12 +1592,13 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
             if (k - n0 < __shfl_sync(kFull, rows_n, row)) copy_async<16>(dst + swizzled(row, chunk), src);
         }
         if (k - n0 >= n1) return;
+        const size_t rows = by_row ? at * pitch1 : (at & ~(size_t)1) * a.own_rows + (at & 1) * pitch1;  // before part `at` of B or D
         if (!by_row) {
-            const float* src = o1 + (at * 128 + d0) * pitch1;
+            const float* src = o1 + rows * 128 + (size_t)d0 * pitch1;
 #pragma unroll
             for (int d = 0; d < kJoinDims; ++d) copy_async<4>(dst + swizzled(lane, d >> 2) + 4 * (d & 3), src + d * pitch1);
         }
-        copy_async<8>(dst + 2048 + 8 * lane, ml1 + at * pitch1);
+        copy_async<8>(dst + 2048 + 8 * lane, ml1 + rows);
     };
     float M = -INFINITY, L = 0.f, x[kJoinDims];
 #pragma unroll
@@ -1710,7 +1723,7 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     };
     const size_t Hkv = ctx->cfg.n_kv_heads, r = ctx->r, tpt = kTileRows / r;
     x.runs = ctx->num_sms;
-    x.own_rows = (int)((std::min<size_t>(max_new, tpt) * r + 3) / 4 * 4);
+    x.own_rows = (int)(std::min<size_t>(max_new, tpt) * r);
     x.head = take(sizeof(PlanHead));
     x.req = take((size_t)B * 32);
     x.c_at = take((size_t)(B + 1) * 8);
@@ -1721,12 +1734,14 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     const size_t tokens = std::min<size_t>(rows, (size_t)B * tpt), tiles = (tokens + tpt - 1) / tpt;
     x.tokens = (int)tokens;
     x.of = take(tokens * 4);
-    const size_t a = prefix_len > 0 ? Hkv * ((tiles + 1) / 2) + x.runs : 0, b = (size_t)max_new * r > kFewRows ? (size_t)B * Hkv + x.runs : 0;
+    const size_t a = prefix_len > 0 ? Hkv * ((tiles + 1) / 2) + x.runs : 0;
+    const size_t b_items = std::min<size_t>((size_t)rows * r, (size_t)B * x.own_rows);  // rows of all B requests
+    const size_t b = (size_t)max_new * r > kFewRows ? Hkv * b_items + (size_t)x.runs * x.own_rows : 0;  // rows of their parts
     const size_t c = (size_t)max_new > tpt ? 2 * (size_t)x.runs : 0;
     x.a_o = take(a * 2 * 128 * kTileRows * 4);
     x.a_ml = take(a * 2 * kTileRows * 8);
-    x.b_o = take(b * 2 * 128 * x.own_rows * 4);
-    x.b_ml = take(b * 2 * x.own_rows * 8);
+    x.b_o = take(b * 2 * 128 * 4);
+    x.b_ml = take(b * 2 * 8);
     x.c_o = take(c * 2 * 128 * kTileRows * 4);
     x.c_ml = take(c * 2 * kTileRows * 8);
     const size_t d = (size_t)B * Hkv + (size_t)kFewWarps * x.runs;

@@ -599,7 +599,8 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
  *   int32; all device memory.  max_new: the largest n_b of the step.
  *   out, lse and the workspace overlap neither each other nor an input.
  *   workspace: device memory of hsq_shared_attn_workspace_size bytes, 256-byte
- *   aligned, caller-owned; its contents are not needed before or after, but calls that may run at the
+ *   aligned, caller-owned (it holds fp32 parts of the rows' results: for rows of requests that fit a tile of 128 / r tokens a
+ *   few kilobytes a row and query head, and some tens of MB for the GPU's SMs); its contents are not needed before or after, but calls that may run at the
  *   same time need one each.  Products are bf16 with fp32 accumulation; softmax
  *   weights are rounded to bf16 for the product with the values, sums and statistics are fp32.
  *   What the pages hold past a request's length does not matter.  Keys and values before

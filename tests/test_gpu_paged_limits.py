@@ -207,3 +207,27 @@ def test_a_table_too_short_for_a_length_moves_no_row(own, new, width, lens, Hq, 
     assert err == {"LEN"}
     # (a length that puts every row past the table gives the same limits as any longer one; the bound of lse goes by it)
     check_attn(dict(x, lens=np.minimum(lens, 16 * width + np.asarray(new))), out, lse)
+
+
+@pytest.mark.parametrize("rows,B,max_new,most", [(1255, 256, 1000, 200 << 20), (5095, 4096, 1000, 700 << 20), (256, 256, 1, 80 << 20)])
+def test_the_workspace_goes_by_the_rows(rows, B, max_new, most):
+    """Decodes with one chunk of 1000 among them: no room is kept for a tile's rows of every request."""
+    import hierarchical_kv_cache_hsq_gb300 as H
+    ctx = make(32, 8, 1)
+    assert H.hsq_shared_attn_workspace_size(ctx, rows, B, 4096, max_new) <= most
+
+
+@pytest.mark.parametrize("Hq,Hkv,own,new,prefix", [
+    (8, 2, [40, 9, 700, 33, 5, 1500, 64], [32, 5, 17, 1, 5, 31, 6], 300), (8, 2, [3000, 17, 2500, 600], [17, 5, 6, 32], 0),
+    (4, 4, [128, 17, 900, 19, 2000], [128, 17, 33, 2, 100], 77), (8, 1, [50, 3, 700, 900], [16, 3, 9, 140], 100),
+    (5, 1, [25, 700, 4, 30], [25, 13, 4, 4], 2000), (8, 2, list(range(20, 220, 2)), [5 + i % 28 for i in range(100)], 40)])
+def test_parts_of_requests_of_unequal_rows_stay_in_the_workspace(Hq, Hkv, own, new, prefix):
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    x = attn_inputs(Hq, Hkv, 16, prefix, np.maximum(own, new), new, pad=1, seed=sum(new))
+    ctx = make(Hq, Hkv, len(own))
+    n = H.hsq_shared_attn_workspace_size(ctx, x["q"].shape[0], len(own), prefix, x["max_new"])
+    room = torch.full((n + (1 << 20),), 255, dtype=torch.uint8, device="cuda")
+    out, lse, err = run_attn(x, ctx, workspace=room[:n])
+    assert not err and (room[n:] == 255).all()
+    check_attn(x, out, lse)
