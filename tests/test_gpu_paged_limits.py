@@ -231,3 +231,16 @@ def test_parts_of_requests_of_unequal_rows_stay_in_the_workspace(Hq, Hkv, own, n
     out, lse, err = run_attn(x, ctx, workspace=room[:n])
     assert not err and (room[n:] == 255).all()
     check_attn(x, out, lse)
+
+
+def test_the_calls_go_to_the_current_stream():
+    """The binding takes the stream's bare handle from torch: it has to be the one that torch's public Stream gives."""
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    from hierarchical_kv_cache_hsq_gb300 import _binding
+    pool = H.allocate_pages(make(8, 2), 4, 16)
+    side = torch.cuda.Stream()
+    assert _binding._stream_on(pool, None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert _binding._stream_on(pool, None) == torch.cuda.current_stream().cuda_stream == side.cuda_stream
+    assert _binding._stream_on(pool, side) == side.cuda_stream != torch.cuda.current_stream().cuda_stream
