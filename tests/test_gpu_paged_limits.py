@@ -244,3 +244,44 @@ def test_the_calls_go_to_the_current_stream():
     with torch.cuda.stream(side):
         assert _binding._stream_on(pool, None) == torch.cuda.current_stream().cuda_stream == side.cuda_stream
     assert _binding._stream_on(pool, side) == side.cuda_stream != torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 1), (5, 1)])
+@pytest.mark.parametrize("new", [[1, 1, 1, 0], [3, 1, 2, 7]])
+@pytest.mark.parametrize("prefix", [0, 33])
+def test_few_rows_over_long_contexts_of_their_own(Hq, Hkv, new, prefix):
+    x = attn_inputs(Hq, Hkv, 32, prefix, [20011, 4096, 9, 12000], new, pad=1, seed=Hq + prefix)
+    out, lse, err = run_attn(x)
+    assert not err
+    check_attn(x, out, lse)
+
+
+def test_a_decode_step_of_rows_all_over_the_pool():
+    """The new token of each of 16 requests: a page and a position of its own, slots as a table gives them."""
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    rng = np.random.default_rng(8)
+    B, Hq, Hkv, page, max_pos = 16, 8, 2, 16, 1 << 15
+    ctx = make(Hq, Hkv, B, max_pos)
+    cached = rng.integers(0, 300, B)
+    have, need = -(-cached // page), -(-(cached + 1) // page)
+    ids = rng.permutation(int(need.sum()) + 3)
+    table, at = np.full((B, 20), -1), 0
+    for b in range(B):
+        table[b, : have[b]] = ids[at: at + have[b]]
+        at += have[b]
+    pool = H.allocate_pages(ctx, len(ids), page)
+    t = dict(table=i32(table), slots=i64([0] * B), pos=i32([0] * B), q_start=i32([0] * (B + 1)), lens=i32([0] * B), used_out=i32([0]))
+    H.hsq_page_tables(ctx, pool, i32(cached), i32([1] * B), i32(ids), i32([at]), **t, base=max_pos - 400)
+    x = torch.from_numpy(rng.standard_normal((B, Hq + 2 * Hkv, 128)).astype(np.float32)).cuda().bfloat16()
+    q, k, v = x[:, :Hq], x[:, Hq: Hq + Hkv], x[:, Hq + Hkv:]
+    rot = torch.zeros((B, Hq, 128), dtype=torch.bfloat16, device="cuda")
+    H.hsq_page_write(ctx, pool, q, k, v, t["pos"], t["slots"], rot)
+    assert word(ctx) == set()
+    zero = np.zeros(tuple(pool.k.shape))
+    slots = host(t["slots"])
+    assert len(set(slots // page)) == B and (host(t["pos"]) == max_pos - 400 + cached).all()
+    wq, wk, wv = P.page_write(zero, zero, host(q), host(k), host(v), host(t["pos"]), slots, THETA, max_pos)
+    for got, want in ((host(rot), wq), (host(pool.k), wk), (host(pool.v), wv)):
+        # one rounding to bf16, and cos and sin from float32 tables: under 8 roundings of 2^-24 of |lo| + |hi| <= 12
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 12 * 2.0 ** -21).all()
