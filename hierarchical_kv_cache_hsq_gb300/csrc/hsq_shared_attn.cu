@@ -6,8 +6,8 @@
 // sum of the softmaxes over each: with m, l, o a reference exponent, the sum of
 // exp(x - m) and the sum of exp(x - m) v of a part,
 //     out = sum_p exp(m_p - M) o_p / sum_p exp(m_p - M) l_p,   M = max_p m_p,
-// so the prefix is read once for all rows of the batch, each request's own pages
-// once for its rows, and the parts are joined at the end.
+// so a pass over the prefix serves rows of any requests, a pass over a request's own pages all of
+// its rows, and the parts are joined at the end.
 //
 // Rows.  The r = Hq / Hkv query heads of a KV head and the rows of the batch make
 // one row index (token * r + head): a tile of 128 rows holds floor(128 / r) tokens
@@ -15,7 +15,7 @@
 // step too.
 //
 // Work.  A request is short when its new tokens fit one tile (n <= 128 / r: decode,
-// proposals), else long (a prompt's chunk).  Three kinds of items:
+// proposals), else long (a prompt's chunk).  Four kinds of items:
 //   A  (KV head, pair of row tiles of the short requests' tokens, packed): the prefix;
 //   B  (short request of more than 16 rows, n r > 16, KV head): its own tokens;
 //   C  (long request, KV head, pair of its row tiles): the prefix, then its own
@@ -26,8 +26,9 @@
 // one after another make a line of cost, cut into as many equal runs as it has CTAs.  So
 // some SMs work on A, bound by the tensor cores, while others stream D's pages, bound
 // by HBM, and both are in use throughout.  A's line is the prefix's keys, head by head; up
-// to four pairs of row tiles have a line each, cut alike, so that CTAs side by side read
-// the same key tiles at the same time and HBM gives them once.
+// to four pairs of row tiles have a line (a lane) each, cut alike, so that CTAs side by side read
+// the same key tiles at the same time and HBM gives them once; more pairs go over the prefix one after
+// another, as every pair of a long request's row tiles does.
 //
 // Three kernels, the later two launched with programmatic serialization (their set-up
 // runs while the one before ends):
@@ -38,9 +39,11 @@
 //   shared_join_kernel   joins the parts.
 //
 // Rounding: q, k and v are bf16, products exact, sums fp32; the softmax weights are
-// rounded to bf16 for the product with the values (an error of 2^-9 of each weight
-// at most, random over the keys, where the output's own rounding is 2^-9 of the
-// result); l sums them before that rounding.
+// rounded to bf16 for the product with the values (an error of 2^-8 of each weight
+// at most, random over the keys, where the output's own rounding is up to 2^-8 of the
+// result); l sums them before that rounding.  Against 64 bits the result is off by 0.0018 to
+// 0.0023 of its size, where rounding the exact one gives 0.0017.  (Two bf16 terms for each weight, as the
+// prefill has them, would be half as many products again on the pipe that bounds the prompts.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -61,7 +64,8 @@ constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which t
 // timing; one up or down, in us: pairs 112.8 / 107.6 / 109.0 (9, 10, 11) and D's groups below 114.3 / 107.6 / 116.4 (3, 4,
 // 5) for 128 requests over a prefix of 32K; one tile 97.5 instead of 91.9 (9, 8) for 8 requests with a chunk of 1000
 // among them; C 93.8 / 92.0 / 91.3 (6, 7, 8) for those and 361 / 359 / 359.5 for four prompts of 1024; A's items
-// without the 128 keys 38.1 instead of 36.4 for 16 requests over 8K.  (Runs of one build differ by 3 %.)
+// without the 128 keys 38.1 instead of 36.4 for 16 requests over 8K.  (Runs of one build differ by 3 %.)  They do not
+// know the head ratio or the rows of a few-rows item.
 constexpr int kCostPair = 10, kCostOne = 8, kCostLong = 7, kCostOwn = 6, kItemKeys = 96, kItemKeysA = 128;
 // D: requests of up to kFewRows rows; a group is 16 keys of one warp, kFewWarps warps share a CTA's run
 constexpr int kFewRows = 16, kFewWarps = 8, kCostFew = 4, kFewItemKeys = 64;
@@ -259,6 +263,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         h.pairs = (h.tiles + 1) >> 1;
         const long long keys = a_keys(a);
         const long long full = h.tiles >> 1, one = h.tiles & 1;
+        // Lanes for up to four pairs.  With lanes and with one line, us: 2 pairs 108.2 / 108.2 (128 requests over 32K), 81.1 / 81.5
+        // (over 2K), verification 46.9 / 47.1; 3 pairs 53.7 / 53.7; 4 pairs 67.4 / 68.0 (128 x 8 heads over 8K); 61 requests of 5 heads,
+        // whose second lane is half empty, 44.2 / 40.5.  Eight lanes would gain for 8 pairs over a long prefix (240 / 257 over 32K, 107.9 /
+        // 109.3 over 8K) and lose over a short one (89.8 / 88.1 over 1K).
         h.lanes = h.pairs <= 4 ? max(h.pairs, 1) : 1;
         // (lanes are cut alike, so a pair of one tile counts as a whole one there)
         h.head_a = h.pairs == 0 ? 0 : h.lanes == 1 ? keys * (full * kCostPair + one * kCostOne) : keys * kCostPair;
@@ -326,8 +334,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // Main kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7 (stream 1),
 // warp 8 walks the run and loads keys and values, warp 9 issues the MMAs (one elected thread), warp 10 loads
 // the queries, warp 11 fetches tensor maps and page ids ahead (168 registers a thread at launch, then 176 for the
-// softmax warps, whose row of logits lives in registers, and 152 for the others; four prompts 349 us, with 168 for all 357,
-// with 184 and 136, where the warps of 136 spill, 357).
+// softmax warps, whose row of logits lives in registers, and 152 for the others; at the time four prompts 349 us, with 168 for
+// all 357, with 184 and 136, where the warps of 136 spill, 357).  NT: D's tiles of 8 rows, 1 where max_new * r <= 8, else 2, which
+// decode runs too (16 requests 37.1 and 37.3 us, 128 over 32K 107.5 and 128.6).
 // A stream is a 128-row query tile with its S / P and O in tensor memory.  The two streams
 // either hold two row tiles and share every key tile (so keys and values are loaded once
 // for 256 rows), or (split) hold the same rows and take the key tiles in turn.  While
@@ -335,11 +344,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 //   shared memory: a ring of three K tiles and one of two V tiles, 32 KB each (TMA, 128-byte swizzle; in
 //     one ring of five a key tile had to wait for the P V of three tiles before), two Q tiles;
 //   tensor memory: S of stream s at columns 128 s (P, bf16, over its first 64), O at 256 + 128 s.
-// What it reaches: four prompts of 1024 over a prefix of 8192 (32/8 heads, 0.58 TFLOP) 340 us of the call's 349
-// to 359, 1.7 PFLOP/s, the tensor pipe 77 % of the time active; bound by the pipe and by what a key tile costs beside it (a
+// What it reaches: four prompts of 1024 over a prefix of 8192 (32/8 heads, 0.58 TFLOP) 345 us of the call's 357
+// to 366 (384 for seconds on end, under the power limit), 1.7 PFLOP/s, the tensor pipe 75 % of the time active; bound by the pipe and by what a key tile costs beside it (a
 // 128 x 128 x 16 MMA takes 64 cycles in any of the forms used here, so a key tile of two row tiles 2048, 1.07 us at 1.9
 // GHz; it takes 1.4).  128 requests over 32K: 98 us for 500 MB, 5.1 TB/s, bound by HBM with some 25 us
-// of start and end.  Few requests (16 over 8K, 79 MB, 25 us): bound by the latencies of start, first loads and end.
+// of start and end.  Few requests (16 over 8K, 79 MB, 27 us): bound by the latencies of start, first loads and end.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kStages = kKeyStages + kValueStages, kQueue = 4;

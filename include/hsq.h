@@ -512,8 +512,10 @@ hsq_status hsq_route_noalloc(const hsq_config* cfg, const hsq_cache* cache, cons
  * Paged serving of uncompressed tokens: the tokens that a batch's requests
  * share (a long common prompt) and those they have just made, as bf16 keys and
  * values in pages of one pool, before (or without) an encode into the tiers.
- * The pages have no counterpart in the summaries; the attention is the model's
- * ordinary one, as in hsq_prefill.  One serving step is hsq_page_tables, then per
+ * The pages have no counterpart in the summaries and do not feed them: hsq_encode, hsq_append
+ * and hsq_prefill take keys before RoPE, which a page no longer holds, so a program that will encode these
+ * tokens later keeps them as they were made.  The attention is the model's ordinary one (hsq_prefill's formula, with bf16
+ * softmax weights and results instead of its split terms and fp32).  One serving step is hsq_page_tables, then per
  * layer hsq_page_write and hsq_shared_attn; none of them allocates, synchronises or
  * keeps state, so a step may be captured into a graph and replayed while
  * the device-side lengths and tables change.
@@ -585,12 +587,13 @@ hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const 
 
 /*
  * hsq_shared_attn -- attention of a batch whose requests share a prefix.  The prefix's
- *   keys and values are read once for all requests.  Row i = q_start[b] + j of
+ *   keys and values are read for rows of all requests together: once for every eight tiles of 128 / (Hq / Hkv) rows of
+ *   requests that fit one tile (where they are no more than eight; else for every two), and for every two tiles of a longer request.  Row i = q_start[b] + j of
  *   request b, query head jq of KV head h = jq / (Hq / Hkv): one softmax, scale
  *   1/sqrt(128), over the prefix's tokens [0, prefix_len) and the request's own
  *   tokens s <= lens[b] - n_b + j (n_b = q_start[b + 1] - q_start[b]; s >= 0).
  *   out[i][jq] the weighted values, lse[i][jq] (optional) the natural log of the sum of
- *   the exponentials (to merge with attention over other tokens).  A row without
+ *   the exponentials (to merge with attention over other tokens that also gives one; hsq_decode_attn does not).  A row without
  *   any token to see gets out = 0 and lse = -inf.  Rows from q_start[B] on are
  *   left as they were.
  *   q: [rows][Hq][128] bf16, rotated (q_out of hsq_page_write); out: the
