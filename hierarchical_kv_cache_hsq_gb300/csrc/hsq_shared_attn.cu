@@ -1842,7 +1842,7 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
     a.d_o = reinterpret_cast<float*>(ws + x.d_o); a.d_ml = reinterpret_cast<float2*>(ws + x.d_ml);
     a.few_rows = x.few_rows;
     a.fault = (int)hsq::fault_mask() & (HSQ_FAULT_WAIT_LOAD | HSQ_FAULT_WAIT_MMA | HSQ_FAULT_WAIT_QUERY | HSQ_FAULT_WAIT_SOFTMAX | HSQ_FAULT_WAIT_FEW);
-    a.polls = a.fault ? 1 << 8 : 1 << 20;
+    a.polls = a.fault ? 1 << 8 : 1 << 18;  // (a poll that finds nothing takes 4 us: 1 ms, or a second, where no wait in use takes 10 ms)
     a.err = ctx->d_err;
     CUtensorMap mq, mk, mv, mk16, mv16;
     if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
