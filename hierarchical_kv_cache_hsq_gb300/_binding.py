@@ -35,6 +35,7 @@ BUFFERS = ["l1_kc", "l1_vc", "l1_kn", "l1_vn", "l1_pos", "l1_count", "l2_kc", "l
            "hot_rec", "hot_tag"]
 HSQ_NBUF = len(BUFFERS)
 CODECS = {"tq": 0, "plain": 1}  # hsq_codec
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3}
 
 
 class HSQError(RuntimeError):
@@ -75,9 +76,18 @@ class hsq_pages(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_n", ctypes.c_int)]
 
 
+class hsq_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("dims", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("max_pos", ctypes.c_int)]
+
+
+class hsq_summaries(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
 _lib = None
 _vp = ctypes.c_void_p
-_int, _i64 = ctypes.c_int, ctypes.c_int64
+_int, _i64, _f64 = ctypes.c_int, ctypes.c_int64, ctypes.c_double
 _SIGS = {
     "hsq_codebook": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _vp, _vp]),
     "hsq_cache_sizes": (ctypes.c_int, [ctypes.POINTER(hsq_config), ctypes.c_int, ctypes.c_int, _vp]),
@@ -100,6 +110,16 @@ _SIGS = {
                               _vp]),
     "hsq_shared_attn_workspace_size": (_int, [_vp] + [_int] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
     "hsq_shared_attn": (_int, [_vp, ctypes.POINTER(hsq_pages)] + [_int] * 5 + [_vp] * 8 + [ctypes.c_size_t, _vp]),
+    "hsq_rope_frequencies": (_int, [_int, _int] + [_f64] * 5 + [_vp, _vp]),
+    "hsq_rope_table": (_int, [_int, _vp, _f64, _int, _vp, ctypes.POINTER(ctypes.c_size_t)]),
+    "hsq_page_write_rope": (_int, [_vp, ctypes.POINTER(hsq_pages), ctypes.POINTER(hsq_rope), _int, _vp, _vp, _vp, _i64, _i64,
+                                   _i64, _int, _vp, _vp, _vp, _vp]),
+    "hsq_page_summaries": (_int, [_vp, ctypes.POINTER(hsq_pages), ctypes.POINTER(hsq_summaries), _int, _vp, _vp]),
+    "hsq_page_select_workspace_size": (_int, [_vp] + [_int] * 7 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "hsq_page_select": (_int, [_vp, ctypes.POINTER(hsq_pages), ctypes.POINTER(hsq_summaries)] + [_int] * 8 + [_vp] * 7 +
+                        [ctypes.c_size_t, _vp]),
+    "hsq_page_attn_workspace_size": (_int, [_vp] + [_int] * 7 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "hsq_page_attn": (_int, [_vp, ctypes.POINTER(hsq_pages)] + [_int] * 6 + [_vp] * 9 + [ctypes.c_size_t, _vp]),
     "hsq_last_error": (ctypes.c_char_p, [_vp]),
     "hsq_debug_set_fault": (ctypes.c_int, [ctypes.c_uint]),
     "hsq_version": (ctypes.c_char_p, []),
@@ -191,6 +211,36 @@ def hsq_debug_set_fault(mask: int):
 
 def hsq_version() -> str:
     return load_library().hsq_version().decode()
+
+
+def hsq_rope_frequencies(dims: int = 128, theta: float = 1.0e6, scaling: str = "none", factor: float = 1.0,
+                         original: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(omega float64 [dims / 2], amplitude) of a rotation: scaling "none", "linear" (positions / factor), "base"
+    (theta factor^(dims / (dims - 2))) or "yarn" (from the frequencies that turn more than beta_fast times over the
+    `original` context, kept, to those below beta_slow, / factor; amplitude 0.1 ln(factor) + 1)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {tuple(ROPE_SCALINGS)}")
+    omega, amp = np.zeros(64, np.float64), _f64(0.0)
+    st = load_library().hsq_rope_frequencies(ROPE_SCALINGS[scaling], _c_int(dims), theta, factor, original, beta_fast, beta_slow,
+                                             omega.ctypes.data, ctypes.addressof(amp))
+    if st:
+        raise HSQError(st, "hsq_rope_frequencies: bad dims, theta, factor, original or betas")
+    return omega[: dims // 2].copy(), amp.value
+
+
+def hsq_rope_table(omega, amplitude: float, max_pos: int) -> np.ndarray:
+    """The rows (float32 [256 + ceil(max_pos / 256), dims]) that a rotation by the angles p omega is put together from."""
+    omega = np.ascontiguousarray(omega, np.float64)
+    dims, n = _c_int(2 * omega.size), ctypes.c_size_t(0)
+    lib = load_library()
+    st = lib.hsq_rope_table(dims, None, amplitude, _c_int(max_pos), None, ctypes.byref(n))
+    if not st:
+        out = np.empty((n.value // dims, dims), np.float32)
+        st = lib.hsq_rope_table(dims, omega.ctypes.data, amplitude, max_pos, out.ctypes.data, ctypes.byref(n))
+    if st:
+        raise HSQError(st, "hsq_rope_table: dims (twice the frequencies) must be a multiple of 8 in [8, 128], max_pos in "
+                           "[1, 2^24], the frequencies and the amplitude finite")
+    return out
 
 
 # -- context and cache ---------------------------------------------------------------
@@ -493,6 +543,74 @@ def allocate_pages(ctx: Context, n_pages: int, page_n: int, device=None) -> Page
                     torch.zeros(shape, dtype=torch.bfloat16, device=dev))
 
 
+@dataclass(frozen=True, eq=False)
+class Rope:
+    """A rotation of the first `dims` dims of a head for hsq_page_write: its table (float32
+    [256 + ceil(max_pos / 256), dims] of hsq_rope_table, on the GPU), pairs (i, i + dims / 2) or, interleaved, (2 i, 2 i + 1)."""
+    table: "object"
+    interleaved: bool
+    max_pos: int
+
+    def __post_init__(self):
+        import torch
+        t = self.table
+        if t.dtype != torch.float32 or t.dim() != 2 or not (t.is_cuda and t.is_contiguous()):
+            raise ValueError("table must be contiguous float32 [rows, dims] on the GPU")
+        if not 1 <= self.max_pos <= 1 << 24 or t.shape[0] != 256 + -(-self.max_pos // 256):
+            raise ValueError("table must have 256 + ceil(max_pos / 256) rows, max_pos in [1, 2^24]")
+        c = hsq_rope(table=t.data_ptr(), dims=t.shape[1], interleaved=1 if self.interleaved else 0, max_pos=self.max_pos)
+        for name, value in (("index", t.get_device()), ("_c", c), ("ref", ctypes.byref(c))):
+            object.__setattr__(self, name, value)
+
+    @property
+    def dims(self) -> int:
+        return self._c.dims
+
+
+def make_rope(ctx: Context, dims: int = 128, interleaved: bool = False, theta: Optional[float] = None,
+              scaling: str = "none", factor: float = 1.0, original: float = 0.0, beta_fast: float = 32.0,
+              beta_slow: float = 1.0, omega=None, amplitude: Optional[float] = None, max_pos: Optional[int] = None,
+              device=None) -> Rope:
+    """A rotation by hsq_rope_frequencies (theta and max_pos: the context's unless given), or by a model's own
+    frequencies omega [dims / 2]; amplitude: the scaling's unless given."""
+    import torch
+    if omega is None:
+        omega, amp = hsq_rope_frequencies(dims, ctx.cfg.rope_theta if theta is None else theta, scaling, factor, original,
+                                          beta_fast, beta_slow)
+    else:
+        amp = 1.0
+    max_pos = ctx.cfg.max_pos if max_pos is None else max_pos
+    table = hsq_rope_table(omega, amp if amplitude is None else amplitude, max_pos)
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    return Rope(torch.from_numpy(table).to(dev), interleaved, max_pos)
+
+
+@dataclass(frozen=True, eq=False)
+class PageSummaries:
+    """The 8-bit summaries of a pool's pages: codes int8 [n_pages, Hkv, 128] and scale float32 [n_pages, Hkv]."""
+    codes: "object"
+    scale: "object"
+
+    def __post_init__(self):
+        import torch
+        c, s = self.codes, self.scale
+        if c.dtype != torch.int8 or c.dim() != 3 or c.shape[2] != 128 or not (c.is_cuda and c.is_contiguous()):
+            raise ValueError("codes must be contiguous int8 [n_pages, Hkv, 128] on the GPU")
+        if s.dtype != torch.float32 or s.shape != c.shape[:2] or s.device != c.device or not s.is_contiguous():
+            raise ValueError("scale must be contiguous float32 [n_pages, Hkv] on the codes' device")
+        v = hsq_summaries(codes=c.data_ptr(), scale=s.data_ptr())
+        for name, value in (("index", c.get_device()), ("shape", tuple(c.shape[:2])), ("_c", v), ("ref", ctypes.byref(v))):
+            object.__setattr__(self, name, value)
+
+
+def allocate_summaries(ctx: Context, pool: PagePool) -> PageSummaries:
+    """Summaries of the pool's pages (0 until hsq_page_summaries makes them)."""
+    import torch
+    shape = (pool.n_pages, ctx.cfg.n_kv_heads)
+    return PageSummaries(torch.zeros(shape + (128,), dtype=torch.int8, device=pool.k.device),
+                         torch.zeros(shape, dtype=torch.float32, device=pool.k.device))
+
+
 def _need(pool: PagePool, dtype, names: str, *tensors):
     """Every tensor given is contiguous, of this type and on the pool's device (names: theirs, in order)."""
     index = pool.index
@@ -551,11 +669,13 @@ def hsq_page_tables(ctx: Context, pool: PagePool, cached, fresh, free_ids, used,
         _check(st, ctx.handle)
 
 
-def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, stream=None):
+def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, stream=None,
+                   rope: Optional[Rope] = None):
     """Rotate q [rows, Hq, 128] and k [rows, Hkv, 128] (bfloat16 or float32; rows may be
     strided, as views of one fused projection) at pos and store k and v [rows, Hkv, 128]
     in the pool at slots; q_out bfloat16 [rows, Hq, 128] gets the rotated queries
-    (q and q_out may both be None).  Rows with pos < 0 are skipped; a slot < 0 stores nothing."""
+    (q and q_out may both be None).  Rows with pos < 0 are skipped; a slot < 0 stores nothing.
+    rope: the model's own rotation (make_rope) in place of the context's."""
     import torch
     _need_heads(ctx, pool)
     _need(pool, torch.int32, "pos", pos)
@@ -583,10 +703,15 @@ def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, str
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
     one = rows == 1  # (the row stride of a single row says nothing)
-    st = ctx.lib.hsq_page_write(ctx.handle, pool.ref, rows, _ptr(q), k.data_ptr(), v.data_ptr(),
-                                0 if q is None else ctx.cfg.n_q_heads * 128 if one else q.stride(0),
-                                Hkv * 128 if one else k.stride(0), Hkv * 128 if one else v.stride(0), dt,
-                                pos.data_ptr(), slots.data_ptr(), _ptr(q_out), _stream_on(pool, stream))
+    args = (rows, _ptr(q), k.data_ptr(), v.data_ptr(), 0 if q is None else ctx.cfg.n_q_heads * 128 if one else q.stride(0),
+            Hkv * 128 if one else k.stride(0), Hkv * 128 if one else v.stride(0), dt, pos.data_ptr(), slots.data_ptr(),
+            _ptr(q_out), _stream_on(pool, stream))
+    if rope is None:
+        st = ctx.lib.hsq_page_write(ctx.handle, pool.ref, *args)
+    else:
+        if rope.index != pool.index:
+            raise ValueError("the rope's table is not on the pool's device")
+        st = ctx.lib.hsq_page_write_rope(ctx.handle, pool.ref, rope.ref, *args)
     if st:
         _check(st, ctx.handle)
 
@@ -635,6 +760,104 @@ def hsq_shared_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, out, 
                                  prefix.data_ptr() if prefix_len > 0 else None, out.data_ptr(), _ptr(lse),
                                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                  _stream_on(pool, stream))
+    if st:
+        _check(st, ctx.handle)
+
+
+def hsq_page_summaries(ctx: Context, pool: PagePool, sums: PageSummaries, slots, stream=None):
+    """Summaries of the pages that slots (int64 [rows], hsq_page_tables's) name, over the tokens that they hold once the
+    step's keys are written (hsq_page_write first); the other pages' are left as they were."""
+    import torch
+    _need_heads(ctx, pool)
+    _need_summaries(pool, sums)
+    _need(pool, torch.int64, "slots", slots)
+    rows = slots.numel()
+    st = ctx.lib.hsq_page_summaries(ctx.handle, pool.ref, sums.ref, _c_int(rows), slots.data_ptr(), _stream_on(pool, stream))
+    if st:
+        _check(st, ctx.handle)
+
+
+def _need_summaries(pool: PagePool, sums: PageSummaries):
+    if sums.index != pool.index or sums.shape != (pool.n_pages, pool.k.shape[1]):
+        raise ValueError("the summaries are not of the pool's pages, or on another device")
+
+
+def _workspace_size(fn, ctx, pool, *sizes) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn(ctx.handle, pool.page_n, *(_c_int(x) for x in sizes), ctypes.byref(n)), ctx.handle)
+    return int(n.value)
+
+
+def hsq_page_select_workspace_size(ctx: Context, pool: PagePool, rows: int, B: int, width: int, prefix_len: int, top: int,
+                                   max_new: int) -> int:
+    return _workspace_size(ctx.lib.hsq_page_select_workspace_size, ctx, pool, rows, B, width, prefix_len, top, max_new)
+
+
+def hsq_page_attn_workspace_size(ctx: Context, pool: PagePool, rows: int, B: int, width: int, prefix_len: int, top: int,
+                                 max_new: int) -> int:
+    return _workspace_size(ctx.lib.hsq_page_attn_workspace_size, ctx, pool, rows, B, width, prefix_len, top, max_new)
+
+
+def _selection_args(ctx, pool, q, q_start, lens, table, sel, workspace, prefix, prefix_len):
+    """Checks what hsq_page_select and hsq_page_attn take alike."""
+    import torch
+    _need_heads(ctx, pool)
+    _need(pool, torch.bfloat16, "q", q)
+    _need(pool, torch.int32, "q_start lens table sel", q_start, lens, table, sel)
+    B, rows = lens.numel(), q.shape[0]
+    if q.shape[1:] != (ctx.cfg.n_q_heads, 128):
+        raise ValueError("q must be [rows, Hq, 128]")
+    if sel.dim() != 3 or sel.shape[:2] != (rows, ctx.cfg.n_kv_heads):
+        raise ValueError("sel must be [rows, Hkv, top]")
+    if q_start.numel() != B + 1 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("q_start [B + 1] and table [B, width] must agree with lens [B]")
+    if (rows | B | table.shape[1] | sel.shape[2]) >> 31:
+        raise ValueError("a tensor has more elements than the library counts")
+    if prefix_len > 0:
+        if prefix is None:
+            raise ValueError("prefix is None with prefix_len > 0")
+        _need(pool, torch.int32, "prefix", prefix)
+        if prefix.numel() * pool.page_n < prefix_len:
+            raise ValueError("prefix has too few pages for prefix_len")
+    if workspace.get_device() != pool.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the pool's device")
+    return rows, B, table.shape[1], sel.shape[2], prefix.data_ptr() if prefix_len > 0 else None
+
+
+def hsq_page_select(ctx: Context, pool: PagePool, sums: PageSummaries, q, q_start, lens, table, sel, workspace, prefix=None,
+                    prefix_len: int = 0, first: int = 1, recent: int = 2, max_new: int = 1, stream=None):
+    """Select pages: sel int32 [rows, Hkv, top] gets, for every row of q [rows, Hq, 128] (bfloat16, rotated) and KV
+    head, the logical pages (the prefix's, then the request's own) to attend to, ascending, -1 behind the last: the first
+    `first`, the last `recent` that the row sees, and those with the highest scores of the row's queries against the
+    summaries.  The other arguments as for hsq_shared_attn; workspace: of hsq_page_select_workspace_size bytes."""
+    rows, B, width, top, pre = _selection_args(ctx, pool, q, q_start, lens, table, sel, workspace, prefix, prefix_len)
+    _need_summaries(pool, sums)
+    st = ctx.lib.hsq_page_select(ctx.handle, pool.ref, sums.ref, rows, B, width, _c_int(prefix_len), top, _c_int(first),
+                                 _c_int(recent), _c_int(max_new), q.data_ptr(), q_start.data_ptr(), lens.data_ptr(),
+                                 table.data_ptr(), pre, sel.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream_on(pool, stream))
+    if st:
+        _check(st, ctx.handle)
+
+
+def hsq_page_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, sel, out, workspace, prefix=None,
+                  prefix_len: int = 0, max_new: int = 1, lse=None, stream=None):
+    """Attention over selected pages: hsq_shared_attn for the tokens, up to each row's last, of the logical pages in
+    sel int32 [rows, Hkv, top] (hsq_page_select's or others: ascending, -1 skipped).  out bfloat16 like q; lse float32
+    [rows, Hq] or None.  workspace: of hsq_page_attn_workspace_size bytes, one for each call that may run at the same time."""
+    import torch
+    rows, B, width, top, pre = _selection_args(ctx, pool, q, q_start, lens, table, sel, workspace, prefix, prefix_len)
+    _need(pool, torch.bfloat16, "out", out)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need(pool, torch.float32, "lse", lse)
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [rows, Hq]")
+    st = ctx.lib.hsq_page_attn(ctx.handle, pool.ref, rows, B, width, _c_int(prefix_len), top, _c_int(max_new), q.data_ptr(),
+                               q_start.data_ptr(), lens.data_ptr(), table.data_ptr(), pre, sel.data_ptr(), out.data_ptr(),
+                               _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _stream_on(pool, stream))
     if st:
         _check(st, ctx.handle)
 

@@ -72,9 +72,22 @@ hsq_status prefill_prep_kv(hsq_ctx* ctx, const PrefillImages& im, const void* K,
 hsq_status prefill_attention(hsq_ctx* ctx, const PrefillImages& im, float* out, int B, int T, cudaStream_t st);
 
 // Paged serving (hsq_pages.cu): the pool's shape (and, with buffers, its memory) is
-// valid; the current device is the context's.
+// valid; the summaries' memory is; the current device is the context's.
 hsq_status check_pages(hsq_ctx* ctx, const hsq_pages* pages, bool buffers);
+hsq_status check_summaries(hsq_ctx* ctx, const hsq_summaries* sums);
 hsq_status check_device(hsq_ctx* ctx);
+
+// What is wrong with the sizes of a call over selected pages (NULL: nothing).
+inline const char* selection_shape_wrong(int page_n, int rows, int B, int width, int prefix_len, int top, int max_new) {
+    if (page_n != 16 && page_n != 32 && page_n != 64 && page_n != 128) return "page_n must be 16, 32, 64 or 128";
+    if (B < 1 || B > HSQ_MAX_REQUESTS) return "B outside [1, HSQ_MAX_REQUESTS]";
+    if (rows < 1 || width < 1 || max_new < 1 || prefix_len < 0 || prefix_len > (1 << 30))
+        return "rows, width and max_new must be positive, prefix_len in [0, 2^30]";
+    if (top < 1 || top > HSQ_MAX_BETA) return "top must be in [1, HSQ_MAX_BETA]";
+    if ((prefix_len + page_n - 1) / page_n + (long long)width > HSQ_MAX_SELECT_PAGES)
+        return "the prefix's pages and width together above HSQ_MAX_SELECT_PAGES";
+    return nullptr;
+}
 
 // A call's buffer, and whether one of `outs` shares a byte with another or with one of `ins` (NULL: not given).
 struct Span {

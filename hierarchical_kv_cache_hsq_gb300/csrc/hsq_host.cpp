@@ -273,6 +273,51 @@ hsq_status hsq_cache_sizes(const hsq_config* cfg, int B, int T, size_t bytes[HSQ
     return HSQ_OK;
 }
 
+hsq_status hsq_rope_frequencies(int scaling, int dims, double theta, double factor, double original, double beta_fast,
+                                double beta_slow, double* omega, double* amplitude) {
+    if (!omega || !amplitude || dims < 8 || dims > hsq::kDim || dims % 8) return HSQ_ERR_INVALID;
+    if (!(theta > 0.0) || !std::isfinite(theta)) return HSQ_ERR_INVALID;
+    if (scaling < HSQ_ROPE_NONE || scaling > HSQ_ROPE_YARN) return HSQ_ERR_INVALID;
+    if (scaling != HSQ_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return HSQ_ERR_INVALID;
+    if (scaling == HSQ_ROPE_YARN &&
+        (!(original > 0.0) || !std::isfinite(original) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast - beta_slow)))
+        return HSQ_ERR_INVALID;
+    const double base = scaling == HSQ_ROPE_BASE ? theta * std::pow(factor, dims / (dims - 2.0)) : theta;
+    constexpr double kTurn = 6.283185307179586476925;
+    for (int i = 0; i < dims / 2; ++i) {
+        double w = std::pow(base, -2.0 * i / dims);
+        if (scaling == HSQ_ROPE_LINEAR) w /= factor;
+        if (scaling == HSQ_ROPE_YARN) {
+            const double turns = original * w / kTurn;
+            const double keep = std::min(std::max((turns - beta_slow) / (beta_fast - beta_slow), 0.0), 1.0);
+            w *= keep + (1.0 - keep) / factor;
+        }
+        omega[i] = w;
+    }
+    *amplitude = scaling == HSQ_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    return HSQ_OK;
+}
+
+hsq_status hsq_rope_table(int dims, const double* omega, double amplitude, int max_pos, float* table, size_t* floats) {
+    if (!floats || dims < 8 || dims > hsq::kDim || dims % 8 || max_pos < 1 || max_pos > (1 << 24)) return HSQ_ERR_INVALID;
+    const int n_hi = (max_pos + hsq::kRopeLoRows - 1) / hsq::kRopeLoRows, half = dims / 2;
+    *floats = (size_t)(hsq::kRopeLoRows + n_hi) * dims;
+    if (!table) return HSQ_OK;
+    if (!omega || !std::isfinite(amplitude)) return HSQ_ERR_INVALID;
+    for (int i = 0; i < half; ++i)
+        if (!std::isfinite(omega[i])) return HSQ_ERR_INVALID;
+    for (int c = 0; c < hsq::kRopeLoRows + n_hi; ++c) {
+        const bool low = c < hsq::kRopeLoRows;
+        const double p = low ? c : (double)(c - hsq::kRopeLoRows) * hsq::kRopeLoRows, amp = low ? amplitude : 1.0;
+        float* row = table + (size_t)c * dims;
+        for (int i = 0; i < half; ++i) {
+            row[i] = (float)(amp * std::cos(p * omega[i]));
+            row[half + i] = (float)(amp * std::sin(p * omega[i]));
+        }
+    }
+    return HSQ_OK;
+}
+
 hsq_status hsq_debug_set_fault(unsigned mask) {
     hsq::g_fault.store(mask);
     return HSQ_OK;

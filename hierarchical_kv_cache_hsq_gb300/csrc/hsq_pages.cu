@@ -1,6 +1,7 @@
 // Paged serving: block tables and slot maps from request lengths
-// (hsq_page_tables), and the rotated, paged write of a step's keys and values
-// (hsq_page_write).
+// (hsq_page_tables), the rotated, paged write of a step's keys and values
+// (hsq_page_write, and with a model's own rotation hsq_page_write_rope), and
+// the summaries of the pages that a step fills (hsq_page_summaries).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -181,17 +182,74 @@ struct WriteArgs {
     long long n_slots;
     unsigned units;          // units of a row: V heads each, of the queries, then keys, then values
     int units_q, units_k;
+    const float* rope;       // hsq_rope's table, row length and limit (with the context's rotation not read)
+    int rope_dims, rope_pos;
     int* err;
 };
 
-__device__ __forceinline__ void store_bf16x8(uint16_t* p, const float v[8]) {
-    const int l = hlane();
+// What turns a half-warp's vectors.  kOwnRope: the context's rotation.  Else the first `dims` dims by hsq_rope's table, in
+// pairs (i, i + dims / 2) (kHalfRope) or (2 i, 2 i + 1) (kPairRope).
+enum { kOwnRope, kHalfRope, kPairRope };
+
+// The two quads of dims that lane l holds: what it turns lies in its own registers (pair k of it has frequency 4 l + k), and
+// lanes past the rotated dims hold those left as they are.
+template <int ROPE>
+__device__ __forceinline__ void lane_quads(int l, int dims, int& qa, int& qb) {
+    if (ROPE == kOwnRope) {
+        qa = 4 * l;
+        qb = 64 + 4 * l;
+    } else if (ROPE == kPairRope || 8 * l >= dims) {
+        qa = 8 * l;
+        qb = 8 * l + 4;
+    } else {
+        qa = 4 * l;
+        qb = (dims >> 1) + 4 * l;
+    }
+}
+
+template <int ROPE>
+__device__ __forceinline__ RopeRows rope_rows_of(int p, const WriteArgs& a, const Tables& tb) {
+    if constexpr (ROPE == kOwnRope) {
+        return rope_rows(p, tb);
+    } else {
+        RopeRows r{};
+        const int l = hlane(), half = a.rope_dims >> 1;
+        if (8 * l < a.rope_dims) {
+            const float* lo = a.rope + (p & 255) * a.rope_dims + 4 * l;
+            const float* hi = a.rope + (size_t)(256 + (p >> 8)) * a.rope_dims + 4 * l;
+            r.cl = __ldg(reinterpret_cast<const float4*>(lo));
+            r.sl = __ldg(reinterpret_cast<const float4*>(lo + half));
+            r.ch = __ldg(reinterpret_cast<const float4*>(hi));
+            r.sh = __ldg(reinterpret_cast<const float4*>(hi + half));
+        }
+        return r;
+    }
+}
+
+template <int ROPE>
+__device__ __forceinline__ void turn(float (&x)[8], const RopeRows& r, int dims) {
+    if (ROPE == kOwnRope) {
+        rope_apply(x, r);
+    } else if (8 * hlane() < dims) {
+        if (ROPE == kHalfRope) {
+            rope_apply(x, r);
+        } else {  // the pairs side by side: (0, 1), (2, 3), ..
+            float y[8] = {x[0], x[2], x[4], x[6], x[1], x[3], x[5], x[7]};
+            rope_apply(y, r);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = y[k];
+                x[2 * k + 1] = y[4 + k];
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void store_bf16x8(uint16_t* pa, uint16_t* pb, const float v[8]) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
     const __nv_bfloat162 c = __floats2bfloat162_rn(v[4], v[5]), d = __floats2bfloat162_rn(v[6], v[7]);
-    *reinterpret_cast<uint2*>(p + 4 * l) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    *reinterpret_cast<uint2*>(p + 64 + 4 * l) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d));
+    *reinterpret_cast<uint2*>(pa) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    *reinterpret_cast<uint2*>(pb) = make_uint2(*reinterpret_cast<const uint32_t*>(&c), *reinterpret_cast<const uint32_t*>(&d));
 }
 
 // One half-warp per (row, V neighbouring heads of its queries, keys or values): all V
@@ -202,11 +260,13 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, const float v[8]) {
 // decide: a prompt of 32K tokens (32/8 heads, bf16, 806 MB) takes 121 us, 6.7 TB/s, 99 % of a plain copy's rate; with V = 1,
 // fewer loads in flight, 185.  For few rows by latency, and V = 1 spreads them over the SMs: 16 rows 4.2 us, with
 // V = 8 5.5.  (2531 float32 rows: 25.2 with V = 1, 23.7 with V = 4.)
-template <bool BF, int V>
+template <bool BF, int V, int ROPE>
 __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Tables tb) {
-    using Raw = typename std::conditional<BF, uint2, float4>::type;  // a lane's dims 4 l .. and 64 + 4 l ..
+    using Raw = typename std::conditional<BF, uint2, float4>::type;  // a quad of dims
     constexpr int kSize = BF ? 2 : 4;
     const int l = hlane();
+    int qa, qb;
+    lane_quads<ROPE>(l, a.rope_dims, qa, qb);
     const unsigned unit = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
     const unsigned row_u = unit / a.units;
     const int row = (int)row_u, u = (int)(unit - row_u * a.units);
@@ -215,20 +275,21 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Table
     const int h0 = (is_q ? u : is_v ? u - a.units_q - a.units_k : u - a.units_q) * V;
     const int count = min(V, (is_q ? a.Hq : a.Hkv) - h0);
     const char* src = static_cast<const char*>(is_q ? a.q : is_v ? a.v : a.k) +
-                      ((long long)row * (is_q ? a.qs : is_v ? a.vs : a.ks) + h0 * kDim) * kSize + l * sizeof(Raw);
+                      ((long long)row * (is_q ? a.qs : is_v ? a.vs : a.ks) + h0 * kDim) * kSize;
     Raw raw[V][2];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if (j < count) {
-            raw[j][0] = __ldg(reinterpret_cast<const Raw*>(src + j * (kDim * kSize)));
-            raw[j][1] = __ldg(reinterpret_cast<const Raw*>(src + j * (kDim * kSize) + 64 * kSize));
+            raw[j][0] = __ldg(reinterpret_cast<const Raw*>(src + j * (kDim * kSize) + qa * kSize));
+            raw[j][1] = __ldg(reinterpret_cast<const Raw*>(src + j * (kDim * kSize) + qb * kSize));
         }
     }
     int p = a.pos[row];
     long long slot = a.slots[row];
     if (p < 0) return;
-    if (p >= tb.max_pos) {
-        p = tb.max_pos - 1;
+    const int max_pos = ROPE == kOwnRope ? tb.max_pos : a.rope_pos;
+    if (p >= max_pos) {
+        p = max_pos - 1;
         if (l == 0) atomicOr(a.err, HSQ_DEVERR_POS);
     }
     if (slot >= a.n_slots) {
@@ -246,13 +307,13 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Table
               (((size_t)(slot >> a.page_shift) * a.Hkv + h0) * a.page_n + (size_t)(slot & (a.page_n - 1))) * kDim;
     }
     RopeRows rr;
-    if (!is_v) rr = rope_rows(p, tb);
+    if (!is_v) rr = rope_rows_of<ROPE>(p, a, tb);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if (j >= count) break;
         if (BF && is_v) {
-            reinterpret_cast<Raw*>(dst + (size_t)j * step)[l] = raw[j][0];
-            reinterpret_cast<Raw*>(dst + (size_t)j * step + 64)[l] = raw[j][1];
+            *reinterpret_cast<Raw*>(dst + (size_t)j * step + qa) = raw[j][0];
+            *reinterpret_cast<Raw*>(dst + (size_t)j * step + qb) = raw[j][1];
             continue;
         }
         float x[8];
@@ -270,18 +331,155 @@ __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Table
                 x[4 * e + 3] = raw[j][e].w;
             }
         }
-        if (!is_v) rope_apply(x, rr);
-        store_bf16x8(dst + (size_t)j * step, x);
+        if (!is_v) turn<ROPE>(x, rr, a.rope_dims);
+        store_bf16x8(dst + (size_t)j * step + qa, dst + (size_t)j * step + qb, x);
     }
 }
 
-template <bool BF, int V>
+template <bool BF, int V, int ROPE>
 void launch_write(WriteArgs a, const Tables& tb, cudaStream_t s) {
     a.units_q = (a.Hq + V - 1) / V;
     a.units_k = (a.Hkv + V - 1) / V;
     a.units = a.units_q + 2 * a.units_k;
     const unsigned ctas = (unsigned)(((unsigned long long)a.rows * a.units + kHalves - 1) / kHalves);
-    page_write_kernel<BF, V><<<ctas, kThreads, 0, s>>>(a, tb);
+    page_write_kernel<BF, V, ROPE><<<ctas, kThreads, 0, s>>>(a, tb);
+}
+
+template <int ROPE>
+void launch_write(const WriteArgs& a, bool bf, bool few, const Tables& tb, cudaStream_t s) {
+    if (bf) {
+        if (few) launch_write<true, 1, ROPE>(a, tb, s);
+        else launch_write<true, 8, ROPE>(a, tb, s);
+    } else {
+        if (few) launch_write<false, 1, ROPE>(a, tb, s);
+        else launch_write<false, 4, ROPE>(a, tb, s);
+    }
+}
+
+// ---- summaries ------------------------------------------------------------------------------
+
+struct SumsArgs {
+    const int64_t* slots;
+    const uint16_t* pk;
+    int8_t* codes; float* scale;
+    int rows, Hkv, page_n, page_shift, n_pages;
+    int* err;
+};
+
+// s + x exactly as the two numbers s (rounded) and what the rounding left out, added to e; two lanes at a time.
+__device__ __forceinline__ void two_sum2(uint64_t& s, uint64_t& e, uint64_t x) {
+    uint64_t t, b, c, d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(s), "l"(x));
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(b) : "l"(t), "l"(s));
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(t), "l"(b));
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(s), "l"(c));
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(b));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(c), "l"(d));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(e) : "l"(e), "l"(c));
+    s = t;
+}
+
+constexpr int kSumThreads = 256;
+constexpr float kSumLeast = 0x1p-64f, kSumMost = 0x1p126f;
+
+// One warp per (R rows of the step, KV head): a row is its page's last of the step when the next row's slot lies on
+// another page, and then the warp sums the page's keys.  A half-warp takes every other token (16 bytes, dims 8 l ..
+// 8 l + 7, a lane), 8 tokens of each in flight.
+// The sums are kept as fp32 pairs (two_sum2), exact to some 48 bits, because a code jumps by one at a border and has to
+// be the same however the sum is ordered; 127 S / max is compared with its border in 64 bits only where fp32 leaves it
+// open (one element in 5000).
+template <int R>
+__global__ void __launch_bounds__(kSumThreads) page_summaries_kernel(SumsArgs a) {
+    const int lane = threadIdx.x & 31, l = lane & 15, odd = lane >> 4;
+    const long long unit = (long long)blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
+    const long long chunk = unit / a.Hkv;
+    const int h = (int)(unit - chunk * a.Hkv);
+    const long long row = chunk * R + lane;
+    long long slot = -1;
+    bool last = false;
+    if (lane < R && row < a.rows) {
+        slot = a.slots[row];
+        const long long after = row + 1 < a.rows ? a.slots[row + 1] : -1;
+        if (slot >= (long long)a.n_pages << a.page_shift) {
+            slot = -1;
+            if (h == 0) atomicOr(a.err, HSQ_DEVERR_PAGE);
+        }
+        last = slot >= 0 && (after < 0 || (after >> a.page_shift) != (slot >> a.page_shift));
+    }
+    unsigned todo = __ballot_sync(kFull, last);
+    while (todo) {
+        const int from = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const long long at = __shfl_sync(kFull, slot, from);
+        const int page = (int)(at >> a.page_shift), n = (int)(at & (a.page_n - 1)) + 1;
+        const size_t head = (size_t)page * a.Hkv + h;
+        const uint4* src = reinterpret_cast<const uint4*>(a.pk + (head << a.page_shift) * kDim) + odd * 16 + l;
+        uint64_t s[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};
+#pragma unroll 1
+        for (int t0 = 0; t0 < n; t0 += 16) {
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int t = t0 + 2 * k + odd;
+                v[k] = t < n ? __ldcs(src + (size_t)(t0 + 2 * k) * 16) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    two_sum2(s[i], e[i], (uint64_t)(w[i] << 16) | ((uint64_t)(w[i] & 0xFFFF0000u) << 32));
+            }
+        }
+        float hi[8], lo[8];
+        float top = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the two halves' sums, and the pair brought to hi = their sum rounded
+            const uint64_t so = __shfl_xor_sync(kFull, s[i], 16), eo = __shfl_xor_sync(kFull, e[i], 16);
+            uint64_t a2 = odd ? so : s[i], b2 = odd ? s[i] : so, r2;  // (in one order, so that both halves get the same)
+            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r2) : "l"(e[i]), "l"(eo));
+            two_sum2(a2, r2, b2);
+            const float x[2] = {__uint_as_float((uint32_t)a2), __uint_as_float((uint32_t)(a2 >> 32))};
+            const float y[2] = {__uint_as_float((uint32_t)r2), __uint_as_float((uint32_t)(r2 >> 32))};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                hi[2 * i + k] = __fadd_rn(x[k], y[k]);
+                lo[2 * i + k] = __fsub_rn(y[k], __fsub_rn(hi[2 * i + k], x[k]));
+                top = fmaxf(top, fabsf(hi[2 * i + k]));
+                bad |= !(fabsf(hi[2 * i + k]) <= kSumMost);
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+        bad = __any_sync(kFull, bad);
+        const bool live = !bad && top >= kSumLeast;
+        const float by = __fdiv_rn(127.f, live ? top : 1.f);
+        int code[8];
+        bool open = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float y = __fmul_rn(hi[k], by);
+            code[k] = live ? __float2int_rn(y) : 0;
+            open |= live && fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f;
+        }
+        if (__any_sync(kFull, open)) {  // (y is off by less than 127 * 2^-22 here, and max by its own low part)
+            double m = 0.0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = fmax(m, fabs((double)hi[k] + lo[k]));
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) m = fmax(m, __shfl_xor_sync(kFull, m, d));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) code[k] = __double2int_rn(127.0 * ((double)hi[k] + lo[k]) / m);
+        }
+        if (odd == 0) {
+            uint32_t w[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(code[k] & 0xFF) << (8 * (k & 3));
+            reinterpret_cast<uint2*>(a.codes + head * kDim)[l] = make_uint2(w[0], w[1]);
+            if (l == 0) a.scale[head] = live ? __fdiv_rn(top, 127.f * (float)n) : bad ? INFINITY : 0.f;
+        }
+    }
 }
 
 }  // namespace
@@ -303,6 +501,13 @@ hsq_status check_pages(hsq_ctx* ctx, const hsq_pages* pages, bool buffers) {
     return HSQ_OK;
 }
 
+hsq_status check_summaries(hsq_ctx* ctx, const hsq_summaries* sums) {
+    if (!sums || !sums->codes || !sums->scale) return fail(ctx, HSQ_ERR_INVALID, "sums, sums->codes or sums->scale is NULL");
+    if (((uintptr_t)sums->codes & 15u) || ((uintptr_t)sums->scale & 3u))
+        return fail(ctx, HSQ_ERR_INVALID, "sums->codes must be 16-byte aligned, sums->scale 4-byte");
+    return HSQ_OK;
+}
+
 hsq_status check_device(hsq_ctx* ctx) {
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
@@ -312,6 +517,64 @@ hsq_status check_device(hsq_ctx* ctx) {
 }
 
 }  // namespace hsq
+
+namespace {
+
+// hsq_page_write (rope NULL) and hsq_page_write_rope
+hsq_status page_write(hsq_ctx* ctx, const hsq_pages* pages, const hsq_rope* rope, int rows, const void* q, const void* k,
+                      const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride, hsq_dtype dtype,
+                      const int32_t* pos, const int64_t* slots, void* q_out, hsq_stream_t stream) {
+    hsq_status st = hsq::check_pages(ctx, pages, true);
+    if (st != HSQ_OK) return st;
+    if (!k || !v || !pos || !slots) return hsq::fail(ctx, HSQ_ERR_INVALID, "k, v, pos or slots is NULL");
+    if (!q != !q_out) return hsq::fail(ctx, HSQ_ERR_INVALID, "q and q_out go together");
+    if (dtype != HSQ_DTYPE_F32 && dtype != HSQ_DTYPE_BF16) return hsq::fail(ctx, HSQ_ERR_INVALID, "bad dtype");
+    if (rows < 1) return hsq::fail(ctx, HSQ_ERR_INVALID, "rows must be positive");
+    const int Hq = q ? ctx->cfg.n_q_heads : 0, Hkv = ctx->cfg.n_kv_heads;
+    const int64_t unit = dtype == HSQ_DTYPE_BF16 ? 8 : 4;  // elements of 16 bytes
+    if ((q && q_stride < (int64_t)Hq * 128) || k_stride < (int64_t)Hkv * 128 || v_stride < (int64_t)Hkv * 128)
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "a row stride is smaller than a row");
+    if ((q && q_stride % unit) || k_stride % unit || v_stride % unit ||
+        (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 15u))
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "rows of q, k, v and q_out must be 16-byte aligned");
+    const long long vectors = (long long)rows * (Hq + 2 * Hkv);
+    if (vectors >= (1LL << 31)) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
+    size_t rope_floats = 0;
+    if (rope) {
+        if (!rope->table || ((uintptr_t)rope->table & 15u))
+            return hsq::fail(ctx, HSQ_ERR_INVALID, "rope->table must be 16-byte aligned and not NULL");
+        if (hsq_rope_table(rope->dims, nullptr, 1.0, rope->max_pos, nullptr, &rope_floats) != HSQ_OK)
+            return hsq::fail(ctx, HSQ_ERR_INVALID, "rope->dims must be a multiple of 8 in [8, 128], max_pos in [1, 2^24]");
+        if (rope->interleaved != 0 && rope->interleaved != 1) return hsq::fail(ctx, HSQ_ERR_INVALID, "rope->interleaved must be 0 or 1");
+    }
+    const size_t size = dtype == HSQ_DTYPE_BF16 ? 2 : 4, pool = (size_t)pages->n_pages * Hkv * pages->page_n * 256;
+    auto strided = [&](const void* p, int64_t stride, int heads) {
+        return hsq::Span{p, ((size_t)(rows - 1) * stride + (size_t)heads * 128) * size};
+    };
+    const hsq::Span ins[] = {strided(q, q_stride, Hq), strided(k, k_stride, Hkv), strided(v, v_stride, Hkv),
+                             {pos, 4 * (size_t)rows}, {slots, 8 * (size_t)rows}, {rope ? rope->table : nullptr, 4 * rope_floats}};
+    const hsq::Span outs[] = {{q_out, (size_t)rows * Hq * 256}, {pages->k, pool}, {pages->v, pool}};
+    if (hsq::outputs_overlap(ins, outs))
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "q_out or the pool's k or v overlaps another argument of hsq_page_write");
+    if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
+    const int shift = pages->page_n == 16 ? 4 : pages->page_n == 32 ? 5 : pages->page_n == 64 ? 6 : 7;
+    WriteArgs a{q, k, v, q_stride, k_stride, v_stride, pos, slots, static_cast<uint16_t*>(q_out),
+                static_cast<uint16_t*>(pages->k), static_cast<uint16_t*>(pages->v), rows, Hq, Hkv, pages->page_n, shift,
+                (long long)pages->n_pages * pages->page_n, 0, 0, 0, rope ? rope->table : nullptr, rope ? rope->dims : 0,
+                rope ? rope->max_pos : 0, ctx->d_err};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const Tables tb = make_tables(ctx);
+    // one vector a half-warp until the GPU's warps (32 a SM) are all in use, then as many as fit its registers
+    const bool few = vectors <= 64LL * ctx->num_sms;
+    const bool bf = dtype == HSQ_DTYPE_BF16;
+    if (!rope) launch_write<kOwnRope>(a, bf, few, tb, s);
+    else if (rope->interleaved) launch_write<kPairRope>(a, bf, few, tb, s);
+    else launch_write<kHalfRope>(a, bf, few, tb, s);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? HSQ_OK : hsq::cuda_fail(ctx, e, "page_write");
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -348,48 +611,43 @@ hsq_status hsq_page_tables(hsq_ctx* ctx, const hsq_pages* pages, int B, int widt
 hsq_status hsq_page_write(hsq_ctx* ctx, const hsq_pages* pages, int rows, const void* q, const void* k, const void* v,
                           int64_t q_stride, int64_t k_stride, int64_t v_stride, hsq_dtype dtype,
                           const int32_t* pos, const int64_t* slots, void* q_out, hsq_stream_t stream) {
+    return page_write(ctx, pages, nullptr, rows, q, k, v, q_stride, k_stride, v_stride, dtype, pos, slots, q_out, stream);
+}
+
+hsq_status hsq_page_write_rope(hsq_ctx* ctx, const hsq_pages* pages, const hsq_rope* rope, int rows, const void* q,
+                               const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               hsq_dtype dtype, const int32_t* pos, const int64_t* slots, void* q_out, hsq_stream_t stream) {
+    if (!rope) return hsq::fail(ctx, HSQ_ERR_INVALID, "rope is NULL");
+    return page_write(ctx, pages, rope, rows, q, k, v, q_stride, k_stride, v_stride, dtype, pos, slots, q_out, stream);
+}
+
+hsq_status hsq_page_summaries(hsq_ctx* ctx, const hsq_pages* pages, const hsq_summaries* sums, int rows,
+                              const int64_t* slots, hsq_stream_t stream) {
     hsq_status st = hsq::check_pages(ctx, pages, true);
     if (st != HSQ_OK) return st;
-    if (!k || !v || !pos || !slots) return hsq::fail(ctx, HSQ_ERR_INVALID, "k, v, pos or slots is NULL");
-    if (!q != !q_out) return hsq::fail(ctx, HSQ_ERR_INVALID, "q and q_out go together");
-    if (dtype != HSQ_DTYPE_F32 && dtype != HSQ_DTYPE_BF16) return hsq::fail(ctx, HSQ_ERR_INVALID, "bad dtype");
-    if (rows < 1) return hsq::fail(ctx, HSQ_ERR_INVALID, "rows must be positive");
-    const int Hq = q ? ctx->cfg.n_q_heads : 0, Hkv = ctx->cfg.n_kv_heads;
-    const int64_t unit = dtype == HSQ_DTYPE_BF16 ? 8 : 4;  // elements of 16 bytes
-    if ((q && q_stride < (int64_t)Hq * 128) || k_stride < (int64_t)Hkv * 128 || v_stride < (int64_t)Hkv * 128)
-        return hsq::fail(ctx, HSQ_ERR_INVALID, "a row stride is smaller than a row");
-    if ((q && q_stride % unit) || k_stride % unit || v_stride % unit ||
-        (((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)q_out) & 15u))
-        return hsq::fail(ctx, HSQ_ERR_INVALID, "rows of q, k, v and q_out must be 16-byte aligned");
-    const long long vectors = (long long)rows * (Hq + 2 * Hkv);
-    if (vectors >= (1LL << 31)) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
-    const size_t size = dtype == HSQ_DTYPE_BF16 ? 2 : 4, pool = (size_t)pages->n_pages * Hkv * pages->page_n * 256;
-    auto strided = [&](const void* p, int64_t stride, int heads) {
-        return hsq::Span{p, ((size_t)(rows - 1) * stride + (size_t)heads * 128) * size};
-    };
-    const hsq::Span ins[] = {strided(q, q_stride, Hq), strided(k, k_stride, Hkv), strided(v, v_stride, Hkv),
-                             {pos, 4 * (size_t)rows}, {slots, 8 * (size_t)rows}};
-    const hsq::Span outs[] = {{q_out, (size_t)rows * Hq * 256}, {pages->k, pool}, {pages->v, pool}};
+    if ((st = hsq::check_summaries(ctx, sums)) != HSQ_OK) return st;
+    if (!slots) return hsq::fail(ctx, HSQ_ERR_INVALID, "slots is NULL");
+    if (rows < 1 || rows >= kMaxLen) return hsq::fail(ctx, HSQ_ERR_INVALID, "rows must be in [1, 2^30)");
+    const int Hkv = ctx->cfg.n_kv_heads, P = pages->page_n;
+    const size_t heads = (size_t)pages->n_pages * Hkv;
+    const hsq::Span ins[] = {{slots, 8 * (size_t)rows}, {pages->k, heads * P * 256}};
+    const hsq::Span outs[] = {{sums->codes, heads * 128}, {sums->scale, heads * 4}};
     if (hsq::outputs_overlap(ins, outs))
-        return hsq::fail(ctx, HSQ_ERR_INVALID, "q_out or the pool's k or v overlaps another argument of hsq_page_write");
+        return hsq::fail(ctx, HSQ_ERR_INVALID, "the summaries overlap another argument of hsq_page_summaries");
     if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
-    const int shift = pages->page_n == 16 ? 4 : pages->page_n == 32 ? 5 : pages->page_n == 64 ? 6 : 7;
-    WriteArgs a{q, k, v, q_stride, k_stride, v_stride, pos, slots, static_cast<uint16_t*>(q_out),
-                static_cast<uint16_t*>(pages->k), static_cast<uint16_t*>(pages->v), rows, Hq, Hkv, pages->page_n, shift,
-                (long long)pages->n_pages * pages->page_n, 0, 0, 0, ctx->d_err};
+    const int shift = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
+    SumsArgs a{slots, static_cast<const uint16_t*>(pages->k), sums->codes, sums->scale, rows, Hkv, P, shift, pages->n_pages,
+               ctx->d_err};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const Tables tb = make_tables(ctx);
-    // one vector a half-warp until the GPU's warps (32 a SM) are all in use, then as many as fit its registers
-    const bool few = vectors <= 64LL * ctx->num_sms;
-    if (dtype == HSQ_DTYPE_BF16) {
-        if (few) launch_write<true, 1>(a, tb, s);
-        else launch_write<true, 8>(a, tb, s);
-    } else {
-        if (few) launch_write<false, 1>(a, tb, s);
-        else launch_write<false, 4>(a, tb, s);
-    }
+    // a row a warp until the GPU's warps (64 a SM) are in use twice over, then 16: a page has at least as many rows of a prompt
+    const long long units = (long long)rows * Hkv;
+    const bool few = units <= 128LL * ctx->num_sms;
+    const long long warps = few ? units : (long long)((rows + 15) / 16) * Hkv;
+    const unsigned ctas = (unsigned)((warps + kSumThreads / 32 - 1) / (kSumThreads / 32));
+    if (few) page_summaries_kernel<1><<<ctas, kSumThreads, 0, s>>>(a);
+    else page_summaries_kernel<16><<<ctas, kSumThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? HSQ_OK : hsq::cuda_fail(ctx, e, "page_write");
+    return e == cudaSuccess ? HSQ_OK : hsq::cuda_fail(ctx, e, "page_summaries");
 }
 
 }  // extern "C"

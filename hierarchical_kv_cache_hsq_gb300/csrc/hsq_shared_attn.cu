@@ -51,11 +51,13 @@
 
 #include "hsq_ctx.h"
 #include "hsq_device.cuh"
+#include "hsq_paged.cuh"
 #include "hsq_tc.cuh"
 
 namespace {
 
 using namespace hsq_tc;
+using namespace hsq_paged;
 
 constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which the maximum is taken anew
@@ -305,31 +307,6 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&x);
-}
-
-// two fp32 lanes in one instruction
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t d, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // ---------------------------------------------------------------------------------------
 // Main kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7 (stream 1),
 // warp 8 walks the run and loads keys and values, warp 9 issues the MMAs (one elected thread), warp 10 loads
@@ -389,33 +366,8 @@ __device__ __forceinline__ int keys_of(const SharedArgs& a, const Segment& s, in
 // What the join has to know of a C item that run c is the second to work on.
 struct CutRecord { int valid, h, tok0, tok1, toks0, toks1, c0, c1; };
 
-// A place in a ring of N stages, and the parity of its barriers' phase.
-template <uint32_t N>
-struct Ring {
-    uint32_t stage, phase;
-    __device__ __forceinline__ void advance() {
-        if (++stage == N) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
-};
 using KeyRing = Ring<kKeyStages>;      // stages 0, 1, 2 of `full` and `empty`
 using ValueRing = Ring<kValueStages>;  // stages 3, 4
-
-// The last b with at[b] <= x (at ascending, at[0] = 0, n entries), by a whole warp: 32 probes a step.
-__device__ __forceinline__ int warp_find(const long long* at, int n, long long x) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, len = n;
-    while (len > 1) {
-        const int step = (len + 31) / 32, i = lo + lane * step;
-        const bool le = lane * step < len && at[i] <= x;
-        const int k = max(__popc(__ballot_sync(kFull, le)) - 1, 0);
-        len = min(step, len - k * step);
-        lo += k * step;
-    }
-    return lo;
-}
 
 // Walks the CTA's run of the line (a whole warp, uniformly).
 struct Walker {
@@ -613,26 +565,6 @@ struct Walker {
 constexpr int kFewStages = 3;
 constexpr uint32_t kFewStageBytes = 16 * 256 * 2, kFewWarpBytes = kFewStages * kFewStageBytes;
 static_assert(kFewWarps * kFewWarpBytes <= kOffBars, "the warps' stages fit the ring and the query tiles");
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};\n"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldmatrix(uint32_t (&x)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldmatrix_trans(uint32_t (&x)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
 
 // Walks a warp's share of D, item by item: groups [s, s1) of (request b, KV head h).
 struct FewWalk {
@@ -1685,31 +1617,6 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
 
 // ---- host side --------------------------------------------------------------------------
 
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
-
-// bf16 rows of 128, seen as boxes of 64 columns (128-byte swizzle)
-bool encode_rows(CUtensorMap* map, void* p, uint64_t rows, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {128, rows}, strides[1] = {256};
-    const cuuint32_t box[2] = {64, box_rows}, es[2] = {1, 1};
-    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // queries [rows][Hq][128]: a box is `tokens` tokens x the r heads of a KV head x 64 columns
 bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint32_t r, uint32_t tokens) {
     const cuuint64_t dims[3] = {128, Hq, rows}, strides[2] = {256, 256 * Hq};
@@ -1758,20 +1665,6 @@ Layout layout_of(const hsq_ctx* ctx, int rows, int B, int prefix_len, int max_ne
     x.d_ml = take(d * x.few_rows * 8);
     x.bytes = at;
     return x;
-}
-
-cudaError_t launch(const void* fn, int grid, int threads, size_t smem, cudaStream_t st, bool after, void** args) {
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3(grid);
-    lc.blockDim = dim3(threads);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelExC(&lc, fn, args);
 }
 
 }  // namespace

@@ -625,6 +625,122 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
                            const int32_t* table, const int32_t* prefix, void* out, float* lse_opt, void* workspace,
                            size_t workspace_bytes, hsq_stream_t stream);
 
+/*
+ * Long contexts over the page pool: the paged write with a model's own rotation, 8-bit summaries of the pages'
+ * keys, the selection of pages by a cheap score, and the attention over the selected pages alone -- the path's idea
+ * (summary, score, top pages, their tokens) for tokens that are not compressed.  One step per layer is
+ * hsq_page_write_rope, hsq_page_summaries, hsq_page_select, hsq_page_attn; like the calls above they neither
+ * allocate, synchronise nor keep state.  The scaled frequencies follow "YaRN: Efficient Context Window Extension of
+ * Large Language Models" (arXiv 2309.00071), section 3; the pages of the method's summaries have no counterpart.
+ *
+ * hsq_rope_frequencies (host) -- the angular frequencies omega_i, i < dims / 2, of a rotation of the first `dims` dims
+ *   of a head, and the factor on the rotated parts (amplitude), in 64 bits:
+ *     HSQ_ROPE_NONE    omega_i = theta^(-2 i / dims);
+ *     HSQ_ROPE_LINEAR  the same / factor (positions interpolated);
+ *     HSQ_ROPE_BASE    theta factor^(dims / (dims - 2)) in place of theta;
+ *     HSQ_ROPE_YARN    omega_i (g + (1 - g) / factor), g = the number of turns over the original context,
+ *                      original omega_i / (2 pi), taken from [beta_slow, beta_fast] to [0, 1] and clipped; amplitude
+ *                      0.1 ln(factor) + 1.
+ *   Other schemes: compute omega and pass it to hsq_rope_table.  dims: a multiple of 8 in [8, 128].  original, beta_fast
+ *   and beta_slow matter to HSQ_ROPE_YARN only.  Errors: HSQ_ERR_INVALID (NULL, dims, theta or factor not positive and
+ *   finite, factor < 1, original not positive, beta_fast <= beta_slow).
+ * hsq_rope_table (host) -- cos and sin of the angles that positions in [0, max_pos) are put together from, fp32 from
+ *   64 bits: 256 + ceil(max_pos / 256) rows of `dims` floats (cos | sin; rows of amplitude cos(c omega), c < 256, then
+ *   of cos(256 a omega)).  *floats gets their number; with table NULL nothing else happens.  max_pos in [1, 2^24].
+ * hsq_rope -- a rotation for hsq_page_write_rope: the table in device memory, 16-byte aligned.  interleaved 0: pairs
+ *   (i, i + dims / 2); 1: pairs (2 i, 2 i + 1).  Dims from `dims` on are left as they are.
+ */
+enum { HSQ_ROPE_NONE = 0, HSQ_ROPE_LINEAR = 1, HSQ_ROPE_BASE = 2, HSQ_ROPE_YARN = 3 };
+
+typedef struct hsq_rope {
+    const float* table;
+    int dims;
+    int interleaved;
+    int max_pos;
+} hsq_rope;
+
+hsq_status hsq_rope_frequencies(int scaling, int dims, double theta, double factor, double original, double beta_fast,
+                                double beta_slow, double* omega, double* amplitude);
+hsq_status hsq_rope_table(int dims, const double* omega, double amplitude, int max_pos, float* table, size_t* floats);
+
+/*
+ * hsq_page_write_rope -- hsq_page_write with this rotation in place of the context's (a pair (a, b) at position p becomes
+ *   (a c - b s, b c + a s), c = amplitude cos(p omega), s = amplitude sin(p omega)).  HSQ_DEVERR_POS: a position
+ *   >= rope->max_pos (clamped).  Errors as there, and for a rope that is NULL or not as above.
+ */
+hsq_status hsq_page_write_rope(hsq_ctx* ctx, const hsq_pages* pages, const hsq_rope* rope, int rows, const void* q,
+                               const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               hsq_dtype dtype, const int32_t* pos, const int64_t* slots, void* q_out, hsq_stream_t stream);
+
+/*
+ * hsq_summaries -- what the selection knows of the pool's pages: of page i and KV head h, with S the sum of its keys and
+ *   n their number, codes[i][h][d] = 127 S_d / max|S| rounded to nearest (ties to even), scale[i][h] = max|S| / (127 n), so
+ *   that codes * scale is the mean key to 8 bits.  codes: [n_pages][Hkv][128] int8, 16-byte aligned; scale:
+ *   [n_pages][Hkv] f32; device memory.
+ * hsq_page_summaries -- the summaries of the pages that a step's slots name, over the tokens that they then hold.
+ *   slots: [rows] int64 as hsq_page_tables gives them: the rows of a page side by side and ascending, tokens before
+ *   them there already.  A page's last row i of the step (slots[i + 1] lies on another page, is negative or past
+ *   the end) makes its summary of tokens 0 .. slots[i] mod page_n.  Negative slots are skipped; the other pages'
+ *   summaries are left as they were.  A page that the step names in two places apart gets one of the two.
+ *   A page whose max|S| is below 2^-64 gets codes and scale 0; one whose is not a number or above 2^126
+ *   codes 0 and scale inf: such a page is selected before all others (see below), so that it shows in the result.
+ *   S is summed to some 48 bits and a code near a border is decided in 64.
+ *   HSQ_DEVERR_PAGE: a slot outside the pool (skipped).
+ *   Errors: HSQ_ERR_INVALID (NULL, rows < 1 or >= 2^30, alignment, codes or scale over each other, slots or the pool's
+ *   k, another current device than the context's), HSQ_ERR_CUDA.
+ */
+typedef struct hsq_summaries {
+    int8_t* codes;
+    float* scale;
+} hsq_summaries;
+
+hsq_status hsq_page_summaries(hsq_ctx* ctx, const hsq_pages* pages, const hsq_summaries* sums, int rows,
+                              const int64_t* slots, hsq_stream_t stream);
+
+/*
+ * hsq_page_select -- the pages that every row and KV head attends to.  Request b's logical pages are the prefix's
+ *   np = ceil(prefix_len / page_n), then its own: page np + i is table[b][i].  Row i = q_start[b] + j sees
+ *   s = lens[b] - n_b + j + 1 own tokens (n_b = q_start[b + 1] - q_start[b]; at least 0, no more than the table holds)
+ *   and so c = np + ceil(s / page_n) logical pages.  sel[i][h]: with c <= top all of them; else the first `first` and the last `recent`
+ *   ones and, of the others, the top - first - recent with the highest scores, ties to the lower page; ascending,
+ *   -1 behind the last.  Score: x = the sum of KV head h's r query rows (fp32, in their order); cq = x (127 / max|x|)
+ *   rounded to nearest even (0 where max|x| is below 2^-64 or x not finite); (sum over d of cq_d codes_d) scale, one
+ *   rounding of an exact whole number's product: the selection is the same for every way the work is divided.  A score that is not a number
+ *   ranks above all.  A page whose id lies outside the pool is never selected by score (HSQ_DEVERR_PAGE).
+ *   Rows from q_start[B] on are left as they were.  The context's routing options (route_max, route_per_head) do not apply.
+ *   q: [rows][Hq][128] bf16, rotated; sel: [rows][Hkv][top] int32; the rest as for hsq_shared_attn.  first >= 0,
+ *   recent >= 1 (a row's last page may hold tokens after it, so its summary decides nothing), first + recent <= top
+ *   <= HSQ_MAX_BETA; np + width <= HSQ_MAX_SELECT_PAGES.
+ *   HSQ_DEVERR_LEN: lens[b] negative (taken as 0), above width * page_n or below n_b; offsets that do not ascend in
+ *   [0, rows] or n_b above max_new (rows of such a request are not written; which request a row
+ *   belongs to where offsets overlap is not defined).
+ *   Errors: HSQ_ERR_INVALID (as for hsq_shared_attn, and top, first, recent), HSQ_ERR_CUDA.
+ */
+enum { HSQ_MAX_SELECT_PAGES = 32768 };
+hsq_status hsq_page_select_workspace_size(const hsq_ctx* ctx, int page_n, int rows, int B, int width, int prefix_len,
+                                          int top, int max_new, size_t* bytes);
+hsq_status hsq_page_select(hsq_ctx* ctx, const hsq_pages* pages, const hsq_summaries* sums, int rows, int B, int width,
+                           int prefix_len, int top, int first, int recent, int max_new, const void* q,
+                           const int32_t* q_start, const int32_t* lens, const int32_t* table, const int32_t* prefix,
+                           int32_t* sel, void* workspace, size_t workspace_bytes, hsq_stream_t stream);
+
+/*
+ * hsq_page_attn -- attention over selected pages: hsq_shared_attn's softmax for row i and KV head h over the tokens, up
+ *   to the row's last, of the logical pages in sel[i][h] (hsq_page_select's, or any others).  A row without any token
+ *   to see gets out = 0 and lse = -inf; rows from q_start[B] on are left as they were.
+ *   sel: [rows][Hkv][top]; -1 is skipped; an entry at or past the row's page count, or not above every entry before it, is
+ *   left out (HSQ_DEVERR_SEL), so no token counts twice.  top <= HSQ_MAX_BETA, np + width <= HSQ_MAX_SELECT_PAGES.
+ *   HSQ_DEVERR_PAGE: a page id outside the pool (its tokens are not attended to).  HSQ_DEVERR_LEN as for
+ *   hsq_page_select.  HSQ_DEVERR_WAIT: a bounded wait ran out, the results of the call are undefined.  Keys and values,
+ *   roundings, the other arguments, the workspace's use and the errors: as for hsq_shared_attn.
+ */
+hsq_status hsq_page_attn_workspace_size(const hsq_ctx* ctx, int page_n, int rows, int B, int width, int prefix_len,
+                                        int top, int max_new, size_t* bytes);
+hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, int width, int prefix_len, int top,
+                         int max_new, const void* q, const int32_t* q_start, const int32_t* lens, const int32_t* table,
+                         const int32_t* prefix, const int32_t* sel, void* out, float* lse_opt, void* workspace,
+                         size_t workspace_bytes, hsq_stream_t stream);
+
 /* hsq_last_error -- text of the last error of ctx (or of the process when ctx is NULL). */
 const char* hsq_last_error(const hsq_ctx* ctx);
 
