@@ -23,8 +23,25 @@ struct PageAttnArgs {
     uint16_t* out; float* lse;
     int rows, B, width, prefix_len, prefix_pages, max_new, n_pages, page_n, page_shift, Hq, Hkv, r, top;
     int polls;   // of a wait, before it has run out
-    int fault;   // HSQ_FAULT_WAIT_FEW: as if one had (0 but in tests)
+    int fault;   // HSQ_FAULT_WAIT_*: the roles that give up at a certain wait (0 but in tests)
     int* err;
+    // requests of more than `few` tokens go by tiles (few >= max_new: there are none, and nothing below is there)
+    int few, tpt, words, cap, runs, units_cap, rows_cap;
+    struct TileHead* head;
+    int4* req;        // [B] first row, rows, own tokens held, own tokens before the first row
+    int2* unit;       // [units] long requests' pairs of row tiles: request, pair
+    int* short_row;   // the other requests' rows
+    int4* count;      // [items] pages of both tiles, of the first alone, of the second alone; cost
+    int2* ent;        // [items][3][cap] page id, logical page
+    uint32_t* mask;   // [items][3][cap][2][words] the tiles' tokens that take the page
+    float* part_o;    // [2 runs][2][128 dims][128 rows]
+    float2* part_ml;  // [2 runs][2][128 rows] maximum of q.k, unscaled; sum
+    float2* pair_ml;  // [runs][128]
+    int4* cut;        // [runs][3] see CutRecord
+};
+
+struct TileHead {
+    int units, shorts;
 };
 
 // ---------------------------------------------------------------------------------------
@@ -62,16 +79,23 @@ __global__ void __launch_bounds__(kThreadsRow)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     cg::cluster_group cluster = cg::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int unit = blockIdx.x / S, h = unit % a.Hkv, row = unit / a.Hkv;
+    const int unit = blockIdx.x / S, h = unit % a.Hkv;
+    int row = unit / a.Hkv;
     int bad = 0;
     bool failed = false;
 
+    bool listed_row = true;
+    if (a.few < a.max_new) {  // the rows that do not go by tiles
+        listed_row = row < a.head->shorts;
+        row = listed_row ? a.short_row[row] : 0;
+    }
     if (tid == 0) {
         for (int i = 0; i < kWarps * kStages; ++i) mbar_init(base + kOffBar + 8 * i, 1);
         mbar_init_fence();
     }
     if (warp == 0) {  // the row's pages
-        const RowOf ro = warp_row(a.q_start, a.lens, a.B, a.rows, a.max_new, a.width << a.page_shift, row, bad);
+        RowOf ro{0, 0, false};
+        if (listed_row) ro = warp_row(a.q_start, a.lens, a.B, a.rows, a.max_new, a.width << a.page_shift, row, bad);
         int n = 0;
         if (ro.live) {
             const int32_t* sel = a.sel + ((size_t)row * a.Hkv + h) * a.top;
@@ -289,6 +313,889 @@ __global__ void __launch_bounds__(kThreadsRow)
     if (bad) atomicOr(a.err, bad);
 }
 
+// ---------------------------------------------------------------------------------------
+// Rows by tiles, for requests of many tokens (a prompt's chunk).  A tile is 128 rows: 128 / r neighbouring tokens times the r
+// heads of a KV head.  Its tokens select different pages, but neighbours many of the same: the tile's products run over the
+// UNION of their pages on the tensor cores, and the softmax hides the pages that a row did not take.
+//   plan     checks the lengths; lists the pairs of tiles of the long requests, and the rows of the others;
+//   list     for each item (pair, KV head): the pages that both tiles take, those of the first alone and of the second
+//            alone, with the tokens that take them;
+//   tiles    the items' key tiles as one line of cost, cut into equal runs, a persistent CTA each; an item that no cut
+//            divides is written at once, else its parts go to the workspace;
+//   join     adds the parts up.
+// Two streams (a row tile each, S / P and O in tensor memory) share the key tiles that both take and have
+// those that one takes in turn, so that while one stream's softmax runs the tensor cores work for the other.  A lone
+// tile is given to both streams, which take its key tiles in turn and are joined through tensor memory.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kTileRows = 128, kTileKeys = 128;
+constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which the maximum is taken anew
+// Requests of up to this many rows (tokens x heads) go row by row.
+constexpr int kFewColumns = 32;
+constexpr int kRunLeast = 16;        // cost of a run at least
+
+constexpr int kPlanThreads = 512;
+
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PageAttnArgs a) {
+    __shared__ int s_w[2][kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int bad = 0, units = 0, shorts = 0;  // before the round
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int first = 0, n = 0, l = 0, held = 0;
+        if (b < a.B) {
+            const int s = a.q_start[b], e = a.q_start[b + 1];
+            l = a.lens[b];
+            if (s < 0 || e < s || e > a.rows || e - s > a.max_new) {
+                bad |= HSQ_DEVERR_LEN;
+            } else {
+                first = s;
+                n = e - s;
+            }
+            held = min(max(l, 0), a.width << a.page_shift);
+            if (held != l || l < n) bad |= HSQ_DEVERR_LEN;
+            a.req[b] = make_int4(first, n, held, max(l, 0) - n);
+        }
+        const int mine[2] = {n > a.few ? (n + 2 * a.tpt - 1) / (2 * a.tpt) : 0, n > a.few ? 0 : n};
+        int x[2] = {min(mine[0], a.units_cap + 1), min(mine[1], a.rows_cap + 1)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFull, x[k], o);
+                if (lane >= o) x[k] += u;
+            }
+            if (lane == 31) s_w[k][warp] = x[k];
+        }
+        __syncthreads();
+        int before[2] = {units, shorts}, total[2] = {units, shorts};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            for (int w = 0; w < kPlanThreads / 32; ++w) {
+                if (w == warp) before[k] = total[k];
+                total[k] = min(total[k] + s_w[k][w], 1 << 29);
+            }
+        // (offsets that overlap can ask for more than there is room for: those behind are left out)
+        const int at_u = before[0] + x[0] - mine[0], at_s = before[1] + x[1] - mine[1];
+        for (int i = 0; i < mine[0]; ++i) {
+            if (at_u + i >= a.units_cap) { bad |= HSQ_DEVERR_LEN; break; }
+            a.unit[at_u + i] = make_int2(b, i);
+        }
+        for (int i = 0; i < mine[1]; ++i) {
+            if (at_s + i >= a.rows_cap) { bad |= HSQ_DEVERR_LEN; break; }
+            a.short_row[at_s + i] = first + i;
+        }
+        units = total[0];
+        shorts = total[1];
+        __syncthreads();
+    }
+    if (tid == 0) *a.head = TileHead{min(units, a.units_cap), min(shorts, a.rows_cap)};
+    if (bad) atomicOr(a.err, bad);
+}
+
+// The tokens of a pair of tiles.
+struct Pair {
+    int b, first, toks[2];  // request; first token's row; tokens of the two tiles
+    int held, ahead;        // token t of the pair sees min(max(ahead + t + 1, 0), held) own tokens
+};
+__device__ __forceinline__ Pair pair_of(const PageAttnArgs& a, int unit) {
+    const int2 u = a.unit[unit];
+    const int4 q = a.req[u.x];
+    const int j0 = u.y * 2 * a.tpt, left = q.y - j0;
+    Pair p;
+    p.b = u.x;
+    p.first = q.x + j0;
+    p.toks[0] = min(left, a.tpt);
+    p.toks[1] = min(max(left - a.tpt, 0), a.tpt);
+    p.held = q.z;
+    p.ahead = q.w + j0;
+    return p;
+}
+
+constexpr int kListThreads = 256, kListBytes = 32768;
+
+__global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_constant__ PageAttnArgs a) {
+    __shared__ uint32_t s_mask[kListBytes / 4];  // [page of the window][2][words]
+    __shared__ int s_n[3][kListThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int units = a.head->units, unit = blockIdx.x / a.Hkv, h = blockIdx.x - unit * a.Hkv;
+    if (unit >= units) return;
+    const int item = h * units + unit, W = a.words, W2 = 2 * W, window = kListBytes / 4 / W2;
+    const Pair p = pair_of(a, unit);
+    const int toks = p.toks[0] + p.toks[1];
+    auto pages_of = [&](int t) {
+        const int seen = min(max(p.ahead + t + 1, 0), p.held);
+        return a.prefix_pages + ((seen + a.page_n - 1) >> a.page_shift);
+    };
+    const int most = pages_of(toks - 1);
+    int bad = 0, n[3] = {0, 0, 0};
+    for (int w0 = 0; w0 < most; w0 += window) {
+        const int w1 = min(most, w0 + window);
+        for (int i = tid; i < (w1 - w0) * W2; i += kListThreads) s_mask[i] = 0;
+        __syncthreads();
+        for (int t = warp; t < toks; t += kListThreads / 32) {
+            const int32_t* sel = a.sel + ((size_t)(p.first + t) * a.Hkv + h) * a.top;
+            const int c = pages_of(t), tile = t >= p.toks[0], i = tile ? t - p.toks[0] : t;
+            int before = -1;
+            for (int i0 = 0; i0 < a.top; i0 += 32) {
+                const int e = i0 + lane < a.top ? sel[i0 + lane] : -1;
+                int top = e;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(kFull, top, d);
+                    if (lane >= d) top = max(top, o);
+                }
+                int ahead = __shfl_up_sync(kFull, top, 1);
+                ahead = max(lane ? ahead : -1, before);
+                before = max(before, __shfl_sync(kFull, top, 31));
+                if (e >= 0) {
+                    if (e >= c || e <= ahead) bad |= HSQ_DEVERR_SEL;
+                    else if (e >= w0 && e < w1) atomicOr(&s_mask[(e - w0) * W2 + tile * W + (i >> 5)], 1u << (i & 31));
+                }
+            }
+        }
+        __syncthreads();
+        for (int i0 = w0; i0 < w1; i0 += kListThreads) {
+            const int e = i0 + tid;
+            uint32_t m[8];
+            bool in[2] = {false, false};
+            int id = -1;
+            if (e < w1) {
+                for (int k = 0; k < W2; ++k) {
+                    m[k & 7] = s_mask[(e - w0) * W2 + k];
+                    in[k >= W] |= m[k & 7] != 0;
+                }
+                if (in[0] | in[1]) {
+                    id = e < a.prefix_pages ? a.prefix[e] : a.table[(size_t)p.b * a.width + e - a.prefix_pages];
+                    if (id < 0 || id >= a.n_pages) {
+                        bad |= HSQ_DEVERR_PAGE;
+                        in[0] = in[1] = false;
+                    }
+                }
+            }
+            const int kind = in[0] ? (in[1] ? 0 : 1) : in[1] ? 2 : 3;
+            int at = 0;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const unsigned bl = __ballot_sync(kFull, kind == k);
+                if (lane == 0) s_n[k][warp] = __popc(bl);
+                if (kind == k) at = __popc(bl & ((1u << lane) - 1u));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                for (int w = 0; w < kListThreads / 32; ++w) {
+                    if (kind == k && w < warp) at += s_n[k][w];
+                }
+                if (kind == k) at += n[k];
+                for (int w = 0; w < kListThreads / 32; ++w) n[k] += s_n[k][w];
+            }
+            if (kind < 3) {
+                const size_t to = ((size_t)item * 3 + kind) * a.cap + at;
+                a.ent[to] = make_int2(id, e);
+                for (int k = 0; k < W2; ++k) a.mask[to * W2 + k] = m[k & 7];
+            }
+            __syncthreads();
+        }
+    }
+    if (tid == 0) {
+        const int per = kTileKeys >> a.page_shift;
+        const int tb = (n[0] + per - 1) / per, t0 = (n[1] + per - 1) / per, t1 = (n[2] + per - 1) / per;
+        a.count[item] = make_int4(n[0], n[1], n[2], max(2 * tb + t0 + t1, 1));  // (an item without a page is written too)
+    }
+    if (bad) atomicOr(a.err, bad);
+}
+
+// ---- tiles ------------------------------------------------------------------------------
+
+constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kTileStages = kKeyStages + kValueStages, kQueue = 2;
+constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
+constexpr uint32_t kOffQ = kTileStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
+// barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | drain | m_full | m_free | seg_full[2] | seg_empty[2]
+constexpr int kTcBars = 2 * kTileStages + 16 + 2 * kQueue;
+constexpr uint32_t kSegBytes = 96;
+constexpr uint32_t kOffSeg = kOffBars + 8 * kTcBars;
+constexpr uint32_t kTcSmem = kOffSeg + kQueue * kSegBytes + 16 + 1024;  // + TMEM address, alignment
+static_assert(kOffSeg % 16 == 0, "segments lie on 16-byte boundaries");
+constexpr int kSegReaders = 10;  // 8 softmax warps, the MMA thread, the query loader
+
+// The key tiles [n0, n1) of an item that a run holds.
+struct alignas(16) TileSegment {
+    int live, h, item, b;
+    int n0, n1, whole, slot;
+    int first, toks0, toks1, split;  // first token's row; the streams' tokens (split: both hold the first's)
+    int held, ahead;
+    int pages[3];                    // both, first alone, second alone
+    int tiles[3];
+    int pad[4];
+};
+static_assert(sizeof(TileSegment) == kSegBytes, "");
+
+// Key tile t: the streams that take it (bits), its pages.
+struct KeyTile {
+    int streams, region, at, np;
+};
+__device__ __forceinline__ KeyTile key_tile(const TileSegment& s, int t, int per) {
+    KeyTile k;
+    int pages;
+    const int x = t - s.tiles[0], m = 2 * min(s.tiles[1], s.tiles[2]);
+    if (x < 0) {
+        k.streams = 3;
+        k.region = 0;
+        k.at = t * per;
+        pages = s.pages[0];
+    } else if (s.split) {
+        k.streams = 1 << (x & 1);
+        k.region = 1;
+        k.at = x * per;
+        pages = s.pages[1];
+    } else {
+        const int st = x < m ? x & 1 : s.tiles[1] > s.tiles[2] ? 0 : 1;
+        k.streams = 1 << st;
+        k.region = 1 + st;
+        k.at = (x < m ? x >> 1 : (m >> 1) + x - m) * per;
+        pages = st ? s.pages[2] : s.pages[1];
+    }
+    k.np = min(per, pages - k.at);
+    return k;
+}
+__device__ __forceinline__ int tiles_of(const TileSegment& s) { return s.tiles[0] + s.tiles[1] + s.tiles[2]; }
+// tiles that begin before place x of the item's line (a tile of both streams costs 2, else 1)
+__device__ __forceinline__ int tiles_before(const TileSegment& s, long long x) {
+    const long long both = 2LL * s.tiles[0];
+    return (int)min((long long)tiles_of(s), x <= 0 ? 0 : x <= both ? (x + 1) / 2 : s.tiles[0] + (x - both));
+}
+__device__ __forceinline__ long long begin_of(const TileSegment& s, int t) {
+    return t <= s.tiles[0] ? 2LL * t : 2LL * s.tiles[0] + (t - s.tiles[0]);
+}
+
+// tiles of stream st among the first n
+__device__ __forceinline__ int stream_tiles(const TileSegment& s, int st, int n) {
+    const int both = min(n, s.tiles[0]), x = n - both, m = s.split ? x : min(x, 2 * min(s.tiles[1], s.tiles[2]));
+    return both + (st ? m / 2 : (m + 1) / 2) + (x > m && (s.tiles[1] > s.tiles[2] ? 0 : 1) == st ? x - m : 0);
+}
+
+// What the join has to know of an item that run c is the second to work on.
+struct CutRecord {
+    int live, h, first, toks0, toks1, split, c0, c1;
+    int pad[4];
+};
+static_assert(sizeof(CutRecord) == 48, "");
+
+__global__ void __launch_bounds__(kTcThreads, 1)
+    page_tiles_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ PageAttnArgs a) {
+    extern __shared__ uint8_t raw_smem[];
+    const uint32_t raw = smem_addr(raw_smem), base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = raw_smem + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t full = base + kOffBars, empty = full + 8 * kTileStages, q_full = empty + 8 * kTileStages, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_full = p_full + 16, tail = o_full + 16;
+    const uint32_t drain = tail + 8, m_full = drain + 8, m_free = m_full + 8, seg_full = m_free + 8, seg_empty = seg_full + 8 * kQueue;
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffSeg + kQueue * kSegBytes);
+    const int per = kTileKeys >> a.page_shift;  // pages of a key tile
+    int bad = 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < kTileStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + 8 * i, 1);
+            mbar_init(q_empty + 8 * i, 1);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        mbar_init(tail, 1);
+        mbar_init(drain, 1);
+        mbar_init(m_full, 4);
+        mbar_init(m_free, 4);
+        for (int i = 0; i < kQueue; ++i) {
+            mbar_init(seg_full + 8 * i, 1);
+            mbar_init(seg_empty + 8 * i, kSegReaders);
+        }
+        mbar_init_fence();
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_addr((const void*)s_tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    bool failed = false;
+    TileSegment s;
+    // A wait that runs out sets its warp's `failed`.  From there on the warp arms no barrier, starts no copy and writes no segment
+    // (a stage or a queue place may still be in use), sees what it has in flight to its end and stops; the others' waits then run
+    // out in turn.  The results are undefined, the error word says so, and the next call finds everything as it should be.
+    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_fast(bar, parity, failed, a.polls); };
+
+    // the next segment of the queue, read by one thread or by a warp
+    auto receive = [&](Ring<kQueue>& q, bool release) {
+        wait(seg_full + 8 * q.stage, q.phase);
+        const int4* src = reinterpret_cast<const int4*>(gbase + kOffSeg + q.stage * kSegBytes);
+        int4* dst = reinterpret_cast<int4*>(&s);
+        if (release) failed = __any_sync(kFull, failed);  // (a warp stays together)
+        if (failed) {
+            s.live = 0;
+            return false;
+        }
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(TileSegment) / 16); ++i) dst[i] = src[i];
+        if (release) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_empty + 8 * q.stage);
+        } else {
+            mbar_arrive(seg_empty + 8 * q.stage);
+        }
+        q.advance();
+        return s.live != 0;
+    };
+
+    // (128 x 168 x 3 registers at launch: 2 x 128 x 176 + 128 x 152)
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 152;\n");
+        if (warp == 8) {
+            // ---- the run's segments, and per key tile the K pages, then the V pages (lane i: page i of the tile) ----
+            Ring<kKeyStages> kr{0, 1};
+            Ring<kValueStages> vr{0, 1};
+            Ring<kQueue> queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
+            uint32_t tail_par = 0;
+            bool tail_due = false;
+            const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
+            const int units = a.head->units, items = units * a.Hkv;
+            long long total = 0;
+            for (int i = lane; i < items; i += 32) total += a.count[i].w;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) total += __shfl_xor_sync(kFull, total, d);
+            const int runs = (int)min((long long)a.runs, max(total / kRunLeast, 1LL)), c = blockIdx.x;
+            const long long lo = c < runs ? total * c / runs : total, hi = c < runs ? total * (c + 1) / runs : total;
+            CutRecord cut{};
+            // the item that holds place lo
+            int item = 0;
+            long long at = 0;  // where it begins
+            for (; item < items; item += 32) {
+                const int w = item + lane < items ? a.count[item + lane].w : 0;
+                int x = w;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(kFull, x, d);
+                    if (lane >= d) x += y;
+                }
+                const int sum = __shfl_sync(kFull, x, 31);
+                if (at + sum > lo) {
+                    const int k = __popc(__ballot_sync(kFull, at + x <= lo));  // items of these 32 that end at or before lo
+                    at += k ? __shfl_sync(kFull, x, k - 1) : 0;
+                    item += k;
+                    break;
+                }
+                at += sum;
+            }
+            auto send = [&] {
+                wait(seg_empty + 8 * queue.stage, queue.phase);
+                failed = __any_sync(kFull, failed);
+                if (failed) return;
+                if (lane == 0) {
+                    *reinterpret_cast<TileSegment*>(gbase + kOffSeg + queue.stage * kSegBytes) = s;
+                    mbar_arrive(seg_full + 8 * queue.stage);
+                }
+                __syncwarp();
+                queue.advance();
+            };
+            for (; at < hi && item < items && !failed; ++item) {
+                const int4 n = a.count[item];
+                const int h = item / units;
+                const Pair p = pair_of(a, item - h * units);
+                s.live = 1;
+                s.h = h;
+                s.item = item;
+                s.b = p.b;
+                s.first = p.first;
+                s.toks0 = p.toks[0];
+                s.split = p.toks[1] == 0;
+                s.toks1 = s.split ? s.toks0 : p.toks[1];
+                s.held = p.held;
+                s.ahead = p.ahead;
+                s.pages[0] = n.x;
+                s.pages[1] = n.y;
+                s.pages[2] = n.z;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) s.tiles[k] = (s.pages[k] + per - 1) / per;
+                const int tiles = tiles_of(s);
+                s.n0 = tiles_before(s, lo - at);
+                s.n1 = tiles_before(s, hi - at);
+                const bool begins = at >= lo;
+                const long long begin = at;
+                at += n.w;
+                if (tiles == 0 ? !begins : s.n0 >= s.n1) continue;
+                s.whole = s.n0 == 0 && s.n1 == tiles;
+                s.slot = 2 * c + (s.n0 == 0);
+                if (!s.whole && s.n0 > 0) {
+                    const int c0 = (int)(((begin + 1) * runs - 1) / total);
+                    if (c0 == c - 1)
+                        cut = CutRecord{1, h, s.first, s.toks0, s.toks1, s.split, c0,
+                                        (int)(((begin + begin_of(s, tiles - 1) + 1) * runs - 1) / total), {}};
+                }
+                send();
+                for (int t = s.n0; t < s.n1 && !failed; ++t) {
+                    const KeyTile k = key_tile(s, t, per);
+                    int2 e = make_int2(0, 0);
+                    int tokens = a.page_n;  // of the page
+                    if (lane < k.np) {
+                        e = a.ent[((size_t)item * 3 + k.region) * a.cap + k.at + lane];
+                        tokens = e.y < a.prefix_pages ? a.prefix_len - (e.y << a.page_shift) : s.held - ((e.y - a.prefix_pages) << a.page_shift);
+                    }
+                    const unsigned ends = __ballot_sync(kFull, tokens < a.page_n);  // pages that the tokens end inside of
+                    const int y = (e.x * a.Hkv + h) << a.page_shift;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t slot = kv ? kKeyStages + vr.stage : kr.stage;
+                        const uint32_t stage = base + slot * kTileBytes, bar = full + 8 * slot;
+                        wait(empty + 8 * slot, kv ? vr.phase : kr.phase);
+                        if (kv) failed |= (a.fault & HSQ_FAULT_WAIT_LOAD) != 0;
+                        failed = __any_sync(kFull, failed);
+                        if (failed) break;
+                        // Rows of values that no token has hold whatever the page holds; their weights are 0, so they have to
+                        // be finite.  Cleared here before the tile is handed over.
+                        const bool ragged = kv && ends;
+                        const uint32_t lands = ragged ? tail : bar;
+                        if (lane == 0) mbar_expect_tx(lands, k.np * page_bytes);
+                        __syncwarp();
+                        if (lane < k.np) {
+                            const void* map = kv ? &mv : &mk;
+                            tma_2d(stage + lane * half_page, map, 0, y, lands);
+                            tma_2d(stage + lane * half_page + kHalfBytes, map, 64, y, lands);
+                        }
+                        if (ragged) {
+                            wait(tail, tail_par);
+                            failed = __any_sync(kFull, failed);
+                            if (failed) {
+                                tail_due = true;
+                                break;
+                            }
+                            tail_par ^= 1;
+                            for (unsigned left = ends; left; left &= left - 1) {
+                                const int i = __ffs(left) - 1, have = max(__shfl_sync(kFull, tokens, i), 0);
+                                const int row0 = (i << a.page_shift) + have, z = (a.page_n - have) * 16;  // 16-byte chunks of both halves
+                                for (int x = lane; x < z; x += 32)
+                                    *reinterpret_cast<uint4*>(gbase + (stage - base) + ((x >> 3) & 1) * kHalfBytes + (row0 + (x >> 4)) * 128 +
+                                                              (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar);
+                        }
+                        if (kv) vr.advance(); else kr.advance();
+                    }
+                }
+            }
+            s.live = 0;
+            send();
+            if (lane == 0) *reinterpret_cast<CutRecord*>(a.cut + 3 * c) = cut;
+            if (failed) {  // see the copies in flight land before the CTA ends
+                for (int i = 0; i < kTileStages; ++i) {
+                    const bool lap = i < kKeyStages ? i < (int)kr.stage : i - kKeyStages < (int)vr.stage;
+                    mbar_wait(full + 8 * i, (i < kKeyStages ? kr.phase : vr.phase) ^ (lap ? 1u : 0u), 1 << 12);
+                }
+                if (tail_due) mbar_wait(tail, tail_par, 1 << 12);
+            }
+        } else if (warp == 9 && elect_one()) {
+            // ---- MMAs, one thread ----
+            constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128);
+            Ring<kQueue> queue{0, 0};
+            uint32_t q_par = 0, p_par = 0;  // a bit for each stream
+            // Key tiles are counted through the segments: tile g is in key stage g mod 3 and value stage g mod 2.  A stream's
+            // product with the values of its last key tile waits (`due`) until its next S is issued, or until the tile is
+            // two behind, when its value stage is needed again.
+            struct Due { uint32_t g; int g16, more, last; bool is; } due[2] = {{0, 0, 0, 0, false}, {0, 0, 0, 0, false}};
+            uint32_t g = 0;
+            int users[2] = {0, 0};  // products that a value stage has still to serve
+            auto scores = [&](int st, uint32_t stage, int g16) {  // S = Q K^T
+                const uint32_t dS = tmem + 128 * st, idS = idesc_bf16_f32(128, 16 * g16);
+                const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + stage * kTileBytes);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
+                    mma_bf16(dS, dq + o, dk + o, idS, k > 0);
+                }
+                mma_commit(s_full + 8 * st);
+            };
+            auto settle = [&](int st) {  // O += P V of the stream's tile that is due
+                Due& d = due[st];
+                if (!d.is) return;
+                const uint32_t stage = kKeyStages + (d.g & 1);
+                const uint32_t pa = tmem + 128 * st, dO = pa + 256;
+                const uint64_t dv = sw128_mn_desc(base + stage * kTileBytes, kHalfBytes);
+                wait(full + 8 * stage, (d.g >> 1) & 1);
+                wait(p_full + 8 * st, (p_par >> st) & 1);
+                if (__builtin_expect(failed, 0)) return;
+                p_par ^= 1u << st;
+                tc_fence_after();
+                if (d.g16 == 8) {
+                    mma_bf16_ts(dO, pa, dv, idO, d.more);
+#pragma unroll
+                    for (int k = 1; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < d.g16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, d.more | (k > 0));
+                }
+                if (--users[d.g & 1] == 0) mma_commit(empty + 8 * stage);
+                if (d.last) mma_commit(o_full + 8 * st);
+                d.is = false;
+            };
+            // (the older first: a stream whose softmax has still to join the other's part takes up no new tile before)
+            auto settle_all = [&] {
+                const bool first1 = due[0].is && due[1].is && (int)(due[1].g - due[0].g) < 0;
+                if (first1) settle(1);
+                settle(0);
+                settle(1);
+            };
+            // (after a wait that ran out no stage is handed back: its copy may still be under way)
+            auto work = [&] {
+                while (receive(queue, false)) {
+                    if (s.n0 == s.n1) settle_all();  // (nobody may wait for what is due behind an item without a tile)
+                    int done[2] = {0, 0};
+                    const int all[2] = {stream_tiles(s, 0, s.n1) - stream_tiles(s, 0, s.n0), stream_tiles(s, 1, s.n1) - stream_tiles(s, 1, s.n0)};
+#pragma unroll 1
+                    for (int t = s.n0; t < s.n1; ++t, ++g) {
+                        const KeyTile k = key_tile(s, t, per);
+                        const uint32_t stage = g % kKeyStages;
+#pragma unroll
+                        for (int st = 0; st < 2; ++st)
+                            if (due[st].is && g - due[st].g >= 2) settle(st);
+                        wait(full + 8 * stage, (g / kKeyStages) & 1);
+                        users[g & 1] = k.streams == 3 ? 2 : 1;
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            if (!((k.streams >> st) & 1)) continue;
+                            settle(st);
+                            if (done[st] == 0) {
+                                wait(q_full + 8 * st, (q_par >> st) & 1);
+                                q_par ^= 1u << st;
+                            }
+                            if (__builtin_expect(failed, 0)) return;
+                            const int g16 = (k.np << a.page_shift) >> 4;
+                            scores(st, stage, g16);
+                            const bool last = ++done[st] == all[st];
+                            if (last) mma_commit(q_empty + 8 * st);
+                            due[st] = Due{g, g16, done[st] > 1, last, true};
+                        }
+                        mma_commit(empty + 8 * stage);
+                        failed |= (a.fault & HSQ_FAULT_WAIT_MMA) != 0;
+                        if (__builtin_expect(failed, 0)) return;
+                    }
+                }
+                if (failed) return;
+                settle_all();
+            };
+            work();
+            if (failed) {  // what is in flight ends before its operands' and results' memory is given up
+                mma_commit(drain);
+                mbar_wait(drain, 0, 1 << 12);
+            }
+        } else if (warp == 10) {
+            // ---- queries of the segments' streams ----
+            Ring<kQueue> queue{0, 0};
+            uint32_t q_par = 3;  // (the buffers start empty)
+            const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
+            while (receive(queue, true)) {
+#pragma unroll 1
+                for (int st = 0; st < 2; ++st) {
+                    if (stream_tiles(s, st, s.n1) == stream_tiles(s, st, s.n0)) continue;
+                    const uint32_t dst = base + kOffQ + st * kTileBytes, bar = q_full + 8 * st;
+                    wait(q_empty + 8 * st, (q_par >> st) & 1);
+                    if (st) failed |= (a.fault & HSQ_FAULT_WAIT_QUERY) != 0;
+                    failed = __any_sync(kFull, failed);
+                    if (failed) break;
+                    q_par ^= 1u << st;
+                    if (lane == 0) {
+                        const int row = s.first + (st && !s.split ? a.tpt : 0);
+                        mbar_expect_tx(bar, q_bytes);
+                        tma_3d(dst, &mq, 0, s.h * a.r, row, bar);
+                        tma_3d(dst + kHalfBytes, &mq, 64, s.h * a.r, row, bar);
+                    }
+                    __syncwarp();
+                }
+                if (failed) break;
+            }
+            if (failed)  // query tiles in flight land before the CTA ends
+                for (int st = 0; st < 2; ++st) mbar_wait(q_full + 8 * st, (q_par >> st) & 1, 1 << 12);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
+        // ---- softmax: thread = row of its stream's tile ----
+        const int st = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + 128 * st, tO = tmem + lanes + 256 + 128 * st;
+        uint32_t s_par = 0, o_par = 0, m_par = 0;
+        Ring<kQueue> queue{0, 0};
+        const int row_token = row / a.r, word = (32 * (warp & 3) / a.r) >> 5;  // (a warp's tokens share a word of the masks)
+        while (receive(queue, true)) {
+            const int toks = st ? s.toks1 : s.toks0, tile = st && !s.split ? 1 : 0, t0 = tile ? a.tpt : 0;
+            const bool live = row_token < toks;
+            const bool idle = 32 * (warp & 3) >= toks * a.r;  // (warp-uniform) no row of this warp in use
+            const int seen = min(max(s.ahead + t0 + row_token + 1, 0), s.held);
+            const int mine = stream_tiles(s, st, s.n1) - stream_tiles(s, st, s.n0);
+            float m = -INFINITY, l = 0.f;
+            int done = 0;
+#pragma unroll 1
+            for (int n = s.n0; n < s.n1; ++n) {
+                const KeyTile k = key_tile(s, n, per);
+                if (!((k.streams >> st) & 1)) continue;
+                // the tile's pages (lane i: page i): logical number, and which of the warp's tokens take it
+                int lp = 0;
+                uint32_t takes = 0;
+                if (lane < k.np) {
+                    const size_t at = ((size_t)s.item * 3 + k.region) * a.cap + k.at + lane;
+                    lp = a.ent[at].y;
+                    takes = a.mask[(at * 2 + tile) * a.words + word];
+                }
+                wait(s_full + 8 * st, s_par);
+                s_par ^= 1;
+                if (!idle) {
+                    uint32_t lm = 0;  // the pages that this row takes
+                    // pages that end inside a row's sight, or that hold rows of no token (whose logits may be no numbers, also for rows
+                    // that do not take the page); columns behind the tile's last page
+                    bool edge = (k.np << a.page_shift) & 31;
+#pragma unroll 1
+                    for (int i = 0; i < k.np; ++i) {
+                        const uint32_t w = __shfl_sync(kFull, takes, i);
+                        const int p = __shfl_sync(kFull, lp, i);
+                        const bool on = live && ((w >> (row_token & 31)) & 1u);
+                        const int lim = p < a.prefix_pages ? a.prefix_len - (p << a.page_shift) : seen - ((p - a.prefix_pages) << a.page_shift);
+                        lm |= on ? 1u << i : 0u;
+                        edge |= lim < a.page_n && (on || lim + s.held - seen < a.page_n || p < a.prefix_pages);
+                    }
+                    tc_fence_after();
+                    if (__any_sync(kFull, edge)) {
+                        // hidden in S itself, so that the code below knows whole pages only
+#pragma unroll 1
+                        for (int c0 = 0; c0 < (k.np << a.page_shift); c0 += 32) {
+                            float x[32];
+                            tmem_ld32(tS + c0, x);
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const int c = c0 + 16 * hf, i = c >> a.page_shift;
+                                const int p = __shfl_sync(kFull, lp, i & 31);
+                                const int lim = p < a.prefix_pages ? a.prefix_len - (p << a.page_shift) : seen - ((p - a.prefix_pages) << a.page_shift);
+                                const int keys = (lm >> i) & 1u ? lim - (c & (a.page_n - 1)) : 0;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (e >= keys) x[16 * hf + e] = -INFINITY;
+                            }
+                            tmem_st32(tS + c0, x);
+                        }
+                    }
+                    float t;
+                    uint32_t p[2][32];
+                    bool look = __any_sync(kFull, lm != 0 && m == -INFINITY);
+#pragma unroll 1
+                    while (true) {
+                        if (look) {
+                            // The running maximum need not be one: any m that keeps the sums in range gives the same result, p and
+                            // l being floating point.  So it is looked for in a row's first tile and where the tile's sum shows
+                            // that the logits have outgrown m by far.
+                            float mn = m;
+#pragma unroll 1
+                            for (int c0 = 0; c0 < (k.np << a.page_shift); c0 += 32) {
+                                const bool h0 = (lm >> (c0 >> a.page_shift)) & 1u, h1 = (lm >> ((c0 + 16) >> a.page_shift)) & 1u;
+                                if (!__any_sync(kFull, h0 || h1)) continue;
+                                float x[32], m0 = -INFINITY, m1 = -INFINITY;
+                                tmem_ld32(tS + c0, x);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    m0 = fmaxf(m0, x[c]);
+                                    m1 = fmaxf(m1, x[16 + c]);
+                                }
+                                if (h0) mn = fmaxf(mn, m0);
+                                if (h1) mn = fmaxf(mn, m1);
+                            }
+                            const float alpha = m == -INFINITY ? 0.f : ex2_approx((m - mn) * kLogitScaleLog2);
+                            m = mn;
+                            l *= alpha;
+                            if (done > 0) {  // O holds the tiles before (S of this tile follows their P V)
+#pragma unroll 1
+                                for (int c0 = 0; c0 < 128; c0 += 32) {
+                                    float o[32];
+                                    tmem_ld32(tO + c0, o);
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) o[c] *= alpha;
+                                    tmem_st32(tO + c0, o);
+                                }
+                            }
+                        }
+                        const float off = m == -INFINITY ? 0.f : -m * kLogitScaleLog2;
+                        const uint64_t scale2 = pack2(kLogitScaleLog2, kLogitScaleLog2);
+                        uint64_t l2[2] = {0, 0};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const bool h0 = (lm >> ((32 * q) >> a.page_shift)) & 1u, h1 = (lm >> ((32 * q + 16) >> a.page_shift)) & 1u;
+                            if (__any_sync(kFull, h0 || h1)) {
+                                float x[32];
+                                tmem_ld32(tS + 32 * q, x);
+                                const float f0 = h0 ? off : -INFINITY, f1 = h1 ? off : -INFINITY;
+#pragma unroll
+                                for (int c = 0; c < 32; c += 2) {
+                                    const float f = c < 16 ? f0 : f1;
+                                    float e0, e1;
+                                    unpack2(fma2(pack2(x[c], x[c + 1]), scale2, pack2(f, f)), e0, e1);
+                                    e0 = ex2_approx(e0);
+                                    e1 = ex2_approx(e1);
+                                    l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pack2(e0, e1));
+                                    p[q >> 1][16 * (q & 1) + (c >> 1)] = pack_bf16(e0, e1);
+                                }
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) p[q >> 1][16 * (q & 1) + c] = 0u;
+                            }
+                        }
+                        float lo, hi;
+                        unpack2(add2(l2[0], l2[1]), lo, hi);
+                        t = lo + hi;
+                        if (look || !__any_sync(kFull, !(t < kTileSum))) break;
+                        look = true;
+                    }
+                    tmem_st32_nowait(tS, p[0]);
+                    tmem_st32_nowait(tS + 32, p[1]);
+                    l += t;
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                warp_arrive(p_full + 8 * st);
+                ++done;
+            }
+            if (mine > 0) {
+                wait(o_full + 8 * st, o_par);
+                o_par ^= 1;
+            }
+            failed |= (a.fault & HSQ_FAULT_WAIT_SOFTMAX) != 0;
+            failed = __any_sync(kFull, failed);
+            if (failed) break;
+            tc_fence_after();
+            bool other = false;  // a lone tile: the second stream's share joins the first's
+            float w0 = 1.f, w1 = 0.f;
+            if (s.split) {
+                float2* ml = a.pair_ml + (size_t)blockIdx.x * kTileRows + row;
+                if (st) {
+                    __stcg(ml, make_float2(m, l));
+                    __threadfence_block();
+                    tc_fence_before();
+                    warp_arrive(m_full);
+                    wait(m_free, m_par);  // (O is read, and the sums)
+                    m_par ^= 1;
+                    failed = __any_sync(kFull, failed);
+                    if (failed) break;
+                    tc_fence_after();
+                    continue;
+                }
+                wait(m_full, m_par);
+                m_par ^= 1;
+                failed = __any_sync(kFull, failed);
+                if (failed) break;
+                tc_fence_after();
+                other = stream_tiles(s, 1, s.n1) > stream_tiles(s, 1, s.n0);
+                const float2 x = __ldcg(ml);
+                const float M = fmaxf(m, x.x);
+                w0 = m == -INFINITY && l == 0.f ? 0.f : ex2_approx((m - M) * kLogitScaleLog2);
+                w1 = x.x == -INFINITY && x.y == 0.f ? 0.f : ex2_approx((x.x - M) * kLogitScaleLog2);
+                l = l * w0 + x.y * w1;
+                m = M;
+            }
+            const bool cut = !s.whole;
+            const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.0f / l;  // (a sum that is not a number shows in the result)
+            const size_t to = (size_t)(s.first + t0 + row_token) * a.Hq + s.h * a.r + (row - row_token * a.r);
+            const size_t part = ((size_t)s.slot * 2 + st) * kTileRows;
+            if (live) {
+                if (cut) a.part_ml[part + row] = make_float2(m, l);
+                else if (a.lse) a.lse[to] = l == 0.f ? -INFINITY : m * kRsqrtD + logf(l);
+            }
+            if (!idle) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < 128; c0 += 32) {
+                    float o[32], y[32];
+                    if (mine > 0) tmem_ld32(tO + c0, o);
+                    if (other) {
+                        tmem_ld32(tO + 128 + c0, y);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = fmaf(y[c], w1, mine > 0 ? o[c] * w0 : 0.f);
+                    } else if (s.split) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] *= w0;
+                    }
+                    if (!live) continue;
+                    if (cut) {  // dims apart, rows side by side, so that a warp writes whole lines
+                        if (mine > 0 || other) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) a.part_o[part * 128 + (size_t)(c0 + c) * kTileRows + row] = o[c];
+                        }
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + to * 128 + c0);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8)
+                            dst[c >> 3] = l == 0.f ? make_uint4(0, 0, 0, 0)
+                                                   : make_uint4(pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
+                                                                pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv));
+                    }
+                }
+            }
+            tc_fence_before();  // (O has been read: the next segment's first P releases it)
+            if (s.split) warp_arrive(m_free);
+        }
+    }
+    if (failed) bad |= HSQ_DEVERR_WAIT;
+    if (bad) atomicOr(a.err, bad);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Join.  A CTA takes the item that run blockIdx.x is the second to work on, one tile, 32 rows (lane = row; a warp has 16 dims).
+__global__ void __launch_bounds__(256) page_join_kernel(const __grid_constant__ PageAttnArgs a) {
+    __shared__ float s_o[32][129];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, st = blockIdx.y & 1, row = 32 * (blockIdx.y >> 1) + lane;
+    const CutRecord c = *reinterpret_cast<const CutRecord*>(a.cut + 3 * blockIdx.x);
+    if (!c.live || (st && c.split)) return;
+    const int rows = (st ? c.toks1 : c.toks0) * a.r;
+    if (32 * (int)(blockIdx.y >> 1) >= rows) return;
+    const bool live = row < rows;
+    float o[16], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int d = 0; d < 16; ++d) o[d] = 0.f;
+    auto slot_of = [&](int k) { return ((size_t)(k == c.c0 ? 2 * k + 1 : 2 * k) * 2 + st) * kTileRows; };
+    if (live) {
+        for (int k = c.c0; k <= c.c1; ++k) M = fmaxf(M, a.part_ml[slot_of(k) + row].x);
+        for (int k = c.c0; k <= c.c1; ++k) {
+            const size_t at = slot_of(k);
+            const float2 ml = a.part_ml[at + row];
+            if (ml.y == 0.f) continue;
+            const float w = ex2_approx((ml.x - M) * kLogitScaleLog2);
+            L = fmaf(ml.y, w, L);
+#pragma unroll
+            for (int d = 0; d < 16; ++d) o[d] = fmaf(a.part_o[at * 128 + (size_t)(16 * warp + d) * kTileRows + row], w, o[d]);
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.0f / L;
+#pragma unroll
+    for (int d = 0; d < 16; ++d) s_o[lane][16 * warp + d] = o[d] * inv;
+    const int first = c.first + (st ? a.tpt : 0);
+    if (live && warp == 0 && a.lse)
+        a.lse[(size_t)(first + row / a.r) * a.Hq + c.h * a.r + row % a.r] = L == 0.f ? -INFINITY : M * kRsqrtD + logf(L);
+    __syncthreads();
+    for (int i = warp; i < 32; i += 8) {
+        const int y = 32 * (blockIdx.y >> 1) + i;
+        if (y >= rows) break;
+        const size_t to = (size_t)(first + y / a.r) * a.Hq + c.h * a.r + y % a.r;
+        const float* x = s_o[i] + 4 * lane;
+        *reinterpret_cast<uint2*>(a.out + to * 128 + 4 * lane) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    }
+}
+
 cudaError_t launch_cluster(const void* fn, unsigned grid, int threads, int cluster, size_t smem, cudaStream_t st, void** args) {
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(grid);
@@ -304,6 +1211,47 @@ cudaError_t launch_cluster(const void* fn, unsigned grid, int threads, int clust
     return cudaLaunchKernelExC(&lc, fn, args);
 }
 
+// The workspace's pieces and their offsets.
+struct Layout {
+    size_t head, req, unit, short_row, count, ent, mask, part_o, part_ml, pair_ml, cut, bytes;
+    int few, tpt, words, cap, runs, units, rows;
+};
+
+Layout layout_of(const hsq_ctx* ctx, int page_n, int rows, int B, int width, int prefix_len, int top, int max_new) {
+    Layout x{};
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += (n + 255) / 256 * 256;
+        return here;
+    };
+    const int r = ctx->r, Hkv = ctx->cfg.n_kv_heads;
+    x.tpt = kTileRows / r;
+    x.words = (x.tpt + 31) / 32;
+    x.few = kFewColumns / r;
+    x.runs = ctx->num_sms;
+    x.head = take(256);
+    if (max_new > x.few) {
+        const int D = 2 * x.tpt;
+        x.units = rows / D + 1 + std::min(B, rows / (x.few + 1));
+        x.rows = (int)std::min<long long>(rows, (long long)B * x.few);
+        x.cap = (int)std::min<long long>((prefix_len + page_n - 1) / page_n + (long long)width, (long long)x.tpt * top);
+        const size_t items = (size_t)x.units * Hkv, lists = items * 3 * x.cap;
+        x.req = take((size_t)B * 16);
+        x.unit = take((size_t)x.units * 8);
+        x.short_row = take((size_t)x.rows * 4);
+        x.count = take(items * 16);
+        x.ent = take(lists * 8);
+        x.mask = take(lists * 8 * x.words);
+        x.part_o = take((size_t)x.runs * 4 * kTileRows * 128 * 4);
+        x.part_ml = take((size_t)x.runs * 4 * kTileRows * 8);
+        x.pair_ml = take((size_t)x.runs * kTileRows * 8);
+        x.cut = take((size_t)x.runs * 48);
+    }
+    x.bytes = at;
+    return x;
+}
+
 }  // namespace
 
 extern "C" {
@@ -313,7 +1261,7 @@ hsq_status hsq_page_attn_workspace_size(const hsq_ctx* ctx, int page_n, int rows
     if (!ctx || !bytes) return hsq::fail(nullptr, HSQ_ERR_INVALID, "ctx or bytes is NULL");
     const char* wrong = hsq::selection_shape_wrong(page_n, rows, B, width, prefix_len, top, max_new);
     if (wrong) return hsq::fail(nullptr, HSQ_ERR_INVALID, wrong);
-    *bytes = 256;
+    *bytes = layout_of(ctx, page_n, rows, B, width, prefix_len, top, max_new).bytes;
     return HSQ_OK;
 }
 
@@ -331,9 +1279,8 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
     if (prefix_len > 0 && !prefix) return hsq::fail(ctx, HSQ_ERR_INVALID, "prefix is NULL with prefix_len > 0");
     if (((uintptr_t)q | (uintptr_t)out) & 15u) return hsq::fail(ctx, HSQ_ERR_INVALID, "q and out must be 16-byte aligned");
     if ((uintptr_t)workspace & 255u) return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace must be 256-byte aligned");
-    size_t need = 0;
-    hsq_page_attn_workspace_size(ctx, pages->page_n, rows, B, width, prefix_len, top, max_new, &need);
-    if (workspace_bytes < need)
+    const Layout x = layout_of(ctx, pages->page_n, rows, B, width, prefix_len, top, max_new);
+    if (workspace_bytes < x.bytes)
         return hsq::fail(ctx, HSQ_ERR_INVALID, "workspace smaller than hsq_page_attn_workspace_size");
     const int Hq = ctx->cfg.n_q_heads, Hkv = ctx->cfg.n_kv_heads, P = pages->page_n, np = (prefix_len + P - 1) / P;
     if ((long long)rows * Hkv >= (1LL << 27)) return hsq::fail(ctx, HSQ_ERR_INVALID, "too many rows");
@@ -341,7 +1288,7 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
     const hsq::Span ins[] = {{q, q_bytes}, {q_start, 4 * ((size_t)B + 1)}, {lens, 4 * (size_t)B}, {table, 4 * (size_t)B * width},
                              {prefix_len > 0 ? prefix : nullptr, 4 * (size_t)np}, {sel, (size_t)rows * Hkv * top * 4},
                              {pages->k, pool}, {pages->v, pool}};
-    const hsq::Span outs[] = {{out, q_bytes}, {lse_opt, (size_t)rows * Hq * 4}, {workspace, need}};
+    const hsq::Span outs[] = {{out, q_bytes}, {lse_opt, (size_t)rows * Hq * 4}, {workspace, x.bytes}};
     if (hsq::outputs_overlap(ins, outs))
         return hsq::fail(ctx, HSQ_ERR_INVALID, "an output or the workspace of hsq_page_attn overlaps another argument");
     if ((st = hsq::check_device(ctx)) != HSQ_OK) return st;
@@ -353,22 +1300,51 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
     a.rows = rows; a.B = B; a.width = width; a.prefix_len = prefix_len; a.prefix_pages = np; a.max_new = max_new;
     a.n_pages = pages->n_pages; a.page_n = P; a.page_shift = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
     a.Hq = Hq; a.Hkv = Hkv; a.r = ctx->r; a.top = top;
-    a.fault = (int)hsq::fault_mask() & HSQ_FAULT_WAIT_FEW;
+    a.fault = (int)hsq::fault_mask() & (HSQ_FAULT_WAIT_LOAD | HSQ_FAULT_WAIT_MMA | HSQ_FAULT_WAIT_QUERY | HSQ_FAULT_WAIT_SOFTMAX | HSQ_FAULT_WAIT_FEW);
     a.polls = a.fault ? 1 << 8 : 1 << 18;  // (a poll that finds nothing takes 4 us: 1 ms, or a second)
     a.err = ctx->d_err;
-    CUtensorMap mk, mv;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.few = x.few; a.tpt = x.tpt; a.words = x.words; a.cap = x.cap; a.runs = x.runs; a.units_cap = x.units; a.rows_cap = x.rows;
+    a.head = reinterpret_cast<TileHead*>(ws + x.head);
+    a.req = reinterpret_cast<int4*>(ws + x.req);
+    a.unit = reinterpret_cast<int2*>(ws + x.unit);
+    a.short_row = reinterpret_cast<int*>(ws + x.short_row);
+    a.count = reinterpret_cast<int4*>(ws + x.count);
+    a.ent = reinterpret_cast<int2*>(ws + x.ent);
+    a.mask = reinterpret_cast<uint32_t*>(ws + x.mask);
+    a.part_o = reinterpret_cast<float*>(ws + x.part_o);
+    a.part_ml = reinterpret_cast<float2*>(ws + x.part_ml);
+    a.pair_ml = reinterpret_cast<float2*>(ws + x.pair_ml);
+    a.cut = reinterpret_cast<int4*>(ws + x.cut);
+    CUtensorMap mq, mk, mv, mk16, mv16;
     if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const uint64_t n = (uint64_t)pages->n_pages * Hkv * P;
-    if (!encode_rows(&mk, pages->k, n, 16) || !encode_rows(&mv, pages->v, n, 16))
+    if (!encode_rows(&mk16, pages->k, n, 16) || !encode_rows(&mv16, pages->v, n, 16))
         return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const long long units = (long long)rows * Hkv;
+    cudaError_t e;
+    const bool tiles = max_new > x.few;
+    if (tiles) {
+        if (!encode_q(&mq, q, rows, Hq, a.r, x.tpt) || !encode_rows(&mk, pages->k, n, P) || !encode_rows(&mv, pages->v, n, P))
+            return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
+        void* args[] = {&a};
+        void* tc_args[] = {&mq, &mk, &mv, &a};
+        if ((e = hsq::raise_smem_limit((const void*)page_tiles_kernel, ctx->device, kTcSmem)) != cudaSuccess)
+            return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(page_tiles)");
+        if ((e = launch((const void*)page_plan_kernel, 1, kPlanThreads, 0, s, false, args)) != cudaSuccess ||
+            (e = launch((const void*)page_list_kernel, x.units * Hkv, kListThreads, 0, s, false, args)) != cudaSuccess ||
+            (e = launch((const void*)page_tiles_kernel, x.runs, kTcThreads, kTcSmem, s, false, tc_args)) != cudaSuccess)
+            return hsq::cuda_fail(ctx, e, "page_attn tiles");
+        page_join_kernel<<<dim3(x.runs, 8), 256, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return hsq::cuda_fail(ctx, e, "page_attn join");
+    }
+    const long long units = (tiles ? (long long)x.rows : rows) * Hkv;
     int S = 1;
     while (S < 8 && units * S < 4LL * ctx->num_sms && (long long)top * P >= 128LL * S) S *= 2;
     const void* fn = (const void*)page_attn_rows_kernel;
-    cudaError_t e = hsq::raise_smem_limit(fn, ctx->device, kRowSmem);
+    e = hsq::raise_smem_limit(fn, ctx->device, kRowSmem);
     if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(page_attn)");
-    void* args[] = {&mk, &mv, &a};
+    void* args[] = {&mk16, &mv16, &a};
     if ((e = launch_cluster(fn, (unsigned)(units * S), kThreadsRow, S, kRowSmem, s, args)) != cudaSuccess)
         return hsq::cuda_fail(ctx, e, "page_attn");
     return HSQ_OK;

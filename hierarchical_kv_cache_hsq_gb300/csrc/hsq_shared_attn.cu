@@ -301,12 +301,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     }
 }
 
-// One arrival for the whole warp, after every lane's writes.
-__device__ __forceinline__ void warp_arrive(uint32_t bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
 // ---------------------------------------------------------------------------------------
 // Main kernel.  One CTA per SM, 12 warps: softmax warps 0-3 (stream 0) and 4-7 (stream 1),
 // warp 8 walks the run and loads keys and values, warp 9 issues the MMAs (one elected thread), warp 10 loads
@@ -1616,15 +1610,6 @@ __global__ void __launch_bounds__(64 * G, G == 8 ? 1 : 4) shared_join_kernel(con
 }
 
 // ---- host side --------------------------------------------------------------------------
-
-// queries [rows][Hq][128]: a box is `tokens` tokens x the r heads of a KV head x 64 columns
-bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint32_t r, uint32_t tokens) {
-    const cuuint64_t dims[3] = {128, Hq, rows}, strides[2] = {256, 256 * Hq};
-    const cuuint32_t box[3] = {64, r, tokens}, es[3] = {1, 1, 1};
-    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // The workspace's pieces and their offsets.
 struct Layout { size_t head, req, of, c_at, b_at, d_at, cut, a_o, a_ml, b_o, b_ml, c_o, c_ml, d_o, d_ml, bytes; int runs, own_rows, few_rows, tokens; };
