@@ -515,9 +515,16 @@ constexpr uint32_t kOffQ = kTileStages * kTileBytes, kOffBars = kOffQ + 2 * kTil
 constexpr int kTcBars = 2 * kTileStages + 16 + 2 * kQueue;
 constexpr uint32_t kSegBytes = 96;
 constexpr uint32_t kOffSeg = kOffBars + 8 * kTcBars;
-constexpr uint32_t kTcSmem = kOffSeg + kQueue * kSegBytes + 16 + 1024;  // + TMEM address, alignment
+// Notes on the key tiles, written with their keys' load: [0] what the MMA thread does (kNote*), [1] the tile's pages, bit
+// 8: the softmax has to look at single keys, [2 + i] page i's logical number, then [page][2][words] the tiles' tokens that take it.
+// Five, because a softmax may be four tiles behind the loads.
+constexpr int kNotes = 5, kNoteWords = 2 + 8 + 64;
+enum : uint32_t { kNoteStreams = 3, kNoteFirst = 4, kNoteLast = 16, kNoteEnd = 64, kNoteGroups = 8 /* shift */ };
+constexpr uint32_t kOffNote = kOffSeg + kQueue * kSegBytes + 16;        // (+ TMEM address)
+constexpr uint32_t kTcSmem = kOffNote + kNotes * kNoteWords * 4 + 1024;  // + alignment
 static_assert(kOffSeg % 16 == 0, "segments lie on 16-byte boundaries");
-constexpr int kSegReaders = 10;  // 8 softmax warps, the MMA thread, the query loader
+static_assert(kTcSmem <= 232448, "shared memory of a CTA");
+constexpr int kSegReaders = 10;  // 8 softmax warps, the loaders of queries and values
 
 // The key tiles [n0, n1) of an item that a run holds.
 struct alignas(16) TileSegment {
@@ -633,24 +640,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // out in turn.  The results are undefined, the error word says so, and the next call finds everything as it should be.
     auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_fast(bar, parity, failed, a.polls); };
 
-    // the next segment of the queue, read by one thread or by a warp
-    auto receive = [&](Ring<kQueue>& q, bool release) {
+    volatile uint32_t* notes = reinterpret_cast<volatile uint32_t*>(gbase + kOffNote);
+    // the next segment of the queue, read by a warp
+    auto receive = [&](Ring<kQueue>& q) {
         wait(seg_full + 8 * q.stage, q.phase);
+        failed = __any_sync(kFull, failed);  // (a warp stays together)
+        if (failed) return false;
         const int4* src = reinterpret_cast<const int4*>(gbase + kOffSeg + q.stage * kSegBytes);
         int4* dst = reinterpret_cast<int4*>(&s);
-        if (release) failed = __any_sync(kFull, failed);  // (a warp stays together)
-        if (failed) {
-            s.live = 0;
-            return false;
-        }
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(TileSegment) / 16); ++i) dst[i] = src[i];
-        if (release) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(seg_empty + 8 * q.stage);
-        } else {
-            mbar_arrive(seg_empty + 8 * q.stage);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty + 8 * q.stage);
         q.advance();
         return s.live != 0;
     };
@@ -659,13 +660,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 152;\n");
         if (warp == 8) {
-            // ---- the run's segments, and per key tile the K pages, then the V pages (lane i: page i of the tile) ----
+            // ---- the run's segments, and the key tiles' pages (lane i: page i of the tile) ----
             Ring<kKeyStages> kr{0, 1};
-            Ring<kValueStages> vr{0, 1};
             Ring<kQueue> queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
-            uint32_t tail_par = 0;
-            bool tail_due = false;
             const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
+            const int W2 = 2 * a.words;
+            int note_at = 0;
+            auto note = [&](uint32_t what) {  // a tile without keys: a word to the MMA thread alone
+                wait(empty + 8 * kr.stage, kr.phase);
+                failed = __any_sync(kFull, failed);
+                if (failed) return;
+                if (lane == 0) {
+                    notes[note_at * kNoteWords] = what;
+                    mbar_arrive(full + 8 * kr.stage);
+                }
+                __syncwarp();
+                if (++note_at == kNotes) note_at = 0;
+                kr.advance();
+            };
             const int units = a.head->units, items = units * a.Hkv;
             long long total = 0;
             for (int i = lane; i < items; i += 32) total += a.count[i].w;
@@ -740,82 +752,89 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                         (int)(((begin + begin_of(s, tiles - 1) + 1) * runs - 1) / total), {}};
                 }
                 send();
+                if (tiles == 0) {  // (nobody may wait for a product that is due behind an item without a tile)
+                    note(0);
+                    continue;
+                }
+                int seen[2] = {0, 0};
+                const int all[2] = {stream_tiles(s, 0, s.n1) - stream_tiles(s, 0, s.n0), stream_tiles(s, 1, s.n1) - stream_tiles(s, 1, s.n0)};
+                const int first_sees = min(max(s.ahead + 1, 0), s.held);  // own tokens of the pair's first token
+                // A tile's pages (lane i: page i) and masks are read one tile ahead.
+                KeyTile k = key_tile(s, s.n0, per);
+                int2 e = make_int2(0, 0);
+                uint32_t m0 = 0, m1 = 0;
+                auto look_up = [&](const KeyTile& u) {
+                    const size_t to = ((size_t)item * 3 + u.region) * a.cap + u.at;
+                    e = lane < u.np ? a.ent[to + lane] : make_int2(0, 0);
+                    const uint32_t* m = a.mask + to * W2;
+                    m0 = lane < u.np * W2 ? m[lane] : 0u;
+                    m1 = lane + 32 < u.np * W2 ? m[lane + 32] : 0u;
+                };
+                look_up(k);
                 for (int t = s.n0; t < s.n1 && !failed; ++t) {
-                    const KeyTile k = key_tile(s, t, per);
-                    int2 e = make_int2(0, 0);
-                    int tokens = a.page_n;  // of the page
-                    if (lane < k.np) {
-                        e = a.ent[((size_t)item * 3 + k.region) * a.cap + k.at + lane];
-                        tokens = e.y < a.prefix_pages ? a.prefix_len - (e.y << a.page_shift) : s.held - ((e.y - a.prefix_pages) << a.page_shift);
-                    }
-                    const unsigned ends = __ballot_sync(kFull, tokens < a.page_n);  // pages that the tokens end inside of
+                    const int np = k.np, streams = k.streams, lp = e.y;
+                    const uint32_t w0 = m0, w1 = m1;
                     const int y = (e.x * a.Hkv + h) << a.page_shift;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t slot = kv ? kKeyStages + vr.stage : kr.stage;
-                        const uint32_t stage = base + slot * kTileBytes, bar = full + 8 * slot;
-                        wait(empty + 8 * slot, kv ? vr.phase : kr.phase);
-                        if (kv) failed |= (a.fault & HSQ_FAULT_WAIT_LOAD) != 0;
-                        failed = __any_sync(kFull, failed);
-                        if (failed) break;
-                        // Rows of values that no token has hold whatever the page holds; their weights are 0, so they have to
-                        // be finite.  Cleared here before the tile is handed over.
-                        const bool ragged = kv && ends;
-                        const uint32_t lands = ragged ? tail : bar;
-                        if (lane == 0) mbar_expect_tx(lands, k.np * page_bytes);
-                        __syncwarp();
-                        if (lane < k.np) {
-                            const void* map = kv ? &mv : &mk;
-                            tma_2d(stage + lane * half_page, map, 0, y, lands);
-                            tma_2d(stage + lane * half_page + kHalfBytes, map, 64, y, lands);
-                        }
-                        if (ragged) {
-                            wait(tail, tail_par);
-                            failed = __any_sync(kFull, failed);
-                            if (failed) {
-                                tail_due = true;
-                                break;
-                            }
-                            tail_par ^= 1;
-                            for (unsigned left = ends; left; left &= left - 1) {
-                                const int i = __ffs(left) - 1, have = max(__shfl_sync(kFull, tokens, i), 0);
-                                const int row0 = (i << a.page_shift) + have, z = (a.page_n - have) * 16;  // 16-byte chunks of both halves
-                                for (int x = lane; x < z; x += 32)
-                                    *reinterpret_cast<uint4*>(gbase + (stage - base) + ((x >> 3) & 1) * kHalfBytes + (row0 + (x >> 4)) * 128 +
-                                                              (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_async_smem();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar);
-                        }
-                        if (kv) vr.advance(); else kr.advance();
+                    int sees = a.page_n;  // tokens of the page that every row sees
+                    if (lane < np) sees = lp < a.prefix_pages ? a.prefix_len - (lp << a.page_shift) : first_sees - ((lp - a.prefix_pages) << a.page_shift);
+                    // (columns behind the tile's last page, where they share 32 with it, are looked at too)
+                    const bool edge = __any_sync(kFull, sees < a.page_n) || ((np << a.page_shift) & 31);
+                    if (t + 1 < s.n1) {
+                        k = key_tile(s, t + 1, per);
+                        look_up(k);
                     }
+                    uint32_t what = (uint32_t)streams | (uint32_t)((np << a.page_shift) >> 4) << kNoteGroups;
+#pragma unroll
+                    for (int st = 0; st < 2; ++st)
+                        if ((streams >> st) & 1) {
+                            if (seen[st] == 0) what |= kNoteFirst << st;
+                            if (++seen[st] == all[st]) what |= kNoteLast << st;
+                        }
+                    const uint32_t stage = base + kr.stage * kTileBytes, bar = full + 8 * kr.stage;
+                    wait(empty + 8 * kr.stage, kr.phase);
+                    failed = __any_sync(kFull, failed);
+                    if (failed) break;
+                    volatile uint32_t* to = notes + note_at * kNoteWords;
+                    if (lane < np) to[2 + lane] = lp;
+                    if (lane < np * W2) to[10 + lane] = w0;
+                    if (lane + 32 < np * W2) to[10 + 32 + lane] = w1;
+                    if (lane == 0) {
+                        to[0] = what;
+                        to[1] = np | (edge ? 256u : 0u);
+                    }
+                    if (++note_at == kNotes) note_at = 0;
+                    __syncwarp();
+                    if (lane == 0) mbar_expect_tx(bar, np * page_bytes);
+                    __syncwarp();
+                    if (lane < np) {
+                        tma_2d(stage + lane * half_page, &mk, 0, y, bar);
+                        tma_2d(stage + lane * half_page + kHalfBytes, &mk, 64, y, bar);
+                    }
+                    kr.advance();
+                    failed |= (a.fault & HSQ_FAULT_WAIT_LOAD) != 0;
                 }
             }
+            note(kNoteEnd);
             s.live = 0;
             send();
             if (lane == 0) *reinterpret_cast<CutRecord*>(a.cut + 3 * c) = cut;
-            if (failed) {  // see the copies in flight land before the CTA ends
-                for (int i = 0; i < kTileStages; ++i) {
-                    const bool lap = i < kKeyStages ? i < (int)kr.stage : i - kKeyStages < (int)vr.stage;
-                    mbar_wait(full + 8 * i, (i < kKeyStages ? kr.phase : vr.phase) ^ (lap ? 1u : 0u), 1 << 12);
-                }
-                if (tail_due) mbar_wait(tail, tail_par, 1 << 12);
-            }
+            if (failed)  // see the copies in flight land before the CTA ends
+                for (int i = 0; i < kKeyStages; ++i) mbar_wait(full + 8 * i, kr.phase ^ (i < (int)kr.stage ? 1u : 0u), 1 << 12);
         } else if (warp == 9 && elect_one()) {
             // ---- MMAs, one thread ----
+            // Key tile by key tile as the notes say.  Key tile g is in key stage g mod 3 and value stage g mod 2.  A stream's product
+            // with the values of its last tile is due until its next S is issued, or until it is two tiles behind, when
+            // its value stage is needed again.
             constexpr uint32_t idO = idesc_bf16_f32_bmn(128, 128);
-            Ring<kQueue> queue{0, 0};
+            Ring<kKeyStages> kr{0, 0};
             uint32_t q_par = 0, p_par = 0;  // a bit for each stream
-            // Key tiles are counted through the segments: tile g is in key stage g mod 3 and value stage g mod 2.  A stream's
-            // product with the values of its last key tile waits (`due`) until its next S is issued, or until the tile is
-            // two behind, when its value stage is needed again.
-            struct Due { uint32_t g; int g16, more, last; bool is; } due[2] = {{0, 0, 0, 0, false}, {0, 0, 0, 0, false}};
-            uint32_t g = 0;
-            int users[2] = {0, 0};  // products that a value stage has still to serve
-            auto scores = [&](int st, uint32_t stage, int g16) {  // S = Q K^T
+            // 0: none; else 1 | its note's word from bit 8 on | behind the segment's first (2) | its last (4); and the tile's number
+            uint32_t due0 = 0, due1 = 0, at0 = 0, at1 = 0;
+            uint32_t users = 0;  // bit i: the tile in value stage i has two products to serve, one is still to come
+            int slot = 0;
+            auto scores = [&](int st, uint32_t g16) {  // S = Q K^T
                 const uint32_t dS = tmem + 128 * st, idS = idesc_bf16_f32(128, 16 * g16);
-                const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + stage * kTileBytes);
+                const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + kr.stage * kTileBytes);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
@@ -823,75 +842,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 mma_commit(s_full + 8 * st);
             };
-            auto settle = [&](int st) {  // O += P V of the stream's tile that is due
-                Due& d = due[st];
-                if (!d.is) return;
-                const uint32_t stage = kKeyStages + (d.g & 1);
+            auto settle = [&](int st, uint32_t& due, uint32_t at) {  // O += P V of the stream's tile that is due
+                const uint32_t v = at & 1, stage = kKeyStages + v, g16 = due >> 8, more = (due >> 1) & 1;
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
                 const uint64_t dv = sw128_mn_desc(base + stage * kTileBytes, kHalfBytes);
-                wait(full + 8 * stage, (d.g >> 1) & 1);
+                wait(full + 8 * stage, (at >> 1) & 1);
                 wait(p_full + 8 * st, (p_par >> st) & 1);
                 if (__builtin_expect(failed, 0)) return;
                 p_par ^= 1u << st;
                 tc_fence_after();
-                if (d.g16 == 8) {
-                    mma_bf16_ts(dO, pa, dv, idO, d.more);
+                if (g16 == 8) {
+                    mma_bf16_ts(dO, pa, dv, idO, more);
 #pragma unroll
                     for (int k = 1; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
                 } else {
 #pragma unroll 1
-                    for (int k = 0; k < d.g16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, d.more | (k > 0));
+                    for (uint32_t k = 0; k < g16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, more | (k > 0));
                 }
-                if (--users[d.g & 1] == 0) mma_commit(empty + 8 * stage);
-                if (d.last) mma_commit(o_full + 8 * st);
-                d.is = false;
+                if (!((users >> v) & 1)) mma_commit(empty + 8 * stage);
+                users &= ~(1u << v);
+                if (due & 4) mma_commit(o_full + 8 * st);
+                due = 0;
             };
-            // (the older first: a stream whose softmax has still to join the other's part takes up no new tile before)
-            auto settle_all = [&] {
-                const bool first1 = due[0].is && due[1].is && (int)(due[1].g - due[0].g) < 0;
-                if (first1) settle(1);
-                settle(0);
-                settle(1);
-            };
-            // (after a wait that ran out no stage is handed back: its copy may still be under way)
-            auto work = [&] {
-                while (receive(queue, false)) {
-                    if (s.n0 == s.n1) settle_all();  // (nobody may wait for what is due behind an item without a tile)
-                    int done[2] = {0, 0};
-                    const int all[2] = {stream_tiles(s, 0, s.n1) - stream_tiles(s, 0, s.n0), stream_tiles(s, 1, s.n1) - stream_tiles(s, 1, s.n0)};
 #pragma unroll 1
-                    for (int t = s.n0; t < s.n1; ++t, ++g) {
-                        const KeyTile k = key_tile(s, t, per);
-                        const uint32_t stage = g % kKeyStages;
-#pragma unroll
-                        for (int st = 0; st < 2; ++st)
-                            if (due[st].is && g - due[st].g >= 2) settle(st);
-                        wait(full + 8 * stage, (g / kKeyStages) & 1);
-                        users[g & 1] = k.streams == 3 ? 2 : 1;
-#pragma unroll
-                        for (int st = 0; st < 2; ++st) {
-                            if (!((k.streams >> st) & 1)) continue;
-                            settle(st);
-                            if (done[st] == 0) {
-                                wait(q_full + 8 * st, (q_par >> st) & 1);
-                                q_par ^= 1u << st;
-                            }
-                            if (__builtin_expect(failed, 0)) return;
-                            const int g16 = (k.np << a.page_shift) >> 4;
-                            scores(st, stage, g16);
-                            const bool last = ++done[st] == all[st];
-                            if (last) mma_commit(q_empty + 8 * st);
-                            due[st] = Due{g, g16, done[st] > 1, last, true};
-                        }
-                        mma_commit(empty + 8 * stage);
-                        failed |= (a.fault & HSQ_FAULT_WAIT_MMA) != 0;
-                        if (__builtin_expect(failed, 0)) return;
+            for (uint32_t g = 0;; ++g) {
+                wait(full + 8 * kr.stage, kr.phase);
+                const uint32_t what = notes[slot * kNoteWords];
+                if (++slot == kNotes) slot = 0;
+                if (__builtin_expect(failed, 0)) break;
+                const bool flush = (what & kNoteStreams) == 0;
+                // (the older first: a stream whose softmax has still to join the other's part takes up no new tile before)
+                if (due1 && (g - at1 >= 2 || (flush && due0 && (int)(at1 - at0) < 0))) settle(1, due1, at1);
+                if (due0 && ((what & 1) || flush || g - at0 >= 2)) settle(0, due0, at0);
+                if (__builtin_expect(failed, 0)) break;
+                if (what & 1) {
+                    if (what & kNoteFirst) {
+                        wait(q_full, q_par & 1);
+                        q_par ^= 1;
                     }
+                    if (__builtin_expect(failed, 0)) break;
+                    scores(0, what >> kNoteGroups);
+                    if (what & kNoteLast) mma_commit(q_empty);
+                    due0 = 1u | (what & kNoteFirst ? 0u : 2u) | (what & kNoteLast ? 4u : 0u) | (what & ~255u);
+                    at0 = g;
                 }
-                if (failed) return;
-                settle_all();
-            };
-            work();
+                if (due1 && ((what & 2) || flush)) settle(1, due1, at1);
+                if (__builtin_expect(failed, 0)) break;
+                if (what & 2) {
+                    if (what & (kNoteFirst << 1)) {
+                        wait(q_full + 8, (q_par >> 1) & 1);
+                        q_par ^= 2;
+                    }
+                    if (__builtin_expect(failed, 0)) break;
+                    scores(1, what >> kNoteGroups);
+                    if (what & (kNoteLast << 1)) mma_commit(q_empty + 8);
+                    due1 = 1u | (what & (kNoteFirst << 1) ? 0u : 2u) | (what & (kNoteLast << 1) ? 4u : 0u) | (what & ~255u);
+                    at1 = g;
+                }
+                // (the value stage's tile of two ago has served: what was due from it has been issued)
+                if ((what & kNoteStreams) == 3) users |= 1u << (g & 1);
+                // (after a wait that ran out no stage is handed back: its copy may still be under way)
+                if (what & kNoteEnd) break;
+                mma_commit(empty + 8 * kr.stage);
+                if (flush) mma_commit(empty + 8 * (kKeyStages + (g & 1)));
+                kr.advance();
+                failed |= (a.fault & HSQ_FAULT_WAIT_MMA) != 0;
+            }
             if (failed) {  // what is in flight ends before its operands' and results' memory is given up
                 mma_commit(drain);
                 mbar_wait(drain, 0, 1 << 12);
@@ -901,7 +917,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             Ring<kQueue> queue{0, 0};
             uint32_t q_par = 3;  // (the buffers start empty)
             const uint32_t q_bytes = (uint32_t)a.tpt * a.r * 256u;
-            while (receive(queue, true)) {
+            while (receive(queue)) {
 #pragma unroll 1
                 for (int st = 0; st < 2; ++st) {
                     if (stream_tiles(s, st, s.n1) == stream_tiles(s, st, s.n0)) continue;
@@ -923,6 +939,74 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (failed)  // query tiles in flight land before the CTA ends
                 for (int st = 0; st < 2; ++st) mbar_wait(q_full + 8 * st, (q_par >> st) & 1, 1 << 12);
+        } else if (warp == 11) {
+            // ---- the value tiles' pages.  (By the keys' warp, in turn with them, the keys waited for the values' stages, one product
+            // later than their own need: 598 us instead of @@.) ----
+            Ring<kValueStages> vr{0, 1};
+            Ring<kQueue> queue{0, 0};
+            uint32_t tail_par = 0;
+            bool tail_due = false;
+            const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
+            while (receive(queue) && !failed) {
+                auto look_up = [&](const KeyTile& u) {
+                    return lane < u.np ? a.ent[((size_t)s.item * 3 + u.region) * a.cap + u.at + lane] : make_int2(0, 0);
+                };
+                KeyTile k = key_tile(s, s.n0, per);
+                int2 e = make_int2(0, 0);
+                if (s.n0 < s.n1) e = look_up(k);
+                for (int t = s.n0; t < max(s.n1, s.n0 + 1); ++t) {
+                    const uint32_t slot = kKeyStages + vr.stage, stage = base + slot * kTileBytes, bar = full + 8 * slot;
+                    const bool none = s.n0 == s.n1;  // (an item without a tile takes a stage too, as its note does)
+                    const int np = none ? 0 : k.np, y = (e.x * a.Hkv + s.h) << a.page_shift;
+                    int tokens = a.page_n;  // of the page
+                    if (lane < np) tokens = e.y < a.prefix_pages ? a.prefix_len - (e.y << a.page_shift) : s.held - ((e.y - a.prefix_pages) << a.page_shift);
+                    // Rows of values that no token has hold whatever the page holds; their weights are 0, so they have to
+                    // be finite.  Cleared here before the tile is handed over.
+                    const unsigned ends = __ballot_sync(kFull, tokens < a.page_n);
+                    if (t + 1 < s.n1) {
+                        k = key_tile(s, t + 1, per);
+                        e = look_up(k);
+                    }
+                    wait(empty + 8 * slot, vr.phase);
+                    failed = __any_sync(kFull, failed);
+                    if (failed) break;
+                    const uint32_t lands = ends ? tail : bar;
+                    if (lane == 0) {
+                        if (none) mbar_arrive(bar);
+                        else mbar_expect_tx(lands, np * page_bytes);
+                    }
+                    __syncwarp();
+                    if (lane < np) {
+                        tma_2d(stage + lane * half_page, &mv, 0, y, lands);
+                        tma_2d(stage + lane * half_page + kHalfBytes, &mv, 64, y, lands);
+                    }
+                    if (ends) {
+                        wait(tail, tail_par);
+                        failed = __any_sync(kFull, failed);
+                        if (failed) {
+                            tail_due = true;
+                            break;
+                        }
+                        tail_par ^= 1;
+                        for (unsigned left = ends; left; left &= left - 1) {
+                            const int i = __ffs(left) - 1, have = max(__shfl_sync(kFull, tokens, i), 0);
+                            const int row0 = (i << a.page_shift) + have, z = (a.page_n - have) * 16;  // 16-byte chunks of both halves
+                            for (int x = lane; x < z; x += 32)
+                                *reinterpret_cast<uint4*>(gbase + (stage - base) + ((x >> 3) & 1) * kHalfBytes + (row0 + (x >> 4)) * 128 +
+                                                          (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar);
+                    }
+                    vr.advance();
+                }
+            }
+            if (failed) {  // see the copies in flight land before the CTA ends
+                for (int i = 0; i < kValueStages; ++i)
+                    mbar_wait(full + 8 * (kKeyStages + i), vr.phase ^ (i < (int)vr.stage ? 1u : 0u), 1 << 12);
+                if (tail_due) mbar_wait(tail, tail_par, 1 << 12);
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n");
@@ -931,57 +1015,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + 128 * st, tO = tmem + lanes + 256 + 128 * st;
         uint32_t s_par = 0, o_par = 0, m_par = 0;
+        int note_at = 0;  // note of the segment's first tile
         Ring<kQueue> queue{0, 0};
         const int row_token = row / a.r, word = (32 * (warp & 3) / a.r) >> 5;  // (a warp's tokens share a word of the masks)
-        while (receive(queue, true)) {
+        while (receive(queue)) {
             const int toks = st ? s.toks1 : s.toks0, tile = st && !s.split ? 1 : 0, t0 = tile ? a.tpt : 0;
             const bool live = row_token < toks;
             const bool idle = 32 * (warp & 3) >= toks * a.r;  // (warp-uniform) no row of this warp in use
             const int seen = min(max(s.ahead + t0 + row_token + 1, 0), s.held);
             const int mine = stream_tiles(s, st, s.n1) - stream_tiles(s, st, s.n0);
+            const int alternate = s.split ? 1 << 30 : 2 * min(s.tiles[1], s.tiles[2]);
             float m = -INFINITY, l = 0.f;
-            int done = 0;
+            int n = s.n0;
 #pragma unroll 1
-            for (int n = s.n0; n < s.n1; ++n) {
-                const KeyTile k = key_tile(s, n, per);
-                if (!((k.streams >> st) & 1)) continue;
-                // the tile's pages (lane i: page i): logical number, and which of the warp's tokens take it
-                int lp = 0;
-                uint32_t takes = 0;
-                if (lane < k.np) {
-                    const size_t at = ((size_t)s.item * 3 + k.region) * a.cap + k.at + lane;
-                    lp = a.ent[at].y;
-                    takes = a.mask[(at * 2 + tile) * a.words + word];
-                }
+            for (int done = 0; done < mine; ++done, ++n) {
+                const int x = n - s.tiles[0];  // behind the tiles of both streams they take turns as long as both have some
+                if (x >= 0 && x < alternate) n += (x & 1) != st;
+                const volatile uint32_t* note = notes + ((note_at + n - s.n0) % kNotes) * kNoteWords;
                 wait(s_full + 8 * st, s_par);
                 s_par ^= 1;
                 if (!idle) {
+                    const uint32_t about = note[1];
+                    const int np = about & 255;
                     uint32_t lm = 0;  // the pages that this row takes
-                    // pages that end inside a row's sight, or that hold rows of no token (whose logits may be no numbers, also for rows
-                    // that do not take the page); columns behind the tile's last page
-                    bool edge = (k.np << a.page_shift) & 31;
-#pragma unroll 1
-                    for (int i = 0; i < k.np; ++i) {
-                        const uint32_t w = __shfl_sync(kFull, takes, i);
-                        const int p = __shfl_sync(kFull, lp, i);
-                        const bool on = live && ((w >> (row_token & 31)) & 1u);
-                        const int lim = p < a.prefix_pages ? a.prefix_len - (p << a.page_shift) : seen - ((p - a.prefix_pages) << a.page_shift);
-                        lm |= on ? 1u << i : 0u;
-                        edge |= lim < a.page_n && (on || lim + s.held - seen < a.page_n || p < a.prefix_pages);
-                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < np) lm |= ((note[10 + (2 * i + tile) * a.words + word] >> (row_token & 31)) & 1u) << i;
+                    if (!live) lm = 0;
+                    uint32_t gm = 0;  // the groups of 16 keys that it takes, and that any row of the warp takes
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) gm |= ((lm >> ((16 * j) >> a.page_shift)) & 1u) << j;
+                    const uint32_t wm = __reduce_or_sync(kFull, gm);
                     tc_fence_after();
-                    if (__any_sync(kFull, edge)) {
-                        // hidden in S itself, so that the code below knows whole pages only
+                    if (about >> 8) {
+                        // pages that end inside a row's sight, and rows of no token (whose logits may be no numbers): hidden in S
+                        // itself, so that the code below knows whole pages only
 #pragma unroll 1
-                        for (int c0 = 0; c0 < (k.np << a.page_shift); c0 += 32) {
+                        for (int c0 = 0; c0 < (np << a.page_shift); c0 += 32) {
                             float x[32];
                             tmem_ld32(tS + c0, x);
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
                                 const int c = c0 + 16 * hf, i = c >> a.page_shift;
-                                const int p = __shfl_sync(kFull, lp, i & 31);
+                                const int p = note[2 + (i & 7)];
                                 const int lim = p < a.prefix_pages ? a.prefix_len - (p << a.page_shift) : seen - ((p - a.prefix_pages) << a.page_shift);
-                                const int keys = (lm >> i) & 1u ? lim - (c & (a.page_n - 1)) : 0;
+                                const int keys = (gm >> (c >> 4)) & 1u ? lim - (c & (a.page_n - 1)) : 0;
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
                                     if (e >= keys) x[16 * hf + e] = -INFINITY;
@@ -1000,9 +1078,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             // that the logits have outgrown m by far.
                             float mn = m;
 #pragma unroll 1
-                            for (int c0 = 0; c0 < (k.np << a.page_shift); c0 += 32) {
-                                const bool h0 = (lm >> (c0 >> a.page_shift)) & 1u, h1 = (lm >> ((c0 + 16) >> a.page_shift)) & 1u;
-                                if (!__any_sync(kFull, h0 || h1)) continue;
+                            for (int c0 = 0; c0 < (np << a.page_shift); c0 += 32) {
+                                if (!((wm >> (c0 >> 4)) & 3u)) continue;
+                                const bool h0 = (gm >> (c0 >> 4)) & 1u, h1 = (gm >> (c0 >> 4)) & 2u;
                                 float x[32], m0 = -INFINITY, m1 = -INFINITY;
                                 tmem_ld32(tS + c0, x);
 #pragma unroll
@@ -1032,11 +1110,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         uint64_t l2[2] = {0, 0};
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const bool h0 = (lm >> ((32 * q) >> a.page_shift)) & 1u, h1 = (lm >> ((32 * q + 16) >> a.page_shift)) & 1u;
-                            if (__any_sync(kFull, h0 || h1)) {
+                            uint32_t* pq = p[q >> 1] + 16 * (q & 1);
+                            if ((wm >> (2 * q)) & 3u) {
                                 float x[32];
                                 tmem_ld32(tS + 32 * q, x);
-                                const float f0 = h0 ? off : -INFINITY, f1 = h1 ? off : -INFINITY;
+                                const float f0 = (gm >> (2 * q)) & 1u ? off : -INFINITY, f1 = (gm >> (2 * q)) & 2u ? off : -INFINITY;
 #pragma unroll
                                 for (int c = 0; c < 32; c += 2) {
                                     const float f = c < 16 ? f0 : f1;
@@ -1045,11 +1123,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                     e0 = ex2_approx(e0);
                                     e1 = ex2_approx(e1);
                                     l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pack2(e0, e1));
-                                    p[q >> 1][16 * (q & 1) + (c >> 1)] = pack_bf16(e0, e1);
+                                    pq[c >> 1] = pack_bf16(e0, e1);
                                 }
                             } else {
 #pragma unroll
-                                for (int c = 0; c < 16; ++c) p[q >> 1][16 * (q & 1) + c] = 0u;
+                                for (int c = 0; c < 16; ++c) pq[c] = 0u;
                             }
                         }
                         float lo, hi;
@@ -1065,8 +1143,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_fence_before();
                 }
                 warp_arrive(p_full + 8 * st);
-                ++done;
             }
+            note_at = (note_at + max(s.n1 - s.n0, 1)) % kNotes;  // (an item without a tile has a note too)
             if (mine > 0) {
                 wait(o_full + 8 * st, o_par);
                 o_par ^= 1;
