@@ -84,18 +84,18 @@ __global__ void __launch_bounds__(kThreadsRow)
     int bad = 0;
     bool failed = false;
 
-    bool listed_row = true;
     if (a.few < a.max_new) {  // the rows that do not go by tiles
-        listed_row = row < a.head->shorts;
-        row = listed_row ? a.short_row[row] : 0;
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (row >= a.head->shorts) return;  // (the whole cluster)
+        row = a.short_row[row];
     }
     if (tid == 0) {
         for (int i = 0; i < kWarps * kStages; ++i) mbar_init(base + kOffBar + 8 * i, 1);
         mbar_init_fence();
     }
     if (warp == 0) {  // the row's pages
-        RowOf ro{0, 0, false};
-        if (listed_row) ro = warp_row(a.q_start, a.lens, a.B, a.rows, a.max_new, a.width << a.page_shift, row, bad);
+        const RowOf ro = warp_row(a.q_start, a.lens, a.B, a.rows, a.max_new, a.width << a.page_shift, row, bad);
         int n = 0;
         if (ro.live) {
             const int32_t* sel = a.sel + ((size_t)row * a.Hkv + h) * a.top;
@@ -337,6 +337,7 @@ constexpr int kRunLeast = 16;        // cost of a run at least
 constexpr int kPlanThreads = 512;
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PageAttnArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int s_w[2][kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int bad = 0, units = 0, shorts = 0;  // before the round
@@ -417,6 +418,8 @@ constexpr int kListThreads = 256, kListBytes = 32768;
 __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_constant__ PageAttnArgs a) {
     __shared__ uint32_t s_mask[kListBytes / 4];  // [page of the window][2][words]
     __shared__ int s_n[3][kListThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int units = a.head->units, unit = blockIdx.x / a.Hkv, h = blockIdx.x - unit * a.Hkv;
     if (unit >= units) return;
@@ -436,18 +439,27 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
         for (int t = warp; t < toks; t += kListThreads / 32) {
             const int32_t* sel = a.sel + ((size_t)(p.first + t) * a.Hkv + h) * a.top;
             const int c = pages_of(t), tile = t >= p.toks[0], i = tile ? t - p.toks[0] : t;
-            int before = -1;
+            int before = -1, next = lane < a.top ? sel[lane] : -1;
             for (int i0 = 0; i0 < a.top; i0 += 32) {
-                const int e = i0 + lane < a.top ? sel[i0 + lane] : -1;
-                int top = e;
+                const int e = next;
+                next = i0 + 32 + lane < a.top ? sel[i0 + 32 + lane] : -1;
+                // the largest entry before this one: the one before it, where they ascend and no -1 stands between them
+                int ahead = __shfl_up_sync(kFull, e, 1);
+                if (lane == 0) ahead = before;
+                const unsigned there = __ballot_sync(kFull, e >= 0);
+                if ((there & (there + 1)) || __any_sync(kFull, e >= 0 && e <= ahead)) {
+                    int top = e;
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(kFull, top, d);
-                    if (lane >= d) top = max(top, o);
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(kFull, top, d);
+                        if (lane >= d) top = max(top, o);
+                    }
+                    ahead = __shfl_up_sync(kFull, top, 1);
+                    ahead = max(lane ? ahead : -1, before);
+                    before = max(before, __shfl_sync(kFull, top, 31));
+                } else if (there) {
+                    before = __shfl_sync(kFull, e, 31 - __clz(there));
                 }
-                int ahead = __shfl_up_sync(kFull, top, 1);
-                ahead = max(lane ? ahead : -1, before);
-                before = max(before, __shfl_sync(kFull, top, 31));
                 if (e >= 0) {
                     if (e >= c || e <= ahead) bad |= HSQ_DEVERR_SEL;
                     else if (e >= w0 && e < w1) atomicOr(&s_mask[(e - w0) * W2 + tile * W + (i >> 5)], 1u << (i & 31));
@@ -511,14 +523,15 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
 constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kTileStages = kKeyStages + kValueStages, kQueue = 2;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kOffQ = kTileStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
-// barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | drain | m_full | m_free | seg_full[2] | seg_empty[2]
-constexpr int kTcBars = 2 * kTileStages + 16 + 2 * kQueue;
+// barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | drain | m_full | m_free | seg_full[2] | seg_empty[2] | note_full[5]
+constexpr int kNotes = 5;
+constexpr int kTcBars = (2 * kTileStages + 16 + 2 * kQueue + kNotes + 1) / 2 * 2;
 constexpr uint32_t kSegBytes = 96;
 constexpr uint32_t kOffSeg = kOffBars + 8 * kTcBars;
 // Notes on the key tiles, written with their keys' load: [0] what the MMA thread does (kNote*), [1] the tile's pages, bit
 // 8: the softmax has to look at single keys, [2 + i] page i's logical number, then [page][2][words] the tiles' tokens that take it.
 // Five, because a softmax may be four tiles behind the loads.
-constexpr int kNotes = 5, kNoteWords = 2 + 8 + 64;
+constexpr int kNoteWords = 2 + 8 + 64;
 enum : uint32_t { kNoteStreams = 3, kNoteFirst = 4, kNoteLast = 16, kNoteEnd = 64, kNoteGroups = 8 /* shift */ };
 constexpr uint32_t kOffNote = kOffSeg + kQueue * kSegBytes + 16;        // (+ TMEM address)
 constexpr uint32_t kTcSmem = kOffNote + kNotes * kNoteWords * 4 + 1024;  // + alignment
@@ -599,6 +612,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t full = base + kOffBars, empty = full + 8 * kTileStages, q_full = empty + 8 * kTileStages, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_full = p_full + 16, tail = o_full + 16;
     const uint32_t drain = tail + 8, m_full = drain + 8, m_free = m_full + 8, seg_full = m_free + 8, seg_empty = seg_full + 8 * kQueue;
+    const uint32_t note_full = seg_empty + 8 * kQueue;
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(gbase + kOffSeg + kQueue * kSegBytes);
     const int per = kTileKeys >> a.page_shift;  // pages of a key tile
     int bad = 0;
@@ -623,6 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(seg_full + 8 * i, 1);
             mbar_init(seg_empty + 8 * i, kSegReaders);
         }
+        for (int i = 0; i < kNotes; ++i) mbar_init(note_full + 8 * i, 1);
         mbar_init_fence();
     }
     if (warp == 9) {
@@ -633,6 +648,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool failed = false;
     TileSegment s;
     // A wait that runs out sets its warp's `failed`.  From there on the warp arms no barrier, starts no copy and writes no segment
@@ -672,6 +689,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (failed) return;
                 if (lane == 0) {
                     notes[note_at * kNoteWords] = what;
+                    mbar_arrive(note_full + 8 * note_at);
                     mbar_arrive(full + 8 * kr.stage);
                 }
                 __syncwarp();
@@ -802,9 +820,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         to[0] = what;
                         to[1] = np | (edge ? 256u : 0u);
                     }
-                    if (++note_at == kNotes) note_at = 0;
                     __syncwarp();
-                    if (lane == 0) mbar_expect_tx(bar, np * page_bytes);
+                    if (lane == 0) {
+                        mbar_arrive(note_full + 8 * note_at);
+                        mbar_expect_tx(bar, np * page_bytes);
+                    }
+                    if (++note_at == kNotes) note_at = 0;
                     __syncwarp();
                     if (lane < np) {
                         tma_2d(stage + lane * half_page, &mk, 0, y, bar);
@@ -831,7 +852,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // 0: none; else 1 | its note's word from bit 8 on | behind the segment's first (2) | its last (4); and the tile's number
             uint32_t due0 = 0, due1 = 0, at0 = 0, at1 = 0;
             uint32_t users = 0;  // bit i: the tile in value stage i has two products to serve, one is still to come
-            int slot = 0;
+            uint32_t slot = 0, note_par = 0;
             auto scores = [&](int st, uint32_t g16) {  // S = Q K^T
                 const uint32_t dS = tmem + 128 * st, idS = idesc_bf16_f32(128, 16 * g16);
                 const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + kr.stage * kTileBytes);
@@ -841,6 +862,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     mma_bf16(dS, dq + o, dk + o, idS, k > 0);
                 }
                 mma_commit(s_full + 8 * st);
+            };
+            auto whole_product = [&](int st, uint32_t v, uint32_t parity) {  // O += P V of a whole tile, not the stream's first
+                const uint32_t pa = tmem + 128 * st, dO = pa + 256;
+                const uint64_t dv = sw128_mn_desc(base + (kKeyStages + v) * kTileBytes, kHalfBytes);
+                wait(full + 8 * (kKeyStages + v), parity);
+                wait(p_full + 8 * st, (p_par >> st) & 1);
+                p_par ^= 1u << st;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
             };
             auto settle = [&](int st, uint32_t& due, uint32_t at) {  // O += P V of the stream's tile that is due
                 const uint32_t v = at & 1, stage = kKeyStages + v, g16 = due >> 8, more = (due >> 1) & 1;
@@ -866,10 +897,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
 #pragma unroll 1
             for (uint32_t g = 0;; ++g) {
-                wait(full + 8 * kr.stage, kr.phase);
+                wait(note_full + 8 * slot, note_par);
                 const uint32_t what = notes[slot * kNoteWords];
-                if (++slot == kNotes) slot = 0;
+                wait(full + 8 * kr.stage, kr.phase);
+                if (++slot == kNotes) {
+                    slot = 0;
+                    note_par ^= 1;
+                }
                 if (__builtin_expect(failed, 0)) break;
+                // What most steps are, in straight code with constant operands (the tensor pipe holds but one or two MMAs more than
+                // the one it works on, so what the thread does in between shows): whole tiles, each stream's product of the tile
+                // before and S of this one.
+                constexpr uint32_t kWhole = 8u << kNoteGroups, kWholeDue = kWhole | 3u;
+                if (due0 == kWholeDue && due1 == kWholeDue) {
+                    if (what == (kWhole | 3u) && at0 == at1) {  // (then both are due of tile g - 1)
+                        whole_product(0, (g - 1) & 1, ((g - 1) >> 1) & 1);
+                        scores(0, 8);
+                        whole_product(1, (g - 1) & 1, ((g - 1) >> 1) & 1);
+                        if (__builtin_expect(failed, 0)) break;
+                        mma_commit(empty + 8 * (kKeyStages + ((g - 1) & 1)));
+                        scores(1, 8);
+                        mma_commit(empty + 8 * kr.stage);
+                        users = 1u << (g & 1);
+                        at0 = at1 = g;
+                        kr.advance();
+                        continue;
+                    }
+                    if (what == (kWhole | 1u) && at0 + 2 == g && at1 + 1 == g && users == 0) {
+                        whole_product(0, g & 1, ((g - 2) >> 1) & 1);
+                        if (__builtin_expect(failed, 0)) break;
+                        mma_commit(empty + 8 * (kKeyStages + (g & 1)));
+                        scores(0, 8);
+                        mma_commit(empty + 8 * kr.stage);
+                        at0 = g;
+                        kr.advance();
+                        continue;
+                    }
+                    if (what == (kWhole | 2u) && at1 + 2 == g && at0 + 1 == g && users == 0) {
+                        whole_product(1, g & 1, ((g - 2) >> 1) & 1);
+                        if (__builtin_expect(failed, 0)) break;
+                        mma_commit(empty + 8 * (kKeyStages + (g & 1)));
+                        scores(1, 8);
+                        mma_commit(empty + 8 * kr.stage);
+                        at1 = g;
+                        kr.advance();
+                        continue;
+                    }
+                }
                 const bool flush = (what & kNoteStreams) == 0;
                 // (the older first: a stream whose softmax has still to join the other's part takes up no new tile before)
                 if (due1 && (g - at1 >= 2 || (flush && due0 && (int)(at1 - at0) < 0))) settle(1, due1, at1);
@@ -1015,7 +1089,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + lanes + 128 * st, tO = tmem + lanes + 256 + 128 * st;
         uint32_t s_par = 0, o_par = 0, m_par = 0;
-        int note_at = 0;  // note of the segment's first tile
+        uint32_t tiles_done = 0;  // of the segments before
         Ring<kQueue> queue{0, 0};
         const int row_token = row / a.r, word = (32 * (warp & 3) / a.r) >> 5;  // (a warp's tokens share a word of the masks)
         while (receive(queue)) {
@@ -1031,21 +1105,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int done = 0; done < mine; ++done, ++n) {
                 const int x = n - s.tiles[0];  // behind the tiles of both streams they take turns as long as both have some
                 if (x >= 0 && x < alternate) n += (x & 1) != st;
-                const volatile uint32_t* note = notes + ((note_at + n - s.n0) % kNotes) * kNoteWords;
-                wait(s_full + 8 * st, s_par);
-                s_par ^= 1;
-                if (!idle) {
-                    const uint32_t about = note[1];
-                    const int np = about & 255;
-                    uint32_t lm = 0;  // the pages that this row takes
+                const uint32_t at = tiles_done + n - s.n0, slot = at % kNotes;
+                const volatile uint32_t* note = notes + slot * kNoteWords;
+                wait(note_full + 8 * slot, (at / kNotes) & 1);
+                const uint32_t about = note[1];
+                const int np = about & 255;
+                uint32_t gm = 0;  // the groups of 16 keys that this row takes, and those that any row of the warp takes
+                {
+                    uint32_t lm = 0;  // the pages
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         if (i < np) lm |= ((note[10 + (2 * i + tile) * a.words + word] >> (row_token & 31)) & 1u) << i;
                     if (!live) lm = 0;
-                    uint32_t gm = 0;  // the groups of 16 keys that it takes, and that any row of the warp takes
 #pragma unroll
                     for (int j = 0; j < 8; ++j) gm |= ((lm >> ((16 * j) >> a.page_shift)) & 1u) << j;
-                    const uint32_t wm = __reduce_or_sync(kFull, gm);
+                }
+                const uint32_t wm = __reduce_or_sync(kFull, gm);
+                wait(s_full + 8 * st, s_par);
+                s_par ^= 1;
+                if (!idle) {
                     tc_fence_after();
                     if (about >> 8) {
                         // pages that end inside a row's sight, and rows of no token (whose logits may be no numbers): hidden in S
@@ -1069,7 +1147,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     float t;
                     uint32_t p[2][32];
-                    bool look = __any_sync(kFull, lm != 0 && m == -INFINITY);
+                    bool look = __any_sync(kFull, gm != 0 && m == -INFINITY);
 #pragma unroll 1
                     while (true) {
                         if (look) {
@@ -1144,7 +1222,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 warp_arrive(p_full + 8 * st);
             }
-            note_at = (note_at + max(s.n1 - s.n0, 1)) % kNotes;  // (an item without a tile has a note too)
+            tiles_done += max(s.n1 - s.n0, 1);  // (an item without a tile has a note too)
             if (mine > 0) {
                 wait(o_full + 8 * st, o_par);
                 o_par ^= 1;
@@ -1233,14 +1311,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-// Join.  A CTA takes the item that run blockIdx.x is the second to work on, one tile, 32 rows (lane = row; a warp has 16 dims).
+// Join.  A CTA takes the item that a run is the second to work on, one tile, 32 rows (lane = row; a warp has 16 dims).
 __global__ void __launch_bounds__(256) page_join_kernel(const __grid_constant__ PageAttnArgs a) {
     __shared__ float s_o[32][129];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, st = blockIdx.y & 1, row = 32 * (blockIdx.y >> 1) + lane;
-    const CutRecord c = *reinterpret_cast<const CutRecord*>(a.cut + 3 * blockIdx.x);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, run = blockIdx.x >> 3, st = blockIdx.x & 1;
+    const int quarter = (blockIdx.x >> 1) & 3, row = 32 * quarter + lane;
+    const CutRecord c = *reinterpret_cast<const CutRecord*>(a.cut + 3 * run);
     if (!c.live || (st && c.split)) return;
     const int rows = (st ? c.toks1 : c.toks0) * a.r;
-    if (32 * (int)(blockIdx.y >> 1) >= rows) return;
+    if (32 * quarter >= rows) return;
     const bool live = row < rows;
     float o[16], M = -INFINITY, L = 0.f;
 #pragma unroll
@@ -1266,7 +1346,7 @@ __global__ void __launch_bounds__(256) page_join_kernel(const __grid_constant__ 
         a.lse[(size_t)(first + row / a.r) * a.Hq + c.h * a.r + row % a.r] = L == 0.f ? -INFINITY : M * kRsqrtD + logf(L);
     __syncthreads();
     for (int i = warp; i < 32; i += 8) {
-        const int y = 32 * (blockIdx.y >> 1) + i;
+        const int y = 32 * quarter + i;
         if (y >= rows) break;
         const size_t to = (size_t)(first + y / a.r) * a.Hq + c.h * a.r + y % a.r;
         const float* x = s_o[i] + 4 * lane;
@@ -1274,18 +1354,20 @@ __global__ void __launch_bounds__(256) page_join_kernel(const __grid_constant__ 
     }
 }
 
-cudaError_t launch_cluster(const void* fn, unsigned grid, int threads, int cluster, size_t smem, cudaStream_t st, void** args) {
+cudaError_t launch_cluster(const void* fn, unsigned grid, int threads, int cluster, size_t smem, cudaStream_t st, bool after, void** args) {
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(grid);
     lc.blockDim = dim3(threads);
     lc.dynamicSmemBytes = smem;
     lc.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
-    lc.numAttrs = 1;
+    lc.numAttrs = after ? 2 : 1;
     return cudaLaunchKernelExC(&lc, fn, args);
 }
 
@@ -1409,12 +1491,12 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
         void* tc_args[] = {&mq, &mk, &mv, &a};
         if ((e = hsq::raise_smem_limit((const void*)page_tiles_kernel, ctx->device, kTcSmem)) != cudaSuccess)
             return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(page_tiles)");
+        // (each behind the first begins while the one before ends, and waits for it before it reads)
         if ((e = launch((const void*)page_plan_kernel, 1, kPlanThreads, 0, s, false, args)) != cudaSuccess ||
-            (e = launch((const void*)page_list_kernel, x.units * Hkv, kListThreads, 0, s, false, args)) != cudaSuccess ||
-            (e = launch((const void*)page_tiles_kernel, x.runs, kTcThreads, kTcSmem, s, false, tc_args)) != cudaSuccess)
+            (e = launch((const void*)page_list_kernel, x.units * Hkv, kListThreads, 0, s, true, args)) != cudaSuccess ||
+            (e = launch((const void*)page_tiles_kernel, x.runs, kTcThreads, kTcSmem, s, true, tc_args)) != cudaSuccess ||
+            (e = launch((const void*)page_join_kernel, x.runs * 8, 256, 0, s, true, args)) != cudaSuccess)
             return hsq::cuda_fail(ctx, e, "page_attn tiles");
-        page_join_kernel<<<dim3(x.runs, 8), 256, 0, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return hsq::cuda_fail(ctx, e, "page_attn join");
     }
     const long long units = (tiles ? (long long)x.rows : rows) * Hkv;
     int S = 1;
@@ -1423,7 +1505,7 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
     e = hsq::raise_smem_limit(fn, ctx->device, kRowSmem);
     if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(page_attn)");
     void* args[] = {&mk16, &mv16, &a};
-    if ((e = launch_cluster(fn, (unsigned)(units * S), kThreadsRow, S, kRowSmem, s, args)) != cudaSuccess)
+    if ((e = launch_cluster(fn, (unsigned)(units * S), kThreadsRow, S, kRowSmem, s, tiles, args)) != cudaSuccess)
         return hsq::cuda_fail(ctx, e, "page_attn");
     return HSQ_OK;
 }
