@@ -196,4 +196,21 @@ inline cudaError_t launch(const void* fn, int grid, int threads, size_t smem, cu
     return cudaLaunchKernelExC(&lc, fn, args);
 }
 
+inline cudaError_t launch_cluster(const void* fn, unsigned grid, int threads, int cluster, size_t smem, cudaStream_t st, bool after, void** args) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = after ? 2 : 1;
+    return cudaLaunchKernelExC(&lc, fn, args);
+}
+
 }  // namespace hsq_paged
