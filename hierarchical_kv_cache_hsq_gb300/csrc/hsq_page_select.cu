@@ -56,8 +56,8 @@ __device__ __forceinline__ uint32_t query_codes(const uint16_t* q, int r) {
 }
 
 // Order-preserving key of a score, never 0 (which stands for a page that cannot be selected).
-__device__ __forceinline__ uint32_t score_key(int dot, float scale) {
-    const float s = __fmul_rn((float)dot, scale);
+__device__ __forceinline__ uint32_t score_key(float dot, float scale) {  // (dot: a whole number)
+    const float s = __fmul_rn(dot, scale);
     return s != s ? kKeyNan : max(ordered_key(s), 1u);
 }
 
@@ -67,14 +67,134 @@ __device__ __forceinline__ uint32_t score_key(int dot, float scale) {
 // shared memory, which selects.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
 
-__global__ void __launch_bounds__(kRowThreads) page_select_rows_kernel(const __grid_constant__ SelectArgs a) {
+struct RowSmem {
+    uint4 count[2][kRowWarps];  // counts at seven pivots, two to a word
+    uint32_t word[2][kRowWarps];
+};
+
+// The whole CTA's selection of the beta largest of the keys s_keys[0 .. G) (0: none; beta >= 1, at least one barrier since they were
+// written): the pages first + i of those taken go to out in ascending order; returns their number.
+// K keys a thread in registers; warp w has the 32 K from 32 K w on, in steps of 32.  A pass counts the keys at or above seven
+// pivots with one barrier: first at doubling distances below the largest key, then at the eighths of the span that holds the
+// beta-th, until exactly beta lie above or the span is one key (whose ties go to the lower pages).
+template <int K>
+__device__ int select_row(const uint32_t* s_keys, int G, int beta, int first, int32_t* out, RowSmem& sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = warp * 32 * K + lane;
+    uint32_t k[K];
+    uint32_t top = 0;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        k[i] = at + 32 * i < G ? s_keys[at + 32 * i] : 0u;
+        top = max(top, k[i]);
+        n += k[i] != 0u;
+    }
+    top = __reduce_max_sync(kFull, top);
+    n = __reduce_add_sync(kFull, n);
+    if (lane == 0) {
+        sm.word[0][warp] = top;
+        sm.word[1][warp] = n;
+    }
+    __syncthreads();
+    top = __reduce_max_sync(kFull, lane < kRowWarps ? sm.word[0][lane] : 0u);
+    n = __reduce_add_sync(kFull, lane < kRowWarps ? (int)sm.word[1][lane] : 0);
+    uint32_t lo = 1;       // at least beta keys (or all there are) lie at or above lo,
+    uint64_t above = (uint64_t)top + 1;  // n_above < beta at or above this
+    int n_lo = n, n_above = 0, turn = 0;
+    if (n > beta) {
+        bool doubling = true;
+        uint32_t step = 1u << 20;
+#pragma unroll 1
+        while (n_lo != beta && above - lo > 1) {
+            uint32_t v[7];
+#pragma unroll
+            for (int i = 0; i < 7; ++i) {  // descending
+                if (doubling) {
+                    const uint64_t d = (uint64_t)step << i;
+                    v[i] = above > d + lo ? (uint32_t)(above - d) : lo;
+                } else {
+                    v[i] = lo + (uint32_t)(((above - lo) * (7 - i)) >> 3);
+                }
+            }
+            uint32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+#pragma unroll
+                for (int j = 0; j < 7; ++j) c[j >> 1] += k[i] >= v[j] ? (j & 1 ? 1u << 16 : 1u) : 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = __reduce_add_sync(kFull, c[j]);
+            if (lane == 0) sm.count[turn][warp] = make_uint4(c[0], c[1], c[2], c[3]);
+            __syncthreads();
+            const uint4 x = lane < kRowWarps ? sm.count[turn][lane] : make_uint4(0, 0, 0, 0);
+            turn ^= 1;
+            c[0] = __reduce_add_sync(kFull, x.x);
+            c[1] = __reduce_add_sync(kFull, x.y);
+            c[2] = __reduce_add_sync(kFull, x.z);
+            c[3] = __reduce_add_sync(kFull, x.w);
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < 7; ++j) {
+                const int m = (int)(j & 1 ? c[j >> 1] >> 16 : c[j >> 1] & 0xFFFFu);
+                if (!found) {
+                    if (m >= beta) {
+                        lo = v[j];
+                        n_lo = m;
+                        found = true;
+                    } else {
+                        above = v[j];
+                        n_above = m;
+                    }
+                }
+            }
+            if (found || (uint64_t)step << 7 > above) doubling = false;
+            else step <<= 7;
+        }
+    }
+    const int ties = n_lo <= beta ? 1 << 30 : beta - n_above;  // of the keys equal to lo, those to be taken
+    int gt = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        gt += __popc(__ballot_sync(kFull, k[i] > lo));
+        eq += __popc(__ballot_sync(kFull, k[i] == lo));
+    }
+    __syncthreads();  // (the words and counts above have been read)
+    if (lane == 0) {
+        sm.word[0][warp] = gt;
+        sm.word[1][warp] = eq;
+    }
+    __syncthreads();
+    int g0 = 0, e0 = 0, g_all = 0, e_all = 0;  // before the warp; in all
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+        const int x = (int)sm.word[0][w], y = (int)sm.word[1][w];
+        g0 += w < warp ? x : 0;
+        e0 += w < warp ? y : 0;
+        g_all += x;
+        e_all += y;
+    }
+    const unsigned lt = (1u << lane) - 1u;
+    if (gt | eq) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const bool is_g = k[i] > lo, is_e = k[i] == lo;
+            const unsigned bg = __ballot_sync(kFull, is_g), be = __ballot_sync(kFull, is_e);
+            const int e = e0 + __popc(be & lt);
+            if (is_g || (is_e && e < ties)) out[g0 + __popc(bg & lt) + min(e, ties)] = first + at + 32 * i;
+            g0 += __popc(bg);
+            e0 += __popc(be);
+        }
+    }
+    return g_all + min(e_all, ties);
+}
+
+template <int K>  // keys a thread that the first CTA selects from, at most
+__global__ void __launch_bounds__(kRowThreads, K <= 16 ? 2 : 1) page_select_rows_kernel(const __grid_constant__ SelectArgs a) {
     extern __shared__ uint32_t s_keys[];
-    __shared__ SelectSmem ss;
+    __shared__ RowSmem s_sel;
     __shared__ uint32_t s_q[32];
     __shared__ int s_row[3];
-    __shared__ int s_out[HSQ_MAX_BETA];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     cg::cluster_group cluster = cg::this_cluster();
     const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -132,7 +252,7 @@ __global__ void __launch_bounds__(kRowThreads) page_select_rows_kernel(const __g
                 const int got = __shfl_sync(kFull, dot, 8 * (lane & 3));
                 if ((lane >> 2) == k) mine = got;
             }
-            if (i < g1) keys[i] = id >= 0 ? score_key(mine, scale) : 0u;
+            if (i < g1) keys[i] = id >= 0 ? score_key((float)mine, scale) : 0u;
         }
     }
     cluster.sync();  // the keys are in the first CTA; no remote access follows
@@ -141,32 +261,32 @@ __global__ void __launch_bounds__(kRowThreads) page_select_rows_kernel(const __g
         if (c <= a.top) {
             for (int i = tid; i < a.top; i += kRowThreads) out[i] = i < c ? i : -1;
         } else {
-            if (score) {
-                select_top_beta<kRowThreads>(s_keys, G, beta, s_out, ss);
-                __syncthreads();
-            }
             // the first pages, the selected ones and the last ones (which move up where fewer could be selected)
             for (int i = tid; i < a.first; i += kRowThreads) out[i] = i;
-            const bool got = tid < beta && s_out[tid] >= 0;
-            if (got) out[a.first + tid] = a.first + s_out[tid];
-            const int n = a.first + __syncthreads_count(got);
+            int n = a.first;
+            if (score) {
+                if (K > 4 && G <= 4 * kRowThreads) n += select_row<4>(s_keys, G, beta, a.first, out + a.first, s_sel);
+                else if (K > 16 && G <= 16 * kRowThreads) n += select_row<16>(s_keys, G, beta, a.first, out + a.first, s_sel);
+                else n += select_row<K>(s_keys, G, beta, a.first, out + a.first, s_sel);
+            }
             for (int i = tid; i < a.recent; i += kRowThreads) out[n + i] = c - a.recent + i;
             for (int i = n + a.recent + tid; i < a.top; i += kRowThreads) out[i] = -1;
         }
     }
     if (bad) atomicOr(a.err, bad);
 }
-static_assert(kRowThreads >= HSQ_MAX_BETA, "an entry a thread");
+static_assert(64 * kRowThreads >= HSQ_MAX_SELECT_PAGES, "the keys fit the registers");
 
 // ---------------------------------------------------------------------------------------
 // Rows by tiles of 16 of one request (prompts' chunks): a CTA for each (tile, KV head) goes over the pages in chunks of 1024.
 //   Scores by tensor-core products of whole numbers in fp16 (exact: |code| <= 127, sums below 2^21 in fp32): 16 rows (A, in
-//   registers) x 8 pages (B).  The dims are taken in an order that gives a lane 32 neighbouring bytes of a page's codes.
-//   Selection by a warp a row, the chunk's keys in its registers beside the best so far: from the largest key down by doubled
-//   steps until enough keys lie above, then halving until exactly as many do (or keys tie).
+//   registers) x 8 pages (B).  The dims are taken in an order that gives a lane 16 neighbouring bytes of a page's codes twice.
+//   Selection by a warp a row, the chunk's keys in its registers beside the best so far: histograms of 256 bins down to a bin of
+//   few keys.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kTileThreads = 256, kTileRow = 16, kChunk = 1024, kPitch = kChunk + 4, kCandRegs = HSQ_MAX_BETA / 32;
+constexpr int kTileThreads = 512, kTileRow = kTileThreads / 32, kChunk = 1024, kPitch = kChunk + 4, kBins = 256;
+static_assert(kTileRow == 16, "a warp a row, 16 rows a product");
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -183,13 +303,17 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x64806480u));
 }
 
-__global__ void __launch_bounds__(kTileThreads) page_select_tiles_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(const __grid_constant__ SelectArgs a) {
     extern __shared__ uint32_t s_dyn[];
     uint32_t* s_key = s_dyn;                                // [16][kPitch] the chunk's keys
     const int beta = a.top - a.first - a.recent;
     uint32_t* s_best = s_key + kTileRow * kPitch;           // [16][beta] the best so far, in the pages' order: key,
     int* s_page = reinterpret_cast<int*>(s_best + kTileRow * max(beta, 0));  // page
     __shared__ uint32_t s_q[kTileRow][32];
+    __shared__ alignas(16) int s_id[kChunk];
+    __shared__ alignas(16) float s_scale[kChunk];
+    __shared__ alignas(16) int s_hist[kTileThreads / 32][kBins + 4];
+    __shared__ uint32_t s_cand[kTileThreads / 32][32];
     __shared__ int s_scan[kTileThreads / 32];
     __shared__ int s_at[5];   // request, first row, rows, rows before it in the request's own count, own tokens held
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -234,166 +358,232 @@ __global__ void __launch_bounds__(kTileThreads) page_select_tiles_kernel(const _
     };
     const int last = pages_of(rows - 1) - a.recent;  // pages in [first, last) are scored
     // codes of the rows' queries
-    for (int j = warp; j < kTileRow; j += kTileThreads / 32)
-        s_q[j][lane] = j < rows ? query_codes(a.q + ((size_t)(first_row + j) * a.Hq + h * a.r) * 128, a.r) : 0u;
+    s_q[warp][lane] = warp < rows ? query_codes(a.q + ((size_t)(first_row + warp) * a.Hq + h * a.r) * 128, a.r) : 0u;
     __syncthreads();
     if (beta > 0 && pages_of(rows - 1) > a.top) {
-        uint32_t qf[8][4];  // k step s of lane t: dims 32 t + 4 s .. + 3 of rows g and g + 8
+        uint32_t qf[8][4];  // step k of lane t: dims 16 t + 4 k .. + 3, from k = 4 on 64 + 16 t + 4 (k - 4) .., of rows g and g + 8
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            codes_f16(s_q[g][8 * t + k], qf[k][0], qf[k][2]);
-            codes_f16(s_q[g + 8][8 * t + k], qf[k][1], qf[k][3]);
+            const int w = (k < 4 ? 4 * t : 12 + 4 * t) + k;
+            codes_f16(s_q[g][w], qf[k][0], qf[k][2]);
+            codes_f16(s_q[g + 8][w], qf[k][1], qf[k][3]);
         }
-        int have[2] = {0, 0};  // best so far of the warp's rows 2 warp, 2 warp + 1
+        int have = 0;  // best so far of the warp's row
         for (int c0 = a.first; c0 < last; c0 += kChunk) {
             const int c1 = min(last, c0 + kChunk);
-            // scores: a warp takes 8 pages at a time (lanes 4 g + t: page g)
-            for (int p0 = c0 + 8 * warp; p0 < c1; p0 += kTileThreads / 4) {
-                const int p = p0 + g;
-                int id = -1;
-                if (p < c1) {
-                    id = p < a.prefix_pages ? a.prefix[p] : a.table[(size_t)b * a.width + p - a.prefix_pages];
-                    if (id < 0 || id >= a.n_pages) {
-                        id = -1;
-                        bad |= HSQ_DEVERR_PAGE;
+            for (int i = tid; i <= c1 - c0 && i < kChunk; i += kTileThreads) {
+                const int p = c0 + i;
+                int id = p == c1 ? 0 : p < a.prefix_pages ? a.prefix[p] : a.table[(size_t)b * a.width + p - a.prefix_pages];
+                if (id < 0 || id >= a.n_pages) {
+                    id = -1;
+                    bad |= HSQ_DEVERR_PAGE;
+                }
+                if (p == c1) id = -1;
+                s_id[i] = id;
+                s_scale[i] = id >= 0 ? __ldg(a.scale + (size_t)id * a.Hkv + h) : 0.f;
+            }
+            __syncthreads();
+            // scores: a warp takes 8 pages at a time (lanes 4 g + t: page g), twice over with the loads first
+            for (int p0 = 8 * warp; p0 < c1 - c0; p0 += 2 * kTileThreads / 4) {
+                uint4 m[2][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int p = p0 + u * (kTileThreads / 4) + g, id = p < c1 - c0 ? s_id[p] : -1;
+                    m[u][0] = m[u][1] = make_uint4(0, 0, 0, 0);
+                    if (id >= 0) {
+                        const uint4* src = reinterpret_cast<const uint4*>(a.codes + ((size_t)id * a.Hkv + h) * 128 + 16 * t);
+                        m[u][0] = __ldg(src);
+                        m[u][1] = __ldg(src + 4);
                     }
                 }
-                uint4 m0 = make_uint4(0, 0, 0, 0), m1 = m0;
-                float scale = 0.f;
-                if (id >= 0) {
-                    const uint4* src = reinterpret_cast<const uint4*>(a.codes + ((size_t)id * a.Hkv + h) * 128 + 32 * t);
-                    m0 = __ldg(src);
-                    m1 = __ldg(src + 1);
-                    scale = __ldg(a.scale + (size_t)id * a.Hkv + h);
-                }
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                const uint32_t w[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+                float d[2][4];  // [u][e]: row g + 8 (e >> 1), page p0 + 128 u + 2 t + (e & 1)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t lo, hi;
-                    codes_f16(w[k], lo, hi);
-                    mma_f16(d, qf[k], lo, hi);
-                }
-                // d[e]: row g + 8 (e >> 1), page p0 + 2 t + (e & 1)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float sc = __shfl_sync(kFull, scale, 4 * (2 * t + e));
-                    const int of = __shfl_sync(kFull, id, 4 * (2 * t + e));
-                    const int col = p0 - c0 + 2 * t + e;
-                    s_key[g * kPitch + col] = of >= 0 ? score_key((int)d[e], sc) : 0u;
-                    s_key[(g + 8) * kPitch + col] = of >= 0 ? score_key((int)d[e + 2], sc) : 0u;
+                    for (int e = 0; e < 4; ++e) d[u][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint4 w = m[u][k >> 2];
+                        uint32_t lo, hi;
+                        codes_f16((k & 3) == 0 ? w.x : (k & 3) == 1 ? w.y : (k & 3) == 2 ? w.z : w.w, lo, hi);
+                        mma_f16(d[u], qf[k], lo, hi);
+                    }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int col = p0 + u * (kTileThreads / 4) + 2 * t;
+                    if (col >= c1 - c0) continue;
+                    const int2 id = *reinterpret_cast<const int2*>(s_id + col);  // (behind the last page: -1)
+                    const float2 sc = *reinterpret_cast<const float2*>(s_scale + col);
+                    *reinterpret_cast<uint2*>(s_key + g * kPitch + col) =
+                        make_uint2(id.x >= 0 ? score_key(d[u][0], sc.x) : 0u, id.y >= 0 ? score_key(d[u][1], sc.y) : 0u);
+                    *reinterpret_cast<uint2*>(s_key + (g + 8) * kPitch + col) =
+                        make_uint2(id.x >= 0 ? score_key(d[u][2], sc.x) : 0u, id.y >= 0 ? score_key(d[u][3], sc.y) : 0u);
                 }
             }
             __syncthreads();
-#pragma unroll 1
-            for (int rr = 0; rr < 2; ++rr) {
-                const int j = 2 * warp + rr, c = j < rows ? pages_of(j) : 0;
-                if (j >= rows || c <= a.top) continue;
+            const int j = warp, c = j < rows ? pages_of(j) : 0;
+            if (c > a.top) {
                 const int G = min(c - a.recent, c1) - c0;  // keys of the chunk that count for the row
                 uint32_t* best = s_best + j * beta;
                 int* page = s_page + j * beta;
-                const int nb = have[rr];
-                uint32_t k[kChunk / 32], o[kCandRegs];
-#pragma unroll
-                for (int i = 0; i < kChunk / 32; ++i) k[i] = 32 * i + lane < G ? s_key[j * kPitch + 32 * i + lane] : 0u;
-#pragma unroll
-                for (int i = 0; i < kCandRegs; ++i) o[i] = 32 * i < nb && 32 * i + lane < nb ? best[32 * i + lane] : 0u;
-                const int used = (nb + 31) / 32;
-                auto count = [&](uint32_t v) {  // keys >= v
-                    int n = 0;
-#pragma unroll
-                    for (int i = 0; i < kChunk / 32; ++i) n += k[i] >= v;
-#pragma unroll
-                    for (int i = 0; i < kCandRegs; ++i)
-                        if (i < used) n += o[i] >= v;
-                    return __reduce_add_sync(kFull, n);
+                uint32_t* row_keys = s_key + j * kPitch;
+                const int nb = have, steps = max(G + 31, 0) >> 5, used = (nb + 31) >> 5;
+                if (G > 0 && (G & 31) && lane >= (G & 31)) row_keys[32 * (steps - 1) + lane] = 0u;  // (the row's own)
+                __syncwarp();
+                // every key: the chunk's, then the best so far
+                auto each = [&](auto&& f) {
+#pragma unroll 8
+                    for (int i = 0; i < steps; ++i) f(row_keys[32 * i + lane]);
+#pragma unroll 2
+                    for (int i = 0; i < used; ++i) f(32 * i + lane < nb ? best[32 * i + lane] : 0u);
                 };
-                uint32_t lo = 1, top = 0;
-                int n_lo = count(1);
-                int ties = 0;  // of the keys equal to lo, those to be taken (all where count says so)
-                if (n_lo > beta) {
+                // The key lo above which fewer than beta keys lie, at or above which beta or more (or all there are).  A histogram of the
+                // keys in play (256 bins: at first of equal width in the score, then of the key's bits) tells the bin that holds the
+                // beta-th; up to 32 keys in it are ranked one against the other, of more the histogram is taken again.
+                uint32_t lo = 1;
+                int ties = 1 << 30;  // of the keys equal to lo, those to be taken (all)
+                int all = 0;
+                uint32_t khi = 0, klo = ~0u;
+                each([&](uint32_t v) {
+                    all += v != 0u;
+                    khi = max(khi, v);
+                    klo = min(klo, v - 1u);  // (0 last)
+                });
+                all = __reduce_add_sync(kFull, all);
+                if (all > beta) {
+                    khi = __reduce_max_sync(kFull, khi);
+                    klo = __reduce_min_sync(kFull, klo) + 1u;
+                    const float fmin = key_to_float(klo), per = (float)(kBins - 1) / (key_to_float(khi) - fmin);
+                    // (bins by rounding to a whole number in the last bits of 2^23 + it: no conversion)
+                    const float shifted = fmaf(-fmin, per, 8388608.f);
+                    bool by_score = isfinite(per) && isfinite(shifted) && isfinite(key_to_float(khi));
+                    int need = beta;  // of the keys in play
+                    int* hist = s_hist[warp];
+                    while (true) {
+                        const int shift = max(32 - __clz(khi - klo) - 8, 0);
+                        auto bin_of = [&](uint32_t v) {  // (monotone in the key)
+                            const int x = __float_as_int(fmaf(key_to_float(v), per, shifted)) - 0x4B000000;
+                            return by_score ? min(max(x, 0), kBins - 1) : (int)((v - klo) >> shift);
+                        };
 #pragma unroll
-                    for (int i = 0; i < kChunk / 32; ++i) top = max(top, k[i]);
+                        for (int i = 0; i < kBins / 128; ++i) reinterpret_cast<int4*>(hist)[32 * i + lane] = make_int4(0, 0, 0, 0);
+                        if (lane == 0) hist[kBins + 1] = 0;
+                        __syncwarp();
+                        each([&](uint32_t v) {
+                            if (v >= klo && v <= khi) atomicAdd(hist + bin_of(v), 1);
+                        });
+                        __syncwarp();
+                        // lane l has the bins 255 - 8 l .. 248 - 8 l
+                        const int4 h1 = reinterpret_cast<const int4*>(hist)[kBins / 4 - 1 - 2 * lane];
+                        const int4 h0 = reinterpret_cast<const int4*>(hist)[kBins / 4 - 2 - 2 * lane];
+                        const int hv[8] = {h1.w, h1.z, h1.y, h1.x, h0.w, h0.z, h0.y, h0.x};
+                        int sum = 0;
 #pragma unroll
-                    for (int i = 0; i < kCandRegs; ++i) top = max(top, o[i]);
-                    uint32_t hi = __reduce_max_sync(kFull, top);  // fewer than beta keys lie at or above hi + 1
-                    // (one past the largest: none)
-                    uint64_t above = (uint64_t)hi + 1;
-                    int n_above = 0;
-                    for (uint32_t step = 1u << 21; n_lo != beta; step = step < (1u << 31) ? step << 1 : step) {
-                        const uint32_t v = above > (uint64_t)step + 1 ? (uint32_t)(above - step) : 1u;
-                        const int n = v == 1 ? n_lo : count(v);
-                        if (n >= beta) {
-                            lo = v;
-                            n_lo = n;
+                        for (int i = 0; i < 8; ++i) sum += hv[i];
+                        int run = sum;
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) {
+                            const int x = __shfl_up_sync(kFull, run, d);
+                            if (lane >= d) run += x;
+                        }
+                        const int from = __ffs(__ballot_sync(kFull, run >= need)) - 1;
+                        run -= sum;
+                        int bin = 0, above = 0, in_bin = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (run < need && run + hv[i] >= need) {
+                                bin = kBins - 1 - 8 * lane - i;
+                                above = run;
+                                in_bin = hv[i];
+                            }
+                            run += hv[i];
+                        }
+                        bin = __shfl_sync(kFull, bin, from);
+                        need -= __shfl_sync(kFull, above, from);
+                        in_bin = __shfl_sync(kFull, in_bin, from);
+                        const bool few = in_bin <= 32;
+                        uint32_t bhi = 0, blo = ~0u;
+                        each([&](uint32_t v) {
+                            if (v >= klo && v <= khi && bin_of(v) == bin) {
+                                if (few) s_cand[warp][atomicAdd(hist + kBins + 1, 1)] = v;
+                                bhi = max(bhi, v);
+                                blo = min(blo, v);
+                            }
+                        });
+                        __syncwarp();
+                        if (few) {
+                            const uint32_t x = lane < in_bin ? s_cand[warp][lane] : 0u;
+                            int gt = 0, eq = 0;
+                            for (int i = 0; i < in_bin; ++i) {
+                                const uint32_t y = __shfl_sync(kFull, x, i);
+                                gt += y > x;
+                                eq += y == x;
+                            }
+                            const int who = __ffs(__ballot_sync(kFull, lane < in_bin && gt < need && gt + eq >= need)) - 1;
+                            lo = __shfl_sync(kFull, x, who);
+                            gt = __shfl_sync(kFull, gt, who);
+                            eq = __shfl_sync(kFull, eq, who);
+                            if (gt + eq > need) ties = need - gt;
                             break;
                         }
-                        above = v;
-                        n_above = n;
-                    }
-                    while (n_lo != beta && above - lo > 1) {
-                        const uint32_t v = lo + (uint32_t)((above - lo) >> 1);
-                        const int n = count(v);
-                        if (n >= beta) {
-                            lo = v;
-                            n_lo = n;
-                        } else {
-                            above = v;
-                            n_above = n;
+                        khi = __reduce_max_sync(kFull, bhi);
+                        klo = __reduce_min_sync(kFull, blo);
+                        by_score = false;
+                        if (klo == khi) {  // one key over and over
+                            lo = klo;
+                            if (in_bin > need) ties = need;
+                            break;
                         }
                     }
-                    ties = n_lo == beta ? 1 << 30 : beta - n_above;
-                } else {
-                    ties = 1 << 30;
                 }
                 // those taken, in the pages' order: the best so far (lower pages), then the chunk's
                 int n = 0, eq = 0;
                 const unsigned lt = (1u << lane) - 1u;
-                auto put = [&](uint32_t key, int pg, bool copy) {
-                    const bool e = key == lo;
-                    const unsigned be = __ballot_sync(kFull, e);
-                    const bool in = key > lo || (e && eq + __popc(be & lt) < ties);
+                auto put = [&](uint32_t key, int pg) {
+                    bool in = key >= lo;
+                    if (ties != 1 << 30) {
+                        const unsigned be = __ballot_sync(kFull, key == lo);
+                        in = key > lo || (key == lo && eq + __popc(be & lt) < ties);
+                        eq += __popc(be);
+                    }
                     const unsigned bi = __ballot_sync(kFull, in);
-                    if (in && copy) {
+                    if (in) {
                         best[n + __popc(bi & lt)] = key;
                         page[n + __popc(bi & lt)] = pg;
                     }
                     n += __popc(bi);
-                    eq += __popc(be);
                 };
-                __syncwarp();
 #pragma unroll 1
                 for (int i = 0; i < used; ++i) {
                     const int at = 32 * i + lane;
                     const uint32_t key = at < nb ? best[at] : 0u;
                     const int pg = at < nb ? page[at] : 0;
                     __syncwarp();
-                    put(key, pg, true);
+                    put(key, pg);
                     __syncwarp();
                 }
-#pragma unroll
-                for (int i = 0; i < kChunk / 32; ++i)
-                    if (32 * i < G) put(k[i], c0 + 32 * i + lane, true);
-                have[rr] = n;
+#pragma unroll 4
+                for (int i = 0; i < steps; ++i) put(row_keys[32 * i + lane], c0 + 32 * i + lane);
+                have = n;
             }
             __syncthreads();
         }
-        // what follows reads the warp's own rows only
-#pragma unroll 1
-        for (int rr = 0; rr < 2; ++rr) {
-            const int j = 2 * warp + rr;
-            if (j >= rows || pages_of(j) <= a.top) continue;
-            int32_t* out = a.sel + ((size_t)(first_row + j) * a.Hkv + h) * a.top;
-            for (int i = lane; i < have[rr]; i += 32) out[a.first + i] = s_page[j * beta + i];
-            const int c = pages_of(j), n = a.first + have[rr];
+        // (the warp's own row)
+        const int c = warp < rows ? pages_of(warp) : 0;
+        if (c > a.top) {
+            int32_t* out = a.sel + ((size_t)(first_row + warp) * a.Hkv + h) * a.top;
+            for (int i = lane; i < have; i += 32) out[a.first + i] = s_page[warp * beta + i];
+            const int n = a.first + have;
             for (int i = lane; i < a.first; i += 32) out[i] = i;
             for (int i = lane; i < a.recent; i += 32) out[n + i] = c - a.recent + i;
             for (int i = n + a.recent + lane; i < a.top; i += 32) out[i] = -1;
         }
     }
-    for (int j = warp; j < rows; j += kTileThreads / 32) {
-        const int c = pages_of(j);
-        int32_t* out = a.sel + ((size_t)(first_row + j) * a.Hkv + h) * a.top;
+    if (warp < rows) {
+        const int c = pages_of(warp);
+        int32_t* out = a.sel + ((size_t)(first_row + warp) * a.Hkv + h) * a.top;
         if (c <= a.top) {
             for (int i = lane; i < a.top; i += 32) out[i] = i < c ? i : -1;
         } else if (beta == 0) {
@@ -464,9 +654,11 @@ hsq_status hsq_page_select(hsq_ctx* ctx, const hsq_pages* pages, const hsq_summa
     if (max_new <= kFewRows) {
         const size_t smem = 4 * (size_t)(np + width);
         int S = 1;
-        while (S < 8 && (long long)rows * Hkv * S < 2LL * ctx->num_sms && np + width >= 512 * S) S *= 2;
-        if ((e = hsq::raise_smem_limit((const void*)page_select_rows_kernel, ctx->device, smem)) == cudaSuccess)
-            e = launch_cluster((const void*)page_select_rows_kernel, (unsigned)(rows * Hkv * S), kRowThreads, S, smem, st_, false, args);
+        while (S < 8 && (long long)rows * Hkv * 2 * S <= 2LL * ctx->num_sms && np + width >= 512 * S) S *= 2;
+        const void* fn = np + width <= 4 * kRowThreads ? (const void*)page_select_rows_kernel<4>
+                         : np + width <= 16 * kRowThreads ? (const void*)page_select_rows_kernel<16> : (const void*)page_select_rows_kernel<64>;
+        if ((e = hsq::raise_smem_limit(fn, ctx->device, smem)) == cudaSuccess)
+            e = launch_cluster(fn, (unsigned)(rows * Hkv * S), kRowThreads, S, smem, st_, false, args);
     } else {
         const int beta = top - first - recent;
         const size_t smem = 4 * (size_t)kTileRow * (kPitch + 2 * beta);
