@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
     __shared__ uint32_t s_q[kTileRow][32];
     __shared__ alignas(16) int s_id[kChunk];
     __shared__ alignas(16) float s_scale[kChunk];
-    __shared__ alignas(16) int s_hist[kTileThreads / 32][kBins + 4];
+    __shared__ alignas(16) int s_hist[kTileThreads / 32][kBins + 4];  // (and the number of candidates)
     __shared__ uint32_t s_cand[kTileThreads / 32][32];
     __shared__ int s_scan[kTileThreads / 32];
     __shared__ int s_at[5];   // request, first row, rows, rows before it in the request's own count, own tokens held
@@ -439,102 +439,158 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
 #pragma unroll 2
                     for (int i = 0; i < used; ++i) f(32 * i + lane < nb ? best[32 * i + lane] : 0u);
                 };
-                // The key lo above which fewer than beta keys lie, at or above which beta or more (or all there are).  A histogram of the
-                // keys in play (256 bins: at first of equal width in the score, then of the key's bits) tells the bin that holds the
-                // beta-th; up to 32 keys in it are ranked one against the other, of more the histogram is taken again.
+                // The key lo above which fewer than beta keys lie, at or above which beta or more (or all there are).  A histogram
+                // of the keys tells the bin that holds the beta-th; up to 32 keys in it are ranked one against the other, of more
+                // the histogram is taken again over the bin.
                 uint32_t lo = 1;
                 int ties = 1 << 30;  // of the keys equal to lo, those to be taken (all)
-                int all = 0;
-                uint32_t khi = 0, klo = ~0u;
-                each([&](uint32_t v) {
-                    all += v != 0u;
-                    khi = max(khi, v);
-                    klo = min(klo, v - 1u);  // (0 last)
-                });
-                all = __reduce_add_sync(kFull, all);
-                if (all > beta) {
-                    khi = __reduce_max_sync(kFull, khi);
-                    klo = __reduce_min_sync(kFull, klo) + 1u;
-                    const float fmin = key_to_float(klo), per = (float)(kBins - 1) / (key_to_float(khi) - fmin);
-                    // (bins by rounding to a whole number in the last bits of 2^23 + it: no conversion)
-                    const float shifted = fmaf(-fmin, per, 8388608.f);
-                    bool by_score = isfinite(per) && isfinite(shifted) && isfinite(key_to_float(khi));
-                    int need = beta;  // of the keys in play
-                    int* hist = s_hist[warp];
-                    while (true) {
-                        const int shift = max(32 - __clz(khi - klo) - 8, 0);
-                        auto bin_of = [&](uint32_t v) {  // (monotone in the key)
-                            const int x = __float_as_int(fmaf(key_to_float(v), per, shifted)) - 0x4B000000;
-                            return by_score ? min(max(x, 0), kBins - 1) : (int)((v - klo) >> shift);
-                        };
+                int need = beta;     // of the keys in play
+                int* hist = s_hist[warp];
+                auto clear = [&] {
 #pragma unroll
-                        for (int i = 0; i < kBins / 128; ++i) reinterpret_cast<int4*>(hist)[32 * i + lane] = make_int4(0, 0, 0, 0);
-                        if (lane == 0) hist[kBins + 1] = 0;
-                        __syncwarp();
+                    for (int i = 0; i < kBins / 128; ++i) reinterpret_cast<int4*>(hist)[32 * i + lane] = make_int4(0, 0, 0, 0);
+                    if (lane == 0) hist[kBins] = 0;  // candidates
+                    __syncwarp();
+                };
+                // the bin of the need-th key from the top (lane l adds up the bins 255 - 8 l .. 248 - 8 l); need becomes the number to
+                // be taken of it.  -1: there are not that many (bin 0 counts for none).
+                auto locate = [&](int& in_bin) {
+                    __syncwarp();
+                    const int4 h1 = reinterpret_cast<const int4*>(hist)[kBins / 4 - 1 - 2 * lane];
+                    const int4 h0 = reinterpret_cast<const int4*>(hist)[kBins / 4 - 2 - 2 * lane];
+                    const int hv[8] = {h1.w, h1.z, h1.y, h1.x, h0.w, h0.z, h0.y, lane == 31 ? 0 : h0.x};
+                    const int sum = ((hv[0] + hv[1]) + (hv[2] + hv[3])) + ((hv[4] + hv[5]) + (hv[6] + hv[7]));
+                    int run = sum;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int x = __shfl_up_sync(kFull, run, d);
+                        if (lane >= d) run += x;
+                    }
+                    const unsigned reach = __ballot_sync(kFull, run >= need);
+                    if (!reach) return -1;
+                    run -= sum;
+                    int bin = 0, above = 0, in = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (run < need && run + hv[i] >= need) {
+                            bin = kBins - 1 - 8 * lane - i;
+                            above = run;
+                            in = hv[i];
+                        }
+                        run += hv[i];
+                    }
+                    const int from = __ffs(reach) - 1;
+                    need -= __shfl_sync(kFull, above, from);
+                    in_bin = __shfl_sync(kFull, in, from);
+                    return __shfl_sync(kFull, bin, from);
+                };
+                auto rank = [&](int in_bin) {  // lo and ties from the candidates
+                    __syncwarp();
+                    const uint32_t x = lane < in_bin ? s_cand[warp][lane] : 0u;
+                    int gt = 0, eq = 0;
+                    for (int i = 0; i < in_bin; ++i) {
+                        const uint32_t y = __shfl_sync(kFull, x, i);
+                        gt += y > x;
+                        eq += y == x;
+                    }
+                    const int who = __ffs(__ballot_sync(kFull, lane < in_bin && gt < need && gt + eq >= need)) - 1;
+                    lo = __shfl_sync(kFull, x, who);
+                    gt = __shfl_sync(kFull, gt, who);
+                    eq = __shfl_sync(kFull, eq, who);
+                    if (gt + eq > need) ties = need - gt;
+                };
+                auto keep = [&](uint32_t v) { s_cand[warp][atomicAdd(hist + kBins, 1)] = v; };
+                // First 255 bins of equal width in the score from 0 to the largest (what lies below goes to bin 1, no key to bin 0):
+                // rounded to a whole number in the last bits of 2^23 + it, which takes no conversion.  The bins of a lane's keys stay in
+                // registers, four to a word, for the second look.
+                uint32_t most = 0;
+#pragma unroll 8
+                for (int i = 0; i < steps; ++i) most = max(most, row_keys[32 * i + lane]);
+#pragma unroll 1
+                for (int i = 0; i < used; ++i) most = max(most, 32 * i + lane < nb ? best[32 * i + lane] : 0u);
+                most = __reduce_max_sync(kFull, most);
+                const float per = 254.f / key_to_float(most);
+                auto bin_of = [&](uint32_t v) {
+                    const int x = __float_as_int(fmaf(key_to_float(v), per, 8388609.f)) - 0x4B000000;
+                    return v == 0u ? 0 : min(max(x, 1), kBins - 1);
+                };
+                const bool by_score = key_to_float(most) > 0.f;  // (also of an infinite score or none that is a number: NaN goes to the last bin)
+                uint32_t bins[kChunk / 128];
+                clear();
+#pragma unroll
+                for (int w = 0; w < kChunk / 128; ++w) {
+                    bins[w] = 0;
+                    if (4 * w < steps) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int x = 4 * w + i < steps ? bin_of(row_keys[32 * (4 * w + i) + lane]) : 0;
+                            atomicAdd(hist + x, 1);
+                            bins[w] |= (uint32_t)x << (8 * i);
+                        }
+                    }
+                }
+#pragma unroll 1
+                for (int i = 0; i < used; ++i) atomicAdd(hist + bin_of(32 * i + lane < nb ? best[32 * i + lane] : 0u), 1);
+                int in_bin = 0;
+                const int bin = locate(in_bin);
+                if (bin >= 0) {  // (else all are taken)
+                    if (by_score && in_bin <= 32) {
+                        const uint32_t four = 0x01010101u * (uint32_t)bin;
+#pragma unroll
+                        for (int w = 0; w < kChunk / 128; ++w) {
+                            uint32_t hit = __vcmpeq4(bins[w], four) & 0x01010101u;
+                            while (hit) {
+                                const int i = (__ffs(hit) - 1) >> 3;
+                                keep(row_keys[32 * (4 * w + i) + lane]);
+                                hit &= hit - 1;
+                            }
+                        }
+#pragma unroll 1
+                        for (int i = 0; i < used; ++i) {
+                            const uint32_t v = 32 * i + lane < nb ? best[32 * i + lane] : 0u;
+                            if (bin_of(v) == bin) keep(v);
+                        }
+                        rank(in_bin);
+                    } else {
+                        // crowded: by the keys' bits, over the bin or over all keys
+                        uint32_t klo = ~0u, khi = 0;
+                        if (!by_score) need = beta;
                         each([&](uint32_t v) {
-                            if (v >= klo && v <= khi) atomicAdd(hist + bin_of(v), 1);
-                        });
-                        __syncwarp();
-                        // lane l has the bins 255 - 8 l .. 248 - 8 l
-                        const int4 h1 = reinterpret_cast<const int4*>(hist)[kBins / 4 - 1 - 2 * lane];
-                        const int4 h0 = reinterpret_cast<const int4*>(hist)[kBins / 4 - 2 - 2 * lane];
-                        const int hv[8] = {h1.w, h1.z, h1.y, h1.x, h0.w, h0.z, h0.y, h0.x};
-                        int sum = 0;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sum += hv[i];
-                        int run = sum;
-#pragma unroll
-                        for (int d = 1; d < 32; d <<= 1) {
-                            const int x = __shfl_up_sync(kFull, run, d);
-                            if (lane >= d) run += x;
-                        }
-                        const int from = __ffs(__ballot_sync(kFull, run >= need)) - 1;
-                        run -= sum;
-                        int bin = 0, above = 0, in_bin = 0;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (run < need && run + hv[i] >= need) {
-                                bin = kBins - 1 - 8 * lane - i;
-                                above = run;
-                                in_bin = hv[i];
-                            }
-                            run += hv[i];
-                        }
-                        bin = __shfl_sync(kFull, bin, from);
-                        need -= __shfl_sync(kFull, above, from);
-                        in_bin = __shfl_sync(kFull, in_bin, from);
-                        const bool few = in_bin <= 32;
-                        uint32_t bhi = 0, blo = ~0u;
-                        each([&](uint32_t v) {
-                            if (v >= klo && v <= khi && bin_of(v) == bin) {
-                                if (few) s_cand[warp][atomicAdd(hist + kBins + 1, 1)] = v;
-                                bhi = max(bhi, v);
-                                blo = min(blo, v);
+                            if (v != 0u && (!by_score || bin_of(v) == bin)) {
+                                klo = min(klo, v);
+                                khi = max(khi, v);
                             }
                         });
-                        __syncwarp();
-                        if (few) {
-                            const uint32_t x = lane < in_bin ? s_cand[warp][lane] : 0u;
-                            int gt = 0, eq = 0;
-                            for (int i = 0; i < in_bin; ++i) {
-                                const uint32_t y = __shfl_sync(kFull, x, i);
-                                gt += y > x;
-                                eq += y == x;
+                        while (true) {
+                            klo = __reduce_min_sync(kFull, klo);
+                            khi = __reduce_max_sync(kFull, khi);
+                            // (the number to be taken is at most the number in play)
+                            const int shift = max(32 - __clz(khi - klo) - 7, 0);  // 128 bins, from 1 on
+                            clear();
+                            each([&](uint32_t v) {
+                                if (v >= klo && v <= khi) atomicAdd(hist + 1 + ((v - klo) >> shift), 1);
+                            });
+                            const int which = locate(in_bin);
+                            uint32_t l = ~0u, u = 0;
+                            const bool few = in_bin <= 32;
+                            each([&](uint32_t v) {
+                                if (v >= klo && v <= khi && 1 + (int)((v - klo) >> shift) == which) {
+                                    if (few) keep(v);
+                                    l = min(l, v);
+                                    u = max(u, v);
+                                }
+                            });
+                            if (few) {
+                                rank(in_bin);
+                                break;
                             }
-                            const int who = __ffs(__ballot_sync(kFull, lane < in_bin && gt < need && gt + eq >= need)) - 1;
-                            lo = __shfl_sync(kFull, x, who);
-                            gt = __shfl_sync(kFull, gt, who);
-                            eq = __shfl_sync(kFull, eq, who);
-                            if (gt + eq > need) ties = need - gt;
-                            break;
-                        }
-                        khi = __reduce_max_sync(kFull, bhi);
-                        klo = __reduce_min_sync(kFull, blo);
-                        by_score = false;
-                        if (klo == khi) {  // one key over and over
-                            lo = klo;
-                            if (in_bin > need) ties = need;
-                            break;
+                            klo = __reduce_min_sync(kFull, l);
+                            khi = __reduce_max_sync(kFull, u);
+                            if (klo == khi) {  // one key over and over
+                                lo = klo;
+                                if (in_bin > need) ties = need;
+                                break;
+                            }
                         }
                     }
                 }
