@@ -25,8 +25,6 @@ struct SelectArgs {
     int* err;
 };
 
-constexpr uint32_t kKeyNan = 0xFFFFFFFEu;
-
 // Codes of the sum of r query rows, by a whole warp: lane holds dims 4 lane .. 4 lane + 3, packed.
 __device__ __forceinline__ uint32_t query_codes(const uint16_t* q, int r) {
     const int lane = threadIdx.x & 31;
@@ -55,10 +53,11 @@ __device__ __forceinline__ uint32_t query_codes(const uint16_t* q, int r) {
     return w;
 }
 
-// Order-preserving key of a score, never 0 (which stands for a page that cannot be selected).
-__device__ __forceinline__ uint32_t score_key(float dot, float scale) {  // (dot: a whole number)
-    const float s = __fmul_rn(dot, scale);
-    return s != s ? kKeyNan : max(ordered_key(s), 1u);
+// Order-preserving key of the score dot * scale (dot: a whole number), never 0, which stands for a page that cannot be selected:
+// 0 and -0 alike (the sum with 0 makes both 0), -inf lowest, and the NaN that a product gives (0x7FFFFFFF) above all.
+__device__ __forceinline__ uint32_t score_key(float dot, float scale) {
+    const uint32_t u = __float_as_uint(__fmaf_rn(dot, scale, 0.f));
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -285,7 +284,10 @@ static_assert(64 * kRowThreads >= HSQ_MAX_SELECT_PAGES, "the keys fit the regist
 //   few keys.
 // ---------------------------------------------------------------------------------------
 
-constexpr int kTileThreads = 512, kTileRow = kTileThreads / 32, kChunk = 1024, kPitch = kChunk + 4, kBins = 256;
+constexpr int kTileThreads = 512, kTileRow = kTileThreads / 32, kChunk = 1024, kBins = 256;
+// A row's keys: 32 neighbours (a lane's) and two words between, so that lanes side by side read and rows side by side are written without bank
+// conflicts.
+constexpr int kLanePitch = 34, kPitch = kChunk / 32 * kLanePitch + 8;
 static_assert(kTileRow == 16, "a warp a row, 16 rows a product");
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
@@ -371,18 +373,19 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
         int have = 0;  // best so far of the warp's row
         for (int c0 = a.first; c0 < last; c0 += kChunk) {
             const int c1 = min(last, c0 + kChunk);
-            for (int i = tid; i <= c1 - c0 && i < kChunk; i += kTileThreads) {
+            bool gone = false;
+            for (int i = tid; i < c1 - c0; i += kTileThreads) {
                 const int p = c0 + i;
-                int id = p == c1 ? 0 : p < a.prefix_pages ? a.prefix[p] : a.table[(size_t)b * a.width + p - a.prefix_pages];
+                int id = p < a.prefix_pages ? a.prefix[p] : a.table[(size_t)b * a.width + p - a.prefix_pages];
                 if (id < 0 || id >= a.n_pages) {
                     id = -1;
                     bad |= HSQ_DEVERR_PAGE;
                 }
-                if (p == c1) id = -1;
+                gone |= id < 0;
                 s_id[i] = id;
                 s_scale[i] = id >= 0 ? __ldg(a.scale + (size_t)id * a.Hkv + h) : 0.f;
             }
-            __syncthreads();
+            gone = __syncthreads_or(gone);
             // scores: a warp takes 8 pages at a time (lanes 4 g + t: page g), twice over with the loads first
             for (int p0 = 8 * warp; p0 < c1 - c0; p0 += 2 * kTileThreads / 4) {
                 uint4 m[2][2];
@@ -414,29 +417,33 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                 for (int u = 0; u < 2; ++u) {
                     const int col = p0 + u * (kTileThreads / 4) + 2 * t;
                     if (col >= c1 - c0) continue;
-                    const int2 id = *reinterpret_cast<const int2*>(s_id + col);  // (behind the last page: -1)
-                    const float2 sc = *reinterpret_cast<const float2*>(s_scale + col);
-                    *reinterpret_cast<uint2*>(s_key + g * kPitch + col) =
-                        make_uint2(id.x >= 0 ? score_key(d[u][0], sc.x) : 0u, id.y >= 0 ? score_key(d[u][1], sc.y) : 0u);
-                    *reinterpret_cast<uint2*>(s_key + (g + 8) * kPitch + col) =
-                        make_uint2(id.x >= 0 ? score_key(d[u][2], sc.x) : 0u, id.y >= 0 ? score_key(d[u][3], sc.y) : 0u);
+                    const float2 sc = *reinterpret_cast<const float2*>(s_scale + col);  // (columns behind the last page are not looked at)
+                    uint32_t* to = s_key + g * kPitch + col + 2 * (col >> 5);
+                    *reinterpret_cast<uint2*>(to) = make_uint2(score_key(d[u][0], sc.x), score_key(d[u][1], sc.y));
+                    *reinterpret_cast<uint2*>(to + 8 * kPitch) = make_uint2(score_key(d[u][2], sc.x), score_key(d[u][3], sc.y));
                 }
             }
             __syncthreads();
+            if (gone) {
+                for (int i = lane; i < c1 - c0; i += 32)
+                    if (s_id[i] < 0) s_key[warp * kPitch + i + 2 * (i >> 5)] = 0u;
+                __syncwarp();
+            }
             const int j = warp, c = j < rows ? pages_of(j) : 0;
             if (c > a.top) {
                 const int G = min(c - a.recent, c1) - c0;  // keys of the chunk that count for the row
                 uint32_t* best = s_best + j * beta;
                 int* page = s_page + j * beta;
                 uint32_t* row_keys = s_key + j * kPitch;
-                const int nb = have, steps = max(G + 31, 0) >> 5, used = (nb + 31) >> 5;
-                if (G > 0 && (G & 31) && lane >= (G & 31)) row_keys[32 * (steps - 1) + lane] = 0u;  // (the row's own)
+                const uint32_t* mine = row_keys + lane * kLanePitch;  // the lane's 32
+                const int nb = have, used = (nb + 31) >> 5;
+                for (int i = max(G, 0) + lane; i < kChunk; i += 32) row_keys[i + 2 * (i >> 5)] = 0u;
                 __syncwarp();
                 // every key: the chunk's, then the best so far
                 auto each = [&](auto&& f) {
-#pragma unroll 8
-                    for (int i = 0; i < steps; ++i) f(row_keys[32 * i + lane]);
-#pragma unroll 2
+#pragma unroll 1
+                    for (int i = 0; i < 32; ++i) f(mine[i]);
+#pragma unroll 1
                     for (int i = 0; i < used; ++i) f(32 * i + lane < nb ? best[32 * i + lane] : 0u);
                 };
                 // The key lo above which fewer than beta keys lie, at or above which beta or more (or all there are).  A histogram
@@ -504,8 +511,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                 // rounded to a whole number in the last bits of 2^23 + it, which takes no conversion.  The bins of a lane's keys stay in
                 // registers, four to a word, for the second look.
                 uint32_t most = 0;
-#pragma unroll 8
-                for (int i = 0; i < steps; ++i) most = max(most, row_keys[32 * i + lane]);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(mine + i);
+                    most = max(most, max(v.x, v.y));
+                }
 #pragma unroll 1
                 for (int i = 0; i < used; ++i) most = max(most, 32 * i + lane < nb ? best[32 * i + lane] : 0u);
                 most = __reduce_max_sync(kFull, most);
@@ -519,14 +529,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                 clear();
 #pragma unroll
                 for (int w = 0; w < kChunk / 128; ++w) {
+                    const uint2 v0 = *reinterpret_cast<const uint2*>(mine + 4 * w), v1 = *reinterpret_cast<const uint2*>(mine + 4 * w + 2);
+                    const int x[4] = {bin_of(v0.x), bin_of(v0.y), bin_of(v1.x), bin_of(v1.y)};
                     bins[w] = 0;
-                    if (4 * w < steps) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int x = 4 * w + i < steps ? bin_of(row_keys[32 * (4 * w + i) + lane]) : 0;
-                            atomicAdd(hist + x, 1);
-                            bins[w] |= (uint32_t)x << (8 * i);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        atomicAdd(hist + x[i], 1);
+                        bins[w] |= (uint32_t)x[i] << (8 * i);
                     }
                 }
 #pragma unroll 1
@@ -541,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                             uint32_t hit = __vcmpeq4(bins[w], four) & 0x01010101u;
                             while (hit) {
                                 const int i = (__ffs(hit) - 1) >> 3;
-                                keep(row_keys[32 * (4 * w + i) + lane]);
+                                keep(mine[4 * w + i]);
                                 hit &= hit - 1;
                             }
                         }
@@ -597,31 +606,57 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                 // those taken, in the pages' order: the best so far (lower pages), then the chunk's
                 int n = 0, eq = 0;
                 const unsigned lt = (1u << lane) - 1u;
-                auto put = [&](uint32_t key, int pg) {
-                    bool in = key >= lo;
-                    if (ties != 1 << 30) {
-                        const unsigned be = __ballot_sync(kFull, key == lo);
-                        in = key > lo || (key == lo && eq + __popc(be & lt) < ties);
-                        eq += __popc(be);
-                    }
-                    const unsigned bi = __ballot_sync(kFull, in);
-                    if (in) {
-                        best[n + __popc(bi & lt)] = key;
-                        page[n + __popc(bi & lt)] = pg;
-                    }
-                    n += __popc(bi);
-                };
 #pragma unroll 1
                 for (int i = 0; i < used; ++i) {
                     const int at = 32 * i + lane;
                     const uint32_t key = at < nb ? best[at] : 0u;
                     const int pg = at < nb ? page[at] : 0;
                     __syncwarp();
-                    put(key, pg);
+                    const unsigned be = __ballot_sync(kFull, key == lo);
+                    const bool in = key > lo || (key == lo && eq + __popc(be & lt) < ties);
+                    eq += __popc(be);
+                    const unsigned bi = __ballot_sync(kFull, in);
+                    if (in) {
+                        best[n + __popc(bi & lt)] = key;
+                        page[n + __popc(bi & lt)] = pg;
+                    }
+                    n += __popc(bi);
                     __syncwarp();
                 }
-#pragma unroll 4
-                for (int i = 0; i < steps; ++i) put(row_keys[32 * i + lane], c0 + 32 * i + lane);
+                uint32_t in = 0;  // of the lane's 32
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(mine + i);
+                    in |= (v.x >= lo ? 1u << i : 0u) | (v.y >= lo ? 2u << i : 0u);
+                }
+                if (ties != 1 << 30) {  // only so many of those equal to lo
+                    uint32_t even = 0;
+                    for (uint32_t x = in; x; x &= x - 1) even |= mine[__ffs(x) - 1] == lo ? x & (0u - x) : 0u;
+                    int e = __popc(even);
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int x = __shfl_up_sync(kFull, e, d);
+                        if (lane >= d) e += x;
+                    }
+                    e += eq - __popc(even);  // before the lane's first
+                    for (; even; even &= even - 1)
+                        if (e++ >= ties) in &= ~(even & (0u - even));
+                }
+                int at = __popc(in), all;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int x = __shfl_up_sync(kFull, at, d);
+                    if (lane >= d) at += x;
+                }
+                all = __shfl_sync(kFull, at, 31);
+                at += n - __popc(in);
+                for (; in; in &= in - 1, ++at) {
+                    const int i = __ffs(in) - 1;
+                    best[at] = mine[i];
+                    page[at] = c0 + 32 * lane + i;
+                }
+                n += all;
+                __syncwarp();
                 have = n;
             }
             __syncthreads();
