@@ -384,20 +384,22 @@ constexpr float kSumLeast = 0x1p-64f, kSumMost = 0x1p126f;
 
 // One warp per (R rows of the step, KV head): a row is its page's last of the step when the next row's slot lies on
 // another page, and then the warp sums the page's keys.  A half-warp takes every other token (16 bytes, dims 8 l ..
-// 8 l + 7, a lane), 8 tokens of each in flight.
+// 8 l + 7, a lane), 8 tokens a time, the next 8 on their way meanwhile.
 // The sums are kept as fp32 pairs (two_sum2), exact to some 48 bits, because a code jumps by one at a border and has to
 // be the same however the sum is ordered; 127 S / max is compared with its border in 64 bits only where fp32 leaves it
 // open (one element in 5000).
 template <int R>
-__global__ void __launch_bounds__(kSumThreads) page_summaries_kernel(SumsArgs a) {
+__global__ void __launch_bounds__(kSumThreads, 3) page_summaries_kernel(SumsArgs a) {
     const int lane = threadIdx.x & 31, l = lane & 15, odd = lane >> 4;
     const long long unit = (long long)blockIdx.x * (kSumThreads / 32) + (threadIdx.x >> 5);
     const long long chunk = unit / a.Hkv;
     const int h = (int)(unit - chunk * a.Hkv);
-    const long long row = chunk * R + lane;
+    constexpr int kWords = (R + 31) / 32;  // 32 rows a look
+    for (int k = 0; k < kWords; ++k) {
+    const long long row = chunk * R + 32 * k + lane;
     long long slot = -1;
     bool last = false;
-    if (lane < R && row < a.rows) {
+    if (32 * k + lane < R && row < a.rows) {
         slot = a.slots[row];
         const long long after = row + 1 < a.rows ? a.slots[row + 1] : -1;
         if (slot >= (long long)a.n_pages << a.page_shift) {
@@ -415,17 +417,21 @@ __global__ void __launch_bounds__(kSumThreads) page_summaries_kernel(SumsArgs a)
         const size_t head = (size_t)page * a.Hkv + h;
         const uint4* src = reinterpret_cast<const uint4*>(a.pk + (head << a.page_shift) * kDim) + odd * 16 + l;
         uint64_t s[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};
+        uint4 v[4];
+        auto load = [&](int t0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = t0 + 2 * k + odd < n ? __ldcs(src + (size_t)(t0 + 2 * k) * 16) : make_uint4(0, 0, 0, 0);
+        };
+        load(0);
 #pragma unroll 1
-        for (int t0 = 0; t0 < n; t0 += 16) {
-            uint4 v[8];
+        for (int t0 = 0; t0 < n; t0 += 8) {
+            uint4 u[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int t = t0 + 2 * k + odd;
-                v[k] = t < n ? __ldcs(src + (size_t)(t0 + 2 * k) * 16) : make_uint4(0, 0, 0, 0);
-            }
+            for (int k = 0; k < 4; ++k) u[k] = v[k];
+            if (t0 + 8 < n) load(t0 + 8);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     two_sum2(s[i], e[i], (uint64_t)(w[i] << 16) | ((uint64_t)(w[i] & 0xFFFF0000u) << 32));
@@ -463,14 +469,19 @@ __global__ void __launch_bounds__(kSumThreads) page_summaries_kernel(SumsArgs a)
             code[k] = live ? __float2int_rn(y) : 0;
             open |= live && fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f;
         }
-        if (__any_sync(kFull, open)) {  // (y is off by less than 127 * 2^-22 here, and max by its own low part)
-            double m = 0.0;
+        if (__any_sync(kFull, open)) {  // (y is off by less than 127 * 2^-22 here)
+            float rest = -INFINITY;  // what the largest sum has beyond top
 #pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmax(m, fabs((double)hi[k] + lo[k]));
+            for (int k = 0; k < 8; ++k)
+                if (fabsf(hi[k]) == top) rest = fmaxf(rest, hi[k] < 0.f ? -lo[k] : lo[k]);
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) m = fmax(m, __shfl_xor_sync(kFull, m, d));
+            for (int d = 1; d < 16; d <<= 1) rest = fmaxf(rest, __shfl_xor_sync(kFull, rest, d));
+            const double m = (double)top + (double)rest;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) code[k] = __double2int_rn(127.0 * ((double)hi[k] + lo[k]) / m);
+            for (int k = 0; k < 8; ++k) {
+                const float y = __fmul_rn(hi[k], by);
+                if (fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f) code[k] = __double2int_rn(127.0 * ((double)hi[k] + lo[k]) / m);
+            }
         }
         if (odd == 0) {
             uint32_t w[2] = {0, 0};
@@ -479,6 +490,7 @@ __global__ void __launch_bounds__(kSumThreads) page_summaries_kernel(SumsArgs a)
             reinterpret_cast<uint2*>(a.codes + head * kDim)[l] = make_uint2(w[0], w[1]);
             if (l == 0) a.scale[head] = live ? __fdiv_rn(top, 127.f * (float)n) : bad ? INFINITY : 0.f;
         }
+    }
     }
 }
 
@@ -639,13 +651,13 @@ hsq_status hsq_page_summaries(hsq_ctx* ctx, const hsq_pages* pages, const hsq_su
     SumsArgs a{slots, static_cast<const uint16_t*>(pages->k), sums->codes, sums->scale, rows, Hkv, P, shift, pages->n_pages,
                ctx->d_err};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // a row a warp until the GPU's warps (64 a SM) are in use twice over, then 16: a page has at least as many rows of a prompt
+    // a row a warp until the GPU's warps (64 a SM) are in use twice over, then 64: a prompt's rows fill pages of up to 128
     const long long units = (long long)rows * Hkv;
     const bool few = units <= 128LL * ctx->num_sms;
-    const long long warps = few ? units : (long long)((rows + 15) / 16) * Hkv;
+    const long long warps = few ? units : (long long)((rows + 63) / 64) * Hkv;
     const unsigned ctas = (unsigned)((warps + kSumThreads / 32 - 1) / (kSumThreads / 32));
     if (few) page_summaries_kernel<1><<<ctas, kSumThreads, 0, s>>>(a);
-    else page_summaries_kernel<16><<<ctas, kSumThreads, 0, s>>>(a);
+    else page_summaries_kernel<64><<<ctas, kSumThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HSQ_OK : hsq::cuda_fail(ctx, e, "page_summaries");
 }
