@@ -44,6 +44,39 @@ struct TileHead {
     int units, shorts;
 };
 
+// The entries of a row's selection that count, by a whole warp: those below the row's number of pages c and above every entry before
+// them; others that are not -1 are flagged.
+template <class F>
+__device__ __forceinline__ void for_selected(const PageAttnArgs& a, const int32_t* sel, int c, int& bad, F&& take) {
+    const int lane = threadIdx.x & 31;
+    int before = -1, next = lane < a.top ? sel[lane] : -1;
+    for (int i0 = 0; i0 < a.top; i0 += 32) {
+        const int e = next;
+        next = i0 + 32 + lane < a.top ? sel[i0 + 32 + lane] : -1;
+        // the largest entry before this one: the one before it, where they ascend and no -1 stands between them
+        int ahead = __shfl_up_sync(kFull, e, 1);
+        if (lane == 0) ahead = before;
+        const unsigned there = __ballot_sync(kFull, e >= 0);
+        if ((there & (there + 1)) || __any_sync(kFull, e >= 0 && e <= ahead)) {
+            int top = e;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(kFull, top, d);
+                if (lane >= d) top = max(top, o);
+            }
+            ahead = __shfl_up_sync(kFull, top, 1);
+            ahead = max(lane ? ahead : -1, before);
+            before = max(before, __shfl_sync(kFull, top, 31));
+        } else if (there) {
+            before = __shfl_sync(kFull, e, 31 - __clz(there));
+        }
+        if (e >= 0) {
+            if (e >= c || e <= ahead) bad |= HSQ_DEVERR_SEL;
+            else take(e);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------------------
 // Rows one by one: a cluster of CTAs for each (row, KV head), four warps a CTA.  The row's pages are listed once a CTA; the
 // cluster's warps cut the line of their groups of 16 keys into equal runs.  A warp loads its groups three ahead (TMA, 128-byte
@@ -154,15 +187,11 @@ __global__ void __launch_bounds__(kThreadsRow)
     auto load = [&] {
         while (ask < s1 && tokens_of(ask) <= 0) ++ask;
         if (ask >= s1) return;
-        if (lane == 0) {
-            const uint32_t dst = stages + in.stage * kStageBytes, bar = bars + 8 * in.stage;
-            const int y = ((list[ask >> sub_shift].x * a.Hkv + h) << a.page_shift) + 16 * (ask & ((1 << sub_shift) - 1));
-            mbar_expect_tx(bar, kStageBytes);
-            tma_2d(dst, &mk, 0, y, bar);
-            tma_2d(dst + 2048, &mk, 64, y, bar);
-            tma_2d(dst + 4096, &mv, 0, y, bar);
-            tma_2d(dst + 6144, &mv, 64, y, bar);
-        }
+        const uint32_t dst = stages + in.stage * kStageBytes, bar = bars + 8 * in.stage;
+        const int y = ((list[ask >> sub_shift].x * a.Hkv + h) << a.page_shift) + 16 * (ask & ((1 << sub_shift) - 1));
+        if (lane == 0) mbar_expect_tx(bar, kStageBytes);
+        __syncwarp();
+        if (lane < 2) tma_3d(dst + 4096 * lane, lane ? &mv : &mk, 0, y, 0, bar);
         __syncwarp();
         in.advance();
         ++ask;
@@ -314,6 +343,379 @@ __global__ void __launch_bounds__(kThreadsRow)
 }
 
 // ---------------------------------------------------------------------------------------
+// Requests of few rows at once (proposals): a cluster of CTAs for each (request, KV head), over the union of its rows' pages, so that
+// a page that several rows take is read once.  The columns of the products are the rows (token x head); a CTA has four streams of
+// keys, and H warps a stream with 16 columns each that share its stages.  The CTAs list the union in shared memory (a word of
+// token bits for each page, in the memory that the stages use afterwards); the rest is as for single rows.
+// ---------------------------------------------------------------------------------------
+
+constexpr int kGroupStages = 3, kGroupList = 400;  // pages of a union at most, a CTA of the cluster
+constexpr uint32_t kGroupWarpBytes = kGroupStages * kStageBytes, kGroupQPitch = 272;  // (272: a fragment's words lie in 32 banks)
+constexpr uint32_t kGOffList = kWarps * kGroupWarpBytes;               // [kGroupList] int4: page id, logical page, tokens
+constexpr uint32_t kGOffWeight = kGOffList;                            // (once the list has served) [warp][32] weights in the CTA's
+constexpr uint32_t kGOffCta = kGOffWeight + kWarps * 32 * 4;           // [32] the CTA's m, l
+constexpr uint32_t kGOffAll = kGOffCta + 32 * 8;                       // [CTA][32] the cluster's
+constexpr uint32_t kGOffMl = kGOffList + kGroupList * 16;              // [warp][32] m, l
+constexpr uint32_t kGOffBar = kGOffMl + kWarps * 32 * 8;
+static_assert(kGOffAll + 8 * 32 * 8 <= kGOffMl, "");
+constexpr uint32_t kGOffScan = kGOffBar + kWarps * kGroupStages * 16;  // [warps]
+constexpr uint32_t kGOffQ = kGOffScan + 32;                            // [16 H] rows' queries
+constexpr uint32_t group_smem(int H) { return kGOffQ + 16 * H * kGroupQPitch + 1024; }  // + alignment
+static_assert(32 * 512 <= kGroupWarpBytes, "a stream's part fits its stages");
+static_assert(kGOffQ % 16 == 0 && group_smem(2) <= 113 * 1024, "two CTAs an SM");
+
+template <int H>
+__global__ void __launch_bounds__(kThreadsRow * H, 2)
+    page_attn_group_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                           const __grid_constant__ PageAttnArgs a) {
+    constexpr int kThreads = kThreadsRow * H, kAllWarps = kWarps * H, NT = 2;
+    extern __shared__ uint8_t raw_smem[];
+    const uint32_t raw = smem_addr(raw_smem), base = (raw + 1023u) & ~1023u;
+    uint8_t* sm = raw_smem + (base - raw);
+    int4* list = reinterpret_cast<int4*>(sm + kGOffList);
+    float2* warp_ml = reinterpret_cast<float2*>(sm + kGOffMl);
+    float2* cta_ml = reinterpret_cast<float2*>(sm + kGOffCta);
+    int* scan = reinterpret_cast<int*>(sm + kGOffScan);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int stream = warp / H, half = warp % H, col0 = 16 * half;  // the warp's keys, its columns' first
+    cg::cluster_group cluster = cg::this_cluster();
+    const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int unit = blockIdx.x / S, h = unit % a.Hkv, b = unit / a.Hkv;
+    int bad = 0;
+    bool failed = false;
+
+    const int first = a.q_start[b], end = a.q_start[b + 1], l_given = a.lens[b];
+    int n = end - first;
+    if (first < 0 || end < first || end > a.rows || n > a.max_new) {
+        bad |= HSQ_DEVERR_LEN;
+        n = 0;
+    }
+    const int held = min(max(l_given, 0), a.width << a.page_shift);
+    if (held != l_given || l_given < n) bad |= HSQ_DEVERR_LEN;
+    if (n > a.few) n = 0;  // (by tiles)
+    const int ahead = max(l_given, 0) - n;
+    auto seen_of = [&](int tok) { return min(max(ahead + tok + 1, 0), held); };
+    auto pages_of = [&](int tok) { return a.prefix_pages + ((seen_of(tok) + a.page_n - 1) >> a.page_shift); };
+    const int last_seen = n > 0 ? seen_of(n - 1) : 0, columns = n * a.r;
+
+    if (tid == 0) {
+        for (int i = 0; i < kWarps * kGroupStages; ++i) {
+            mbar_init(base + kGOffBar + 8 * i, 1);
+            mbar_init(base + kGOffBar + 8 * (kWarps * kGroupStages + i), H);
+        }
+        mbar_init_fence();
+    }
+    for (int i = tid; i < 16 * H * 16; i += kThreads) {  // 16 bytes each
+        const int col = i >> 4, tok = col / a.r, head = col - tok * a.r;
+        uint8_t* to = sm + kGOffQ + col * kGroupQPitch + 16 * (i & 15);
+        if (col < columns) cp_async16(to, a.q + ((size_t)(first + tok) * a.Hq + h * a.r + head) * 128 + 8 * (i & 15));
+        else *reinterpret_cast<uint4*>(to) = make_uint4(0, 0, 0, 0);
+    }
+    cp_async_commit();
+
+    // ---- the union of the rows' pages ----
+    // (the words of up to 24576 pages lie in the stages' memory; of more, which only pages of 16 or 32 tokens can be, in two
+    // goes, the first only counted where a second follows)
+    const int sub_shift = a.page_shift - 4;
+    int listed = 0, page0 = 0, here = 0;  // pages of the union; the CTA's first and number of them
+    {
+        uint32_t* word = reinterpret_cast<uint32_t*>(sm);
+        constexpr int kWindow = kWarps * kGroupWarpBytes / 4;
+        const int most = n > 0 ? pages_of(n - 1) : 0, windows = (most + kWindow - 1) / kWindow;
+        int total = 0;
+        for (int go = 0; go < (windows > 1 ? 2 : 1); ++go) {
+            const bool write = windows <= 1 || go == 1;
+            int at0 = 0;
+            for (int w0 = 0; w0 < most; w0 += kWindow) {
+                const int w1 = min(most, w0 + kWindow);
+                for (int i = tid; i < w1 - w0; i += kThreads) word[i] = 0;
+                __syncthreads();
+                for (int tok = warp; tok < n; tok += kAllWarps)
+                    for_selected(a, a.sel + ((size_t)(first + tok) * a.Hkv + h) * a.top, pages_of(tok), bad, [&](int e) {
+                        if (e >= w0 && e < w1) atomicOr(word + e - w0, 1u << tok);
+                    });
+                __syncthreads();
+                // a thread's share of the pages (an odd number, for the banks): counted, then written
+                const int share = ((w1 - w0 + kThreads - 1) / kThreads) | 1, i0 = min(tid * share, w1 - w0), i1 = min(i0 + share, w1 - w0);
+                int mine = 0;
+                for (int i = i0; i < i1; ++i) mine += word[i] != 0;
+                int at = mine;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int x = __shfl_up_sync(kFull, at, d);
+                    if (lane >= d) at += x;
+                }
+                if (lane == 31) scan[warp] = at;
+                __syncthreads();
+                at += at0 - mine;
+#pragma unroll
+                for (int w = 0; w < kAllWarps; ++w) {
+                    if (w < warp) at += scan[w];
+                    at0 += scan[w];
+                }
+                if (write) {
+                    if (windows <= 1) total = at0;
+                    // the pages of the groups [total rank / S, total (rank + 1) / S)
+                    page0 = (int)((long long)total * rank / S);
+                    here = (int)((long long)total * (rank + 1) / S) - page0;
+                    for (int i = i0; i < i1; ++i)
+                        if (word[i] != 0) {
+                            if (at >= page0 && at - page0 < min(here, kGroupList)) list[at - page0] = make_int4(0, w0 + i, (int)word[i], 0);
+                            ++at;
+                        }
+                }
+                __syncthreads();
+            }
+            if (!write) total = at0;
+        }
+        listed = total;
+        here = min(here, kGroupList);
+        for (int i = tid; i < here; i += kThreads) {
+            const int e = list[i].y;
+            const int id = e < a.prefix_pages ? a.prefix[e] : a.table[(size_t)b * a.width + e - a.prefix_pages];
+            const bool in = id >= 0 && id < a.n_pages;
+            if (!in) bad |= HSQ_DEVERR_PAGE;
+            list[i].x = in ? id : 0;
+            if (!in) list[i].z = 0;
+        }
+        cp_async_wait_all();
+        fence_async_smem();  // (the words' memory takes copies from here on)
+        __syncthreads();
+    }
+    if (blockIdx.x == 0) bad |= offsets_bad(a.q_start, a.B, a.rows, kThreads);
+
+    // the warp's groups [s0, s1) of 16 keys, of the CTA's
+    const int groups = here << sub_shift, s0 = groups * stream / kWarps, s1 = groups * (stream + 1) / kWarps;
+    const uint32_t stages = base + stream * kGroupWarpBytes, bars = base + kGOffBar + 8 * kGroupStages * stream;
+    const uint32_t read = bars + 8 * kWarps * kGroupStages;  // every warp of the stream has read the stage
+    uint8_t* stages_g = sm + stream * kGroupWarpBytes;
+    Ring<kGroupStages> in{0, 0}, out{0, 0};
+    // place of the group's first key among the prefix's tokens or the request's own
+    auto begin_of = [&](int s, int lp) {
+        return ((lp < a.prefix_pages ? lp : lp - a.prefix_pages) << a.page_shift) + 16 * (s & ((1 << sub_shift) - 1));
+    };
+    auto valid_of = [&](int s) {  // tokens of the group and behind that any row sees; 0: nothing to do
+        const int4 e = list[s >> sub_shift];
+        return e.z == 0 ? 0 : (e.y < a.prefix_pages ? a.prefix_len : last_seen) - begin_of(s, e.y);
+    };
+    int ask = s0, asked = 0;
+    auto load = [&] {  // (by the stream's first warp)
+        if (half != 0) return;
+        while (ask < s1 && valid_of(ask) <= 0) ++ask;
+        if (ask >= s1) return;
+        if (H > 1 && ++asked > kGroupStages) {
+            mbar_wait_fast(read + 8 * in.stage, in.phase ^ 1, failed, a.polls);
+            failed = __any_sync(kFull, failed);
+            if (failed) return;
+        }
+        const uint32_t dst = stages + in.stage * kStageBytes, bar = bars + 8 * in.stage;
+        const int y = ((list[ask >> sub_shift].x * a.Hkv + h) << a.page_shift) + 16 * (ask & ((1 << sub_shift) - 1));
+        if (lane == 0) mbar_expect_tx(bar, kStageBytes);
+        __syncwarp();
+        if (lane < 2) tma_3d(dst + 4096 * lane, lane ? &mv : &mk, 0, y, 0, bar);
+        __syncwarp();
+        in.advance();
+        ++ask;
+    };
+    for (int i = 0; i < kGroupStages; ++i) load();
+    failed |= (a.fault & HSQ_FAULT_WAIT_FEW) != 0;
+    float o[NT][8][4], m[NT][2], l[NT][2];
+    int seen[NT][2];        // of the lane's columns col0 + 8 nt + 2 t + e
+    uint32_t bit[NT][2];    // their tokens' bits (0: no row)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int col = col0 + 8 * nt + 2 * t + e, tok = col / a.r;
+            seen[nt][e] = seen_of(tok);
+            bit[nt][e] = col < columns ? 1u << tok : 0u;
+            m[nt][e] = -INFINITY;
+            l[nt][e] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+    }
+    const uint32_t k_row = (lane & 15) * 128, k_x = lane & 7, k_c = lane >> 4;
+    const uint32_t v_row = ((lane & 7) + 8 * (lane >> 4)) * 128, v_c = (lane >> 3) & 1;
+    // queries: rows (lane & 7), 16 bytes lane >> 3 of the two k steps' 64
+    const uint32_t q_lane = base + kGOffQ + (col0 + (lane & 7)) * kGroupQPitch + 16 * (lane >> 3);
+#pragma unroll 1
+    for (int s = s0; s < s1 && !failed; ++s) {
+        const int valid = valid_of(s);
+        if (valid <= 0) continue;
+        const int4 page = list[s >> sub_shift];
+        const uint32_t kb = stages + out.stage * kStageBytes, vb = kb + 4096;
+        mbar_wait_fast(bars + 8 * out.stage, out.phase, failed, a.polls);
+        failed = __any_sync(kFull, failed);
+        if (failed) break;
+        if (valid < 16) {  // the rest of the page is stale: weight 0, but it has to be finite
+            for (int i = lane; i < (16 - valid) * 16; i += 32)
+                *reinterpret_cast<uint4*>(stages_g + out.stage * kStageBytes + 4096 + ((i >> 3) & 1) * 2048 + (valid + (i >> 4)) * 128 +
+                                          (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            __syncwarp();
+        }
+        float x[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+        // (tiles whose tokens do not take the page are multiplied too: a branch would keep the products of the others apart)
+#pragma unroll
+        for (int kk = 0; kk < 8; kk += 2) {
+            uint32_t k0[4], k1[4];
+            ldmatrix(k0, kb + (kk >> 2) * 2048 + k_row + ((((2 * kk + k_c) & 7) ^ k_x) << 4));
+            ldmatrix(k1, kb + (kk >> 2) * 2048 + k_row + ((((2 * kk + 2 + k_c) & 7) ^ k_x) << 4));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t q[4];
+                ldmatrix(q, q_lane + nt * 8 * kGroupQPitch + 32 * kk);
+                mma_16816(x[nt], k0, q[0], q[1]);
+                mma_16816(x[nt], k1, q[2], q[3]);
+            }
+        }
+        const int begin = begin_of(s, page.y);
+        const bool pre = page.y < a.prefix_pages;
+        bool look = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // key g + 8 (e >> 1), column 8 nt + 2 t + (e & 1)
+                const int keys = (page.z & bit[nt][e & 1]) ? (pre ? a.prefix_len : seen[nt][e & 1]) - begin : 0;
+                if (g + 8 * (e >> 1) >= keys) x[nt][e] = -INFINITY;
+                look |= x[nt][e] * kLogitScaleLog2 > m[nt][e & 1] * kLogitScaleLog2 + 8.f;  // (the first key raises from -inf)
+            }
+        if (__any_sync(kFull, look)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(m[nt][e], fmaxf(x[nt][e], x[nt][e + 2]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, d));
+                    const float alpha = mx == -INFINITY ? 1.f : ex2_approx((m[nt][e] - mx) * kLogitScaleLog2);
+                    m[nt][e] = mx;
+                    l[nt][e] *= alpha;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[nt][i][e] *= alpha;
+                        o[nt][i][e + 2] *= alpha;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float off = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1] * kLogitScaleLog2;
+                pr[e] = ex2_approx(fmaf(x[nt][e], kLogitScaleLog2, -off));
+                l[nt][e & 1] += pr[e];
+            }
+            pf[nt][0] = transpose_8x8(pack_bf16(pr[0], pr[1]));
+            pf[nt][1] = transpose_8x8(pack_bf16(pr[2], pr[3]));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t v[4];
+            ldmatrix_trans(v, vb + (i >> 2) * 2048 + v_row + ((((2 * i + v_c) & 7) ^ k_x) << 4));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][i], v, pf[nt][0], pf[nt][1]);
+        }
+        __syncwarp();  // (every lane has read the stage)
+        if (H > 1 && lane == 0) mbar_arrive(read + 8 * out.stage);
+        out.advance();
+        load();
+    }
+    if (failed) {  // see the copies in flight (one a stage at most) land: their memory is used again
+        if (half == 0)
+        for (int i = 0; i < kGroupStages; ++i) mbar_wait(bars + 8 * i, i < (int)in.stage ? in.phase : in.phase ^ 1, 1 << 12);
+        bad |= HSQ_DEVERR_WAIT;
+    }
+    // the warp's part (its stream's stages are free once every warp of it is through)
+    if (H > 1) __syncthreads();
+    float* part = reinterpret_cast<float*>(stages_g);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], d);
+            const int j = col0 + 8 * nt + 2 * t + e;
+            if (g == 0) warp_ml[32 * stream + j] = failed ? make_float2(-INFINITY, 0.f) : make_float2(m[nt][e], l[nt][e]);
+            if (!failed && j < columns) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    part[j * 128 + 16 * i + g] = o[nt][i][e];
+                    part[j * 128 + 16 * i + 8 + g] = o[nt][i][e + 2];
+                }
+            }
+        }
+    __syncthreads();
+    float* weight = reinterpret_cast<float*>(sm + kGOffWeight);
+    {
+        float M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, warp_ml[32 * i + lane].x);
+        float L = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            const float2 ml = warp_ml[32 * i + lane];
+            const float c = ml.y == 0.f ? 0.f : ex2_approx((ml.x - M) * kLogitScaleLog2);
+            L = fmaf(ml.y, c, L);
+            if (i == warp) weight[32 * i + lane] = c;
+        }
+        if (warp == 0) cta_ml[lane] = make_float2(M, L);
+    }
+    __syncthreads();
+    float* cta_o = reinterpret_cast<float*>(sm);  // the CTA's, in the first stream's place: a thread a dim
+#pragma unroll 4
+    for (int j = tid >> 7; j < columns; j += H) {
+        const int d = tid & 127;
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i)
+            y = fmaf(reinterpret_cast<const float*>(sm + i * kGroupWarpBytes)[j * 128 + d], weight[32 * i + j], y);
+        cta_o[j * 128 + d] = y;
+    }
+    cluster.sync();
+    float2* all_ml = reinterpret_cast<float2*>(sm + kGOffAll);
+    for (int i = tid; i < 32 * S; i += kThreads) all_ml[i] = cluster.map_shared_rank(cta_ml, i >> 5)[i & 31];
+    __syncthreads();
+#pragma unroll 1
+    for (int e = rank * kThreads + tid; e < columns * 32; e += S * kThreads) {
+        const int j = e >> 5, d = 4 * (e & 31);
+        float4 y[8];
+        float M = -INFINITY, L = 0.f, z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < S) {
+                y[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(cta_o, i) + j * 128 + d);
+                M = fmaxf(M, all_ml[32 * i + j].x);
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < S) {
+                const float2 ml = all_ml[32 * i + j];
+                const float c = ml.y == 0.f ? 0.f : ex2_approx((ml.x - M) * kLogitScaleLog2);
+                L = fmaf(ml.y, c, L);
+                z[0] = fmaf(y[i].x, c, z[0]);
+                z[1] = fmaf(y[i].y, c, z[1]);
+                z[2] = fmaf(y[i].z, c, z[2]);
+                z[3] = fmaf(y[i].w, c, z[3]);
+            }
+        const float inv = L == 0.f ? 0.f : 1.0f / L;  // (a sum that is not a number shows in the result)
+        const int tok = j / a.r;
+        const size_t to = (size_t)(first + tok) * a.Hq + h * a.r + j - tok * a.r;
+        *reinterpret_cast<uint2*>(a.out + to * 128 + d) = make_uint2(pack_bf16(z[0] * inv, z[1] * inv), pack_bf16(z[2] * inv, z[3] * inv));
+        if (a.lse && d == 0) a.lse[to] = L == 0.f ? -INFINITY : M * kRsqrtD + logf(L);
+    }
+    cluster.sync();  // (no CTA ends while another reads its part)
+    if (bad) atomicOr(a.err, bad);
+}
+
+// ---------------------------------------------------------------------------------------
 // Rows by tiles, for requests of many tokens (a prompt's chunk).  A tile is 128 rows: 128 / r neighbouring tokens times the r
 // heads of a KV head.  Its tokens select different pages, but neighbours many of the same: the tile's products run over the
 // UNION of their pages on the tensor cores, and the softmax hides the pages that a row did not take.
@@ -438,33 +840,10 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
         __syncthreads();
         for (int t = warp; t < toks; t += kListThreads / 32) {
             const int32_t* sel = a.sel + ((size_t)(p.first + t) * a.Hkv + h) * a.top;
-            const int c = pages_of(t), tile = t >= p.toks[0], i = tile ? t - p.toks[0] : t;
-            int before = -1, next = lane < a.top ? sel[lane] : -1;
-            for (int i0 = 0; i0 < a.top; i0 += 32) {
-                const int e = next;
-                next = i0 + 32 + lane < a.top ? sel[i0 + 32 + lane] : -1;
-                // the largest entry before this one: the one before it, where they ascend and no -1 stands between them
-                int ahead = __shfl_up_sync(kFull, e, 1);
-                if (lane == 0) ahead = before;
-                const unsigned there = __ballot_sync(kFull, e >= 0);
-                if ((there & (there + 1)) || __any_sync(kFull, e >= 0 && e <= ahead)) {
-                    int top = e;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int o = __shfl_up_sync(kFull, top, d);
-                        if (lane >= d) top = max(top, o);
-                    }
-                    ahead = __shfl_up_sync(kFull, top, 1);
-                    ahead = max(lane ? ahead : -1, before);
-                    before = max(before, __shfl_sync(kFull, top, 31));
-                } else if (there) {
-                    before = __shfl_sync(kFull, e, 31 - __clz(there));
-                }
-                if (e >= 0) {
-                    if (e >= c || e <= ahead) bad |= HSQ_DEVERR_SEL;
-                    else if (e >= w0 && e < w1) atomicOr(&s_mask[(e - w0) * W2 + tile * W + (i >> 5)], 1u << (i & 31));
-                }
-            }
+            const int tile = t >= p.toks[0], i = tile ? t - p.toks[0] : t;
+            for_selected(a, sel, pages_of(t), bad, [&](int e) {
+                if (e >= w0 && e < w1) atomicOr(&s_mask[(e - w0) * W2 + tile * W + (i >> 5)], 1u << (i & 31));
+            });
         }
         __syncthreads();
         for (int i0 = w0; i0 < w1; i0 += kListThreads) {
@@ -1354,6 +1733,21 @@ __global__ void __launch_bounds__(256) page_join_kernel(const __grid_constant__ 
     }
 }
 
+// CTAs of a cluster for units of some `keys` keys each where `slots` CTAs run at once: what a CTA costs, its share of the keys and
+// what it costs beside them (in keys), times the CTAs a slot has (one at least).
+int cluster_of(long long units, long long slots, long long keys, long long beside) {
+    int best = 1;
+    long long least = -1;
+    for (int S = 1; S <= 8; ++S) {
+        const long long cost = std::max(units * S, slots) * (beside + 16 * S + (keys + S - 1) / S);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = S;
+        }
+    }
+    return best;
+}
+
 // The workspace's pieces and their offsets.
 struct Layout {
     size_t head, req, unit, short_row, count, ent, mask, part_o, part_ml, pair_ml, cut, bytes;
@@ -1462,11 +1856,26 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
     CUtensorMap mq, mk, mv, mk16, mv16;
     if (!encode_fn()) return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const uint64_t n = (uint64_t)pages->n_pages * Hkv * P;
-    if (!encode_rows(&mk16, pages->k, n, 16) || !encode_rows(&mv16, pages->v, n, 16))
+    if (!encode_halves(&mk16, pages->k, n, 16) || !encode_halves(&mv16, pages->v, n, 16))
         return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     const bool tiles = max_new > x.few;
+    // requests of a few rows together, where the union of their pages has room
+    const int most = std::min(max_new, x.few);
+    const long long unit_pages = std::min<long long>(np + width, (long long)most * top);
+    const bool group = most > 1 && unit_pages <= 8 * (kGroupList - 1);
+    if (group) {
+        const long long units = (long long)B * Hkv;
+        int S = cluster_of(units, 2LL * ctx->num_sms, std::max<long long>(top, unit_pages / 2) * P, 512);
+        while (unit_pages > S * (kGroupList - 1LL)) ++S;
+        const int H = most * a.r <= 16 ? 1 : 2;
+        const void* fn = H == 1 ? (const void*)page_attn_group_kernel<1> : (const void*)page_attn_group_kernel<2>;
+        void* args[] = {&mk16, &mv16, &a};
+        if ((e = hsq::raise_smem_limit(fn, ctx->device, group_smem(H))) == cudaSuccess)
+            e = launch_cluster(fn, (unsigned)(units * S), kThreadsRow * H, S, group_smem(H), s, false, args);
+        if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "page_attn groups");
+    }
     if (tiles) {
         if (!encode_q(&mq, q, rows, Hq, a.r, x.tpt) || !encode_rows(&mk, pages->k, n, P) || !encode_rows(&mv, pages->v, n, P))
             return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
@@ -1481,9 +1890,9 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
             (e = launch((const void*)page_join_kernel, x.runs * 8, 256, 0, s, true, args)) != cudaSuccess)
             return hsq::cuda_fail(ctx, e, "page_attn tiles");
     }
+    if (max_new > 1 && group) return HSQ_OK;
     const long long units = (tiles ? (long long)x.rows : rows) * Hkv;
-    int S = 1;
-    while (S < 8 && units * S < 4LL * ctx->num_sms && (long long)top * P >= 128LL * S) S *= 2;
+    const int S = cluster_of(units, 2LL * ctx->num_sms, (long long)top * P, 256);
     const void* fn = (const void*)page_attn_rows_kernel;
     e = hsq::raise_smem_limit(fn, ctx->device, kRowSmem);
     if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(page_attn)");
