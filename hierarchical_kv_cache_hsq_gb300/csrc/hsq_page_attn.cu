@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
     page_attn_group_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                            const __grid_constant__ PageAttnArgs a) {
     constexpr int kThreads = kThreadsRow * H, kAllWarps = kWarps * H, NT = 2;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the plan reads nothing of what is written here)
     extern __shared__ uint8_t raw_smem[];
     const uint32_t raw = smem_addr(raw_smem), base = (raw + 1023u) & ~1023u;
     uint8_t* sm = raw_smem + (base - raw);
@@ -734,7 +735,7 @@ constexpr int kTileRows = 128, kTileKeys = 128;
 constexpr float kTileSum = 65536.f;  // sum of a tile's 128 weights from which the maximum is taken anew
 // Requests of up to this many rows (tokens x heads) go row by row.
 constexpr int kFewColumns = 32;
-constexpr int kRunLeast = 16;        // cost of a run at least
+constexpr int kRunLeast = 6;         // cost of a run at least
 
 constexpr int kPlanThreads = 512;
 
@@ -815,11 +816,11 @@ __device__ __forceinline__ Pair pair_of(const PageAttnArgs& a, int unit) {
     return p;
 }
 
-constexpr int kListThreads = 256, kListBytes = 32768;
+constexpr int kListThreads = 1024, kListWarps = kListThreads / 32, kListBytes = 32768;
 
 __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_constant__ PageAttnArgs a) {
     __shared__ uint32_t s_mask[kListBytes / 4];  // [page of the window][2][words]
-    __shared__ int s_n[3][kListThreads / 32];
+    __shared__ int s_n[3][kListWarps], s_all[3];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
         const int w1 = min(most, w0 + window);
         for (int i = tid; i < (w1 - w0) * W2; i += kListThreads) s_mask[i] = 0;
         __syncthreads();
-        for (int t = warp; t < toks; t += kListThreads / 32) {
+        for (int t = warp; t < toks; t += kListWarps) {
             const int32_t* sel = a.sel + ((size_t)(p.first + t) * a.Hkv + h) * a.top;
             const int tile = t >= p.toks[0], i = tile ? t - p.toks[0] : t;
             for_selected(a, sel, pages_of(t), bad, [&](int e) {
@@ -873,14 +874,21 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
                 if (kind == k) at = __popc(bl & ((1u << lane) - 1u));
             }
             __syncthreads();
+            if (warp < 3) {  // before each warp, and in all
+                const int own = s_n[warp][lane];
+                int x = own;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                for (int w = 0; w < kListThreads / 32; ++w) {
-                    if (kind == k && w < warp) at += s_n[k][w];
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(kFull, x, d);
+                    if (lane >= d) x += y;
                 }
-                if (kind == k) at += n[k];
-                for (int w = 0; w < kListThreads / 32; ++w) n[k] += s_n[k][w];
+                s_n[warp][lane] = x - own;
+                if (lane == 31) s_all[warp] = x;
             }
+            __syncthreads();
+            if (kind < 3) at += s_n[kind][warp] + (kind == 0 ? n[0] : kind == 1 ? n[1] : n[2]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) n[k] += s_all[k];
             if (kind < 3) {
                 const size_t to = ((size_t)item * 3 + kind) * a.cap + at;
                 a.ent[to] = make_int2(id, e);
@@ -1883,8 +1891,9 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
         void* tc_args[] = {&mq, &mk, &mv, &a};
         if ((e = hsq::raise_smem_limit((const void*)page_tiles_kernel, ctx->device, kTcSmem)) != cudaSuccess)
             return hsq::cuda_fail(ctx, e, "cudaFuncSetAttribute(page_tiles)");
-        // (each behind the first begins while the one before ends, and waits for it before it reads)
-        if ((e = launch((const void*)page_plan_kernel, 1, kPlanThreads, 0, s, false, args)) != cudaSuccess ||
+        // (each begins while the one before ends, and waits for it before it reads; the plan needs nothing of the groups' kernel, which
+        // everything before the call precedes)
+        if ((e = launch((const void*)page_plan_kernel, 1, kPlanThreads, 0, s, group, args)) != cudaSuccess ||
             (e = launch((const void*)page_list_kernel, x.units * Hkv, kListThreads, 0, s, true, args)) != cudaSuccess ||
             (e = launch((const void*)page_tiles_kernel, x.runs, kTcThreads, kTcSmem, s, true, tc_args)) != cudaSuccess ||
             (e = launch((const void*)page_join_kernel, x.runs * 8, 256, 0, s, true, args)) != cudaSuccess)
