@@ -47,9 +47,9 @@ struct TileHead {
 // The entries of a row's selection that count, by a whole warp: those below the row's number of pages c and above every entry before
 // them; others that are not -1 are flagged.
 template <class F>
-__device__ __forceinline__ void for_selected(const PageAttnArgs& a, const int32_t* sel, int c, int& bad, F&& take) {
+__device__ __forceinline__ void for_selected(const PageAttnArgs& a, const int32_t* sel, int begin, int c, int& bad, F&& take) {
     const int lane = threadIdx.x & 31;
-    int before = -1, next = lane < a.top ? sel[lane] : -1;
+    int before = -1, next = begin;  // (the lane's of the first 32, read ahead by the caller)
     for (int i0 = 0; i0 < a.top; i0 += 32) {
         const int e = next;
         next = i0 + 32 + lane < a.top ? sel[i0 + 32 + lane] : -1;
@@ -431,10 +431,16 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
                 const int w1 = min(most, w0 + kWindow);
                 for (int i = tid; i < w1 - w0; i += kThreads) word[i] = 0;
                 __syncthreads();
-                for (int tok = warp; tok < n; tok += kAllWarps)
-                    for_selected(a, a.sel + ((size_t)(first + tok) * a.Hkv + h) * a.top, pages_of(tok), bad, [&](int e) {
+                const int32_t* sel = a.sel + ((size_t)(first + warp) * a.Hkv + h) * a.top;
+                const size_t step = (size_t)kAllWarps * a.Hkv * a.top;
+                int ahead = warp < n && lane < a.top ? sel[lane] : -1;
+                for (int tok = warp; tok < n; tok += kAllWarps, sel += step) {
+                    const int begin = ahead;
+                    ahead = tok + kAllWarps < n && lane < a.top ? sel[step + lane] : -1;
+                    for_selected(a, sel, begin, pages_of(tok), bad, [&](int e) {
                         if (e >= w0 && e < w1) atomicOr(word + e - w0, 1u << tok);
                     });
+                }
                 __syncthreads();
                 // a thread's share of the pages (an odd number, for the banks): counted, then written
                 const int share = ((w1 - w0 + kThreads - 1) / kThreads) | 1, i0 = min(tid * share, w1 - w0), i1 = min(i0 + share, w1 - w0);
@@ -839,10 +845,13 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
         const int w1 = min(most, w0 + window);
         for (int i = tid; i < (w1 - w0) * W2; i += kListThreads) s_mask[i] = 0;
         __syncthreads();
-        for (int t = warp; t < toks; t += kListWarps) {
-            const int32_t* sel = a.sel + ((size_t)(p.first + t) * a.Hkv + h) * a.top;
-            const int tile = t >= p.toks[0], i = tile ? t - p.toks[0] : t;
-            for_selected(a, sel, pages_of(t), bad, [&](int e) {
+        const int32_t* sel = a.sel + ((size_t)(p.first + warp) * a.Hkv + h) * a.top;
+        const size_t step = (size_t)kListWarps * a.Hkv * a.top;
+        int ahead = warp < toks && lane < a.top ? sel[lane] : -1;
+        for (int t = warp; t < toks; t += kListWarps, sel += step) {
+            const int tile = t >= p.toks[0], i = tile ? t - p.toks[0] : t, begin = ahead;
+            ahead = t + kListWarps < toks && lane < a.top ? sel[step + lane] : -1;
+            for_selected(a, sel, begin, pages_of(t), bad, [&](int e) {
                 if (e >= w0 && e < w1) atomicOr(&s_mask[(e - w0) * W2 + tile * W + (i >> 5)], 1u << (i & 31));
             });
         }
@@ -982,7 +991,7 @@ __device__ __forceinline__ int stream_tiles(const TileSegment& s, int st, int n)
     return both + (st ? m / 2 : (m + 1) / 2) + (x > m && (s.tiles[1] > s.tiles[2] ? 0 : 1) == st ? x - m : 0);
 }
 
-// What the join has to know of an item that run c is the second to work on.
+// What the join has to know of an item that a run is not the first to work on.
 struct CutRecord {
     int live, h, first, toks0, toks1, split, c0, c1;
     int pad[4];
@@ -1152,9 +1161,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 s.slot = 2 * c + (s.n0 == 0);
                 if (!s.whole && s.n0 > 0) {
                     const int c0 = (int)(((begin + 1) * runs - 1) / total);
-                    if (c0 == c - 1)
-                        cut = CutRecord{1, h, s.first, s.toks0, s.toks1, s.split, c0,
-                                        (int)(((begin + begin_of(s, tiles - 1) + 1) * runs - 1) / total), {}};
+                    cut = CutRecord{1, h, s.first, s.toks0, s.toks1, s.split, c0,
+                                    (int)(((begin + begin_of(s, tiles - 1) + 1) * runs - 1) / total), {}};
                 }
                 send();
                 if (tiles == 0) {  // (nobody may wait for a product that is due behind an item without a tile)
@@ -1698,9 +1706,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-// Join.  A CTA takes the item that a run is the second to work on, one tile, 32 rows (lane = row; a warp has 16 dims).
+// Join.  The runs of a cut item behind its first deal its dims among them, in eighths; a CTA takes a run's share of one tile's 32 rows
+// (lane = row).  A warp has 16 dims; where the share has fewer eighths than the CTA warps, they deal the parts among them too (one
+// warp after the other, eight items in 19 parts each took 32 us).
 __global__ void __launch_bounds__(256) page_join_kernel(const __grid_constant__ PageAttnArgs a) {
-    __shared__ float s_o[32][129];
+    __shared__ float s_o[8][32][17];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, run = blockIdx.x >> 3, st = blockIdx.x & 1;
     const int quarter = (blockIdx.x >> 1) & 3, row = 32 * quarter + lane;
@@ -1708,36 +1718,68 @@ __global__ void __launch_bounds__(256) page_join_kernel(const __grid_constant__ 
     if (!c.live || (st && c.split)) return;
     const int rows = (st ? c.toks1 : c.toks0) * a.r;
     if (32 * quarter >= rows) return;
+    const int shares = min(c.c1 - c.c0, 8), share = run - c.c0 - 1;
+    if (share >= shares) return;
+    const int w0 = 8 * share / shares, eighths = 8 * (share + 1) / shares - w0, groups = 8 / eighths;
+    const int mine = warp % eighths, group = warp / eighths;  // eighth of the share, group of parts (the last warps may have none)
     const bool live = row < rows;
-    float o[16], M = -INFINITY, L = 0.f;
+    const int first = c.first + (st ? a.tpt : 0);
+    float M = -INFINITY, L = 0.f, o[16];
 #pragma unroll
     for (int d = 0; d < 16; ++d) o[d] = 0.f;
-    auto slot_of = [&](int k) { return ((size_t)(k == c.c0 ? 2 * k + 1 : 2 * k) * 2 + st) * kTileRows; };
-    if (live) {
-        for (int k = c.c0; k <= c.c1; ++k) M = fmaxf(M, a.part_ml[slot_of(k) + row].x);
-        for (int k = c.c0; k <= c.c1; ++k) {
-            const size_t at = slot_of(k);
-            const float2 ml = a.part_ml[at + row];
-            if (ml.y == 0.f) continue;
-            const float w = ex2_approx((ml.x - M) * kLogitScaleLog2);
-            L = fmaf(ml.y, w, L);
+    if (live && group < groups) {
+        auto slot_of = [&](int k) { return ((size_t)(k == c.c0 ? 2 * k + 1 : 2 * k) * 2 + st) * kTileRows + row; };
+        for (int k0 = c.c0; k0 <= c.c1; k0 += 8) {
+            float2 v[8];
+            float top = M;
 #pragma unroll
-            for (int d = 0; d < 16; ++d) o[d] = fmaf(a.part_o[at * 128 + (size_t)(16 * warp + d) * kTileRows + row], w, o[d]);
+            for (int i = 0; i < 8; ++i) v[i] = k0 + i <= c.c1 ? a.part_ml[slot_of(k0 + i)] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, v[i].x);
+            if (L != 0.f) L *= ex2_approx((M - top) * kLogitScaleLog2);
+            M = top;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (v[i].y != 0.f) L = fmaf(v[i].y, ex2_approx((v[i].x - M) * kLogitScaleLog2), L);
+        }
+        for (int k = c.c0 + group; k <= c.c1; k += 2 * groups) {
+            float x[2][16];
+            float2 ml[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const size_t at = slot_of(min(k + i * groups, c.c1));
+                const float* src = a.part_o + (at - row) * 128 + (size_t)16 * (w0 + mine) * kTileRows + row;
+                ml[i] = k + i * groups <= c.c1 ? a.part_ml[at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int d = 0; d < 16; ++d) x[i][d] = src[(size_t)d * kTileRows];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float w = ex2_approx((ml[i].x - M) * kLogitScaleLog2);
+                if (ml[i].y != 0.f) {  // (else nothing was written)
+#pragma unroll
+                    for (int d = 0; d < 16; ++d) o[d] = fmaf(x[i][d], w, o[d]);
+                }
+            }
         }
     }
     const float inv = L == 0.f ? 0.f : 1.0f / L;
 #pragma unroll
-    for (int d = 0; d < 16; ++d) s_o[lane][16 * warp + d] = o[d] * inv;
-    const int first = c.first + (st ? a.tpt : 0);
-    if (live && warp == 0 && a.lse)
+    for (int d = 0; d < 16; ++d) s_o[warp][lane][d] = o[d] * inv;
+    if (live && warp == 0 && w0 == 0 && a.lse)
         a.lse[(size_t)(first + row / a.r) * a.Hq + c.h * a.r + row % a.r] = L == 0.f ? -INFINITY : M * kRsqrtD + logf(L);
     __syncthreads();
-    for (int i = warp; i < 32; i += 8) {
-        const int y = 32 * quarter + i;
+    const int pairs = 8 * eighths;  // of dims
+    for (int e = tid; e < 32 * pairs; e += 256) {
+        const int i = e / pairs, y = 32 * quarter + i, d = 2 * (e - i * pairs), u = d >> 4;
         if (y >= rows) break;
+        float y0 = 0.f, y1 = 0.f;
+        for (int q = 0; q < groups; ++q) {
+            y0 += s_o[q * eighths + u][i][d & 15];
+            y1 += s_o[q * eighths + u][i][(d & 15) + 1];
+        }
         const size_t to = (size_t)(first + y / a.r) * a.Hq + c.h * a.r + y % a.r;
-        const float* x = s_o[i] + 4 * lane;
-        *reinterpret_cast<uint2*>(a.out + to * 128 + 4 * lane) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        *reinterpret_cast<uint32_t*>(a.out + to * 128 + 16 * w0 + d) = pack_bf16(y0, y1);
     }
 }
 
