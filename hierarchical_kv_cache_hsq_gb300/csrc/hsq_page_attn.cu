@@ -925,11 +925,12 @@ constexpr int kTcBars = (2 * kTileStages + 16 + 2 * kQueue + kNotes + 1) / 2 * 2
 constexpr uint32_t kSegBytes = 96;
 constexpr uint32_t kOffSeg = kOffBars + 8 * kTcBars;
 // Notes on the key tiles, written with their keys' load: [0] what the MMA thread does (kNote*), [1] the tile's pages, bit
-// 8: the softmax has to look at single keys, [2 + i] page i's logical number, then [page][2][words] the tiles' tokens that take it.
+// 8: the softmax has to look at single keys, [4 + i] page i's logical number, then [tile][word][page] the tiles' tokens that take it.
 // Five, because a softmax may be four tiles behind the loads.
-constexpr int kNoteWords = 2 + 8 + 64;
+constexpr int kNotePages = 4, kNoteMasks = 12, kNoteWords = kNoteMasks + 64;
 enum : uint32_t { kNoteStreams = 3, kNoteFirst = 4, kNoteLast = 16, kNoteEnd = 64, kNoteGroups = 8 /* shift */ };
 constexpr uint32_t kOffNote = kOffSeg + kQueue * kSegBytes + 16;        // (+ TMEM address)
+static_assert(kOffNote % 16 == 0 && kNoteWords % 4 == 0, "eight words of a mask are read as two vectors");
 constexpr uint32_t kTcSmem = kOffNote + kNotes * kNoteWords * 4 + 1024;  // + alignment
 static_assert(kOffSeg % 16 == 0, "segments lie on 16-byte boundaries");
 static_assert(kTcSmem <= 232448, "shared memory of a CTA");
@@ -1208,9 +1209,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     failed = __any_sync(kFull, failed);
                     if (failed) break;
                     volatile uint32_t* to = notes + note_at * kNoteWords;
-                    if (lane < np) to[2 + lane] = lp;
-                    if (lane < np * W2) to[10 + lane] = w0;
-                    if (lane + 32 < np * W2) to[10 + 32 + lane] = w1;
+                    if (lane < np) to[kNotePages + lane] = lp;
+                    if (lane < np * W2) to[kNoteMasks + 8 * (lane % W2) + lane / W2] = w0;
+                    if (lane + 32 < np * W2) to[kNoteMasks + 8 * ((lane + 32) % W2) + (lane + 32) / W2] = w1;
                     if (lane == 0) {
                         to[0] = what;
                         to[1] = np | (edge ? 256u : 0u);
@@ -1507,13 +1508,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int np = about & 255;
                 uint32_t gm = 0;  // the groups of 16 keys that this row takes, and those that any row of the warp takes
                 {
-                    uint32_t lm = 0;  // the pages
+                    uint32_t w[8];  // (behind the tile's last page: of some tile before)
+                    const uint32_t from = base + kOffNote + 4 * (slot * kNoteWords + kNoteMasks + 8 * (tile * a.words + word));
+                    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
+                    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(from + 16) : "memory");
+                    const int per_page = a.page_n >> 4;
+                    uint32_t one = (1u << per_page) - 1u;  // a page's groups
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < np) lm |= ((note[10 + (2 * i + tile) * a.words + word] >> (row_token & 31)) & 1u) << i;
-                    if (!live) lm = 0;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) gm |= ((lm >> ((16 * j) >> a.page_shift)) & 1u) << j;
+                    for (int i = 0; i < 8; ++i, one <<= per_page) gm |= (w[i] >> (row_token & 31)) & 1u ? one : 0u;
+                    gm &= live ? (1u << (np * per_page)) - 1u : 0u;
                 }
                 const uint32_t wm = __reduce_or_sync(kFull, gm);
                 wait(s_full + 8 * st, s_par);
@@ -1530,7 +1533,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
                                 const int c = c0 + 16 * hf, i = c >> a.page_shift;
-                                const int p = note[2 + (i & 7)];
+                                const int p = note[kNotePages + (i & 7)];
                                 const int lim = p < a.prefix_pages ? a.prefix_len - (p << a.page_shift) : seen - ((p - a.prefix_pages) << a.page_shift);
                                 const int keys = (gm >> (c >> 4)) & 1u ? lim - (c & (a.page_n - 1)) : 0;
 #pragma unroll
