@@ -1259,15 +1259,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 mma_commit(s_full + 8 * st);
             };
-            auto whole_product = [&](int st, uint32_t v, uint32_t parity) {  // O += P V of a whole tile, not the stream's first
+            auto whole_product = [&](int st, uint32_t v) {  // O += P V of a whole tile, not the stream's first
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
                 const uint64_t dv = sw128_mn_desc(base + (kKeyStages + v) * kTileBytes, kHalfBytes);
-                wait(full + 8 * (kKeyStages + v), parity);
                 wait(p_full + 8 * st, (p_par >> st) & 1);
                 p_par ^= 1u << st;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+            };
+            // The next tile's note, where it is there already: looked for while the pipe works off a product.
+            bool peeked = false;
+            uint32_t next = 0;
+            auto peek = [&] {
+                uint32_t done;
+                asm volatile(
+                    "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                    : "=r"(done)
+                    : "r"(note_full + 8 * slot), "r"(note_par)
+                    : "memory");
+                peeked = done != 0;
+                if (peeked) next = notes[slot * kNoteWords];
             };
             auto settle = [&](int st, uint32_t& due, uint32_t at) {  // O += P V of the stream's tile that is due
                 const uint32_t v = at & 1, stage = kKeyStages + v, g16 = due >> 8, more = (due >> 1) & 1;
@@ -1293,9 +1305,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
 #pragma unroll 1
             for (uint32_t g = 0;; ++g) {
-                wait(note_full + 8 * slot, note_par);
-                const uint32_t what = notes[slot * kNoteWords];
-                wait(full + 8 * kr.stage, kr.phase);
+                if (!peeked) {
+                    wait(note_full + 8 * slot, note_par);
+                    next = notes[slot * kNoteWords];
+                }
+                peeked = false;
+                const uint32_t what = next;
                 if (++slot == kNotes) {
                     slot = 0;
                     note_par ^= 1;
@@ -1307,11 +1322,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 constexpr uint32_t kWhole = 8u << kNoteGroups, kWholeDue = kWhole | 3u;
                 if (due0 == kWholeDue && due1 == kWholeDue) {
                     if (what == (kWhole | 3u) && at0 == at1) {  // (then both are due of tile g - 1)
-                        whole_product(0, (g - 1) & 1, ((g - 1) >> 1) & 1);
+                        wait(full + 8 * (kKeyStages + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
+                        whole_product(0, (g - 1) & 1);
+                        wait(full + 8 * kr.stage, kr.phase);
                         scores(0, 8);
-                        whole_product(1, (g - 1) & 1, ((g - 1) >> 1) & 1);
+                        whole_product(1, (g - 1) & 1);
                         if (__builtin_expect(failed, 0)) break;
                         mma_commit(empty + 8 * (kKeyStages + ((g - 1) & 1)));
+                        peek();
                         scores(1, 8);
                         mma_commit(empty + 8 * kr.stage);
                         users = 1u << (g & 1);
@@ -1320,9 +1338,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         continue;
                     }
                     if (what == (kWhole | 1u) && at0 + 2 == g && at1 + 1 == g && users == 0) {
-                        whole_product(0, g & 1, ((g - 2) >> 1) & 1);
+                        wait(full + 8 * (kKeyStages + (g & 1)), ((g - 2) >> 1) & 1);
+                        whole_product(0, g & 1);
+                        wait(full + 8 * kr.stage, kr.phase);
                         if (__builtin_expect(failed, 0)) break;
                         mma_commit(empty + 8 * (kKeyStages + (g & 1)));
+                        peek();
                         scores(0, 8);
                         mma_commit(empty + 8 * kr.stage);
                         at0 = g;
@@ -1330,9 +1351,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         continue;
                     }
                     if (what == (kWhole | 2u) && at1 + 2 == g && at0 + 1 == g && users == 0) {
-                        whole_product(1, g & 1, ((g - 2) >> 1) & 1);
+                        wait(full + 8 * (kKeyStages + (g & 1)), ((g - 2) >> 1) & 1);
+                        whole_product(1, g & 1);
+                        wait(full + 8 * kr.stage, kr.phase);
                         if (__builtin_expect(failed, 0)) break;
                         mma_commit(empty + 8 * (kKeyStages + (g & 1)));
+                        peek();
                         scores(1, 8);
                         mma_commit(empty + 8 * kr.stage);
                         at1 = g;
@@ -1340,6 +1364,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         continue;
                     }
                 }
+                wait(full + 8 * kr.stage, kr.phase);
+                if (__builtin_expect(failed, 0)) break;
                 const bool flush = (what & kNoteStreams) == 0;
                 // (the older first: a stream whose softmax has still to join the other's part takes up no new tile before)
                 if (due1 && (g - at1 >= 2 || (flush && due0 && (int)(at1 - at0) < 0))) settle(1, due1, at1);
