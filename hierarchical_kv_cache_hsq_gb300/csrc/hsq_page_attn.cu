@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreadsRow)
         ++ask;
     };
     for (int i = 0; i < kStages; ++i) load();
-    failed |= (a.fault & HSQ_FAULT_WAIT_FEW) != 0;
+    failed |= s0 < s1 && (a.fault & HSQ_FAULT_WAIT_FEW) != 0;
     uint32_t qf[8][2];
     {
         const bool in_use = live && g < a.r;
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
         ++ask;
     };
     for (int i = 0; i < kGroupStages; ++i) load();
-    failed |= (a.fault & HSQ_FAULT_WAIT_FEW) != 0;
+    failed |= s0 < s1 && (a.fault & HSQ_FAULT_WAIT_FEW) != 0;
     float o[NT][8][4], m[NT][2], l[NT][2];
     int seen[NT][2];        // of the lane's columns col0 + 8 nt + 2 t + e
     uint32_t bit[NT][2];    // their tokens' bits (0: no row)
@@ -801,6 +801,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     }
     if (tid == 0) *a.head = TileHead{min(units, a.units_cap), min(shorts, a.rows_cap)};
     if (bad) atomicOr(a.err, bad);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (so that the end of the call's last kernel is the end of the groups' too)
 }
 
 // The tokens of a pair of tiles.
@@ -1400,7 +1401,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // (after a wait that ran out no stage is handed back: its copy may still be under way)
                 if (what & kNoteEnd) break;
                 mma_commit(empty + 8 * kr.stage);
-                if (flush) mma_commit(empty + 8 * (kKeyStages + (g & 1)));
+                if (flush) {  // (its value stage is handed back only once it has been taken, or the stage's phases would run ahead)
+                    wait(full + 8 * (kKeyStages + (g & 1)), (g >> 1) & 1);
+                    if (__builtin_expect(failed, 0)) break;
+                    mma_commit(empty + 8 * (kKeyStages + (g & 1)));
+                }
                 kr.advance();
                 failed |= (a.fault & HSQ_FAULT_WAIT_MMA) != 0;
             }
@@ -1547,6 +1552,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t wm = __reduce_or_sync(kFull, gm);
                 wait(s_full + 8 * st, s_par);
                 s_par ^= 1;
+                failed = __any_sync(kFull, failed);
+                if (failed) break;  // (the note may be none: its number of pages would lead past the tensor memory)
                 if (!idle) {
                     tc_fence_after();
                     if (about >> 8) {

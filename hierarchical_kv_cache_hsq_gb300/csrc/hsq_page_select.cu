@@ -76,8 +76,9 @@ struct RowSmem {
 // The whole CTA's selection of the beta largest of the keys s_keys[0 .. G) (0: none; beta >= 1, at least one barrier since they were
 // written): the pages first + i of those taken go to out in ascending order; returns their number.
 // K keys a thread in registers; warp w has the 32 K from 32 K w on, in steps of 32.  A pass counts the keys at or above seven
-// pivots with one barrier: first at doubling distances below the largest key, then at the eighths of the span that holds the
-// beta-th, until exactly beta lie above or the span is one key (whose ties go to the lower pages).
+// pivots with one barrier: first at doubling distances below the largest key, then in turn close around where the count should
+// be met and at the eighths of the span that holds the beta-th, until exactly beta lie above or the span is one key (whose ties go
+// to the lower pages).
 template <int K>
 __device__ int select_row(const uint32_t* s_keys, int G, int beta, int first, int32_t* out, RowSmem& sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = warp * 32 * K + lane;
@@ -99,24 +100,31 @@ __device__ int select_row(const uint32_t* s_keys, int G, int beta, int first, in
     __syncthreads();
     top = __reduce_max_sync(kFull, lane < kRowWarps ? sm.word[0][lane] : 0u);
     n = __reduce_add_sync(kFull, lane < kRowWarps ? (int)sm.word[1][lane] : 0);
-    uint32_t lo = 1;       // at least beta keys (or all there are) lie at or above lo,
-    uint64_t above = (uint64_t)top + 1;  // n_above < beta at or above this
+    // At least beta keys (or all there are) lie at or above lo, n_above < beta at or above lo + span.  (32 bits throughout: the
+    // span of all keys is top - 1 + 1.)
+    uint32_t lo = 1, span = top;
     int n_lo = n, n_above = 0, turn = 0;
     if (n > beta) {
-        bool doubling = true;
+        bool doubling = true, even = false;
         uint32_t step = 1u << 20;
 #pragma unroll 1
-        while (n_lo != beta && above - lo > 1) {
-            uint32_t v[7];
+        while (n_lo != beta && span > 1) {
+            uint32_t v[7];  // as distances from lo, descending
+            if (doubling) {
 #pragma unroll
-            for (int i = 0; i < 7; ++i) {  // descending
-                if (doubling) {
-                    const uint64_t d = (uint64_t)step << i;
-                    v[i] = above > d + lo ? (uint32_t)(above - d) : lo;
-                } else {
-                    v[i] = lo + (uint32_t)(((above - lo) * (7 - i)) >> 3);
-                }
+                for (int i = 0; i < 7; ++i) v[i] = span > step << i && step << i >> i == step ? span - (step << i) : 0u;
+            } else if (even) {
+                const uint32_t whole = span >> 3, rest = span & 7;
+#pragma unroll
+                for (int i = 0; i < 7; ++i) v[i] = whole * (7 - i) + (rest * (7 - i) >> 3);
+            } else {  // close around where the count should be met if the keys were spread evenly
+                const float width = (float)span, at = width * __fdividef((float)(n_lo - beta) + 0.5f, (float)(n_lo - n_above));
+#pragma unroll
+                for (int i = 0; i < 7; ++i) v[i] = min(max(__float2uint_rz(fmaf(width, (float)(3 - i) * (1.f / 24.f), at)), 1u), span - 1);
             }
+            even = !doubling && !even;
+#pragma unroll
+            for (int i = 0; i < 7; ++i) v[i] += lo;
             uint32_t c[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < K; ++i)
@@ -133,6 +141,7 @@ __device__ int select_row(const uint32_t* s_keys, int G, int beta, int first, in
             c[2] = __reduce_add_sync(kFull, x.z);
             c[3] = __reduce_add_sync(kFull, x.w);
             bool found = false;
+            uint32_t above = lo + span;  // (0: past the last key there can be)
 #pragma unroll
             for (int j = 0; j < 7; ++j) {
                 const int m = (int)(j & 1 ? c[j >> 1] >> 16 : c[j >> 1] & 0xFFFFu);
@@ -147,7 +156,8 @@ __device__ int select_row(const uint32_t* s_keys, int G, int beta, int first, in
                     }
                 }
             }
-            if (found || (uint64_t)step << 7 > above) doubling = false;
+            span = above - lo;
+            if (found) doubling = false;
             else step <<= 7;
         }
     }
@@ -265,6 +275,7 @@ __global__ void __launch_bounds__(kRowThreads, K <= 16 ? 2 : 1) page_select_rows
             int n = a.first;
             if (score) {
                 if (K > 4 && G <= 4 * kRowThreads) n += select_row<4>(s_keys, G, beta, a.first, out + a.first, s_sel);
+                else if (K > 8 && G <= 8 * kRowThreads) n += select_row<8>(s_keys, G, beta, a.first, out + a.first, s_sel);
                 else if (K > 16 && G <= 16 * kRowThreads) n += select_row<16>(s_keys, G, beta, a.first, out + a.first, s_sel);
                 else n += select_row<K>(s_keys, G, beta, a.first, out + a.first, s_sel);
             }
@@ -747,6 +758,7 @@ hsq_status hsq_page_select(hsq_ctx* ctx, const hsq_pages* pages, const hsq_summa
         int S = 1;
         while (S < 8 && (long long)rows * Hkv * 2 * S <= 2LL * ctx->num_sms && np + width >= 512 * S) S *= 2;
         const void* fn = np + width <= 4 * kRowThreads ? (const void*)page_select_rows_kernel<4>
+                         : np + width <= 8 * kRowThreads ? (const void*)page_select_rows_kernel<8>
                          : np + width <= 16 * kRowThreads ? (const void*)page_select_rows_kernel<16> : (const void*)page_select_rows_kernel<64>;
         if ((e = hsq::raise_smem_limit(fn, ctx->device, smem)) == cudaSuccess)
             e = launch_cluster(fn, (unsigned)(rows * Hkv * S), kRowThreads, S, smem, st_, false, args);
