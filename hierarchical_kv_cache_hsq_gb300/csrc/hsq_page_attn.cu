@@ -1536,7 +1536,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const volatile uint32_t* note = notes + slot * kNoteWords;
                 wait(note_full + 8 * slot, (at / kNotes) & 1);
                 const uint32_t about = note[1];
-                const int np = about & 255;
+                const int np = min((int)(about & 255), per);  // (behind a wait that ran out the note may be none: not past the tensor memory)
                 uint32_t gm = 0;  // the groups of 16 keys that this row takes, and those that any row of the warp takes
                 {
                     uint32_t w[8];  // (behind the tile's last page: of some tile before)
@@ -1552,8 +1552,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t wm = __reduce_or_sync(kFull, gm);
                 wait(s_full + 8 * st, s_par);
                 s_par ^= 1;
-                failed = __any_sync(kFull, failed);
-                if (failed) break;  // (the note may be none: its number of pages would lead past the tensor memory)
                 if (!idle) {
                     tc_fence_after();
                     if (about >> 8) {
