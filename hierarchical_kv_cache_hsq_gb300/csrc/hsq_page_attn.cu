@@ -84,7 +84,10 @@ __device__ __forceinline__ void for_selected(const PageAttnArgs& a, const int32_
 //   S^T (16 keys x 8 heads) = K (A operand, by ldmatrix) Q^T (B);
 //   O^T (128 dims x 8 heads) += V^T (A, by transposing ldmatrix) P^T (B), P^T from S^T by two 8 x 8 transposes,
 // so no lane exchanges logits but for a new maximum.  The warps' parts are joined in shared memory, the CTAs' through
-// distributed shared memory.
+// distributed shared memory: one launch and no workspace.
+// Bound by the way of the pages: 64 rows x 8 heads x 2048 tokens take 61 us for 532 MB into the SMs (339 MB of it from HBM:
+// rows share pages of the prefix), 8.7 TB/s; with a copy for each half of a row and twice the CTAs 75.  Few rows (4 x 8
+// heads x 256 tokens) take 5.7 us: launch and four dependent loads.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kWarps = 4, kThreadsRow = 32 * kWarps, kStages = 3;
@@ -347,6 +350,8 @@ __global__ void __launch_bounds__(kThreadsRow)
 // a page that several rows take is read once.  The columns of the products are the rows (token x head); a CTA has four streams of
 // keys, and H warps a stream with 16 columns each that share its stages.  The CTAs list the union in shared memory (a word of
 // token bits for each page, in the memory that the stages use afterwards); the rest is as for single rows.
+// 24 requests x 5 rows of 40/8 heads, 64 pages of 16 tokens each: 48 us for 146 MB (row by row 67).  Bound by latency and the
+// products' pipe: a step of 16 keys takes a warp 1500 to 1900 cycles, in which an SM quarter's four warps have 1050 of products.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kGroupStages = 3, kGroupList = 400;  // pages of a union at most, a CTA of the cluster
@@ -735,6 +740,11 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
 // Two streams (a row tile each, S / P and O in tensor memory) share the key tiles that both take and have
 // those that one takes in turn, so that while one stream's softmax runs the tensor cores work for the other.  A lone
 // tile is given to both streams, which take its key tiles in turn and are joined through tensor memory.
+// A chunk of 2048 tokens over 32K (32/8 heads, 64 of 1024 pages a row and head): 387 us, row by row 1530.  The rows of a tile
+// take 450 pages, seven times a row's, so the products are 0.48 TFLOP where the selection's own are 0.07; the tiles' kernel
+// does them in 360 us, 1.34 PFLOP/s.  Bound by the MMA thread and the softmax in turn: a tile of 128 rows x 128 keys takes an
+// SM 1800 cycles, 1024 of them the pipe's; 2.7 GB come through L2 (7.5 TB/s).  The union, and the time, shrink where
+// neighbouring rows take the same pages.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kTileRows = 128, kTileKeys = 128;
@@ -939,13 +949,13 @@ constexpr int kSegReaders = 10;  // 8 softmax warps, the loaders of queries and 
 
 // The key tiles [n0, n1) of an item that a run holds.
 struct alignas(16) TileSegment {
-    int live, h, item, b;
-    int n0, n1, whole, slot;
-    int first, toks0, toks1, split;  // first token's row; the streams' tokens (split: both hold the first's)
+    int live, h, item, slot;
+    int n0, n1, whole, split;        // split: both streams hold the first's tokens
+    int first, toks0, toks1;         // first token's row; the streams' tokens
     int held, ahead;
     int pages[3];                    // both, first alone, second alone
     int tiles[3];
-    int pad[4];
+    int pad[5];
 };
 static_assert(sizeof(TileSegment) == kSegBytes, "");
 
@@ -1140,7 +1150,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 s.live = 1;
                 s.h = h;
                 s.item = item;
-                s.b = p.b;
                 s.first = p.first;
                 s.toks0 = p.toks[0];
                 s.split = p.toks[1] == 0;
@@ -1442,7 +1451,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int st = 0; st < 2; ++st) mbar_wait(q_full + 8 * st, (q_par >> st) & 1, 1 << 12);
         } else if (warp == 11) {
             // ---- the value tiles' pages.  (By the keys' warp, in turn with them, the keys waited for the values' stages, one product
-            // later than their own need: 598 us instead of @@.) ----
+            // later than their own need: a chunk of 2048 over 32K 598 us instead of 469 at the time.) ----
             Ring<kValueStages> vr{0, 1};
             Ring<kQueue> queue{0, 0};
             uint32_t tail_par = 0;

@@ -187,12 +187,13 @@ struct WriteArgs {
     int* err;
 };
 
-// What turns a half-warp's vectors.  kOwnRope: the context's rotation.  Else the first `dims` dims by hsq_rope's table, in
-// pairs (i, i + dims / 2) (kHalfRope) or (2 i, 2 i + 1) (kPairRope).
+// What turns a half-warp's vectors.  kOwnRope: the context's rotation.  Else the first `dims` dims by hsq_rope's
+// table, in pairs (i, i + dims / 2) (kHalfRope) or (2 i, 2 i + 1) (kPairRope).  A table costs no time over the
+// context's rotation (a prompt of 32K tokens 121 us, 6.7 TB/s; 2531 float32 rows 17.2; 16 rows 2.0 in a graph).
 enum { kOwnRope, kHalfRope, kPairRope };
 
-// The two quads of dims that lane l holds: what it turns lies in its own registers (pair k of it has frequency 4 l + k), and
-// lanes past the rotated dims hold those left as they are.
+// The two quads of dims that lane l holds: what it turns lies in its own registers (pair k of it has frequency 4 l +
+// k), and lanes past the rotated dims hold those left as they are.
 template <int ROPE>
 __device__ __forceinline__ void lane_quads(int l, int dims, int& qa, int& qb) {
     if (ROPE == kOwnRope) {
@@ -257,9 +258,9 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* pa, uint16_t* pb, const f
 // vectors), then rotate, round, store.  A unit has one kind of vectors, so that its
 // pointers are two bases and two strides (with the kind chosen vector by vector, address arithmetic
 // took half of the issue slots).  Bound by HBM for many rows, where reads and writes in flight
-// decide: a prompt of 32K tokens (32/8 heads, bf16, 806 MB) takes 121 us, 6.7 TB/s, 99 % of a plain copy's rate; with V = 1,
-// fewer loads in flight, 185.  For few rows by latency, and V = 1 spreads them over the SMs: 16 rows 4.2 us, with
-// V = 8 5.5.  (2531 float32 rows: 25.2 with V = 1, 23.7 with V = 4.)
+// decide: a prompt of 32K tokens (32/8 heads, bf16, 806 MB) takes 121 us, 6.7 TB/s, 99 % of a plain copy's rate;
+// with V = 1, fewer loads in flight, 185.  For few rows by latency, and V = 1 spreads them over the SMs: 16 rows 4.2
+// us, with V = 8 5.5.  (2531 float32 rows: 25.2 with V = 1, 23.7 with V = 4.)
 template <bool BF, int V, int ROPE>
 __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Tables tb) {
     using Raw = typename std::conditional<BF, uint2, float4>::type;  // a quad of dims
@@ -387,7 +388,8 @@ constexpr float kSumLeast = 0x1p-64f, kSumMost = 0x1p126f;
 // 8 l + 7, a lane), 8 tokens a time, the next 8 on their way meanwhile.
 // The sums are kept as fp32 pairs (two_sum2), exact to some 48 bits, because a code jumps by one at a border and has to
 // be the same however the sum is ordered; 127 S / max is compared with its border in 64 bits only where fp32 leaves it
-// open (one element in 5000).
+// open (one element in 5000).  Bound by HBM and, at both ends, latency: the pages of 32K tokens (8 heads, 67 MB)
+// take 15 us, 4.5 TB/s over the whole of it; those of 16 decodes 4.4 us, launch and two dependent loads.
 template <int R>
 __global__ void __launch_bounds__(kSumThreads, 3) page_summaries_kernel(SumsArgs a) {
     const int lane = threadIdx.x & 31, l = lane & 15, odd = lane >> 4;
@@ -396,101 +398,101 @@ __global__ void __launch_bounds__(kSumThreads, 3) page_summaries_kernel(SumsArgs
     const int h = (int)(unit - chunk * a.Hkv);
     constexpr int kWords = (R + 31) / 32;  // 32 rows a look
     for (int k = 0; k < kWords; ++k) {
-    const long long row = chunk * R + 32 * k + lane;
-    long long slot = -1;
-    bool last = false;
-    if (32 * k + lane < R && row < a.rows) {
-        slot = a.slots[row];
-        const long long after = row + 1 < a.rows ? a.slots[row + 1] : -1;
-        if (slot >= (long long)a.n_pages << a.page_shift) {
-            slot = -1;
-            if (h == 0) atomicOr(a.err, HSQ_DEVERR_PAGE);
+        const long long row = chunk * R + 32 * k + lane;
+        long long slot = -1;
+        bool last = false;
+        if (32 * k + lane < R && row < a.rows) {
+            slot = a.slots[row];
+            const long long after = row + 1 < a.rows ? a.slots[row + 1] : -1;
+            if (slot >= (long long)a.n_pages << a.page_shift) {
+                slot = -1;
+                if (h == 0) atomicOr(a.err, HSQ_DEVERR_PAGE);
+            }
+            last = slot >= 0 && (after < 0 || (after >> a.page_shift) != (slot >> a.page_shift));
         }
-        last = slot >= 0 && (after < 0 || (after >> a.page_shift) != (slot >> a.page_shift));
-    }
-    unsigned todo = __ballot_sync(kFull, last);
-    while (todo) {
-        const int from = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const long long at = __shfl_sync(kFull, slot, from);
-        const int page = (int)(at >> a.page_shift), n = (int)(at & (a.page_n - 1)) + 1;
-        const size_t head = (size_t)page * a.Hkv + h;
-        const uint4* src = reinterpret_cast<const uint4*>(a.pk + (head << a.page_shift) * kDim) + odd * 16 + l;
-        uint64_t s[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};
-        uint4 v[4];
-        auto load = [&](int t0) {
+        unsigned todo = __ballot_sync(kFull, last);
+        while (todo) {
+            const int from = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const long long at = __shfl_sync(kFull, slot, from);
+            const int page = (int)(at >> a.page_shift), n = (int)(at & (a.page_n - 1)) + 1;
+            const size_t head = (size_t)page * a.Hkv + h;
+            const uint4* src = reinterpret_cast<const uint4*>(a.pk + (head << a.page_shift) * kDim) + odd * 16 + l;
+            uint64_t s[4] = {0, 0, 0, 0}, e[4] = {0, 0, 0, 0};
+            uint4 v[4];
+            auto load = [&](int t0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = t0 + 2 * k + odd < n ? __ldcs(src + (size_t)(t0 + 2 * k) * 16) : make_uint4(0, 0, 0, 0);
-        };
-        load(0);
+                for (int k = 0; k < 4; ++k) v[k] = t0 + 2 * k + odd < n ? __ldcs(src + (size_t)(t0 + 2 * k) * 16) : make_uint4(0, 0, 0, 0);
+            };
+            load(0);
 #pragma unroll 1
-        for (int t0 = 0; t0 < n; t0 += 8) {
-            uint4 u[4];
+            for (int t0 = 0; t0 < n; t0 += 8) {
+                uint4 u[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) u[k] = v[k];
-            if (t0 + 8 < n) load(t0 + 8);
+                for (int k = 0; k < 4; ++k) u[k] = v[k];
+                if (t0 + 8 < n) load(t0 + 8);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    two_sum2(s[i], e[i], (uint64_t)(w[i] << 16) | ((uint64_t)(w[i] & 0xFFFF0000u) << 32));
+                    for (int i = 0; i < 4; ++i)
+                        two_sum2(s[i], e[i], (uint64_t)(w[i] << 16) | ((uint64_t)(w[i] & 0xFFFF0000u) << 32));
+                }
             }
-        }
-        float hi[8], lo[8];
-        float top = 0.f;
-        bool bad = false;
+            float hi[8], lo[8];
+            float top = 0.f;
+            bool bad = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // the two halves' sums, and the pair brought to hi = their sum rounded
-            const uint64_t so = __shfl_xor_sync(kFull, s[i], 16), eo = __shfl_xor_sync(kFull, e[i], 16);
-            uint64_t a2 = odd ? so : s[i], b2 = odd ? s[i] : so, r2;  // (in one order, so that both halves get the same)
-            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r2) : "l"(e[i]), "l"(eo));
-            two_sum2(a2, r2, b2);
-            const float x[2] = {__uint_as_float((uint32_t)a2), __uint_as_float((uint32_t)(a2 >> 32))};
-            const float y[2] = {__uint_as_float((uint32_t)r2), __uint_as_float((uint32_t)(r2 >> 32))};
+            for (int i = 0; i < 4; ++i) {  // the two halves' sums, and the pair brought to hi = their sum rounded
+                const uint64_t so = __shfl_xor_sync(kFull, s[i], 16), eo = __shfl_xor_sync(kFull, e[i], 16);
+                uint64_t a2 = odd ? so : s[i], b2 = odd ? s[i] : so, r2;  // (in one order, so that both halves get the same)
+                asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r2) : "l"(e[i]), "l"(eo));
+                two_sum2(a2, r2, b2);
+                const float x[2] = {__uint_as_float((uint32_t)a2), __uint_as_float((uint32_t)(a2 >> 32))};
+                const float y[2] = {__uint_as_float((uint32_t)r2), __uint_as_float((uint32_t)(r2 >> 32))};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                hi[2 * i + k] = __fadd_rn(x[k], y[k]);
-                lo[2 * i + k] = __fsub_rn(y[k], __fsub_rn(hi[2 * i + k], x[k]));
-                top = fmaxf(top, fabsf(hi[2 * i + k]));
-                bad |= !(fabsf(hi[2 * i + k]) <= kSumMost);
+                for (int k = 0; k < 2; ++k) {
+                    hi[2 * i + k] = __fadd_rn(x[k], y[k]);
+                    lo[2 * i + k] = __fsub_rn(y[k], __fsub_rn(hi[2 * i + k], x[k]));
+                    top = fmaxf(top, fabsf(hi[2 * i + k]));
+                    bad |= !(fabsf(hi[2 * i + k]) <= kSumMost);
+                }
             }
-        }
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-        bad = __any_sync(kFull, bad);
-        const bool live = !bad && top >= kSumLeast;
-        const float by = __fdiv_rn(127.f, live ? top : 1.f);
-        int code[8];
-        bool open = false;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float y = __fmul_rn(hi[k], by);
-            code[k] = live ? __float2int_rn(y) : 0;
-            open |= live && fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f;
-        }
-        if (__any_sync(kFull, open)) {  // (y is off by less than 127 * 2^-22 here)
-            float rest = -INFINITY;  // what the largest sum has beyond top
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (fabsf(hi[k]) == top) rest = fmaxf(rest, hi[k] < 0.f ? -lo[k] : lo[k]);
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) rest = fmaxf(rest, __shfl_xor_sync(kFull, rest, d));
-            const double m = (double)top + (double)rest;
+            for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+            bad = __any_sync(kFull, bad);
+            const bool live = !bad && top >= kSumLeast;
+            const float by = __fdiv_rn(127.f, live ? top : 1.f);
+            int code[8];
+            bool open = false;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const float y = __fmul_rn(hi[k], by);
-                if (fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f) code[k] = __double2int_rn(127.0 * ((double)hi[k] + lo[k]) / m);
+                code[k] = live ? __float2int_rn(y) : 0;
+                open |= live && fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f;
+            }
+            if (__any_sync(kFull, open)) {  // (y is off by less than 127 * 2^-22 here)
+                float rest = -INFINITY;  // what the largest sum has beyond top
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (fabsf(hi[k]) == top) rest = fmaxf(rest, hi[k] < 0.f ? -lo[k] : lo[k]);
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) rest = fmaxf(rest, __shfl_xor_sync(kFull, rest, d));
+                const double m = (double)top + (double)rest;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float y = __fmul_rn(hi[k], by);
+                    if (fabsf(fabsf(y - rintf(y)) - 0.5f) < 1e-4f) code[k] = __double2int_rn(127.0 * ((double)hi[k] + lo[k]) / m);
+                }
+            }
+            if (odd == 0) {
+                uint32_t w[2] = {0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(code[k] & 0xFF) << (8 * (k & 3));
+                reinterpret_cast<uint2*>(a.codes + head * kDim)[l] = make_uint2(w[0], w[1]);
+                if (l == 0) a.scale[head] = live ? __fdiv_rn(top, 127.f * (float)n) : bad ? INFINITY : 0.f;
             }
         }
-        if (odd == 0) {
-            uint32_t w[2] = {0, 0};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k >> 2] |= (uint32_t)(code[k] & 0xFF) << (8 * (k & 3));
-            reinterpret_cast<uint2*>(a.codes + head * kDim)[l] = make_uint2(w[0], w[1]);
-            if (l == 0) a.scale[head] = live ? __fdiv_rn(top, 127.f * (float)n) : bad ? INFINITY : 0.f;
-        }
-    }
     }
 }
 

@@ -79,7 +79,7 @@ enum {
     HSQ_DEVERR_L1_OVER = 4,   /* more L1 tokens than max_l1: extra tokens dropped from L1 */
     HSQ_DEVERR_WAIT = 8,      /* a bounded wait (on copies or tensor-core work) ran out: of the
                                  prefill attention kernel, whose output is then not written, or
-                                 of hsq_shared_attn, whose results are then undefined */
+                                 of hsq_shared_attn or hsq_page_attn, whose results are then undefined */
     HSQ_DEVERR_GROW = 16,     /* hsq_append: the token leaving the recent window was not in L1
                                  (the cache was not encoded with that window): L1 left as is */
     HSQ_DEVERR_PAGE = 32,     /* paged calls: the free list ran out, or a page id or slot lies outside
@@ -99,13 +99,13 @@ enum {
     HSQ_FAULT_ALLOC = 1,      /* hsq_create fails with HSQ_ERR_NOMEM before any CUDA call */
     HSQ_FAULT_FETCH = 2,      /* hsq_fetch_dequant / hsq_decode_attn return HSQ_ERR_CUDA
                                  without launching */
-    /* hsq_shared_attn: a part of its main kernel goes on as where a bounded wait has run out
+    /* hsq_shared_attn, hsq_page_attn: a part of its main kernel goes on as where a bounded wait has run out
        (and all waits get a short bound): HSQ_DEVERR_WAIT, results undefined, the next call as ever */
     HSQ_FAULT_WAIT_LOAD = 4,     /* the loads of keys and values, between the two */
     HSQ_FAULT_WAIT_MMA = 8,      /* the issue of the products, behind a long request's first tile */
     HSQ_FAULT_WAIT_QUERY = 16,   /* the loads of queries, between two row tiles */
     HSQ_FAULT_WAIT_SOFTMAX = 32, /* the softmax, behind its first item */
-    HSQ_FAULT_WAIT_FEW = 64      /* requests of up to 16 rows, with their first loads under way */
+    HSQ_FAULT_WAIT_FEW = 64      /* requests of few rows, with their first loads under way */
 };
 
 typedef struct hsq_config {
@@ -682,8 +682,9 @@ hsq_status hsq_page_write_rope(hsq_ctx* ctx, const hsq_pages* pages, const hsq_r
  *   them there already.  A page's last row i of the step (slots[i + 1] lies on another page, is negative or past
  *   the end) makes its summary of tokens 0 .. slots[i] mod page_n.  Negative slots are skipped; the other pages'
  *   summaries are left as they were.  A page that the step names in two places apart gets one of the two.
- *   A page whose max|S| is below 2^-64 gets codes and scale 0; one whose is not a number or above 2^126
- *   codes 0 and scale inf: such a page is selected before all others (see below), so that it shows in the result.
+ *   A page whose max|S| is below 2^-64 gets codes and scale 0; one whose is not a number, above 2^126 or past
+ *   fp32's range on the way codes 0 and scale inf: such a page is selected before all others (see below), so that
+ *   it shows in the result.
  *   S is summed to some 48 bits and a code near a border is decided in 64.
  *   HSQ_DEVERR_PAGE: a slot outside the pool (skipped).
  *   Errors: HSQ_ERR_INVALID (NULL, rows < 1 or >= 2^30, alignment, codes or scale over each other, slots or the pool's
