@@ -64,10 +64,11 @@ constexpr int kBins = 256;
 
 // The bin of a key where the largest, `most`, has a positive score: bins 1 .. 255 of equal width in the score from 0 to the largest
 // (what lies below goes to bin 1), rounded to a whole number in the last bits of 2^23 + it, which takes no conversion; 0 for no key.
-// Monotone in the key; NaN, above all numbers, goes to the last bin.
+// Monotone in the key.  (A product that is no number, of an infinite largest score or one whose 254th part is past fp32's range, goes to
+// bin 1 with all that lies at or below it.)
 __device__ __forceinline__ int score_bin(uint32_t key, float per) {
-    const int x = __float_as_int(fmaf(key_to_float(key), per, 8388609.f)) - 0x4B000000;
-    return key == 0u ? 0 : min(max(x, 1), kBins - 1);
+    const int x = __float_as_int(fmaxf(fmaf(key_to_float(key), per, 8388609.f), 8388609.f)) - 0x4B000000;
+    return key == 0u ? 0 : min(x, kBins - 1);
 }
 
 // By a warp: the bin of the need-th key from the top of a histogram (lane l adds up the bins 255 - 8 l .. 248 - 8 l; bin 0 counts for
@@ -142,10 +143,11 @@ struct RowSmem {
 // written): the pages first + i of those taken go to out in ascending order; returns their number.
 // K keys a thread in registers; warp w has the 32 K from 32 K w on, in steps of 32.  A histogram of the scores tells the bin
 // that holds the beta-th key, and up to 32 keys in it are ranked one against the other.  Where more share the bin, or no score is
-// positive, passes of counting find it (each some 0.5 us: as the only way 13.8 us in place of 12.4 for 16 decodes of up to 2048 pages, 12.6 in place of 9.7 for 4 of 4096).  A pass counts the keys at or above seven
-// pivots with one barrier: first at doubling distances below the largest key, then in turn close around where the count should
-// be met and at the eighths of the span that holds the beta-th, until exactly beta lie above or the span is one key (whose ties go
-// to the lower pages).
+// positive, passes of counting find it (each some 0.5 us: as the only way 13.8 us in place of 12.4 for 16 decodes of up
+// to 2048 pages, 12.6 in place of 9.7 for 4 of 4096).  A pass counts the keys at or above seven pivots with one barrier:
+// first at doubling distances below the largest key, then in turn close around where the count should be met and at the
+// eighths of the span that holds the beta-th, until exactly beta lie above or the span is one key (whose ties go to the
+// lower pages).
 template <int K>
 __device__ int select_row(const uint32_t* s_keys, int G, int beta, int first, int32_t* out, RowSmem& sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = warp * 32 * K + lane;
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                 most = __reduce_max_sync(kFull, most);
                 const float per = 254.f / key_to_float(most);
                 auto bin_of = [&](uint32_t v) { return score_bin(v, per); };
-                const bool by_score = key_to_float(most) > 0.f;  // (also of an infinite score or none that is a number: NaN goes to the last bin)
+                const bool by_score = key_to_float(most) > 0.f;  // (not where the largest is NaN)
                 uint32_t bins[kChunk / 128];
                 clear();
 #pragma unroll

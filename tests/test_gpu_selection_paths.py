@@ -91,6 +91,31 @@ def test_selection_of_scores_that_lie_badly(new, kind):
     np.testing.assert_array_equal(sel, want_select(x)[0])
 
 
+@pytest.mark.parametrize("new", [1, 12])
+@pytest.mark.parametrize("most", [1e-3, 1e-40, np.inf])
+@pytest.mark.parametrize("top", [20, 64])
+def test_selection_where_most_scores_lie_far_below_the_best(new, most, top):
+    """A few small (or infinite) scores above zero, the others below it by factors of up to 1e6 of the largest."""
+    pages = 2100
+    x = with_summaries(long_inputs(4, 2, 16, [16 * pages - 3], [new], seed=17), top, seed=18)
+    q = x["q"].clone()
+    q[:] = 0
+    q[:, :, 0] = 1.0
+    x["q"] = q
+    rng = np.random.default_rng(19)
+    n = x["codes"].shape[0]
+    good = rng.random(n) < 0.005  # (some ten pages: fewer than are taken)
+    far = np.where(rng.random(n) < 0.2, rng.uniform(-1, 6, n), rng.uniform(5, 6, n))
+    x["codes"][:], x["codes"][:, :, 0] = 0, np.where(good, 1, -1)[:, None]
+    # the first head's rest below zero, the second's some at zero too
+    x["codes"][:, 1, 0][~good & (rng.random(n) < 0.5)] = 0
+    low = (most if 0 < most < np.inf else 1e-3) / 127 * 10.0 ** far
+    x["scale"][:] = np.where(good, most / 127 * (1 - rng.random(n) / 8), low).astype(np.float32)[:, None]
+    sel, err = run_select(x)
+    assert not err
+    np.testing.assert_array_equal(sel, want_select(x)[0])
+
+
 # tiles' lists go by windows of 1024 (one head a KV head), 2048 and 4096 pages; a group's by 24576
 @pytest.mark.parametrize("Hq,Hkv,page,own,new,top", [
     (1, 1, 16, [18000, 40], [140, 1], 20), (2, 1, 16, [36000], [70], 30), (4, 1, 16, [70000], [40], 9),
