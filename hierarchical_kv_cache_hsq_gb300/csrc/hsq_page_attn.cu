@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
     }
     if (failed) {  // see the copies in flight (one a stage at most) land: their memory is used again
         if (half == 0)
-        for (int i = 0; i < kGroupStages; ++i) mbar_wait(bars + 8 * i, i < (int)in.stage ? in.phase : in.phase ^ 1, 1 << 12);
+            for (int i = 0; i < kGroupStages; ++i) mbar_wait(bars + 8 * i, i < (int)in.stage ? in.phase : in.phase ^ 1, 1 << 12);
         bad |= HSQ_DEVERR_WAIT;
     }
     // the warp's part (its stream's stages are free once every warp of it is through)
