@@ -740,10 +740,10 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
 // Two streams (a row tile each, S / P and O in tensor memory) share the key tiles that both take and have
 // those that one takes in turn, so that while one stream's softmax runs the tensor cores work for the other.  A lone
 // tile is given to both streams, which take its key tiles in turn and are joined through tensor memory.
-// A chunk of 2048 tokens over 32K (32/8 heads, 64 of 1024 pages a row and head): 387 us, row by row 1530.  The rows of a tile
+// A chunk of 2048 tokens over 32K (32/8 heads, 64 of 1024 pages a row and head): 380 us, row by row 1530.  The rows of a tile
 // take 450 pages, seven times a row's, so the products are 0.48 TFLOP where the selection's own are 0.07; the tiles' kernel
-// does them in 360 us, 1.34 PFLOP/s.  Bound by the MMA thread and the softmax in turn: a tile of 128 rows x 128 keys takes an
-// SM 1800 cycles, 1024 of them the pipe's; 2.7 GB come through L2 (7.5 TB/s).  The union, and the time, shrink where
+// does them in some 350 us, 1.38 PFLOP/s.  Bound by the MMA thread and the softmax in turn: a tile of 128 rows x 128 keys takes an
+// SM 1750 cycles, 1024 of them the pipe's; 2.7 GB come through L2 (7.7 TB/s).  The union, and the time, shrink where
 // neighbouring rows take the same pages.
 // ---------------------------------------------------------------------------------------
 
@@ -929,6 +929,9 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
 
 constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kTileStages = kKeyStages + kValueStages, kQueue = 2;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
+// Keys and values lie in groups of 8 rows, the group's halves side by side (kGroupHalf apart), so that a page is one copy (with a
+// copy for each half, and the copies behind the notes, a chunk of 2048 over 32K 387 us in place of 380).
+constexpr uint32_t kGroupBytes = 8 * 256, kGroupHalf = kGroupBytes / 2;
 constexpr uint32_t kOffQ = kTileStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
 // barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | drain | m_full | m_free | seg_full[2] | seg_empty[2] | note_full[5]
 constexpr int kNotes = 5;
@@ -1088,9 +1091,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // ---- the run's segments, and the key tiles' pages (lane i: page i of the tile) ----
             Ring<kKeyStages> kr{0, 1};
             Ring<kQueue> queue{0, 1};  // (a fresh barrier lets a wait for parity 1 pass: the stages start empty)
-            const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
+            const uint32_t page_bytes = (uint32_t)a.page_n * 256u;
             const int W2 = 2 * a.words;
             int note_at = 0;
+            // where in a note the lane's two words of a tile's masks go (word i of page p from p W2 + i)
+            const int mask0 = kNoteMasks + 8 * (lane % W2) + lane / W2, mask1 = kNoteMasks + 8 * ((lane + 32) % W2) + (lane + 32) / W2;
             auto note = [&](uint32_t what) {  // a tile without keys: a word to the MMA thread alone
                 wait(empty + 8 * kr.stage, kr.phase);
                 failed = __any_sync(kFull, failed);
@@ -1218,25 +1223,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     wait(empty + 8 * kr.stage, kr.phase);
                     failed = __any_sync(kFull, failed);
                     if (failed) break;
+                    // (the copies first: they take longest, each some 150 cycles of the warp's and then its way)
+                    if (lane == 0) mbar_expect_tx(bar, np * page_bytes);
+                    __syncwarp();
+                    if (lane < np) tma_4d(stage + lane * page_bytes, &mk, 0, 0, 0, y >> 3, bar);
                     volatile uint32_t* to = notes + note_at * kNoteWords;
                     if (lane < np) to[kNotePages + lane] = lp;
-                    if (lane < np * W2) to[kNoteMasks + 8 * (lane % W2) + lane / W2] = w0;
-                    if (lane + 32 < np * W2) to[kNoteMasks + 8 * ((lane + 32) % W2) + (lane + 32) / W2] = w1;
+                    if (lane < np * W2) to[mask0] = w0;
+                    if (lane + 32 < np * W2) to[mask1] = w1;
                     if (lane == 0) {
                         to[0] = what;
                         to[1] = np | (edge ? 256u : 0u);
                     }
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(note_full + 8 * note_at);
-                        mbar_expect_tx(bar, np * page_bytes);
-                    }
+                    warp_arrive(note_full + 8 * note_at);
                     if (++note_at == kNotes) note_at = 0;
-                    __syncwarp();
-                    if (lane < np) {
-                        tma_2d(stage + lane * half_page, &mk, 0, y, bar);
-                        tma_2d(stage + lane * half_page + kHalfBytes, &mk, 64, y, bar);
-                    }
                     kr.advance();
                     failed |= (a.fault & HSQ_FAULT_WAIT_LOAD) != 0;
                 }
@@ -1261,22 +1261,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t slot = 0, note_par = 0;
             auto scores = [&](int st, uint32_t g16) {  // S = Q K^T
                 const uint32_t dS = tmem + 128 * st, idS = idesc_bf16_f32(128, 16 * g16);
-                const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + kr.stage * kTileBytes);
+                const uint64_t dq = sw128_desc(base + kOffQ + st * kTileBytes), dk = sw128_desc(base + kr.stage * kTileBytes, kGroupBytes);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const uint32_t o = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4;
-                    mma_bf16(dS, dq + o, dk + o, idS, k > 0);
+                    const uint32_t q = ((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4, o = ((k >> 2) * kGroupHalf + (k & 3) * 32) >> 4;
+                    mma_bf16(dS, dq + q, dk + o, idS, k > 0);
                 }
                 mma_commit(s_full + 8 * st);
             };
             auto whole_product = [&](int st, uint32_t v) {  // O += P V of a whole tile, not the stream's first
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
-                const uint64_t dv = sw128_mn_desc(base + (kKeyStages + v) * kTileBytes, kHalfBytes);
+                const uint64_t dv = sw128_mn_desc(base + (kKeyStages + v) * kTileBytes, kGroupHalf, kGroupBytes);
                 wait(p_full + 8 * st, (p_par >> st) & 1);
                 p_par ^= 1u << st;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+                for (int k = 0; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2 * kGroupBytes >> 4), idO, 1);
             };
             // The next tile's note, where it is there already: looked for while the pipe works off a product.
             bool peeked = false;
@@ -1294,7 +1294,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             auto settle = [&](int st, uint32_t& due, uint32_t at) {  // O += P V of the stream's tile that is due
                 const uint32_t v = at & 1, stage = kKeyStages + v, g16 = due >> 8, more = (due >> 1) & 1;
                 const uint32_t pa = tmem + 128 * st, dO = pa + 256;
-                const uint64_t dv = sw128_mn_desc(base + stage * kTileBytes, kHalfBytes);
+                const uint64_t dv = sw128_mn_desc(base + stage * kTileBytes, kGroupHalf, kGroupBytes);
                 wait(full + 8 * stage, (at >> 1) & 1);
                 wait(p_full + 8 * st, (p_par >> st) & 1);
                 if (__builtin_expect(failed, 0)) return;
@@ -1303,10 +1303,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (g16 == 8) {
                     mma_bf16_ts(dO, pa, dv, idO, more);
 #pragma unroll
-                    for (int k = 1; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, 1);
+                    for (int k = 1; k < 8; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2 * kGroupBytes >> 4), idO, 1);
                 } else {
 #pragma unroll 1
-                    for (uint32_t k = 0; k < g16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2048 >> 4), idO, more | (k > 0));
+                    for (uint32_t k = 0; k < g16; ++k) mma_bf16_ts(dO, pa + 8 * k, dv + k * (2 * kGroupBytes >> 4), idO, more | (k > 0));
                 }
                 if (!((users >> v) & 1)) mma_commit(empty + 8 * stage);
                 users &= ~(1u << v);
@@ -1456,7 +1456,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             Ring<kQueue> queue{0, 0};
             uint32_t tail_par = 0;
             bool tail_due = false;
-            const uint32_t page_bytes = (uint32_t)a.page_n * 256u, half_page = (uint32_t)a.page_n * 128u;
+            const uint32_t page_bytes = (uint32_t)a.page_n * 256u;
             while (receive(queue) && !failed) {
                 auto look_up = [&](const KeyTile& u) {
                     return lane < u.np ? a.ent[((size_t)s.item * 3 + u.region) * a.cap + u.at + lane] : make_int2(0, 0);
@@ -1486,10 +1486,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         else mbar_expect_tx(lands, np * page_bytes);
                     }
                     __syncwarp();
-                    if (lane < np) {
-                        tma_2d(stage + lane * half_page, &mv, 0, y, lands);
-                        tma_2d(stage + lane * half_page + kHalfBytes, &mv, 64, y, lands);
-                    }
+                    if (lane < np) tma_4d(stage + lane * page_bytes, &mv, 0, 0, 0, y >> 3, lands);
                     if (ends) {
                         wait(tail, tail_par);
                         failed = __any_sync(kFull, failed);
@@ -1502,8 +1499,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const int i = __ffs(left) - 1, have = max(__shfl_sync(kFull, tokens, i), 0);
                             const int row0 = (i << a.page_shift) + have, z = (a.page_n - have) * 16;  // 16-byte chunks of both halves
                             for (int x = lane; x < z; x += 32)
-                                *reinterpret_cast<uint4*>(gbase + (stage - base) + ((x >> 3) & 1) * kHalfBytes + (row0 + (x >> 4)) * 128 +
-                                                          (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(gbase + (stage - base) + ((row0 + (x >> 4)) >> 3) * kGroupBytes + ((x >> 3) & 1) * kGroupHalf +
+                                                          ((row0 + (x >> 4)) & 7) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         fence_async_smem();
                         __syncwarp();
@@ -1970,7 +1967,7 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
         if (e != cudaSuccess) return hsq::cuda_fail(ctx, e, "page_attn groups");
     }
     if (tiles) {
-        if (!encode_q(&mq, q, rows, Hq, a.r, x.tpt) || !encode_rows(&mk, pages->k, n, P) || !encode_rows(&mv, pages->v, n, P))
+        if (!encode_q(&mq, q, rows, Hq, a.r, x.tpt) || !encode_groups(&mk, pages->k, n, P) || !encode_groups(&mv, pages->v, n, P))
             return hsq::fail(ctx, HSQ_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor map");
         void* args[] = {&a};
         void* tc_args[] = {&mq, &mk, &mv, &a};

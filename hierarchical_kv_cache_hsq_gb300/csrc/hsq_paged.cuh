@@ -183,6 +183,15 @@ inline bool encode_halves(CUtensorMap* map, void* p, uint64_t rows, uint32_t box
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same in groups of 8 rows: a group's first halves, then its second ones.  rows and box_rows: multiples of 8.
+inline bool encode_groups(CUtensorMap* map, void* p, uint64_t rows, uint32_t box_rows) {
+    const cuuint64_t dims[4] = {64, 8, 2, rows / 8}, strides[3] = {256, 128, 2048};
+    const cuuint32_t box[4] = {64, 8, 2, box_rows / 8}, es[4] = {1, 1, 1, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // queries [rows][Hq][128]: a box is `tokens` tokens x the r heads of a KV head x 64 columns
 inline bool encode_q(CUtensorMap* map, const void* p, uint64_t rows, uint64_t Hq, uint32_t r, uint32_t tokens) {
     const cuuint64_t dims[3] = {128, Hq, rows}, strides[2] = {256, 256 * Hq};

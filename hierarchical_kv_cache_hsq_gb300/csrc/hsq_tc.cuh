@@ -117,6 +117,14 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const void* map, int x, int
         : "memory");
 }
 
+__device__ __forceinline__ void tma_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];\n"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
 // ---- tensor memory ---------------------------------------------------------
 
 // one full warp: allocate ncols (a power of two >= 32) columns, address written to shared `slot`
@@ -140,8 +148,8 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 // used by this layout), stride byte offset >> 4 = 1024 bytes between 8-row
 // groups (bits 32-45), descriptor version 1 (bits 46-47), base offset 0,
 // layout type 2 = 128-byte swizzle (bits 61-63).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(16u >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t stride = 1024) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(16u >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
 
@@ -153,10 +161,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 }
 
 // The same operand read along its other dimension (MN-major, 128-byte swizzle): rows of 64 elements of
-// the M or N dimension (128 bytes), one row per K index, 8 rows to an atom.  Stride byte offset: 1024
+// the M or N dimension (128 bytes), one row per K index, 8 rows to an atom.  Stride byte offset: `stride`
 // bytes between 8-row groups; leading byte offset: `lead` bytes between blocks of 64 elements.
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t lead) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t lead, uint32_t stride = 1024) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
 
