@@ -260,6 +260,7 @@ class Context:
 
     def __init__(self, cfg: hsq_config):
         self.cfg = cfg
+        self.heads = (cfg.n_q_heads, cfg.n_kv_heads)
         self.lib = load_library()
         h = _vp()
         _check(self.lib.hsq_create(ctypes.byref(cfg), ctypes.byref(h)))
@@ -522,7 +523,7 @@ class PagePool:
         if self.k.shape != self.v.shape or self.k.device != self.v.device:
             raise ValueError("k and v must have one shape and one device")
         c = hsq_pages(k=self.k.data_ptr(), v=self.v.data_ptr(), n_pages=self.k.shape[0], page_n=self.k.shape[2])
-        for name, value in (("index", self.k.get_device()), ("_c", c), ("ref", ctypes.byref(c))):
+        for name, value in (("index", self.k.get_device()), ("heads", self.k.shape[1]), ("_c", c), ("ref", ctypes.byref(c))):
             object.__setattr__(self, name, value)
 
     @property
@@ -624,7 +625,7 @@ def _stream_on(pool: PagePool, stream) -> int:
     """The given stream's handle, or the current one's; the pool has to be on the current device (as the
     library holds the context to it)."""
     import torch
-    if torch.cuda.current_device() != pool.index:
+    if torch._C._cuda_getDevice() != pool.index:
         raise ValueError("the pool is not on the current device")
     # (the handle alone, as torch's own launchers take it: 0.1 us, through a Stream object 2.8 of a call's 9)
     return torch._C._cuda_getCurrentRawStream(pool.index) if stream is None else stream.cuda_stream
@@ -636,7 +637,7 @@ def _c_int(x: int) -> int:
 
 
 def _need_heads(ctx: Context, pool: PagePool):
-    if pool.k.shape[1] != ctx.cfg.n_kv_heads:
+    if pool.heads != ctx.heads[1]:
         raise ValueError("the pool's KV heads are not the context's")
 
 
@@ -686,26 +687,25 @@ def hsq_page_write(ctx: Context, pool: PagePool, q, k, v, pos, slots, q_out, str
         dt = HSQ_DTYPE_F32
     else:
         raise ValueError("q, k and v must be bfloat16 or float32")
-    rows, Hkv = pos.numel(), ctx.cfg.n_kv_heads
-    parts = (("k", k, Hkv), ("v", v, Hkv)) if q is None else (("k", k, Hkv), ("v", v, Hkv), ("q", q, ctx.cfg.n_q_heads))
+    rows, (Hq, Hkv), strides = pos.numel(), ctx.heads, []
+    parts = (("k", k, Hkv), ("v", v, Hkv)) if q is None else (("k", k, Hkv), ("v", v, Hkv), ("q", q, Hq))
     for name, x, heads in parts:
         if x.dtype != k.dtype or x.get_device() != pool.index or x.shape != (rows, heads, 128):
             raise ValueError(f"{name} must be [rows, heads, 128], of one dtype, on the pool's device")
         s = x.stride()
         if s[2] != 1 or (s[1] != 128 and heads > 1):
             raise ValueError(f"{name}: the heads of a row must lie side by side")
+        strides.append(heads * 128 if rows == 1 else s[0])  # (the row stride of a single row says nothing)
     if slots.numel() != rows or rows >> 31:
         raise ValueError("pos and slots must be [rows], rows below 2^31")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
         _need(pool, torch.bfloat16, "q_out", q_out)
-        if q_out.shape != q.shape:
+        if q_out.shape != (rows, Hq, 128):
             raise ValueError("q_out must have q's shape")
-    one = rows == 1  # (the row stride of a single row says nothing)
-    args = (rows, _ptr(q), k.data_ptr(), v.data_ptr(), 0 if q is None else ctx.cfg.n_q_heads * 128 if one else q.stride(0),
-            Hkv * 128 if one else k.stride(0), Hkv * 128 if one else v.stride(0), dt, pos.data_ptr(), slots.data_ptr(),
-            _ptr(q_out), _stream_on(pool, stream))
+    args = (rows, _ptr(q), k.data_ptr(), v.data_ptr(), 0 if q is None else strides[2], strides[0], strides[1], dt,
+            pos.data_ptr(), slots.data_ptr(), _ptr(q_out), _stream_on(pool, stream))
     if rope is None:
         st = ctx.lib.hsq_page_write(ctx.handle, pool.ref, *args)
     else:
@@ -778,7 +778,7 @@ def hsq_page_summaries(ctx: Context, pool: PagePool, sums: PageSummaries, slots,
 
 
 def _need_summaries(pool: PagePool, sums: PageSummaries):
-    if sums.index != pool.index or sums.shape != (pool.n_pages, pool.k.shape[1]):
+    if sums.index != pool.index or sums.shape != (pool.n_pages, pool.heads):
         raise ValueError("the summaries are not of the pool's pages, or on another device")
 
 
@@ -804,14 +804,16 @@ def _selection_args(ctx, pool, q, q_start, lens, table, sel, workspace, prefix, 
     _need_heads(ctx, pool)
     _need(pool, torch.bfloat16, "q", q)
     _need(pool, torch.int32, "q_start lens table sel", q_start, lens, table, sel)
-    B, rows = lens.numel(), q.shape[0]
-    if q.shape[1:] != (ctx.cfg.n_q_heads, 128):
+    B, qs, ts, ss = lens.numel(), q.shape, table.shape, sel.shape
+    Hq, Hkv = ctx.heads
+    if len(qs) != 3 or qs[1] != Hq or qs[2] != 128:
         raise ValueError("q must be [rows, Hq, 128]")
-    if sel.dim() != 3 or sel.shape[:2] != (rows, ctx.cfg.n_kv_heads):
+    rows = qs[0]
+    if len(ss) != 3 or ss[0] != rows or ss[1] != Hkv:
         raise ValueError("sel must be [rows, Hkv, top]")
-    if q_start.numel() != B + 1 or table.dim() != 2 or table.shape[0] != B:
+    if q_start.numel() != B + 1 or len(ts) != 2 or ts[0] != B:
         raise ValueError("q_start [B + 1] and table [B, width] must agree with lens [B]")
-    if (rows | B | table.shape[1] | sel.shape[2]) >> 31:
+    if (rows | B | ts[1] | ss[2]) >> 31:
         raise ValueError("a tensor has more elements than the library counts")
     if prefix_len > 0:
         if prefix is None:
@@ -821,7 +823,7 @@ def _selection_args(ctx, pool, q, q_start, lens, table, sel, workspace, prefix, 
             raise ValueError("prefix has too few pages for prefix_len")
     if workspace.get_device() != pool.index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the pool's device")
-    return rows, B, table.shape[1], sel.shape[2], prefix.data_ptr() if prefix_len > 0 else None
+    return rows, B, ts[1], ss[2], prefix.data_ptr() if prefix_len > 0 else None
 
 
 def hsq_page_select(ctx: Context, pool: PagePool, sums: PageSummaries, q, q_start, lens, table, sel, workspace, prefix=None,
@@ -835,7 +837,7 @@ def hsq_page_select(ctx: Context, pool: PagePool, sums: PageSummaries, q, q_star
     st = ctx.lib.hsq_page_select(ctx.handle, pool.ref, sums.ref, rows, B, width, _c_int(prefix_len), top, _c_int(first),
                                  _c_int(recent), _c_int(max_new), q.data_ptr(), q_start.data_ptr(), lens.data_ptr(),
                                  table.data_ptr(), pre, sel.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream_on(pool, stream))
+                                 workspace.nbytes, _stream_on(pool, stream))
     if st:
         _check(st, ctx.handle)
 
@@ -848,15 +850,15 @@ def hsq_page_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, sel, ou
     import torch
     rows, B, width, top, pre = _selection_args(ctx, pool, q, q_start, lens, table, sel, workspace, prefix, prefix_len)
     _need(pool, torch.bfloat16, "out", out)
-    if out.shape != q.shape:
+    if out.shape != (rows, ctx.heads[0], 128):
         raise ValueError("out must have q's shape")
     if lse is not None:
         _need(pool, torch.float32, "lse", lse)
-        if lse.shape != q.shape[:2]:
+        if lse.shape != (rows, ctx.heads[0]):
             raise ValueError("lse must be [rows, Hq]")
     st = ctx.lib.hsq_page_attn(ctx.handle, pool.ref, rows, B, width, _c_int(prefix_len), top, _c_int(max_new), q.data_ptr(),
                                q_start.data_ptr(), lens.data_ptr(), table.data_ptr(), pre, sel.data_ptr(), out.data_ptr(),
-                               _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _ptr(lse), workspace.data_ptr(), workspace.nbytes,
                                _stream_on(pool, stream))
     if st:
         _check(st, ctx.handle)
