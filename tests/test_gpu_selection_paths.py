@@ -11,7 +11,8 @@ import pytest
 from hsq_harness import ensure_built
 from oracle import paged as P
 from test_gpu_paged import attn_inputs, host, i32, i64, make
-from test_gpu_selection import (check_page_attn, run_page_attn, run_select, selection_inputs, some_selection, want_select, word)
+from test_gpu_selection import (check_page_attn, check_summaries, run_page_attn, run_select, selection_inputs, some_selection,
+                                want_select, word)
 
 pytestmark = pytest.mark.gpu
 
@@ -185,6 +186,35 @@ def test_a_longer_bound_on_rows_changes_nothing(new):
             sel, err = run_select(y, max_new=bound)
             assert not err
             np.testing.assert_array_equal(sel, want_select(y)[0])
+
+
+@pytest.mark.parametrize("new", [1, 4, 60])
+def test_pages_past_four_gigabytes(new):
+    """The same pages behind some 2^31 elements of others give the same results."""
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    x = selection_inputs(8, 8, 64, 100, [700, 300], [new, 1], 5, seed=70)
+    few, off = x["k"].shape[0], (1 << 32) // (8 * 64 * 256) + 7
+    y = dict(x, prefix=x["prefix"] + off, table=np.where(x["table"] >= 0, x["table"] + off, -1).astype(np.int32),
+             codes=np.zeros((off + few, 8, 128), np.int8), scale=np.zeros((off + few, 8), np.float32))
+    y["codes"][off:], y["scale"][off:] = x["codes"], x["scale"]
+    for n in "kv":
+        y[n] = torch.empty((off + few, 8, 64, 128), dtype=torch.bfloat16, device="cuda")
+        y[n][off:] = x[n]
+    sel, err = run_select(y)
+    assert not err
+    np.testing.assert_array_equal(sel, want_select(x)[0])
+    out, lse, err = run_page_attn(y, sel)
+    assert not err
+    check_page_attn(x, sel, out, lse)
+    ctx, pool = make(8, 8, 1), H.PagePool(y["k"], y["v"])
+    sums = H.allocate_summaries(ctx, pool)
+    pages = np.unique(np.concatenate([x["prefix"][:1], x["table"][0, :4]]))
+    slots = pages.astype(np.int64) * 64 + 63
+    H.hsq_page_summaries(ctx, pool, sums, i64(slots + 64 * off))
+    assert word(ctx) == set()
+    want = P.page_summaries(host(x["k"]), slots, np.zeros((few, 8, 128), np.int8), np.zeros((few, 8), np.float32))
+    check_summaries(sums.codes[off:].cpu().numpy(), host(sums.scale[off:]), want[0], want[1])
 
 
 def test_calls_on_two_streams_at_once():
