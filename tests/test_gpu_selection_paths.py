@@ -217,6 +217,21 @@ def test_pages_past_four_gigabytes(new):
     check_summaries(sums.codes[off:].cpu().numpy(), host(sums.scale[off:]), want[0], want[1])
 
 
+@pytest.mark.parametrize("most", [1, 4, 40])
+def test_more_requests_than_a_block_has_threads(most):
+    """1300 requests, the kernels that look through all of them in several rounds."""
+    rng = np.random.default_rng(most)
+    own = rng.integers(1, 120, 1300)
+    new = np.minimum(own, rng.integers(1, most + 1, 1300) if most < 9 else np.where(rng.random(1300) < 0.03, most, 1))
+    x = selection_inputs(2, 1, 16, 20, [int(n) for n in own], [int(n) for n in new], 4, pad=2, seed=most)
+    sel, err = run_select(x)
+    assert not err
+    np.testing.assert_array_equal(sel, want_select(x)[0])
+    out, lse, err = run_page_attn(x, sel)
+    assert not err
+    check_page_attn(x, sel, out, lse)
+
+
 def test_calls_on_two_streams_at_once():
     """Each with its own context, workspace and outputs; the same pool."""
     import torch
