@@ -742,9 +742,10 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
 // tile is given to both streams, which take its key tiles in turn and are joined through tensor memory.
 // A chunk of 2048 tokens over 32K (32/8 heads, 64 of 1024 pages a row and head): 380 us, row by row 1530.  The rows of a tile
 // take 450 pages, seven times a row's, so the products are 0.48 TFLOP where the selection's own are 0.07; the tiles' kernel
-// does them in some 350 us, 1.38 PFLOP/s.  Bound by the MMA thread and the softmax in turn: a tile of 128 rows x 128 keys takes an
-// SM 1750 cycles, 1024 of them the pipe's; 2.7 GB come through L2 (7.7 TB/s).  The union, and the time, shrink where
-// neighbouring rows take the same pages.
+// does them in some 350 us, 1.38 PFLOP/s.  Bound by the way of the pages into the SMs, 2.7 GB at 7.1 TB/s over the
+// whole of it (single rows reach 8.7; all loads from the same 256 KB make no more than 371 us of it), beside the MMA thread
+// and the softmax in turn: a tile of 128 rows x 128 keys takes an SM 1750 cycles, 1024 of them the pipe's.  The union, and the
+// time, shrink where neighbouring rows take the same pages.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kTileRows = 128, kTileKeys = 128;
