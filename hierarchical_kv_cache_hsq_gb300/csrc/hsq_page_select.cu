@@ -62,6 +62,17 @@ __device__ __forceinline__ uint32_t score_key(float dot, float scale) {
 
 constexpr int kBins = 256;
 
+// The tiles' keys are the score's bits, as whole numbers with a sign: what is not below 0 is in order as it stands (NaN on top), and
+// most rows take nothing else; for the others `ordered` puts all in order.  kNoKey stands for a page that cannot be selected (no
+// score is -0, a whole number times a scale being 0 or not below the scale).
+constexpr int kNoKey = (int)0x80000000;
+__device__ __forceinline__ int score_bits(float dot, float scale) { return __float_as_int(__fmaf_rn(dot, scale, 0.f)); }
+__device__ __forceinline__ int ordered(int v) { return v == kNoKey ? v : v ^ ((v >> 31) & 0x7FFFFFFF); }
+// The same bins as score_bin's, and bin 1 for no key, as the last byte of a word that starts with 0x4B0000.
+__device__ __forceinline__ uint32_t bits_bin(int v, float per) {
+    return __float_as_uint(fminf(fmaxf(fmaf(__int_as_float(v), per, 8388609.f), 8388609.f), 8388608.f + (kBins - 1)));
+}
+
 // The bin of a key where the largest, `most`, has a positive score: bins 1 .. 255 of equal width in the score from 0 to the largest
 // (what lies below goes to bin 1), rounded to a whole number in the last bits of 2^23 + it, which takes no conversion; 0 for no key.
 // Monotone in the key.  (A product that is no number, of an infinite largest score or one whose 254th part is past fp32's range, goes to
@@ -105,12 +116,13 @@ __device__ __forceinline__ int locate_bin(const int* hist, int& need, int& in_bi
 }
 
 // By a warp: the need-th of up to 32 candidates from the top, and how many of those equal to it are to be taken (all: 1 << 30).
-__device__ __forceinline__ uint32_t rank_candidates(const uint32_t* cand, int count, int need, int& ties) {
+template <class T>
+__device__ __forceinline__ T rank_candidates(const T* cand, int count, int need, int& ties) {
     const int lane = threadIdx.x & 31;
-    const uint32_t x = lane < count ? cand[lane] : 0u;
+    const T x = lane < count ? cand[lane] : T(0);
     int gt = 0, eq = 0;
     for (int i = 0; i < count; ++i) {
-        const uint32_t y = __shfl_sync(kFull, x, i);
+        const T y = __shfl_sync(kFull, x, i);
         gt += y > x;
         eq += y == x;
     }
@@ -385,8 +397,8 @@ static_assert(64 * kRowThreads >= HSQ_MAX_SELECT_PAGES, "the keys fit the regist
 //   registers) x 8 pages (B).  The dims are taken in an order that gives a lane 16 neighbouring bytes of a page's codes twice.
 //   Selection by a warp a row: a histogram of the row's keys, the ranks of those in the bin that holds the last to be
 //   taken, and the taken ones in order from masks of 32 neighbours a lane.
-// 2048 rows x 8 heads over 1024 pages, 64 taken: 67 us (with a CTA a row 375).  Bound by issue slots (61 %) and the latency of
-// the codes' loads: with one page taken it is still 62 us, which are the lookups and the scores.
+// 2048 rows x 8 heads over 1024 pages, 64 taken: 64 us (with a CTA a row 375; with the keys in order from the start 67).  Bound by
+// issue slots (60 %) and the latency of the codes' loads; with one page taken it is 4 us less.
 // ---------------------------------------------------------------------------------------
 
 constexpr int kTileThreads = 512, kTileRow = kTileThreads / 32, kChunk = 1024;
@@ -411,16 +423,16 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
 }
 
 __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(const __grid_constant__ SelectArgs a) {
-    extern __shared__ uint32_t s_dyn[];
-    uint32_t* s_key = s_dyn;                                // [16][kPitch] the chunk's keys
+    extern __shared__ int s_dyn[];
+    int* s_key = s_dyn;                                     // [16][kPitch] the chunk's keys
     const int beta = a.top - a.first - a.recent;
-    uint32_t* s_best = s_key + kTileRow * kPitch;           // [16][beta] the best so far, in the pages' order: key,
-    int* s_page = reinterpret_cast<int*>(s_best + kTileRow * max(beta, 0));  // page
+    int* s_best = s_key + kTileRow * kPitch;                // [16][beta] the best so far, in the pages' order: key,
+    int* s_page = s_best + kTileRow * max(beta, 0);         // page
     __shared__ uint32_t s_q[kTileRow][32];
     __shared__ alignas(16) int s_id[kChunk];
     __shared__ alignas(16) float s_scale[kChunk];
     __shared__ alignas(16) int s_hist[kTileThreads / 32][kBins + 4];  // (and the number of candidates)
-    __shared__ uint32_t s_cand[kTileThreads / 32][32];
+    __shared__ int s_cand[kTileThreads / 32][32];
     __shared__ int s_scan[kTileThreads / 32];
     __shared__ int s_at[5];   // request, first row, rows, rows before it in the request's own count, own tokens held
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -523,38 +535,38 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                     const int col = p0 + u * (kTileThreads / 4) + 2 * t;
                     if (col >= c1 - c0) continue;
                     const float2 sc = *reinterpret_cast<const float2*>(s_scale + col);  // (columns behind the last page are not looked at)
-                    uint32_t* to = s_key + g * kPitch + col + 2 * (col >> 5);
-                    *reinterpret_cast<uint2*>(to) = make_uint2(score_key(d[u][0], sc.x), score_key(d[u][1], sc.y));
-                    *reinterpret_cast<uint2*>(to + 8 * kPitch) = make_uint2(score_key(d[u][2], sc.x), score_key(d[u][3], sc.y));
+                    int* to = s_key + g * kPitch + col + 2 * (col >> 5);
+                    *reinterpret_cast<int2*>(to) = make_int2(score_bits(d[u][0], sc.x), score_bits(d[u][1], sc.y));
+                    *reinterpret_cast<int2*>(to + 8 * kPitch) = make_int2(score_bits(d[u][2], sc.x), score_bits(d[u][3], sc.y));
                 }
             }
             __syncthreads();
             if (gone) {
                 for (int i = lane; i < c1 - c0; i += 32)
-                    if (s_id[i] < 0) s_key[warp * kPitch + i + 2 * (i >> 5)] = 0u;
+                    if (s_id[i] < 0) s_key[warp * kPitch + i + 2 * (i >> 5)] = kNoKey;
                 __syncwarp();
             }
             const int j = warp, c = j < rows ? pages_of(j) : 0;
             if (c > a.top) {
                 const int G = min(c - a.recent, c1) - c0;  // keys of the chunk that count for the row
-                uint32_t* best = s_best + j * beta;
+                int* best = s_best + j * beta;
                 int* page = s_page + j * beta;
-                uint32_t* row_keys = s_key + j * kPitch;
-                const uint32_t* mine = row_keys + lane * kLanePitch;  // the lane's 32
+                int* row_keys = s_key + j * kPitch;
+                int* mine = row_keys + lane * kLanePitch;  // the lane's 32
                 const int nb = have, used = (nb + 31) >> 5;
-                for (int i = max(G, 0) + lane; i < kChunk; i += 32) row_keys[i + 2 * (i >> 5)] = 0u;
+                for (int i = max(G, 0) + lane; i < kChunk; i += 32) row_keys[i + 2 * (i >> 5)] = kNoKey;
                 __syncwarp();
                 // every key: the chunk's, then the best so far
                 auto each = [&](auto&& f) {
 #pragma unroll 1
                     for (int i = 0; i < 32; ++i) f(mine[i]);
 #pragma unroll 1
-                    for (int i = 0; i < used; ++i) f(32 * i + lane < nb ? best[32 * i + lane] : 0u);
+                    for (int i = 0; i < used; ++i) f(32 * i + lane < nb ? best[32 * i + lane] : kNoKey);
                 };
                 // The key lo above which fewer than beta keys lie, at or above which beta or more (or all there are).  A histogram
                 // of the keys tells the bin that holds the beta-th; up to 32 keys in it are ranked one against the other, of more
                 // the histogram is taken again over the bin.
-                uint32_t lo = 1;
+                int lo = kNoKey + 1;
                 int ties = 1 << 30;  // of the keys equal to lo, those to be taken (all)
                 int need = beta;     // of the keys in play
                 int* hist = s_hist[warp];
@@ -572,39 +584,37 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                     __syncwarp();
                     lo = rank_candidates(s_cand[warp], in_bin, need, ties);
                 };
-                auto keep = [&](uint32_t v) { s_cand[warp][atomicAdd(hist + kBins, 1)] = v; };
-                // First by the score.  The bins of a lane's keys stay in registers, four to a word, for the second look.
-                uint32_t most = 0;
+                auto keep = [&](int v) { s_cand[warp][atomicAdd(hist + kBins, 1)] = v; };
+                // First by the score, for rows that take scores above 0 alone.  The bins of a lane's keys stay in registers, four to
+                // a word, for the second look.
+                int most = kNoKey;
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(mine + i);
+                    const int2 v = *reinterpret_cast<const int2*>(mine + i);
                     most = max(most, max(v.x, v.y));
                 }
 #pragma unroll 1
-                for (int i = 0; i < used; ++i) most = max(most, 32 * i + lane < nb ? best[32 * i + lane] : 0u);
+                for (int i = 0; i < used; ++i) most = max(most, 32 * i + lane < nb ? best[32 * i + lane] : kNoKey);
                 most = __reduce_max_sync(kFull, most);
-                const float per = 254.f / key_to_float(most);
-                auto bin_of = [&](uint32_t v) { return score_bin(v, per); };
-                const bool by_score = key_to_float(most) > 0.f;  // (not where the largest is NaN)
-                uint32_t bins[kChunk / 128];
-                clear();
-#pragma unroll
-                for (int w = 0; w < kChunk / 128; ++w) {
-                    const uint2 v0 = *reinterpret_cast<const uint2*>(mine + 4 * w), v1 = *reinterpret_cast<const uint2*>(mine + 4 * w + 2);
-                    const int x[4] = {bin_of(v0.x), bin_of(v0.y), bin_of(v1.x), bin_of(v1.y)};
-                    bins[w] = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        atomicAdd(hist + x[i], 1);
-                        bins[w] |= (uint32_t)x[i] << (8 * i);
-                    }
-                }
-#pragma unroll 1
-                for (int i = 0; i < used; ++i) atomicAdd(hist + bin_of(32 * i + lane < nb ? best[32 * i + lane] : 0u), 1);
+                bool found = false;
                 int in_bin = 0;
-                const int bin = locate(in_bin);
-                if (bin >= 0) {  // (else all are taken)
-                    if (by_score && in_bin <= 32) {
+                if (most > 0 && most <= 0x7F800000) {  // (else the largest is no number, or none is above 0)
+                    const float per = 254.f / __int_as_float(most);
+                    uint32_t bins[kChunk / 128];
+                    clear();
+#pragma unroll
+                    for (int w = 0; w < kChunk / 128; ++w) {
+                        const int2 v0 = *reinterpret_cast<const int2*>(mine + 4 * w), v1 = *reinterpret_cast<const int2*>(mine + 4 * w + 2);
+                        const uint32_t x[4] = {bits_bin(v0.x, per), bits_bin(v0.y, per), bits_bin(v1.x, per), bits_bin(v1.y, per)};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) atomicAdd(hist + (x[i] & 0xFFu), 1);
+                        bins[w] = __byte_perm(__byte_perm(x[0], x[1], 0x0040), __byte_perm(x[2], x[3], 0x0040), 0x5410);
+                    }
+#pragma unroll 1
+                    for (int i = 0; i < used; ++i)
+                        if (32 * i + lane < nb) atomicAdd(hist + (bits_bin(best[32 * i + lane], per) & 0xFFu), 1);
+                    const int bin = locate(in_bin);
+                    if (bin > 1 && in_bin <= 32) {
                         const uint32_t four = 0x01010101u * (uint32_t)bin;
 #pragma unroll
                         for (int w = 0; w < kChunk / 128; ++w) {
@@ -617,50 +627,56 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                         }
 #pragma unroll 1
                         for (int i = 0; i < used; ++i) {
-                            const uint32_t v = 32 * i + lane < nb ? best[32 * i + lane] : 0u;
-                            if (bin_of(v) == bin) keep(v);
+                            const int v = 32 * i + lane < nb ? best[32 * i + lane] : kNoKey;
+                            if (v != kNoKey && (int)(bits_bin(v, per) & 0xFFu) == bin) keep(v);
                         }
                         rank(in_bin);
-                    } else {
-                        // crowded: by the keys' bits, over the bin or over all keys
-                        uint32_t klo = ~0u, khi = 0;
-                        if (!by_score) need = beta;
-                        each([&](uint32_t v) {
-                            if (v != 0u && (!by_score || bin_of(v) == bin)) {
-                                klo = min(klo, v);
-                                khi = max(khi, v);
+                        found = true;
+                    }
+                }
+                if (!found) {
+                    // Crowded, or scores not above 0: in order, by the keys' bits.
+                    need = beta;
+                    int klo = 0x7FFFFFFF, khi = kNoKey, there = 0;
+#pragma unroll 1
+                    for (int i = 0; i < 32; ++i) mine[i] = ordered(mine[i]);
+                    each([&](int v) {
+                        if (v != kNoKey) {
+                            klo = min(klo, v);
+                            khi = max(khi, v);
+                            ++there;
+                        }
+                    });
+                    there = __reduce_add_sync(kFull, there);
+                    while (there >= beta) {  // (else all are taken)
+                        klo = __reduce_min_sync(kFull, klo);
+                        khi = __reduce_max_sync(kFull, khi);
+                        // (the number to be taken is at most the number in play)
+                        const int shift = max(32 - __clz((uint32_t)khi - (uint32_t)klo) - 7, 0);  // 128 bins, from 1 on
+                        clear();
+                        each([&](int v) {
+                            if (v != kNoKey && v >= klo && v <= khi) atomicAdd(hist + 1 + (((uint32_t)v - (uint32_t)klo) >> shift), 1);
+                        });
+                        const int which = locate(in_bin);
+                        int l = 0x7FFFFFFF, u = kNoKey;
+                        const bool few = in_bin <= 32;
+                        each([&](int v) {
+                            if (v != kNoKey && v >= klo && v <= khi && 1 + (int)(((uint32_t)v - (uint32_t)klo) >> shift) == which) {
+                                if (few) keep(v);
+                                l = min(l, v);
+                                u = max(u, v);
                             }
                         });
-                        while (true) {
-                            klo = __reduce_min_sync(kFull, klo);
-                            khi = __reduce_max_sync(kFull, khi);
-                            // (the number to be taken is at most the number in play)
-                            const int shift = max(32 - __clz(khi - klo) - 7, 0);  // 128 bins, from 1 on
-                            clear();
-                            each([&](uint32_t v) {
-                                if (v >= klo && v <= khi) atomicAdd(hist + 1 + ((v - klo) >> shift), 1);
-                            });
-                            const int which = locate(in_bin);
-                            uint32_t l = ~0u, u = 0;
-                            const bool few = in_bin <= 32;
-                            each([&](uint32_t v) {
-                                if (v >= klo && v <= khi && 1 + (int)((v - klo) >> shift) == which) {
-                                    if (few) keep(v);
-                                    l = min(l, v);
-                                    u = max(u, v);
-                                }
-                            });
-                            if (few) {
-                                rank(in_bin);
-                                break;
-                            }
-                            klo = __reduce_min_sync(kFull, l);
-                            khi = __reduce_max_sync(kFull, u);
-                            if (klo == khi) {  // one key over and over
-                                lo = klo;
-                                if (in_bin > need) ties = need;
-                                break;
-                            }
+                        if (few) {
+                            rank(in_bin);
+                            break;
+                        }
+                        klo = __reduce_min_sync(kFull, l);
+                        khi = __reduce_max_sync(kFull, u);
+                        if (klo == khi) {  // one key over and over
+                            lo = klo;
+                            if (in_bin > need) ties = need;
+                            break;
                         }
                     }
                 }
@@ -670,7 +686,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
 #pragma unroll 1
                 for (int i = 0; i < used; ++i) {
                     const int at = 32 * i + lane;
-                    const uint32_t key = at < nb ? best[at] : 0u;
+                    const int key = at < nb ? best[at] : kNoKey;
                     const int pg = at < nb ? page[at] : 0;
                     __syncwarp();
                     const unsigned be = __ballot_sync(kFull, key == lo);
@@ -687,7 +703,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                 uint32_t in = 0;  // of the lane's 32
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(mine + i);
+                    const int2 v = *reinterpret_cast<const int2*>(mine + i);
                     in |= (v.x >= lo ? 1u << i : 0u) | (v.y >= lo ? 2u << i : 0u);
                 }
                 if (ties != 1 << 30) {  // only so many of those equal to lo
