@@ -564,8 +564,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) page_select_tiles_kernel(cons
                     for (int i = 0; i < used; ++i) f(32 * i + lane < nb ? best[32 * i + lane] : kNoKey);
                 };
                 // The key lo above which fewer than beta keys lie, at or above which beta or more (or all there are).  A histogram
-                // of the keys tells the bin that holds the beta-th; up to 32 keys in it are ranked one against the other, of more
-                // the histogram is taken again over the bin.
+                // of the scores tells the bin that holds the beta-th; up to 32 keys in it are ranked one against the other.  Where
+                // more share it, or scores not above 0 are taken, histograms of the keys' bits lead there, each over a bin of the last.
                 int lo = kNoKey + 1;
                 int ties = 1 << 30;  // of the keys equal to lo, those to be taken (all)
                 int need = beta;     // of the keys in play
