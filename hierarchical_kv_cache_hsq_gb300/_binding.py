@@ -625,7 +625,7 @@ def _stream_on(pool: PagePool, stream) -> int:
     """The given stream's handle, or the current one's; the pool has to be on the current device (as the
     library holds the context to it)."""
     import torch
-    if torch._C._cuda_getDevice() != pool.index:
+    if torch.cuda.current_device() != pool.index:
         raise ValueError("the pool is not on the current device")
     # (the handle alone, as torch's own launchers take it: 0.1 us, through a Stream object 2.8 of a call's 9)
     return torch._C._cuda_getCurrentRawStream(pool.index) if stream is None else stream.cuda_stream
