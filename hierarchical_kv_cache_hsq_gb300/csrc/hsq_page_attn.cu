@@ -742,8 +742,8 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
 // tile is given to both streams, which take its key tiles in turn and are joined through tensor memory.
 // A chunk of 2048 tokens over 32K (32/8 heads, 64 of 1024 pages a row and head): 380 us, row by row 1530.  The rows of a tile
 // take 450 pages, seven times a row's, so the products are 0.48 TFLOP where the selection's own are 0.07; the tiles' kernel
-// does them in some 350 us, 1.38 PFLOP/s.  Bound by the way of the pages into the SMs, 2.7 GB at 7.1 TB/s over the
-// whole of it (single rows reach 8.7; all loads from the same 256 KB make no more than 371 us of it), beside the MMA thread
+// does them in 346 us, 1.40 PFLOP/s.  Bound by the way of the pages into the SMs, 2.7 GB at 7.8 TB/s
+// (single rows reach 8.7; with all loads from the same 256 KB the call takes 371 us), beside the MMA thread
 // and the softmax in turn: a tile of 128 rows x 128 keys takes an SM 1750 cycles, 1024 of them the pipe's.  The union, and the
 // time, shrink where neighbouring rows take the same pages.
 // ---------------------------------------------------------------------------------------
