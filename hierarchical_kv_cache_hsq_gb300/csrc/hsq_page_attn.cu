@@ -1647,7 +1647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         float lo, hi;
                         unpack2(add2(l2[0], l2[1]), lo, hi);
                         t = lo + hi;
-                        if (look || !__any_sync(kFull, !(t < kTileSum))) break;
+                        if (look || !__any_sync(kFull, live && !(t < kTileSum))) break;  // (rows of no token hold anything)
                         look = true;
                     }
                     tmem_st32_nowait(tS, p[0]);

@@ -1,0 +1,55 @@
+"""What one row of the attention over selected pages holds, or one of its pages, is nothing to the others: rows of no
+token, and keys that are no numbers."""
+
+import numpy as np
+import pytest
+
+from hsq_harness import ensure_built
+from test_gpu_paged import attn_inputs, make
+from test_gpu_selection import check_page_attn, run_page_attn, some_selection
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+# the last tile's rows, its first warp's among them, are not all of a token: 70 tokens are two tiles of 32 and 6 of a third
+@pytest.mark.parametrize("Hq,Hkv,page,new", [(8, 2, 16, 70), (8, 2, 64, 34), (16, 2, 16, 17), (5, 1, 32, 55), (2, 2, 128, 135)])
+@pytest.mark.parametrize("rest", [float("nan"), float("inf"), 2.0e4])
+def test_rows_behind_a_request_change_nothing(Hq, Hkv, page, new, rest):
+    """A tile's load of queries goes on behind its request's last row, into padding or another request."""
+    x = attn_inputs(Hq, Hkv, page, 0, [1500, 300], [new, 1], pad=40, seed=new)
+    sel = some_selection(x, page, 1500 // page, seed=new)
+    q = x["q"].clone()
+    q[new:] = 0.0
+    want, lse = run_page_attn(dict(x, q=q), sel)[:2]
+    q = q.clone()
+    q[new:] = rest
+    x["q"] = q
+    got, glse, err = run_page_attn(x, sel)
+    assert not err
+    np.testing.assert_array_equal(got[:new], want[:new])
+    np.testing.assert_array_equal(glse[:new], lse[:new])
+    assert (got[new + 1:] == 7.0).all()
+
+
+@pytest.mark.parametrize("new", [50, 333])
+def test_what_an_earlier_call_left_in_shared_memory_changes_nothing(new):
+    """With 5 heads a KV head a tile has 125 rows: the places of the other three are whatever a call of 4 heads, whose tiles
+    have 128, left there."""
+    y = attn_inputs(4, 1, 16, 0, [2000] * 8, [1500] * 8, seed=1)
+    ysel = some_selection(y, 16, 3, seed=2)
+    x = attn_inputs(5, 1, 16, 0, [1500] * 8, [new] * 8, seed=3)
+    sel = some_selection(x, 16, 90, seed=4)
+    got = []
+    for rest in (0.0, float("nan"), float("inf"), -3.0e38):
+        y["q"] = y["q"].clone().fill_(rest)
+        run_page_attn(y, ysel)
+        got.append(run_page_attn(x, sel)[:2])
+    for out, lse in got[1:]:
+        np.testing.assert_array_equal(out, got[0][0])
+        np.testing.assert_array_equal(lse, got[0][1])
+    check_page_attn(x, sel, *got[0])
