@@ -733,7 +733,8 @@ hsq_status hsq_page_select(hsq_ctx* ctx, const hsq_pages* pages, const hsq_summa
  *   left out (HSQ_DEVERR_SEL), so no token counts twice.  top <= HSQ_MAX_BETA, np + width <= HSQ_MAX_SELECT_PAGES.
  *   HSQ_DEVERR_PAGE: a page id outside the pool (its tokens are not attended to).  HSQ_DEVERR_LEN as for
  *   hsq_page_select.  HSQ_DEVERR_WAIT: a bounded wait ran out, the results of the call are undefined.  Keys and values
- *   (a value that is not finite may reach every row of a request of which one takes its page),
+ *   (a value that is not finite may reach every row of a request of which one takes its page; a key that is not, or whose
+ *   logit is not, the rows alone that take its page),
  *   roundings, the other arguments, the workspace's use and the errors: as for hsq_shared_attn.
  */
 hsq_status hsq_page_attn_workspace_size(const hsq_ctx* ctx, int page_n, int rows, int B, int width, int prefix_len,

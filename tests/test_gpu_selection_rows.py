@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from hsq_harness import ensure_built
-from test_gpu_paged import attn_inputs, make
+from test_gpu_paged import attn_inputs
 from test_gpu_selection import check_page_attn, run_page_attn, some_selection
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +53,37 @@ def test_what_an_earlier_call_left_in_shared_memory_changes_nothing(new):
         np.testing.assert_array_equal(out, got[0][0])
         np.testing.assert_array_equal(lse, got[0][1])
     check_page_attn(x, sel, *got[0])
+
+
+@pytest.mark.parametrize("new", [1, 4, 60, 333])
+@pytest.mark.parametrize("Hq,Hkv,page", [(8, 2, 16), (5, 1, 32), (2, 2, 64), (16, 2, 128)])
+@pytest.mark.parametrize("key", [float("nan"), float("inf"), -3.3e38])
+def test_a_key_that_gives_no_numbers_shows_in_the_rows_that_take_its_page_alone(new, Hq, Hkv, page, key):
+    """Neighbouring rows share a tile and its products, but a page that a row does not take is not there for it.  (-3.3e38: its
+    logits pass fp32's range.)"""
+    x = attn_inputs(Hq, Hkv, page, 3 * page, [40 * page] * 2, [new] * 2, pad=3, seed=new + page)
+    rng = np.random.default_rng(new)
+    rows, top, r = 2 * new, 12, Hq // Hkv
+    whole = 43 - -(-new // page) - 1  # pages that every row sees all of
+    sel = np.full((rows + 3, Hkv, top), -1, np.int32)
+    for i in range(rows):
+        for h in range(Hkv):
+            n = int(rng.integers(1, top - 1))
+            sel[i, h, :n] = np.sort(rng.permutation(whole - 2)[:n])
+    # one row alone takes page whole - 1, and some take page 2, of the prefix
+    sel[int(rng.integers(0, new)), 0, top - 1] = whole - 1
+    k = x["k"].clone()
+    k[int(x["table"][0][whole - 4]), 0, page // 2] = key
+    k[int(x["prefix"][2]), Hkv - 1, 1] = key
+    out, lse, err = run_page_attn(dict(x, k=k), sel)
+    assert not err
+    takers = np.zeros((rows + 3, Hq), bool)
+    takers[:new, :r] |= (sel[:new, 0] == whole - 1).any(-1)[:, None]
+    takers[:, (Hkv - 1) * r:] |= (sel[:, Hkv - 1] == 2).any(-1)[:, None]
+    assert takers.any() and (new == 1 or not takers[:rows].all())
+    if np.isnan(key):
+        assert np.isnan(out[takers]).all() and np.isnan(lse[takers]).all()
+    assert np.isfinite(out[:rows][~takers[:rows]]).all()
+    # the others: the oracle's bounds with any other key there
+    quiet = (np.arange(rows + 3) < rows) & ~takers.any(1)
+    check_page_attn(x, sel, np.where(quiet[:, None, None], out, 7.0), np.where(quiet[:, None], lse, 7.0), quiet)
