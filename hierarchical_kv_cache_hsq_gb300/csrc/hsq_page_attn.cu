@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsRow)
             head[1] = ro.live;
         }
     }
-    if (blockIdx.x == 0) bad |= offsets_bad(a.q_start, a.B, a.rows, kThreadsRow);
+    if (blockIdx.x == 0) bad |= requests_bad(a.q_start, a.lens, a.B, a.rows, a.width << a.page_shift, kThreadsRow);
     __syncthreads();
     const int listed = head[0];
     const bool live = head[1];
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
         fence_async_smem();  // (the words' memory takes copies from here on)
         __syncthreads();
     }
-    if (blockIdx.x == 0) bad |= offsets_bad(a.q_start, a.B, a.rows, kThreads);
+    if (blockIdx.x == 0) bad |= requests_bad(a.q_start, a.lens, a.B, a.rows, a.width << a.page_shift, kThreads);
 
     // the warp's groups [s0, s1) of 16 keys, of the CTA's
     const int groups = here << sub_shift, s0 = groups * stream / kWarps, s1 = groups * (stream + 1) / kWarps;

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kRowThreads, K <= 16 ? 2 : 1) page_select_rows
     } else if (warp == 1) {
         s_q[lane] = query_codes(a.q + ((size_t)row * a.Hq + h * a.r) * 128, a.r);
     }
-    if (blockIdx.x == 0) bad |= offsets_bad(a.q_start, a.B, a.rows, kRowThreads);
+    if (blockIdx.x == 0) bad |= requests_bad(a.q_start, a.lens, a.B, a.rows, a.width << a.page_shift, kRowThreads);
     __syncthreads();
     asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");  // every CTA of the cluster runs: remote stores may start
     const bool live = s_row[2];

@@ -138,12 +138,13 @@ __device__ __forceinline__ RowOf warp_row(const int32_t* q_start, const int32_t*
     return r;
 }
 
-// Whether the offsets ascend in [0, rows], by a whole CTA of `threads`; what does not is flagged.
-__device__ __forceinline__ int offsets_bad(const int32_t* q_start, int B, int rows, int threads) {
+// Whether the offsets ascend in [0, rows] and the lengths are none below 0, past their table or below the request's rows, by a
+// whole CTA of `threads`; what is not so is flagged.  (A request without rows has no CTA that would look at its length.)
+__device__ __forceinline__ int requests_bad(const int32_t* q_start, const int32_t* lens, int B, int rows, int held_most, int threads) {
     int bad = 0;
     for (int b = threadIdx.x; b < B; b += threads) {
-        const int s = q_start[b], e = q_start[b + 1];
-        if (s < 0 || e < s || e > rows) bad = HSQ_DEVERR_LEN;
+        const int s = q_start[b], e = q_start[b + 1], l = lens[b];
+        if (s < 0 || e < s || e > rows || l < 0 || l > held_most || l < e - s) bad = HSQ_DEVERR_LEN;
     }
     return bad;
 }

@@ -6,7 +6,8 @@ import pytest
 
 from hsq_harness import ensure_built
 from test_gpu_paged import attn_inputs
-from test_gpu_selection import check_page_attn, run_page_attn, some_selection
+from test_gpu_selection import (check_page_attn, run_page_attn, run_select, selection_inputs, some_selection,
+                                want_select)
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,22 @@ def test_a_key_that_gives_no_numbers_shows_in_the_rows_that_take_its_page_alone(
     # the others: the oracle's bounds with any other key there
     quiet = (np.arange(rows + 3) < rows) & ~takers.any(1)
     check_page_attn(x, sel, np.where(quiet[:, None, None], out, 7.0), np.where(quiet[:, None], lse, 7.0), quiet)
+
+
+@pytest.mark.parametrize("most", [1, 5, 40])
+@pytest.mark.parametrize("length", [-1, 10 ** 6])
+def test_the_length_of_a_request_without_rows_is_looked_at_too(most, length):
+    x = selection_inputs(8, 2, 16, 40, [200, 100, 90], [most, 0, most], 5, seed=most)
+    sel, err = run_select(x)
+    assert not err
+    out, lse, err = run_page_attn(x, sel)
+    assert not err
+    x["lens"][1] = length
+    sel2, err = run_select(x)
+    assert err == {"LEN"}
+    np.testing.assert_array_equal(sel2, sel)
+    np.testing.assert_array_equal(sel, want_select(x)[0])
+    out2, lse2, err = run_page_attn(x, sel)
+    assert err == {"LEN"}
+    np.testing.assert_array_equal(out2, out)
+    np.testing.assert_array_equal(lse2, lse)
