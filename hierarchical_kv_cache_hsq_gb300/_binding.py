@@ -766,7 +766,8 @@ def hsq_shared_attn(ctx: Context, pool: PagePool, q, q_start, lens, table, out, 
 
 def hsq_page_summaries(ctx: Context, pool: PagePool, sums: PageSummaries, slots, stream=None):
     """Summaries of the pages that slots (int64 [rows], hsq_page_tables's) name, over the tokens that they hold once the
-    step's keys are written (hsq_page_write first); the other pages' are left as they were."""
+    step's keys are written (hsq_page_write first); the other pages' are left as they were.  The rows of a page lie side by
+    side: the summary of one that is named in two places apart may be a mix of two."""
     import torch
     _need_heads(ctx, pool)
     _need_summaries(pool, sums)

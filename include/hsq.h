@@ -681,7 +681,8 @@ hsq_status hsq_page_write_rope(hsq_ctx* ctx, const hsq_pages* pages, const hsq_r
  *   slots: [rows] int64 as hsq_page_tables gives them: the rows of a page side by side and ascending, tokens before
  *   them there already.  A page's last row i of the step (slots[i + 1] lies on another page, is negative or past
  *   the end) makes its summary of tokens 0 .. slots[i] mod page_n.  Negative slots are skipped; the other pages'
- *   summaries are left as they were.  A page that the step names in two places apart gets one of the two.
+ *   summaries are left as they were.  A page that the step names in two places apart (with rows of other pages, or a negative
+ *   slot, between) has two last rows, and its codes and scale may be of one summary, of the other or some of each.
  *   A page whose max|S| is below 2^-64 gets codes and scale 0; one whose is not a number, above 2^126 or past
  *   fp32's range on the way codes 0 and scale inf: such a page is selected before all others (see below), so that
  *   it shows in the result.

@@ -5,9 +5,10 @@ import numpy as np
 import pytest
 
 from hsq_harness import ensure_built
-from test_gpu_paged import attn_inputs
-from test_gpu_selection import (check_page_attn, run_page_attn, run_select, selection_inputs, some_selection,
-                                want_select)
+from oracle import paged as P
+from test_gpu_paged import attn_inputs, host, i64, make
+from test_gpu_selection import (check_page_attn, check_summaries, run_page_attn, run_select, selection_inputs, some_selection,
+                                want_select, word)
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +108,27 @@ def test_the_length_of_a_request_without_rows_is_looked_at_too(most, length):
     assert err == {"LEN"}
     np.testing.assert_array_equal(out2, out)
     np.testing.assert_array_equal(lse2, lse)
+
+
+@pytest.mark.parametrize("repeat", [1, 400])
+def test_a_page_that_a_step_names_in_two_places_gets_codes_of_the_two(repeat):
+    """Its codes and scale may be of either (of a row before a negative slot, and of a later one); the others are as ever."""
+    import torch
+    import hierarchical_kv_cache_hsq_gb300 as H
+    rng = np.random.default_rng(repeat)
+    Hkv, n = 8, 3 * repeat
+    pool = H.PagePool(*[torch.from_numpy(rng.standard_normal((n, Hkv, 16, 128)).astype(np.float32)).cuda().bfloat16()] * 2)
+    slots = np.concatenate([[48 * i + 3, -1, 48 * i + 5, 48 * i + 31, 48 * i + 9, 48 * i + 40] for i in range(repeat)])
+    ctx, none = make(Hkv, Hkv, 1), (np.zeros((n, Hkv, 128), np.int8), np.zeros((n, Hkv), np.float32))
+    sums = H.allocate_summaries(ctx, pool)
+    H.hsq_page_summaries(ctx, pool, sums, i64(slots))
+    assert word(ctx) == set()
+    codes, scale = sums.codes.cpu().numpy(), host(sums.scale)
+    k, apart = host(pool.k), np.arange(0, n, 3)
+    ways = [P.page_summaries(k, 16 * apart + last, *none)[:2] for last in (3, 5, 9)]
+    assert np.logical_or.reduce([codes[apart] == c[apart] for c, _ in ways]).all()
+    near = [np.abs(scale[apart] - s[apart]) <= s[apart] * 2.0 ** -22 for _, s in ways]
+    assert np.logical_or.reduce(near).all()
+    rest = np.delete(np.arange(n), apart)
+    want = P.page_summaries(k, slots, *none)
+    check_summaries(codes[rest], scale[rest], want[0][rest], want[1][rest])
