@@ -35,7 +35,7 @@ BUFFERS = ["l1_kc", "l1_vc", "l1_kn", "l1_vn", "l1_pos", "l1_count", "l2_kc", "l
            "hot_rec", "hot_tag"]
 HSQ_NBUF = len(BUFFERS)
 CODECS = {"tq": 0, "plain": 1}  # hsq_codec
-ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "yarn_index": 4}
 
 
 class HSQError(RuntimeError):
@@ -216,8 +216,9 @@ def hsq_version() -> str:
 def hsq_rope_frequencies(dims: int = 128, theta: float = 1.0e6, scaling: str = "none", factor: float = 1.0,
                          original: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
     """(omega float64 [dims / 2], amplitude) of a rotation: scaling "none", "linear" (positions / factor), "base"
-    (theta factor^(dims / (dims - 2))) or "yarn" (from the frequencies that turn more than beta_fast times over the
-    `original` context, kept, to those below beta_slow, / factor; amplitude 0.1 ln(factor) + 1)."""
+    (theta factor^(dims / (dims - 2))), "yarn" (from the frequencies that turn more than beta_fast times over the
+    `original` context, kept, to those below beta_slow, / factor, by the number of turns as in the paper; amplitude 0.1
+    ln(factor) + 1) or "yarn_index" (the same by the pair's index between the two, as the models trained with it are mostly run)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {tuple(ROPE_SCALINGS)}")
     omega, amp = np.zeros(64, np.float64), _f64(0.0)

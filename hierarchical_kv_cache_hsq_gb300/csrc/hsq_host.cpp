@@ -277,13 +277,22 @@ hsq_status hsq_rope_frequencies(int scaling, int dims, double theta, double fact
                                 double beta_slow, double* omega, double* amplitude) {
     if (!omega || !amplitude || dims < 8 || dims > hsq::kDim || dims % 8) return HSQ_ERR_INVALID;
     if (!(theta > 0.0) || !std::isfinite(theta)) return HSQ_ERR_INVALID;
-    if (scaling < HSQ_ROPE_NONE || scaling > HSQ_ROPE_YARN) return HSQ_ERR_INVALID;
+    if (scaling < HSQ_ROPE_NONE || scaling > HSQ_ROPE_YARN_INDEX) return HSQ_ERR_INVALID;
+    const bool yarn = scaling == HSQ_ROPE_YARN || scaling == HSQ_ROPE_YARN_INDEX;
     if (scaling != HSQ_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return HSQ_ERR_INVALID;
-    if (scaling == HSQ_ROPE_YARN &&
+    if (yarn &&
         (!(original > 0.0) || !std::isfinite(original) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast - beta_slow)))
         return HSQ_ERR_INVALID;
+    if (scaling == HSQ_ROPE_YARN_INDEX && (!(theta > 1.0) || !(beta_slow > 0.0))) return HSQ_ERR_INVALID;
     const double base = scaling == HSQ_ROPE_BASE ? theta * std::pow(factor, dims / (dims - 2.0)) : theta;
     constexpr double kTurn = 6.283185307179586476925;
+    double from = 0.0, to = 0.0;  // HSQ_ROPE_YARN_INDEX: the pairs between which the ramp runs
+    if (scaling == HSQ_ROPE_YARN_INDEX) {
+        auto index_of = [&](double turns) { return dims * std::log(original / (kTurn * turns)) / (2.0 * std::log(theta)); };
+        from = std::min(std::max(std::floor(index_of(beta_fast)), 0.0), dims - 1.0);
+        to = std::min(std::max(std::ceil(index_of(beta_slow)), 0.0), dims - 1.0);
+        if (to == from) to += 0.001;
+    }
     for (int i = 0; i < dims / 2; ++i) {
         double w = std::pow(base, -2.0 * i / dims);
         if (scaling == HSQ_ROPE_LINEAR) w /= factor;
@@ -292,9 +301,13 @@ hsq_status hsq_rope_frequencies(int scaling, int dims, double theta, double fact
             const double keep = std::min(std::max((turns - beta_slow) / (beta_fast - beta_slow), 0.0), 1.0);
             w *= keep + (1.0 - keep) / factor;
         }
+        if (scaling == HSQ_ROPE_YARN_INDEX) {
+            const double keep = 1.0 - std::min(std::max((i - from) / (to - from), 0.0), 1.0);
+            w *= keep + (1.0 - keep) / factor;
+        }
         omega[i] = w;
     }
-    *amplitude = scaling == HSQ_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    *amplitude = yarn ? 0.1 * std::log(factor) + 1.0 : 1.0;
     return HSQ_OK;
 }
 

@@ -640,17 +640,22 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
  *     HSQ_ROPE_BASE    theta factor^(dims / (dims - 2)) in place of theta;
  *     HSQ_ROPE_YARN    omega_i (g + (1 - g) / factor), g = the number of turns over the original context,
  *                      original omega_i / (2 pi), taken from [beta_slow, beta_fast] to [0, 1] and clipped; amplitude
- *                      0.1 ln(factor) + 1.
+ *                      0.1 ln(factor) + 1: the paper's ramp, by turns;
+ *     HSQ_ROPE_YARN_INDEX  the same with the ramp by the pair's index, as the models trained with the method are mostly run:
+ *                      g = 1 - (i - a) / (b - a) clipped to [0, 1], with d(t) = dims ln(original / (2 pi t)) / (2 ln theta) the index at
+ *                      which t turns are made, a = floor(d(beta_fast)), b = ceil(d(beta_slow)), both brought into [0, dims - 1] (and b
+ *                      0.001 above a where they meet).  For 128 dims, theta 1e6, original 32768 and factor 4 sixteen of the 64 frequencies differ
+ *                      from HSQ_ROPE_YARN's, by up to a factor of 1.7: which of the two a model wants is the model's to say.
  *   Other schemes: compute omega and pass it to hsq_rope_table.  dims: a multiple of 8 in [8, 128].  original, beta_fast
- *   and beta_slow matter to HSQ_ROPE_YARN only.  Errors: HSQ_ERR_INVALID (NULL, dims, theta or factor not positive and
- *   finite, factor < 1, original not positive, beta_fast <= beta_slow).
+ *   and beta_slow matter to the last two only.  Errors: HSQ_ERR_INVALID (NULL, dims, theta or factor not positive and
+ *   finite, factor < 1, original not positive, beta_fast <= beta_slow; for HSQ_ROPE_YARN_INDEX theta <= 1 or beta_slow not positive).
  * hsq_rope_table (host) -- cos and sin of the angles that positions in [0, max_pos) are put together from, fp32 from
  *   64 bits: 256 + ceil(max_pos / 256) rows of `dims` floats (cos | sin; rows of amplitude cos(c omega), c < 256, then
  *   of cos(256 a omega)).  *floats gets their number; with table NULL nothing else happens.  max_pos in [1, 2^24].
  * hsq_rope -- a rotation for hsq_page_write_rope: the table in device memory, 16-byte aligned.  interleaved 0: pairs
  *   (i, i + dims / 2); 1: pairs (2 i, 2 i + 1).  Dims from `dims` on are left as they are.
  */
-enum { HSQ_ROPE_NONE = 0, HSQ_ROPE_LINEAR = 1, HSQ_ROPE_BASE = 2, HSQ_ROPE_YARN = 3 };
+enum { HSQ_ROPE_NONE = 0, HSQ_ROPE_LINEAR = 1, HSQ_ROPE_BASE = 2, HSQ_ROPE_YARN = 3, HSQ_ROPE_YARN_INDEX = 4 };
 
 typedef struct hsq_rope {
     const float* table;

@@ -127,6 +127,10 @@ def shared_attn(pages_k, pages_v, q, q_start, lens, table, prefix, prefix_len):
 def rope_frequencies(dims, theta, scaling="none", factor=1.0, original=0.0, beta_fast=32.0, beta_slow=1.0):
     """(omega [dims / 2], amplitude), one frequency at a time."""
     omega, amp = [], 1.0
+    if scaling == "yarn_index":
+        # the (real) index whose frequency theta^(-2 i / dims) makes t turns over the original context
+        first, last = (dims / 2 * (np.log(original / (2 * np.pi)) - np.log(t)) / np.log(theta) for t in (beta_fast, beta_slow))
+        first, last = (int(np.clip(x, 0, dims - 1)) for x in (np.floor(first), np.ceil(last)))
     for i in range(dims // 2):
         base = theta * factor ** (dims / (dims - 2)) if scaling == "base" else theta
         w = base ** (-2 * i / dims)
@@ -140,8 +144,14 @@ def rope_frequencies(dims, theta, scaling="none", factor=1.0, original=0.0, beta
             elif turns < beta_fast:
                 g = (turns - beta_slow) / (beta_fast - beta_slow)
                 w = (1 - g) * w / factor + g * w
+        elif scaling == "yarn_index":
+            if i >= last and (last > first or i > first):
+                w = w / factor
+            elif i > first:
+                g = (i - first) / (last - first)
+                w = g * w / factor + (1 - g) * w
         omega.append(w)
-    if scaling == "yarn":
+    if scaling in ("yarn", "yarn_index"):
         amp = 0.1 * np.log(factor) + 1
     return np.array(omega), amp
 
