@@ -569,17 +569,22 @@ class Rope:
         return self._c.dims
 
 
-def make_rope(ctx: Context, dims: int = 128, interleaved: bool = False, theta: Optional[float] = None,
+def make_rope(ctx: Context, dims: Optional[int] = None, interleaved: bool = False, theta: Optional[float] = None,
               scaling: str = "none", factor: float = 1.0, original: float = 0.0, beta_fast: float = 32.0,
               beta_slow: float = 1.0, omega=None, amplitude: Optional[float] = None, max_pos: Optional[int] = None,
               device=None) -> Rope:
-    """A rotation by hsq_rope_frequencies (theta and max_pos: the context's unless given), or by a model's own
-    frequencies omega [dims / 2]; amplitude: the scaling's unless given."""
+    """A rotation by hsq_rope_frequencies (dims 128 unless given, theta and max_pos the context's; amplitude: the scaling's
+    unless given), or by a model's own frequencies omega [dims / 2].  omega stands for what a scaling would make of theta: it
+    goes with none of theta, scaling, factor, original and the betas, and its amplitude is 1 unless given."""
     import torch
     if omega is None:
-        omega, amp = hsq_rope_frequencies(dims, ctx.cfg.rope_theta if theta is None else theta, scaling, factor, original,
-                                          beta_fast, beta_slow)
+        omega, amp = hsq_rope_frequencies(128 if dims is None else dims, ctx.cfg.rope_theta if theta is None else theta,
+                                          scaling, factor, original, beta_fast, beta_slow)
     else:
+        if theta is not None or (scaling, factor, original, beta_fast, beta_slow) != ("none", 1.0, 0.0, 32.0, 1.0):
+            raise ValueError("omega goes with no theta, scaling, factor, original or betas (amplitude: pass it)")
+        if dims is not None and dims != 2 * len(omega):
+            raise ValueError("omega must be [dims / 2]")
         amp = 1.0
     max_pos = ctx.cfg.max_pos if max_pos is None else max_pos
     table = hsq_rope_table(omega, amp if amplitude is None else amplitude, max_pos)

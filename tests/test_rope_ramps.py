@@ -1,5 +1,5 @@
 """YaRN's ramp by the pair's index: against the oracle, numbers worked out by hand with 40 digits, and the ramp by turns;
-the rotation that it makes, on the GPU."""
+the rotation that it makes, on the GPU; what make_rope refuses."""
 
 import numpy as np
 import pytest
@@ -52,6 +52,24 @@ def test_ramp_by_index_refusals(H):
                 dict(beta_fast=1.0), dict(beta_fast=float("inf")), dict(original=0.0), dict(original=float("inf")), dict(factor=0.5)):
         with pytest.raises(H.HSQError):
             H.hsq_rope_frequencies(**dict(ok, **bad))
+
+
+def test_frequencies_of_ones_own_go_with_no_scaling(H):
+    """(they were taken, and the scaling, its factor and its amplitude dropped)"""
+    for bad in (dict(scaling="yarn", factor=4.0, original=32768.0), dict(scaling="linear", factor=2.0), dict(factor=2.0),
+                dict(theta=1e6), dict(original=10.0), dict(beta_fast=16.0), dict(beta_slow=2.0), dict(dims=128), dict(dims=4)):
+        with pytest.raises(ValueError):
+            H.make_rope(None, omega=[0.5, 0.25, 0.0, -1.0], max_pos=10, **bad)
+
+
+@pytest.mark.gpu
+def test_frequencies_of_ones_own(H):
+    from test_gpu_paged import make
+    for kw in (dict(), dict(dims=8)):
+        rope = H.make_rope(make(4, 2, 1, 64), omega=np.array([0.5, 0.25, 0.0, -1.0]), max_pos=300, **kw)
+        assert rope.dims == 8
+        np.testing.assert_allclose(rope.table[1].cpu().numpy()[:4], np.cos([0.5, 0.25, 0.0, -1.0]), rtol=1e-6)
+    assert H.make_rope(make(4, 2, 1, 64)).dims == 128
 
 
 @pytest.mark.gpu
