@@ -240,7 +240,7 @@ def hsq_rope_table(omega, amplitude: float, max_pos: int) -> np.ndarray:
         st = lib.hsq_rope_table(dims, omega.ctypes.data, amplitude, max_pos, out.ctypes.data, ctypes.byref(n))
     if st:
         raise HSQError(st, "hsq_rope_table: dims (twice the frequencies) must be a multiple of 8 in [8, 128], max_pos in "
-                           "[1, 2^24], the frequencies and the amplitude finite")
+                           "[1, 2^24], the angles and the amplitude (as fp32) finite")
     return out
 
 

@@ -316,9 +316,9 @@ hsq_status hsq_rope_table(int dims, const double* omega, double amplitude, int m
     const int n_hi = (max_pos + hsq::kRopeLoRows - 1) / hsq::kRopeLoRows, half = dims / 2;
     *floats = (size_t)(hsq::kRopeLoRows + n_hi) * dims;
     if (!table) return HSQ_OK;
-    if (!omega || !std::isfinite(amplitude)) return HSQ_ERR_INVALID;
+    if (!omega || !(std::fabs(amplitude) <= 3.4028234663852886e38)) return HSQ_ERR_INVALID;
     for (int i = 0; i < half; ++i)
-        if (!std::isfinite(omega[i])) return HSQ_ERR_INVALID;
+        if (!std::isfinite(omega[i] * max_pos)) return HSQ_ERR_INVALID;  // (an angle of infinity has no cosine)
     for (int c = 0; c < hsq::kRopeLoRows + n_hi; ++c) {
         const bool low = c < hsq::kRopeLoRows;
         const double p = low ? c : (double)(c - hsq::kRopeLoRows) * hsq::kRopeLoRows, amp = low ? amplitude : 1.0;

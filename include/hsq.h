@@ -652,6 +652,7 @@ hsq_status hsq_shared_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B
  * hsq_rope_table (host) -- cos and sin of the angles that positions in [0, max_pos) are put together from, fp32 from
  *   64 bits: 256 + ceil(max_pos / 256) rows of `dims` floats (cos | sin; rows of amplitude cos(c omega), c < 256, then
  *   of cos(256 a omega)).  *floats gets their number; with table NULL nothing else happens.  max_pos in [1, 2^24].
+ *   HSQ_ERR_INVALID also for an amplitude past fp32's range, or angles max_pos omega past fp64's.
  * hsq_rope -- a rotation for hsq_page_write_rope: the table in device memory, 16-byte aligned.  interleaved 0: pairs
  *   (i, i + dims / 2); 1: pairs (2 i, 2 i + 1).  Dims from `dims` on are left as they are.
  */

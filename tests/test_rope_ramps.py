@@ -1,5 +1,5 @@
 """YaRN's ramp by the pair's index: against the oracle, numbers worked out by hand with 40 digits, and the ramp by turns;
-the rotation that it makes, on the GPU; what make_rope refuses."""
+the rotation that it makes, on the GPU; what make_rope and the tables refuse."""
 
 import numpy as np
 import pytest
@@ -60,6 +60,14 @@ def test_frequencies_of_ones_own_go_with_no_scaling(H):
                 dict(theta=1e6), dict(original=10.0), dict(beta_fast=16.0), dict(beta_slow=2.0), dict(dims=128), dict(dims=4)):
         with pytest.raises(ValueError):
             H.make_rope(None, omega=[0.5, 0.25, 0.0, -1.0], max_pos=10, **bad)
+
+
+def test_tables_without_numbers_are_refused(H):
+    for omega, amp, most in (([1.0] * 4, 1e39, 10), ([1.0] * 4, -1e39, 10), ([1e305] * 4, 1.0, 1 << 24),
+                             ([1.0, -1e308, 0.0, 1.0], 1.0, 1000)):
+        with pytest.raises(H.HSQError):
+            H.hsq_rope_table(omega, amp, most)
+    assert np.isfinite(H.hsq_rope_table([1e300] * 4, 3e38, 1 << 20)).all()
 
 
 @pytest.mark.gpu
