@@ -1989,7 +1989,7 @@ hsq_status hsq_page_attn(hsq_ctx* ctx, const hsq_pages* pages, int rows, int B, 
             (e = launch((const void*)page_join_kernel, x.runs * 8, 256, 0, s, true, args)) != cudaSuccess)
             return hsq::cuda_fail(ctx, e, "page_attn tiles");
     }
-    if (max_new > 1 && group) return HSQ_OK;
+    if (group) return HSQ_OK;
     const long long units = (tiles ? (long long)x.rows : rows) * Hkv;
     const int S = cluster_of(units, 2LL * ctx->num_sms, (long long)top * P, 256);
     const void* fn = (const void*)page_attn_rows_kernel;

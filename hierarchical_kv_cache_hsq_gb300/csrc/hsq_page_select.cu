@@ -83,7 +83,7 @@ __device__ __forceinline__ int score_bin(uint32_t key, float per) {
 }
 
 // By a warp: the bin of the need-th key from the top of a histogram (lane l adds up the bins 255 - 8 l .. 248 - 8 l; bin 0 counts for
-// none); need becomes the number to be taken of it.  -1: there are not that many.
+// none, and there are need of the others); need becomes the number to be taken of it.
 __device__ __forceinline__ int locate_bin(const int* hist, int& need, int& in_bin) {
     const int lane = threadIdx.x & 31;
     const int4 h1 = reinterpret_cast<const int4*>(hist)[kBins / 4 - 1 - 2 * lane];
@@ -97,7 +97,6 @@ __device__ __forceinline__ int locate_bin(const int* hist, int& need, int& in_bi
         if (lane >= d) run += x;
     }
     const unsigned reach = __ballot_sync(kFull, run >= need);
-    if (!reach) return -1;
     run -= sum;
     int bin = 0, above = 0, in = 0;
 #pragma unroll
