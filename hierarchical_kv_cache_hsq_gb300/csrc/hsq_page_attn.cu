@@ -3,7 +3,10 @@
 // For row i and query head jq of KV head h: one softmax, scale 1/sqrt(128), over the tokens (up to the row's last) of the
 // logical pages in sel[i][h].  Parts of a softmax over disjoint sets of keys join as
 //     out = sum_p exp(m_p - M) o_p / sum_p exp(m_p - M) l_p,   M = max_p m_p,
-// with m, l, o a reference exponent, the sum of exp(x - m) and the sum of exp(x - m) v of a part.
+// with m, l, o a reference exponent, the sum of exp(x - m) and the sum of exp(x - m) v of a part, all fp32.  The weights
+// exp(x - m) alone are rounded to bf16, by up to 2^-8 of each, for their product with the values: the matrix instructions take both
+// in one type.  (The error against 64 bits is 0.0023 of the result, in root mean square; with weights in fp32 it would be the 0.0017
+// of the result's own rounding to bf16.)
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -740,10 +743,10 @@ __global__ void __launch_bounds__(kThreadsRow * H, 2)
 // Two streams (a row tile each, S / P and O in tensor memory) share the key tiles that both take and have
 // those that one takes in turn, so that while one stream's softmax runs the tensor cores work for the other.  A lone
 // tile is given to both streams, which take its key tiles in turn and are joined through tensor memory.
-// A chunk of 2048 tokens over 32K (32/8 heads, 64 of 1024 pages a row and head): 380 us, row by row 1530.  The rows of a tile
+// A chunk of 2048 tokens over 32K (32/8 heads, 64 of 1024 pages a row and head): 385 us, row by row 1530.  The rows of a tile
 // take 450 pages, seven times a row's, so the products are 0.48 TFLOP where the selection's own are 0.07; the tiles' kernel
-// does them in 346 us, 1.40 PFLOP/s.  Bound by the way of the pages into the SMs, 2.7 GB at 7.8 TB/s
-// (single rows reach 8.7; with all loads from the same 256 KB the call takes 371 us), beside the MMA thread
+// does them in 356 us, 1.36 PFLOP/s.  Bound by the way of the pages into the SMs, 2.7 GB at 7.6 TB/s
+// (single rows reach 8.7; with all loads from the same 256 KB the call took 371 us where it took 380), beside the MMA thread
 // and the softmax in turn: a tile of 128 rows x 128 keys takes an SM 1750 cycles, 1024 of them the pipe's.  The union, and the
 // time, shrink where neighbouring rows take the same pages.
 // ---------------------------------------------------------------------------------------
@@ -931,7 +934,7 @@ __global__ void __launch_bounds__(kListThreads) page_list_kernel(const __grid_co
 constexpr int kTcThreads = 384, kKeyStages = 3, kValueStages = 2, kTileStages = kKeyStages + kValueStages, kQueue = 2;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
 // Keys and values lie in groups of 8 rows, the group's halves side by side (kGroupHalf apart), so that a page is one copy (with a
-// copy for each half, and the copies behind the notes, a chunk of 2048 over 32K 387 us in place of 380).
+// copy for each half, and the copies behind the notes, a chunk of 2048 over 32K 387 us where it takes 380 otherwise).
 constexpr uint32_t kGroupBytes = 8 * 256, kGroupHalf = kGroupBytes / 2;
 constexpr uint32_t kOffQ = kTileStages * kTileBytes, kOffBars = kOffQ + 2 * kTileBytes;
 // barriers: full[5] | empty[5] | q_full[2] | q_empty[2] | s_full[2] | p_full[2] | o_full[2] | tail | drain | m_full | m_free | seg_full[2] | seg_empty[2] | note_full[5]

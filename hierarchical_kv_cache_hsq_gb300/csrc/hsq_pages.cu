@@ -189,7 +189,7 @@ struct WriteArgs {
 
 // What turns a half-warp's vectors.  kOwnRope: the context's rotation.  Else the first `dims` dims by hsq_rope's
 // table, in pairs (i, i + dims / 2) (kHalfRope) or (2 i, 2 i + 1) (kPairRope).  A table costs no time over the
-// context's rotation (a prompt of 32K tokens 121 us, 6.7 TB/s; 2531 float32 rows 17.2; 16 rows 2.0 in a graph).
+// context's rotation.
 enum { kOwnRope, kHalfRope, kPairRope };
 
 // The two quads of dims that lane l holds: what it turns lies in its own registers (pair k of it has frequency 4 l +
@@ -259,8 +259,9 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* pa, uint16_t* pb, const f
 // pointers are two bases and two strides (with the kind chosen vector by vector, address arithmetic
 // took half of the issue slots).  Bound by HBM for many rows, where reads and writes in flight
 // decide: a prompt of 32K tokens (32/8 heads, bf16, 806 MB) takes 121 us, 6.7 TB/s, 99 % of a plain copy's rate;
-// with V = 1, fewer loads in flight, 185.  For few rows by latency, and V = 1 spreads them over the SMs: 16 rows 4.2
-// us, with V = 8 5.5.  (2531 float32 rows: 25.2 with V = 1, 23.7 with V = 4.)
+// with V = 1, fewer loads in flight, 187.  For few rows by latency, and V = 1 spreads them over the SMs: 16 rows 2.0
+// us, with V = 8 2.9.  (2531 float32 rows: 20.1 with V = 1, 17.1 with V = 4.  Replayed from a graph, the inputs in L2
+// where they fit; with other inputs in turn 16 rows take 4.2.)
 template <bool BF, int V, int ROPE>
 __global__ void __launch_bounds__(kThreads) page_write_kernel(WriteArgs a, Tables tb) {
     using Raw = typename std::conditional<BF, uint2, float4>::type;  // a quad of dims

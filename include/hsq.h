@@ -718,7 +718,11 @@ hsq_status hsq_page_summaries(hsq_ctx* ctx, const hsq_pages* pages, const hsq_su
  *   Rows from q_start[B] on are left as they were.  The context's routing options (route_max, route_per_head) do not apply.
  *   q: [rows][Hq][128] bf16, rotated; sel: [rows][Hkv][top] int32; the rest as for hsq_shared_attn.  first >= 0,
  *   recent >= 1 (a row's last page may hold tokens after it, so its summary decides nothing), first + recent <= top
- *   <= HSQ_MAX_BETA; np + width <= HSQ_MAX_SELECT_PAGES.
+ *   <= HSQ_MAX_BETA; np + width <= HSQ_MAX_SELECT_PAGES.  workspace: as there, of hsq_page_select_workspace_size bytes; kept for
+ *   ways of the call that need one, of which there is none: nothing of it is read or written.
+ *   What the score can see: a page by its mean key, a row by the sum of its heads.  One token among others that a head does
+ *   not look at brings its page in where its logit stands out by some 3 sqrt(page_n r) spreads of theirs (one page in
+ *   eight taken), so small pages find more.
  *   HSQ_DEVERR_LEN: lens[b] negative (taken as 0), above width * page_n or below n_b; offsets that do not ascend in
  *   [0, rows] or n_b above max_new (rows of such a request are not written; which request a row
  *   belongs to where offsets overlap is not defined).
